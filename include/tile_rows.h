@@ -343,6 +343,140 @@ int tile_run_backward_plan_ex(int op, int plan_id, int dtype, const void *in, co
  * success only. */
 int tile_describe_backward_plan(int op, int dtype, int rows, int width, tile_plan_t *plan);
 
+/* ---- block norm ---------------------------------------------------------
+ * The norms around one block of a residual network, fused with the block's
+ * gate and the scaled residual sum.  For every row, with
+ * norm(v; gamma) = v / sqrt(mean(v^2) + eps) * gamma (RMSNorm):
+ *
+ *   n      = norm(in; gamma_post)          with TILE_NORM_POST, else n = in
+ *   hidden = residual_scale * residual + gate * n
+ *   out    = norm(hidden; gamma_pre)       with TILE_NORM_PRE
+ *
+ * in: the block's output; residual: the residual stream the block read;
+ * hidden: the residual stream after it; out: the next block's input.  (The
+ * notes this library follows have no counterpart.)  out is computed from the
+ * unrounded hidden row and rounded once; hidden is rounded once.
+ *
+ * Rows are [rows][width] of `dtype`, contiguous; gammas [width] FP32, NULL
+ * for ones; gate [ceil(rows / rows_per_gate)][width] FP32, NULL for ones:
+ * row i takes gate row i / rows_per_gate (rows_per_gate >= rows: one learned
+ * gate per channel; the tokens of a sequence: a gate per sequence; 1: a
+ * gate per element).  rows_per_gate is ignored without a gate.  Any
+ * alignment of the element type works; rows whose pointers are all 16-byte
+ * aligned and whose width is a multiple of 16 bytes take vector accesses.
+ * No output may overlap an input or another output.  Everything is FP32
+ * inside, and results are bitwise reproducible for a given (shape, dtype,
+ * alignment) on the same GPU.  Captured into CUDA graphs as any launch. */
+#define TILE_NORM_POST 1   /* norm after the block                           */
+#define TILE_NORM_PRE  2   /* norm before the next block                     */
+
+typedef struct tile_block_norm_args {
+    const void *in;            /* [rows][width]                              */
+    const void *residual;      /* [rows][width]                              */
+    const float *gamma_post;   /* TILE_NORM_POST: [width] or NULL            */
+    const float *gate;         /* [ceil(rows / rows_per_gate)][width] or NULL */
+    const float *gamma_pre;    /* TILE_NORM_PRE: [width] or NULL             */
+    void *hidden;              /* [rows][width], written                     */
+    void *out;                 /* TILE_NORM_PRE: [rows][width], written      */
+    int rows, width;           /* 1 <= width <= tile_max_width()             */
+    int rows_per_gate;         /* >= 1 with a gate                           */
+    int norms;                 /* TILE_NORM_POST | TILE_NORM_PRE, at least one */
+    float residual_scale;      /* finite                                     */
+    float eps;
+    int dtype;                 /* TILE_DTYPE_*                               */
+} tile_block_norm_args_t;
+
+/* Errors as the row entry points; TILE_ERR_OP for norms that are not a
+ * non-empty set of the two bits; TILE_ERR_SHAPE also for rows_per_gate < 1
+ * with a gate; TILE_ERR_EPS also for a residual_scale that is not finite. */
+int tile_block_norm(const tile_block_norm_args_t *args, cudaStream_t stream);
+
+/* Gradients of a block norm.  dhidden, dout: the gradients of hidden and
+ * out; dhidden may be NULL (no use of hidden but out), dout is read with
+ * TILE_NORM_PRE only.  in is the forward `in`, hidden the forward's rounded
+ * `hidden`, whose statistics are taken again from it.  Writes
+ *
+ *   din, dresidual          [rows][width] of dtype
+ *   dgamma_post, dgamma_pre [width] FP32 (NULL: not wanted)
+ *   dgate                   the gate's shape, FP32 (NULL: not wanted)
+ *
+ * Column sums are FP32 partial sums of contiguous row ranges in the caller's
+ * device `workspace` (16-byte aligned), joined in a fixed order; no atomics.
+ * `in` may be NULL without TILE_NORM_POST and gate; `hidden` and dout may
+ * be NULL without TILE_NORM_PRE.  rows == 0 writes zero parameter
+ * gradients.  dgamma_post needs TILE_NORM_POST, dgamma_pre TILE_NORM_PRE,
+ * dgate a gate (TILE_ERR_OP).  Calls that overlap in time need workspaces
+ * of their own. */
+typedef struct tile_block_norm_backward_args {
+    const void *in, *hidden, *dhidden, *dout;
+    const float *gamma_post, *gate, *gamma_pre;
+    void *din, *dresidual;
+    float *dgamma_post, *dgate, *dgamma_pre;
+    int rows, width, rows_per_gate, norms;
+    float residual_scale, eps;
+    int dtype;
+} tile_block_norm_backward_args_t;
+
+size_t tile_block_norm_backward_workspace_bytes(int rows, int width);
+int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
+/* ---- linear cross entropy --------------------------------------------------
+ * The loss at the end of a language model: a linear head over a vocabulary
+ * and the softmax cross entropy of its logits, without keeping them.  For
+ * every row i of `in` ([rows][width]), with the logits
+ * l_v = sum_h in[i][h] weight[v][h], v < vocab:
+ *
+ *   lse[i]  = log(sum_v exp(l_v))
+ *   loss[i] = lse[i] - l_target[i]
+ *
+ * Both FP32 [rows]; a row whose target is ignore_index gets loss = lse = 0.
+ * dtype: TILE_DTYPE_BF16 or TILE_DTYPE_F16 of in and weight ([vocab][width]);
+ * the products of 16-bit elements are exact, and every sum is FP32.  (FP32
+ * operands are refused with TILE_ERR_DTYPE: the tensor cores would round
+ * them.)  target: [rows] 64-bit integers on the device.  A target that is
+ * neither ignore_index nor in [0, vocab) gives that row a NaN loss and sets
+ * the device status word (tile_check_device_status).
+ *
+ * `workspace`: device memory of the caller, 256-byte aligned, at least
+ * tile_linear_cross_entropy_workspace_bytes(rows, width, vocab) bytes: two
+ * numbers per row and 256 vocabulary entries, and, for widths that are not
+ * multiples of 8, copies of in and weight in rows that are.  Calls that
+ * overlap in time need workspaces of their own.  in and weight: 16-byte
+ * aligned where width is a multiple of 8, else 2-byte (TILE_ERR_ALIGN).
+ * Other rules and errors as the row entry points (TILE_ERR_SHAPE also for
+ * vocab < 1, and rows or vocab above 2^30; rows == 0 is a no-op).  The call
+ * may be captured into a CUDA graph. */
+size_t tile_linear_cross_entropy_workspace_bytes(int rows, int width, int vocab);
+int tile_linear_cross_entropy(int dtype, const void *in, const void *weight,
+                              const long long *target, float *loss, float *lse, int rows,
+                              int width, int vocab, long long ignore_index, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
+/* Its gradients: with g[i][v] = (exp(l_v - lse[i]) - [v = target[i]]) dloss[i],
+ *
+ *   din = g weight ([rows][width]),   dweight = g^T in ([vocab][width])
+ *
+ * of dtype, either may be NULL.  lse: the forward's.  dloss: [rows] FP32,
+ * the gradient of each row's loss (1 / rows of a mean).  Rows whose target is
+ * ignore_index or whose dloss is 0 get din = 0 and take no part in dweight,
+ * whatever they hold; so do rows with a target out of range, which set the
+ * device status word.
+ *
+ * g is made in pieces of the vocabulary (a workspace of at most about
+ * 512 MiB, or 4096 columns) and held in 16 bits for one piece: dtype
+ * values rounded once, FP16 ones after scaling by a power of two taken from
+ * the largest |dloss|.  Sums are FP32, din and dweight rounded once.  No
+ * atomics: results are bitwise reproducible.  rows == 0 writes a zero
+ * dweight. */
+size_t tile_linear_cross_entropy_backward_workspace_bytes(int rows, int width, int vocab);
+int tile_linear_cross_entropy_backward(int dtype, const void *in, const void *weight,
+                                       const long long *target, const float *lse,
+                                       const float *dloss, void *din, void *dweight, int rows,
+                                       int width, int vocab, long long ignore_index,
+                                       void *workspace, size_t workspace_bytes,
+                                       cudaStream_t stream);
+
 /* ---- pointwise value/derivative pairs ---------------------------------- */
 
 /* value[k] = sigmoid(in[k]) and derivative[k] = sigmoid'(in[k]) for k < n,

@@ -35,6 +35,10 @@ __all__ = [
     "tile_describe_plan_ex", "tile_plan_info_ex",
     "tile_layernorm_backward_f32", "tile_rmsnorm_backward_f32", "tile_softmax_backward_f32",
     "tile_run_backward_plan_f32", "tile_norm_param_grad_workspace_bytes",
+    "tile_block_norm", "tile_block_norm_backward", "tile_block_norm_backward_workspace_bytes",
+    "tile_linear_cross_entropy", "tile_linear_cross_entropy_workspace_bytes",
+    "tile_linear_cross_entropy_backward", "tile_linear_cross_entropy_backward_workspace_bytes",
+    "block_norm", "block_norm_backward", "linear_cross_entropy", "linear_cross_entropy_backward",
     "tile_norm_param_grad_f32", "tile_run_backward_plan_ex",
     "tile_layernorm_backward_bf16", "tile_rmsnorm_backward_bf16", "tile_softmax_backward_bf16",
     "tile_norm_param_grad_bf16", "tile_layernorm_backward_f16", "tile_rmsnorm_backward_f16",
@@ -78,6 +82,28 @@ class TilePlan(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class TileBlockNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("in_", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("gamma_post", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p), ("gamma_pre", ctypes.c_void_p), ("hidden", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("rows", ctypes.c_int), ("width", ctypes.c_int),
+        ("rows_per_gate", ctypes.c_int), ("norms", ctypes.c_int),
+        ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float), ("dtype", ctypes.c_int),
+    ]
+
+
+class TileBlockNormBackwardArgs(ctypes.Structure):
+    _fields_ = [
+        ("in_", ctypes.c_void_p), ("hidden", ctypes.c_void_p), ("dhidden", ctypes.c_void_p),
+        ("dout", ctypes.c_void_p), ("gamma_post", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+        ("gamma_pre", ctypes.c_void_p), ("din", ctypes.c_void_p), ("dresidual", ctypes.c_void_p),
+        ("dgamma_post", ctypes.c_void_p), ("dgate", ctypes.c_void_p),
+        ("dgamma_pre", ctypes.c_void_p), ("rows", ctypes.c_int), ("width", ctypes.c_int),
+        ("rows_per_gate", ctypes.c_int), ("norms", ctypes.c_int),
+        ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float), ("dtype", ctypes.c_int),
+    ]
 
 
 class TileRowArgs(ctypes.Structure):
@@ -166,6 +192,13 @@ def load():
         "tile_inject_launch_failure": [I, I, I],
         "tile_test_force_general_kernels": [I],
         "tile_describe_backward_plan": [I, I, I, I, ctypes.POINTER(TilePlan)],
+        "tile_block_norm": [ctypes.POINTER(TileBlockNormArgs), P],
+        "tile_block_norm_backward": [ctypes.POINTER(TileBlockNormBackwardArgs), P,
+                                     ctypes.c_size_t, P],
+        "tile_linear_cross_entropy": [I, P, P, P, P, P, I, I, I, ctypes.c_longlong, P,
+                                      ctypes.c_size_t, P],
+        "tile_linear_cross_entropy_backward": [I, P, P, P, P, P, P, P, I, I, I,
+                                               ctypes.c_longlong, P, ctypes.c_size_t, P],
     }
     for name, argtypes in sigs.items():
         fn = getattr(lib, name)
@@ -173,6 +206,12 @@ def load():
         fn.restype = ctypes.c_int
     lib.tile_norm_param_grad_workspace_bytes.argtypes = [I, I]
     lib.tile_norm_param_grad_workspace_bytes.restype = ctypes.c_size_t
+    lib.tile_block_norm_backward_workspace_bytes.argtypes = [I, I]
+    lib.tile_block_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+    for name in ("tile_linear_cross_entropy_workspace_bytes",
+                 "tile_linear_cross_entropy_backward_workspace_bytes"):
+        getattr(lib, name).argtypes = [I, I, I]
+        getattr(lib, name).restype = ctypes.c_size_t
     lib.tile_host_workspace_bytes.argtypes = [I, I, I]
     lib.tile_host_workspace_bytes.restype = ctypes.c_size_t
     lib.tile_status_string.argtypes = [I]
@@ -762,6 +801,190 @@ def tile_last_cuda_error():
     return load().tile_last_cuda_error()
 
 
+# ---- block norm --------------------------------------------------------------
+
+def _row_dtype(t, name):
+    """The element type of a row tensor, by the names of DTYPES."""
+    import torch
+    kinds = {torch.float32: "f32", torch.bfloat16: "bf16", torch.float16: "f16"}
+    if not isinstance(t, torch.Tensor) or t.dtype not in kinds:
+        raise ValueError(f"{name} must be a float32, bfloat16 or float16 tensor")
+    return kinds[t.dtype]
+
+
+class _on_device_of:
+    """Makes the device of ``t`` current for a call (its launches, and the
+    stream that ``stream=None`` stands for); every tensor given has to be on
+    it."""
+
+    def __init__(self, t, *others):
+        import torch
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
+        for o in others:
+            if o is not None and o.device != t.device:
+                raise ValueError(f"tensors must be on one device: {t.device} and {o.device}")
+        self.guard = None
+        if t.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _workspace(t):
+    """(pointer, bytes) of a contiguous CUDA workspace tensor."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _gates(t, rows, width, rows_per_gate, name):
+    """Pointer of a gate matrix [ceil(rows / rows_per_gate)][width], or None."""
+    import torch
+    if t is None:
+        return None
+    if rows_per_gate < 1:
+        raise ValueError("rows_per_gate must be at least 1 with a gate")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
+        raise ValueError(f"{name} must be a CUDA float32 tensor")
+    want = (-(-rows // rows_per_gate), width)
+    if not t.is_contiguous() or (tuple(t.shape) != want and not (want[0] == 1 and
+                                                                 tuple(t.shape) == want[1:])):
+        raise ValueError(f"{name} must be contiguous of shape {want}")
+    return t.data_ptr()
+
+
+def tile_block_norm(x, residual, hidden, out, gamma_post=None, gate=None, gamma_pre=None,
+                    post=True, pre=True, rows_per_gate=0, residual_scale=1.0, eps=1e-5,
+                    stream=None):
+    """hidden = residual_scale * residual + gate * norm(x; gamma_post) and
+    out = norm(hidden; gamma_pre), RMSNorms, of float32, bfloat16 or float16
+    rows; see ``tile_block_norm`` in include/tile_rows.h.  ``post`` / ``pre``
+    switch the norms (without ``pre``, ``out`` is None); ``rows_per_gate``
+    0 with a gate stands for all rows."""
+    dt = _row_dtype(x, "x")
+    with _on_device_of(x, residual, hidden, out, gamma_post, gate, gamma_pre):
+        a = TileBlockNormArgs()
+        a.in_, rows, width = _matrix(x, "x", dt)
+        a.rows, a.width, a.dtype = rows, width, DTYPES[dt]
+        a.residual, a.hidden = _matrix(residual, "residual", dt)[0], _matrix(hidden, "hidden", dt)[0]
+        _same_shape(x, residual, "x/residual")
+        _same_shape(x, hidden, "x/hidden")
+        if pre:
+            a.out = _matrix(out, "out", dt)[0]
+            _same_shape(x, out, "x/out")
+        a.rows_per_gate = rows_per_gate or max(rows, 1)
+        a.gamma_post = _vector(gamma_post, width, "gamma_post")
+        a.gate = _gates(gate, rows, width, a.rows_per_gate, "gate")
+        a.gamma_pre = _vector(gamma_pre, width, "gamma_pre")
+        a.norms = (1 if post else 0) | (2 if pre else 0)
+        a.residual_scale, a.eps = residual_scale, eps
+        _check(load().tile_block_norm(ctypes.byref(a), _stream(stream)), "tile_block_norm")
+
+
+def tile_block_norm_backward_workspace_bytes(rows, width):
+    return load().tile_block_norm_backward_workspace_bytes(rows, width)
+
+
+def tile_block_norm_backward(x, hidden, dhidden, dout, din, dresidual, workspace,
+                             gamma_post=None, gate=None, gamma_pre=None, dgamma_post=None,
+                             dgate=None, dgamma_pre=None, post=True, pre=True, rows_per_gate=0,
+                             residual_scale=1.0, eps=1e-5, stream=None):
+    """The gradients of ``tile_block_norm`` (see include/tile_rows.h).
+    ``hidden`` is the forward's; ``dhidden`` may be None (``dout`` is then
+    the only gradient), as may any parameter gradient."""
+    dt = _row_dtype(din, "din")
+    with _on_device_of(din, x, hidden, dhidden, dout, dresidual, workspace, gamma_post, gate,
+                       gamma_pre, dgamma_post, dgate, dgamma_pre):
+        a = TileBlockNormBackwardArgs()
+        a.din, rows, width = _matrix(din, "din", dt)
+        a.rows, a.width, a.dtype = rows, width, DTYPES[dt]
+        for name, t, field in (("x", x, "in_"), ("hidden", hidden, "hidden"),
+                               ("dhidden", dhidden, "dhidden"), ("dout", dout, "dout"),
+                               ("dresidual", dresidual, "dresidual")):
+            if t is not None:
+                setattr(a, field, _matrix(t, name, dt)[0])
+                _same_shape(din, t, f"din/{name}")
+        a.rows_per_gate = rows_per_gate or max(rows, 1)
+        a.gamma_post = _vector(gamma_post, width, "gamma_post")
+        a.gate = _gates(gate, rows, width, a.rows_per_gate, "gate")
+        a.gamma_pre = _vector(gamma_pre, width, "gamma_pre")
+        a.dgamma_post = _vector(dgamma_post, width, "dgamma_post")
+        a.dgate = _gates(dgate, rows, width, a.rows_per_gate, "dgate")
+        a.dgamma_pre = _vector(dgamma_pre, width, "dgamma_pre")
+        a.norms = (1 if post else 0) | (2 if pre else 0)
+        a.residual_scale, a.eps = residual_scale, eps
+        ws, nbytes = _workspace(workspace)
+        _check(load().tile_block_norm_backward(ctypes.byref(a), ws, nbytes, _stream(stream)),
+               "tile_block_norm_backward")
+
+
+# ---- linear cross entropy -------------------------------------------------------
+
+def _ce_inputs(x, weight, target):
+    """(dtype name, x, weight, target pointers, rows, width, vocab)."""
+    import torch
+    dt = _row_dtype(x, "x")
+    if dt == "f32":
+        raise ValueError("x must be bfloat16 or float16")
+    px, rows, width = _matrix(x, "x", dt)
+    pw, vocab, w2 = _matrix(weight, "weight", dt)
+    if w2 != width:
+        raise ValueError(f"x/weight: widths {width} and {w2} differ")
+    if not isinstance(target, torch.Tensor) or not target.is_cuda or target.dtype != torch.int64:
+        raise ValueError("target must be a CUDA int64 tensor")
+    if not target.is_contiguous() or target.numel() != rows:
+        raise ValueError(f"target must be contiguous with {rows} elements")
+    return dt, px, pw, target.data_ptr(), rows, width, vocab
+
+
+def tile_linear_cross_entropy_workspace_bytes(rows, width, vocab):
+    return load().tile_linear_cross_entropy_workspace_bytes(rows, width, vocab)
+
+
+def tile_linear_cross_entropy_backward_workspace_bytes(rows, width, vocab):
+    return load().tile_linear_cross_entropy_backward_workspace_bytes(rows, width, vocab)
+
+
+def tile_linear_cross_entropy(x, weight, target, loss, lse, workspace, ignore_index=-100,
+                              stream=None):
+    """loss and log-sum-exp of the rows' logits x weight^T (bfloat16 or
+    float16) without keeping them; see include/tile_rows.h."""
+    with _on_device_of(x, weight, target, loss, lse, workspace):
+        dt, px, pw, pt, rows, width, vocab = _ce_inputs(x, weight, target)
+        ws, nbytes = _workspace(workspace)
+        _check(load().tile_linear_cross_entropy(
+            DTYPES[dt], px, pw, pt, _vector(loss, rows, "loss"), _vector(lse, rows, "lse"), rows,
+            width, vocab, ignore_index, ws, nbytes, _stream(stream)), "tile_linear_cross_entropy")
+
+
+def tile_linear_cross_entropy_backward(x, weight, target, lse, dloss, dx, dweight, workspace,
+                                       ignore_index=-100, stream=None):
+    """Gradients of ``tile_linear_cross_entropy`` for the gradient ``dloss``
+    of each row's loss; ``dx`` or ``dweight`` may be None."""
+    with _on_device_of(x, weight, target, lse, dloss, dx, dweight, workspace):
+        dt, px, pw, pt, rows, width, vocab = _ce_inputs(x, weight, target)
+        pdx = pdw = None
+        if dx is not None:
+            pdx = _matrix(dx, "dx", dt)[0]
+            _same_shape(x, dx, "x/dx")
+        if dweight is not None:
+            pdw = _matrix(dweight, "dweight", dt)[0]
+            _same_shape(weight, dweight, "weight/dweight")
+        ws, nbytes = _workspace(workspace)
+        _check(load().tile_linear_cross_entropy_backward(
+            DTYPES[dt], px, pw, pt, _vector(lse, rows, "lse"), _vector(dloss, rows, "dloss"), pdx,
+            pdw, rows, width, vocab, ignore_index, ws, nbytes, _stream(stream)),
+            "tile_linear_cross_entropy_backward")
+
+
 # ---------------------------------------------------------------------------
 # convenience wrappers (allocate the output with torch when not given)
 # ---------------------------------------------------------------------------
@@ -792,6 +1015,79 @@ def softmax(x, out=None, stream=None):
     out = torch.empty_like(x) if out is None else out
     tile_softmax_f32(x, out, 0.0, stream)
     return out
+
+
+def _allocating_on(stream):
+    """Makes ``stream`` current, so that what a wrapper allocates belongs to
+    the stream its kernels run on."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def _scratch(nbytes, device):
+    import torch
+    return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+
+
+def block_norm(x, residual, gamma_post=None, gate=None, gamma_pre=None, post=True, pre=True,
+               rows_per_gate=0, residual_scale=1.0, eps=1e-5, stream=None):
+    """(hidden, out) of ``tile_block_norm``; out is None without ``pre``."""
+    import torch
+    with _allocating_on(stream):
+        hidden = torch.empty_like(x)
+        out = torch.empty_like(x) if pre else None
+        tile_block_norm(x, residual, hidden, out, gamma_post, gate, gamma_pre, post, pre,
+                        rows_per_gate, residual_scale, eps, stream)
+    return hidden, out
+
+
+def block_norm_backward(x, hidden, gamma_post, gate, gamma_pre, dhidden, dout, post=True,
+                        pre=True, rows_per_gate=0, residual_scale=1.0, eps=1e-5, stream=None):
+    """(din, dresidual, dgamma_post, dgate, dgamma_pre) of
+    ``tile_block_norm_backward``; the gradients of parameters that are None
+    are None."""
+    import torch
+    like = hidden if hidden is not None else dhidden
+    with _allocating_on(stream):
+        din, dresidual = torch.empty_like(like), torch.empty_like(like)
+        dgamma_post = torch.empty_like(gamma_post) if post and gamma_post is not None else None
+        dgate = torch.empty_like(gate) if gate is not None else None
+        dgamma_pre = torch.empty_like(gamma_pre) if pre and gamma_pre is not None else None
+        ws = _scratch(tile_block_norm_backward_workspace_bytes(*like.shape), like.device)
+        tile_block_norm_backward(x, hidden, dhidden, dout, din, dresidual, ws, gamma_post, gate,
+                                 gamma_pre, dgamma_post, dgate, dgamma_pre, post, pre,
+                                 rows_per_gate, residual_scale, eps, stream)
+    return din, dresidual, dgamma_post, dgate, dgamma_pre
+
+
+def linear_cross_entropy(x, weight, target, ignore_index=-100, stream=None):
+    """(loss, lse) of ``tile_linear_cross_entropy``, float32, one per row."""
+    import torch
+    rows = x.shape[0]
+    with _allocating_on(stream):
+        loss = torch.empty(rows, dtype=torch.float32, device=x.device)
+        lse = torch.empty_like(loss)
+        ws = _scratch(tile_linear_cross_entropy_workspace_bytes(rows, x.shape[1],
+                                                                weight.shape[0]), x.device)
+        tile_linear_cross_entropy(x, weight, target, loss, lse, ws, ignore_index, stream)
+    return loss, lse
+
+
+def linear_cross_entropy_backward(x, weight, target, lse, dloss, ignore_index=-100,
+                                  need_dx=True, need_dweight=True, stream=None):
+    """(dx, dweight) of ``tile_linear_cross_entropy_backward``."""
+    import torch
+    with _allocating_on(stream):
+        dx = torch.empty_like(x) if need_dx else None
+        dweight = torch.empty_like(weight) if need_dweight else None
+        ws = _scratch(tile_linear_cross_entropy_backward_workspace_bytes(
+            x.shape[0], x.shape[1], weight.shape[0]), x.device)
+        tile_linear_cross_entropy_backward(x, weight, target, lse, dloss, dx, dweight, ws,
+                                           ignore_index, stream)
+    return dx, dweight
 
 
 def run(op, x, residual=None, out=None, eps=1e-5, stream=None):

@@ -1,0 +1,328 @@
+// Block norm, backward.  With r1, r2 = 1 / sqrt(mean square + eps) of the
+// block's output b and of h, w = gate * gamma_post and n the width:
+//
+//   gy = dy * gamma_pre
+//   gh = dh + r2 gy - h r2^3 sum(gy h) / n            (the whole gradient of h)
+//   dresidual = a gh,   dgamma_pre = sum_rows dy h r2
+//   u  = w gh
+//   db = r1 u - b r1^3 sum(u b) / n
+//   S[gate row] = sum_rows gh b r1,   dgate = gamma_post S,
+//   dgamma_post = sum over gate rows of gate S
+//
+// sum(u b) is linear in gh, so the six sums of h^2, gy h, b^2, w b dh,
+// w b gy and w b h give every scalar of a row in one reduction round.
+//
+// Bound by DRAM: b, h, dh, dy are read once, db and dresidual written once.
+// A program walks over a contiguous range of rows; parameters and the column
+// sums of its columns stay in registers (FP32), and go to the workspace once
+// at its end.  Gate rows that lie within one program's range are written by
+// it; the others, and the gamma sums, are joined in program order by a
+// second kernel, so results do not depend on timing.
+#include "block_norm.cuh"
+#include "device_status.h"
+
+TILE_DEVICE_STATUS(block_norm_backward)
+
+namespace tile {
+namespace {
+
+// Column sums of a program in the workspace [unit][slot][width].
+enum { SLOT_PRE = 0, SLOT_POST = 1, SLOT_FIRST = 2, SLOT_LAST = 3, SLOTS = 4 };
+
+// Programs of a call: at most this many, each of at least four rows where
+// there are more rows than SMs.
+constexpr int kMaxUnits = 1024;
+
+long long units_of(long long rows, int slots) {
+    long long u = rows / 4 > slots ? slots : rows;
+    const long long sms = 152;
+    if (rows / 4 <= slots && u > sms) u = rows / 4 > sms ? rows / 4 : sms;
+    if (u > kMaxUnits) u = kMaxUnits;
+    return u < 1 ? 1 : u;
+}
+
+template <class T, int V, int K, bool CL>
+__global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockArgs a, int cluster) {
+    using A = Access<T, V>;
+    constexpr int E = K * V;
+    __shared__ ReduceMem<6> mem;
+    const int W = blockDim.x;
+    const int warps = W >> 5;
+    const int rank = CL ? static_cast<int>(cluster_rank()) : 0;
+    const long long units = gridDim.x / (CL ? cluster : 1);
+    const long long unit = blockIdx.x / (CL ? cluster : 1);
+    const long long begin = a.rows * unit / units, end = a.rows * (unit + 1) / units;
+    const T *x = static_cast<const T *>(a.x), *hid = static_cast<const T *>(a.hidden);
+    const T *dhid = static_cast<const T *>(a.dhidden), *dout = static_cast<const T *>(a.dout);
+    T *din = static_cast<T *>(a.din), *dres = static_cast<T *>(a.dresidual);
+    const float inv_n = 1.0f / static_cast<float>(a.width);
+    const bool has_x = a.post || a.gate != nullptr, has_dh = dhid != nullptr;
+
+    int col[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        col[k] = ((k * (CL ? cluster : 1) + rank) * W + static_cast<int>(threadIdx.x)) * V;
+
+    float g2[E], w[E], sum_pre[E], sum_post[E], sum_gate[E];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        float p[V];
+        if (col[k] < a.width) load_params<V>(a.gamma_pre, col[k], p);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = k * V + j;
+            g2[i] = col[k] < a.width ? p[j] : 0.0f;
+            w[i] = sum_pre[i] = sum_post[i] = sum_gate[i] = 0.0f;
+        }
+    }
+    const long long first_gate = begin / a.per_gate;
+    long long gate_row = first_gate - 1, gate_end = begin;
+    int turn = 0;
+    for (long long row = begin; row < end; ++row) {
+        if (row == gate_end) {
+            gate_row = row / a.per_gate;
+            gate_end = (gate_row + 1) * a.per_gate;
+            const float *gate = a.gate != nullptr ? a.gate + gate_row * a.width : nullptr;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (col[k] < a.width) {
+                    float p[V], q[V];
+                    load_params<V>(a.gamma_post, col[k], p);
+                    load_params<V>(gate, col[k], q);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) w[k * V + j] = p[j] * q[j];
+                }
+        }
+        typename A::Raw xr[K], hr[K], dhr[K], dyr[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            xr[k] = hr[k] = dhr[k] = dyr[k] = typename A::Raw{};
+            if (col[k] < a.width) {
+                const long long at = row * a.width + col[k];
+                if (has_x) xr[k] = A::load(x + at);
+                if (a.pre) hr[k] = A::load(hid + at);
+                if (has_dh) dhr[k] = A::load(dhid + at);
+                if (a.pre) dyr[k] = A::load(dout + at);
+            }
+        }
+        float s[6] = {};   // h^2, gy h, b^2, w b dh, w b gy, w b h
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float b[V], h[V], dh[V], dy[V];
+            A::widen(xr[k], b);
+            A::widen(hr[k], h);
+            A::widen(dhr[k], dh);
+            A::widen(dyr[k], dy);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float gy = dy[j] * g2[k * V + j], wb = w[k * V + j] * b[j];
+                s[0] = fmaf(h[j], h[j], s[0]);
+                s[1] = fmaf(gy, h[j], s[1]);
+                s[2] = fmaf(b[j], b[j], s[2]);
+                s[3] = fmaf(wb, dh[j], s[3]);
+                s[4] = fmaf(wb, gy, s[4]);
+                s[5] = fmaf(wb, h[j], s[5]);
+            }
+        }
+        row_sum<6, CL>(s, mem, turn, warps, cluster);
+        // gh = dh + r2 gy - ch h
+        const float r2 = a.pre ? 1.0f / sqrtf(fmaf(s[0], inv_n, a.eps)) : 0.0f;
+        const float ch = r2 * r2 * r2 * (s[1] * inv_n);
+        const float r1 = a.post ? 1.0f / sqrtf(fmaf(s[2], inv_n, a.eps)) : 1.0f;
+        // db = r1 u - cb b
+        const float ub = fmaf(r2, s[4], s[3]) - ch * s[5];
+        const float cb = a.post ? r1 * r1 * r1 * (ub * inv_n) : 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (col[k] >= a.width) continue;
+            float b[V], h[V], dh[V], dy[V], db[V], dr[V];
+            A::widen(xr[k], b);
+            A::widen(hr[k], h);
+            A::widen(dhr[k], dh);
+            A::widen(dyr[k], dy);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int i = k * V + j;
+                const float gh = fmaf(-ch, h[j], fmaf(r2, dy[j] * g2[i], dh[j]));
+                sum_pre[i] = fmaf(dy[j], h[j] * r2, sum_pre[i]);
+                sum_gate[i] = fmaf(gh, b[j] * r1, sum_gate[i]);
+                dr[j] = a.scale * gh;
+                db[j] = fmaf(-cb, b[j], r1 * (w[i] * gh));
+            }
+            const long long at = row * a.width + col[k];
+            A::store(din + at, db);
+            A::store(dres + at, dr);
+        }
+        if (row + 1 == end || row + 1 == gate_end) {   // end of this gate row's part
+            const long long gate_begin = gate_row * a.per_gate;
+            const bool whole = gate_begin >= begin && (gate_end <= end || end == a.rows);
+            const int slot = gate_row == first_gate ? SLOT_FIRST : SLOT_LAST;
+            float *part = a.ws + (unit * SLOTS + slot) * a.width;
+            const float *gate = a.gate != nullptr ? a.gate + gate_row * a.width : nullptr;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (col[k] < a.width) {
+                    float p[V], q[V];
+                    load_params<V>(a.gamma_post, col[k], p);
+                    load_params<V>(gate, col[k], q);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const int i = k * V + j;
+                        sum_post[i] = fmaf(q[j], sum_gate[i], sum_post[i]);
+                        if (a.dgate != nullptr) {
+                            if (whole)
+                                a.dgate[gate_row * a.width + col[k] + j] = p[j] * sum_gate[i];
+                            else
+                                part[col[k] + j] = sum_gate[i];
+                        }
+                        sum_gate[i] = 0.0f;
+                    }
+                }
+        }
+    }
+    float *pre = a.ws + (unit * SLOTS + SLOT_PRE) * a.width;
+    float *post = a.ws + (unit * SLOTS + SLOT_POST) * a.width;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (col[k] < a.width)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (a.dgamma_pre != nullptr) pre[col[k] + j] = sum_pre[k * V + j];
+                if (a.dgamma_post != nullptr) post[col[k] + j] = sum_post[k * V + j];
+            }
+    if constexpr (CL) cluster_barrier();   // peers may still read this CTA's sums
+}
+
+// Joins the programs' column sums, in program order: blockIdx.y 0 the gamma
+// gradients, the others the gate rows that more than one program holds.  A
+// CTA sums 32 columns with 16 threads each, over 16 contiguous runs of
+// programs, joined in order.
+constexpr int kJoinCols = 32, kJoinRuns = 16;
+
+__global__ void __launch_bounds__(kJoinCols *kJoinRuns)
+    block_norm_join_kernel(const BlockArgs a, long long units, long long gates) {
+    __shared__ float run_sum[kJoinRuns][kJoinCols];
+    const int c = threadIdx.x % kJoinCols, run = threadIdx.x / kJoinCols;
+    const int col = blockIdx.x * kJoinCols + c;
+    // sum over units [u0, u1] of the slot that holds gate row g (g < 0: slot)
+    auto join = [&](long long u0, long long u1, int slot, long long g) {
+        const long long n = u1 - u0 + 1;
+        float t = 0.0f;
+        if (col < a.width) {
+#pragma unroll 4
+            for (long long u = u0 + n * run / kJoinRuns; u < u0 + n * (run + 1) / kJoinRuns; ++u) {
+                int at = slot;
+                if (g >= 0) at = a.rows * u / units / a.per_gate == g ? SLOT_FIRST : SLOT_LAST;
+                t += a.ws[(u * SLOTS + at) * a.width + col];
+            }
+        }
+        run_sum[run][c] = t;
+        __syncthreads();
+        t = 0.0f;
+        for (int i = 0; i < kJoinRuns; ++i) t += run_sum[i][c];
+        __syncthreads();
+        return t;
+    };
+    if (blockIdx.y == 0) {
+        for (int which = 0; which < 2; ++which) {
+            float *to = which == 0 ? a.dgamma_pre : a.dgamma_post;
+            if (to == nullptr) continue;
+            const float t = join(0, units - 1, which == 0 ? SLOT_PRE : SLOT_POST, -1);
+            if (run == 0 && col < a.width) to[col] = t;
+        }
+        return;
+    }
+    for (long long g = blockIdx.y - 1; g < gates; g += gridDim.y - 1) {
+        const long long last = (g + 1) * a.per_gate < a.rows ? (g + 1) * a.per_gate : a.rows;
+        const long long u0 = unit_of_row(g * a.per_gate, a.rows, units);
+        const long long u1 = unit_of_row(last - 1, a.rows, units);
+        if (u0 == u1) continue;   // written by its program
+        const float t = join(u0, u1, 0, g);
+        if (run == 0 && col < a.width) {
+            const float p = a.gamma_post != nullptr ? a.gamma_post[col] : 1.0f;
+            a.dgate[g * a.width + col] = p * t;
+        }
+    }
+}
+
+template <class T, int V, int K, bool CL>
+cudaError_t launch_kernel(const BlockArgs &a, const BlockPlan &p, cudaStream_t stream,
+                          long long *units_out) {
+    static std::atomic<int> per_sm[kMaxDevices][17];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    int occ = per_sm[dev][p.threads / 32].load(std::memory_order_relaxed);
+    if (occ == 0) {
+        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+            &occ, block_norm_backward_kernel<T, V, K, CL>, p.threads, 0);
+        if (err != cudaSuccess) return err;
+        if (occ < 1) occ = 1;
+        per_sm[dev][p.threads / 32].store(occ, std::memory_order_relaxed);
+    }
+    const long long units = units_of(a.rows, sm_count_of_device() * occ / p.cluster);
+    *units_out = units;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(units * p.cluster));
+    cfg.blockDim = dim3(p.threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    if (CL) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = p.cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, block_norm_backward_kernel<T, V, K, CL>, a, p.cluster);
+}
+
+template <class T, int V>
+cudaError_t launch_typed(const BlockArgs &a, cudaStream_t stream, long long *units) {
+    const BlockPlan p = block_plan(a.width);
+    if (p.elems == 8) return launch_kernel<T, V, 8 / V, false>(a, p, stream, units);
+    if (p.elems == 32) return launch_kernel<T, V, 32 / V, true>(a, p, stream, units);
+    return p.cluster > 1 ? launch_kernel<T, V, 16 / V, true>(a, p, stream, units)
+                         : launch_kernel<T, V, 16 / V, false>(a, p, stream, units);
+}
+
+}  // namespace
+
+size_t block_norm_backward_workspace(long long rows, int width) {
+    const long long units = rows < kMaxUnits ? rows : kMaxUnits;
+    return static_cast<size_t>(units) * SLOTS * static_cast<size_t>(width) * sizeof(float);
+}
+
+cudaError_t launch_block_norm_backward(int elem, bool vec, const BlockArgs &args,
+                                       cudaStream_t stream) {
+    BlockArgs a = args;
+    cudaError_t err = cudaSuccess;
+    a.status = status_address(&err);
+    if (a.status == nullptr) return err;
+    long long units = 0;
+    switch (elem) {
+        case ELEM_F32:
+            err = vec ? launch_typed<float, 4>(a, stream, &units)
+                      : launch_typed<float, 1>(a, stream, &units);
+            break;
+        case ELEM_BF16:
+            err = vec ? launch_typed<__nv_bfloat16, 8>(a, stream, &units)
+                      : launch_typed<__nv_bfloat16, 1>(a, stream, &units);
+            break;
+        case ELEM_F16:
+            err = vec ? launch_typed<__half, 8>(a, stream, &units)
+                      : launch_typed<__half, 1>(a, stream, &units);
+            break;
+        default: return cudaErrorInvalidValue;
+    }
+    if (err != cudaSuccess) return err;
+    const long long gates = a.dgate != nullptr ? (a.rows + a.per_gate - 1) / a.per_gate : 0;
+    if (a.dgamma_pre == nullptr && a.dgamma_post == nullptr && gates == 0) return cudaSuccess;
+    const dim3 grid((a.width + kJoinCols - 1) / kJoinCols,
+                    1 + static_cast<unsigned>(gates < 1024 ? gates : 1024));
+    block_norm_join_kernel<<<grid, kJoinCols * kJoinRuns, 0, stream>>>(a, units, gates);
+    return cudaGetLastError();
+}
+
+}  // namespace tile

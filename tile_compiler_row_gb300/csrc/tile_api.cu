@@ -8,10 +8,14 @@
 #include <cstdint>
 #include <mutex>
 
+#include "host_checks.h"
 #include "launch.h"
 #include "plans.h"
 
 namespace {
+
+using tile::misaligned_to;
+using tile::overlaps;
 
 struct PlanDesc {
     int id, V, S, P, K, C;
@@ -202,12 +206,6 @@ void fill_plan(const PlanDesc &p, int op, int dtype, int rows, int width, tile_p
     if (p.staged) out->grid = 0;   // persistent: min(rows, SMs x resident CTAs), device dependent
 }
 
-bool overlaps(const void *a, size_t abytes, const void *b, size_t bbytes) {
-    if (a == nullptr || b == nullptr) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + bbytes && y < x + abytes;
-}
-
 bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 bool valid_op(int op) { return op >= TILE_OP_RESIDUAL_LAYERNORM && op <= TILE_OP_RMSNORM_WEIGHTED; }
@@ -252,10 +250,6 @@ bool coaligned16(const Call &c) {
 // Checks shared by every row entry point.  Returns TILE_OK with *noop set
 // when there is nothing to launch.  No CUDA call is made.
 size_t elem_size(int dtype) { return two_byte(dtype) ? 2 : 4; }
-
-bool misaligned_to(const void *p, size_t bytes) {
-    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
-}
 
 int validate(const Call &c, bool *noop) {
     *noop = false;
@@ -905,7 +899,8 @@ int tile_check_device_status(cudaStream_t stream) {
         tile::status_layernorm_f16, tile::status_rmsnorm_f16, tile::status_softmax_f16,
         tile::status_row_sum_f16, tile::status_row_minmax_f16, tile::status_pairs,
         tile::status_backward, tile::status_backward_bf16, tile::status_backward_f16,
-        tile::status_param_grad, tile::status_staged, tile::status_multi};
+        tile::status_param_grad, tile::status_staged, tile::status_multi,
+        tile::status_block_norm, tile::status_block_norm_backward, tile::status_linear_ce};
     for (auto f : fetch) {
         v = 0;
         const cudaError_t err = f(&v, stream);
