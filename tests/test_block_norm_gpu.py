@@ -126,7 +126,7 @@ def reference_backward(s, hidden, post, pre, per, scale, eps, use_dhidden=True):
 # vectors, warps and CTAs of a row, clusters of 2, 4 and 8, the widest row;
 # row counts below, at and above the programs
 SHAPES = [(1, 1, 0), (3, 7, 2), (1, 8, 1), (5, 63, 0), (37, 64, 10), (200, 257, 7),
-          (1000, 256, 1000), (700, 1537, 100), (9, 4095, 4), (64, 4096, 64), (11, 4104, 0),
+          (1000, 256, 1000), (700, 1537, 100), (64, 2048, 10), (9, 4095, 4), (64, 4096, 64), (11, 4104, 0),
           (6, 8192, 5), (5, 9001, 2), (7, 16384, 3), (3, 20000, 2), (3, 40008, 2), (2, 65536, 1),
           (2, 70001, 0), (2, 131072, 2), (2, 131071, 1), (5000, 136, 17)]
 

@@ -801,64 +801,85 @@ def tile_last_cuda_error():
     return load().tile_last_cuda_error()
 
 
-# ---- block norm --------------------------------------------------------------
+# ---- block norm and linear cross entropy: marshalling ---------------------------
+#
+# A decode step calls these for a few rows at a time, where the host's part of
+# a call is longer than the kernel's: each tensor is checked by one expression,
+# and only a tensor that fails it is looked at again for the message.
 
-def _row_dtype(t, name):
-    """The element type of a row tensor, by the names of DTYPES."""
-    import torch
-    kinds = {torch.float32: "f32", torch.bfloat16: "bf16", torch.float16: "f16"}
-    if not isinstance(t, torch.Tensor) or t.dtype not in kinds:
-        raise ValueError(f"{name} must be a float32, bfloat16 or float16 tensor")
-    return kinds[t.dtype]
+_CODES = {}      # torch dtype -> DTYPES code, filled on first use
 
 
-class _on_device_of:
-    """Makes the device of ``t`` current for a call (its launches, and the
-    stream that ``stream=None`` stands for); every tensor given has to be on
-    it."""
-
-    def __init__(self, t, *others):
+def _row_code(t, name):
+    """The element type code of a row tensor."""
+    if not _CODES:
         import torch
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
-        for o in others:
-            if o is not None and o.device != t.device:
-                raise ValueError(f"tensors must be on one device: {t.device} and {o.device}")
-        self.guard = None
-        if t.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(t.device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        _CODES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    code = _CODES.get(getattr(t, "dtype", None))
+    if code is None:
+        raise ValueError(f"{name} must be a float32, bfloat16 or float16 tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D [rows, width]")
+    return code
 
 
-def _workspace(t):
-    """(pointer, bytes) of a contiguous CUDA workspace tensor."""
+def _ptr(t, name, dtype, shape, dev):
+    """Pointer of a contiguous CUDA tensor of this type and shape on device
+    index ``dev`` (None -> NULL)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev} like the other tensors")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _device_index(t, name):
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    return t.get_device()
+
+
+def _workspace(t, dev):
+    """(pointer, bytes) of a workspace tensor on device index ``dev``."""
+    if not t.is_cuda or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _gates(t, rows, width, rows_per_gate, name):
-    """Pointer of a gate matrix [ceil(rows / rows_per_gate)][width], or None."""
+def _call_on(dev, stream, name, *args):
+    """Calls a C entry point with device ``dev`` current; ``stream`` None is
+    that device's current stream."""
+    import torch
+    fn = getattr(load(), name)
+    if torch._C._cuda_getDevice() == dev:
+        s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+        _check(fn(*args, s), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)), name)
+
+
+# ---- block norm --------------------------------------------------------------
+
+def _gates(t, rows, width, per_gate, dev, name):
+    """Pointer of a gate matrix [ceil(rows / per_gate)][width] (a single gate
+    row may be a vector), or None."""
     import torch
     if t is None:
         return None
-    if rows_per_gate < 1:
+    if per_gate < 1:
         raise ValueError("rows_per_gate must be at least 1 with a gate")
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
-        raise ValueError(f"{name} must be a CUDA float32 tensor")
-    want = (-(-rows // rows_per_gate), width)
-    if not t.is_contiguous() or (tuple(t.shape) != want and not (want[0] == 1 and
-                                                                 tuple(t.shape) == want[1:])):
-        raise ValueError(f"{name} must be contiguous of shape {want}")
-    return t.data_ptr()
+    n = -(-rows // per_gate)
+    return _ptr(t, name, torch.float32, (width,) if n == 1 and t.dim() == 1 else (n, width), dev)
 
 
 def tile_block_norm(x, residual, hidden, out, gamma_post=None, gate=None, gamma_pre=None,
@@ -869,24 +890,18 @@ def tile_block_norm(x, residual, hidden, out, gamma_post=None, gate=None, gamma_
     rows; see ``tile_block_norm`` in include/tile_rows.h.  ``post`` / ``pre``
     switch the norms (without ``pre``, ``out`` is None); ``rows_per_gate``
     0 with a gate stands for all rows."""
-    dt = _row_dtype(x, "x")
-    with _on_device_of(x, residual, hidden, out, gamma_post, gate, gamma_pre):
-        a = TileBlockNormArgs()
-        a.in_, rows, width = _matrix(x, "x", dt)
-        a.rows, a.width, a.dtype = rows, width, DTYPES[dt]
-        a.residual, a.hidden = _matrix(residual, "residual", dt)[0], _matrix(hidden, "hidden", dt)[0]
-        _same_shape(x, residual, "x/residual")
-        _same_shape(x, hidden, "x/hidden")
-        if pre:
-            a.out = _matrix(out, "out", dt)[0]
-            _same_shape(x, out, "x/out")
-        a.rows_per_gate = rows_per_gate or max(rows, 1)
-        a.gamma_post = _vector(gamma_post, width, "gamma_post")
-        a.gate = _gates(gate, rows, width, a.rows_per_gate, "gate")
-        a.gamma_pre = _vector(gamma_pre, width, "gamma_pre")
-        a.norms = (1 if post else 0) | (2 if pre else 0)
-        a.residual_scale, a.eps = residual_scale, eps
-        _check(load().tile_block_norm(ctypes.byref(a), _stream(stream)), "tile_block_norm")
+    import torch
+    code, dev = _row_code(x, "x"), _device_index(x, "x")
+    shape, dt, f32 = x.shape, x.dtype, torch.float32
+    rows, width = shape
+    vec, per = (width,), rows_per_gate or rows or 1
+    a = TileBlockNormArgs(
+        _ptr(x, "x", dt, shape, dev), _ptr(residual, "residual", dt, shape, dev),
+        _ptr(gamma_post, "gamma_post", f32, vec, dev), _gates(gate, rows, width, per, dev, "gate"),
+        _ptr(gamma_pre, "gamma_pre", f32, vec, dev), _ptr(hidden, "hidden", dt, shape, dev),
+        _ptr(out, "out", dt, shape, dev) if pre else None, rows, width, per,
+        (1 if post else 0) | (2 if pre else 0), residual_scale, eps, code)
+    _call_on(dev, stream, "tile_block_norm", ctypes.byref(a))
 
 
 def tile_block_norm_backward_workspace_bytes(rows, width):
@@ -900,50 +915,26 @@ def tile_block_norm_backward(x, hidden, dhidden, dout, din, dresidual, workspace
     """The gradients of ``tile_block_norm`` (see include/tile_rows.h).
     ``hidden`` is the forward's; ``dhidden`` may be None (``dout`` is then
     the only gradient), as may any parameter gradient."""
-    dt = _row_dtype(din, "din")
-    with _on_device_of(din, x, hidden, dhidden, dout, dresidual, workspace, gamma_post, gate,
-                       gamma_pre, dgamma_post, dgate, dgamma_pre):
-        a = TileBlockNormBackwardArgs()
-        a.din, rows, width = _matrix(din, "din", dt)
-        a.rows, a.width, a.dtype = rows, width, DTYPES[dt]
-        for name, t, field in (("x", x, "in_"), ("hidden", hidden, "hidden"),
-                               ("dhidden", dhidden, "dhidden"), ("dout", dout, "dout"),
-                               ("dresidual", dresidual, "dresidual")):
-            if t is not None:
-                setattr(a, field, _matrix(t, name, dt)[0])
-                _same_shape(din, t, f"din/{name}")
-        a.rows_per_gate = rows_per_gate or max(rows, 1)
-        a.gamma_post = _vector(gamma_post, width, "gamma_post")
-        a.gate = _gates(gate, rows, width, a.rows_per_gate, "gate")
-        a.gamma_pre = _vector(gamma_pre, width, "gamma_pre")
-        a.dgamma_post = _vector(dgamma_post, width, "dgamma_post")
-        a.dgate = _gates(dgate, rows, width, a.rows_per_gate, "dgate")
-        a.dgamma_pre = _vector(dgamma_pre, width, "dgamma_pre")
-        a.norms = (1 if post else 0) | (2 if pre else 0)
-        a.residual_scale, a.eps = residual_scale, eps
-        ws, nbytes = _workspace(workspace)
-        _check(load().tile_block_norm_backward(ctypes.byref(a), ws, nbytes, _stream(stream)),
-               "tile_block_norm_backward")
+    import torch
+    code, dev = _row_code(din, "din"), _device_index(din, "din")
+    shape, dt, f32 = din.shape, din.dtype, torch.float32
+    rows, width = shape
+    vec, per = (width,), rows_per_gate or rows or 1
+    a = TileBlockNormBackwardArgs(
+        _ptr(x, "x", dt, shape, dev), _ptr(hidden, "hidden", dt, shape, dev),
+        _ptr(dhidden, "dhidden", dt, shape, dev), _ptr(dout, "dout", dt, shape, dev),
+        _ptr(gamma_post, "gamma_post", f32, vec, dev), _gates(gate, rows, width, per, dev, "gate"),
+        _ptr(gamma_pre, "gamma_pre", f32, vec, dev), _ptr(din, "din", dt, shape, dev),
+        _ptr(dresidual, "dresidual", dt, shape, dev),
+        _ptr(dgamma_post, "dgamma_post", f32, vec, dev),
+        _gates(dgate, rows, width, per, dev, "dgate"),
+        _ptr(dgamma_pre, "dgamma_pre", f32, vec, dev), rows, width, per,
+        (1 if post else 0) | (2 if pre else 0), residual_scale, eps, code)
+    ws, nbytes = _workspace(workspace, dev)
+    _call_on(dev, stream, "tile_block_norm_backward", ctypes.byref(a), ws, nbytes)
 
 
 # ---- linear cross entropy -------------------------------------------------------
-
-def _ce_inputs(x, weight, target):
-    """(dtype name, x, weight, target pointers, rows, width, vocab)."""
-    import torch
-    dt = _row_dtype(x, "x")
-    if dt == "f32":
-        raise ValueError("x must be bfloat16 or float16")
-    px, rows, width = _matrix(x, "x", dt)
-    pw, vocab, w2 = _matrix(weight, "weight", dt)
-    if w2 != width:
-        raise ValueError(f"x/weight: widths {width} and {w2} differ")
-    if not isinstance(target, torch.Tensor) or not target.is_cuda or target.dtype != torch.int64:
-        raise ValueError("target must be a CUDA int64 tensor")
-    if not target.is_contiguous() or target.numel() != rows:
-        raise ValueError(f"target must be contiguous with {rows} elements")
-    return dt, px, pw, target.data_ptr(), rows, width, vocab
-
 
 def tile_linear_cross_entropy_workspace_bytes(rows, width, vocab):
     return load().tile_linear_cross_entropy_workspace_bytes(rows, width, vocab)
@@ -953,36 +944,45 @@ def tile_linear_cross_entropy_backward_workspace_bytes(rows, width, vocab):
     return load().tile_linear_cross_entropy_backward_workspace_bytes(rows, width, vocab)
 
 
+def _ce_inputs(x, weight, target):
+    """(type code, device, x, weight and target pointers, rows, width, vocab)."""
+    import torch
+    code, dev = _row_code(x, "x"), _device_index(x, "x")
+    if code == 0:
+        raise ValueError("x must be bfloat16 or float16")
+    rows, width = x.shape
+    vocab = weight.shape[0]
+    return (code, dev, _ptr(x, "x", x.dtype, x.shape, dev),
+            _ptr(weight, "weight", x.dtype, (vocab, width), dev),
+            _ptr(target, "target", torch.int64, (rows,), dev), rows, width, vocab)
+
+
 def tile_linear_cross_entropy(x, weight, target, loss, lse, workspace, ignore_index=-100,
                               stream=None):
     """loss and log-sum-exp of the rows' logits x weight^T (bfloat16 or
     float16) without keeping them; see include/tile_rows.h."""
-    with _on_device_of(x, weight, target, loss, lse, workspace):
-        dt, px, pw, pt, rows, width, vocab = _ce_inputs(x, weight, target)
-        ws, nbytes = _workspace(workspace)
-        _check(load().tile_linear_cross_entropy(
-            DTYPES[dt], px, pw, pt, _vector(loss, rows, "loss"), _vector(lse, rows, "lse"), rows,
-            width, vocab, ignore_index, ws, nbytes, _stream(stream)), "tile_linear_cross_entropy")
+    import torch
+    code, dev, px, pw, pt, rows, width, vocab = _ce_inputs(x, weight, target)
+    ws, nbytes = _workspace(workspace, dev)
+    _call_on(dev, stream, "tile_linear_cross_entropy", code, px, pw, pt,
+             _ptr(loss, "loss", torch.float32, (rows,), dev),
+             _ptr(lse, "lse", torch.float32, (rows,), dev), rows, width, vocab, ignore_index, ws,
+             nbytes)
 
 
 def tile_linear_cross_entropy_backward(x, weight, target, lse, dloss, dx, dweight, workspace,
                                        ignore_index=-100, stream=None):
     """Gradients of ``tile_linear_cross_entropy`` for the gradient ``dloss``
     of each row's loss; ``dx`` or ``dweight`` may be None."""
-    with _on_device_of(x, weight, target, lse, dloss, dx, dweight, workspace):
-        dt, px, pw, pt, rows, width, vocab = _ce_inputs(x, weight, target)
-        pdx = pdw = None
-        if dx is not None:
-            pdx = _matrix(dx, "dx", dt)[0]
-            _same_shape(x, dx, "x/dx")
-        if dweight is not None:
-            pdw = _matrix(dweight, "dweight", dt)[0]
-            _same_shape(weight, dweight, "weight/dweight")
-        ws, nbytes = _workspace(workspace)
-        _check(load().tile_linear_cross_entropy_backward(
-            DTYPES[dt], px, pw, pt, _vector(lse, rows, "lse"), _vector(dloss, rows, "dloss"), pdx,
-            pdw, rows, width, vocab, ignore_index, ws, nbytes, _stream(stream)),
-            "tile_linear_cross_entropy_backward")
+    import torch
+    code, dev, px, pw, pt, rows, width, vocab = _ce_inputs(x, weight, target)
+    ws, nbytes = _workspace(workspace, dev)
+    _call_on(dev, stream, "tile_linear_cross_entropy_backward", code, px, pw, pt,
+             _ptr(lse, "lse", torch.float32, (rows,), dev),
+             _ptr(dloss, "dloss", torch.float32, (rows,), dev),
+             _ptr(dx, "dx", x.dtype, x.shape, dev),
+             _ptr(dweight, "dweight", x.dtype, weight.shape, dev), rows, width, vocab,
+             ignore_index, ws, nbytes)
 
 
 # ---------------------------------------------------------------------------
@@ -1017,76 +1017,82 @@ def softmax(x, out=None, stream=None):
     return out
 
 
-def _allocating_on(stream):
-    """Makes ``stream`` current, so that what a wrapper allocates belongs to
-    the stream its kernels run on."""
-    import contextlib
+def _on_stream(fn):
+    """A wrapper that allocates runs with its ``stream`` current, so that what
+    it allocates belongs to the stream its kernels run on."""
+    import functools
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        import torch
+        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        with torch.cuda.stream(s):
+            return fn(*args, **kwargs)
+    return call
+
+
+def _scratch(nbytes, like):
     import torch
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return torch.empty(nbytes or 1, dtype=torch.uint8, device=like.device)
 
 
-def _scratch(nbytes, device):
-    import torch
-    return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
-
-
+@_on_stream
 def block_norm(x, residual, gamma_post=None, gate=None, gamma_pre=None, post=True, pre=True,
-               rows_per_gate=0, residual_scale=1.0, eps=1e-5, stream=None):
+               rows_per_gate=0, residual_scale=1.0, eps=1e-5):
     """(hidden, out) of ``tile_block_norm``; out is None without ``pre``."""
     import torch
-    with _allocating_on(stream):
-        hidden = torch.empty_like(x)
-        out = torch.empty_like(x) if pre else None
-        tile_block_norm(x, residual, hidden, out, gamma_post, gate, gamma_pre, post, pre,
-                        rows_per_gate, residual_scale, eps, stream)
+    hidden = torch.empty_like(x)
+    out = torch.empty_like(x) if pre else None
+    tile_block_norm(x, residual, hidden, out, gamma_post, gate, gamma_pre, post, pre,
+                    rows_per_gate, residual_scale, eps)
     return hidden, out
 
 
+@_on_stream
 def block_norm_backward(x, hidden, gamma_post, gate, gamma_pre, dhidden, dout, post=True,
-                        pre=True, rows_per_gate=0, residual_scale=1.0, eps=1e-5, stream=None):
+                        pre=True, rows_per_gate=0, residual_scale=1.0, eps=1e-5):
     """(din, dresidual, dgamma_post, dgate, dgamma_pre) of
     ``tile_block_norm_backward``; the gradients of parameters that are None
     are None."""
     import torch
     like = hidden if hidden is not None else dhidden
-    with _allocating_on(stream):
-        din, dresidual = torch.empty_like(like), torch.empty_like(like)
-        dgamma_post = torch.empty_like(gamma_post) if post and gamma_post is not None else None
-        dgate = torch.empty_like(gate) if gate is not None else None
-        dgamma_pre = torch.empty_like(gamma_pre) if pre and gamma_pre is not None else None
-        ws = _scratch(tile_block_norm_backward_workspace_bytes(*like.shape), like.device)
-        tile_block_norm_backward(x, hidden, dhidden, dout, din, dresidual, ws, gamma_post, gate,
-                                 gamma_pre, dgamma_post, dgate, dgamma_pre, post, pre,
-                                 rows_per_gate, residual_scale, eps, stream)
+    din, dresidual = torch.empty_like(like), torch.empty_like(like)
+    dgamma_post = torch.empty_like(gamma_post) if post and gamma_post is not None else None
+    dgate = torch.empty_like(gate) if gate is not None else None
+    dgamma_pre = torch.empty_like(gamma_pre) if pre and gamma_pre is not None else None
+    ws = _scratch(tile_block_norm_backward_workspace_bytes(*like.shape), like)
+    tile_block_norm_backward(x, hidden, dhidden, dout, din, dresidual, ws, gamma_post, gate,
+                             gamma_pre, dgamma_post, dgate, dgamma_pre, post, pre, rows_per_gate,
+                             residual_scale, eps)
     return din, dresidual, dgamma_post, dgate, dgamma_pre
 
 
-def linear_cross_entropy(x, weight, target, ignore_index=-100, stream=None):
+@_on_stream
+def linear_cross_entropy(x, weight, target, ignore_index=-100):
     """(loss, lse) of ``tile_linear_cross_entropy``, float32, one per row."""
     import torch
-    rows = x.shape[0]
-    with _allocating_on(stream):
-        loss = torch.empty(rows, dtype=torch.float32, device=x.device)
-        lse = torch.empty_like(loss)
-        ws = _scratch(tile_linear_cross_entropy_workspace_bytes(rows, x.shape[1],
-                                                                weight.shape[0]), x.device)
-        tile_linear_cross_entropy(x, weight, target, loss, lse, ws, ignore_index, stream)
+    rows, width = x.shape
+    loss = torch.empty(rows, dtype=torch.float32, device=x.device)
+    lse = torch.empty_like(loss)
+    ws = _scratch(tile_linear_cross_entropy_workspace_bytes(rows, width, weight.shape[0]), x)
+    tile_linear_cross_entropy(x, weight, target, loss, lse, ws, ignore_index)
     return loss, lse
 
 
+@_on_stream
 def linear_cross_entropy_backward(x, weight, target, lse, dloss, ignore_index=-100,
-                                  need_dx=True, need_dweight=True, stream=None):
+                                  need_dx=True, need_dweight=True):
     """(dx, dweight) of ``tile_linear_cross_entropy_backward``."""
     import torch
-    with _allocating_on(stream):
-        dx = torch.empty_like(x) if need_dx else None
-        dweight = torch.empty_like(weight) if need_dweight else None
-        ws = _scratch(tile_linear_cross_entropy_backward_workspace_bytes(
-            x.shape[0], x.shape[1], weight.shape[0]), x.device)
-        tile_linear_cross_entropy_backward(x, weight, target, lse, dloss, dx, dweight, ws,
-                                           ignore_index, stream)
+    rows, width = x.shape
+    dx = torch.empty_like(x) if need_dx else None
+    dweight = torch.empty_like(weight) if need_dweight else None
+    ws = _scratch(tile_linear_cross_entropy_backward_workspace_bytes(rows, width,
+                                                                     weight.shape[0]), x)
+    tile_linear_cross_entropy_backward(x, weight, target, lse, dloss, dx, dweight, ws,
+                                       ignore_index)
     return dx, dweight
 
 

@@ -2,12 +2,9 @@
 // access, and the reduction of a row's partial sums over its threads.
 //
 // A row program is W = 32 * S threads of each of C CTAs (a thread-block
-// cluster when C > 1).  Thread w of CTA rank c owns, of every row it
-// handles, the columns ((k * C + c) * W + w) * V + v, k < K, v < V: the same
-// columns in every row, so that per-column parameters and column sums stay
-// in registers while the program walks over rows.  V is a 16-byte vector
-// (4 FP32 or 8 two-byte elements) or 1 (odd widths, pointers that are not
-// 16-byte aligned).
+// cluster when C > 1); a thread owns E = K * V columns, in K groups of V.  V
+// is a 16-byte vector (4 FP32 or 8 two-byte elements) or 1 (odd widths,
+// pointers that are not 16-byte aligned).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -20,23 +17,36 @@
 
 namespace tile {
 
-// How one row is spread over threads.
-struct BlockPlan {
-    int elems;     // E = K * V elements a thread owns (8, 16 or 32)
-    int threads;   // W per CTA
-    int cluster;   // C
+// Two FP32 values in one packed instruction (PTX mul / fma .rn.f32x2,
+// sm_100 and later), each rounded as by the scalar one: these kernels issue
+// 30 to 60 instructions per element without, and the issue slots bind.
+struct F2 {
+    float x, y;
 };
-
-// 8 elements a thread keep the parameters, the column sums and a prefetched
-// row in registers at 512 threads (4096 columns); wider rows take 16, then a
-// cluster of CTAs, and the widest 32.
-inline BlockPlan block_plan(int width) {
-    auto warps = [](int n) { return (n + 31) / 32 * 32; };
-    if (width <= 8 * 512) return {8, warps((width + 7) / 8), 1};
-    if (width <= 16 * 512) return {16, warps((width + 15) / 16), 1};
-    for (int c = 2; c <= 8; c *= 2)
-        if (width <= 16 * 512 * c) return {16, 512, c};
-    return {32, 512, 8};
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 d;
+    asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 ra, ra, rb, rc;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ F2 both(float v) { return F2{v, v}; }
+template <int N>
+__device__ __forceinline__ F2 pair(const float (&v)[N], int i) {
+    return F2{v[2 * i], v[2 * i + 1]};
+}
+template <int N>
+__device__ __forceinline__ void put(float (&v)[N], int i, F2 p) {
+    v[2 * i] = p.x;
+    v[2 * i + 1] = p.y;
 }
 
 template <class T, int V>
@@ -84,12 +94,25 @@ struct Access {
     __device__ static void store(T *p, const float (&v)[V]) { Elem<T>::store_vec(p, v); }
 };
 
-// V parameters of a column group (FP32, any 4-byte alignment; 1 when p is
-// NULL).
+// V FP32 parameters of a column group, 1 when p is NULL.  Vector accesses
+// (V > 1) take parameters whose rows are aligned to V of them: one load of
+// 16 or 32 bytes, so that a warp reads one contiguous run.
 template <int V>
 __device__ __forceinline__ void load_params(const float *p, int col, float (&v)[V]) {
+    if (p == nullptr) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = p != nullptr ? __ldg(p + col + j) : 1.0f;
+        for (int j = 0; j < V; ++j) v[j] = 1.0f;
+    } else if constexpr (V == 8) {
+        asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+              "=f"(v[7])
+            : "l"(p + col));
+    } else if constexpr (V == 4) {
+        const float4 t = __ldg(reinterpret_cast<const float4 *>(p + col));
+        v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+    } else {
+        v[0] = __ldg(p + col);
+    }
 }
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -120,12 +143,13 @@ __device__ __forceinline__ void row_sum(float (&s)[N], ReduceMem<N> &mem, int &t
 #pragma unroll
             for (int i = 0; i < N; ++i) buf[i * 32 + (threadIdx.x >> 5)] = s[i];
         __syncthreads();
-        // every warp adds the warps' partials (at most 32) in the same tree
-        const int lane = threadIdx.x & 31;
+        // every warp adds the warps' partials (at most 16) in the same tree:
+        // half the power of two that holds them, down to neighbours
+        const int half = warps > 8 ? 8 : warps > 4 ? 4 : warps > 2 ? 2 : 1;
+        const int lane = threadIdx.x & (2 * half - 1);
 #pragma unroll
         for (int i = 0; i < N; ++i) s[i] = lane < warps ? buf[i * 32 + lane] : 0.0f;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
+        for (int d = half; d > 0; d >>= 1)
 #pragma unroll
             for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
     }

@@ -16,11 +16,15 @@ bool valid_dtype(int dtype) {
 }
 size_t elem_size(int dtype) { return dtype == TILE_DTYPE_F32 ? 4 : 2; }
 
-// Whether every pointer of a row matrix allows 16-byte accesses in each row.
-bool vectors(const void *const *p, int n, int width, size_t es) {
+// Whether every row allows vector accesses: 16 bytes of the row matrices,
+// and the FP32 parameters of that many elements in one load.
+bool vectors(const void *const *mats, int nmats, const void *const *params, int nparams, int width,
+             size_t es) {
     if (static_cast<size_t>(width) * es % 16 != 0) return false;
-    for (int i = 0; i < n; ++i)
-        if (misaligned_to(p[i], 16)) return false;
+    for (int i = 0; i < nmats; ++i)
+        if (misaligned_to(mats[i], 16)) return false;
+    for (int i = 0; i < nparams; ++i)
+        if (misaligned_to(params[i], 64 / es)) return false;
     return true;
 }
 
@@ -91,7 +95,8 @@ int tile_block_norm(const tile_block_norm_args_t *args, cudaStream_t stream) {
     if (tile::any_overlap(out, 2, in, 5)) return TILE_ERR_ALIAS;
     const cudaError_t inj = tile::injected_launch_failure();
     if (inj != cudaSuccess) return cuda_status(inj);
-    return cuda_status(tile::launch_block_norm(c.dtype, vectors(mats, 4, c.width, es), a, stream));
+    return cuda_status(tile::launch_block_norm(
+        c.dtype, vectors(mats, 4, params, 3, c.width, es), a, stream));
 }
 
 size_t tile_block_norm_backward_workspace_bytes(int rows, int width) {
@@ -161,8 +166,8 @@ int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *
     if (tile::any_overlap(out, 6, in, 7)) return TILE_ERR_ALIAS;
     const cudaError_t inj = tile::injected_launch_failure();
     if (inj != cudaSuccess) return cuda_status(inj);
-    return cuda_status(
-        tile::launch_block_norm_backward(c.dtype, vectors(mats, 6, c.width, es), a, stream));
+    return cuda_status(tile::launch_block_norm_backward(
+        c.dtype, vectors(mats, 6, params, 3, c.width, es), a, stream));
 }
 
 }  // extern "C"

@@ -18,16 +18,19 @@
 // at its end.  Gate rows that lie within one program's range are written by
 // it; the others, and the gamma sums, are joined in program order by a
 // second kernel, so results do not depend on timing.
-#include "block_norm.cuh"
+//
+// block_norm_ring.cuh is the kernel for all but the widest rows;
+// block_norm_backward_kernel here takes those (above 65536 two-byte or
+// 32768 FP32 columns, where a row of four inputs leaves a cluster of 8 CTAs
+// no room for a second one), each row loaded into registers when its turn
+// comes.
+#include "block_norm_ring.cuh"
 #include "device_status.h"
 
 TILE_DEVICE_STATUS(block_norm_backward)
 
 namespace tile {
 namespace {
-
-// Column sums of a program in the workspace [unit][slot][width].
-enum { SLOT_PRE = 0, SLOT_POST = 1, SLOT_FIRST = 2, SLOT_LAST = 3, SLOTS = 4 };
 
 // Programs of a call: at most this many, each of at least four rows where
 // there are more rows than SMs.
@@ -245,46 +248,78 @@ __global__ void __launch_bounds__(kJoinCols *kJoinRuns)
     }
 }
 
-template <class T, int V, int K, bool CL>
-cudaError_t launch_kernel(const BlockArgs &a, const BlockPlan &p, cudaStream_t stream,
-                          long long *units_out) {
-    static std::atomic<int> per_sm[kMaxDevices][17];
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+// The ring kernel's layout of a row of `width` columns, or cluster 0 where
+// it does not take the row.  A slot holds the four inputs' parts of a row:
+// at most 64 KiB, so that three fit an SM.  16 columns a thread for two-byte
+// rows, 8 for FP32.
+template <class T, int V>
+RingPlan ring_plan(int width) {
+    constexpr int E = sizeof(T) == 2 ? 16 : 8;
+    RingPlan p = {};
+    int c = 1;
+    while (c <= 8 && (width + c - 1) / c > 512 * E) c *= 2;
+    if (c > 8) return p;
+    p.cluster = c;
+    p.workers = ((width + c - 1) / c + 32 * E - 1) / (32 * E) * 32;
+    const int cols = c == 1 ? width : p.workers * E;
+    p.pitch = static_cast<int>((cols * sizeof(T) + 15) / 16 * 16 + (V == 1 ? 16 : 0));
+    // as many CTAs to an SM as registers allow, the ring cut to fit
+    int per_sm = 65536 / (p.workers * 128);
+    per_sm = per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm;
+    p.slots = ((224 << 10) / per_sm - 3072) / (4 * p.pitch);
+    p.slots = p.slots > kRingMost ? kRingMost : p.slots;
+    p.smem = p.slots * 4 * p.pitch;
+    return p;
+}
+
+// Attributes of a kernel on the current device: its shared memory limit
+// raised once, and its CTAs to an SM for a launch shape.
+template <class Kernel>
+cudaError_t occupancy(Kernel kernel, int threads, int smem, int *per_sm) {
+    cudaError_t err = cudaSuccess;
+    if (smem > 40 << 10)   // with the static part above 48 KiB
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    int occ = per_sm[dev][p.threads / 32].load(std::memory_order_relaxed);
-    if (occ == 0) {
-        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-            &occ, block_norm_backward_kernel<T, V, K, CL>, p.threads, 0);
-        if (err != cudaSuccess) return err;
-        if (occ < 1) occ = 1;
-        per_sm[dev][p.threads / 32].store(occ, std::memory_order_relaxed);
-    }
-    const long long units = units_of(a.rows, sm_count_of_device() * occ / p.cluster);
-    *units_out = units;
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kernel, threads, smem);
+    if (err == cudaSuccess && *per_sm < 1) *per_sm = 1;
+    return err;
+}
+
+template <class Kernel, class Plan>
+cudaError_t launch_programs(Kernel kernel, const BlockArgs &a, const Plan &plan, int threads,
+                            int cluster, int smem, cudaStream_t stream, long long *units) {
+    int per_sm = 0;
+    const cudaError_t err = occupancy(kernel, threads, smem, &per_sm);
+    if (err != cudaSuccess) return err;
+    *units = units_of(a.rows, sm_count_of_device() * per_sm / cluster);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(units * p.cluster));
-    cfg.blockDim = dim3(p.threads);
+    cfg.gridDim = dim3(static_cast<unsigned>(*units * cluster));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    if (CL) {
+    if (cluster > 1) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = p.cluster;
+        attr[0].val.clusterDim.x = cluster;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, block_norm_backward_kernel<T, V, K, CL>, a, p.cluster);
+    return cudaLaunchKernelEx(&cfg, kernel, a, plan);
 }
 
 template <class T, int V>
 cudaError_t launch_typed(const BlockArgs &a, cudaStream_t stream, long long *units) {
-    const BlockPlan p = block_plan(a.width);
-    if (p.elems == 8) return launch_kernel<T, V, 8 / V, false>(a, p, stream, units);
-    if (p.elems == 32) return launch_kernel<T, V, 32 / V, true>(a, p, stream, units);
-    return p.cluster > 1 ? launch_kernel<T, V, 16 / V, true>(a, p, stream, units)
-                         : launch_kernel<T, V, 16 / V, false>(a, p, stream, units);
+    constexpr int E = sizeof(T) == 2 ? 16 : 8;
+    const RingPlan p = ring_plan<T, V>(a.width);
+    if (p.cluster == 1)
+        return launch_programs(block_norm_ring_kernel<T, V, E, false>, a, p, p.workers, 1,
+                               p.smem, stream, units);
+    if (p.cluster > 1)
+        return launch_programs(block_norm_ring_kernel<T, V, E, true>, a, p, p.workers,
+                               p.cluster, p.smem, stream, units);
+    return launch_programs(block_norm_backward_kernel<T, V, 32 / V, true>, a, 8, 512, 8, 0, stream,
+                           units);
 }
 
 }  // namespace

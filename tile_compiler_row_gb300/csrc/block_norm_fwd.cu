@@ -1,14 +1,15 @@
 // Block norm, forward: h = a r + gate * post(b), y = pre(h), both norms
 // RMSNorms (v / sqrt(mean v^2 + eps) * gamma), each optional.
 //
-// Bound by DRAM: x and the residual are read once, h and y written once.  A
-// program walks over a contiguous range of rows with gate * gamma_post and
-// gamma_pre of its columns in registers (read for every row they would cost
-// 12 bytes of L2 traffic per element against the 8 of two-byte rows), and
-// loads the next row before it works on the present one.  The mean square of
-// h is taken from the FP32 h that this row's threads hold, not from a
-// combination of sums over x and r, which cancels where the block undoes the
-// residual; y is computed from that h and rounded once.
+// Bound by DRAM: x and the residual are read once, h and y written once.
+// One program a row, and enough of them on an SM that one row's reductions
+// run under the others' loads; 32 two-byte or 16 FP32 columns a thread, as
+// the two reductions cost each thread some 150 instructions whatever it
+// holds.  gate, gamma_post and gamma_pre (12 bytes per element, against 8 of
+// two-byte rows) come from L1, which the programs of an SM share.  The mean
+// square of h is taken from the FP32 h that this row's threads hold, not
+// from a combination of sums over x and r, which cancels where the block
+// undoes the residual; y is computed from that h and rounded once.
 #include "block_norm.cuh"
 #include "device_status.h"
 
@@ -18,156 +19,147 @@ namespace tile {
 namespace {
 
 template <class T, int V, int K, bool CL>
-__global__ void __launch_bounds__(512) block_norm_kernel(const BlockArgs a, int cluster) {
+__global__ void __launch_bounds__(512) block_norm_kernel(const BlockArgs a, int warps, int cluster) {
     using A = Access<T, V>;
+    constexpr int G = V == 1 ? 2 : V, GK = G / V;   // columns handled together, in GK groups
     constexpr int E = K * V;
+    static_assert(K % GK == 0, "whole pairs");
     __shared__ ReduceMem<1> mem;
-    const int W = blockDim.x;
-    const int warps = W >> 5;
+    const int W = warps * 32;
+    const int programs = CL ? 1 : blockDim.x / W;
     const int rank = CL ? static_cast<int>(cluster_rank()) : 0;
-    const long long units = gridDim.x / (CL ? cluster : 1);
-    const long long unit = blockIdx.x / (CL ? cluster : 1);
-    const long long begin = a.rows * unit / units, end = a.rows * (unit + 1) / units;
-    const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
-    T *hid = static_cast<T *>(a.hidden_out), *out = static_cast<T *>(a.out);
+    const int worker = CL ? threadIdx.x : threadIdx.x % W;
+    const long long row = CL ? blockIdx.x / cluster
+                             : static_cast<long long>(blockIdx.x) * programs + threadIdx.x / W;
+    if (row >= a.rows) return;   // whole warps: programs share a CTA only at one warp each
     const float inv_n = 1.0f / static_cast<float>(a.width);
-
-    int col[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        col[k] = ((k * (CL ? cluster : 1) + rank) * W + static_cast<int>(threadIdx.x)) * V;
+    const int step = (CL ? cluster : 1) * W * V, first = (rank * W + worker) * V;
+    const T *x = static_cast<const T *>(a.x) + row * a.width + first;
+    const T *res = static_cast<const T *>(a.residual) + row * a.width + first;
+    T *hid = static_cast<T *>(a.hidden_out) + row * a.width + first;
+    T *out = static_cast<T *>(a.out) + row * a.width + first;
+    const float *gate = a.gate != nullptr ? a.gate + row / a.per_gate * a.width : nullptr;
 
     typename A::Raw xr[K], rr[K];
-    auto fetch = [&](long long row) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (col[k] < a.width) {
-                xr[k] = A::load(x + row * a.width + col[k]);
-                rr[k] = A::load(res + row * a.width + col[k]);
-            }
-    };
-    if (begin < end) fetch(begin);
-
-    float w[E], g2[E];
+    for (int k = 0; k < K; ++k) {
+        xr[k] = rr[k] = typename A::Raw{};
+        if (first + k * step < a.width) {
+            xr[k] = A::load(x + k * step);
+            rr[k] = A::load(res + k * step);
+        }
+    }
+    float v[E];
+    F2 sq = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         float p[V];
-        if (col[k] < a.width) load_params<V>(a.gamma_pre, col[k], p);
+        A::widen(xr[k], p);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            g2[k * V + j] = col[k] < a.width ? p[j] : 0.0f;
-            w[k * V + j] = 0.0f;
-        }
+        for (int j = 0; j < V; ++j) v[k * V + j] = p[j];
     }
-    long long gate_end = begin;   // first row that needs the next gate row
     int turn = 0;
-    for (long long row = begin; row < end; ++row) {
-        if (row == gate_end) {
-            const long long gate_row = row / a.per_gate;
-            gate_end = (gate_row + 1) * a.per_gate;
-            const float *gate = a.gate != nullptr ? a.gate + gate_row * a.width : nullptr;
+    float r1 = 1.0f;
+    if (a.post) {
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (col[k] < a.width) {
-                    float p[V], q[V];
-                    load_params<V>(a.gamma_post, col[k], p);
-                    load_params<V>(gate, col[k], q);
+        for (int i = 0; i < E / 2; ++i) sq = fma2(pair(v, i), pair(v, i), sq);
+        float s[1] = {sq.x + sq.y};
+        row_sum<1, CL>(s, mem, turn, warps, cluster);
+        r1 = inv_sqrt<T>(fmaf(s[0], inv_n, a.eps));
+    }
+    sq = F2{0.0f, 0.0f};
 #pragma unroll
-                    for (int j = 0; j < V; ++j) w[k * V + j] = p[j] * q[j];
-                }
-        }
-        float v[E], r[E];
+    for (int k = 0; k < K; k += GK) {
+        float p[G], q[G], g[G], h[G];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float p[V], q[V];
-            if (col[k] < a.width) {
-                A::widen(xr[k], p);
-                A::widen(rr[k], q);
-            }
+        for (int u = 0; u < GK; ++u) {
+            float pu[V], qu[V], gu[V];
+            A::widen(rr[k + u], gu);
+            const int col = first + (k + u) * step;
+            const bool in = col < a.width;
+            load_params<V>(in ? a.gamma_post : nullptr, col, pu);
+            load_params<V>(in ? gate : nullptr, col, qu);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                v[k * V + j] = col[k] < a.width ? p[j] : 0.0f;
-                r[k * V + j] = col[k] < a.width ? q[j] : 0.0f;
+                p[u * V + j] = pu[j];
+                q[u * V + j] = qu[j];
+                g[u * V + j] = gu[j];
             }
         }
-        if (row + 1 < end) fetch(row + 1);
-        float r1 = 1.0f;
-        if (a.post) {
-            float s[1] = {0.0f};
 #pragma unroll
-            for (int i = 0; i < E; ++i) s[0] = fmaf(v[i], v[i], s[0]);
-            row_sum<1, CL>(s, mem, turn, warps, cluster);
-            r1 = 1.0f / sqrtf(fmaf(s[0], inv_n, a.eps));
+        for (int i = 0; i < G / 2; ++i) {
+            const int at = k * V / 2 + i;
+            const F2 n = mul2(pair(v, at), both(r1));
+            const F2 t = fma2(mul2(pair(p, i), pair(q, i)), n, mul2(pair(g, i), both(a.scale)));
+            sq = fma2(t, t, sq);
+            put(v, at, t);
+            put(h, i, t);
         }
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = fmaf(a.scale, r[i], w[i] * (v[i] * r1));
+        for (int u = 0; u < GK; ++u)
+            if (first + (k + u) * step < a.width) {
+                float o[V];
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (col[k] < a.width) {
-                float p[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) p[j] = v[k * V + j];
-                A::store(hid + row * a.width + col[k], p);
+                for (int j = 0; j < V; ++j) o[j] = h[u * V + j];
+                A::store(hid + (k + u) * step, o);
             }
-        if (a.pre) {
-            float s[1] = {0.0f};
+    }
+    if (a.pre) {
+        float s[1] = {sq.x + sq.y};
+        row_sum<1, CL>(s, mem, turn, warps, cluster);
+        const float r2 = inv_sqrt<T>(fmaf(s[0], inv_n, a.eps));
 #pragma unroll
-            for (int i = 0; i < E; ++i) s[0] = fmaf(v[i], v[i], s[0]);
-            row_sum<1, CL>(s, mem, turn, warps, cluster);
-            const float r2 = 1.0f / sqrtf(fmaf(s[0], inv_n, a.eps));
+        for (int i = 0; i < E / 2; ++i) put(v, i, mul2(pair(v, i), both(r2)));
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (col[k] < a.width) {
-                    float p[V];
+        for (int k = 0; k < K; ++k) {
+            const int col = first + k * step;
+            if (col >= a.width) continue;
+            float p[V];
+            load_params<V>(a.gamma_pre, col, p);
+            if constexpr (V == 1) {
+                p[0] *= v[k];
+            } else {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) p[j] = (v[k * V + j] * r2) * g2[k * V + j];
-                    A::store(out + row * a.width + col[k], p);
-                }
+                for (int i = 0; i < V / 2; ++i)
+                    put(p, i, mul2(pair(v, k * V / 2 + i), pair(p, i)));
+            }
+            A::store(out + k * step, p);
         }
     }
     if constexpr (CL) cluster_barrier();   // peers may still read this CTA's sums
 }
 
-template <class T, int V, int K, bool CL>
-cudaError_t launch_kernel(const BlockArgs &a, const BlockPlan &p, cudaStream_t stream) {
-    static std::atomic<int> per_sm[kMaxDevices][17];
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    int occ = per_sm[dev][p.threads / 32].load(std::memory_order_relaxed);
-    if (occ == 0) {
-        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, block_norm_kernel<T, V, K, CL>,
-                                                            p.threads, 0);
-        if (err != cudaSuccess) return err;
-        if (occ < 1) occ = 1;
-        per_sm[dev][p.threads / 32].store(occ, std::memory_order_relaxed);
-    }
-    long long units = static_cast<long long>(sm_count_of_device()) * occ / p.cluster;
-    if (units > a.rows) units = a.rows;
-    if (units < 1) units = 1;
+template <class T, int V, int E, bool CL>
+cudaError_t launch_kernel(const BlockArgs &a, int cluster, cudaStream_t stream) {
+    const int threads = (a.width + cluster * E * 32 - 1) / (cluster * E * 32) * 32;
+    // rows of one warp share a CTA: 8 of them
+    const int programs = threads == 32 && !CL ? 8 : 1;
+    const long long grid = (a.rows + programs - 1) / programs * cluster;
+    if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(units * p.cluster));
-    cfg.blockDim = dim3(p.threads);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(threads * programs);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     if (CL) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = p.cluster;
+        attr[0].val.clusterDim.x = cluster;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, V, K, CL>, a, p.cluster);
+    return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, V, E / V, CL>, a, threads / 32, cluster);
 }
 
+// One CTA a row up to 512 threads, then a cluster of up to 8, then (FP32 and
+// single elements above 65536 columns) 32 columns a thread.
 template <class T, int V>
 cudaError_t launch_typed(const BlockArgs &a, cudaStream_t stream) {
-    const BlockPlan p = block_plan(a.width);
-    if (p.elems == 8) return launch_kernel<T, V, 8 / V, false>(a, p, stream);
-    if (p.elems == 32) return launch_kernel<T, V, 32 / V, true>(a, p, stream);
-    return p.cluster > 1 ? launch_kernel<T, V, 16 / V, true>(a, p, stream)
-                         : launch_kernel<T, V, 16 / V, false>(a, p, stream);
+    constexpr int E = V == 8 ? 32 : 16;
+    if (a.width <= 512 * E) return launch_kernel<T, V, E, false>(a, 1, stream);
+    for (int c = 2; c <= 8; c *= 2)
+        if (a.width <= 512 * E * c) return launch_kernel<T, V, E, true>(a, c, stream);
+    return launch_kernel<T, V, 32, true>(a, 8, stream);
 }
 
 }  // namespace

@@ -8,8 +8,13 @@
 // of it is the epilogue:
 //
 //   forward    a tile of l is reduced to each row's maximum and sum of
-//              exponentials (and its target's logit), two numbers per tile
-//              and row; a second kernel joins them.
+//              exponentials, two numbers per tile and row; a second kernel
+//              joins them and takes the target's logit as a dot product of
+//              its own, in FP32 FMAs: the tensor cores truncate as they add
+//              (at 4096 columns a logit was off by 1e-5), which an lse mostly
+//              averages out and one logit does not (the loss of 4096 tokens
+//              over 131072 entries was 1.5e-6 off in the 2-norm with the
+//              tile's logit).
 //   backward   in pieces of the vocabulary: l is computed again, turned into
 //              g and kept in 16 bits for this piece only; then dW of the
 //              piece's rows is g^T x, and g W is added to an FP32 dx.
@@ -44,7 +49,7 @@ enum { EPI_LSE, EPI_GRAD, EPI_DWEIGHT, EPI_DX };
 // What a backward call learns on the device before its products.
 struct CeState {
     int valid;        // packed rows
-    float inv_scale;  // 1 / the power of two that dloss was scaled by
+    float unscale;    // what the scaled gradients are multiplied by at the end
 };
 
 struct GemmArgs {
@@ -52,9 +57,7 @@ struct GemmArgs {
     const CeState *state;       // limits m (GRAD, DX) or k (DWEIGHT) to the packed rows
     int bf16;
     // EPI_LSE
-    const long long *target;
     float2 *partial;            // [m][n tiles]
-    float *target_logit;        // [m]
     // EPI_GRAD: packed rows' target, lse log2(e) and scaled dloss
     const int *ptarget;
     const float *plse2, *pdloss;
@@ -225,7 +228,6 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             const bool none = kb_begin(sp) == kb_begin(sp + 1);   // no product was made: zero
             if (EPI == EPI_LSE) {
                 float m = -INFINITY, s = 0.0f;
-                const long long want = row < m_ext ? g.target[row] - col0 : -1;
                 for (int c = 0; c < BN && col0 + c < g.n; c += 32) {
                     float v[32];
                     tmem_load32(d + c, v);
@@ -241,10 +243,6 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) s += ex2(fmaf(v[j], kLog2e, -ref));
                     m = top;
-                    if (want >= c && want < c + 32)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (want == c + j) g.target_logit[row] = v[j];
                 }
                 if (row < m_ext)
                     g.partial[static_cast<long long>(row) * n_tiles + nt] = make_float2(m, s);
@@ -270,7 +268,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                             pack2(g.bf16, v[j + 4], v[j + 5]), pack2(g.bf16, v[j + 6], v[j + 7]));
                 }
             } else if (EPI == EPI_DWEIGHT) {
-                const float f = g.state->inv_scale;
+                const float f = g.state->unscale;
                 unsigned short *to = static_cast<unsigned short *>(g.out) +
                                      static_cast<long long>(row) * g.ld + col0;
                 const bool vec = (g.ld % 8 == 0) && (reinterpret_cast<uintptr_t>(g.out) % 16 == 0);
@@ -333,39 +331,81 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 
 // ---- forward: joining the tiles --------------------------------------------------
 
+template <class T>
+__device__ __forceinline__ float widen16(unsigned int bits) {
+    if constexpr (std::is_same<T, __half>::value)
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+    else
+        return __uint_as_float(bits << 16);
+}
+
+// sum_h x[h] w[h] over the lanes of a warp (every lane gets it).
+template <class T>
+__device__ __forceinline__ float warp_dot(const unsigned short *x, const unsigned short *w, int n,
+                                          int lane) {
+    float t = 0.0f;
+    if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15) == 0) {
+        const int vectors = n / 8;
+#pragma unroll 4
+        for (int i = lane; i < vectors; i += 32) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x) + i);
+            const uint4 b = __ldg(reinterpret_cast<const uint4 *>(w) + i);
+            const unsigned int p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                t = fmaf(widen16<T>(p[j] & 0xffffu), widen16<T>(q[j] & 0xffffu), t);
+                t = fmaf(widen16<T>(p[j] >> 16), widen16<T>(q[j] >> 16), t);
+            }
+        }
+        x += vectors * 8;
+        w += vectors * 8;
+        n -= vectors * 8;
+    }
+    for (int i = lane; i < n; i += 32) t = fmaf(widen16<T>(x[i]), widen16<T>(w[i]), t);
+    for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+    return t;
+}
+
+struct JoinArgs {
+    const float2 *partial;
+    const unsigned short *x, *weight;
+    const long long *target;
+    long long ignore;
+    int rows, width, vocab, n_tiles;
+    float *loss, *lse;
+    unsigned int *status;
+};
+
 // One warp a row: lanes over the n tiles, joined in a fixed tree.
-__global__ void __launch_bounds__(256)
-    join_lse_kernel(const float2 *partial, const float *target_logit, const long long *target,
-                    long long ignore, int rows, int vocab, int n_tiles, float *loss, float *lse,
-                    unsigned int *status) {
+template <class T>
+__global__ void __launch_bounds__(256) join_lse_kernel(const JoinArgs a) {
     const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    const float2 *p = partial + static_cast<long long>(row) * n_tiles;
+    if (row >= a.rows) return;
+    const long long t = a.target[row];
+    if (t == a.ignore) {
+        if (lane == 0) a.loss[row] = a.lse[row] = 0.0f;
+        return;
+    }
+    const float2 *p = a.partial + static_cast<long long>(row) * a.n_tiles;
     float m = -INFINITY;
-    for (int i = lane; i < n_tiles; i += 32) m = fmaxf(m, p[i].x);
+    for (int i = lane; i < a.n_tiles; i += 32) m = fmaxf(m, p[i].x);
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float ref = m == -INFINITY ? 0.0f : m;
     float s = 0.0f;
-    for (int i = lane; i < n_tiles; i += 32) {
+    for (int i = lane; i < a.n_tiles; i += 32) {
         const float2 q = p[i];
-        // a tile of -inf alone has the sum of its ones-at-reference 0
         s += q.y * expf(q.x - ref);
     }
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (lane != 0) return;
-    const long long t = target[row];
-    if (t == ignore) {
-        loss[row] = lse[row] = 0.0f;
-        return;
-    }
     const float log_s = logf(s);
-    lse[row] = m + log_s;
-    if (t < 0 || t >= vocab) {
-        loss[row] = NAN;
-        atomicOr(status, CE_BAD_TARGET);
-    } else {
-        loss[row] = (m - target_logit[row]) + log_s;   // m - l is exact where they are close
-    }
+    const bool in = t >= 0 && t < a.vocab;
+    const float l = in ? warp_dot<T>(a.x + static_cast<long long>(row) * a.width,
+                                     a.weight + t * a.width, a.width, lane)
+                       : NAN;
+    if (lane != 0) return;
+    a.lse[row] = m + log_s;
+    a.loss[row] = (m - l) + log_s;   // m - l is exact where they are close
+    if (!in) atomicOr(a.status, CE_BAD_TARGET);
 }
 
 // ---- backward: packing rows ----------------------------------------------------------
@@ -375,10 +415,14 @@ __device__ __forceinline__ bool counts(long long t, long long ignore, int vocab,
 }
 
 // One CTA: place[i] = position of row i among the rows that count, or -1;
-// row_of, target, lse and dloss of the packed rows.  FP16 gradients are
-// scaled by a power of two that brings the largest |dloss| into
-// [2^14, 2^15): |softmax - onehot| <= 1, so nothing overflows, and what
-// underflows is below 2^-39 of it.
+// row_of, target, lse and dloss of the packed rows.  dloss is held over its
+// largest magnitude: the equal weights of a mean become 1, so that the
+// 16-bit gradients round p - onehot and not its product with, say, 1 / 48,
+// which is off by the same 2^-9 in every row's largest entry (dx of 48 rows
+// was 2.6e-3 off in the 2-norm with dloss in it, 2.0e-3 without; the output's
+// own rounding is 1.7e-3).  FP16 gradients are scaled by 2^15 too: |p -
+// onehot| <= 1, so nothing overflows, and what underflows is below 2^-40 of
+// the largest.
 __global__ void __launch_bounds__(1024)
     place_rows_kernel(const long long *target, const float *lse, const float *dloss,
                       long long ignore, int rows, int vocab, int scaled, CeState *state,
@@ -416,12 +460,9 @@ __global__ void __launch_bounds__(1024)
         total += warp_count[i];
         top = fmaxf(top, warp_top[i]);
     }
-    int e = 0;
-    if (scaled && top > 0.0f) {
-        frexpf(top, &e);   // top = f 2^e, f in [1/2, 1)
-        e = 15 - e;
-        e = e < -100 ? -100 : e > 100 ? 100 : e;
-    }
+    // 32768 / top and top / 32768 are finite and not 0 for any normal top
+    top = fminf(fmaxf(top, 1e-30f), 1e30f);
+    const float full = scaled ? 32768.0f : 1.0f;
     for (int i = begin; i < end; ++i) {
         const long long t = target[i];
         const float dl = dloss[i];
@@ -430,7 +471,7 @@ __global__ void __launch_bounds__(1024)
             row_of[at] = i;
             ptarget[at] = static_cast<int>(t);
             plse2[at] = lse[i] * kLog2e;
-            pdloss[at] = ldexpf(dl, e);
+            pdloss[at] = full * (dl / top);
             ++at;
         } else {
             place[i] = -1;
@@ -438,7 +479,7 @@ __global__ void __launch_bounds__(1024)
     }
     if (tid == 0) {
         state->valid = total;
-        state->inv_scale = ldexpf(1.0f, -e);
+        state->unscale = top / full;
     }
 }
 
@@ -477,7 +518,7 @@ __global__ void __launch_bounds__(256)
     finish_dx_kernel(const float *acc, int splits, long long slice, int acc_ld, const int *place,
                      const CeState *state, int bf16, unsigned short *dx, int rows, int width) {
     const long long n = static_cast<long long>(rows) * width;
-    const float f = state->inv_scale;
+    const float f = state->unscale;
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
         const long long r = i / width;
         const int c = static_cast<int>(i % width);
@@ -572,7 +613,6 @@ bool odd_rows(int width) { return width % 8 != 0; }
 struct ForwardSpace {
     unsigned short *x, *w;
     float2 *partial;
-    float *target_logit;
     size_t bytes;
 };
 
@@ -586,7 +626,6 @@ ForwardSpace forward_space(void *ws, int rows, int width, int vocab) {
         s.w = c.take<unsigned short>(vocab * ld);
     }
     s.partial = c.take<float2>(rows * (up(vocab, BN) / BN));
-    s.target_logit = c.take<float>(rows);
     s.bytes = c.at;
     return s;
 }
@@ -686,14 +725,17 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
     g.n = vocab;
     g.k = width;
     g.bf16 = bf16;
-    g.target = args.target;
     g.partial = s.partial;
-    g.target_logit = s.target_logit;
     g.status = status;
     CE_TRY((launch_gemm<false, false, EPI_LSE>(ma, mb, g, stream)));
-    join_lse_kernel<<<(rows + 7) / 8, 256, 0, stream>>>(
-        s.partial, s.target_logit, args.target, args.ignore, rows, vocab,
-        static_cast<int>(up(vocab, BN) / BN), args.loss, args.lse, status);
+    const JoinArgs j = {s.partial, static_cast<const unsigned short *>(args.x),
+                        static_cast<const unsigned short *>(args.weight), args.target, args.ignore,
+                        rows, width, vocab, static_cast<int>(up(vocab, BN) / BN), args.loss,
+                        args.lse, status};
+    if (bf16)
+        join_lse_kernel<__nv_bfloat16><<<(rows + 7) / 8, 256, 0, stream>>>(j);
+    else
+        join_lse_kernel<__half><<<(rows + 7) / 8, 256, 0, stream>>>(j);
     return cudaGetLastError();
 }
 
