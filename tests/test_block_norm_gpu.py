@@ -128,7 +128,9 @@ def reference_backward(s, hidden, post, pre, per, scale, eps, use_dhidden=True):
 SHAPES = [(1, 1, 0), (3, 7, 2), (1, 8, 1), (5, 63, 0), (37, 64, 10), (200, 257, 7),
           (1000, 256, 1000), (700, 1537, 100), (64, 2048, 10), (9, 4095, 4), (64, 4096, 64), (11, 4104, 0),
           (6, 8192, 5), (5, 9001, 2), (7, 16384, 3), (3, 20000, 2), (3, 40008, 2), (2, 65536, 1),
-          (2, 70001, 0), (2, 131072, 2), (2, 131071, 1), (5000, 136, 17)]
+          (2, 70001, 0), (2, 131072, 2), (2, 131071, 1), (5000, 136, 17),
+          # odd widths with more gate rows than programs keep to
+          (1000, 63, 3), (301, 129, 1), (1100, 68, 1)]
 
 
 @pytest.mark.parametrize("post,pre", [(True, True), (False, True), (True, False)],

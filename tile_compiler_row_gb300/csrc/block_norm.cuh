@@ -17,36 +17,122 @@
 
 namespace tile {
 
-// Two FP32 values in one packed instruction (PTX mul / fma .rn.f32x2,
-// sm_100 and later), each rounded as by the scalar one: these kernels issue
-// 30 to 60 instructions per element without, and the issue slots bind.
-struct F2 {
-    float x, y;
-};
+// Two FP32 values in one 64-bit register pair, for the packed instructions
+// (PTX mul / fma .rn.f32x2, sm_100 and later), each half rounded as by the
+// scalar one: these kernels issued 50 to 66 instructions per element
+// without, and the issue slots bind.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 pack(float lo, float hi) {
+    F2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpack(F2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ F2 both(float v) { return pack(v, v); }
+__device__ __forceinline__ float total(F2 v) {
+    float lo, hi;
+    unpack(v, lo, hi);
+    return lo + hi;
+}
 __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
     F2 d;
-    asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "mul.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     F2 d;
-    asm("{\n\t.reg .b64 ra, rb, rc;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 ra, ra, rb, rc;\n\tmov.b64 {%0, %1}, ra;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
-__device__ __forceinline__ F2 both(float v) { return F2{v, v}; }
-template <int N>
-__device__ __forceinline__ F2 pair(const float (&v)[N], int i) {
-    return F2{v[2 * i], v[2 * i + 1]};
+
+// One 16-byte vector of T as FP32 pairs, and back (rounded to nearest even).
+template <class T>
+struct Vec {
+    static constexpr int N = 16 / sizeof(T), P = N / 2;
+    __device__ static void widen(uint4 t, F2 (&v)[P]) {
+        const unsigned int w[4] = {t.x, t.y, t.z, t.w};
+        if constexpr (sizeof(T) == 4) {
+            v[0] = pack(__uint_as_float(w[0]), __uint_as_float(w[1]));
+            v[1] = pack(__uint_as_float(w[2]), __uint_as_float(w[3]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (std::is_same<T, __half>::value) {
+                    const float2 f = Elem<__half>::widen2(w[i]);
+                    v[i] = pack(f.x, f.y);
+                } else {
+                    v[i] = pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+                }
+            }
+        }
+    }
+    __device__ static uint4 narrow(const F2 (&v)[P]) {
+        unsigned int w[4];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float lo, hi;
+            unpack(v[i], lo, hi);
+            if constexpr (sizeof(T) == 4) {
+                w[2 * i] = __float_as_uint(lo);
+                w[2 * i + 1] = __float_as_uint(hi);
+            } else {
+                w[i] = Elem<T>::narrow2(lo, hi);
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// A vector of a row that lies off the 16-byte grid: `first` is the column of
+// its first element (negative, or so near the width that not all of it is
+// the row's, at the row's ends).
+template <class T>
+__device__ __forceinline__ uint4 mask_vec(uint4 t, int first, int width) {
+    constexpr int N = 16 / sizeof(T);
+    if (first >= 0 && first + N <= width) return t;
+    unsigned int w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (first + j < 0 || first + j >= width) {
+            if constexpr (sizeof(T) == 4)
+                w[j] = 0u;
+            else
+                w[j / 2] &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// Its store: whole, or the elements that are the row's.
+template <class T>
+__device__ __forceinline__ void store_vec_at(T *p, uint4 t, int first, int width) {
+    constexpr int N = 16 / sizeof(T);
+    if (first >= 0 && first + N <= width) {
+        __stcs(reinterpret_cast<uint4 *>(p), t);
+        return;
+    }
+    const unsigned int w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (first + j >= 0 && first + j < width) {
+            if constexpr (sizeof(T) == 4)
+                reinterpret_cast<unsigned int *>(p)[j] = w[j];
+            else
+                reinterpret_cast<unsigned short *>(p)[j] =
+                    static_cast<unsigned short>((j & 1) ? w[j / 2] >> 16 : w[j / 2]);
+        }
+}
+// N parameters from column `first` on, as pairs; 0 outside the row, 1 when p
+// is NULL.
 template <int N>
-__device__ __forceinline__ void put(float (&v)[N], int i, F2 p) {
-    v[2 * i] = p.x;
-    v[2 * i + 1] = p.y;
+__device__ __forceinline__ void params_at(const float *p, int first, int width, F2 (&v)[N / 2]) {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+        const int c = first + 2 * j;
+        const float lo = c < 0 || c >= width ? 0.0f : p == nullptr ? 1.0f : __ldg(p + c);
+        const float hi = c + 1 < 0 || c + 1 >= width ? 0.0f : p == nullptr ? 1.0f : __ldg(p + c + 1);
+        v[j] = pack(lo, hi);
+    }
 }
 
 template <class T, int V>
@@ -177,6 +263,46 @@ __host__ __device__ inline long long unit_of_row(long long r, long long rows, lo
     return u;
 }
 
+// The layout of a program that walks over rows.
+struct RingPlan {
+    int workers;    // W: threads of a CTA
+    int cluster;    // C
+    int slots;      // ring kernel: slots, and bytes of a slot's part for one input
+    int pitch;
+    int smem;
+    int classes;    // row classes by where rows start in a 16-byte block
+    int parts;      // above one class: programs that share a class of a group of rows
+};
+
+// The rows of a program: first, first + step, ...
+struct RowWalk {
+    long long first, count;
+    int step;
+};
+// With one class, contiguous ranges of all rows; with more, programs keep to
+// one group of `group` rows, and to one class there.
+__device__ __forceinline__ RowWalk row_walk(long long rows, long long group, const RingPlan &p,
+                                            long long unit, long long units) {
+    RowWalk w;
+    if (p.classes == 1) {
+        w.first = rows * unit / units;
+        w.count = rows * (unit + 1) / units - w.first;
+        w.step = 1;
+        return w;
+    }
+    const int part = static_cast<int>(unit % p.parts);
+    const int cls = static_cast<int>(unit / p.parts % p.classes);
+    const long long begin = unit / (p.classes * p.parts) * group;
+    const long long end = begin + group < rows ? begin + group : rows;
+    // classes is a power of two
+    const long long first = begin + ((cls - begin) & (p.classes - 1));
+    const long long n = first < end ? (end - 1 - first) / p.classes + 1 : 0;
+    w.first = first + p.classes * (n * part / p.parts);
+    w.count = n * (part + 1) / p.parts - n * part / p.parts;
+    w.step = p.classes;
+    return w;
+}
+
 // One block-norm call (forward and backward); see include/tile_rows.h.
 struct BlockArgs {
     const void *x, *residual, *hidden, *dhidden, *dout;
@@ -192,8 +318,14 @@ struct BlockArgs {
     unsigned int *status;
 };
 
-cudaError_t launch_block_norm(int elem, bool vec, const BlockArgs &a, cudaStream_t stream);
-cudaError_t launch_block_norm_backward(int elem, bool vec, const BlockArgs &a,
+// What the pointers of a call allow: every row and parameter row on vectors;
+// row matrices that start on 16 bytes (rows of any width, parameters of any
+// alignment); neither.
+enum BlockAccess { ACCESS_VECTORS, ACCESS_SHIFTED, ACCESS_ELEMENTS };
+
+cudaError_t launch_block_norm(int elem, BlockAccess access, const BlockArgs &a,
+                              cudaStream_t stream);
+cudaError_t launch_block_norm_backward(int elem, BlockAccess access, const BlockArgs &a,
                                        cudaStream_t stream);
 size_t block_norm_backward_workspace(long long rows, int width);
 

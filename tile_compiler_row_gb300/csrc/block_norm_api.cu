@@ -16,16 +16,15 @@ bool valid_dtype(int dtype) {
 }
 size_t elem_size(int dtype) { return dtype == TILE_DTYPE_F32 ? 4 : 2; }
 
-// Whether every row allows vector accesses: 16 bytes of the row matrices,
-// and the FP32 parameters of that many elements in one load.
-bool vectors(const void *const *mats, int nmats, const void *const *params, int nparams, int width,
-             size_t es) {
-    if (static_cast<size_t>(width) * es % 16 != 0) return false;
+tile::BlockAccess access_of(const void *const *mats, int nmats, const void *const *params,
+                            int nparams, int width, size_t es) {
     for (int i = 0; i < nmats; ++i)
-        if (misaligned_to(mats[i], 16)) return false;
+        if (misaligned_to(mats[i], 16)) return tile::ACCESS_ELEMENTS;
+    if (static_cast<size_t>(width) * es % 16 != 0) return tile::ACCESS_SHIFTED;
+    // the FP32 parameters of 16 bytes of a row are one load
     for (int i = 0; i < nparams; ++i)
-        if (misaligned_to(params[i], 64 / es)) return false;
-    return true;
+        if (misaligned_to(params[i], 64 / es)) return tile::ACCESS_SHIFTED;
+    return tile::ACCESS_VECTORS;
 }
 
 bool any_misaligned(const void *const *p, int n, size_t to) {
@@ -96,7 +95,7 @@ int tile_block_norm(const tile_block_norm_args_t *args, cudaStream_t stream) {
     const cudaError_t inj = tile::injected_launch_failure();
     if (inj != cudaSuccess) return cuda_status(inj);
     return cuda_status(tile::launch_block_norm(
-        c.dtype, vectors(mats, 4, params, 3, c.width, es), a, stream));
+        c.dtype, access_of(mats, 4, params, 3, c.width, es), a, stream));
 }
 
 size_t tile_block_norm_backward_workspace_bytes(int rows, int width) {
@@ -167,7 +166,7 @@ int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *
     const cudaError_t inj = tile::injected_launch_failure();
     if (inj != cudaSuccess) return cuda_status(inj);
     return cuda_status(tile::launch_block_norm_backward(
-        c.dtype, vectors(mats, 6, params, 3, c.width, es), a, stream));
+        c.dtype, access_of(mats, 6, params, 3, c.width, es), a, stream));
 }
 
 }  // extern "C"

@@ -13,17 +13,18 @@
 // w b gy and w b h give every scalar of a row in one reduction round.
 //
 // Bound by DRAM: b, h, dh, dy are read once, db and dresidual written once.
-// A program walks over a contiguous range of rows; parameters and the column
-// sums of its columns stay in registers (FP32), and go to the workspace once
-// at its end.  Gate rows that lie within one program's range are written by
-// it; the others, and the gamma sums, are joined in program order by a
-// second kernel, so results do not depend on timing.
+// A program walks over many rows; parameters and the column sums of its
+// columns stay in registers (FP32), and go to the workspace once at its end.
+// Gate rows that lie within one program's range are written by it; the
+// others, and the gamma sums, are joined in program order by a second
+// kernel, so results do not depend on timing.
 //
-// block_norm_ring.cuh is the kernel for all but the widest rows;
-// block_norm_backward_kernel here takes those (above 65536 two-byte or
-// 32768 FP32 columns, where a row of four inputs leaves a cluster of 8 CTAs
-// no room for a second one), each row loaded into registers when its turn
-// comes.
+// block_norm_ring.cuh is the kernel for nearly every call;
+// block_norm_backward_kernel here takes what that does not: the widest rows
+// (above 65536 two-byte or 32768 FP32 columns, where a row of four inputs
+// leaves a cluster of 8 CTAs no room for a second one), row matrices that
+// are not all 16-byte aligned, and odd widths with more than 128 gate rows.
+// It loads each row into registers when its turn comes.
 #include "block_norm_ring.cuh"
 #include "device_status.h"
 
@@ -66,6 +67,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockArg
     for (int k = 0; k < K; ++k)
         col[k] = ((k * (CL ? cluster : 1) + rank) * W + static_cast<int>(threadIdx.x)) * V;
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float g2[E], w[E], sum_pre[E], sum_post[E], sum_gate[E];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -196,28 +198,32 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockArg
     if constexpr (CL) cluster_barrier();   // peers may still read this CTA's sums
 }
 
-// Joins the programs' column sums, in program order: blockIdx.y 0 the gamma
-// gradients, the others the gate rows that more than one program holds.  A
-// CTA sums 32 columns with 16 threads each, over 16 contiguous runs of
-// programs, joined in order.
+// Joins the programs' column sums, in program order: blockIdx.y 0 and 1 the
+// gamma gradients, the others the gate rows that more than one program
+// holds.  A CTA sums 32 columns with 16 threads each, over 16 contiguous
+// runs of programs, joined in order.  per_gate_units: programs of a gate row
+// where programs keep to one, else 0 (contiguous ranges of rows).
 constexpr int kJoinCols = 32, kJoinRuns = 16;
 
 __global__ void __launch_bounds__(kJoinCols *kJoinRuns)
-    block_norm_join_kernel(const BlockArgs a, long long units, long long gates) {
+    block_norm_join_kernel(const BlockArgs a, long long units, long long gates,
+                           int per_gate_units) {
     __shared__ float run_sum[kJoinRuns][kJoinCols];
     const int c = threadIdx.x % kJoinCols, run = threadIdx.x / kJoinCols;
     const int col = blockIdx.x * kJoinCols + c;
-    // sum over units [u0, u1] of the slot that holds gate row g (g < 0: slot)
-    auto join = [&](long long u0, long long u1, int slot, long long g) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are written
+    // sum of slot `slot0` of unit u0 and slot `slot` of the units after it
+    auto join = [&](long long u0, long long u1, int slot0, int slot) {
         const long long n = u1 - u0 + 1;
         float t = 0.0f;
         if (col < a.width) {
-#pragma unroll 4
-            for (long long u = u0 + n * run / kJoinRuns; u < u0 + n * (run + 1) / kJoinRuns; ++u) {
-                int at = slot;
-                if (g >= 0) at = a.rows * u / units / a.per_gate == g ? SLOT_FIRST : SLOT_LAST;
-                t += a.ws[(u * SLOTS + at) * a.width + col];
-            }
+            const float *p = a.ws + (u0 * SLOTS + slot) * a.width + col;
+            const long long step = static_cast<long long>(SLOTS) * a.width;
+            const int from = static_cast<int>(n * run / kJoinRuns);
+            const int to = static_cast<int>(n * (run + 1) / kJoinRuns);
+#pragma unroll 8
+            for (int u = from; u < to; ++u)
+                t += u == 0 ? p[static_cast<long long>(slot0 - slot) * a.width] : p[u * step];
         }
         run_sum[run][c] = t;
         __syncthreads();
@@ -226,21 +232,27 @@ __global__ void __launch_bounds__(kJoinCols *kJoinRuns)
         __syncthreads();
         return t;
     };
-    if (blockIdx.y == 0) {
-        for (int which = 0; which < 2; ++which) {
-            float *to = which == 0 ? a.dgamma_pre : a.dgamma_post;
-            if (to == nullptr) continue;
-            const float t = join(0, units - 1, which == 0 ? SLOT_PRE : SLOT_POST, -1);
-            if (run == 0 && col < a.width) to[col] = t;
-        }
+    if (blockIdx.y < 2) {
+        float *to = blockIdx.y == 0 ? a.dgamma_pre : a.dgamma_post;
+        const int slot = blockIdx.y == 0 ? SLOT_PRE : SLOT_POST;
+        if (to == nullptr) return;
+        const float t = join(0, units - 1, slot, slot);
+        if (run == 0 && col < a.width) to[col] = t;
         return;
     }
-    for (long long g = blockIdx.y - 1; g < gates; g += gridDim.y - 1) {
-        const long long last = (g + 1) * a.per_gate < a.rows ? (g + 1) * a.per_gate : a.rows;
-        const long long u0 = unit_of_row(g * a.per_gate, a.rows, units);
-        const long long u1 = unit_of_row(last - 1, a.rows, units);
-        if (u0 == u1) continue;   // written by its program
-        const float t = join(u0, u1, 0, g);
+    for (long long g = blockIdx.y - 2; g < gates; g += gridDim.y - 2) {
+        long long u0 = g * per_gate_units, u1 = u0 + per_gate_units - 1;
+        int slot0 = SLOT_FIRST;
+        if (per_gate_units == 0) {
+            const long long end = (g + 1) * a.per_gate < a.rows ? (g + 1) * a.per_gate : a.rows;
+            u0 = unit_of_row(g * a.per_gate, a.rows, units);
+            u1 = unit_of_row(end - 1, a.rows, units);
+            if (u0 == u1) continue;   // written by its program
+            // the gate row is its first program's first, or its last, and
+            // the first of every other program
+            if (a.rows * u0 / units < g * a.per_gate) slot0 = SLOT_LAST;
+        }
+        const float t = join(u0, u1, slot0, SLOT_FIRST);
         if (run == 0 && col < a.width) {
             const float p = a.gamma_post != nullptr ? a.gamma_post[col] : 1.0f;
             a.dgate[g * a.width + col] = p * t;
@@ -250,25 +262,30 @@ __global__ void __launch_bounds__(kJoinCols *kJoinRuns)
 
 // The ring kernel's layout of a row of `width` columns, or cluster 0 where
 // it does not take the row.  A slot holds the four inputs' parts of a row:
-// at most 64 KiB, so that three fit an SM.  16 columns a thread for two-byte
-// rows, 8 for FP32.
-template <class T, int V>
+// at most 64 KiB, so that three fit an SM.  Two vectors a thread: 16 columns
+// of two-byte rows, 8 of FP32.
+constexpr int kRingVecs = 2;
+
+template <class T, bool SHIFT>
 RingPlan ring_plan(int width) {
-    constexpr int E = sizeof(T) == 2 ? 16 : 8;
+    constexpr int N = Vec<T>::N, K = kRingVecs;
     RingPlan p = {};
+    // vectors that hold a row, wherever it starts
+    const int vecs = (width + (SHIFT ? N - 1 : 0) + N - 1) / N;
     int c = 1;
-    while (c <= 8 && (width + c - 1) / c > 512 * E) c *= 2;
+    while (c <= 8 && (vecs + c - 1) / c > 512 * K) c *= 2;
     if (c > 8) return p;
     p.cluster = c;
-    p.workers = ((width + c - 1) / c + 32 * E - 1) / (32 * E) * 32;
-    const int cols = c == 1 ? width : p.workers * E;
-    p.pitch = static_cast<int>((cols * sizeof(T) + 15) / 16 * 16 + (V == 1 ? 16 : 0));
+    p.workers = ((vecs + c - 1) / c + 32 * K - 1) / (32 * K) * 32;
+    p.pitch = (c == 1 ? vecs : p.workers * K) * 16;
     // as many CTAs to an SM as registers allow, the ring cut to fit
     int per_sm = 65536 / (p.workers * 128);
     per_sm = per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm;
     p.slots = ((224 << 10) / per_sm - 3072) / (4 * p.pitch);
     p.slots = p.slots > kRingMost ? kRingMost : p.slots;
     p.smem = p.slots * 4 * p.pitch;
+    p.classes = 1;
+    while (SHIFT && static_cast<long long>(p.classes) * width % N != 0) p.classes *= 2;
     return p;
 }
 
@@ -286,14 +303,10 @@ cudaError_t occupancy(Kernel kernel, int threads, int smem, int *per_sm) {
 }
 
 template <class Kernel, class Plan>
-cudaError_t launch_programs(Kernel kernel, const BlockArgs &a, const Plan &plan, int threads,
-                            int cluster, int smem, cudaStream_t stream, long long *units) {
-    int per_sm = 0;
-    const cudaError_t err = occupancy(kernel, threads, smem, &per_sm);
-    if (err != cudaSuccess) return err;
-    *units = units_of(a.rows, sm_count_of_device() * per_sm / cluster);
+cudaError_t launch_programs(Kernel kernel, const BlockArgs &a, const Plan &plan, long long units,
+                            int threads, int cluster, int smem, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(*units * cluster));
+    cfg.gridDim = dim3(static_cast<unsigned>(units * cluster));
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -308,56 +321,107 @@ cudaError_t launch_programs(Kernel kernel, const BlockArgs &a, const Plan &plan,
     return cudaLaunchKernelEx(&cfg, kernel, a, plan);
 }
 
-template <class T, int V>
-cudaError_t launch_typed(const BlockArgs &a, cudaStream_t stream, long long *units) {
-    constexpr int E = sizeof(T) == 2 ? 16 : 8;
-    const RingPlan p = ring_plan<T, V>(a.width);
-    if (p.cluster == 1)
-        return launch_programs(block_norm_ring_kernel<T, V, E, false>, a, p, p.workers, 1,
-                               p.smem, stream, units);
-    if (p.cluster > 1)
-        return launch_programs(block_norm_ring_kernel<T, V, E, true>, a, p, p.workers,
-                               p.cluster, p.smem, stream, units);
-    return launch_programs(block_norm_backward_kernel<T, V, 32 / V, true>, a, 8, 512, 8, 0, stream,
-                           units);
+// What the join needs to know of the programs.
+struct Programs {
+    long long units;
+    int per_gate;   // programs of a gate row, 0: contiguous ranges of rows
+};
+
+template <class Kernel>
+cudaError_t launch_ring(Kernel kernel, const BlockArgs &a, RingPlan p, cudaStream_t stream,
+                        Programs *out) {
+    int per_sm = 0;
+    const cudaError_t err = occupancy(kernel, p.workers, p.smem, &per_sm);
+    if (err != cudaSuccess) return err;
+    const long long room = static_cast<long long>(sm_count_of_device()) * per_sm / p.cluster;
+    if (p.classes == 1) {
+        *out = {units_of(a.rows, room), 0};
+    } else {
+        const long long gates = (a.rows + a.per_gate - 1) / a.per_gate;
+        long long parts = units_of(a.rows, room) / (gates * p.classes);
+        p.parts = parts < 1 ? 1 : static_cast<int>(parts);
+        *out = {gates * p.classes * p.parts, p.classes * p.parts};
+    }
+    return launch_programs(kernel, a, p, out->units, p.workers, p.cluster, p.smem, stream);
+}
+
+template <class T, bool SHIFT>
+cudaError_t launch_ring_typed(const BlockArgs &a, const RingPlan &p, cudaStream_t stream,
+                              Programs *out) {
+    return p.cluster == 1
+               ? launch_ring(block_norm_ring_kernel<T, kRingVecs, SHIFT, false>, a, p, stream, out)
+               : launch_ring(block_norm_ring_kernel<T, kRingVecs, SHIFT, true>, a, p, stream, out);
+}
+
+template <class T, int V, int E, bool CL>
+cudaError_t launch_registers(const BlockArgs &a, cudaStream_t stream, Programs *out) {
+    const int cluster = CL ? 8 : 1;
+    const int threads = (a.width + cluster * E * 32 - 1) / (cluster * E * 32) * 32;
+    int per_sm = 0;
+    const cudaError_t err = occupancy(block_norm_backward_kernel<T, V, E / V, CL>, threads, 0, &per_sm);
+    if (err != cudaSuccess) return err;
+    const long long room = static_cast<long long>(sm_count_of_device()) * per_sm / cluster;
+    *out = {units_of(a.rows, room), 0};
+    return launch_programs(block_norm_backward_kernel<T, V, E / V, CL>, a, cluster, out->units,
+                           threads, cluster, 0, stream);
+}
+
+template <class T>
+cudaError_t launch_typed(const BlockArgs &a, BlockAccess access, cudaStream_t stream,
+                         Programs *out) {
+    constexpr int N = Vec<T>::N;
+    if (access == ACCESS_VECTORS) {
+        const RingPlan p = ring_plan<T, false>(a.width);
+        if (p.cluster > 0) return launch_ring_typed<T, false>(a, p, stream, out);
+        return launch_registers<T, N, 32, true>(a, stream, out);
+    }
+    if (access == ACCESS_SHIFTED) {
+        const RingPlan p = ring_plan<T, true>(a.width);
+        const long long gates = (a.rows + a.per_gate - 1) / a.per_gate;
+        if (p.cluster > 0 && (p.classes == 1 || gates * p.classes <= kMaxUnits))
+            return launch_ring_typed<T, true>(a, p, stream, out);
+    }
+    if (a.width <= 512 * 16) return launch_registers<T, 1, 16, false>(a, stream, out);
+    return launch_registers<T, 1, 32, true>(a, stream, out);
 }
 
 }  // namespace
 
 size_t block_norm_backward_workspace(long long rows, int width) {
-    const long long units = rows < kMaxUnits ? rows : kMaxUnits;
+    // programs that keep to a row class of a gate row may be more than rows
+    const long long units = 8 * rows < kMaxUnits ? 8 * rows : kMaxUnits;
     return static_cast<size_t>(units) * SLOTS * static_cast<size_t>(width) * sizeof(float);
 }
 
-cudaError_t launch_block_norm_backward(int elem, bool vec, const BlockArgs &args,
+cudaError_t launch_block_norm_backward(int elem, BlockAccess access, const BlockArgs &args,
                                        cudaStream_t stream) {
     BlockArgs a = args;
     cudaError_t err = cudaSuccess;
     a.status = status_address(&err);
     if (a.status == nullptr) return err;
-    long long units = 0;
+    Programs programs = {};
     switch (elem) {
-        case ELEM_F32:
-            err = vec ? launch_typed<float, 4>(a, stream, &units)
-                      : launch_typed<float, 1>(a, stream, &units);
-            break;
-        case ELEM_BF16:
-            err = vec ? launch_typed<__nv_bfloat16, 8>(a, stream, &units)
-                      : launch_typed<__nv_bfloat16, 1>(a, stream, &units);
-            break;
-        case ELEM_F16:
-            err = vec ? launch_typed<__half, 8>(a, stream, &units)
-                      : launch_typed<__half, 1>(a, stream, &units);
-            break;
+        case ELEM_F32: err = launch_typed<float>(a, access, stream, &programs); break;
+        case ELEM_BF16: err = launch_typed<__nv_bfloat16>(a, access, stream, &programs); break;
+        case ELEM_F16: err = launch_typed<__half>(a, access, stream, &programs); break;
         default: return cudaErrorInvalidValue;
     }
     if (err != cudaSuccess) return err;
     const long long gates = a.dgate != nullptr ? (a.rows + a.per_gate - 1) / a.per_gate : 0;
     if (a.dgamma_pre == nullptr && a.dgamma_post == nullptr && gates == 0) return cudaSuccess;
-    const dim3 grid((a.width + kJoinCols - 1) / kJoinCols,
-                    1 + static_cast<unsigned>(gates < 1024 ? gates : 1024));
-    block_norm_join_kernel<<<grid, kJoinCols * kJoinRuns, 0, stream>>>(a, units, gates);
-    return cudaGetLastError();
+    // launched while the programs run (it waits for their end itself)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.width + kJoinCols - 1) / kJoinCols,
+                       2 + static_cast<unsigned>(gates < 1024 ? gates : 1024));
+    cfg.blockDim = dim3(kJoinCols * kJoinRuns);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, block_norm_join_kernel, a, programs.units, gates,
+                              programs.per_gate);
 }
 
 }  // namespace tile

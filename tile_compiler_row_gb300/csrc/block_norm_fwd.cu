@@ -49,28 +49,34 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const BlockArgs a, int 
             rr[k] = A::load(res + k * step);
         }
     }
-    float v[E];
-    F2 sq = {0.0f, 0.0f};
+    F2 v[E / 2], sq = 0;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        float p[V];
-        A::widen(xr[k], p);
+    for (int k = 0; k < K; k += GK) {
+        float p[G];
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[k * V + j] = p[j];
+        for (int u = 0; u < GK; ++u) {
+            float q[V];
+            A::widen(xr[k + u], q);
+#pragma unroll
+            for (int j = 0; j < V; ++j) p[u * V + j] = q[j];
+        }
+#pragma unroll
+        for (int i = 0; i < G / 2; ++i) v[k * V / 2 + i] = pack(p[2 * i], p[2 * i + 1]);
     }
     int turn = 0;
     float r1 = 1.0f;
     if (a.post) {
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) sq = fma2(pair(v, i), pair(v, i), sq);
-        float s[1] = {sq.x + sq.y};
+        for (int i = 0; i < E / 2; ++i) sq = fma2(v[i], v[i], sq);
+        float s[1] = {total(sq)};
         row_sum<1, CL>(s, mem, turn, warps, cluster);
         r1 = inv_sqrt<T>(fmaf(s[0], inv_n, a.eps));
     }
-    sq = F2{0.0f, 0.0f};
+    sq = 0;
+    const F2 r1s = both(r1), scale = both(a.scale);
 #pragma unroll
     for (int k = 0; k < K; k += GK) {
-        float p[G], q[G], g[G], h[G];
+        float p[G], q[G], g[G];
 #pragma unroll
         for (int u = 0; u < GK; ++u) {
             float pu[V], qu[V], gu[V];
@@ -88,45 +94,218 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const BlockArgs a, int 
         }
 #pragma unroll
         for (int i = 0; i < G / 2; ++i) {
-            const int at = k * V / 2 + i;
-            const F2 n = mul2(pair(v, at), both(r1));
-            const F2 t = fma2(mul2(pair(p, i), pair(q, i)), n, mul2(pair(g, i), both(a.scale)));
-            sq = fma2(t, t, sq);
-            put(v, at, t);
-            put(h, i, t);
+            F2 &at = v[k * V / 2 + i];
+            const F2 w = mul2(pack(p[2 * i], p[2 * i + 1]), pack(q[2 * i], q[2 * i + 1]));
+            at = fma2(w, mul2(at, r1s), mul2(pack(g[2 * i], g[2 * i + 1]), scale));
+            sq = fma2(at, at, sq);
+            unpack(at, g[2 * i], g[2 * i + 1]);
         }
 #pragma unroll
         for (int u = 0; u < GK; ++u)
             if (first + (k + u) * step < a.width) {
                 float o[V];
 #pragma unroll
-                for (int j = 0; j < V; ++j) o[j] = h[u * V + j];
+                for (int j = 0; j < V; ++j) o[j] = g[u * V + j];
                 A::store(hid + (k + u) * step, o);
             }
     }
     if (a.pre) {
-        float s[1] = {sq.x + sq.y};
+        float s[1] = {total(sq)};
         row_sum<1, CL>(s, mem, turn, warps, cluster);
-        const float r2 = inv_sqrt<T>(fmaf(s[0], inv_n, a.eps));
+        const F2 r2 = both(inv_sqrt<T>(fmaf(s[0], inv_n, a.eps)));
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) put(v, i, mul2(pair(v, i), both(r2)));
+        for (int k = 0; k < K; k += GK) {
+            float p[G];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int col = first + k * step;
-            if (col >= a.width) continue;
-            float p[V];
-            load_params<V>(a.gamma_pre, col, p);
-            if constexpr (V == 1) {
-                p[0] *= v[k];
-            } else {
+            for (int u = 0; u < GK; ++u) {
+                float q[V];
+                const int col = first + (k + u) * step;
+                load_params<V>(col < a.width ? a.gamma_pre : nullptr, col, q);
 #pragma unroll
-                for (int i = 0; i < V / 2; ++i)
-                    put(p, i, mul2(pair(v, k * V / 2 + i), pair(p, i)));
+                for (int j = 0; j < V; ++j) p[u * V + j] = q[j];
             }
-            A::store(out + k * step, p);
+#pragma unroll
+            for (int i = 0; i < G / 2; ++i)
+                unpack(mul2(mul2(v[k * V / 2 + i], r2), pack(p[2 * i], p[2 * i + 1])), p[2 * i],
+                       p[2 * i + 1]);
+#pragma unroll
+            for (int u = 0; u < GK; ++u)
+                if (first + (k + u) * step < a.width) {
+                    float o[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) o[j] = p[u * V + j];
+                    A::store(out + (k + u) * step, o);
+                }
         }
     }
     if constexpr (CL) cluster_barrier();   // peers may still read this CTA's sums
+}
+
+// Rows that are not whole vectors: a program takes rows that start at the
+// same offset into a 16-byte block (every second, fourth or eighth), so each
+// thread reads and writes the same aligned vectors of them and owns the same
+// columns, whose parameters it keeps in registers (from L1 they would be
+// single-element loads); the vectors at a row's ends are masked.  The next
+// row is loaded before the present one is worked on.  Single-element
+// accesses (the kernel above with V = 1) ran 16384 x 4097 BF16 in 291 us.
+template <class T, int K, bool CL>
+__global__ void __launch_bounds__(512)
+    block_norm_shift_kernel(const BlockArgs a, const RingPlan plan) {
+    using X = Vec<T>;
+    constexpr int N = X::N, P = X::P;
+    __shared__ ReduceMem<1> mem;
+    const int W = plan.workers, warps = W >> 5, tid = threadIdx.x;
+    const int C = CL ? plan.cluster : 1;
+    const int rank = CL ? static_cast<int>(cluster_rank()) : 0;
+    const int width = a.width;
+    const RowWalk walk = row_walk(a.rows, a.rows, plan, blockIdx.x / C, gridDim.x / C);
+    const int shift = static_cast<int>((walk.first * width) & (N - 1));
+    const int vecs = (width + shift + N - 1) / N;
+    auto vec = [&](int k) { return rank * W * K + k * W + tid; };
+    auto first = [&](int k) { return vec(k) * N - shift; };   // column of vector k
+    const float inv_n = 1.0f / static_cast<float>(width);
+    const long long size = a.rows * width;
+    const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
+    auto load = [&](const T *p, long long row, int k) {
+        const long long at = row * width + first(k);
+        if (at + N <= size) return __ldcs(reinterpret_cast<const uint4 *>(p + at));
+        unsigned int w[4] = {};   // the matrix ends in this block
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (at + j < size) {
+                if constexpr (sizeof(T) == 4)
+                    w[j] = reinterpret_cast<const unsigned int *>(p + at)[j];
+                else
+                    w[j / 2] |= static_cast<unsigned int>(
+                                    reinterpret_cast<const unsigned short *>(p + at)[j])
+                                << (16 * (j & 1));
+            }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    uint4 xr[K], rr[K];
+    auto fetch = [&](long long row) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (vec(k) < vecs) {
+                xr[k] = load(x, row, k);
+                rr[k] = load(res, row, k);
+            }
+    };
+    if (walk.count > 0) fetch(walk.first);
+    F2 w[K * P], g2[K * P];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        F2 p[P];
+        params_at<N>(a.gamma_pre, first(k), width, p);
+#pragma unroll
+        for (int i = 0; i < P; ++i) g2[k * P + i] = p[i];
+    }
+    long long gate_end = walk.first;
+    int turn = 0;
+    const F2 scale = both(a.scale);
+    for (long long i_row = 0; i_row < walk.count; ++i_row) {
+        const long long row = walk.first + i_row * walk.step;
+        if (row >= gate_end) {
+            const long long gate_row = row / a.per_gate;
+            gate_end = (gate_row + 1) * a.per_gate;
+            const float *gate = a.gate != nullptr ? a.gate + gate_row * width : nullptr;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                F2 p[P], q[P];
+                params_at<N>(a.gamma_post, first(k), width, p);
+                params_at<N>(gate, first(k), width, q);
+#pragma unroll
+                for (int i = 0; i < P; ++i) w[k * P + i] = mul2(p[i], q[i]);
+            }
+        }
+        F2 v[K * P], r[K * P], sq = 0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            uint4 p = make_uint4(0, 0, 0, 0), q = p;
+            if (vec(k) < vecs) {
+                p = mask_vec<T>(xr[k], first(k), width);
+                q = mask_vec<T>(rr[k], first(k), width);
+            }
+            F2 t[P], u[P];
+            X::widen(p, t);
+            X::widen(q, u);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                v[k * P + i] = t[i];
+                r[k * P + i] = mul2(u[i], scale);
+            }
+        }
+        if (i_row + 1 < walk.count) fetch(row + walk.step);
+        float r1 = 1.0f;
+        if (a.post) {
+#pragma unroll
+            for (int i = 0; i < K * P; ++i) sq = fma2(v[i], v[i], sq);
+            float s[1] = {total(sq)};
+            row_sum<1, CL>(s, mem, turn, warps, C);
+            r1 = inv_sqrt<T>(fmaf(s[0], inv_n, a.eps));
+        }
+        const F2 r1s = both(r1);
+        sq = 0;
+#pragma unroll
+        for (int i = 0; i < K * P; ++i) {
+            v[i] = fma2(w[i], mul2(v[i], r1s), r[i]);
+            sq = fma2(v[i], v[i], sq);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (vec(k) < vecs) {
+                F2 t[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i) t[i] = v[k * P + i];
+                store_vec_at<T>(static_cast<T *>(a.hidden_out) + row * width + first(k),
+                                X::narrow(t), first(k), width);
+            }
+        if (a.pre) {
+            float s[1] = {total(sq)};
+            row_sum<1, CL>(s, mem, turn, warps, C);
+            const F2 r2 = both(inv_sqrt<T>(fmaf(s[0], inv_n, a.eps)));
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (vec(k) < vecs) {
+                    F2 t[P];
+#pragma unroll
+                    for (int i = 0; i < P; ++i)
+                        t[i] = mul2(mul2(v[k * P + i], r2), g2[k * P + i]);
+                    store_vec_at<T>(static_cast<T *>(a.out) + row * width + first(k), X::narrow(t),
+                                    first(k), width);
+                }
+        }
+    }
+    if constexpr (CL) cluster_barrier();   // peers may still read this CTA's sums
+}
+
+template <class T, bool CL>
+cudaError_t launch_shift(const BlockArgs &a, RingPlan p, cudaStream_t stream) {
+    constexpr int N = Vec<T>::N, K = 2;
+    int occ = 0;
+    cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        &occ, block_norm_shift_kernel<T, K, CL>, p.workers, 0);
+    if (err != cudaSuccess) return err;
+    p.classes = 1;
+    while (static_cast<long long>(p.classes) * a.width % N != 0) p.classes *= 2;
+    const long long room = static_cast<long long>(sm_count_of_device()) * (occ < 1 ? 1 : occ) / p.cluster;
+    const long long most = (a.rows + p.classes - 1) / p.classes;   // rows of a class
+    long long parts = room / p.classes;
+    parts = parts > most ? most : parts < 1 ? 1 : parts;
+    p.parts = static_cast<int>(parts);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(parts * p.classes * p.cluster));
+    cfg.blockDim = dim3(p.workers);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    if (CL) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = p.cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, block_norm_shift_kernel<T, K, CL>, a, p);
 }
 
 template <class T, int V, int E, bool CL>
@@ -154,7 +333,7 @@ cudaError_t launch_kernel(const BlockArgs &a, int cluster, cudaStream_t stream) 
 // One CTA a row up to 512 threads, then a cluster of up to 8, then (FP32 and
 // single elements above 65536 columns) 32 columns a thread.
 template <class T, int V>
-cudaError_t launch_typed(const BlockArgs &a, cudaStream_t stream) {
+cudaError_t launch_rows(const BlockArgs &a, cudaStream_t stream) {
     constexpr int E = V == 8 ? 32 : 16;
     if (a.width <= 512 * E) return launch_kernel<T, V, E, false>(a, 1, stream);
     for (int c = 2; c <= 8; c *= 2)
@@ -162,21 +341,36 @@ cudaError_t launch_typed(const BlockArgs &a, cudaStream_t stream) {
     return launch_kernel<T, V, 32, true>(a, 8, stream);
 }
 
+template <class T>
+cudaError_t launch_typed(const BlockArgs &a, BlockAccess access, cudaStream_t stream) {
+    constexpr int N = Vec<T>::N;
+    if (access == ACCESS_VECTORS) return launch_rows<T, N>(a, stream);
+    if (access == ACCESS_SHIFTED) {
+        const int vecs = (a.width + N - 1 + N - 1) / N;   // wherever a row starts
+        for (int c = 1; c <= 8; c *= 2)
+            if (vecs <= 2 * 512 * c) {
+                RingPlan p = {};
+                p.cluster = c;
+                p.workers = ((vecs + c - 1) / c + 63) / 64 * 32;
+                return c == 1 ? launch_shift<T, false>(a, p, stream)
+                              : launch_shift<T, true>(a, p, stream);
+            }
+    }
+    return launch_rows<T, 1>(a, stream);
+}
+
 }  // namespace
 
-cudaError_t launch_block_norm(int elem, bool vec, const BlockArgs &args, cudaStream_t stream) {
+cudaError_t launch_block_norm(int elem, BlockAccess access, const BlockArgs &args,
+                              cudaStream_t stream) {
     BlockArgs a = args;
     cudaError_t err = cudaSuccess;
     a.status = status_address(&err);
     if (a.status == nullptr) return err;
     switch (elem) {
-        case ELEM_F32:
-            return vec ? launch_typed<float, 4>(a, stream) : launch_typed<float, 1>(a, stream);
-        case ELEM_BF16:
-            return vec ? launch_typed<__nv_bfloat16, 8>(a, stream)
-                       : launch_typed<__nv_bfloat16, 1>(a, stream);
-        case ELEM_F16:
-            return vec ? launch_typed<__half, 8>(a, stream) : launch_typed<__half, 1>(a, stream);
+        case ELEM_F32: return launch_typed<float>(a, access, stream);
+        case ELEM_BF16: return launch_typed<__nv_bfloat16>(a, access, stream);
+        case ELEM_F16: return launch_typed<__half>(a, access, stream);
         default: return cudaErrorInvalidValue;
     }
 }
