@@ -435,8 +435,8 @@ int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *
  * the products of 16-bit elements are exact, and every sum is FP32.  (FP32
  * operands are refused with TILE_ERR_DTYPE: the tensor cores would round
  * them.)  target: [rows] 64-bit integers on the device.  A target that is
- * neither ignore_index nor in [0, vocab) gives that row a NaN loss and sets
- * the device status word (tile_check_device_status).
+ * neither ignore_index nor in [0, vocab) gives that row a NaN loss, an lse
+ * of 0, and sets the device status word (tile_check_device_status).
  *
  * `workspace`: device memory of the caller, 256-byte aligned, at least
  * tile_linear_cross_entropy_workspace_bytes(rows, width, vocab) bytes: two

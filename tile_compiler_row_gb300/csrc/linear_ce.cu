@@ -4,8 +4,8 @@
 //   g = (exp(l - lse) - onehot(target)) dloss,  dx = g W,  dW = g^T x
 //
 // Every product is a matrix product on the fifth-generation tensor cores
-// with FP32 accumulators in tensor memory; what becomes of a 128 x 256 tile
-// of it is the epilogue:
+// with FP32 accumulators in tensor memory (gemm_kernel); what becomes of a
+// 128 x 256 tile of it is the epilogue:
 //
 //   forward    a tile of l is reduced to each row's maximum and sum of
 //              exponentials, two numbers per tile and row; a second kernel
@@ -21,7 +21,8 @@
 //
 // Backward first packs the rows whose target counts (and whose dloss is not
 // 0) to the front of a copy of x, so rows that are ignored cost nothing and
-// a NaN in one of them reaches no gradient.
+// a NaN in one of them reaches no gradient.  Forward does so where the
+// product is long enough to pay for it.
 #include "linear_ce.h"
 
 #include <cuda_bf16.h>
@@ -38,38 +39,51 @@ namespace {
 
 enum { CE_WAIT_TIMEOUT = 2u, CE_BAD_TARGET = 8u };
 
-constexpr int BM = 128, BN = 256, BK = 64, STAGES = 4;
-constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int GEMM_SMEM = STAGES * STAGE_BYTES + 1024;   // + slack to align to 1024
+constexpr int BM = 128, BN = 256, BK = 64;
+constexpr int MOST_STAGES = 8;
+constexpr int PIPE_BYTES = 192 << 10;                    // stages of A and B tiles
+constexpr int STORE_BYTES = 32 << 10;                    // 4 warps, 2 buffers of 32 rows x 128 bytes
+constexpr int GEMM_SMEM = PIPE_BYTES + STORE_BYTES + 1024;   // + slack to align to 1024
 constexpr int GEMM_THREADS = 192;                        // 4 epilogue warps, TMA, MMA
+constexpr int TILE_RING = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum { EPI_LSE, EPI_GRAD, EPI_DWEIGHT, EPI_DX };
+enum { EPI_NONE, EPI_LSE, EPI_GRAD, EPI_DWEIGHT, EPI_DX };
 
-// What a backward call learns on the device before its products.
+// What a call learns on the device before its products.
 struct CeState {
     int valid;        // packed rows
     float unscale;    // what the scaled gradients are multiplied by at the end
 };
 
-struct GemmArgs {
+// One product of a launch.
+struct Job {
     int m, n, k;                // extents (rows of A, rows of B, reduction)
-    const CeState *state;       // limits m (GRAD, DX) or k (DWEIGHT) to the packed rows
+    int bn;                     // columns of a tile (256, or less to even out the CTAs)
+    int a_rows;                 // rows of A that a tile loads (fewer than 128 in a short call)
+    int splits;                 // parts of k, each with its own slice of out (EPI_DX)
+    void *out;                  // EPI_DWEIGHT, EPI_DX
+    long long ld;               // its elements per row
+    int store;                  // EPI_DWEIGHT: through shared memory and map_out
+};
+
+struct GemmArgs {
+    Job job[2];
+    const CeState *state;       // limits the packed rows (m of GRAD and DX, k of DWEIGHT), or NULL
+    unsigned int *counter;      // two jobs: the next tile, 0 at the launch
     int bf16;
-    // EPI_LSE
-    float2 *partial;            // [m][n tiles]
+    float2 *partial;            // EPI_LSE: [m][n tiles]
     // EPI_GRAD: packed rows' target, lse log2(e) and scaled dloss
     const int *ptarget;
     const float *plse2, *pdloss;
-    void *grad;                 // [m padded][ld]
     int n0;                     // first vocabulary entry of the piece
-    // EPI_DWEIGHT / EPI_DX
-    void *out;
-    long long ld;               // elements per row of grad / out
     int accumulate;             // EPI_DX: add to what is there
-    int splits;                 // EPI_DX: parts of k, each with its own slice
     long long slice;            // elements of a slice
     unsigned int *status;
+};
+
+struct GemmMaps {
+    CUtensorMap a[2], b[2], out;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -87,27 +101,133 @@ __device__ __forceinline__ uint32_t pack2(int bf16, float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// C[m][n] = sum_k A[m][k] B[n][k], tile by tile on a persistent grid.
-// A_MN / B_MN: the operand lies in memory as [k][m] / [k][n].
-template <bool A_MN, bool B_MN, int EPI>
+// How an epilogue's product lies in memory: K-major operands are [m or n][k],
+// MN-major ones [k][m or n].
+__device__ __forceinline__ constexpr bool a_mn(int epi) { return epi == EPI_DWEIGHT; }
+__device__ __forceinline__ constexpr bool b_mn(int epi) { return epi == EPI_DWEIGHT || epi == EPI_DX; }
+
+// Tile t of a product.  Tiles run along the shorter side of the product's
+// tile grid first, in bands of 32 tiles of it, so that the CTAs at work at
+// one time share their operands' tiles in L2 and each operand is read from
+// DRAM about once: the band (32 x 128 rows of 4096 columns are 32 MiB) stays,
+// the other operand streams by.
+struct Tile {
+    int m, n, split;
+};
+__device__ __forceinline__ Tile tile_of(int t, int m_tiles, int n_tiles, bool n_first) {
+    const int fast = n_first ? n_tiles : m_tiles, slow = n_first ? m_tiles : n_tiles;
+    Tile r;
+    const int plane = m_tiles * n_tiles;
+    r.split = t / plane;
+    t -= r.split * plane;
+    const int band = t / (32 * slow), rest = t - band * 32 * slow;
+    const int wide = min(32, fast - band * 32);
+    const int f = band * 32 + rest % wide, s = rest / wide;
+    r.m = n_first ? s : f;
+    r.n = n_first ? f : s;
+    return r;
+}
+
+struct Extents {
+    int m, n, k, m_tiles, n_tiles, k_blocks, splits, tiles;
+};
+template <int EPI>
+__device__ __forceinline__ Extents extents(const Job &j, const CeState *state) {
+    Extents e;
+    e.m = j.m;
+    e.n = j.n;
+    e.k = j.k;
+    if (state != nullptr) {
+        // (a product that is not wanted has no rows)
+        if (EPI == EPI_LSE || EPI == EPI_GRAD || EPI == EPI_DX) e.m = min(j.m, state->valid);
+        if (EPI == EPI_DWEIGHT) e.k = state->valid;
+    }
+    e.m_tiles = (e.m + BM - 1) / BM;
+    e.n_tiles = (e.n + j.bn - 1) / j.bn;
+    e.k_blocks = (e.k + BK - 1) / BK;
+    e.splits = EPI == EPI_DX ? j.splits : 1;
+    e.tiles = EPI == EPI_NONE ? 0 : e.m_tiles * e.n_tiles * e.splits;
+    return e;
+}
+
+// A tile of FP32 accumulators as 16-bit rows in memory: 32 rows x 64 columns
+// at a time through this warp's part of shared memory and a tensor-map store
+// (128-byte swizzled; whole lines whatever the row stride, and clipped at
+// the matrix's edges).  `value` maps column c + j's accumulator.
+template <class F>
+__device__ __forceinline__ void store_tile16(const CUtensorMap *map, uint32_t tmem, uint32_t buf,
+                                             int &turn, int lane, int bf16, int row0, int col0,
+                                             int cols, bool inside, F value) {
+    for (int c = 0; c < cols; c += 64) {
+        const uint32_t to = buf + turn * 4096 + lane * 128;
+        if (lane == 0) store_wait_read<1>();   // the buffer's store before last has read it
+        __syncwarp();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float v[32];
+            tmem_load32(tmem + c + half * 32, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = value(v[j], c + half * 32 + j);
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+                const int chunk = half * 4 + j / 8;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 to + 16 * (chunk ^ (lane & 7))),
+                             "r"(pack2(bf16, v[j], v[j + 1])), "r"(pack2(bf16, v[j + 2], v[j + 3])),
+                             "r"(pack2(bf16, v[j + 4], v[j + 5])),
+                             "r"(pack2(bf16, v[j + 6], v[j + 7]))
+                             : "memory");
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            if (inside) tma_store(map, col0 + c, row0, buf + turn * 4096);
+            store_commit();
+        }
+        turn ^= 1;
+    }
+}
+
+// C[m][n] = sum_k A[m][k] B[n][k] for one or two jobs, tile by tile on a
+// persistent grid: a TMA warp fills a ring of A and B tiles in shared memory,
+// one thread issues the MMAs into one of two accumulators in tensor memory
+// (256 columns each), and four warps turn the other into the epilogue's
+// output.  One CTA per SM; pairs of SMs on one tile are not needed: the
+// product of 4096 x 131072 x 4096 runs at the measured cuBLAS rate.
+//
+// With two jobs the tiles of the first (long: its reduction is the piece of
+// the vocabulary) come first, and CTAs take the next tile off a counter, so
+// the second's short tiles even out the end: 512 long tiles alone would
+// leave 152 SMs at 84 %.  Which CTA computes a tile changes no result.
+template <int EPI0, int EPI1>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
-    gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                const GemmArgs g) {
+    gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs g) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * STAGES + 4];
+    __shared__ __align__(8) uint64_t bars[2 * MOST_STAGES + 4 + 2 * TILE_RING];
+    __shared__ int tile_ring[TILE_RING];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
-    auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
-    auto acc_full = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
-    auto acc_empty = [&](int s) { return bar0 + 8u * (2 * STAGES + 2 + s); };
+    auto empty = [&](int s) { return bar0 + 8u * (MOST_STAGES + s); };
+    auto acc_full = [&](int s) { return bar0 + 8u * (2 * MOST_STAGES + s); };
+    auto acc_empty = [&](int s) { return bar0 + 8u * (2 * MOST_STAGES + 2 + s); };
+    auto tile_full = [&](int s) { return bar0 + 8u * (2 * MOST_STAGES + 4 + s); };
+    auto tile_empty = [&](int s) { return bar0 + 8u * (2 * MOST_STAGES + 4 + TILE_RING + s); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int *aborted = &abort_flag;
+    // a stage holds the larger job's tiles; A's part may be short (its last
+    // rows are then what follows, and only rows that are not there read it)
+    const int a_bytes = max(g.job[0].a_rows, EPI1 ? g.job[1].a_rows : 0) * BK * 2;
+    const int stage_bytes = a_bytes + max(g.job[0].bn, EPI1 ? g.job[1].bn : 0) * BK * 2;
+    // the tail of the last stage's short A is read up to 16 KiB from its start
+    const int stages = min(MOST_STAGES, PIPE_BYTES / stage_bytes);
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             bar_init(full(s), 1);
             bar_init(empty(s), 1);
         }
@@ -115,91 +235,130 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             bar_init(acc_full(s), 1);
             bar_init(acc_empty(s), 128);
         }
+        for (int s = 0; s < TILE_RING; ++s) {
+            bar_init(tile_full(s), 1);
+            bar_init(tile_empty(s), 5);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&maps.a[0]);
+        prefetch_map(&maps.b[0]);
     }
     if (warp == 5) tmem_alloc(smem_u32(&tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *const_cast<volatile uint32_t *>(&tmem_slot);
-    volatile int *aborted = &abort_flag;
+    dependency_wait();
+    dependency_launch();
 
-    int m_ext = g.m, k_ext = g.k;
-    if (EPI == EPI_GRAD || EPI == EPI_DX) m_ext = g.state->valid;
-    if (EPI == EPI_DWEIGHT) k_ext = g.state->valid;
-    const int m_tiles = (m_ext + BM - 1) / BM, n_tiles = (g.n + BN - 1) / BN;
-    const int k_blocks = (k_ext + BK - 1) / BK;
-    const int splits = EPI == EPI_DX ? g.splits : 1;
-    const long long tiles = static_cast<long long>(m_tiles) * n_tiles * splits;
-    auto kb_begin = [&](int split) { return k_blocks * split / splits; };
+    const Extents e0 = extents<EPI0>(g.job[0], g.state);
+    const Extents e1 = extents<EPI1>(g.job[EPI1 ? 1 : 0], g.state);
+    const int tiles = e0.tiles + e1.tiles;
+    // job[1] runs along n first (its n is the width, its m the vocabulary)
+    auto where = [&](int t) {
+        return t < e0.tiles ? tile_of(t, e0.m_tiles, e0.n_tiles, e0.n_tiles < e0.m_tiles)
+                            : tile_of(t - e0.tiles, e1.m_tiles, e1.n_tiles, e1.n_tiles < e1.m_tiles);
+    };
+    auto k_begin = [&](int t, int split) {
+        return t < e0.tiles ? static_cast<int>(static_cast<long long>(e0.k_blocks) * split / e0.splits)
+                            : (split == 0 ? 0 : e1.k_blocks);
+    };
+    // the next tile as the MMA thread and the epilogue warps see it
+    auto next_tile = [&](int i, bool &ok) {
+        const int s = i % TILE_RING;
+        ok = bar_wait(tile_full(s), (i / TILE_RING) & 1u, aborted, g.status, CE_WAIT_TIMEOUT);
+        const int t = ok ? const_cast<volatile int *>(tile_ring)[s] : -1;
+        return t;
+    };
 
-    if (warp == 4 && lane == 0) {   // TMA producer
+    if (warp == 4 && lane == 0) {   // TMA producer, and the tiles' order
         int stage = 0;
         unsigned int phase = 0;
         long long issued = 0;
         bool ok = true;
-        for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            const int mt = static_cast<int>(t % m_tiles);
-            const int nt = static_cast<int>(t / m_tiles % n_tiles);
-            const int sp = static_cast<int>(t / m_tiles / n_tiles);
-            for (int kb = kb_begin(sp); kb < kb_begin(sp + 1); ++kb) {
+        int t = blockIdx.x;
+        for (int i = 0; ok; ++i) {
+            // the tile after this one is asked for before this one's loads
+            int after = t + gridDim.x;
+            if (EPI1 && t < tiles) after = static_cast<int>(atomicAdd(g.counter, 1u) + gridDim.x);
+            const int slot = i % TILE_RING;
+            if (!bar_wait(tile_empty(slot), ((i / TILE_RING) & 1u) ^ 1u, aborted, g.status,
+                          CE_WAIT_TIMEOUT))
+                break;
+            const_cast<volatile int *>(tile_ring)[slot] = t < tiles ? t : -1;
+            bar_arrive(tile_full(slot));
+            if (t >= tiles) break;
+            const bool second = EPI1 && t >= e0.tiles;
+            const Job &job = g.job[second ? 1 : 0];
+            const CUtensorMap *ma = &maps.a[second ? 1 : 0], *mb = &maps.b[second ? 1 : 0];
+            const bool amn = second ? a_mn(EPI1) : a_mn(EPI0), bmn = second ? b_mn(EPI1) : b_mn(EPI0);
+            const Tile w = where(t);
+            const int bytes = (job.a_rows + job.bn) * BK * 2;
+            for (int kb = k_begin(t, w.split); kb < k_begin(t, w.split + 1); ++kb) {
                 if (!(ok = bar_wait(empty(stage), phase ^ 1u, aborted, g.status, CE_WAIT_TIMEOUT)))
                     break;
-                const uint32_t a = base + stage * STAGE_BYTES, b = a + A_BYTES;
-                bar_expect_tx(full(stage), STAGE_BYTES);
-                if (A_MN) {
-                    for (int i = 0; i < BM / 64; ++i)
-                        tma_load(a + i * 8192, &map_a, mt * BM + i * 64, kb * BK, full(stage));
+                const uint32_t a = base + stage * stage_bytes, b = a + a_bytes;
+                bar_expect_tx(full(stage), bytes);
+                if (amn) {
+                    for (int c = 0; c < BM; c += 64)
+                        tma_load(a + c * 128, ma, w.m * BM + c, kb * BK, full(stage));
                 } else {
-                    tma_load(a, &map_a, kb * BK, mt * BM, full(stage));
+                    tma_load(a, ma, kb * BK, w.m * BM, full(stage));
                 }
-                if (B_MN) {
-                    for (int i = 0; i < BN / 64; ++i)
-                        tma_load(b + i * 8192, &map_b, nt * BN + i * 64, kb * BK, full(stage));
+                if (bmn) {
+                    for (int c = 0; c < job.bn; c += 64)
+                        tma_load(b + c * 128, mb, w.n * job.bn + c, kb * BK, full(stage));
                 } else {
-                    tma_load(b, &map_b, kb * BK, nt * BN, full(stage));
+                    tma_load(b, mb, kb * BK, w.n * job.bn, full(stage));
                 }
                 ++issued;
-                if (++stage == STAGES) {
+                if (++stage == stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
+            t = after;
         }
         // An aborted CTA waits (bounded) for the copies it issued: none may
         // land in shared memory that it no longer owns.
         if (*aborted)
-            for (long long i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+            for (long long i = issued > stages ? issued - stages : 0; i < issued; ++i)
                 for (unsigned int n = 0; n < kBarSpins; ++n)
-                    if (bar_test(full(static_cast<int>(i % STAGES)), (i / STAGES) & 1)) break;
+                    if (bar_test(full(static_cast<int>(i % stages)), (i / stages) & 1)) break;
     } else if (warp == 5 && lane == 0) {   // MMA issuer
-        const uint32_t idesc = mma_idesc(g.bf16 != 0, A_MN, B_MN, BM, BN);
         int stage = 0, acc = 0;
         unsigned int phase = 0, acc_phase = 0;
         bool ok = true;
-        for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            const int sp = static_cast<int>(t / m_tiles / n_tiles);
+        for (int i = 0; ok; ++i) {
+            const int t = next_tile(i, ok);
+            if (t < 0) break;
+            bar_arrive(tile_empty(i % TILE_RING));
+            const bool second = EPI1 && t >= e0.tiles;
+            const bool amn = second ? a_mn(EPI1) : a_mn(EPI0), bmn = second ? b_mn(EPI1) : b_mn(EPI0);
+            const uint32_t idesc =
+                mma_idesc(g.bf16 != 0, amn, bmn, BM, g.job[second ? 1 : 0].bn);
+            const Tile w = where(t);
             if (!(ok = bar_wait(acc_empty(acc), acc_phase ^ 1u, aborted, g.status, CE_WAIT_TIMEOUT)))
                 break;
             tc_fence_after();
             const uint32_t d = tmem + acc * BN;
             bool first = true;
-            for (int kb = kb_begin(sp); kb < kb_begin(sp + 1); ++kb) {
+            for (int kb = k_begin(t, w.split); kb < k_begin(t, w.split + 1); ++kb) {
                 if (!(ok = bar_wait(full(stage), phase, aborted, g.status, CE_WAIT_TIMEOUT))) break;
                 tc_fence_after();
-                const uint32_t a = base + stage * STAGE_BYTES, b = a + A_BYTES;
-                const uint64_t da = smem_desc(a, A_MN ? 8192 : 16, 1024);
-                const uint64_t db = smem_desc(b, B_MN ? 8192 : 16, 1024);
+                const uint32_t a = base + stage * stage_bytes, b = a + a_bytes;
+                const uint64_t da = smem_desc(a, amn ? 8192 : 16, 1024);
+                const uint64_t db = smem_desc(b, bmn ? 8192 : 16, 1024);
+                // 16 elements along K: 32 bytes of a K-major row, or 16 rows
+                // of 128 bytes
+                const int sa = amn ? 2048 >> 4 : 32 >> 4, sb = bmn ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
                 for (int k = 0; k < BK / 16; ++k) {
-                    // 16 elements along K: 32 bytes of a K-major row, or 16
-                    // rows of 128 bytes
-                    tc_mma(d, da + k * (A_MN ? 2048 >> 4 : 32 >> 4),
-                           db + k * (B_MN ? 2048 >> 4 : 32 >> 4), idesc, !first);
+                    tc_mma(d, da + k * sa, db + k * sb, idesc, !first);
                     first = false;
                 }
                 tc_commit(empty(stage));
-                if (++stage == STAGES) {
+                if (++stage == stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -214,119 +373,301 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 if (bar_test(acc_full(acc), acc_phase)) break;
         }
     } else if (warp < 4) {   // epilogue: thread = row of the tile
-        int acc = 0;
+        int acc = 0, turn = 0;
         unsigned int acc_phase = 0;
-        for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
-            const int mt = static_cast<int>(t % m_tiles);
-            const int nt = static_cast<int>(t / m_tiles % n_tiles);
-            const int sp = static_cast<int>(t / m_tiles / n_tiles);
-            const bool ok = bar_wait(acc_full(acc), acc_phase, aborted, g.status, CE_WAIT_TIMEOUT);
+        const uint32_t buf = base + PIPE_BYTES + warp * 8192;
+        for (int i = 0;; ++i) {
+            bool ok;
+            const int t = next_tile(i, ok);
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, t >= 0)) break;
+            if (lane == 0) bar_arrive(tile_empty(i % TILE_RING));
+            const Tile w = where(t);
+            ok = bar_wait(acc_full(acc), acc_phase, aborted, g.status, CE_WAIT_TIMEOUT);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            const int row = mt * BM + warp * 32 + lane, col0 = nt * BN;
+            const bool second = EPI1 && t >= e0.tiles;
+            const Job &job = g.job[second ? 1 : 0];
+            const Extents &e = second ? e1 : e0;
+            const int row0 = w.m * BM + warp * 32, row = row0 + lane, col0 = w.n * job.bn;
             const uint32_t d = tmem + acc * BN + (static_cast<uint32_t>(warp * 32) << 16);
-            const bool none = kb_begin(sp) == kb_begin(sp + 1);   // no product was made: zero
-            if (EPI == EPI_LSE) {
+            // no product was made: zero
+            const bool none = k_begin(t, w.split) == k_begin(t, w.split + 1);
+            const int epi = second ? EPI1 : EPI0;
+            if (epi == EPI_LSE) {
                 float m = -INFINITY, s = 0.0f;
-                for (int c = 0; c < BN && col0 + c < g.n; c += 32) {
+                for (int c = 0; c < job.bn && col0 + c < e.n; c += 32) {
                     float v[32];
                     tmem_load32(d + c, v);
-                    if (col0 + c + 32 > g.n)
+                    const int limit = min(job.bn - c, e.n - col0 - c);
+                    if (limit < 32)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (col0 + c + j >= g.n) v[j] = -INFINITY;
+                            if (j >= limit) v[j] = -INFINITY;
                     float top = m;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
                     const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
                     s *= ex2(m * kLog2e - ref);
+                    float part[4] = {};
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) s += ex2(fmaf(v[j], kLog2e, -ref));
+                    for (int j = 0; j < 32; ++j) part[j & 3] += ex2(fmaf(v[j], kLog2e, -ref));
+                    s += (part[0] + part[1]) + (part[2] + part[3]);
                     m = top;
                 }
-                if (row < m_ext)
-                    g.partial[static_cast<long long>(row) * n_tiles + nt] = make_float2(m, s);
-            } else if (EPI == EPI_GRAD) {
-                const bool in = row < m_ext;
-                const long long want = in ? g.ptarget[row] - g.n0 - col0 : -1;
+                if (row < e.m)
+                    g.partial[static_cast<long long>(row) * e.n_tiles + w.n] = make_float2(m, s);
+            } else if (epi == EPI_GRAD) {
+                const bool in = row < e.m;
+                const int want = in ? g.ptarget[row] - g.n0 - col0 : -1;
                 const float lse2 = in ? g.plse2[row] : 0.0f, dl = in ? g.pdloss[row] : 0.0f;
-                uint32_t *to = reinterpret_cast<uint32_t *>(
-                    static_cast<unsigned short *>(g.grad) + static_cast<long long>(row) * g.ld + col0);
-                for (int c = 0; c < BN; c += 32) {
-                    float v[32];
-                    tmem_load32(d + c, v);
+                const int limit = in ? e.n - col0 : 0;
+                store_tile16(&maps.out, d, buf, turn, lane, g.bf16, row0, col0, BN, true,
+                             [&](float v, int c) {
+                                 const float p = ex2(fmaf(v, kLog2e, -lse2));
+                                 return c < limit ? (want == c ? p - 1.0f : p) * dl : 0.0f;
+                             });
+            } else if (epi == EPI_DWEIGHT) {
+                const float f = none ? 0.0f : g.state->unscale;
+                if (job.store) {
+                    const int cols = min(job.bn, (e.n - col0 + 63) / 64 * 64);
+                    store_tile16(&maps.out, d, buf, turn, lane, g.bf16, row0, col0, cols, row0 < e.m,
+                                 [&](float v, int) { return none ? 0.0f : v * f; });
+                } else {
+                    unsigned short *to = static_cast<unsigned short *>(job.out) +
+                                         static_cast<long long>(row) * job.ld + col0;
+                    for (int c = 0; c < job.bn && col0 + c < e.n; c += 32) {
+                        float v[32];
+                        tmem_load32(d + c, v);
+                        if (row < e.m)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float p = ex2(fmaf(v[j], kLog2e, -lse2));
-                        const float q = (want == c + j ? p - 1.0f : p) * dl;
-                        v[j] = in && col0 + c + j < g.n ? q : 0.0f;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8)
-                        *reinterpret_cast<uint4 *>(to + (c + j) / 2) = make_uint4(
-                            pack2(g.bf16, v[j], v[j + 1]), pack2(g.bf16, v[j + 2], v[j + 3]),
-                            pack2(g.bf16, v[j + 4], v[j + 5]), pack2(g.bf16, v[j + 6], v[j + 7]));
-                }
-            } else if (EPI == EPI_DWEIGHT) {
-                const float f = g.state->unscale;
-                unsigned short *to = static_cast<unsigned short *>(g.out) +
-                                     static_cast<long long>(row) * g.ld + col0;
-                const bool vec = (g.ld % 8 == 0) && (reinterpret_cast<uintptr_t>(g.out) % 16 == 0);
-                for (int c = 0; c < BN && col0 + c < g.n; c += 32) {
-                    float v[32];
-                    tmem_load32(d + c, v);
-                    if (row >= g.m) continue;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = none ? 0.0f : v[j] * f;
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        const uint4 q = make_uint4(
-                            pack2(g.bf16, v[j], v[j + 1]), pack2(g.bf16, v[j + 2], v[j + 3]),
-                            pack2(g.bf16, v[j + 4], v[j + 5]), pack2(g.bf16, v[j + 6], v[j + 7]));
-                        if (vec && col0 + c + j < g.n) {
-                            *reinterpret_cast<uint4 *>(to + c + j) = q;
-                        } else {
-                            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (col0 + c + j + e < g.n)
-                                    to[c + j + e] = static_cast<unsigned short>(
-                                        w[e / 2] >> (16 * (e & 1)));
-                        }
+                            for (int j = 0; j < 32; ++j)
+                                if (col0 + c + j < e.n)
+                                    to[c + j] = static_cast<unsigned short>(
+                                        pack2(g.bf16, none ? 0.0f : v[j] * f, 0.0f));
                     }
                 }
-            } else {   // EPI_DX: FP32, ld a multiple of 4, rows of whole vectors
-                float *to = static_cast<float *>(g.out) + sp * g.slice +
-                            static_cast<long long>(row) * g.ld + col0;
-                for (int c = 0; c < BN && col0 + c < g.ld; c += 32) {
+            } else if (epi == EPI_DX) {   // FP32, ld a multiple of 4: rows of whole vectors
+                float *to = static_cast<float *>(job.out) + w.split * g.slice +
+                            static_cast<long long>(row) * job.ld + col0;
+                for (int c = 0; c < job.bn && col0 + c < job.ld; c += 32) {
                     float v[32];
                     tmem_load32(d + c, v);
-                    if (row >= m_ext) continue;
+                    if (row < e.m)
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        if (col0 + c + j >= g.ld) break;
-                        float4 q = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                                        : make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                        float4 *p = reinterpret_cast<float4 *>(to + c + j);
-                        if (g.accumulate) {
-                            const float4 o = *p;
-                            q = make_float4(q.x + o.x, q.y + o.y, q.z + o.z, q.w + o.w);
+                        for (int j = 0; j < 32; j += 4) {
+                            if (col0 + c + j >= job.ld) break;
+                            float4 q = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                            : make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                            float4 *p = reinterpret_cast<float4 *>(to + c + j);
+                            if (g.accumulate) {
+                                const float4 o = *p;
+                                q = make_float4(q.x + o.x, q.y + o.y, q.z + o.z, q.w + o.w);
+                            }
+                            *p = q;
                         }
-                        *p = q;
-                    }
                 }
             }
+            __syncwarp();
             tc_fence_before();
             bar_arrive(acc_empty(acc));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
+        if (lane == 0) store_wait<0>();   // the stores are written before the CTA ends
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 5) tmem_free(tmem, 512);
+}
+
+// ---- packing rows ----------------------------------------------------------------------
+
+struct PackArgs {
+    const unsigned short *x, *weight;   // weight NULL: only x
+    const long long *target;
+    const float *lse, *dloss;           // NULL in a forward call
+    long long ignore;
+    int rows, width, vocab, ld;
+    int scaled;                         // FP16: gradients by 2^15
+    int row_ctas;                       // CTAs that pack x; the others copy the weight
+    int place_rows;                     // 0: x is copied as it lies
+    unsigned short *px, *pw;
+    CeState *state;
+    int *place, *row_of, *ptarget;
+    float *plse2, *pdloss;
+    unsigned int *counters;
+    int ncounters;
+    unsigned int *status;
+};
+
+__device__ __forceinline__ bool counts(long long t, long long ignore, int vocab, float dl) {
+    return t != ignore && t >= 0 && t < vocab && dl != 0.0f;
+}
+
+// One warp copies a row of `width` two-byte elements, from any 2-byte
+// alignment, to a row of `ld` (a multiple of 8; 16-byte aligned), padded with
+// zeros; `from` NULL: zeros.  Two aligned source blocks make one of the
+// target's; the second is the next lane's first.
+__device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned short *to, int width,
+                                           int ld, int lane) {
+    const int vecs = ld / 8;
+    uint4 *out = reinterpret_cast<uint4 *>(to);
+    if (from == nullptr) {
+        for (int i = lane; i < vecs; i += 32) out[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    if (width == ld && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
+        const uint4 *in = reinterpret_cast<const uint4 *>(from);
+        for (int i = lane; i < vecs; i += 32) out[i] = __ldg(in + i);
+        return;
+    }
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(from);
+    const uintptr_t end = begin + static_cast<uintptr_t>(width) * 2;
+    const int skew = static_cast<int>(begin & 15);
+    const uintptr_t block0 = begin - skew;
+    for (int i0 = 0; i0 < vecs; i0 += 32) {
+        const int i = i0 + lane;
+        // a block with bytes outside the row is read by element
+        auto block = [&](int b) {
+            const uintptr_t at = block0 + static_cast<uintptr_t>(b) * 16;
+            if (at >= begin && at + 16 <= end) return __ldg(reinterpret_cast<const uint4 *>(at));
+            unsigned int w[4] = {};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uintptr_t p = at + 2 * j;
+                if (p >= begin && p < end)
+                    w[j / 2] |= static_cast<unsigned int>(
+                                    *reinterpret_cast<const unsigned short *>(p)) << (16 * (j & 1));
+            }
+            return make_uint4(w[0], w[1], w[2], w[3]);
+        };
+        const uint4 a = block(i);
+        uint4 b;
+        b.x = __shfl_down_sync(0xffffffffu, a.x, 1);
+        b.y = __shfl_down_sync(0xffffffffu, a.y, 1);
+        b.z = __shfl_down_sync(0xffffffffu, a.z, 1);
+        b.w = __shfl_down_sync(0xffffffffu, a.w, 1);
+        if (lane == 31) b = block(i + 1);
+        // bytes [skew, skew + 16) of a, b
+        const unsigned int w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        unsigned int r[4];
+        const int words = skew >> 2, bits = (skew & 3) * 8;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // w[words + j], w[words + j + 1] without indexing by a variable
+            unsigned int lo = w[j], hi = w[j + 1];
+            if (words == 1) { lo = w[j + 1]; hi = w[j + 2]; }
+            if (words == 2) { lo = w[j + 2]; hi = w[j + 3]; }
+            if (words == 3) { lo = w[j + 3]; hi = w[j + 4 < 8 ? j + 4 : 7]; }
+            r[j] = __funnelshift_r(lo, hi, bits);
+        }
+        if (i < vecs) out[i] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+}
+
+// The rows that count, packed to the front of px in their order (place[i] =
+// position of row i or -1; row_of, target, lse and dloss by position), rows
+// behind them zero; and the weight's rows copied to whole vectors.  A CTA
+// packs 32 rows and counts the rows before them for itself (the targets of a
+// call are small and in L2), so there is no pass before it.
+//
+// dloss is held over its largest magnitude: the equal weights of a mean
+// become 1, so that the 16-bit gradients round p - onehot and not its
+// product with, say, 1 / 48, which is off by the same 2^-9 in every row's
+// largest entry (dx of 48 rows was 2.6e-3 off in the 2-norm with dloss in
+// it, 1.8e-3 without; the output's own rounding is 1.7e-3).  FP16 gradients
+// are scaled by 2^15 too: |p - onehot| <= 1, so nothing overflows, and what
+// underflows is below 2^-40 of the largest.
+constexpr int PACK_ROWS = 32;
+
+__global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
+    __shared__ int warp_before[8], warp_total[8], row_at[PACK_ROWS];
+    __shared__ float warp_top[8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    dependency_launch();
+    if (static_cast<int>(blockIdx.x) >= a.row_ctas) {
+        const int ctas = gridDim.x - a.row_ctas, cta = blockIdx.x - a.row_ctas;
+        for (long long r = static_cast<long long>(cta) * 8 + warp; r < a.vocab; r += ctas * 8ll)
+            copy_row16(a.weight + r * a.width, a.pw + r * a.ld, a.width, a.ld, lane);
+        return;
+    }
+    const int r0 = blockIdx.x * PACK_ROWS;
+    int valid = a.rows;
+    if (a.place_rows) {
+        int before = 0, all = 0;
+        float top = 0.0f;
+#pragma unroll 4
+        for (int i = tid; i < a.rows; i += 256) {
+            const long long t = a.target[i];
+            const float dl = a.dloss != nullptr ? a.dloss[i] : 1.0f;
+            const bool in = counts(t, a.ignore, a.vocab, dl);
+            all += in;
+            before += in && i < r0;
+            if (in && isfinite(dl)) top = fmaxf(top, fabsf(dl));
+        }
+        for (int d = 16; d > 0; d >>= 1) {
+            before += __shfl_xor_sync(0xffffffffu, before, d);
+            all += __shfl_xor_sync(0xffffffffu, all, d);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        }
+        if (lane == 0) {
+            warp_before[warp] = before;
+            warp_total[warp] = all;
+            warp_top[warp] = top;
+        }
+        __syncthreads();
+        before = all = 0;
+        top = 0.0f;
+        for (int i = 0; i < 8; ++i) {
+            before += warp_before[i];
+            all += warp_total[i];
+            top = fmaxf(top, warp_top[i]);
+        }
+        valid = all;
+        // 32768 / top and top / 32768 are finite and not 0 for any normal top
+        top = fminf(fmaxf(top, 1e-30f), 1e30f);
+        const float full = a.scaled ? 32768.0f : 1.0f;
+        if (warp == 0) {
+            const int i = r0 + lane;
+            const long long t = i < a.rows ? a.target[i] : a.ignore;
+            const float dl = i < a.rows && a.dloss != nullptr ? a.dloss[i] : 1.0f;
+            const bool in = i < a.rows && counts(t, a.ignore, a.vocab, dl);
+            const unsigned int mask = __ballot_sync(0xffffffffu, in);
+            const int at = before + __popc(mask & ((1u << lane) - 1u));
+            row_at[lane] = in ? at : -1;
+            if (i < a.rows) {
+                a.place[i] = in ? at : -1;
+                if (t != a.ignore && (t < 0 || t >= a.vocab)) atomicOr(a.status, CE_BAD_TARGET);
+            }
+            if (in) {
+                a.row_of[at] = i;
+                if (a.dloss != nullptr) {
+                    a.ptarget[at] = static_cast<int>(t);
+                    a.plse2[at] = a.lse[i] * kLog2e;
+                    a.pdloss[at] = full * (dl / top);
+                }
+            }
+            if (blockIdx.x == 0 && lane == 0) {
+                a.state->valid = all;
+                a.state->unscale = top / full;
+            }
+        }
+        __syncthreads();
+    }
+    if (blockIdx.x == 0)
+        for (int i = tid; i < a.ncounters; i += 256) a.counters[i] = 0;
+    for (int q = warp; q < PACK_ROWS; q += 8) {
+        const int i = r0 + q;
+        if (i >= a.rows) break;
+        const int at = a.place_rows ? row_at[q] : i;
+        if (at >= 0)
+            copy_row16(a.x + static_cast<long long>(i) * a.width,
+                       a.px + static_cast<long long>(at) * a.ld, a.width, a.ld, lane);
+        if (i >= valid) copy_row16(nullptr, a.px + static_cast<long long>(i) * a.ld, 0, a.ld, lane);
+    }
 }
 
 // ---- forward: joining the tiles --------------------------------------------------
@@ -370,6 +711,7 @@ struct JoinArgs {
     const float2 *partial;
     const unsigned short *x, *weight;
     const long long *target;
+    const int *place;   // where a row was packed, or NULL
     long long ignore;
     int rows, width, vocab, n_tiles;
     float *loss, *lse;
@@ -378,15 +720,30 @@ struct JoinArgs {
 
 // One warp a row: lanes over the n tiles, joined in a fixed tree.
 template <class T>
-__global__ void __launch_bounds__(256) join_lse_kernel(const JoinArgs a) {
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(128) join_lse_kernel(const JoinArgs a) {
+    const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= a.rows) return;
+    // the target's logit needs nothing of the product before
     const long long t = a.target[row];
+    const bool in = t >= 0 && t < a.vocab;
+    const float l = in && t != a.ignore ? warp_dot<T>(a.x + static_cast<long long>(row) * a.width,
+                                                      a.weight + t * a.width, a.width, lane)
+                                        : NAN;
+    dependency_wait();
     if (t == a.ignore) {
         if (lane == 0) a.loss[row] = a.lse[row] = 0.0f;
         return;
     }
-    const float2 *p = a.partial + static_cast<long long>(row) * a.n_tiles;
+    if (!in) {   // not among the rows that were multiplied, or of no use there
+        if (lane == 0) {
+            a.loss[row] = NAN;
+            a.lse[row] = 0.0f;
+            atomicOr(a.status, CE_BAD_TARGET);
+        }
+        return;
+    }
+    const int at = a.place != nullptr ? a.place[row] : row;
+    const float2 *p = a.partial + static_cast<long long>(at) * a.n_tiles;
     float m = -INFINITY;
     for (int i = lane; i < a.n_tiles; i += 32) m = fmaxf(m, p[i].x);
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -398,136 +755,46 @@ __global__ void __launch_bounds__(256) join_lse_kernel(const JoinArgs a) {
     }
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
     const float log_s = logf(s);
-    const bool in = t >= 0 && t < a.vocab;
-    const float l = in ? warp_dot<T>(a.x + static_cast<long long>(row) * a.width,
-                                     a.weight + t * a.width, a.width, lane)
-                       : NAN;
     if (lane != 0) return;
     a.lse[row] = m + log_s;
     a.loss[row] = (m - l) + log_s;   // m - l is exact where they are close
-    if (!in) atomicOr(a.status, CE_BAD_TARGET);
 }
 
-// ---- backward: packing rows ----------------------------------------------------------
-
-__device__ __forceinline__ bool counts(long long t, long long ignore, int vocab, float dl) {
-    return t != ignore && t >= 0 && t < vocab && dl != 0.0f;
-}
-
-// One CTA: place[i] = position of row i among the rows that count, or -1;
-// row_of, target, lse and dloss of the packed rows.  dloss is held over its
-// largest magnitude: the equal weights of a mean become 1, so that the
-// 16-bit gradients round p - onehot and not its product with, say, 1 / 48,
-// which is off by the same 2^-9 in every row's largest entry (dx of 48 rows
-// was 2.6e-3 off in the 2-norm with dloss in it, 2.0e-3 without; the output's
-// own rounding is 1.7e-3).  FP16 gradients are scaled by 2^15 too: |p -
-// onehot| <= 1, so nothing overflows, and what underflows is below 2^-40 of
-// the largest.
-__global__ void __launch_bounds__(1024)
-    place_rows_kernel(const long long *target, const float *lse, const float *dloss,
-                      long long ignore, int rows, int vocab, int scaled, CeState *state,
-                      int *place, int *row_of, int *ptarget, float *plse2, float *pdloss,
-                      unsigned int *status) {
-    __shared__ int warp_count[32];
-    __shared__ float warp_top[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (rows + 1023) / 1024;
-    const int begin = min(rows, tid * per), end = min(rows, begin + per);
-    int n = 0;
-    float top = 0.0f;
-    for (int i = begin; i < end; ++i) {
-        const long long t = target[i];
-        const float dl = dloss[i];
-        if (t != ignore && (t < 0 || t >= vocab)) atomicOr(status, CE_BAD_TARGET);
-        if (counts(t, ignore, vocab, dl)) {
-            ++n;
-            if (isfinite(dl)) top = fmaxf(top, fabsf(dl));
-        }
-    }
-    int before = n;
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, before, d);
-        if (lane >= d) before += o;
-    }
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (lane == 31) warp_count[warp] = before;
-    if (lane == 0) warp_top[warp] = top;
-    __syncthreads();
-    int at = before - n, total = 0;
-    top = 0.0f;
-    for (int i = 0; i < 32; ++i) {
-        if (i < warp) at += warp_count[i];
-        total += warp_count[i];
-        top = fmaxf(top, warp_top[i]);
-    }
-    // 32768 / top and top / 32768 are finite and not 0 for any normal top
-    top = fminf(fmaxf(top, 1e-30f), 1e30f);
-    const float full = scaled ? 32768.0f : 1.0f;
-    for (int i = begin; i < end; ++i) {
-        const long long t = target[i];
-        const float dl = dloss[i];
-        if (counts(t, ignore, vocab, dl)) {
-            place[i] = at;
-            row_of[at] = i;
-            ptarget[at] = static_cast<int>(t);
-            plse2[at] = lse[i] * kLog2e;
-            pdloss[at] = full * (dl / top);
-            ++at;
-        } else {
-            place[i] = -1;
-        }
-    }
-    if (tid == 0) {
-        state->valid = total;
-        state->unscale = top / full;
-    }
-}
-
-// to[i] = from[row_of[i]] (i itself without row_of), rows of `width`
-// two-byte elements into rows of `ld` (a multiple of 8), padded with zeros;
-// rows from state->valid on are zero.
-__global__ void __launch_bounds__(256)
-    pack_rows_kernel(const unsigned short *from, unsigned short *to, long long rows, int width, int ld,
-                     const int *row_of, const CeState *state) {
-    const int per_row = ld / 8;
-    const long long n = rows * per_row;
-    const long long valid = state != nullptr ? state->valid : rows;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
-        const long long r = i / per_row;
-        const int c = static_cast<int>(i % per_row) * 8;
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (r < valid) {
-            const unsigned short *p = from + (row_of != nullptr ? row_of[r] : r) * width + c;
-            if (width == ld) {
-                q = *reinterpret_cast<const uint4 *>(p);
-            } else {
-                unsigned int w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = c + j < width ? p[j] : 0u;
-                q = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16,
-                               w[6] | w[7] << 16);
-            }
-        }
-        *reinterpret_cast<uint4 *>(to + r * ld + c) = q;
-    }
-}
+// ---- backward: the end ----------------------------------------------------------------
 
 // dx[i] = the sum of the slices' rows place[i], scaled back and rounded; 0
-// for rows that do not count.
-__global__ void __launch_bounds__(256)
+// for rows that do not count.  One CTA a row.
+template <class T>
+__global__ void __launch_bounds__(128)
     finish_dx_kernel(const float *acc, int splits, long long slice, int acc_ld, const int *place,
-                     const CeState *state, int bf16, unsigned short *dx, int rows, int width) {
-    const long long n = static_cast<long long>(rows) * width;
+                     const CeState *state, T *dx, int width) {
+    dependency_wait();
+    const long long r = blockIdx.x;
+    const int p = place[r];
     const float f = state->unscale;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
-        const long long r = i / width;
-        const int c = static_cast<int>(i % width);
-        const int p = place[r];
-        float t = 0.0f;
-        if (p >= 0)
-            for (int s = 0; s < splits; ++s)
-                t += acc[s * slice + static_cast<long long>(p) * acc_ld + c];
-        dx[i] = static_cast<unsigned short>(pack2(bf16, t * f, 0.0f));
+    T *to = dx + r * width;
+    const bool vec = width % 4 == 0 && (reinterpret_cast<uintptr_t>(dx) & 7) == 0;
+    for (int c = threadIdx.x * 4; c < width; c += 512) {
+        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (p >= 0) {
+            const float *from = acc + static_cast<long long>(p) * acc_ld + c;
+#pragma unroll 4
+            for (int s = 0; s < splits; ++s) {
+                const float4 q = __ldcs(reinterpret_cast<const float4 *>(from + s * slice));
+                t = make_float4(t.x + q.x, t.y + q.y, t.z + q.z, t.w + q.w);
+            }
+        }
+        constexpr int bf16 = std::is_same<T, __nv_bfloat16>::value;
+        const uint32_t lo = pack2(bf16, t.x * f, t.y * f), hi = pack2(bf16, t.z * f, t.w * f);
+        if (vec) {
+            *reinterpret_cast<uint2 *>(to + c) = make_uint2(lo, hi);
+        } else {
+            unsigned short *o = reinterpret_cast<unsigned short *>(to);
+            o[c] = static_cast<unsigned short>(lo);
+            if (c + 1 < width) o[c + 1] = static_cast<unsigned short>(lo >> 16);
+            if (c + 2 < width) o[c + 2] = static_cast<unsigned short>(hi);
+            if (c + 3 < width) o[c + 3] = static_cast<unsigned short>(hi >> 16);
+        }
     }
 }
 
@@ -572,26 +839,45 @@ cudaError_t make_map(CUtensorMap *map, int bf16, const void *p, long long rows, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <bool A_MN, bool B_MN, int EPI>
-cudaError_t launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g,
-                        cudaStream_t stream) {
+// A launch that may start before the kernel before it has ended (that kernel
+// lets it, and it waits itself).
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+                             cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+long long job_tiles(const Job &j) { return up(j.m, BM) / BM * (up(j.n, j.bn) / j.bn) * j.splits; }
+
+template <int EPI0, int EPI1>
+cudaError_t launch_gemm(const GemmMaps &maps, const GemmArgs &g, cudaStream_t stream) {
     static std::atomic<int> ready[kMaxDevices];
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (ready[dev].load(std::memory_order_acquire) == 0) {
-        err = cudaFuncSetAttribute(gemm_kernel<A_MN, B_MN, EPI>,
+        err = cudaFuncSetAttribute(gemm_kernel<EPI0, EPI1>,
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM);
         if (err != cudaSuccess) return err;
         ready[dev].store(1, std::memory_order_release);
     }
-    const long long tiles = (up(g.m, BM) / BM) * (up(g.n, BN) / BN) * (EPI == EPI_DX ? g.splits : 1);
+    const long long tiles = job_tiles(g.job[0]) + (EPI1 ? job_tiles(g.job[1]) : 0);
+    if (tiles > 0x3fffffff) return cudaErrorInvalidValue;   // tile numbers are ints
     long long grid = sm_count_of_device();
     if (grid > tiles) grid = tiles;
-    gemm_kernel<A_MN, B_MN, EPI>
-        <<<static_cast<unsigned>(grid), GEMM_THREADS, GEMM_SMEM, stream>>>(a, b, g);
-    return cudaGetLastError();
+    return launch_dependent(gemm_kernel<EPI0, EPI1>, static_cast<unsigned>(grid), GEMM_THREADS,
+                            GEMM_SMEM, stream, maps, g);
 }
 
 // Parts of a workspace, in order, each on 256 bytes.
@@ -610,32 +896,66 @@ struct Carver {
 // wants strides of 16 bytes).
 bool odd_rows(int width) { return width % 8 != 0; }
 
+// Whether a forward call packs the rows that count: where x is copied
+// anyway, and where the product takes some 300 us, against which finding and
+// copying the rows (about 10 us) is little even if none is ignored.
+bool forward_packs(int rows, int width, int vocab) {
+    return odd_rows(width) ||
+           (rows > 2 * BM && 2.0 * rows * width * static_cast<double>(vocab) > 5e11);
+}
+
 struct ForwardSpace {
+    CeState *state;
+    int *place, *row_of;
     unsigned short *x, *w;
     float2 *partial;
     size_t bytes;
 };
 
+// Columns of a forward call's tiles: 256 or a little less, so that the last
+// round of tiles leaves few SMs idle (32768 columns: 147 tiles of 224 in one
+// round instead of 128 of 256).
+int forward_columns(int rows, int vocab) {
+    const long long m_tiles = up(rows, BM) / BM;
+    int best = BN;
+    long long least = 0;
+    for (int bn = BN; bn >= 192; bn -= 16) {
+        const long long tiles = m_tiles * (up(vocab, bn) / bn);
+        // a tile costs its columns and about 4 more for its start
+        const long long cost = (tiles + 151) / 152 * (bn + 4);
+        if (bn == BN || cost < least) {
+            least = cost;
+            best = bn;
+        }
+    }
+    return best;
+}
+
 ForwardSpace forward_space(void *ws, int rows, int width, int vocab) {
     Carver c{static_cast<unsigned char *>(ws), 0};
-    ForwardSpace s;
+    ForwardSpace s = {};
     const long long ld = up(width, 8);
-    s.x = s.w = nullptr;
-    if (odd_rows(width)) {
+    const int bn = forward_columns(rows, vocab);
+    s.partial = c.take<float2>(rows * (up(vocab, bn) / bn));
+    if (forward_packs(rows, width, vocab)) {
+        s.state = c.take<CeState>(1);
+        s.place = c.take<int>(rows);
+        s.row_of = c.take<int>(rows);
         s.x = c.take<unsigned short>(rows * ld);
-        s.w = c.take<unsigned short>(vocab * ld);
+        if (odd_rows(width)) s.w = c.take<unsigned short>(vocab * ld);
     }
-    s.partial = c.take<float2>(rows * (up(vocab, BN) / BN));
     s.bytes = c.at;
     return s;
 }
 
 // A piece of the vocabulary: as many columns as keep its 16-bit gradients
-// within 512 MiB, at least 4096 (each piece adds to the FP32 dx once more).
+// within 512 MiB, at least 4096 (each piece adds to the FP32 dx once more),
+// and pieces of even size.
 long long piece_of(int rows, int vocab) {
     long long n = (512ll << 20) / (2 * up(rows, BM)) / BN * BN;
     if (n < 4096) n = 4096;
-    return n < up(vocab, BN) ? n : up(vocab, BN);
+    const long long pieces = (vocab + n - 1) / n;
+    return up((vocab + pieces - 1) / pieces, BN);
 }
 
 // Parts of a dx product's reduction: where its tiles alone would leave SMs
@@ -652,6 +972,8 @@ struct BackwardSpace {
     CeState *state;
     int *place, *row_of, *ptarget;
     float *plse2, *pdloss;
+    unsigned int *counters;
+    int pieces;
     unsigned short *x, *w, *grad;
     float *acc;
     size_t bytes;
@@ -660,8 +982,10 @@ struct BackwardSpace {
 BackwardSpace backward_space(void *ws, int rows, int width, int vocab) {
     Carver c{static_cast<unsigned char *>(ws), 0};
     BackwardSpace s;
-    const long long ld = up(width, 8);
+    const long long ld = up(width, 8), piece = piece_of(rows, vocab);
+    s.pieces = static_cast<int>((vocab + piece - 1) / piece);
     s.state = c.take<CeState>(1);
+    s.counters = c.take<unsigned int>(s.pieces);
     s.place = c.take<int>(rows);
     s.row_of = c.take<int>(rows);
     s.ptarget = c.take<int>(rows);
@@ -669,17 +993,25 @@ BackwardSpace backward_space(void *ws, int rows, int width, int vocab) {
     s.pdloss = c.take<float>(rows);
     s.x = c.take<unsigned short>(rows * ld);
     s.w = odd_rows(width) ? c.take<unsigned short>(vocab * ld) : nullptr;
-    s.grad = c.take<unsigned short>(up(rows, BM) * piece_of(rows, vocab));
+    s.grad = c.take<unsigned short>(up(rows, BM) * piece);
     s.acc = c.take<float>(splits_of(rows, width, vocab) * up(rows, BM) * up(width, 4));
     s.bytes = c.at;
     return s;
 }
 
-unsigned grid_for(long long items) {
-    long long b = (items + 255) / 256;
-    const long long cap = 152 * 16;
-    return static_cast<unsigned>(b < 1 ? 1 : b > cap ? cap : b);
+// The pack kernel's CTAs for x, and with a weight to copy two waves more.
+cudaError_t launch_pack(PackArgs p, cudaStream_t stream) {
+    p.row_ctas = (p.rows + PACK_ROWS - 1) / PACK_ROWS;
+    int weight_ctas = 0;
+    if (p.weight != nullptr) {
+        weight_ctas = sm_count_of_device() * 8;
+        if (weight_ctas > (p.vocab + 7) / 8) weight_ctas = (p.vocab + 7) / 8;
+    }
+    pack_rows_kernel<<<p.row_ctas + weight_ctas, 256, 0, stream>>>(p);
+    return cudaGetLastError();
 }
+
+int rows_of_a(int rows) { return rows >= BM ? BM : static_cast<int>(up(rows, 8)); }
 
 }  // namespace
 
@@ -706,37 +1038,45 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
     const ForwardSpace s = forward_space(args.ws, rows, width, vocab);
     const long long ld = up(width, 8);
     const void *x = args.x, *w = args.weight;
-    if (odd_rows(width)) {
-        pack_rows_kernel<<<grid_for(rows * ld / 8), 256, 0, stream>>>(
-            static_cast<const unsigned short *>(x), s.x, rows, width, static_cast<int>(ld), nullptr,
-            nullptr);
-        pack_rows_kernel<<<grid_for(vocab * ld / 8), 256, 0, stream>>>(
-            static_cast<const unsigned short *>(w), s.w, vocab, width, static_cast<int>(ld), nullptr,
-            nullptr);
-        CE_TRY(cudaGetLastError());
+    const bool packs = forward_packs(rows, width, vocab);
+    if (packs) {
+        PackArgs p = {};
+        p.x = static_cast<const unsigned short *>(x);
+        p.weight = odd_rows(width) ? static_cast<const unsigned short *>(w) : nullptr;
+        p.target = args.target;
+        p.ignore = args.ignore;
+        p.rows = rows;
+        p.width = width;
+        p.vocab = vocab;
+        p.ld = static_cast<int>(ld);
+        p.place_rows = 1;
+        p.px = s.x;
+        p.pw = s.w;
+        p.state = s.state;
+        p.place = s.place;
+        p.row_of = s.row_of;
+        p.status = status;
+        CE_TRY(launch_pack(p, stream));
         x = s.x;
-        w = s.w;
+        if (odd_rows(width)) w = s.w;
     }
-    CUtensorMap ma, mb;
-    CE_TRY(make_map(&ma, bf16, x, rows, width, ld, BM));
-    CE_TRY(make_map(&mb, bf16, w, vocab, width, ld, BN));
+    const int bn = forward_columns(rows, vocab);
+    GemmMaps maps = {};
     GemmArgs g = {};
-    g.m = rows;
-    g.n = vocab;
-    g.k = width;
+    g.job[0] = {rows, vocab, width, bn, rows_of_a(rows), 1, nullptr, 0, 0};
+    g.state = packs ? s.state : nullptr;
     g.bf16 = bf16;
     g.partial = s.partial;
     g.status = status;
-    CE_TRY((launch_gemm<false, false, EPI_LSE>(ma, mb, g, stream)));
+    CE_TRY(make_map(&maps.a[0], bf16, x, rows, width, ld, g.job[0].a_rows));
+    CE_TRY(make_map(&maps.b[0], bf16, w, vocab, width, ld, bn));
+    CE_TRY((launch_gemm<EPI_LSE, EPI_NONE>(maps, g, stream)));
     const JoinArgs j = {s.partial, static_cast<const unsigned short *>(args.x),
-                        static_cast<const unsigned short *>(args.weight), args.target, args.ignore,
-                        rows, width, vocab, static_cast<int>(up(vocab, BN) / BN), args.loss,
-                        args.lse, status};
-    if (bf16)
-        join_lse_kernel<__nv_bfloat16><<<(rows + 7) / 8, 256, 0, stream>>>(j);
-    else
-        join_lse_kernel<__half><<<(rows + 7) / 8, 256, 0, stream>>>(j);
-    return cudaGetLastError();
+                        static_cast<const unsigned short *>(args.weight), args.target,
+                        packs ? s.place : nullptr, args.ignore, rows, width, vocab,
+                        static_cast<int>(up(vocab, bn) / bn), args.loss, args.lse, status};
+    return launch_dependent(bf16 ? join_lse_kernel<__nv_bfloat16> : join_lse_kernel<__half>,
+                            (rows + 3) / 4, 128, 0, stream, j);
 }
 
 cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t stream) {
@@ -747,71 +1087,81 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
     const int bf16 = args.elem == ELEM_BF16;
     const BackwardSpace s = backward_space(args.ws, rows, width, vocab);
     const long long ld = up(width, 8), piece = piece_of(rows, vocab), acc_ld = up(width, 4);
-    const int splits = splits_of(rows, width, vocab);
-    place_rows_kernel<<<1, 1024, 0, stream>>>(args.target, args.lse, args.dloss, args.ignore, rows,
-                                              vocab, !bf16, s.state, s.place, s.row_of, s.ptarget,
-                                              s.plse2, s.pdloss, status);
-    pack_rows_kernel<<<grid_for(rows * ld / 8), 256, 0, stream>>>(
-        static_cast<const unsigned short *>(args.x), s.x, rows, width, static_cast<int>(ld),
-        s.row_of, s.state);
+    const int splits = splits_of(rows, width, vocab), a_rows = rows_of_a(rows);
     const unsigned short *w = static_cast<const unsigned short *>(args.weight);
-    if (odd_rows(width)) {
-        pack_rows_kernel<<<grid_for(vocab * ld / 8), 256, 0, stream>>>(
-            w, s.w, vocab, width, static_cast<int>(ld), nullptr, nullptr);
-        w = s.w;
-    }
-    CE_TRY(cudaGetLastError());
-    CUtensorMap x_k, x_mn, grad_k, grad_mn;
-    CE_TRY(make_map(&x_k, bf16, s.x, rows, width, ld, BM));
-    CE_TRY(make_map(&x_mn, bf16, s.x, rows, width, ld, BK));
-    CE_TRY(make_map(&grad_k, bf16, s.grad, up(rows, BM), piece, piece, BM));
-    CE_TRY(make_map(&grad_mn, bf16, s.grad, up(rows, BM), piece, piece, BK));
-    for (long long n0 = 0; n0 < vocab; n0 += piece) {
+    PackArgs p = {};
+    p.x = static_cast<const unsigned short *>(args.x);
+    p.weight = odd_rows(width) ? w : nullptr;
+    p.target = args.target;
+    p.lse = args.lse;
+    p.dloss = args.dloss;
+    p.ignore = args.ignore;
+    p.rows = rows;
+    p.width = width;
+    p.vocab = vocab;
+    p.ld = static_cast<int>(ld);
+    p.scaled = !bf16;
+    p.place_rows = 1;
+    p.px = s.x;
+    p.pw = s.w;
+    p.state = s.state;
+    p.place = s.place;
+    p.row_of = s.row_of;
+    p.ptarget = s.ptarget;
+    p.plse2 = s.plse2;
+    p.pdloss = s.pdloss;
+    p.counters = s.counters;
+    p.ncounters = s.pieces;
+    p.status = status;
+    CE_TRY(launch_pack(p, stream));
+    if (odd_rows(width)) w = s.w;
+    // dweight through shared memory and tensor-map stores where its rows allow
+    const bool store = width % 8 == 0 && reinterpret_cast<uintptr_t>(args.dweight) % 16 == 0;
+    GemmMaps grad = {}, both = {};
+    CE_TRY(make_map(&grad.a[0], bf16, s.x, rows, width, ld, a_rows));
+    CE_TRY(make_map(&grad.out, bf16, s.grad, up(rows, BM), piece, piece, 32));
+    CE_TRY(make_map(&both.a[0], bf16, s.grad, up(rows, BM), piece, piece, a_rows));   // dx: g
+    CE_TRY(make_map(&both.a[1], bf16, s.grad, up(rows, BM), piece, piece, BK));       // dW: g^T
+    CE_TRY(make_map(&both.b[1], bf16, s.x, rows, width, ld, BK));                      // dW: x
+    GemmArgs g = {};
+    g.state = s.state;
+    g.bf16 = bf16;
+    g.status = status;
+    g.ptarget = s.ptarget;
+    g.plse2 = s.plse2;
+    g.pdloss = s.pdloss;
+    g.slice = up(rows, BM) * acc_ld;
+    for (int i = 0; i < s.pieces; ++i) {
+        const long long n0 = i * piece;
         const int n = static_cast<int>(vocab - n0 < piece ? vocab - n0 : piece);
-        CUtensorMap w_k, w_mn;
-        CE_TRY(make_map(&w_k, bf16, w + n0 * ld, n, width, ld, BN));
-        CE_TRY(make_map(&w_mn, bf16, w + n0 * ld, n, width, ld, BK));
-        GemmArgs g = {};
-        g.state = s.state;
-        g.bf16 = bf16;
-        g.status = status;
-        g.m = rows;
-        g.n = n;
-        g.k = width;
-        g.ptarget = s.ptarget;
-        g.plse2 = s.plse2;
-        g.pdloss = s.pdloss;
-        g.grad = s.grad;
-        g.ld = piece;
+        CE_TRY(make_map(&grad.b[0], bf16, w + n0 * ld, n, width, ld, BN));
+        CE_TRY(make_map(&both.b[0], bf16, w + n0 * ld, n, width, ld, BK));             // dx: W
         g.n0 = static_cast<int>(n0);
-        CE_TRY((launch_gemm<false, false, EPI_GRAD>(x_k, w_k, g, stream)));
+        g.accumulate = i > 0;
+        g.counter = s.counters + i;
+        g.job[0] = {rows, n, width, BN, a_rows, 1, nullptr, 0, 0};
+        CE_TRY((launch_gemm<EPI_GRAD, EPI_NONE>(grad, g, stream)));
+        g.job[0] = {args.dx != nullptr ? rows : 0, width, n, BN, a_rows, splits, s.acc, acc_ld, 0};
+        g.job[1] = {args.dweight != nullptr ? n : 0, width, rows, BN, BM, 1, nullptr, width, store};
         if (args.dweight != nullptr) {
-            g.m = n;
-            g.n = width;
-            g.k = rows;
-            g.out = static_cast<unsigned short *>(args.dweight) + n0 * width;
-            g.ld = width;
-            CE_TRY((launch_gemm<true, true, EPI_DWEIGHT>(grad_mn, x_mn, g, stream)));
+            unsigned short *to = static_cast<unsigned short *>(args.dweight) + n0 * width;
+            g.job[1].out = to;
+            if (store) CE_TRY(make_map(&both.out, bf16, to, n, width, width, 32));
         }
-        if (args.dx != nullptr) {
-            g.m = rows;
-            g.n = width;
-            g.k = n;
-            g.out = s.acc;
-            g.ld = acc_ld;
-            g.accumulate = n0 > 0;
-            g.splits = splits;
-            g.slice = up(rows, BM) * acc_ld;
-            CE_TRY((launch_gemm<false, true, EPI_DX>(grad_k, w_mn, g, stream)));
-        }
+        CE_TRY((launch_gemm<EPI_DX, EPI_DWEIGHT>(both, g, stream)));
     }
-    if (args.dx != nullptr) {
-        finish_dx_kernel<<<grid_for(static_cast<long long>(rows) * width), 256, 0, stream>>>(
-            s.acc, splits, up(rows, BM) * acc_ld, static_cast<int>(acc_ld), s.place, s.state, bf16,
-            static_cast<unsigned short *>(args.dx), rows, width);
-        CE_TRY(cudaGetLastError());
-    }
-    return cudaSuccess;
+    if (args.dx == nullptr) return cudaSuccess;
+    if (bf16)
+        return launch_dependent(finish_dx_kernel<__nv_bfloat16>, rows, 128, 0, stream,
+                                static_cast<const float *>(s.acc), splits, g.slice,
+                                static_cast<int>(acc_ld), static_cast<const int *>(s.place),
+                                static_cast<const CeState *>(s.state),
+                                static_cast<__nv_bfloat16 *>(args.dx), width);
+    return launch_dependent(finish_dx_kernel<__half>, rows, 128, 0, stream,
+                            static_cast<const float *>(s.acc), splits, g.slice,
+                            static_cast<int>(acc_ld), static_cast<const int *>(s.place),
+                            static_cast<const CeState *>(s.state), static_cast<__half *>(args.dx),
+                            width);
 }
 
 }  // namespace tile
