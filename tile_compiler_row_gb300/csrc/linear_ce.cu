@@ -5,7 +5,7 @@
 //
 // Every product is a matrix product on the fifth-generation tensor cores
 // with FP32 accumulators in tensor memory (gemm_kernel); what becomes of a
-// 128 x 256 tile of it is the epilogue:
+// 256 x 256 tile of it is the epilogue:
 //
 //   forward    a tile of l is reduced to each row's maximum and sum of
 //              exponentials, two numbers per tile and row; a second kernel
@@ -39,13 +39,13 @@ namespace {
 
 enum { CE_WAIT_TIMEOUT = 2u, CE_BAD_TARGET = 8u };
 
-constexpr int BM = 128, BN = 256, BK = 64;
-constexpr int MOST_STAGES = 8;
+constexpr int BM = 256, BN = 256, BK = 64;               // a CTA pair's tile
+constexpr int CM = BM / 2;                               // a CTA's rows of it
+constexpr int MOST_STAGES = 12;
 constexpr int PIPE_BYTES = 192 << 10;                    // stages of A and B tiles
 constexpr int STORE_BYTES = 32 << 10;                    // 4 warps, 2 buffers of 32 rows x 128 bytes
 constexpr int GEMM_SMEM = PIPE_BYTES + STORE_BYTES + 1024;   // + slack to align to 1024
 constexpr int GEMM_THREADS = 192;                        // 4 epilogue warps, TMA, MMA
-constexpr int TILE_RING = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum { EPI_NONE, EPI_LSE, EPI_GRAD, EPI_DWEIGHT, EPI_DX };
@@ -60,8 +60,9 @@ struct CeState {
 struct Job {
     int m, n, k;                // extents (rows of A, rows of B, reduction)
     int bn;                     // columns of a tile (256, or less to even out the CTAs)
-    int a_rows;                 // rows of A that a tile loads (fewer than 128 in a short call)
+    int a_rows;                 // rows of A that a CTA loads (fewer than 128 in a short call)
     int splits;                 // parts of k, each with its own slice of out (EPI_DX)
+    int band;                   // tile rows that are gone down before the next column
     void *out;                  // EPI_DWEIGHT, EPI_DX
     long long ld;               // its elements per row
     int store;                  // EPI_DWEIGHT: through shared memory and map_out
@@ -70,7 +71,6 @@ struct Job {
 struct GemmArgs {
     Job job[2];
     const CeState *state;       // limits the packed rows (m of GRAD and DX, k of DWEIGHT), or NULL
-    unsigned int *counter;      // two jobs: the next tile, 0 at the launch
     int bf16;
     float2 *partial;            // EPI_LSE: [m][n tiles]
     // EPI_GRAD: packed rows' target, lse log2(e) and scaled dloss
@@ -85,6 +85,15 @@ struct GemmArgs {
 struct GemmMaps {
     CUtensorMap a[2], b[2], out;
 };
+
+__device__ __forceinline__ unsigned int cluster_ctarank() {
+    unsigned int r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -106,25 +115,24 @@ __device__ __forceinline__ uint32_t pack2(int bf16, float lo, float hi) {
 __device__ __forceinline__ constexpr bool a_mn(int epi) { return epi == EPI_DWEIGHT; }
 __device__ __forceinline__ constexpr bool b_mn(int epi) { return epi == EPI_DWEIGHT || epi == EPI_DX; }
 
-// Tile t of a product.  Tiles run along the shorter side of the product's
-// tile grid first, in bands of 32 tiles of it, so that the CTAs at work at
-// one time share their operands' tiles in L2 and each operand is read from
-// DRAM about once: the band (32 x 128 rows of 4096 columns are 32 MiB) stays,
-// the other operand streams by.
+// Tile t of a product: down the rows of a band of `band` tiles first, then
+// along the columns, then the next band.  The band's A tiles stay in L2 while
+// B streams by: 4096 rows of 4096 columns for the logits; for dx, whose
+// operands are both long, about as many rows as columns at work at a time;
+// for dW, whose A is the piece of g, as many tiles as keep about one round of
+// pairs in a band, so that g is read from DRAM once.
 struct Tile {
     int m, n, split;
 };
-__device__ __forceinline__ Tile tile_of(int t, int m_tiles, int n_tiles, bool n_first) {
-    const int fast = n_first ? n_tiles : m_tiles, slow = n_first ? m_tiles : n_tiles;
+__device__ __forceinline__ Tile tile_of(int t, int m_tiles, int n_tiles, int band) {
     Tile r;
     const int plane = m_tiles * n_tiles;
     r.split = t / plane;
     t -= r.split * plane;
-    const int band = t / (32 * slow), rest = t - band * 32 * slow;
-    const int wide = min(32, fast - band * 32);
-    const int f = band * 32 + rest % wide, s = rest / wide;
-    r.m = n_first ? s : f;
-    r.n = n_first ? f : s;
+    const int b = t / (band * n_tiles), rest = t - b * band * n_tiles;
+    const int high = min(band, m_tiles - b * band);
+    r.m = b * band + rest % high;
+    r.n = rest / high;
     return r;
 }
 
@@ -190,22 +198,24 @@ __device__ __forceinline__ void store_tile16(const CUtensorMap *map, uint32_t tm
 }
 
 // C[m][n] = sum_k A[m][k] B[n][k] for one or two jobs, tile by tile on a
-// persistent grid: a TMA warp fills a ring of A and B tiles in shared memory,
-// one thread issues the MMAs into one of two accumulators in tensor memory
-// (256 columns each), and four warps turn the other into the epilogue's
-// output.  One CTA per SM; pairs of SMs on one tile are not needed: the
-// product of 4096 x 131072 x 4096 runs at the measured cuBLAS rate.
+// persistent grid of CTA pairs: in each CTA a TMA warp fills a ring of A and
+// B tiles in shared memory, one thread of the pair issues the MMAs into one of
+// two accumulators in tensor memory (256 columns each), and four warps turn
+// the other into the epilogue's output.  A pair reads 32 KiB per CTA and 64
+// columns of K from L2, where a CTA with a tile of its own reads 48: L2
+// delivers some 12.5 TB/s, which bound the gradients' products with single
+// CTAs (56 % of the tensor cores' time in use).
 //
-// With two jobs the tiles of the first (long: its reduction is the piece of
-// the vocabulary) come first, and CTAs take the next tile off a counter, so
-// the second's short tiles even out the end: 512 long tiles alone would
-// leave 152 SMs at 84 %.  Which CTA computes a tile changes no result.
+// With two jobs the tiles of the first come first; they are long (their
+// reduction is the piece of the vocabulary) and few, 256 of them over 76
+// pairs leave a sixth of the pairs' time.  So pairs that get one less of
+// them start on the second job's short tiles while the others do their last
+// long one, and all go on in turn from there (tile_at).
 template <int EPI0, int EPI1>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs g) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * MOST_STAGES + 4 + 2 * TILE_RING];
-    __shared__ int tile_ring[TILE_RING];
+    __shared__ __align__(8) uint64_t bars[2 * MOST_STAGES + 4];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -214,30 +224,24 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     auto empty = [&](int s) { return bar0 + 8u * (MOST_STAGES + s); };
     auto acc_full = [&](int s) { return bar0 + 8u * (2 * MOST_STAGES + s); };
     auto acc_empty = [&](int s) { return bar0 + 8u * (2 * MOST_STAGES + 2 + s); };
-    auto tile_full = [&](int s) { return bar0 + 8u * (2 * MOST_STAGES + 4 + s); };
-    auto tile_empty = [&](int s) { return bar0 + 8u * (2 * MOST_STAGES + 4 + TILE_RING + s); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
     volatile int *aborted = &abort_flag;
     // a stage holds the larger job's tiles; A's part may be short (its last
     // rows are then what follows, and only rows that are not there read it)
     const int a_bytes = max(g.job[0].a_rows, EPI1 ? g.job[1].a_rows : 0) * BK * 2;
-    const int stage_bytes = a_bytes + max(g.job[0].bn, EPI1 ? g.job[1].bn : 0) * BK * 2;
-    // the tail of the last stage's short A is read up to 16 KiB from its start
+    const int stage_bytes = a_bytes + max(g.job[0].bn, EPI1 ? g.job[1].bn : 0) / 2 * BK * 2;
     const int stages = min(MOST_STAGES, PIPE_BYTES / stage_bytes);
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int s = 0; s < stages; ++s) {
-            bar_init(full(s), 1);
-            bar_init(empty(s), 1);
+            bar_init(full(s), 1);      // rank 0's: its own arrival, both CTAs' bytes
+            bar_init(empty(s), 1);     // the MMAs' commit
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(acc_full(s), 1);
-            bar_init(acc_empty(s), 128);
-        }
-        for (int s = 0; s < TILE_RING; ++s) {
-            bar_init(tile_full(s), 1);
-            bar_init(tile_empty(s), 5);
+            bar_init(acc_empty(s), 8); // rank 0's: four epilogue warps of each CTA
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&maps.a[0]);
@@ -246,6 +250,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     if (warp == 5) tmem_alloc(smem_u32(&tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *const_cast<volatile uint32_t *>(&tmem_slot);
     dependency_wait();
@@ -253,63 +258,70 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 
     const Extents e0 = extents<EPI0>(g.job[0], g.state);
     const Extents e1 = extents<EPI1>(g.job[EPI1 ? 1 : 0], g.state);
-    const int tiles = e0.tiles + e1.tiles;
-    // job[1] runs along n first (its n is the width, its m the vocabulary)
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    // The i-th tile of this pair, or -1.  The first job's tiles go round the
+    // pairs; its last round serves `last` of them, and the others do `ahead`
+    // tiles of the second job in that time.
+    const int rounds = e0.tiles / pairs, last = e0.tiles % pairs;
+    const int ahead = EPI1 && last > 0 && e1.k_blocks > 0
+                          ? (e0.k_blocks / e0.splits + e1.k_blocks / 2) / e1.k_blocks : 0;
+    auto tile_at = [&](int i) {
+        if (i < rounds || (i == rounds && pair < last)) return i * pairs + pair;
+        if (!EPI1) return -1;
+        int j = i - rounds;   // tiles of the second job before this one, counted
+        long long t;          // as if the pairs with a last long tile did `ahead` short ones
+        if (pair < last) j += ahead - 1;
+        if (j < ahead)
+            t = static_cast<long long>(j) * (pairs - last) + pair - last;
+        else
+            t = static_cast<long long>(ahead) * (pairs - last) +
+                static_cast<long long>(j - ahead) * pairs +
+                (pair < last ? pair + pairs - last : pair - last);
+        return t < e1.tiles ? static_cast<int>(e0.tiles + t) : -1;
+    };
     auto where = [&](int t) {
-        return t < e0.tiles ? tile_of(t, e0.m_tiles, e0.n_tiles, e0.n_tiles < e0.m_tiles)
-                            : tile_of(t - e0.tiles, e1.m_tiles, e1.n_tiles, e1.n_tiles < e1.m_tiles);
+        return t < e0.tiles ? tile_of(t, e0.m_tiles, e0.n_tiles, g.job[0].band)
+                            : tile_of(t - e0.tiles, e1.m_tiles, e1.n_tiles, g.job[1].band);
     };
     auto k_begin = [&](int t, int split) {
         return t < e0.tiles ? static_cast<int>(static_cast<long long>(e0.k_blocks) * split / e0.splits)
                             : (split == 0 ? 0 : e1.k_blocks);
     };
-    // the next tile as the MMA thread and the epilogue warps see it
-    auto next_tile = [&](int i, bool &ok) {
-        const int s = i % TILE_RING;
-        ok = bar_wait(tile_full(s), (i / TILE_RING) & 1u, aborted, g.status, CE_WAIT_TIMEOUT);
-        const int t = ok ? const_cast<volatile int *>(tile_ring)[s] : -1;
-        return t;
-    };
 
-    if (warp == 4 && lane == 0) {   // TMA producer, and the tiles' order
+    if (warp == 4 && lane == 0) {   // TMA producer
         int stage = 0;
         unsigned int phase = 0;
         long long issued = 0;
         bool ok = true;
-        int t = blockIdx.x;
-        for (int i = 0; ok; ++i) {
-            // the tile after this one is asked for before this one's loads
-            int after = t + gridDim.x;
-            if (EPI1 && t < tiles) after = static_cast<int>(atomicAdd(g.counter, 1u) + gridDim.x);
-            const int slot = i % TILE_RING;
-            if (!bar_wait(tile_empty(slot), ((i / TILE_RING) & 1u) ^ 1u, aborted, g.status,
-                          CE_WAIT_TIMEOUT))
-                break;
-            const_cast<volatile int *>(tile_ring)[slot] = t < tiles ? t : -1;
-            bar_arrive(tile_full(slot));
-            if (t >= tiles) break;
+        int t;
+        for (int i = 0; ok && (t = tile_at(i)) >= 0; ++i) {
             const bool second = EPI1 && t >= e0.tiles;
             const Job &job = g.job[second ? 1 : 0];
             const CUtensorMap *ma = &maps.a[second ? 1 : 0], *mb = &maps.b[second ? 1 : 0];
             const bool amn = second ? a_mn(EPI1) : a_mn(EPI0), bmn = second ? b_mn(EPI1) : b_mn(EPI0);
             const Tile w = where(t);
-            const int bytes = (job.a_rows + job.bn) * BK * 2;
-            for (int kb = k_begin(t, w.split); kb < k_begin(t, w.split + 1); ++kb) {
+            const int half = job.bn / 2;
+            const int m0 = w.m * BM + rank * CM, n0 = w.n * job.bn + rank * half;
+            const unsigned int bytes = (job.a_rows + half) * BK * 2;
+            // (once a tile: a division takes longer than the MMAs of a block)
+            const int kb0 = k_begin(t, w.split), kb1 = k_begin(t, w.split + 1);
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (!(ok = bar_wait(empty(stage), phase ^ 1u, aborted, g.status, CE_WAIT_TIMEOUT)))
                     break;
                 const uint32_t a = base + stage * stage_bytes, b = a + a_bytes;
-                bar_expect_tx(full(stage), bytes);
+                const uint32_t bar = peer_addr(full(stage), 0);
+                if (rank == 0) bar_expect_tx(full(stage), 2 * bytes);
                 if (amn) {
-                    for (int c = 0; c < BM; c += 64)
-                        tma_load(a + c * 128, ma, w.m * BM + c, kb * BK, full(stage));
+                    tma_load(a, ma, m0, kb * BK, bar);
+                    tma_load(a + 8192, ma, m0 + 64, kb * BK, bar);
                 } else {
-                    tma_load(a, ma, kb * BK, w.m * BM, full(stage));
+                    tma_load(a, ma, kb * BK, m0, bar);
                 }
-                if (bmn) {
-                    for (int c = 0; c < job.bn; c += 64)
-                        tma_load(b + c * 128, mb, w.n * job.bn + c, kb * BK, full(stage));
+                if (bmn) {   // (256 columns to a tile)
+                    tma_load(b, mb, n0, kb * BK, bar);
+                    tma_load(b + 8192, mb, n0 + 64, kb * BK, bar);
                 } else {
-                    tma_load(b, mb, kb * BK, w.n * job.bn, full(stage));
+                    tma_load(b, mb, kb * BK, n0, bar);
                 }
                 ++issued;
                 if (++stage == stages) {
@@ -317,22 +329,19 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     phase ^= 1u;
                 }
             }
-            t = after;
         }
-        // An aborted CTA waits (bounded) for the copies it issued: none may
+        // An aborted pair waits (bounded) for the copies it issued: none may
         // land in shared memory that it no longer owns.
-        if (*aborted)
+        if (*aborted && rank == 0)
             for (long long i = issued > stages ? issued - stages : 0; i < issued; ++i)
                 for (unsigned int n = 0; n < kBarSpins; ++n)
                     if (bar_test(full(static_cast<int>(i % stages)), (i / stages) & 1)) break;
-    } else if (warp == 5 && lane == 0) {   // MMA issuer
+    } else if (warp == 5 && lane == 0 && rank == 0) {   // MMA issuer
         int stage = 0, acc = 0;
         unsigned int phase = 0, acc_phase = 0;
         bool ok = true;
-        for (int i = 0; ok; ++i) {
-            const int t = next_tile(i, ok);
-            if (t < 0) break;
-            bar_arrive(tile_empty(i % TILE_RING));
+        int t;
+        for (int i = 0; ok && (t = tile_at(i)) >= 0; ++i) {
             const bool second = EPI1 && t >= e0.tiles;
             const bool amn = second ? a_mn(EPI1) : a_mn(EPI0), bmn = second ? b_mn(EPI1) : b_mn(EPI0);
             const uint32_t idesc =
@@ -343,15 +352,16 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             tc_fence_after();
             const uint32_t d = tmem + acc * BN;
             bool first = true;
-            for (int kb = k_begin(t, w.split); kb < k_begin(t, w.split + 1); ++kb) {
+            // 16 elements along K: 32 bytes of a K-major row, or 16 rows of
+            // 128 bytes
+            const int sa = amn ? 2048 >> 4 : 32 >> 4, sb = bmn ? 2048 >> 4 : 32 >> 4;
+            const uint32_t lead_a = amn ? 8192 : 16, lead_b = bmn ? 8192 : 16;
+            const int kb0 = k_begin(t, w.split), kb1 = k_begin(t, w.split + 1);
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (!(ok = bar_wait(full(stage), phase, aborted, g.status, CE_WAIT_TIMEOUT))) break;
                 tc_fence_after();
                 const uint32_t a = base + stage * stage_bytes, b = a + a_bytes;
-                const uint64_t da = smem_desc(a, amn ? 8192 : 16, 1024);
-                const uint64_t db = smem_desc(b, bmn ? 8192 : 16, 1024);
-                // 16 elements along K: 32 bytes of a K-major row, or 16 rows
-                // of 128 bytes
-                const int sa = amn ? 2048 >> 4 : 32 >> 4, sb = bmn ? 2048 >> 4 : 32 >> 4;
+                const uint64_t da = smem_desc(a, lead_a, 1024), db = smem_desc(b, lead_b, 1024);
 #pragma unroll
                 for (int k = 0; k < BK / 16; ++k) {
                     tc_mma(d, da + k * sa, db + k * sb, idesc, !first);
@@ -367,7 +377,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
-        if (*aborted) {   // wait (bounded) until no MMA touches this CTA's memory
+        if (*aborted) {   // wait (bounded) until no MMA touches the pair's memory
             tc_commit(acc_full(acc));
             for (unsigned int n = 0; n < kBarSpins; ++n)
                 if (bar_test(acc_full(acc), acc_phase)) break;
@@ -376,20 +386,18 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         int acc = 0, turn = 0;
         unsigned int acc_phase = 0;
         const uint32_t buf = base + PIPE_BYTES + warp * 8192;
-        for (int i = 0;; ++i) {
-            bool ok;
-            const int t = next_tile(i, ok);
-            __syncwarp();
-            if (!__all_sync(0xffffffffu, t >= 0)) break;
-            if (lane == 0) bar_arrive(tile_empty(i % TILE_RING));
+        const uint32_t drained0 = peer_addr(acc_empty(0), 0), drained1 = peer_addr(acc_empty(1), 0);
+        int t;
+        for (int i = 0; (t = tile_at(i)) >= 0; ++i) {
             const Tile w = where(t);
-            ok = bar_wait(acc_full(acc), acc_phase, aborted, g.status, CE_WAIT_TIMEOUT);
+            const bool ok = bar_wait(acc_full(acc), acc_phase, aborted, g.status, CE_WAIT_TIMEOUT);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const bool second = EPI1 && t >= e0.tiles;
             const Job &job = g.job[second ? 1 : 0];
             const Extents &e = second ? e1 : e0;
-            const int row0 = w.m * BM + warp * 32, row = row0 + lane, col0 = w.n * job.bn;
+            const int row0 = w.m * BM + rank * CM + warp * 32, row = row0 + lane;
+            const int col0 = w.n * job.bn;
             const uint32_t d = tmem + acc * BN + (static_cast<uint32_t>(warp * 32) << 16);
             // no product was made: zero
             const bool none = k_begin(t, w.split) == k_begin(t, w.split + 1);
@@ -422,7 +430,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 const int want = in ? g.ptarget[row] - g.n0 - col0 : -1;
                 const float lse2 = in ? g.plse2[row] : 0.0f, dl = in ? g.pdloss[row] : 0.0f;
                 const int limit = in ? e.n - col0 : 0;
-                store_tile16(&maps.out, d, buf, turn, lane, g.bf16, row0, col0, BN, true,
+                // rows up to the next 64 are written: dW's reduction reads them
+                store_tile16(&maps.out, d, buf, turn, lane, g.bf16, row0, col0, BN,
+                             row0 < (e.m + BK - 1) / BK * BK,
                              [&](float v, int c) {
                                  const float p = ex2(fmaf(v, kLog2e, -lse2));
                                  return c < limit ? (want == c ? p - 1.0f : p) * dl : 0.0f;
@@ -468,9 +478,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                         }
                 }
             }
-            __syncwarp();
             tc_fence_before();
-            bar_arrive(acc_empty(acc));
+            __syncwarp();
+            if (lane == 0) bar_arrive_cluster(acc ? drained1 : drained0);
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
@@ -479,6 +489,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    cluster_sync();   // neither CTA leaves while the other uses its memory
     tc_fence_after();
     if (warp == 5) tmem_free(tmem, 512);
 }
@@ -498,8 +509,6 @@ struct PackArgs {
     CeState *state;
     int *place, *row_of, *ptarget;
     float *plse2, *pdloss;
-    unsigned int *counters;
-    int ncounters;
     unsigned int *status;
 };
 
@@ -571,7 +580,7 @@ __device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned 
 // The rows that count, packed to the front of px in their order (place[i] =
 // position of row i or -1; row_of, target, lse and dloss by position), rows
 // behind them zero; and the weight's rows copied to whole vectors.  A CTA
-// packs 32 rows and counts the rows before them for itself (the targets of a
+// packs 8 rows and counts the rows before them for itself (the targets of a
 // call are small and in L2), so there is no pass before it.
 //
 // dloss is held over its largest magnitude: the equal weights of a mean
@@ -581,7 +590,7 @@ __device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned 
 // it, 1.8e-3 without; the output's own rounding is 1.7e-3).  FP16 gradients
 // are scaled by 2^15 too: |p - onehot| <= 1, so nothing overflows, and what
 // underflows is below 2^-40 of the largest.
-constexpr int PACK_ROWS = 32;
+constexpr int PACK_ROWS = 8;
 
 __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
     __shared__ int warp_before[8], warp_total[8], row_at[PACK_ROWS];
@@ -657,8 +666,6 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
         }
         __syncthreads();
     }
-    if (blockIdx.x == 0)
-        for (int i = tid; i < a.ncounters; i += 256) a.counters[i] = 0;
     for (int q = warp; q < PACK_ROWS; q += 8) {
         const int i = r0 + q;
         if (i >= a.rows) break;
@@ -842,18 +849,21 @@ cudaError_t make_map(CUtensorMap *map, int bf16, const void *p, long long rows, 
 // A launch that may start before the kernel before it has ended (that kernel
 // lets it, and it waits itself).
 template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
-                             cudaStream_t stream, A... args) {
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned cluster, unsigned block,
+                             size_t smem, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -874,10 +884,11 @@ cudaError_t launch_gemm(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st
     }
     const long long tiles = job_tiles(g.job[0]) + (EPI1 ? job_tiles(g.job[1]) : 0);
     if (tiles > 0x3fffffff) return cudaErrorInvalidValue;   // tile numbers are ints
-    long long grid = sm_count_of_device();
-    if (grid > tiles) grid = tiles;
-    return launch_dependent(gemm_kernel<EPI0, EPI1>, static_cast<unsigned>(grid), GEMM_THREADS,
-                            GEMM_SMEM, stream, maps, g);
+    long long pairs = sm_count_of_device() / 2;
+    if (pairs > tiles) pairs = tiles;
+    if (pairs < 1) pairs = 1;
+    return launch_dependent(gemm_kernel<EPI0, EPI1>, static_cast<unsigned>(2 * pairs), 2,
+                            GEMM_THREADS, GEMM_SMEM, stream, maps, g);
 }
 
 // Parts of a workspace, in order, each on 256 bytes.
@@ -901,7 +912,7 @@ bool odd_rows(int width) { return width % 8 != 0; }
 // copying the rows (about 10 us) is little even if none is ignored.
 bool forward_packs(int rows, int width, int vocab) {
     return odd_rows(width) ||
-           (rows > 2 * BM && 2.0 * rows * width * static_cast<double>(vocab) > 5e11);
+           (rows > BM && 2.0 * rows * width * static_cast<double>(vocab) > 5e11);
 }
 
 struct ForwardSpace {
@@ -913,16 +924,16 @@ struct ForwardSpace {
 };
 
 // Columns of a forward call's tiles: 256 or a little less, so that the last
-// round of tiles leaves few SMs idle (32768 columns: 147 tiles of 224 in one
-// round instead of 128 of 256).
+// round of tiles leaves few SMs idle (32768 columns over 76 pairs: two rounds
+// of 224 instead of two of 256).
 int forward_columns(int rows, int vocab) {
     const long long m_tiles = up(rows, BM) / BM;
     int best = BN;
     long long least = 0;
-    for (int bn = BN; bn >= 192; bn -= 16) {
+    for (int bn = BN; bn >= 192; bn -= 32) {
         const long long tiles = m_tiles * (up(vocab, bn) / bn);
         // a tile costs its columns and about 4 more for its start
-        const long long cost = (tiles + 151) / 152 * (bn + 4);
+        const long long cost = (tiles + 75) / 76 * (bn + 4);
         if (bn == BN || cost < least) {
             least = cost;
             best = bn;
@@ -962,7 +973,7 @@ long long piece_of(int rows, int vocab) {
 // idle, the vocabulary is split, in parts of at least 512 columns.
 int splits_of(int rows, int width, int vocab) {
     const long long tiles = up(rows, BM) / BM * (up(width, BN) / BN);
-    long long s = 152 / tiles;
+    long long s = 76 / tiles;
     const long long most = piece_of(rows, vocab) / 512;
     if (s > most) s = most;
     return s < 1 ? 1 : static_cast<int>(s);
@@ -972,7 +983,6 @@ struct BackwardSpace {
     CeState *state;
     int *place, *row_of, *ptarget;
     float *plse2, *pdloss;
-    unsigned int *counters;
     int pieces;
     unsigned short *x, *w, *grad;
     float *acc;
@@ -985,7 +995,6 @@ BackwardSpace backward_space(void *ws, int rows, int width, int vocab) {
     const long long ld = up(width, 8), piece = piece_of(rows, vocab);
     s.pieces = static_cast<int>((vocab + piece - 1) / piece);
     s.state = c.take<CeState>(1);
-    s.counters = c.take<unsigned int>(s.pieces);
     s.place = c.take<int>(rows);
     s.row_of = c.take<int>(rows);
     s.ptarget = c.take<int>(rows);
@@ -1011,7 +1020,7 @@ cudaError_t launch_pack(PackArgs p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-int rows_of_a(int rows) { return rows >= BM ? BM : static_cast<int>(up(rows, 8)); }
+int rows_of_a(int rows) { return rows >= CM ? CM : static_cast<int>(up(rows, 8)); }
 
 }  // namespace
 
@@ -1063,20 +1072,20 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
     const int bn = forward_columns(rows, vocab);
     GemmMaps maps = {};
     GemmArgs g = {};
-    g.job[0] = {rows, vocab, width, bn, rows_of_a(rows), 1, nullptr, 0, 0};
+    g.job[0] = {rows, vocab, width, bn, rows_of_a(rows), 1, 16, nullptr, 0, 0};
     g.state = packs ? s.state : nullptr;
     g.bf16 = bf16;
     g.partial = s.partial;
     g.status = status;
     CE_TRY(make_map(&maps.a[0], bf16, x, rows, width, ld, g.job[0].a_rows));
-    CE_TRY(make_map(&maps.b[0], bf16, w, vocab, width, ld, bn));
+    CE_TRY(make_map(&maps.b[0], bf16, w, vocab, width, ld, bn / 2));
     CE_TRY((launch_gemm<EPI_LSE, EPI_NONE>(maps, g, stream)));
     const JoinArgs j = {s.partial, static_cast<const unsigned short *>(args.x),
                         static_cast<const unsigned short *>(args.weight), args.target,
                         packs ? s.place : nullptr, args.ignore, rows, width, vocab,
                         static_cast<int>(up(vocab, bn) / bn), args.loss, args.lse, status};
     return launch_dependent(bf16 ? join_lse_kernel<__nv_bfloat16> : join_lse_kernel<__half>,
-                            (rows + 3) / 4, 128, 0, stream, j);
+                            (rows + 3) / 4, 1, 128, 0, stream, j);
 }
 
 cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t stream) {
@@ -1110,13 +1119,13 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
     p.ptarget = s.ptarget;
     p.plse2 = s.plse2;
     p.pdloss = s.pdloss;
-    p.counters = s.counters;
-    p.ncounters = s.pieces;
     p.status = status;
     CE_TRY(launch_pack(p, stream));
     if (odd_rows(width)) w = s.w;
     // dweight through shared memory and tensor-map stores where its rows allow
     const bool store = width % 8 == 0 && reinterpret_cast<uintptr_t>(args.dweight) % 16 == 0;
+    const int n_tiles = static_cast<int>(up(width, BN) / BN);
+    const int band = n_tiles >= 19 ? 4 : n_tiles <= 4 ? 19 : 76 / n_tiles;
     GemmMaps grad = {}, both = {};
     CE_TRY(make_map(&grad.a[0], bf16, s.x, rows, width, ld, a_rows));
     CE_TRY(make_map(&grad.out, bf16, s.grad, up(rows, BM), piece, piece, 32));
@@ -1134,15 +1143,15 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
     for (int i = 0; i < s.pieces; ++i) {
         const long long n0 = i * piece;
         const int n = static_cast<int>(vocab - n0 < piece ? vocab - n0 : piece);
-        CE_TRY(make_map(&grad.b[0], bf16, w + n0 * ld, n, width, ld, BN));
+        CE_TRY(make_map(&grad.b[0], bf16, w + n0 * ld, n, width, ld, BN / 2));
         CE_TRY(make_map(&both.b[0], bf16, w + n0 * ld, n, width, ld, BK));             // dx: W
         g.n0 = static_cast<int>(n0);
         g.accumulate = i > 0;
-        g.counter = s.counters + i;
-        g.job[0] = {rows, n, width, BN, a_rows, 1, nullptr, 0, 0};
+        g.job[0] = {rows, n, width, BN, a_rows, 1, 16, nullptr, 0, 0};
         CE_TRY((launch_gemm<EPI_GRAD, EPI_NONE>(grad, g, stream)));
-        g.job[0] = {args.dx != nullptr ? rows : 0, width, n, BN, a_rows, splits, s.acc, acc_ld, 0};
-        g.job[1] = {args.dweight != nullptr ? n : 0, width, rows, BN, BM, 1, nullptr, width, store};
+        g.job[0] = {args.dx != nullptr ? rows : 0, width, n, BN, a_rows, splits, 8, s.acc, acc_ld, 0};
+        g.job[1] = {args.dweight != nullptr ? n : 0, width, rows, BN, CM, 1, band, nullptr, width,
+                    store};
         if (args.dweight != nullptr) {
             unsigned short *to = static_cast<unsigned short *>(args.dweight) + n0 * width;
             g.job[1].out = to;
@@ -1152,12 +1161,12 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
     }
     if (args.dx == nullptr) return cudaSuccess;
     if (bf16)
-        return launch_dependent(finish_dx_kernel<__nv_bfloat16>, rows, 128, 0, stream,
+        return launch_dependent(finish_dx_kernel<__nv_bfloat16>, rows, 1, 128, 0, stream,
                                 static_cast<const float *>(s.acc), splits, g.slice,
                                 static_cast<int>(acc_ld), static_cast<const int *>(s.place),
                                 static_cast<const CeState *>(s.state),
                                 static_cast<__nv_bfloat16 *>(args.dx), width);
-    return launch_dependent(finish_dx_kernel<__half>, rows, 128, 0, stream,
+    return launch_dependent(finish_dx_kernel<__half>, rows, 1, 128, 0, stream,
                             static_cast<const float *>(s.acc), splits, g.slice,
                             static_cast<int>(acc_ld), static_cast<const int *>(s.place),
                             static_cast<const CeState *>(s.state), static_cast<__half *>(args.dx),

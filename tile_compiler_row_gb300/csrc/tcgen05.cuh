@@ -1,5 +1,9 @@
 // Inline PTX of the fifth-generation tensor cores (tcgen05), the tensor-map
-// copies (TMA) and mbarriers with bounded waits, for sm_103a.
+// copies (TMA) and mbarriers with bounded waits, for sm_103a.  MMAs, their
+// tensor memory and their loads are those of a CTA pair (cta_group::2): a
+// cluster of two CTAs works on one tile of 256 rows, each with half of A's
+// rows and half of B's in its shared memory and half of the accumulators'
+// rows in its tensor memory; the CTA of rank 0 issues.
 #pragma once
 
 #include <cuda.h>
@@ -22,6 +26,17 @@ __device__ __forceinline__ void bar_expect_tx(uint32_t bar, unsigned int bytes) 
 }
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The address that shared memory at `addr` of this CTA has in CTA `rank` of
+// the cluster.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+// Arrives on a barrier of any CTA of the cluster (a peer_addr).
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool bar_test(uint32_t bar, unsigned int parity) {
     unsigned int ok;
@@ -53,11 +68,13 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned int parity, vola
 }
 
 // ---- TMA -------------------------------------------------------------------------
+// A box at (x, y) into this CTA's shared memory, counted on `bar`, a
+// peer_addr of either CTA of the pair.
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y,
                                          uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
@@ -87,13 +104,13 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
 
 // ---- tensor memory and MMA -----------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, unsigned int columns) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
                  "r"(columns)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_free(uint32_t addr, unsigned int columns) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns)
                  : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() {
@@ -102,16 +119,19 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// Arrives on `bar` when every MMA issued so far by this thread is done.
+// Arrives on the barrier at `bar` of both CTAs of the pair when every MMA
+// issued so far by this thread is done.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     bar)
-                 : "memory");
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"(static_cast<unsigned short>(3))
+        : "memory");
 }
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        bool accumulate) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
                  "l"(a), "l"(b), "r"(idesc), "r"(static_cast<unsigned int>(accumulate))
                  : "memory");
 }
