@@ -590,7 +590,7 @@ __device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned 
 // it, 1.8e-3 without; the output's own rounding is 1.7e-3).  FP16 gradients
 // are scaled by 2^15 too: |p - onehot| <= 1, so nothing overflows, and what
 // underflows is below 2^-40 of the largest.
-constexpr int PACK_ROWS = 8;
+constexpr int PACK_ROWS = 8;   // at most a warp
 
 __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
     __shared__ int warp_before[8], warp_total[8], row_at[PACK_ROWS];
@@ -641,13 +641,14 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
         const float full = a.scaled ? 32768.0f : 1.0f;
         if (warp == 0) {
             const int i = r0 + lane;
-            const long long t = i < a.rows ? a.target[i] : a.ignore;
-            const float dl = i < a.rows && a.dloss != nullptr ? a.dloss[i] : 1.0f;
-            const bool in = i < a.rows && counts(t, a.ignore, a.vocab, dl);
+            const bool mine = lane < PACK_ROWS && i < a.rows;
+            const long long t = mine ? a.target[i] : a.ignore;
+            const float dl = mine && a.dloss != nullptr ? a.dloss[i] : 1.0f;
+            const bool in = mine && counts(t, a.ignore, a.vocab, dl);
             const unsigned int mask = __ballot_sync(0xffffffffu, in);
             const int at = before + __popc(mask & ((1u << lane) - 1u));
-            row_at[lane] = in ? at : -1;
-            if (i < a.rows) {
+            if (lane < PACK_ROWS) row_at[lane] = in ? at : -1;
+            if (mine) {
                 a.place[i] = in ? at : -1;
                 if (t != a.ignore && (t < 0 || t >= a.vocab)) atomicOr(a.status, CE_BAD_TARGET);
             }
