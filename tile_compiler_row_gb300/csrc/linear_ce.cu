@@ -197,6 +197,53 @@ __device__ __forceinline__ void store_tile16(const CUtensorMap *map, uint32_t tm
     }
 }
 
+// The same for rows off the 16-byte grid, which tensor-map stores do not
+// take: 32 rows x 64 columns through shared memory, then row by row, a warp
+// writing one row's 64 elements as 4-byte words (and single elements at its
+// ends where the row starts on an odd element).  Columns end at `end`.
+template <class F>
+__device__ __forceinline__ void store_rows16(unsigned short *out, long long ld, uint32_t tmem,
+                                             uint32_t buf, int lane, int bf16, int row0, int rows,
+                                             int col0, int end, F value) {
+    for (int c = 0; col0 + c < end; c += 64) {
+        __syncwarp();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float v[32];
+            tmem_load32(tmem + c + half * 32, v);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+                // word w of row r lies at word w ^ r of the row's 32
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(
+                                 buf + lane * 128 + 4 * ((half * 16 + j / 2) ^ lane)),
+                             "r"(pack2(bf16, value(v[j]), value(v[j + 1])))
+                             : "memory");
+            }
+        }
+        __syncwarp();
+        const int n = min(64, end - col0 - c), count = min(32, rows - row0);
+        for (int r = 0; r < count; ++r) {
+            unsigned int w;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(buf + r * 128 + 4 * (lane ^ r))
+                         : "memory");
+            unsigned short *to = out + static_cast<long long>(row0 + r) * ld + col0 + c;
+            const unsigned int next = __shfl_down_sync(0xffffffffu, w, 1);
+            if (reinterpret_cast<uintptr_t>(to) & 2) {   // words of elements 2 l + 1, 2 l + 2
+                if (lane == 0) to[0] = static_cast<unsigned short>(w);
+                if (2 * lane + 2 < n && lane < 31)
+                    *reinterpret_cast<unsigned int *>(to + 2 * lane + 1) = __funnelshift_r(w, next, 16);
+                else if (2 * lane + 1 < n)
+                    to[2 * lane + 1] = static_cast<unsigned short>(w >> 16);
+            } else {
+                if (2 * lane + 1 < n)
+                    *reinterpret_cast<unsigned int *>(to + 2 * lane) = w;
+                else if (2 * lane < n)
+                    to[2 * lane] = static_cast<unsigned short>(w);
+            }
+        }
+    }
+}
+
 // C[m][n] = sum_k A[m][k] B[n][k] for one or two jobs, tile by tile on a
 // persistent grid of CTA pairs: in each CTA a TMA warp fills a ring of A and
 // B tiles in shared memory, one thread of the pair issues the MMAs into one of
@@ -263,8 +310,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     // pairs; its last round serves `last` of them, and the others do `ahead`
     // tiles of the second job in that time.
     const int rounds = e0.tiles / pairs, last = e0.tiles % pairs;
-    const int ahead = EPI1 && last > 0 && e1.k_blocks > 0
-                          ? (e0.k_blocks / e0.splits + e1.k_blocks / 2) / e1.k_blocks : 0;
+    // (a short tile of few k blocks takes as long as its output's way to
+    // memory, about that of 6: 128 KiB of a pair's share of 6.8 TB/s)
+    const int cost = max(e1.k_blocks, 6);
+    const int ahead = EPI1 && last > 0 ? (e0.k_blocks / e0.splits + cost / 2) / cost : 0;
     auto tile_at = [&](int i) {
         if (i < rounds || (i == rounds && pair < last)) return i * pairs + pair;
         if (!EPI1) return -1;
@@ -444,18 +493,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     store_tile16(&maps.out, d, buf, turn, lane, g.bf16, row0, col0, cols, row0 < e.m,
                                  [&](float v, int) { return none ? 0.0f : v * f; });
                 } else {
-                    unsigned short *to = static_cast<unsigned short *>(job.out) +
-                                         static_cast<long long>(row) * job.ld + col0;
-                    for (int c = 0; c < job.bn && col0 + c < e.n; c += 32) {
-                        float v[32];
-                        tmem_load32(d + c, v);
-                        if (row < e.m)
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (col0 + c + j < e.n)
-                                    to[c + j] = static_cast<unsigned short>(
-                                        pack2(g.bf16, none ? 0.0f : v[j] * f, 0.0f));
-                    }
+                    store_rows16(static_cast<unsigned short *>(job.out), job.ld, d, buf, lane, g.bf16,
+                                 row0, e.m, col0, min(e.n, col0 + job.bn),
+                                 [&](float v) { return none ? 0.0f : v * f; });
                 }
             } else if (epi == EPI_DX) {   // FP32, ld a multiple of 4: rows of whole vectors
                 float *to = static_cast<float *>(job.out) + w.split * g.slice +
@@ -537,13 +577,12 @@ __device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned 
     const uintptr_t end = begin + static_cast<uintptr_t>(width) * 2;
     const int skew = static_cast<int>(begin & 15);
     const uintptr_t block0 = begin - skew;
-    for (int i0 = 0; i0 < vecs; i0 += 32) {
-        const int i = i0 + lane;
-        // a block with bytes outside the row is read by element
-        auto block = [&](int b) {
-            const uintptr_t at = block0 + static_cast<uintptr_t>(b) * 16;
-            if (at >= begin && at + 16 <= end) return __ldg(reinterpret_cast<const uint4 *>(at));
-            unsigned int w[4] = {};
+    // a block with bytes outside the row is read by element
+    auto block = [&](int b) {
+        const uintptr_t at = block0 + static_cast<uintptr_t>(b) * 16;
+        if (at >= begin && at + 16 <= end) return __ldg(reinterpret_cast<const uint4 *>(at));
+        unsigned int w[4] = {};
+        if (at < end)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uintptr_t p = at + 2 * j;
@@ -551,29 +590,36 @@ __device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned 
                     w[j / 2] |= static_cast<unsigned int>(
                                     *reinterpret_cast<const unsigned short *>(p)) << (16 * (j & 1));
             }
-            return make_uint4(w[0], w[1], w[2], w[3]);
-        };
-        const uint4 a = block(i);
-        uint4 b;
-        b.x = __shfl_down_sync(0xffffffffu, a.x, 1);
-        b.y = __shfl_down_sync(0xffffffffu, a.y, 1);
-        b.z = __shfl_down_sync(0xffffffffu, a.z, 1);
-        b.w = __shfl_down_sync(0xffffffffu, a.w, 1);
-        if (lane == 31) b = block(i + 1);
-        // bytes [skew, skew + 16) of a, b
-        const unsigned int w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        unsigned int r[4];
-        const int words = skew >> 2, bits = (skew & 3) * 8;
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    const int words = skew >> 2, bits = (skew & 3) * 8;
+    for (int i0 = 0; i0 < vecs; i0 += 128) {
+        uint4 a[5];   // the loads of four rounds at once
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            // w[words + j], w[words + j + 1] without indexing by a variable
-            unsigned int lo = w[j], hi = w[j + 1];
-            if (words == 1) { lo = w[j + 1]; hi = w[j + 2]; }
-            if (words == 2) { lo = w[j + 2]; hi = w[j + 3]; }
-            if (words == 3) { lo = w[j + 3]; hi = w[j + 4 < 8 ? j + 4 : 7]; }
-            r[j] = __funnelshift_r(lo, hi, bits);
+        for (int u = 0; u < 4; ++u) a[u] = block(i0 + u * 32 + lane);
+        // the block after this round's last, for lane 31
+        a[4] = block(i0 + 128);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            // the next lane's block; for the last lane the first of the next round
+            uint4 b;
+            b.x = __shfl_sync(0xffffffffu, lane == 0 ? a[u + 1].x : a[u].x, (lane + 1) & 31);
+            b.y = __shfl_sync(0xffffffffu, lane == 0 ? a[u + 1].y : a[u].y, (lane + 1) & 31);
+            b.z = __shfl_sync(0xffffffffu, lane == 0 ? a[u + 1].z : a[u].z, (lane + 1) & 31);
+            b.w = __shfl_sync(0xffffffffu, lane == 0 ? a[u + 1].w : a[u].w, (lane + 1) & 31);
+            // bytes [skew, skew + 16) of a, b: words moved by `words`, in two steps
+            unsigned int w[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b.x, b.y, b.z, b.w};
+            if (words & 1)
+#pragma unroll
+                for (int j = 0; j < 7; ++j) w[j] = w[j + 1];
+            if (words & 2)
+#pragma unroll
+                for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+            const int i = i0 + u * 32 + lane;
+            if (i < vecs)
+                out[i] = make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
         }
-        if (i < vecs) out[i] = make_uint4(r[0], r[1], r[2], r[3]);
     }
 }
 
@@ -771,38 +817,46 @@ __global__ void __launch_bounds__(128) join_lse_kernel(const JoinArgs a) {
 // ---- backward: the end ----------------------------------------------------------------
 
 // dx[i] = the sum of the slices' rows place[i], scaled back and rounded; 0
-// for rows that do not count.  One CTA a row.
+// for rows that do not count.  A CTA does 512 columns of a row, its slices'
+// loads 16 at a time.
+constexpr int FINISH_COLS = 512;
+
 template <class T>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(FINISH_COLS / 4)
     finish_dx_kernel(const float *acc, int splits, long long slice, int acc_ld, const int *place,
                      const CeState *state, T *dx, int width) {
     dependency_wait();
-    const long long r = blockIdx.x;
+    const int chunks = (width + FINISH_COLS - 1) / FINISH_COLS;
+    const long long r = blockIdx.x / chunks;
+    const int c = static_cast<int>(blockIdx.x % chunks) * FINISH_COLS + threadIdx.x * 4;
+    if (c >= width) return;
     const int p = place[r];
     const float f = state->unscale;
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (p >= 0) {
+        const float *from = acc + static_cast<long long>(p) * acc_ld + c;
+        for (int s = 0; s < splits; s += 16) {
+            float4 q[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (s + i < splits) q[i] = __ldcs(reinterpret_cast<const float4 *>(from + (s + i) * slice));
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (s + i < splits)
+                    t = make_float4(t.x + q[i].x, t.y + q[i].y, t.z + q[i].z, t.w + q[i].w);
+        }
+    }
     T *to = dx + r * width;
-    const bool vec = width % 4 == 0 && (reinterpret_cast<uintptr_t>(dx) & 7) == 0;
-    for (int c = threadIdx.x * 4; c < width; c += 512) {
-        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (p >= 0) {
-            const float *from = acc + static_cast<long long>(p) * acc_ld + c;
-#pragma unroll 4
-            for (int s = 0; s < splits; ++s) {
-                const float4 q = __ldcs(reinterpret_cast<const float4 *>(from + s * slice));
-                t = make_float4(t.x + q.x, t.y + q.y, t.z + q.z, t.w + q.w);
-            }
-        }
-        constexpr int bf16 = std::is_same<T, __nv_bfloat16>::value;
-        const uint32_t lo = pack2(bf16, t.x * f, t.y * f), hi = pack2(bf16, t.z * f, t.w * f);
-        if (vec) {
-            *reinterpret_cast<uint2 *>(to + c) = make_uint2(lo, hi);
-        } else {
-            unsigned short *o = reinterpret_cast<unsigned short *>(to);
-            o[c] = static_cast<unsigned short>(lo);
-            if (c + 1 < width) o[c + 1] = static_cast<unsigned short>(lo >> 16);
-            if (c + 2 < width) o[c + 2] = static_cast<unsigned short>(hi);
-            if (c + 3 < width) o[c + 3] = static_cast<unsigned short>(hi >> 16);
-        }
+    constexpr int bf16 = std::is_same<T, __nv_bfloat16>::value;
+    const uint32_t lo = pack2(bf16, t.x * f, t.y * f), hi = pack2(bf16, t.z * f, t.w * f);
+    if (width % 4 == 0 && (reinterpret_cast<uintptr_t>(dx) & 7) == 0) {
+        *reinterpret_cast<uint2 *>(to + c) = make_uint2(lo, hi);
+    } else {
+        unsigned short *o = reinterpret_cast<unsigned short *>(to);
+        o[c] = static_cast<unsigned short>(lo);
+        if (c + 1 < width) o[c + 1] = static_cast<unsigned short>(lo >> 16);
+        if (c + 2 < width) o[c + 2] = static_cast<unsigned short>(hi);
+        if (c + 3 < width) o[c + 3] = static_cast<unsigned short>(hi >> 16);
     }
 }
 
@@ -1161,13 +1215,16 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
         CE_TRY((launch_gemm<EPI_DX, EPI_DWEIGHT>(both, g, stream)));
     }
     if (args.dx == nullptr) return cudaSuccess;
+    const long long finish = rows * (up(width, FINISH_COLS) / FINISH_COLS);
+    if (finish > 0x7fffffffll) return cudaErrorInvalidValue;
+    const unsigned ctas = static_cast<unsigned>(finish);
     if (bf16)
-        return launch_dependent(finish_dx_kernel<__nv_bfloat16>, rows, 1, 128, 0, stream,
+        return launch_dependent(finish_dx_kernel<__nv_bfloat16>, ctas, 1, FINISH_COLS / 4, 0, stream,
                                 static_cast<const float *>(s.acc), splits, g.slice,
                                 static_cast<int>(acc_ld), static_cast<const int *>(s.place),
                                 static_cast<const CeState *>(s.state),
                                 static_cast<__nv_bfloat16 *>(args.dx), width);
-    return launch_dependent(finish_dx_kernel<__half>, rows, 1, 128, 0, stream,
+    return launch_dependent(finish_dx_kernel<__half>, ctas, 1, FINISH_COLS / 4, 0, stream,
                             static_cast<const float *>(s.acc), splits, g.slice,
                             static_cast<int>(acc_ld), static_cast<const int *>(s.place),
                             static_cast<const CeState *>(s.state), static_cast<__half *>(args.dx),
