@@ -43,9 +43,10 @@ constexpr int BM = 256, BN = 256, BK = 64;               // a CTA pair's tile
 constexpr int CM = BM / 2;                               // a CTA's rows of it
 constexpr int MOST_STAGES = 12;
 constexpr int PIPE_BYTES = 192 << 10;                    // stages of A and B tiles
-constexpr int STORE_BYTES = 32 << 10;                    // 4 warps, 2 buffers of 32 rows x 128 bytes
+constexpr int EPI_WARPS = 8;                             // two for each 32 rows of a CTA's tile
+constexpr int STORE_BYTES = EPI_WARPS * 4096;            // 32 rows x 128 bytes for each
 constexpr int GEMM_SMEM = PIPE_BYTES + STORE_BYTES + 1024;   // + slack to align to 1024
-constexpr int GEMM_THREADS = 192;                        // 4 epilogue warps, TMA, MMA
+constexpr int GEMM_THREADS = 32 * (EPI_WARPS + 2);       // and TMA, MMA
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum { EPI_NONE, EPI_LSE, EPI_GRAD, EPI_DWEIGHT, EPI_DX };
@@ -72,7 +73,7 @@ struct GemmArgs {
     Job job[2];
     const CeState *state;       // limits the packed rows (m of GRAD and DX, k of DWEIGHT), or NULL
     int bf16;
-    float2 *partial;            // EPI_LSE: [m][n tiles]
+    float2 *partial;            // EPI_LSE: [m][2 n tiles], each half of a tile's columns
     // EPI_GRAD: packed rows' target, lse log2(e) and scaled dloss
     const int *ptarget;
     const float *plse2, *pdloss;
@@ -164,11 +165,11 @@ __device__ __forceinline__ Extents extents(const Job &j, const CeState *state) {
 // the matrix's edges).  `value` maps column c + j's accumulator.
 template <class F>
 __device__ __forceinline__ void store_tile16(const CUtensorMap *map, uint32_t tmem, uint32_t buf,
-                                             int &turn, int lane, int bf16, int row0, int col0,
-                                             int cols, bool inside, F value) {
-    for (int c = 0; c < cols; c += 64) {
-        const uint32_t to = buf + turn * 4096 + lane * 128;
-        if (lane == 0) store_wait_read<1>();   // the buffer's store before last has read it
+                                             int lane, int bf16, int row0, int col0, int from,
+                                             int end, bool inside, F value) {
+    for (int c = from; c < end; c += 64) {
+        const uint32_t to = buf + lane * 128;
+        if (lane == 0) store_wait_read<0>();   // the buffer's last store has read it
         __syncwarp();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -190,22 +191,21 @@ __device__ __forceinline__ void store_tile16(const CUtensorMap *map, uint32_t tm
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-            if (inside) tma_store(map, col0 + c, row0, buf + turn * 4096);
+            if (inside) tma_store(map, col0 + c, row0, buf);
             store_commit();
         }
-        turn ^= 1;
     }
 }
 
 // The same for rows off the 16-byte grid, which tensor-map stores do not
 // take: 32 rows x 64 columns through shared memory, then row by row, a warp
 // writing one row's 64 elements as 4-byte words (and single elements at its
-// ends where the row starts on an odd element).  Columns end at `end`.
+// ends where the row starts on an odd element).
 template <class F>
 __device__ __forceinline__ void store_rows16(unsigned short *out, long long ld, uint32_t tmem,
                                              uint32_t buf, int lane, int bf16, int row0, int rows,
-                                             int col0, int end, F value) {
-    for (int c = 0; col0 + c < end; c += 64) {
+                                             int col0, int from, int end, F value) {
+    for (int c = from; c < end; c += 64) {
         __syncwarp();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -221,7 +221,8 @@ __device__ __forceinline__ void store_rows16(unsigned short *out, long long ld, 
             }
         }
         __syncwarp();
-        const int n = min(64, end - col0 - c), count = min(32, rows - row0);
+        const int n = min(64, end - c), count = min(32, rows - row0);
+#pragma unroll 8
         for (int r = 0; r < count; ++r) {
             unsigned int w;
             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(buf + r * 128 + 4 * (lane ^ r))
@@ -247,7 +248,7 @@ __device__ __forceinline__ void store_rows16(unsigned short *out, long long ld, 
 // C[m][n] = sum_k A[m][k] B[n][k] for one or two jobs, tile by tile on a
 // persistent grid of CTA pairs: in each CTA a TMA warp fills a ring of A and
 // B tiles in shared memory, one thread of the pair issues the MMAs into one of
-// two accumulators in tensor memory (256 columns each), and four warps turn
+// two accumulators in tensor memory (256 columns each), and eight warps turn
 // the other into the epilogue's output.  A pair reads 32 KiB per CTA and 64
 // columns of K from L2, where a CTA with a tile of its own reads 48: L2
 // delivers some 12.5 TB/s, which bound the gradients' products with single
@@ -288,13 +289,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(acc_full(s), 1);
-            bar_init(acc_empty(s), 8); // rank 0's: four epilogue warps of each CTA
+            bar_init(acc_empty(s), 2 * EPI_WARPS);   // rank 0's: both CTAs' epilogue warps
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&maps.a[0]);
         prefetch_map(&maps.b[0]);
     }
-    if (warp == 5) tmem_alloc(smem_u32(&tmem_slot), 512);
+    if (warp == EPI_WARPS + 1) tmem_alloc(smem_u32(&tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
     cluster_sync();
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                             : (split == 0 ? 0 : e1.k_blocks);
     };
 
-    if (warp == 4 && lane == 0) {   // TMA producer
+    if (warp == EPI_WARPS && lane == 0) {   // TMA producer
         int stage = 0;
         unsigned int phase = 0;
         long long issued = 0;
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             for (long long i = issued > stages ? issued - stages : 0; i < issued; ++i)
                 for (unsigned int n = 0; n < kBarSpins; ++n)
                     if (bar_test(full(static_cast<int>(i % stages)), (i / stages) & 1)) break;
-    } else if (warp == 5 && lane == 0 && rank == 0) {   // MMA issuer
+    } else if (warp == EPI_WARPS + 1 && lane == 0 && rank == 0) {   // MMA issuer
         int stage = 0, acc = 0;
         unsigned int phase = 0, acc_phase = 0;
         bool ok = true;
@@ -431,10 +432,14 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             for (unsigned int n = 0; n < kBarSpins; ++n)
                 if (bar_test(acc_full(acc), acc_phase)) break;
         }
-    } else if (warp < 4) {   // epilogue: thread = row of the tile
-        int acc = 0, turn = 0;
+    } else if (warp < EPI_WARPS) {
+        // epilogue: thread = row of the tile; warps w and w + 4 share 32 rows
+        // (a warp reads the quarter of tensor memory's lanes of its number
+        // modulo 4) and take half of the columns each
+        int acc = 0;
         unsigned int acc_phase = 0;
-        const uint32_t buf = base + PIPE_BYTES + warp * 8192;
+        const uint32_t buf = base + PIPE_BYTES + warp * 4096;
+        const int quarter = warp & 3, half = warp >> 2;
         const uint32_t drained0 = peer_addr(acc_empty(0), 0), drained1 = peer_addr(acc_empty(1), 0);
         int t;
         for (int i = 0; (t = tile_at(i)) >= 0; ++i) {
@@ -445,18 +450,21 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             const bool second = EPI1 && t >= e0.tiles;
             const Job &job = g.job[second ? 1 : 0];
             const Extents &e = second ? e1 : e0;
-            const int row0 = w.m * BM + rank * CM + warp * 32, row = row0 + lane;
+            const int row0 = w.m * BM + rank * CM + quarter * 32, row = row0 + lane;
             const int col0 = w.n * job.bn;
-            const uint32_t d = tmem + acc * BN + (static_cast<uint32_t>(warp * 32) << 16);
+            // this warp's columns of the tile: [from, to), and those that exist
+            const int from = half * (job.bn / 2), to = from + job.bn / 2;
+            const int end = min(to, e.n - col0);
+            const uint32_t d = tmem + acc * BN + (static_cast<uint32_t>(quarter * 32) << 16);
             // no product was made: zero
             const bool none = k_begin(t, w.split) == k_begin(t, w.split + 1);
             const int epi = second ? EPI1 : EPI0;
             if (epi == EPI_LSE) {
                 float m = -INFINITY, s = 0.0f;
-                for (int c = 0; c < job.bn && col0 + c < e.n; c += 32) {
+                for (int c = from; c < end; c += 32) {
                     float v[32];
                     tmem_load32(d + c, v);
-                    const int limit = min(job.bn - c, e.n - col0 - c);
+                    const int limit = end - c;
                     if (limit < 32)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -473,14 +481,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     m = top;
                 }
                 if (row < e.m)
-                    g.partial[static_cast<long long>(row) * e.n_tiles + w.n] = make_float2(m, s);
+                    g.partial[(static_cast<long long>(row) * e.n_tiles + w.n) * 2 + half] =
+                        make_float2(m, s);
             } else if (epi == EPI_GRAD) {
                 const bool in = row < e.m;
                 const int want = in ? g.ptarget[row] - g.n0 - col0 : -1;
                 const float lse2 = in ? g.plse2[row] : 0.0f, dl = in ? g.pdloss[row] : 0.0f;
                 const int limit = in ? e.n - col0 : 0;
                 // rows up to the next 64 are written: dW's reduction reads them
-                store_tile16(&maps.out, d, buf, turn, lane, g.bf16, row0, col0, BN,
+                store_tile16(&maps.out, d, buf, lane, g.bf16, row0, col0, from, to,
                              row0 < (e.m + BK - 1) / BK * BK,
                              [&](float v, int c) {
                                  const float p = ex2(fmaf(v, kLog2e, -lse2));
@@ -489,18 +498,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             } else if (epi == EPI_DWEIGHT) {
                 const float f = none ? 0.0f : g.state->unscale;
                 if (job.store) {
-                    const int cols = min(job.bn, (e.n - col0 + 63) / 64 * 64);
-                    store_tile16(&maps.out, d, buf, turn, lane, g.bf16, row0, col0, cols, row0 < e.m,
+                    store_tile16(&maps.out, d, buf, lane, g.bf16, row0, col0, from, end, row0 < e.m,
                                  [&](float v, int) { return none ? 0.0f : v * f; });
                 } else {
                     store_rows16(static_cast<unsigned short *>(job.out), job.ld, d, buf, lane, g.bf16,
-                                 row0, e.m, col0, min(e.n, col0 + job.bn),
+                                 row0, e.m, col0, from, end,
                                  [&](float v) { return none ? 0.0f : v * f; });
                 }
             } else if (epi == EPI_DX) {   // FP32, ld a multiple of 4: rows of whole vectors
-                float *to = static_cast<float *>(job.out) + w.split * g.slice +
-                            static_cast<long long>(row) * job.ld + col0;
-                for (int c = 0; c < job.bn && col0 + c < job.ld; c += 32) {
+                float *out = static_cast<float *>(job.out) + w.split * g.slice +
+                             static_cast<long long>(row) * job.ld + col0;
+                for (int c = from; c < to && col0 + c < job.ld; c += 32) {
                     float v[32];
                     tmem_load32(d + c, v);
                     if (row < e.m)
@@ -509,7 +517,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                             if (col0 + c + j >= job.ld) break;
                             float4 q = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
                                             : make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                            float4 *p = reinterpret_cast<float4 *>(to + c + j);
+                            float4 *p = reinterpret_cast<float4 *>(out + c + j);
                             if (g.accumulate) {
                                 const float4 o = *p;
                                 q = make_float4(q.x + o.x, q.y + o.y, q.z + o.z, q.w + o.w);
@@ -531,7 +539,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     __syncthreads();
     cluster_sync();   // neither CTA leaves while the other uses its memory
     tc_fence_after();
-    if (warp == 5) tmem_free(tmem, 512);
+    if (warp == EPI_WARPS + 1) tmem_free(tmem, 512);
 }
 
 // ---- packing rows ----------------------------------------------------------------------
@@ -767,12 +775,12 @@ struct JoinArgs {
     const long long *target;
     const int *place;   // where a row was packed, or NULL
     long long ignore;
-    int rows, width, vocab, n_tiles;
+    int rows, width, vocab, partials;
     float *loss, *lse;
     unsigned int *status;
 };
 
-// One warp a row: lanes over the n tiles, joined in a fixed tree.
+// One warp a row: lanes over the half tiles, joined in a fixed tree.
 template <class T>
 __global__ void __launch_bounds__(128) join_lse_kernel(const JoinArgs a) {
     const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -797,13 +805,13 @@ __global__ void __launch_bounds__(128) join_lse_kernel(const JoinArgs a) {
         return;
     }
     const int at = a.place != nullptr ? a.place[row] : row;
-    const float2 *p = a.partial + static_cast<long long>(at) * a.n_tiles;
+    const float2 *p = a.partial + static_cast<long long>(at) * a.partials;
     float m = -INFINITY;
-    for (int i = lane; i < a.n_tiles; i += 32) m = fmaxf(m, p[i].x);
+    for (int i = lane; i < a.partials; i += 32) m = fmaxf(m, p[i].x);
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float ref = m == -INFINITY ? 0.0f : m;
     float s = 0.0f;
-    for (int i = lane; i < a.n_tiles; i += 32) {
+    for (int i = lane; i < a.partials; i += 32) {
         const float2 q = p[i];
         s += q.y * expf(q.x - ref);
     }
@@ -1002,7 +1010,7 @@ ForwardSpace forward_space(void *ws, int rows, int width, int vocab) {
     ForwardSpace s = {};
     const long long ld = up(width, 8);
     const int bn = forward_columns(rows, vocab);
-    s.partial = c.take<float2>(rows * (up(vocab, bn) / bn));
+    s.partial = c.take<float2>(rows * (up(vocab, bn) / bn) * 2);
     if (forward_packs(rows, width, vocab)) {
         s.state = c.take<CeState>(1);
         s.place = c.take<int>(rows);
@@ -1138,7 +1146,7 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
     const JoinArgs j = {s.partial, static_cast<const unsigned short *>(args.x),
                         static_cast<const unsigned short *>(args.weight), args.target,
                         packs ? s.place : nullptr, args.ignore, rows, width, vocab,
-                        static_cast<int>(up(vocab, bn) / bn), args.loss, args.lse, status};
+                        static_cast<int>(up(vocab, bn) / bn * 2), args.loss, args.lse, status};
     return launch_dependent(bf16 ? join_lse_kernel<__nv_bfloat16> : join_lse_kernel<__half>,
                             (rows + 3) / 4, 1, 128, 0, stream, j);
 }
