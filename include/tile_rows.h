@@ -439,9 +439,10 @@ int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *
  * of 0, and sets the device status word (tile_check_device_status).
  *
  * `workspace`: device memory of the caller, 256-byte aligned, at least
- * tile_linear_cross_entropy_workspace_bytes(rows, width, vocab) bytes: two
- * numbers per row and 256 vocabulary entries, and, for widths that are not
- * multiples of 8, copies of in and weight in rows that are.  Calls that
+ * tile_linear_cross_entropy_workspace_bytes(rows, width, vocab) bytes: four
+ * numbers per row and tile of 192 to 256 vocabulary entries, for long calls
+ * a copy of in (the rows that count), and, for widths that are not multiples
+ * of 8, of weight, in rows of whole 128 bytes.  Calls that
  * overlap in time need workspaces of their own.  in and weight: 16-byte
  * aligned where width is a multiple of 8, else 2-byte (TILE_ERR_ALIGN).
  * Other rules and errors as the row entry points (TILE_ERR_SHAPE also for

@@ -576,9 +576,11 @@ __device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned 
         for (int i = lane; i < vecs; i += 32) out[i] = make_uint4(0, 0, 0, 0);
         return;
     }
-    if (width == ld && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
+    if (width % 8 == 0 && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
         const uint4 *in = reinterpret_cast<const uint4 *>(from);
-        for (int i = lane; i < vecs; i += 32) out[i] = __ldg(in + i);
+#pragma unroll 4
+        for (int i = lane; i < vecs; i += 32)
+            out[i] = i < width / 8 ? __ldg(in + i) : make_uint4(0, 0, 0, 0);
         return;
     }
     const uintptr_t begin = reinterpret_cast<uintptr_t>(from);
@@ -966,9 +968,12 @@ struct Carver {
     }
 };
 
-// Rows of an odd width are copied to rows of a multiple of 8 elements (TMA
-// wants strides of 16 bytes).
+// Rows of an odd width are copied (TMA wants strides of 16 bytes), and copies
+// have rows of whole 128-byte lines: with 16-byte strides every 128-byte row
+// of a box lies in two lines, and the products of 1537 columns used the
+// tensor cores 62 % of the time.
 bool odd_rows(int width) { return width % 8 != 0; }
+long long copied_ld(int width) { return up(width, 64); }
 
 // Whether a forward call packs the rows that count: where x is copied
 // anyway, and where the product takes some 300 us, against which finding and
@@ -1008,7 +1013,7 @@ int forward_columns(int rows, int vocab) {
 ForwardSpace forward_space(void *ws, int rows, int width, int vocab) {
     Carver c{static_cast<unsigned char *>(ws), 0};
     ForwardSpace s = {};
-    const long long ld = up(width, 8);
+    const long long ld = copied_ld(width);
     const int bn = forward_columns(rows, vocab);
     s.partial = c.take<float2>(rows * (up(vocab, bn) / bn) * 2);
     if (forward_packs(rows, width, vocab)) {
@@ -1055,7 +1060,7 @@ struct BackwardSpace {
 BackwardSpace backward_space(void *ws, int rows, int width, int vocab) {
     Carver c{static_cast<unsigned char *>(ws), 0};
     BackwardSpace s;
-    const long long ld = up(width, 8), piece = piece_of(rows, vocab);
+    const long long ld = copied_ld(width), piece = piece_of(rows, vocab);
     s.pieces = static_cast<int>((vocab + piece - 1) / piece);
     s.state = c.take<CeState>(1);
     s.place = c.take<int>(rows);
@@ -1108,7 +1113,7 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
     const int rows = args.rows, width = args.width, vocab = args.vocab;
     const int bf16 = args.elem == ELEM_BF16;
     const ForwardSpace s = forward_space(args.ws, rows, width, vocab);
-    const long long ld = up(width, 8);
+    long long x_ld = width, w_ld = width;
     const void *x = args.x, *w = args.weight;
     const bool packs = forward_packs(rows, width, vocab);
     if (packs) {
@@ -1120,7 +1125,8 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
         p.rows = rows;
         p.width = width;
         p.vocab = vocab;
-        p.ld = static_cast<int>(ld);
+        x_ld = copied_ld(width);
+        p.ld = static_cast<int>(x_ld);
         p.place_rows = 1;
         p.px = s.x;
         p.pw = s.w;
@@ -1130,7 +1136,10 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
         p.status = status;
         CE_TRY(launch_pack(p, stream));
         x = s.x;
-        if (odd_rows(width)) w = s.w;
+        if (odd_rows(width)) {
+            w = s.w;
+            w_ld = x_ld;
+        }
     }
     const int bn = forward_columns(rows, vocab);
     GemmMaps maps = {};
@@ -1140,8 +1149,8 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
     g.bf16 = bf16;
     g.partial = s.partial;
     g.status = status;
-    CE_TRY(make_map(&maps.a[0], bf16, x, rows, width, ld, g.job[0].a_rows));
-    CE_TRY(make_map(&maps.b[0], bf16, w, vocab, width, ld, bn / 2));
+    CE_TRY(make_map(&maps.a[0], bf16, x, rows, width, x_ld, g.job[0].a_rows));
+    CE_TRY(make_map(&maps.b[0], bf16, w, vocab, width, w_ld, bn / 2));
     CE_TRY((launch_gemm<EPI_LSE, EPI_NONE>(maps, g, stream)));
     const JoinArgs j = {s.partial, static_cast<const unsigned short *>(args.x),
                         static_cast<const unsigned short *>(args.weight), args.target,
@@ -1158,7 +1167,8 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
     const int rows = args.rows, width = args.width, vocab = args.vocab;
     const int bf16 = args.elem == ELEM_BF16;
     const BackwardSpace s = backward_space(args.ws, rows, width, vocab);
-    const long long ld = up(width, 8), piece = piece_of(rows, vocab), acc_ld = up(width, 4);
+    const long long ld = copied_ld(width), w_ld = odd_rows(width) ? ld : width;
+    const long long piece = piece_of(rows, vocab), acc_ld = up(width, 4);
     const int splits = splits_of(rows, width, vocab), a_rows = rows_of_a(rows);
     const unsigned short *w = static_cast<const unsigned short *>(args.weight);
     PackArgs p = {};
@@ -1206,8 +1216,8 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
     for (int i = 0; i < s.pieces; ++i) {
         const long long n0 = i * piece;
         const int n = static_cast<int>(vocab - n0 < piece ? vocab - n0 : piece);
-        CE_TRY(make_map(&grad.b[0], bf16, w + n0 * ld, n, width, ld, BN / 2));
-        CE_TRY(make_map(&both.b[0], bf16, w + n0 * ld, n, width, ld, BK));             // dx: W
+        CE_TRY(make_map(&grad.b[0], bf16, w + n0 * w_ld, n, width, w_ld, BN / 2));
+        CE_TRY(make_map(&both.b[0], bf16, w + n0 * w_ld, n, width, w_ld, BK));             // dx: W
         g.n0 = static_cast<int>(n0);
         g.accumulate = i > 0;
         g.job[0] = {rows, n, width, BN, a_rows, 1, 16, nullptr, 0, 0};
