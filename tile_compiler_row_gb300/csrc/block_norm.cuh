@@ -85,23 +85,44 @@ struct Vec {
     }
 };
 
-// A vector of a row that lies off the 16-byte grid: `first` is the column of
-// its first element (negative, or so near the width that not all of it is
-// the row's, at the row's ends).
+// The vectors that hold a row which lies off the 16-byte grid: its first
+// begins `shift` elements before the row, and its last may reach past its end.
+// The masks of those two lie in shared memory (a thread's own test of eight
+// elements for each vector, row and input made the threads at a row's ends
+// the last of their CTA: 16384 x 4097 BF16 backward 345 us).
+struct EdgeMasks {
+    uint4 first, last;
+};
+enum { EDGE_FIRST = 1, EDGE_LAST = 2 };
+
 template <class T>
-__device__ __forceinline__ uint4 mask_vec(uint4 t, int first, int width) {
+__device__ __forceinline__ uint4 mask_of(int from, int to) {   // elements [from, to) of a vector
     constexpr int N = 16 / sizeof(T);
-    if (first >= 0 && first + N <= width) return t;
-    unsigned int w[4] = {t.x, t.y, t.z, t.w};
+    unsigned int w[4] = {};
 #pragma unroll
     for (int j = 0; j < N; ++j)
-        if (first + j < 0 || first + j >= width) {
-            if constexpr (sizeof(T) == 4)
-                w[j] = 0u;
-            else
-                w[j / 2] &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
-        }
+        if (j >= from && j < to)
+            w[j * static_cast<int>(sizeof(T)) / 4] |=
+                sizeof(T) == 4 ? 0xffffffffu : 0xffffu << (16 * (j & 1));
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <class T>
+__device__ __forceinline__ void edge_masks(EdgeMasks &m, int shift, int width) {
+    constexpr int N = 16 / sizeof(T);
+    m.first = mask_of<T>(shift, N);
+    m.last = mask_of<T>(0, (width + shift - 1) % N + 1);
+}
+// Which ends vector v of `vecs` is.
+__device__ __forceinline__ int edge_of(int v, int vecs) {
+    return (v == 0 ? EDGE_FIRST : 0) | (v == vecs - 1 ? EDGE_LAST : 0);
+}
+__device__ __forceinline__ uint4 and4(uint4 a, uint4 b) {
+    return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
+}
+__device__ __forceinline__ uint4 mask_vec(uint4 t, int edge, const EdgeMasks &m) {
+    if (edge & EDGE_FIRST) t = and4(t, m.first);
+    if (edge & EDGE_LAST) t = and4(t, m.last);
+    return t;
 }
 // Its store: whole, or the elements that are the row's.
 template <class T>
@@ -215,10 +236,18 @@ struct ReduceMem {
     float cta[2][N];
 };
 
-// Sums of s over the row's threads, in a fixed order, for all of them.
+// Sums of s over the row's threads, in a fixed order, for all of them: the
+// threads of `warps` warps of each CTA of the cluster, or `lanes` neighbours
+// of a warp (a power of two).
 template <int N, bool CL>
 __device__ __forceinline__ void row_sum(float (&s)[N], ReduceMem<N> &mem, int &turn, int warps,
-                                        int cluster) {
+                                        int cluster, int lanes = 32) {
+    if (lanes < 32) {
+        for (int d = lanes >> 1; d > 0; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
+        return;
+    }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
@@ -265,7 +294,7 @@ __host__ __device__ inline long long unit_of_row(long long r, long long rows, lo
 
 // The layout of a program that walks over rows.
 struct RingPlan {
-    int workers;    // W: threads of a CTA
+    int workers;    // W: threads of a program in a CTA (below 32: neighbours in a warp)
     int cluster;    // C
     int slots;      // ring kernel: slots, and bytes of a slot's part for one input
     int pitch;

@@ -200,10 +200,10 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockArg
 
 // Joins the programs' column sums, in program order: blockIdx.y 0 and 1 the
 // gamma gradients, the others the gate rows that more than one program
-// holds.  A CTA sums 32 columns with 16 threads each, over 16 contiguous
+// holds.  A CTA sums 32 columns with 32 threads each, over 32 contiguous
 // runs of programs, joined in order.  per_gate_units: programs of a gate row
 // where programs keep to one, else 0 (contiguous ranges of rows).
-constexpr int kJoinCols = 32, kJoinRuns = 16;
+constexpr int kJoinCols = 32, kJoinRuns = 32;
 
 __global__ void __launch_bounds__(kJoinCols *kJoinRuns)
     block_norm_join_kernel(const BlockArgs a, long long units, long long gates,
@@ -228,9 +228,11 @@ __global__ void __launch_bounds__(kJoinCols *kJoinRuns)
         run_sum[run][c] = t;
         __syncthreads();
         t = 0.0f;
-        for (int i = 0; i < kJoinRuns; ++i) t += run_sum[i][c];
+        if (run == 0)
+#pragma unroll
+            for (int i = 0; i < kJoinRuns; ++i) t += run_sum[i][c];
         __syncthreads();
-        return t;
+        return t;   // (run 0's)
     };
     if (blockIdx.y < 2) {
         float *to = blockIdx.y == 0 ? a.dgamma_pre : a.dgamma_post;
@@ -272,6 +274,8 @@ RingPlan ring_plan(int width) {
     RingPlan p = {};
     // vectors that hold a row, wherever it starts
     const int vecs = (width + (SHIFT ? N - 1 : 0) + N - 1) / N;
+    // (CTAs of 512 threads, one to an SM, before clusters: 8192 x 8192 BF16
+    // took 177 us in clusters of two, two CTAs to an SM, and 149 us so)
     int c = 1;
     while (c <= 8 && (vecs + c - 1) / c > 512 * K) c *= 2;
     if (c > 8) return p;
@@ -280,8 +284,9 @@ RingPlan ring_plan(int width) {
     p.pitch = (c == 1 ? vecs : p.workers * K) * 16;
     // as many CTAs to an SM as registers allow, the ring cut to fit
     int per_sm = 65536 / (p.workers * 128);
+    if (p.workers == 288 || p.workers == 320) per_sm = 2;   // (96 registers)
     per_sm = per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm;
-    p.slots = ((224 << 10) / per_sm - 3072) / (4 * p.pitch);
+    p.slots = ((224 << 10) / per_sm - (3 << 10)) / (4 * p.pitch);
     p.slots = p.slots > kRingMost ? kRingMost : p.slots;
     p.smem = p.slots * 4 * p.pitch;
     p.classes = 1;
@@ -348,9 +353,18 @@ cudaError_t launch_ring(Kernel kernel, const BlockArgs &a, RingPlan p, cudaStrea
 template <class T, bool SHIFT>
 cudaError_t launch_ring_typed(const BlockArgs &a, const RingPlan &p, cudaStream_t stream,
                               Programs *out) {
+    constexpr int K = kRingVecs;
+    if (p.workers <= 256)
+        return p.cluster == 1
+                   ? launch_ring(block_norm_ring_kernel<T, K, SHIFT, false, 256, 2>, a, p, stream, out)
+                   : launch_ring(block_norm_ring_kernel<T, K, SHIFT, true, 256, 2>, a, p, stream, out);
+    if (p.workers <= 320)
+        return p.cluster == 1
+                   ? launch_ring(block_norm_ring_kernel<T, K, SHIFT, false, 320, 2>, a, p, stream, out)
+                   : launch_ring(block_norm_ring_kernel<T, K, SHIFT, true, 320, 2>, a, p, stream, out);
     return p.cluster == 1
-               ? launch_ring(block_norm_ring_kernel<T, kRingVecs, SHIFT, false>, a, p, stream, out)
-               : launch_ring(block_norm_ring_kernel<T, kRingVecs, SHIFT, true>, a, p, stream, out);
+               ? launch_ring(block_norm_ring_kernel<T, K, SHIFT, false, 512, 1>, a, p, stream, out)
+               : launch_ring(block_norm_ring_kernel<T, K, SHIFT, true, 512, 1>, a, p, stream, out);
 }
 
 template <class T, int V, int E, bool CL>

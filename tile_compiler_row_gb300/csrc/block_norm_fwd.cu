@@ -18,20 +18,25 @@ TILE_DEVICE_STATUS(block_norm)
 namespace tile {
 namespace {
 
-template <class T, int V, int K, bool CL>
-__global__ void __launch_bounds__(512) block_norm_kernel(const BlockArgs a, int warps, int cluster) {
+// A row is `workers` threads of each of `cluster` CTAs: whole warps, or a
+// power of two of neighbours of a warp, which then holds several rows.
+template <class T, int V, int K, bool CL, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB)
+    block_norm_kernel(const BlockArgs a, int workers, int cluster) {
     using A = Access<T, V>;
     constexpr int G = V == 1 ? 2 : V, GK = G / V;   // columns handled together, in GK groups
     constexpr int E = K * V;
     static_assert(K % GK == 0, "whole pairs");
     __shared__ ReduceMem<1> mem;
-    const int W = warps * 32;
+    const int W = workers, warps = (W + 31) / 32, lanes = W < 32 ? W : 32;
     const int programs = CL ? 1 : blockDim.x / W;
     const int rank = CL ? static_cast<int>(cluster_rank()) : 0;
     const int worker = CL ? threadIdx.x : threadIdx.x % W;
-    const long long row = CL ? blockIdx.x / cluster
-                             : static_cast<long long>(blockIdx.x) * programs + threadIdx.x / W;
-    if (row >= a.rows) return;   // whole warps: programs share a CTA only at one warp each
+    const long long row0 = CL ? blockIdx.x / cluster
+                              : static_cast<long long>(blockIdx.x) * programs + threadIdx.x / W;
+    // threads behind the last row do it once more, without stores
+    const bool live = row0 < a.rows;
+    const long long row = live ? row0 : a.rows - 1;
     const float inv_n = 1.0f / static_cast<float>(a.width);
     const int step = (CL ? cluster : 1) * W * V, first = (rank * W + worker) * V;
     const T *x = static_cast<const T *>(a.x) + row * a.width + first;
@@ -69,7 +74,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const BlockArgs a, int 
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) sq = fma2(v[i], v[i], sq);
         float s[1] = {total(sq)};
-        row_sum<1, CL>(s, mem, turn, warps, cluster);
+        row_sum<1, CL>(s, mem, turn, warps, cluster, lanes);
         r1 = inv_sqrt<T>(fmaf(s[0], inv_n, a.eps));
     }
     sq = 0;
@@ -102,7 +107,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const BlockArgs a, int 
         }
 #pragma unroll
         for (int u = 0; u < GK; ++u)
-            if (first + (k + u) * step < a.width) {
+            if (live && first + (k + u) * step < a.width) {
                 float o[V];
 #pragma unroll
                 for (int j = 0; j < V; ++j) o[j] = g[u * V + j];
@@ -111,7 +116,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const BlockArgs a, int 
     }
     if (a.pre) {
         float s[1] = {total(sq)};
-        row_sum<1, CL>(s, mem, turn, warps, cluster);
+        row_sum<1, CL>(s, mem, turn, warps, cluster, lanes);
         const F2 r2 = both(inv_sqrt<T>(fmaf(s[0], inv_n, a.eps)));
 #pragma unroll
         for (int k = 0; k < K; k += GK) {
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const BlockArgs a, int 
                        p[2 * i + 1]);
 #pragma unroll
             for (int u = 0; u < GK; ++u)
-                if (first + (k + u) * step < a.width) {
+                if (live && first + (k + u) * step < a.width) {
                     float o[V];
 #pragma unroll
                     for (int j = 0; j < V; ++j) o[j] = p[u * V + j];
@@ -141,25 +146,41 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const BlockArgs a, int 
     if constexpr (CL) cluster_barrier();   // peers may still read this CTA's sums
 }
 
-// Rows that are not whole vectors: a program takes rows that start at the
+// Two-byte rows that are not whole vectors: a program takes rows that start at the
 // same offset into a 16-byte block (every second, fourth or eighth), so each
 // thread reads and writes the same aligned vectors of them and owns the same
 // columns, whose parameters it keeps in registers (from L1 they would be
 // single-element loads); the vectors at a row's ends are masked.  The next
 // row is loaded before the present one is worked on.  Single-element
 // accesses (the kernel above with V = 1) ran 16384 x 4097 BF16 in 291 us.
-template <class T, int K, bool CL>
-__global__ void __launch_bounds__(512)
+template <class T, int K, bool CL, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB)
     block_norm_shift_kernel(const BlockArgs a, const RingPlan plan) {
     using X = Vec<T>;
     constexpr int N = X::N, P = X::P;
     __shared__ ReduceMem<1> mem;
-    const int W = plan.workers, warps = W >> 5, tid = threadIdx.x;
-    const int C = CL ? plan.cluster : 1;
+    const int W = plan.workers, warps = (W + 31) / 32, lanes = W < 32 ? W : 32;
+    const int C = CL ? plan.cluster : 1, programs = CL ? 1 : blockDim.x / W;
     const int rank = CL ? static_cast<int>(cluster_rank()) : 0;
-    const int width = a.width;
-    const RowWalk walk = row_walk(a.rows, a.rows, plan, blockIdx.x / C, gridDim.x / C);
+    const int width = a.width, tid = CL ? threadIdx.x : threadIdx.x % W;
+    const RowWalk walk = row_walk(a.rows, a.rows, plan,
+                                  CL ? blockIdx.x / C
+                                     : static_cast<long long>(blockIdx.x) * programs + threadIdx.x / W,
+                                  gridDim.x / C * static_cast<long long>(programs));
+    // programs of one warp go round together, those without a row left idly
+    long long rounds = walk.count;
+    if (lanes < 32)
+        for (int d = 16; d > 0; d >>= 1) {
+            const long long o = __shfl_xor_sync(0xffffffffu, rounds, d);
+            rounds = o > rounds ? o : rounds;
+        }
     const int shift = static_cast<int>((walk.first * width) & (N - 1));
+    // masks of this program's rows (programs of at most 32 threads share a CTA
+    // of 256, so up to 256 of them)
+    __shared__ EdgeMasks all_masks[CL ? 1 : 256];
+    EdgeMasks &masks = all_masks[CL ? 0 : threadIdx.x / W];
+    if (tid == 0) edge_masks<T>(masks, shift, width);
+    __syncthreads();
     const int vecs = (width + shift + N - 1) / N;
     auto vec = [&](int k) { return rank * W * K + k * W + tid; };
     auto first = [&](int k) { return vec(k) * N - shift; };   // column of vector k
@@ -203,9 +224,10 @@ __global__ void __launch_bounds__(512)
     long long gate_end = walk.first;
     int turn = 0;
     const F2 scale = both(a.scale);
-    for (long long i_row = 0; i_row < walk.count; ++i_row) {
+    for (long long i_row = 0; i_row < rounds; ++i_row) {
         const long long row = walk.first + i_row * walk.step;
-        if (row >= gate_end) {
+        const bool live = i_row < walk.count;
+        if (live && row >= gate_end) {
             const long long gate_row = row / a.per_gate;
             gate_end = (gate_row + 1) * a.per_gate;
             const float *gate = a.gate != nullptr ? a.gate + gate_row * width : nullptr;
@@ -222,9 +244,9 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             uint4 p = make_uint4(0, 0, 0, 0), q = p;
-            if (vec(k) < vecs) {
-                p = mask_vec<T>(xr[k], first(k), width);
-                q = mask_vec<T>(rr[k], first(k), width);
+            if (live && vec(k) < vecs) {
+                p = mask_vec(xr[k], edge_of(vec(k), vecs), masks);
+                q = mask_vec(rr[k], edge_of(vec(k), vecs), masks);
             }
             F2 t[P], u[P];
             X::widen(p, t);
@@ -241,7 +263,7 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
             for (int i = 0; i < K * P; ++i) sq = fma2(v[i], v[i], sq);
             float s[1] = {total(sq)};
-            row_sum<1, CL>(s, mem, turn, warps, C);
+            row_sum<1, CL>(s, mem, turn, warps, C, lanes);
             r1 = inv_sqrt<T>(fmaf(s[0], inv_n, a.eps));
         }
         const F2 r1s = both(r1);
@@ -253,7 +275,7 @@ __global__ void __launch_bounds__(512)
         }
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (vec(k) < vecs) {
+            if (live && vec(k) < vecs) {
                 F2 t[P];
 #pragma unroll
                 for (int i = 0; i < P; ++i) t[i] = v[k * P + i];
@@ -262,11 +284,11 @@ __global__ void __launch_bounds__(512)
             }
         if (a.pre) {
             float s[1] = {total(sq)};
-            row_sum<1, CL>(s, mem, turn, warps, C);
+            row_sum<1, CL>(s, mem, turn, warps, C, lanes);
             const F2 r2 = both(inv_sqrt<T>(fmaf(s[0], inv_n, a.eps)));
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (vec(k) < vecs) {
+                if (live && vec(k) < vecs) {
                     F2 t[P];
 #pragma unroll
                     for (int i = 0; i < P; ++i)
@@ -279,82 +301,110 @@ __global__ void __launch_bounds__(512)
     if constexpr (CL) cluster_barrier();   // peers may still read this CTA's sums
 }
 
-template <class T, bool CL>
-cudaError_t launch_shift(const BlockArgs &a, RingPlan p, cudaStream_t stream) {
-    constexpr int N = Vec<T>::N, K = 2;
-    int occ = 0;
-    cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        &occ, block_norm_shift_kernel<T, K, CL>, p.workers, 0);
-    if (err != cudaSuccess) return err;
-    p.classes = 1;
-    while (static_cast<long long>(p.classes) * a.width % N != 0) p.classes *= 2;
-    const long long room = static_cast<long long>(sm_count_of_device()) * (occ < 1 ? 1 : occ) / p.cluster;
-    const long long most = (a.rows + p.classes - 1) / p.classes;   // rows of a class
-    long long parts = room / p.classes;
-    parts = parts > most ? most : parts < 1 ? 1 : parts;
-    p.parts = static_cast<int>(parts);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(parts * p.classes * p.cluster));
-    cfg.blockDim = dim3(p.workers);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    if (CL) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = p.cluster;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    return cudaLaunchKernelEx(&cfg, block_norm_shift_kernel<T, K, CL>, a, p);
-}
-
-template <class T, int V, int E, bool CL>
-cudaError_t launch_kernel(const BlockArgs &a, int cluster, cudaStream_t stream) {
-    const int threads = (a.width + cluster * E * 32 - 1) / (cluster * E * 32) * 32;
-    // rows of one warp share a CTA: 8 of them
-    const int programs = threads == 32 && !CL ? 8 : 1;
-    const long long grid = (a.rows + programs - 1) / programs * cluster;
+// Launch of `grid` CTAs of `threads`, in clusters.
+template <class Kernel, class... Args>
+cudaError_t launch_grid(Kernel kernel, long long grid, int threads, int cluster,
+                        cudaStream_t stream, Args... args) {
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(threads * programs);
+    cfg.blockDim = dim3(threads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    if (CL) {
+    if (cluster > 1) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = cluster;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, V, E / V, CL>, a, threads / 32, cluster);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// One CTA a row up to 512 threads, then a cluster of up to 8, then (FP32 and
-// single elements above 65536 columns) 32 columns a thread.
+// Threads of a row that is `groups` groups of columns, each thread taking at
+// most `each`: a power of two up to a warp, then whole warps.
+int threads_of(int groups, int each) {
+    const int n = (groups + each - 1) / each;
+    int w = 1;
+    while (w < n && w < 32) w *= 2;
+    return n <= 32 ? w : (n + 31) / 32 * 32;
+}
+// Threads of a CTA of programs of w threads: programs of at most a warp share
+// one.
+int cta_threads(int w) { return w <= 32 ? 256 : w; }
+
+template <class T, bool CL, int MAXT, int MINB>
+cudaError_t launch_shift(const BlockArgs &a, RingPlan p, cudaStream_t stream) {
+    constexpr int N = Vec<T>::N, K = 2;
+    const auto kernel = block_norm_shift_kernel<T, K, CL, MAXT, MINB>;
+    const int threads = CL ? p.workers : cta_threads(p.workers);
+    int occ = 0;
+    cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, 0);
+    if (err != cudaSuccess) return err;
+    p.classes = 1;
+    while (static_cast<long long>(p.classes) * a.width % N != 0) p.classes *= 2;
+    const int programs = threads / p.workers;   // of a CTA
+    const long long room =
+        static_cast<long long>(sm_count_of_device()) * (occ < 1 ? 1 : occ) / p.cluster * programs;
+    // parts of a class: as many as there is room for, but not more than rows
+    long long parts = room / p.classes;
+    const long long most = (a.rows + p.classes - 1) / p.classes;
+    parts = parts > most ? most : parts < 1 ? 1 : parts;
+    while (parts * p.classes % programs != 0) ++parts;   // whole CTAs
+    p.parts = static_cast<int>(parts);
+    return launch_grid(kernel, parts * p.classes / programs * p.cluster, threads, p.cluster, stream,
+                       a, p);
+}
+
+template <class T, int V, int E, bool CL, int MAXT, int MINB>
+cudaError_t launch_kernel(const BlockArgs &a, int cluster, cudaStream_t stream) {
+    const int groups = (a.width + V - 1) / V;
+    const int w = CL ? (groups + cluster * (E / V) * 32 - 1) / (cluster * (E / V) * 32) * 32
+                     : threads_of(groups, E / V);
+    const int threads = CL ? w : cta_threads(w), programs = threads / w;
+    return launch_grid(block_norm_kernel<T, V, E / V, CL, MAXT, MINB>,
+                       (a.rows + programs - 1) / programs * cluster, threads, cluster, stream, a, w,
+                       cluster);
+}
+
+// 32 two-byte or 16 FP32 columns a thread, up to 512 threads a row, then a
+// cluster of up to 8 CTAs, then 32 columns of either.  (16 two-byte columns a
+// thread from 8192 columns on, in a cluster of two from 16384 on, took 177 us
+// where 32 take 126, at 4096 x 16384.)
 template <class T, int V>
 cudaError_t launch_rows(const BlockArgs &a, cudaStream_t stream) {
     constexpr int E = V == 8 ? 32 : 16;
-    if (a.width <= 512 * E) return launch_kernel<T, V, E, false>(a, 1, stream);
+    constexpr int MINB = V == 8 ? 1 : 2;   // 64 registers for 16 columns
+    // 96 for 32, as long as that leaves room for two CTAs or more (with 128,
+    // 16384 x 4096 BF16 took 107 us instead of 88)
+    if constexpr (V == 8)
+        if (a.width <= 320 * E) return launch_kernel<T, V, E, false, 320, 2>(a, 1, stream);
+    if (a.width <= 512 * E) return launch_kernel<T, V, E, false, 512, MINB>(a, 1, stream);
     for (int c = 2; c <= 8; c *= 2)
-        if (a.width <= 512 * E * c) return launch_kernel<T, V, E, true>(a, c, stream);
-    return launch_kernel<T, V, 32, true>(a, 8, stream);
+        if (a.width <= 512 * E * c) return launch_kernel<T, V, E, true, 512, MINB>(a, c, stream);
+    return launch_kernel<T, V, 32, true, 512, 1>(a, 8, stream);
 }
 
 template <class T>
 cudaError_t launch_typed(const BlockArgs &a, BlockAccess access, cudaStream_t stream) {
     constexpr int N = Vec<T>::N;
     if (access == ACCESS_VECTORS) return launch_rows<T, N>(a, stream);
-    if (access == ACCESS_SHIFTED) {
+    // (FP32 rows off the grid go by single elements: a warp's 128 bytes are
+    // one line or two, as with vectors; 5000 x 1537 took 27 us, by shifted
+    // vectors 41 us)
+    if constexpr (N == 8) {
         const int vecs = (a.width + N - 1 + N - 1) / N;   // wherever a row starts
-        for (int c = 1; c <= 8; c *= 2)
-            if (vecs <= 2 * 512 * c) {
-                RingPlan p = {};
-                p.cluster = c;
-                p.workers = ((vecs + c - 1) / c + 63) / 64 * 32;
-                return c == 1 ? launch_shift<T, false>(a, p, stream)
-                              : launch_shift<T, true>(a, p, stream);
-            }
+        if (access == ACCESS_SHIFTED && vecs <= 8 * 512 * 2) {
+            RingPlan p = {};
+            p.cluster = 1;
+            p.workers = threads_of(vecs, 2);
+            if (p.workers <= 256) return launch_shift<T, false, 256, 2>(a, p, stream);
+            if (p.workers <= 320) return launch_shift<T, false, 320, 2>(a, p, stream);
+            if (p.workers <= 512) return launch_shift<T, false, 512, 1>(a, p, stream);
+            while (vecs > 2 * 512 * p.cluster) p.cluster *= 2;
+            p.workers = ((vecs + p.cluster - 1) / p.cluster + 63) / 64 * 32;
+            return launch_shift<T, true, 512, 1>(a, p, stream);
+        }
     }
     return launch_rows<T, 1>(a, stream);
 }

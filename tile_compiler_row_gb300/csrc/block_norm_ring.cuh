@@ -67,8 +67,8 @@ __device__ __forceinline__ uint4 shared_vec(uint32_t at) {
     return v;
 }
 
-template <class T, int K, bool SHIFT, bool CL>
-__global__ void __launch_bounds__(512)
+template <class T, int K, bool SHIFT, bool CL, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB)
     block_norm_ring_kernel(const BlockArgs a, const RingPlan plan) {
     using X = Vec<T>;
     constexpr int N = X::N, P = X::P;   // elements, pairs of a vector
@@ -76,17 +76,24 @@ __global__ void __launch_bounds__(512)
     __shared__ __align__(16) float warp_part[2][6][16];
     __shared__ __align__(16) float cta_part[2][8][8];
     __shared__ __align__(8) uint64_t full[kRingMost], peer[2];
+    __shared__ EdgeMasks masks;
     __shared__ int abort_flag;
     const int W = plan.workers, warps = W >> 5, slots = plan.slots;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = CL ? plan.cluster : 1;
     const int rank = CL ? static_cast<int>(cluster_rank()) : 0;
     volatile int *aborted = &abort_flag;
+    const long long units = gridDim.x / C, unit = blockIdx.x / C;
+    const RowWalk walk = row_walk(a.rows, a.per_gate, plan, unit, units);
+    const int width = a.width;
+    // elements of the rows' first block that lie before the row
+    const int shift = SHIFT ? static_cast<int>((walk.first * width) & (N - 1)) : 0;
 
     // unused warps' and CTAs' partial sums stay 0
     for (int i = tid; i < 2 * 6 * 16; i += W) (&warp_part[0][0][0])[i] = 0.0f;
     for (int i = tid; i < 2 * 8 * 8; i += W) (&cta_part[0][0][0])[i] = 0.0f;
     if (tid == 0) {
+        if (SHIFT) edge_masks<T>(masks, shift, width);
         abort_flag = 0;
         for (int s = 0; s < slots; ++s) bar_init(smem_u32(&full[s]), 1);
         bar_init(smem_u32(&peer[0]), 1);
@@ -97,14 +104,10 @@ __global__ void __launch_bounds__(512)
     if constexpr (CL) cluster_barrier();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const long long units = gridDim.x / C, unit = blockIdx.x / C;
-    const RowWalk walk = row_walk(a.rows, a.per_gate, plan, unit, units);
-    const int width = a.width;
-    // elements of the rows' first block that lie before the row
-    const int shift = SHIFT ? static_cast<int>((walk.first * width) & (N - 1)) : 0;
     // this CTA's vectors of a row: [v0, v0 + nv) of those that hold it
     const int v0 = rank * W * K;
-    const int nv = min((width + shift + N - 1) / N - v0, W * K);
+    const int vecs = (width + shift + N - 1) / N;
+    const int nv = min(vecs - v0, W * K);
     const bool has_x = a.post || a.gate != nullptr, has_dh = a.dhidden != nullptr;
     const uint32_t ring0 = smem_u32(ring);
     // element of the matrix where this CTA's part of a row begins (its block)
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(512)
             uint4 q = make_uint4(0, 0, 0, 0);
             if (use) {
                 q = shared_vec(at + t * plan.pitch + k * W * 16);
-                if (SHIFT) q = mask_vec<T>(q, first(k), width);
+                if (SHIFT) q = mask_vec(q, edge_of(v0 + k * W + tid, vecs), masks);
             }
             X::widen(q, v);
         };
