@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "launch.h"
 #include "row_kernel.cuh"
 
@@ -330,6 +332,39 @@ __device__ __forceinline__ RowWalk row_walk(long long rows, long long group, con
     w.count = n * (part + 1) / p.parts - n * part / p.parts;
     w.step = p.classes;
     return w;
+}
+
+// CTAs of a kernel to an SM of the current device for a launch shape, its
+// shared memory limit raised to the shape's.  The last answer for a kernel is
+// kept per device: calls of one shape follow one another, and the two CUDA
+// calls take longer than a launch.
+struct OccupancyCache {
+    std::atomic<unsigned long long> last[kMaxDevices];   // threads, smem, CTAs
+};
+
+template <class Kernel>
+cudaError_t occupancy(Kernel kernel, OccupancyCache &cache, int threads, int smem, int *per_sm) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    const unsigned long long key = (static_cast<unsigned long long>(threads) << 32 |
+                                    static_cast<unsigned int>(smem)) << 8;
+    const unsigned long long known = cache.last[dev].load(std::memory_order_acquire);
+    if (known >> 8 == key >> 8 && (known & 0xff) != 0) {
+        *per_sm = static_cast<int>(known & 0xff);
+        return cudaSuccess;
+    }
+    // the limit only ever grows, so that a call of another thread that is
+    // between this and its launch keeps what it needs
+    if (smem > 40 << 10)   // with the static part above 48 KiB
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 << 10);
+    if (err != cudaSuccess) return err;
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kernel, threads, smem);
+    if (err != cudaSuccess) return err;
+    if (*per_sm < 1) *per_sm = 1;
+    cache.last[dev].store(key | static_cast<unsigned long long>(*per_sm), std::memory_order_release);
+    return cudaSuccess;
 }
 
 // One block-norm call (forward and backward); see include/tile_rows.h.

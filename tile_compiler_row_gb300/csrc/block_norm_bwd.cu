@@ -294,19 +294,6 @@ RingPlan ring_plan(int width) {
     return p;
 }
 
-// Attributes of a kernel on the current device: its shared memory limit
-// raised once, and its CTAs to an SM for a launch shape.
-template <class Kernel>
-cudaError_t occupancy(Kernel kernel, int threads, int smem, int *per_sm) {
-    cudaError_t err = cudaSuccess;
-    if (smem > 40 << 10)   // with the static part above 48 KiB
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err != cudaSuccess) return err;
-    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kernel, threads, smem);
-    if (err == cudaSuccess && *per_sm < 1) *per_sm = 1;
-    return err;
-}
-
 template <class Kernel, class Plan>
 cudaError_t launch_programs(Kernel kernel, const BlockArgs &a, const Plan &plan, long long units,
                             int threads, int cluster, int smem, cudaStream_t stream) {
@@ -332,11 +319,12 @@ struct Programs {
     int per_gate;   // programs of a gate row, 0: contiguous ranges of rows
 };
 
-template <class Kernel>
-cudaError_t launch_ring(Kernel kernel, const BlockArgs &a, RingPlan p, cudaStream_t stream,
-                        Programs *out) {
+template <class T, bool SHIFT, bool CL, int MAXT, int MINB>
+cudaError_t launch_ring(const BlockArgs &a, RingPlan p, cudaStream_t stream, Programs *out) {
+    static OccupancyCache cache;
+    const auto kernel = block_norm_ring_kernel<T, kRingVecs, SHIFT, CL, MAXT, MINB>;
     int per_sm = 0;
-    const cudaError_t err = occupancy(kernel, p.workers, p.smem, &per_sm);
+    const cudaError_t err = occupancy(kernel, cache, p.workers, p.smem, &per_sm);
     if (err != cudaSuccess) return err;
     const long long room = static_cast<long long>(sm_count_of_device()) * per_sm / p.cluster;
     if (p.classes == 1) {
@@ -353,26 +341,25 @@ cudaError_t launch_ring(Kernel kernel, const BlockArgs &a, RingPlan p, cudaStrea
 template <class T, bool SHIFT>
 cudaError_t launch_ring_typed(const BlockArgs &a, const RingPlan &p, cudaStream_t stream,
                               Programs *out) {
-    constexpr int K = kRingVecs;
+    const bool one = p.cluster == 1;
     if (p.workers <= 256)
-        return p.cluster == 1
-                   ? launch_ring(block_norm_ring_kernel<T, K, SHIFT, false, 256, 2>, a, p, stream, out)
-                   : launch_ring(block_norm_ring_kernel<T, K, SHIFT, true, 256, 2>, a, p, stream, out);
+        return one ? launch_ring<T, SHIFT, false, 256, 2>(a, p, stream, out)
+                   : launch_ring<T, SHIFT, true, 256, 2>(a, p, stream, out);
     if (p.workers <= 320)
-        return p.cluster == 1
-                   ? launch_ring(block_norm_ring_kernel<T, K, SHIFT, false, 320, 2>, a, p, stream, out)
-                   : launch_ring(block_norm_ring_kernel<T, K, SHIFT, true, 320, 2>, a, p, stream, out);
-    return p.cluster == 1
-               ? launch_ring(block_norm_ring_kernel<T, K, SHIFT, false, 512, 1>, a, p, stream, out)
-               : launch_ring(block_norm_ring_kernel<T, K, SHIFT, true, 512, 1>, a, p, stream, out);
+        return one ? launch_ring<T, SHIFT, false, 320, 2>(a, p, stream, out)
+                   : launch_ring<T, SHIFT, true, 320, 2>(a, p, stream, out);
+    return one ? launch_ring<T, SHIFT, false, 512, 1>(a, p, stream, out)
+               : launch_ring<T, SHIFT, true, 512, 1>(a, p, stream, out);
 }
 
 template <class T, int V, int E, bool CL>
 cudaError_t launch_registers(const BlockArgs &a, cudaStream_t stream, Programs *out) {
     const int cluster = CL ? 8 : 1;
     const int threads = (a.width + cluster * E * 32 - 1) / (cluster * E * 32) * 32;
+    static OccupancyCache cache;
     int per_sm = 0;
-    const cudaError_t err = occupancy(block_norm_backward_kernel<T, V, E / V, CL>, threads, 0, &per_sm);
+    const cudaError_t err =
+        occupancy(block_norm_backward_kernel<T, V, E / V, CL>, cache, threads, 0, &per_sm);
     if (err != cudaSuccess) return err;
     const long long room = static_cast<long long>(sm_count_of_device()) * per_sm / cluster;
     *out = {units_of(a.rows, room), 0};

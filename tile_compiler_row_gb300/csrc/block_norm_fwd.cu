@@ -338,14 +338,15 @@ cudaError_t launch_shift(const BlockArgs &a, RingPlan p, cudaStream_t stream) {
     constexpr int N = Vec<T>::N, K = 2;
     const auto kernel = block_norm_shift_kernel<T, K, CL, MAXT, MINB>;
     const int threads = CL ? p.workers : cta_threads(p.workers);
+    static OccupancyCache cache;
     int occ = 0;
-    cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, 0);
+    const cudaError_t err = occupancy(kernel, cache, threads, 0, &occ);
     if (err != cudaSuccess) return err;
     p.classes = 1;
     while (static_cast<long long>(p.classes) * a.width % N != 0) p.classes *= 2;
     const int programs = threads / p.workers;   // of a CTA
     const long long room =
-        static_cast<long long>(sm_count_of_device()) * (occ < 1 ? 1 : occ) / p.cluster * programs;
+        static_cast<long long>(sm_count_of_device()) * occ / p.cluster * programs;
     // parts of a class: as many as there is room for, but not more than rows
     long long parts = room / p.classes;
     const long long most = (a.rows + p.classes - 1) / p.classes;
