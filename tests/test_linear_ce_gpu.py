@@ -100,7 +100,8 @@ def check_gradients(x, weight, target, lse, dloss, dx, dweight):
 
 # one token, one column, one class; around the tiles of 128 rows, 64 and 256
 # columns; odd widths and vocabularies; vocabularies split among CTAs
-SHAPES = [(1, 1, 1), (1, 8, 2), (2, 3, 5), (1, 64, 1000), (5, 72, 257), (17, 100, 256),
+# (few rows of many columns, many rows and entries of few)
+SHAPES = [(3, 9001, 700), (70, 16384, 300), (17000, 64, 520), (2, 64, 300001), (1, 1, 1), (1, 8, 2), (2, 3, 5), (1, 64, 1000), (5, 72, 257), (17, 100, 256),
           (127, 64, 255), (128, 128, 512), (129, 136, 511), (130, 65, 777), (256, 256, 300),
           (300, 520, 1025), (3, 2048, 9000), (64, 333, 20011), (1000, 96, 3001), (257, 1537, 640)]
 

@@ -166,7 +166,7 @@ __device__ __forceinline__ Extents extents(const Job &j, const CeState *state) {
 template <class F>
 __device__ __forceinline__ void store_tile16(const CUtensorMap *map, uint32_t tmem, uint32_t buf,
                                              int lane, int bf16, int row0, int col0, int from,
-                                             int end, bool inside, F value) {
+                                             int end, F value) {
     for (int c = from; c < end; c += 64) {
         const uint32_t to = buf + lane * 128;
         if (lane == 0) store_wait_read<0>();   // the buffer's last store has read it
@@ -191,7 +191,7 @@ __device__ __forceinline__ void store_tile16(const CUtensorMap *map, uint32_t tm
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-            if (inside) tma_store(map, col0 + c, row0, buf);
+            tma_store(map, col0 + c, row0, buf);
             store_commit();
         }
     }
@@ -221,26 +221,24 @@ __device__ __forceinline__ void store_rows16(unsigned short *out, long long ld, 
             }
         }
         __syncwarp();
+        // without branches, so that the rows' shared-memory reads and shuffles
+        // run side by side (row after row, 18 x 3356 x 68330 took 539 us)
         const int n = min(64, end - c), count = min(32, rows - row0);
+        unsigned short *to = out + static_cast<long long>(row0) * ld + col0 + c;
 #pragma unroll 8
-        for (int r = 0; r < count; ++r) {
+        for (int r = 0; r < 32; ++r) {
             unsigned int w;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(buf + r * 128 + 4 * (lane ^ r))
-                         : "memory");
-            unsigned short *to = out + static_cast<long long>(row0 + r) * ld + col0 + c;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(buf + r * 128 + 4 * (lane ^ r)));
             const unsigned int next = __shfl_down_sync(0xffffffffu, w, 1);
-            if (reinterpret_cast<uintptr_t>(to) & 2) {   // words of elements 2 l + 1, 2 l + 2
-                if (lane == 0) to[0] = static_cast<unsigned short>(w);
-                if (2 * lane + 2 < n && lane < 31)
-                    *reinterpret_cast<unsigned int *>(to + 2 * lane + 1) = __funnelshift_r(w, next, 16);
-                else if (2 * lane + 1 < n)
-                    to[2 * lane + 1] = static_cast<unsigned short>(w >> 16);
-            } else {
-                if (2 * lane + 1 < n)
-                    *reinterpret_cast<unsigned int *>(to + 2 * lane) = w;
-                else if (2 * lane < n)
-                    to[2 * lane] = static_cast<unsigned short>(w);
-            }
+            unsigned short *at = to + r * ld;
+            // on an odd element the words are elements 2 l + 1, 2 l + 2
+            const int odd = (reinterpret_cast<uintptr_t>(at) >> 1) & 1;
+            const int e = 2 * lane + odd;
+            const unsigned int word = odd ? __funnelshift_r(w, next, 16) : w;
+            if (r < count && e + 1 < n) *reinterpret_cast<unsigned int *>(at + e) = word;
+            // the elements that no word holds: the first, and the last
+            if (r < count && odd && lane == 0) at[0] = static_cast<unsigned short>(w);
+            if (r < count && e + 1 == n) at[e] = static_cast<unsigned short>(word);
         }
     }
 }
@@ -459,7 +457,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             // no product was made: zero
             const bool none = k_begin(t, w.split) == k_begin(t, w.split + 1);
             const int epi = second ? EPI1 : EPI0;
-            if (epi == EPI_LSE) {
+            // rows of this warp that are looked at: those that are there, and
+            // for g those up to the next 64, which dW's reduction reads
+            if (row0 >= (epi == EPI_GRAD ? (e.m + BK - 1) / BK * BK : e.m)) {
+            } else if (epi == EPI_LSE) {
                 float m = -INFINITY, s = 0.0f;
                 for (int c = from; c < end; c += 32) {
                     float v[32];
@@ -488,9 +489,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 const int want = in ? g.ptarget[row] - g.n0 - col0 : -1;
                 const float lse2 = in ? g.plse2[row] : 0.0f, dl = in ? g.pdloss[row] : 0.0f;
                 const int limit = in ? e.n - col0 : 0;
-                // rows up to the next 64 are written: dW's reduction reads them
                 store_tile16(&maps.out, d, buf, lane, g.bf16, row0, col0, from, to,
-                             row0 < (e.m + BK - 1) / BK * BK,
                              [&](float v, int c) {
                                  const float p = ex2(fmaf(v, kLog2e, -lse2));
                                  return c < limit ? (want == c ? p - 1.0f : p) * dl : 0.0f;
@@ -498,7 +497,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             } else if (epi == EPI_DWEIGHT) {
                 const float f = none ? 0.0f : g.state->unscale;
                 if (job.store) {
-                    store_tile16(&maps.out, d, buf, lane, g.bf16, row0, col0, from, end, row0 < e.m,
+                    store_tile16(&maps.out, d, buf, lane, g.bf16, row0, col0, from, end,
                                  [&](float v, int) { return none ? 0.0f : v * f; });
                 } else {
                     store_rows16(static_cast<unsigned short *>(job.out), job.ld, d, buf, lane, g.bf16,
@@ -552,10 +551,10 @@ struct PackArgs {
     int rows, width, vocab, ld;
     int scaled;                         // FP16: gradients by 2^15
     int row_ctas;                       // CTAs that pack x; the others copy the weight
-    int place_rows;                     // 0: x is copied as it lies
+    int cta_rows;                       // rows of a CTA that packs x
     unsigned short *px, *pw;
     CeState *state;
-    int *place, *row_of, *ptarget;
+    int *place, *ptarget;
     float *plse2, *pdloss;
     unsigned int *status;
 };
@@ -564,22 +563,25 @@ __device__ __forceinline__ bool counts(long long t, long long ignore, int vocab,
     return t != ignore && t >= 0 && t < vocab && dl != 0.0f;
 }
 
-// One warp copies a row of `width` two-byte elements, from any 2-byte
+// `lanes` neighbours (8, 16 or 32) copy a row of `width` two-byte elements, from any 2-byte
 // alignment, to a row of `ld` (a multiple of 8; 16-byte aligned), padded with
 // zeros; `from` NULL: zeros.  Two aligned source blocks make one of the
 // target's; the second is the next lane's first.
 __device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned short *to, int width,
-                                           int ld, int lane) {
+                                           int ld, int lanes) {
+    const int lane = threadIdx.x & (lanes - 1);
+    // the next lane of this row, the first after the last
+    const int beside = (threadIdx.x & 31 & ~(lanes - 1)) | ((lane + 1) & (lanes - 1));
     const int vecs = ld / 8;
     uint4 *out = reinterpret_cast<uint4 *>(to);
     if (from == nullptr) {
-        for (int i = lane; i < vecs; i += 32) out[i] = make_uint4(0, 0, 0, 0);
+        for (int i = lane; i < vecs; i += lanes) out[i] = make_uint4(0, 0, 0, 0);
         return;
     }
     if (width % 8 == 0 && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
         const uint4 *in = reinterpret_cast<const uint4 *>(from);
 #pragma unroll 4
-        for (int i = lane; i < vecs; i += 32)
+        for (int i = lane; i < vecs; i += lanes)
             out[i] = i < width / 8 ? __ldg(in + i) : make_uint4(0, 0, 0, 0);
         return;
     }
@@ -603,20 +605,20 @@ __device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned 
         return make_uint4(w[0], w[1], w[2], w[3]);
     };
     const int words = skew >> 2, bits = (skew & 3) * 8;
-    for (int i0 = 0; i0 < vecs; i0 += 128) {
+    for (int i0 = 0; i0 < vecs; i0 += 4 * lanes) {
         uint4 a[5];   // the loads of four rounds at once
 #pragma unroll
-        for (int u = 0; u < 4; ++u) a[u] = block(i0 + u * 32 + lane);
-        // the block after this round's last, for lane 31
-        a[4] = block(i0 + 128);
+        for (int u = 0; u < 4; ++u) a[u] = block(i0 + u * lanes + lane);
+        // the block after this round's last, for the last lane
+        a[4] = block(i0 + 4 * lanes);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             // the next lane's block; for the last lane the first of the next round
             uint4 b;
-            b.x = __shfl_sync(0xffffffffu, lane == 0 ? a[u + 1].x : a[u].x, (lane + 1) & 31);
-            b.y = __shfl_sync(0xffffffffu, lane == 0 ? a[u + 1].y : a[u].y, (lane + 1) & 31);
-            b.z = __shfl_sync(0xffffffffu, lane == 0 ? a[u + 1].z : a[u].z, (lane + 1) & 31);
-            b.w = __shfl_sync(0xffffffffu, lane == 0 ? a[u + 1].w : a[u].w, (lane + 1) & 31);
+            b.x = __shfl_sync(0xffffffffu, lane == 0 ? a[u + 1].x : a[u].x, beside);
+            b.y = __shfl_sync(0xffffffffu, lane == 0 ? a[u + 1].y : a[u].y, beside);
+            b.z = __shfl_sync(0xffffffffu, lane == 0 ? a[u + 1].z : a[u].z, beside);
+            b.w = __shfl_sync(0xffffffffu, lane == 0 ? a[u + 1].w : a[u].w, beside);
             // bytes [skew, skew + 16) of a, b: words moved by `words`, in two steps
             unsigned int w[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b.x, b.y, b.z, b.w};
             if (words & 1)
@@ -625,7 +627,7 @@ __device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned 
             if (words & 2)
 #pragma unroll
                 for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
-            const int i = i0 + u * 32 + lane;
+            const int i = i0 + u * lanes + lane;
             if (i < vecs)
                 out[i] = make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
                                     __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
@@ -634,9 +636,9 @@ __device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned 
 }
 
 // The rows that count, packed to the front of px in their order (place[i] =
-// position of row i or -1; row_of, target, lse and dloss by position), rows
+// position of row i or -1; target, lse and dloss by position), rows
 // behind them zero; and the weight's rows copied to whole vectors.  A CTA
-// packs 8 rows and counts the rows before them for itself (the targets of a
+// packs a few rows and counts the rows before them for itself (the targets of a
 // call are small and in L2), so there is no pass before it.
 //
 // dloss is held over its largest magnitude: the equal weights of a mean
@@ -646,91 +648,92 @@ __device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned 
 // it, 1.8e-3 without; the output's own rounding is 1.7e-3).  FP16 gradients
 // are scaled by 2^15 too: |p - onehot| <= 1, so nothing overflows, and what
 // underflows is below 2^-40 of the largest.
-constexpr int PACK_ROWS = 8;   // at most a warp
-
 __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
-    __shared__ int warp_before[8], warp_total[8], row_at[PACK_ROWS];
+    __shared__ int warp_before[8], warp_total[8], row_at[32];
     __shared__ float warp_top[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     dependency_launch();
     if (static_cast<int>(blockIdx.x) >= a.row_ctas) {
         const int ctas = gridDim.x - a.row_ctas, cta = blockIdx.x - a.row_ctas;
-        for (long long r = static_cast<long long>(cta) * 8 + warp; r < a.vocab; r += ctas * 8ll)
-            copy_row16(a.weight + r * a.width, a.pw + r * a.ld, a.width, a.ld, lane);
+        // short rows two or four to a warp, so that its loads fill a round
+        const int lanes = a.ld > 512 ? 32 : a.ld > 256 ? 16 : 8, each = 32 / lanes;
+        for (long long r0 = (static_cast<long long>(cta) * 8 + warp) * each; r0 < a.vocab;
+             r0 += ctas * 8ll * each) {
+            // (behind the last row: that row once more)
+            const long long r = min(static_cast<long long>(a.vocab) - 1, r0 + lane / lanes);
+            copy_row16(a.weight + r * a.width, a.pw + r * a.ld, a.width, a.ld, lanes);
+        }
         return;
     }
-    const int r0 = blockIdx.x * PACK_ROWS;
-    int valid = a.rows;
-    if (a.place_rows) {
-        int before = 0, all = 0;
-        float top = 0.0f;
+    const int r0 = blockIdx.x * a.cta_rows, r1 = min(a.rows, r0 + a.cta_rows);
+    int before = 0, valid = 0;   // packed rows before this CTA's, and all of them
+    float top = 0.0f;
 #pragma unroll 4
-        for (int i = tid; i < a.rows; i += 256) {
-            const long long t = a.target[i];
-            const float dl = a.dloss != nullptr ? a.dloss[i] : 1.0f;
-            const bool in = counts(t, a.ignore, a.vocab, dl);
-            all += in;
-            before += in && i < r0;
-            if (in && isfinite(dl)) top = fmaxf(top, fabsf(dl));
-        }
-        for (int d = 16; d > 0; d >>= 1) {
-            before += __shfl_xor_sync(0xffffffffu, before, d);
-            all += __shfl_xor_sync(0xffffffffu, all, d);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        }
-        if (lane == 0) {
-            warp_before[warp] = before;
-            warp_total[warp] = all;
-            warp_top[warp] = top;
-        }
-        __syncthreads();
-        before = all = 0;
-        top = 0.0f;
-        for (int i = 0; i < 8; ++i) {
-            before += warp_before[i];
-            all += warp_total[i];
-            top = fmaxf(top, warp_top[i]);
-        }
-        valid = all;
-        // 32768 / top and top / 32768 are finite and not 0 for any normal top
-        top = fminf(fmaxf(top, 1e-30f), 1e30f);
-        const float full = a.scaled ? 32768.0f : 1.0f;
+    for (int i = tid; i < a.rows; i += 256) {
+        const long long t = a.target[i];
+        const float dl = a.dloss != nullptr ? a.dloss[i] : 1.0f;
+        const bool in = counts(t, a.ignore, a.vocab, dl);
+        valid += in;
+        before += in && i < r0;
+        if (in && isfinite(dl)) top = fmaxf(top, fabsf(dl));
+    }
+    for (int d = 16; d > 0; d >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, d);
+        valid += __shfl_xor_sync(0xffffffffu, valid, d);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    }
+    if (lane == 0) {
+        warp_before[warp] = before;
+        warp_total[warp] = valid;
+        warp_top[warp] = top;
+    }
+    __syncthreads();
+    before = valid = 0;
+    top = 0.0f;
+    for (int i = 0; i < 8; ++i) {
+        before += warp_before[i];
+        valid += warp_total[i];
+        top = fmaxf(top, warp_top[i]);
+    }
+    // 32768 / top and top / 32768 are finite and not 0 for any normal top
+    top = fminf(fmaxf(top, 1e-30f), 1e30f);
+    const float full = a.scaled ? 32768.0f : 1.0f;
+    if (blockIdx.x == 0 && tid == 0) {
+        a.state->valid = valid;
+        a.state->unscale = top / full;
+    }
+    for (int c = r0; c < r1; c += 32) {   // up to 32 rows at a time, a lane of warp 0 each
         if (warp == 0) {
-            const int i = r0 + lane;
-            const bool mine = lane < PACK_ROWS && i < a.rows;
+            const int i = c + lane;
+            const bool mine = i < r1;
             const long long t = mine ? a.target[i] : a.ignore;
             const float dl = mine && a.dloss != nullptr ? a.dloss[i] : 1.0f;
             const bool in = mine && counts(t, a.ignore, a.vocab, dl);
             const unsigned int mask = __ballot_sync(0xffffffffu, in);
             const int at = before + __popc(mask & ((1u << lane) - 1u));
-            if (lane < PACK_ROWS) row_at[lane] = in ? at : -1;
+            before += __popc(mask);
+            row_at[lane] = in ? at : -1;
             if (mine) {
                 a.place[i] = in ? at : -1;
                 if (t != a.ignore && (t < 0 || t >= a.vocab)) atomicOr(a.status, CE_BAD_TARGET);
             }
-            if (in) {
-                a.row_of[at] = i;
-                if (a.dloss != nullptr) {
-                    a.ptarget[at] = static_cast<int>(t);
-                    a.plse2[at] = a.lse[i] * kLog2e;
-                    a.pdloss[at] = full * (dl / top);
-                }
-            }
-            if (blockIdx.x == 0 && lane == 0) {
-                a.state->valid = all;
-                a.state->unscale = top / full;
+            if (in && a.dloss != nullptr) {
+                a.ptarget[at] = static_cast<int>(t);
+                a.plse2[at] = a.lse[i] * kLog2e;
+                a.pdloss[at] = full * (dl / top);
             }
         }
         __syncthreads();
-    }
-    for (int q = warp; q < PACK_ROWS; q += 8) {
-        const int i = r0 + q;
-        if (i >= a.rows) break;
-        const int at = a.place_rows ? row_at[q] : i;
-        if (at >= 0)
-            copy_row16(a.x + static_cast<long long>(i) * a.width,
-                       a.px + static_cast<long long>(at) * a.ld, a.width, a.ld, lane);
-        if (i >= valid) copy_row16(nullptr, a.px + static_cast<long long>(i) * a.ld, 0, a.ld, lane);
+        for (int q = warp; q < 32; q += 8) {
+            const int i = c + q, at = row_at[q];
+            if (i >= r1) break;
+            if (at >= 0)
+                copy_row16(a.x + static_cast<long long>(i) * a.width,
+                           a.px + static_cast<long long>(at) * a.ld, a.width, a.ld, 32);
+            if (i >= valid)
+                copy_row16(nullptr, a.px + static_cast<long long>(i) * a.ld, 0, a.ld, 32);
+        }
+        __syncthreads();
     }
 }
 
@@ -773,7 +776,8 @@ __device__ __forceinline__ float warp_dot(const unsigned short *x, const unsigne
 
 struct JoinArgs {
     const float2 *partial;
-    const unsigned short *x, *weight;
+    const unsigned short *x, *weight;   // as they were multiplied
+    long long x_ld, weight_ld;
     const long long *target;
     const int *place;   // where a row was packed, or NULL
     long long ignore;
@@ -787,11 +791,13 @@ template <class T>
 __global__ void __launch_bounds__(128) join_lse_kernel(const JoinArgs a) {
     const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= a.rows) return;
-    // the target's logit needs nothing of the product before
+    // The target's logit needs nothing of the product before, only what that
+    // waited for before it let this kernel start.
     const long long t = a.target[row];
     const bool in = t >= 0 && t < a.vocab;
-    const float l = in && t != a.ignore ? warp_dot<T>(a.x + static_cast<long long>(row) * a.width,
-                                                      a.weight + t * a.width, a.width, lane)
+    const int at = a.place != nullptr ? a.place[row] : row;
+    const float l = in && t != a.ignore ? warp_dot<T>(a.x + at * a.x_ld, a.weight + t * a.weight_ld,
+                                                      a.width, lane)
                                         : NAN;
     dependency_wait();
     if (t == a.ignore) {
@@ -806,7 +812,6 @@ __global__ void __launch_bounds__(128) join_lse_kernel(const JoinArgs a) {
         }
         return;
     }
-    const int at = a.place != nullptr ? a.place[row] : row;
     const float2 *p = a.partial + static_cast<long long>(at) * a.partials;
     float m = -INFINITY;
     for (int i = lane; i < a.partials; i += 32) m = fmaxf(m, p[i].x);
@@ -985,7 +990,7 @@ bool forward_packs(int rows, int width, int vocab) {
 
 struct ForwardSpace {
     CeState *state;
-    int *place, *row_of;
+    int *place;
     unsigned short *x, *w;
     float2 *partial;
     size_t bytes;
@@ -1019,7 +1024,6 @@ ForwardSpace forward_space(void *ws, int rows, int width, int vocab) {
     if (forward_packs(rows, width, vocab)) {
         s.state = c.take<CeState>(1);
         s.place = c.take<int>(rows);
-        s.row_of = c.take<int>(rows);
         s.x = c.take<unsigned short>(rows * ld);
         if (odd_rows(width)) s.w = c.take<unsigned short>(vocab * ld);
     }
@@ -1049,7 +1053,7 @@ int splits_of(int rows, int width, int vocab) {
 
 struct BackwardSpace {
     CeState *state;
-    int *place, *row_of, *ptarget;
+    int *place, *ptarget;
     float *plse2, *pdloss;
     int pieces;
     unsigned short *x, *w, *grad;
@@ -1064,7 +1068,6 @@ BackwardSpace backward_space(void *ws, int rows, int width, int vocab) {
     s.pieces = static_cast<int>((vocab + piece - 1) / piece);
     s.state = c.take<CeState>(1);
     s.place = c.take<int>(rows);
-    s.row_of = c.take<int>(rows);
     s.ptarget = c.take<int>(rows);
     s.plse2 = c.take<float>(rows);
     s.pdloss = c.take<float>(rows);
@@ -1078,7 +1081,10 @@ BackwardSpace backward_space(void *ws, int rows, int width, int vocab) {
 
 // The pack kernel's CTAs for x, and with a weight to copy two waves more.
 cudaError_t launch_pack(PackArgs p, cudaStream_t stream) {
-    p.row_ctas = (p.rows + PACK_ROWS - 1) / PACK_ROWS;
+    // 8 rows to a CTA, in long calls as many as leave 1024 CTAs, which all read
+    // all targets
+    p.cta_rows = p.rows <= 8192 ? 8 : static_cast<int>(up((p.rows + 1023) / 1024, 32));
+    p.row_ctas = (p.rows + p.cta_rows - 1) / p.cta_rows;
     int weight_ctas = 0;
     if (p.weight != nullptr) {
         weight_ctas = sm_count_of_device() * 8;
@@ -1127,12 +1133,10 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
         p.vocab = vocab;
         x_ld = copied_ld(width);
         p.ld = static_cast<int>(x_ld);
-        p.place_rows = 1;
         p.px = s.x;
         p.pw = s.w;
         p.state = s.state;
         p.place = s.place;
-        p.row_of = s.row_of;
         p.status = status;
         CE_TRY(launch_pack(p, stream));
         x = s.x;
@@ -1152,8 +1156,8 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
     CE_TRY(make_map(&maps.a[0], bf16, x, rows, width, x_ld, g.job[0].a_rows));
     CE_TRY(make_map(&maps.b[0], bf16, w, vocab, width, w_ld, bn / 2));
     CE_TRY((launch_gemm<EPI_LSE, EPI_NONE>(maps, g, stream)));
-    const JoinArgs j = {s.partial, static_cast<const unsigned short *>(args.x),
-                        static_cast<const unsigned short *>(args.weight), args.target,
+    const JoinArgs j = {s.partial, static_cast<const unsigned short *>(x),
+                        static_cast<const unsigned short *>(w), x_ld, w_ld, args.target,
                         packs ? s.place : nullptr, args.ignore, rows, width, vocab,
                         static_cast<int>(up(vocab, bn) / bn * 2), args.loss, args.lse, status};
     return launch_dependent(bf16 ? join_lse_kernel<__nv_bfloat16> : join_lse_kernel<__half>,
@@ -1183,12 +1187,10 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
     p.vocab = vocab;
     p.ld = static_cast<int>(ld);
     p.scaled = !bf16;
-    p.place_rows = 1;
     p.px = s.x;
     p.pw = s.w;
     p.state = s.state;
     p.place = s.place;
-    p.row_of = s.row_of;
     p.ptarget = s.ptarget;
     p.plse2 = s.plse2;
     p.pdloss = s.pdloss;
