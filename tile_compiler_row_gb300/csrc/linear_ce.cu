@@ -72,7 +72,6 @@ struct Job {
 struct GemmArgs {
     Job job[2];
     const CeState *state;       // limits the packed rows (m of GRAD and DX, k of DWEIGHT), or NULL
-    int bf16;
     float2 *partial;            // EPI_LSE: [m][2 n tiles], each half of a tile's columns
     // EPI_GRAD: packed rows' target, lse log2(e) and scaled dloss
     const int *ptarget;
@@ -102,13 +101,15 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t pack2(int bf16, float lo, float hi) {
-    if (bf16) {
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (BF16) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
     }
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // How an epilogue's product lies in memory: K-major operands are [m or n][k],
@@ -163,31 +164,24 @@ __device__ __forceinline__ Extents extents(const Job &j, const CeState *state) {
 // at a time through this warp's part of shared memory and a tensor-map store
 // (128-byte swizzled; whole lines whatever the row stride, and clipped at
 // the matrix's edges).  `value` maps column c + j's accumulator.
-template <class F>
+template <bool BF16, class F>
 __device__ __forceinline__ void store_tile16(const CUtensorMap *map, uint32_t tmem, uint32_t buf,
-                                             int lane, int bf16, int row0, int col0, int from,
-                                             int end, F value) {
+                                             int lane, int row0, int col0, int from, int end,
+                                             F value) {
     for (int c = from; c < end; c += 64) {
-        const uint32_t to = buf + lane * 128;
+        float v[64];
+        tmem_load64(tmem + c, v);
+#pragma unroll
+        for (int j = 0; j < 64; ++j) v[j] = value(v[j], c + j);
         if (lane == 0) store_wait_read<0>();   // the buffer's last store has read it
         __syncwarp();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v[32];
-            tmem_load32(tmem + c + half * 32, v);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = value(v[j], c + half * 32 + j);
-#pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-                const int chunk = half * 4 + j / 8;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 to + 16 * (chunk ^ (lane & 7))),
-                             "r"(pack2(bf16, v[j], v[j + 1])), "r"(pack2(bf16, v[j + 2], v[j + 3])),
-                             "r"(pack2(bf16, v[j + 4], v[j + 5])),
-                             "r"(pack2(bf16, v[j + 6], v[j + 7]))
-                             : "memory");
-            }
-        }
+        for (int j = 0; j < 64; j += 8)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             buf + lane * 128 + 16 * ((j / 8) ^ (lane & 7))),
+                         "r"(pack2<BF16>(v[j], v[j + 1])), "r"(pack2<BF16>(v[j + 2], v[j + 3])),
+                         "r"(pack2<BF16>(v[j + 4], v[j + 5])), "r"(pack2<BF16>(v[j + 6], v[j + 7]))
+                         : "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
@@ -201,25 +195,19 @@ __device__ __forceinline__ void store_tile16(const CUtensorMap *map, uint32_t tm
 // take: 32 rows x 64 columns through shared memory, then row by row, a warp
 // writing one row's 64 elements as 4-byte words (and single elements at its
 // ends where the row starts on an odd element).
-template <class F>
+template <bool BF16, class F>
 __device__ __forceinline__ void store_rows16(unsigned short *out, long long ld, uint32_t tmem,
-                                             uint32_t buf, int lane, int bf16, int row0, int rows,
-                                             int col0, int from, int end, F value) {
+                                             uint32_t buf, int lane, int row0, int rows, int col0,
+                                             int from, int end, F value) {
     for (int c = from; c < end; c += 64) {
-        __syncwarp();
+        float v[64];
+        tmem_load64(tmem + c, v);   // (its barrier: the rows before are out of the buffer)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v[32];
-            tmem_load32(tmem + c + half * 32, v);
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-                // word w of row r lies at word w ^ r of the row's 32
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(
-                                 buf + lane * 128 + 4 * ((half * 16 + j / 2) ^ lane)),
-                             "r"(pack2(bf16, value(v[j]), value(v[j + 1])))
-                             : "memory");
-            }
-        }
+        for (int j = 0; j < 64; j += 2)
+            // word w of row r lies at word w ^ r of the row's 32
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + lane * 128 + 4 * ((j / 2) ^ lane)),
+                         "r"(pack2<BF16>(value(v[j]), value(v[j + 1])))
+                         : "memory");
         __syncwarp();
         // without branches, so that the rows' shared-memory reads and shuffles
         // run side by side (row after row, 18 x 3356 x 68330 took 539 us)
@@ -257,7 +245,7 @@ __device__ __forceinline__ void store_rows16(unsigned short *out, long long ld, 
 // pairs leave a sixth of the pairs' time.  So pairs that get one less of
 // them start on the second job's short tiles while the others do their last
 // long one, and all go on in turn from there (tile_at).
-template <int EPI0, int EPI1>
+template <int EPI0, int EPI1, bool BF16>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs g) {
     extern __shared__ unsigned char smem_raw[];
@@ -393,7 +381,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             const bool second = EPI1 && t >= e0.tiles;
             const bool amn = second ? a_mn(EPI1) : a_mn(EPI0), bmn = second ? b_mn(EPI1) : b_mn(EPI0);
             const uint32_t idesc =
-                mma_idesc(g.bf16 != 0, amn, bmn, BM, g.job[second ? 1 : 0].bn);
+                mma_idesc(BF16, amn, bmn, BM, g.job[second ? 1 : 0].bn);
             const Tile w = where(t);
             if (!(ok = bar_wait(acc_empty(acc), acc_phase ^ 1u, aborted, g.status, CE_WAIT_TIMEOUT)))
                 break;
@@ -489,20 +477,20 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 const int want = in ? g.ptarget[row] - g.n0 - col0 : -1;
                 const float lse2 = in ? g.plse2[row] : 0.0f, dl = in ? g.pdloss[row] : 0.0f;
                 const int limit = in ? e.n - col0 : 0;
-                store_tile16(&maps.out, d, buf, lane, g.bf16, row0, col0, from, to,
+                store_tile16<BF16>(&maps.out, d, buf, lane, row0, col0, from, to,
                              [&](float v, int c) {
                                  const float p = ex2(fmaf(v, kLog2e, -lse2));
                                  return c < limit ? (want == c ? p - 1.0f : p) * dl : 0.0f;
                              });
             } else if (epi == EPI_DWEIGHT) {
-                const float f = none ? 0.0f : g.state->unscale;
+                const float f = g.state->unscale;
                 if (job.store) {
-                    store_tile16(&maps.out, d, buf, lane, g.bf16, row0, col0, from, end,
-                                 [&](float v, int) { return none ? 0.0f : v * f; });
+                    store_tile16<BF16>(&maps.out, d, buf, lane, row0, col0, from, end,
+                                       [&](float v, int) { return none ? 0.0f : v * f; });
                 } else {
-                    store_rows16(static_cast<unsigned short *>(job.out), job.ld, d, buf, lane, g.bf16,
-                                 row0, e.m, col0, from, end,
-                                 [&](float v) { return none ? 0.0f : v * f; });
+                    store_rows16<BF16>(static_cast<unsigned short *>(job.out), job.ld, d, buf, lane,
+                                       row0, e.m, col0, from, end,
+                                       [&](float v) { return none ? 0.0f : v * f; });
                 }
             } else if (epi == EPI_DX) {   // FP32, ld a multiple of 4: rows of whole vectors
                 float *out = static_cast<float *>(job.out) + w.split * g.slice +
@@ -862,8 +850,8 @@ __global__ void __launch_bounds__(FINISH_COLS / 4)
         }
     }
     T *to = dx + r * width;
-    constexpr int bf16 = std::is_same<T, __nv_bfloat16>::value;
-    const uint32_t lo = pack2(bf16, t.x * f, t.y * f), hi = pack2(bf16, t.z * f, t.w * f);
+    constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
+    const uint32_t lo = pack2<BF16>(t.x * f, t.y * f), hi = pack2<BF16>(t.z * f, t.w * f);
     if (width % 4 == 0 && (reinterpret_cast<uintptr_t>(dx) & 7) == 0) {
         *reinterpret_cast<uint2 *>(to + c) = make_uint2(lo, hi);
     } else {
@@ -939,16 +927,16 @@ cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned clust
 
 long long job_tiles(const Job &j) { return up(j.m, BM) / BM * (up(j.n, j.bn) / j.bn) * j.splits; }
 
-template <int EPI0, int EPI1>
-cudaError_t launch_gemm(const GemmMaps &maps, const GemmArgs &g, cudaStream_t stream) {
+template <int EPI0, int EPI1, bool BF16>
+cudaError_t launch_gemm_typed(const GemmMaps &maps, const GemmArgs &g, cudaStream_t stream) {
     static std::atomic<int> ready[kMaxDevices];
+    const auto kernel = gemm_kernel<EPI0, EPI1, BF16>;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (ready[dev].load(std::memory_order_acquire) == 0) {
-        err = cudaFuncSetAttribute(gemm_kernel<EPI0, EPI1>,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM);
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM);
         if (err != cudaSuccess) return err;
         ready[dev].store(1, std::memory_order_release);
     }
@@ -957,8 +945,13 @@ cudaError_t launch_gemm(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st
     long long pairs = sm_count_of_device() / 2;
     if (pairs > tiles) pairs = tiles;
     if (pairs < 1) pairs = 1;
-    return launch_dependent(gemm_kernel<EPI0, EPI1>, static_cast<unsigned>(2 * pairs), 2,
-                            GEMM_THREADS, GEMM_SMEM, stream, maps, g);
+    return launch_dependent(kernel, static_cast<unsigned>(2 * pairs), 2, GEMM_THREADS, GEMM_SMEM,
+                            stream, maps, g);
+}
+template <int EPI0, int EPI1>
+cudaError_t launch_gemm(int bf16, const GemmMaps &maps, const GemmArgs &g, cudaStream_t stream) {
+    return bf16 ? launch_gemm_typed<EPI0, EPI1, true>(maps, g, stream)
+                : launch_gemm_typed<EPI0, EPI1, false>(maps, g, stream);
 }
 
 // Parts of a workspace, in order, each on 256 bytes.
@@ -1150,12 +1143,11 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
     GemmArgs g = {};
     g.job[0] = {rows, vocab, width, bn, rows_of_a(rows), 1, 16, nullptr, 0, 0};
     g.state = packs ? s.state : nullptr;
-    g.bf16 = bf16;
     g.partial = s.partial;
     g.status = status;
     CE_TRY(make_map(&maps.a[0], bf16, x, rows, width, x_ld, g.job[0].a_rows));
     CE_TRY(make_map(&maps.b[0], bf16, w, vocab, width, w_ld, bn / 2));
-    CE_TRY((launch_gemm<EPI_LSE, EPI_NONE>(maps, g, stream)));
+    CE_TRY((launch_gemm<EPI_LSE, EPI_NONE>(bf16, maps, g, stream)));
     const JoinArgs j = {s.partial, static_cast<const unsigned short *>(x),
                         static_cast<const unsigned short *>(w), x_ld, w_ld, args.target,
                         packs ? s.place : nullptr, args.ignore, rows, width, vocab,
@@ -1209,7 +1201,6 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
     CE_TRY(make_map(&both.b[1], bf16, s.x, rows, width, ld, BK));                      // dW: x
     GemmArgs g = {};
     g.state = s.state;
-    g.bf16 = bf16;
     g.status = status;
     g.ptarget = s.ptarget;
     g.plse2 = s.plse2;
@@ -1223,7 +1214,7 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
         g.n0 = static_cast<int>(n0);
         g.accumulate = i > 0;
         g.job[0] = {rows, n, width, BN, a_rows, 1, 16, nullptr, 0, 0};
-        CE_TRY((launch_gemm<EPI_GRAD, EPI_NONE>(grad, g, stream)));
+        CE_TRY((launch_gemm<EPI_GRAD, EPI_NONE>(bf16, grad, g, stream)));
         g.job[0] = {args.dx != nullptr ? rows : 0, width, n, BN, a_rows, splits, 8, s.acc, acc_ld, 0};
         g.job[1] = {args.dweight != nullptr ? n : 0, width, rows, BN, CM, 1, band, nullptr, width,
                     store};
@@ -1232,7 +1223,7 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
             g.job[1].out = to;
             if (store) CE_TRY(make_map(&both.out, bf16, to, n, width, width, 32));
         }
-        CE_TRY((launch_gemm<EPI_DX, EPI_DWEIGHT>(both, g, stream)));
+        CE_TRY((launch_gemm<EPI_DX, EPI_DWEIGHT>(bf16, both, g, stream)));
     }
     if (args.dx == nullptr) return cudaSuccess;
     const long long finish = rows * (up(width, FINISH_COLS) / FINISH_COLS);
