@@ -29,6 +29,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "device_status.h"
 #include "tcgen05.cuh"
 
@@ -126,16 +128,57 @@ __device__ __forceinline__ constexpr bool b_mn(int epi) { return epi == EPI_DWEI
 struct Tile {
     int m, n, split;
 };
-__device__ __forceinline__ Tile tile_of(int t, int m_tiles, int n_tiles, int band) {
-    Tile r;
-    const int plane = m_tiles * n_tiles;
-    r.split = t / plane;
-    t -= r.split * plane;
-    const int b = t / (band * n_tiles), rest = t - b * band * n_tiles;
-    const int high = min(band, m_tiles - b * band);
-    r.m = b * band + rest % high;
-    r.n = rest / high;
+
+// A divisor of tile numbers (below 2^30) with its reciprocal, for quotients in
+// a dozen instructions: every role works out the place of every tile.
+struct Divisor {
+    int d;
+    float inv;
+};
+__device__ __forceinline__ Divisor divisor(int d) {
+    return Divisor{d, 1.0f / static_cast<float>(d)};
+}
+__device__ __forceinline__ int divide(int a, Divisor v, int &rest) {
+    // the first estimate is off by up to a / d 2^-22 (256 at most), the
+    // second by one
+    int q = static_cast<int>(static_cast<float>(a) * v.inv);
+    rest = a - q * v.d;
+    const int more = static_cast<int>(floorf(static_cast<float>(rest) * v.inv));
+    q += more;
+    rest -= more * v.d;
+    if (rest < 0) {
+        rest += v.d;
+        --q;
+    } else if (rest >= v.d) {
+        rest -= v.d;
+        ++q;
+    }
+    return q;
+}
+
+// The tile grid of a job: `plane` tiles a split, in bands of `band` rows.
+struct Raster {
+    int band, bands;
+    Divisor plane, band_tiles, high, last;   // tiles of a band; its rows, and the last band's
+};
+__device__ __forceinline__ Raster raster(int m_tiles, int n_tiles, int band) {
+    Raster r;
+    r.band = band;
+    r.bands = (m_tiles + band - 1) / band;
+    r.plane = divisor(max(1, m_tiles * n_tiles));
+    r.band_tiles = divisor(max(1, band * n_tiles));
+    r.high = divisor(band);
+    r.last = divisor(max(1, m_tiles - (r.bands - 1) * band));
     return r;
+}
+__device__ __forceinline__ Tile tile_of(int t, const Raster &r) {
+    Tile w;
+    int rest;
+    w.split = divide(t, r.plane, t);
+    const int b = divide(t, r.band_tiles, rest);
+    w.n = divide(rest, b == r.bands - 1 ? r.last : r.high, w.m);
+    w.m += b * r.band;
+    return w;
 }
 
 struct Extents {
@@ -315,13 +358,25 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 (pair < last ? pair + pairs - last : pair - last);
         return t < e1.tiles ? static_cast<int>(e0.tiles + t) : -1;
     };
-    auto where = [&](int t) {
-        return t < e0.tiles ? tile_of(t, e0.m_tiles, e0.n_tiles, g.job[0].band)
-                            : tile_of(t - e0.tiles, e1.m_tiles, e1.n_tiles, g.job[1].band);
-    };
-    auto k_begin = [&](int t, int split) {
-        return t < e0.tiles ? static_cast<int>(static_cast<long long>(e0.k_blocks) * split / e0.splits)
-                            : (split == 0 ? 0 : e1.k_blocks);
+    const Raster r0 = raster(e0.m_tiles, e0.n_tiles, g.job[0].band);
+    const Raster r1 = raster(e1.m_tiles, e1.n_tiles, g.job[EPI1 ? 1 : 0].band);
+    // f(job, tile, first and last k block) for tile t, the job's number as a
+    // constant: what f reads of the launch's arguments is then at fixed places
+    // (looked up by a variable, and with the scale read again for every tile,
+    // the epilogue of a short tile took 4850 cycles, 2200 of them for that)
+    auto on_tile = [&](int t, auto f) {
+        if constexpr (EPI1 != EPI_NONE)
+            if (t >= e0.tiles) {
+                f(std::integral_constant<int, 1>{}, tile_of(t - e0.tiles, r1), 0, e1.k_blocks);
+                return;
+            }
+        const Tile w = tile_of(t, r0);
+        int kb0 = 0, kb1 = e0.k_blocks;
+        if (EPI0 == EPI_DX) {
+            kb0 = static_cast<int>(static_cast<long long>(e0.k_blocks) * w.split / e0.splits);
+            kb1 = static_cast<int>(static_cast<long long>(e0.k_blocks) * (w.split + 1) / e0.splits);
+        }
+        f(std::integral_constant<int, 0>{}, w, kb0, kb1);
     };
 
     if (warp == EPI_WARPS && lane == 0) {   // TMA producer
@@ -331,40 +386,38 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         bool ok = true;
         int t;
         for (int i = 0; ok && (t = tile_at(i)) >= 0; ++i) {
-            const bool second = EPI1 && t >= e0.tiles;
-            const Job &job = g.job[second ? 1 : 0];
-            const CUtensorMap *ma = &maps.a[second ? 1 : 0], *mb = &maps.b[second ? 1 : 0];
-            const bool amn = second ? a_mn(EPI1) : a_mn(EPI0), bmn = second ? b_mn(EPI1) : b_mn(EPI0);
-            const Tile w = where(t);
-            const int half = job.bn / 2;
-            const int m0 = w.m * BM + rank * CM, n0 = w.n * job.bn + rank * half;
-            const unsigned int bytes = (job.a_rows + half) * BK * 2;
-            // (once a tile: a division takes longer than the MMAs of a block)
-            const int kb0 = k_begin(t, w.split), kb1 = k_begin(t, w.split + 1);
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!(ok = bar_wait(empty(stage), phase ^ 1u, aborted, g.status, CE_WAIT_TIMEOUT)))
-                    break;
-                const uint32_t a = base + stage * stage_bytes, b = a + a_bytes;
-                const uint32_t bar = peer_addr(full(stage), 0);
-                if (rank == 0) bar_expect_tx(full(stage), 2 * bytes);
-                if (amn) {
-                    tma_load(a, ma, m0, kb * BK, bar);
-                    tma_load(a + 8192, ma, m0 + 64, kb * BK, bar);
-                } else {
-                    tma_load(a, ma, kb * BK, m0, bar);
+            on_tile(t, [&](auto j, Tile w, int kb0, int kb1) {
+                constexpr int J = decltype(j)::value, EPI = J ? EPI1 : EPI0;
+                const Job &job = g.job[J];
+                const int half = job.bn / 2;
+                const int m0 = w.m * BM + rank * CM, n0 = w.n * job.bn + rank * half;
+                const unsigned int bytes = (job.a_rows + half) * BK * 2;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!(ok = bar_wait(empty(stage), phase ^ 1u, aborted, g.status,
+                                        CE_WAIT_TIMEOUT)))
+                        break;
+                    const uint32_t a = base + stage * stage_bytes, b = a + a_bytes;
+                    const uint32_t bar = peer_addr(full(stage), 0);
+                    if (rank == 0) bar_expect_tx(full(stage), 2 * bytes);
+                    if (a_mn(EPI)) {
+                        tma_load(a, &maps.a[J], m0, kb * BK, bar);
+                        tma_load(a + 8192, &maps.a[J], m0 + 64, kb * BK, bar);
+                    } else {
+                        tma_load(a, &maps.a[J], kb * BK, m0, bar);
+                    }
+                    if (b_mn(EPI)) {   // (256 columns to a tile)
+                        tma_load(b, &maps.b[J], n0, kb * BK, bar);
+                        tma_load(b + 8192, &maps.b[J], n0 + 64, kb * BK, bar);
+                    } else {
+                        tma_load(b, &maps.b[J], kb * BK, n0, bar);
+                    }
+                    ++issued;
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
-                if (bmn) {   // (256 columns to a tile)
-                    tma_load(b, mb, n0, kb * BK, bar);
-                    tma_load(b + 8192, mb, n0 + 64, kb * BK, bar);
-                } else {
-                    tma_load(b, mb, kb * BK, n0, bar);
-                }
-                ++issued;
-                if (++stage == stages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
+            });
         }
         // An aborted pair waits (bounded) for the copies it issued: none may
         // land in shared memory that it no longer owns.
@@ -378,40 +431,40 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         bool ok = true;
         int t;
         for (int i = 0; ok && (t = tile_at(i)) >= 0; ++i) {
-            const bool second = EPI1 && t >= e0.tiles;
-            const bool amn = second ? a_mn(EPI1) : a_mn(EPI0), bmn = second ? b_mn(EPI1) : b_mn(EPI0);
-            const uint32_t idesc =
-                mma_idesc(BF16, amn, bmn, BM, g.job[second ? 1 : 0].bn);
-            const Tile w = where(t);
-            if (!(ok = bar_wait(acc_empty(acc), acc_phase ^ 1u, aborted, g.status, CE_WAIT_TIMEOUT)))
-                break;
-            tc_fence_after();
-            const uint32_t d = tmem + acc * BN;
-            bool first = true;
-            // 16 elements along K: 32 bytes of a K-major row, or 16 rows of
-            // 128 bytes
-            const int sa = amn ? 2048 >> 4 : 32 >> 4, sb = bmn ? 2048 >> 4 : 32 >> 4;
-            const uint32_t lead_a = amn ? 8192 : 16, lead_b = bmn ? 8192 : 16;
-            const int kb0 = k_begin(t, w.split), kb1 = k_begin(t, w.split + 1);
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!(ok = bar_wait(full(stage), phase, aborted, g.status, CE_WAIT_TIMEOUT))) break;
+            on_tile(t, [&](auto j, Tile, int kb0, int kb1) {
+                constexpr int J = decltype(j)::value, EPI = J ? EPI1 : EPI0;
+                const uint32_t idesc = mma_idesc(BF16, a_mn(EPI), b_mn(EPI), BM, g.job[J].bn);
+                if (!(ok = bar_wait(acc_empty(acc), acc_phase ^ 1u, aborted, g.status,
+                                    CE_WAIT_TIMEOUT)))
+                    return;
                 tc_fence_after();
-                const uint32_t a = base + stage * stage_bytes, b = a + a_bytes;
-                const uint64_t da = smem_desc(a, lead_a, 1024), db = smem_desc(b, lead_b, 1024);
+                const uint32_t d = tmem + acc * BN;
+                bool first = true;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!(ok = bar_wait(full(stage), phase, aborted, g.status, CE_WAIT_TIMEOUT)))
+                        break;
+                    tc_fence_after();
+                    const uint32_t a = base + stage * stage_bytes, b = a + a_bytes;
+                    const uint64_t da = smem_desc(a, a_mn(EPI) ? 8192 : 16, 1024);
+                    const uint64_t db = smem_desc(b, b_mn(EPI) ? 8192 : 16, 1024);
 #pragma unroll
-                for (int k = 0; k < BK / 16; ++k) {
-                    tc_mma(d, da + k * sa, db + k * sb, idesc, !first);
-                    first = false;
+                    for (int k = 0; k < BK / 16; ++k) {
+                        // 16 elements along K: 32 bytes of a K-major row, or
+                        // 16 rows of 128 bytes
+                        tc_mma(d, da + k * (a_mn(EPI) ? 2048 >> 4 : 32 >> 4),
+                               db + k * (b_mn(EPI) ? 2048 >> 4 : 32 >> 4), idesc, !first);
+                        first = false;
+                    }
+                    tc_commit(empty(stage));
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
-                tc_commit(empty(stage));
-                if (++stage == stages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-            tc_commit(acc_full(acc));
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
+                tc_commit(acc_full(acc));
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            });
         }
         if (*aborted) {   // wait (bounded) until no MMA touches the pair's memory
             tc_commit(acc_full(acc));
@@ -427,95 +480,98 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         const uint32_t buf = base + PIPE_BYTES + warp * 4096;
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t drained0 = peer_addr(acc_empty(0), 0), drained1 = peer_addr(acc_empty(1), 0);
+        const float unscale = EPI1 == EPI_DWEIGHT ? g.state->unscale : 1.0f;
         int t;
         for (int i = 0; (t = tile_at(i)) >= 0; ++i) {
-            const Tile w = where(t);
-            const bool ok = bar_wait(acc_full(acc), acc_phase, aborted, g.status, CE_WAIT_TIMEOUT);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
-            const bool second = EPI1 && t >= e0.tiles;
-            const Job &job = g.job[second ? 1 : 0];
-            const Extents &e = second ? e1 : e0;
-            const int row0 = w.m * BM + rank * CM + quarter * 32, row = row0 + lane;
-            const int col0 = w.n * job.bn;
-            // this warp's columns of the tile: [from, to), and those that exist
-            const int from = half * (job.bn / 2), to = from + job.bn / 2;
-            const int end = min(to, e.n - col0);
-            const uint32_t d = tmem + acc * BN + (static_cast<uint32_t>(quarter * 32) << 16);
-            // no product was made: zero
-            const bool none = k_begin(t, w.split) == k_begin(t, w.split + 1);
-            const int epi = second ? EPI1 : EPI0;
-            // rows of this warp that are looked at: those that are there, and
-            // for g those up to the next 64, which dW's reduction reads
-            if (row0 >= (epi == EPI_GRAD ? (e.m + BK - 1) / BK * BK : e.m)) {
-            } else if (epi == EPI_LSE) {
-                float m = -INFINITY, s = 0.0f;
-                for (int c = from; c < end; c += 32) {
-                    float v[32];
-                    tmem_load32(d + c, v);
-                    const int limit = end - c;
-                    if (limit < 32)
+            bool ok = true;
+            on_tile(t, [&](auto j, Tile w, int kb0, int kb1) {
+                constexpr int J = decltype(j)::value, EPI = J ? EPI1 : EPI0;
+                const Job &job = g.job[J];
+                const Extents &e = J ? e1 : e0;
+                ok = __all_sync(0xffffffffu, bar_wait(acc_full(acc), acc_phase, aborted, g.status,
+                                                      CE_WAIT_TIMEOUT));
+                if (!ok) return;
+                tc_fence_after();
+                const int row0 = w.m * BM + rank * CM + quarter * 32, row = row0 + lane;
+                const int col0 = w.n * job.bn;
+                // this warp's columns of the tile: [from, to), and those that exist
+                const int from = half * (job.bn / 2), to = from + job.bn / 2;
+                const int end = min(to, e.n - col0);
+                const uint32_t d = tmem + acc * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+                const bool none = kb0 == kb1;   // no product was made: zero
+                // rows of this warp that are looked at: those that are there, and
+                // for g those up to the next 64, which dW's reduction reads
+                if (row0 >= (EPI == EPI_GRAD ? (e.m + BK - 1) / BK * BK : e.m)) return;
+                if constexpr (EPI == EPI_LSE) {
+                    float m = -INFINITY, s = 0.0f;
+                    for (int c = from; c < end; c += 32) {
+                        float v[32];
+                        tmem_load32(d + c, v);
+                        const int limit = end - c;
+                        if (limit < 32)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j >= limit) v[j] = -INFINITY;
-                    float top = m;
+                            for (int j = 0; j < 32; ++j)
+                                if (j >= limit) v[j] = -INFINITY;
+                        float top = m;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
-                    const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
-                    s *= ex2(m * kLog2e - ref);
-                    float part[4] = {};
+                        for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
+                        const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
+                        s *= ex2(m * kLog2e - ref);
+                        float part[4] = {};
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) part[j & 3] += ex2(fmaf(v[j], kLog2e, -ref));
-                    s += (part[0] + part[1]) + (part[2] + part[3]);
-                    m = top;
-                }
-                if (row < e.m)
-                    g.partial[(static_cast<long long>(row) * e.n_tiles + w.n) * 2 + half] =
-                        make_float2(m, s);
-            } else if (epi == EPI_GRAD) {
-                const bool in = row < e.m;
-                const int want = in ? g.ptarget[row] - g.n0 - col0 : -1;
-                const float lse2 = in ? g.plse2[row] : 0.0f, dl = in ? g.pdloss[row] : 0.0f;
-                const int limit = in ? e.n - col0 : 0;
-                store_tile16<BF16>(&maps.out, d, buf, lane, row0, col0, from, to,
-                             [&](float v, int c) {
-                                 const float p = ex2(fmaf(v, kLog2e, -lse2));
-                                 return c < limit ? (want == c ? p - 1.0f : p) * dl : 0.0f;
-                             });
-            } else if (epi == EPI_DWEIGHT) {
-                const float f = g.state->unscale;
-                if (job.store) {
-                    store_tile16<BF16>(&maps.out, d, buf, lane, row0, col0, from, end,
-                                       [&](float v, int) { return none ? 0.0f : v * f; });
-                } else {
-                    store_rows16<BF16>(static_cast<unsigned short *>(job.out), job.ld, d, buf, lane,
-                                       row0, e.m, col0, from, end,
-                                       [&](float v) { return none ? 0.0f : v * f; });
-                }
-            } else if (epi == EPI_DX) {   // FP32, ld a multiple of 4: rows of whole vectors
-                float *out = static_cast<float *>(job.out) + w.split * g.slice +
-                             static_cast<long long>(row) * job.ld + col0;
-                for (int c = from; c < to && col0 + c < job.ld; c += 32) {
-                    float v[32];
-                    tmem_load32(d + c, v);
+                        for (int j = 0; j < 32; ++j) part[j & 3] += ex2(fmaf(v[j], kLog2e, -ref));
+                        s += (part[0] + part[1]) + (part[2] + part[3]);
+                        m = top;
+                    }
                     if (row < e.m)
+                        g.partial[(static_cast<long long>(row) * e.n_tiles + w.n) * 2 + half] =
+                            make_float2(m, s);
+                } else if constexpr (EPI == EPI_GRAD) {
+                    const bool in = row < e.m;
+                    const int want = in ? g.ptarget[row] - g.n0 - col0 : -1;
+                    const float lse2 = in ? g.plse2[row] : 0.0f, dl = in ? g.pdloss[row] : 0.0f;
+                    const int limit = in ? e.n - col0 : 0;
+                    store_tile16<BF16>(&maps.out, d, buf, lane, row0, col0, from, to,
+                                 [&](float v, int c) {
+                                     const float p = ex2(fmaf(v, kLog2e, -lse2));
+                                     return c < limit ? (want == c ? p - 1.0f : p) * dl : 0.0f;
+                                 });
+                } else if constexpr (EPI == EPI_DWEIGHT) {
+                    const float f = unscale;
+                    if (job.store) {
+                        store_tile16<BF16>(&maps.out, d, buf, lane, row0, col0, from, end,
+                                           [&](float v, int) { return none ? 0.0f : v * f; });
+                    } else {
+                        store_rows16<BF16>(static_cast<unsigned short *>(job.out), job.ld, d, buf, lane,
+                                           row0, e.m, col0, from, end,
+                                           [&](float v) { return none ? 0.0f : v * f; });
+                    }
+                } else if constexpr (EPI == EPI_DX) {   // FP32, ld a multiple of 4: rows of whole vectors
+                    float *out = static_cast<float *>(job.out) + w.split * g.slice +
+                                 static_cast<long long>(row) * job.ld + col0;
+                    for (int c = from; c < to && col0 + c < job.ld; c += 32) {
+                        float v[32];
+                        tmem_load32(d + c, v);
+                        if (row < e.m)
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            if (col0 + c + j >= job.ld) break;
-                            float4 q = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                                            : make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                            float4 *p = reinterpret_cast<float4 *>(out + c + j);
-                            if (g.accumulate) {
-                                const float4 o = *p;
-                                q = make_float4(q.x + o.x, q.y + o.y, q.z + o.z, q.w + o.w);
+                            for (int j = 0; j < 32; j += 4) {
+                                if (col0 + c + j >= job.ld) break;
+                                float4 q = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                                : make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                                float4 *p = reinterpret_cast<float4 *>(out + c + j);
+                                if (g.accumulate) {
+                                    const float4 o = *p;
+                                    q = make_float4(q.x + o.x, q.y + o.y, q.z + o.z, q.w + o.w);
+                                }
+                                *p = q;
                             }
-                            *p = q;
-                        }
+                    }
                 }
-            }
+            });
+            if (!ok) break;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive_cluster(acc ? drained1 : drained0);
+            if (lane == 0) bar_arrive_peer(acc ? drained1 : drained0);
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }

@@ -34,9 +34,12 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// Arrives on a barrier of any CTA of the cluster (a peer_addr).
-__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrives on a barrier of any CTA of the cluster (a peer_addr).  What it tells
+// of is this thread's reads of tensor memory (ordered by tc_fence_before), no
+// memory that the other CTA reads: the release is the CTA's, as a release to
+// the cluster waits for every store of the thread.
+__device__ __forceinline__ void bar_arrive_peer(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool bar_test(uint32_t bar, unsigned int parity) {
     unsigned int ok;
