@@ -325,6 +325,28 @@ def test_streams_and_graph():
             assert torch.equal(a, b)
 
 
+def test_rows_behind_are_left_as_they_were():
+    """Outputs' neighbours in memory, and the workspace's, are not written
+    (whole vectors, and rows that end inside one)."""
+    for width in (96, 99):
+        s = make(37, width, "bf16", 5)
+        bufs = [torch.full((41, width), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        mats = [b[:37] for b in bufs]
+        need = tile.tile_block_norm_backward_workspace_bytes(37, width)
+        ws = torch.full((need + 512,), 3, dtype=torch.uint8, device="cuda")
+        grads = torch.full((12, width), 7.0, device="cuda")
+        tile.tile_block_norm(s["x"], s["residual"], mats[0], mats[1], s["gamma_post"], s["gate"],
+                             s["gamma_pre"], rows_per_gate=5)
+        tile.tile_block_norm_backward(s["x"], mats[0], s["dhidden"], s["dout"], mats[2], mats[3],
+                                      ws[:need], s["gamma_post"], s["gate"], s["gamma_pre"],
+                                      grads[0], grads[1:9], grads[9], rows_per_gate=5)
+        assert all((b[37:] == 7).all() for b in bufs)
+        assert (grads[10:] == 7).all() and (ws[need:] == 3).all()
+        ref = reference_backward(s, mats[0], True, True, 5, 1.0, 1e-5)
+        check(mats[2], *ref["din"], 192, "din")
+        check(grads[1:9], *ref["dgate"], 400, "dgate")
+
+
 def test_agrees_with_the_weighted_rmsnorm():
     """Without a block norm and with a zero residual the block norm is the
     library's weighted RMSNorm."""

@@ -274,6 +274,25 @@ def test_repeats_streams_and_graph():
             assert torch.equal(a, b)
 
 
+def test_two_calls_at_once():
+    """Calls on two streams with no synchronisation between them, each with a
+    workspace of its own, forward and backward, small beside large."""
+    calls = [make(700, 256, 9000, "bf16", 0.2, seed=5), make(9, 136, 3000, "f16", seed=6)]
+
+    def both(x, weight, target, dloss, stream=None):
+        loss, lse = tile.linear_cross_entropy(x, weight, target, stream=stream)
+        return (loss, lse) + tile.linear_cross_entropy_backward(x, weight, target, lse, dloss,
+                                                                stream=stream)
+    alone = [both(*c) for c in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [both(*c, stream=s) for c, s in zip(calls, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
 def test_rows_behind_are_left_as_they_were():
     """The outputs' neighbours in memory are not written."""
     x, weight, target, dloss = make(37, 72, 300, "bf16")

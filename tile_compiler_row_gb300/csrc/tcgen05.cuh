@@ -24,9 +24,6 @@ __device__ __forceinline__ void bar_expect_tx(uint32_t bar, unsigned int bytes) 
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 // The address that shared memory at `addr` of this CTA has in CTA `rank` of
 // the cluster.
 __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
@@ -52,9 +49,10 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, unsigned int parity) {
     return ok != 0;
 }
 
-// Polls of a barrier before a wait gives up (each poll may suspend the
-// thread for a hardware-defined time): far beyond the longest tile.
-constexpr unsigned int kBarSpins = 1u << 24;
+// Polls of a barrier before a wait gives up.  A poll suspends the thread for
+// up to 4.0 us (measured), so a wait that runs out has lasted 2 s; a tile
+// takes microseconds, or 0.1 s where a gradient sums over 20 million tokens.
+constexpr unsigned int kBarSpins = 1u << 19;
 
 // Bounded wait for the phase `parity` of a barrier.  A wait that runs out
 // sets `bit` in the device status word and the CTA's abort flag; every

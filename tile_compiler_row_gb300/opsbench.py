@@ -4,8 +4,10 @@ For each op: ``--warmup`` calls, then ``--iters`` calls timed one by one
 with CUDA events on the current stream; the mean call time gives the
 achieved bandwidth from the op's algorithmic bytes (each input element read
 once, each output element written once), reported against the measured HBM
-copy bandwidth.  Inputs are uniform random device tensors (timing only;
-parity is covered by the GPU tests).  The default 65536 x 4096 shape keeps
+copy bandwidth.  The linear cross entropy (at most 4096 of the rows, against a
+vocabulary of ``--vocab`` entries) is reported by its matrix products, against
+the measured BF16 rate.  Inputs are uniform random device tensors (timing
+only; parity is covered by the GPU tests).  The default 65536 x 4096 shape keeps
 every working set far above the 129 MB L2.
 
     python -m tile_compiler_row_gb300.opsbench [--rows R --width W] [--json out.json]
@@ -29,10 +31,20 @@ def measured_hbm_gbs():
         return 6800.0, "fallback"
 
 
+def measured_bf16_tflops():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    try:
+        with open(os.path.join(root, "MEASURED_PEAKS.json")) as fh:
+            return float(json.load(fh)["bf16_tflops"]), "measured"
+    except (OSError, KeyError, ValueError):
+        return 1900.0, "fallback"
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--rows", type=int, default=65536)
     ap.add_argument("--width", type=int, default=4096)
+    ap.add_argument("--vocab", type=int, default=32768)
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--iters", type=int, default=50)
     ap.add_argument("--json", default=None)
@@ -69,6 +81,21 @@ def main(argv=None):
     smb = sm.to(torch.bfloat16)
     smh = sm.to(torch.float16)
     tile.tile_layernorm_backward_f32(x, None, r, y, stats)
+    # the block norm: both norms, a learned gate per channel
+    gate = g[None, :].contiguous()
+    block = {}
+    for kind, a, c in (("f32", x, r), ("bf16", xb, rb), ("f16", xh, rh)):
+        h, o = torch.empty_like(a), torch.empty_like(a)
+        d, e = torch.empty_like(a), torch.empty_like(a)
+        tile.tile_block_norm(a, c, h, o, g, gate, g)
+        bws = torch.empty(tile.tile_block_norm_backward_workspace_bytes(rows, width),
+                          dtype=torch.uint8, device="cuda")
+        grads = [torch.empty(width, device="cuda"), torch.empty_like(gate),
+                 torch.empty(width, device="cuda")]
+        block[kind] = (
+            lambda a=a, c=c, h=h, o=o: tile.tile_block_norm(a, c, h, o, g, gate, g),
+            lambda a=a, c=c, h=h, o=o, d=d, e=e, bws=bws, grads=grads:
+                tile.tile_block_norm_backward(a, h, c, o, d, e, bws, g, gate, g, *grads))
 
     ops = {
         # name: (callable, algorithmic bytes per element, plan description)
@@ -111,14 +138,33 @@ def main(argv=None):
         "softmax_backward_f16": (lambda: tile.tile_softmax_backward_f16(smh, rh, yh), 6),
         "norm_param_grad_f16": (lambda: tile.tile_norm_param_grad_f16(xh, rh, stats, dg, db, ws),
                                 4),
+        "block_norm_f32": (block["f32"][0], 16),
+        "block_norm_bf16": (block["bf16"][0], 8),
+        "block_norm_f16": (block["f16"][0], 8),
+        "block_norm_backward_f32": (block["f32"][1], 24),
+        "block_norm_backward_bf16": (block["bf16"][1], 12),
+        "block_norm_backward_f16": (block["f16"][1], 12),
     }
+    # the loss: name -> (callable, products of 2 rows width vocab operations)
+    tokens = min(rows, 4096)
+    losses = {}
+    for kind, a in (("bf16", xb), ("f16", xh)):
+        xs = a[:tokens]
+        w = torch.rand(args.vocab, width, device="cuda", generator=gen).sub_(0.5).to(a.dtype)
+        target = torch.randint(args.vocab, (tokens,), device="cuda", generator=gen)
+        dloss = torch.full((tokens,), 1.0 / tokens, device="cuda")
+        lse = tile.linear_cross_entropy(xs, w, target)[1]
+        losses[f"linear_cross_entropy_{kind}"] = (
+            lambda xs=xs, w=w, target=target: tile.linear_cross_entropy(xs, w, target), 1)
+        losses[f"linear_cross_entropy_backward_{kind}"] = (
+            lambda xs=xs, w=w, target=target, lse=lse, dloss=dloss:
+                tile.linear_cross_entropy_backward(xs, w, target, lse, dloss), 3)
     only = set(args.only.split(",")) if args.only else None
     peak, src = measured_hbm_gbs()
     stream = torch.cuda.current_stream()
     results = []
-    for name, (fn, bpe) in ops.items():
-        if only and name not in only:
-            continue
+    def timed(fn):
+        """Milliseconds of each of the timed calls."""
         for _ in range(args.warmup):
             fn()
         evs = [torch.cuda.Event(enable_timing=True) for _ in range(args.iters + 1)]
@@ -127,13 +173,31 @@ def main(argv=None):
             fn()
             evs[i + 1].record(stream)
         torch.cuda.synchronize()
-        per = [evs[i].elapsed_time(evs[i + 1]) for i in range(args.iters)]
+        return [evs[i].elapsed_time(evs[i + 1]) for i in range(args.iters)]
+
+    for name, (fn, bpe) in ops.items():
+        if only and name not in only:
+            continue
+        per = timed(fn)
         ms = statistics.mean(per)
         gbs = bpe * n / (ms * 1e-3) / 1e9
         res = {"op": name, "rows": rows, "width": width, "bytes_per_elem": bpe,
                "us_per_call": round(ms * 1e3, 2), "median_us": round(statistics.median(per) * 1e3, 2),
                "achieved_gbs": round(gbs, 1), "frac_of_copy": round(gbs / peak, 4),
                "peak": f"{peak} GB/s ({src} HBM copy)"}
+        results.append(res)
+        print(json.dumps(res), flush=True)
+    rate, src = measured_bf16_tflops()
+    for name, (fn, products) in losses.items():
+        if only and name not in only:
+            continue
+        per = timed(fn)
+        ms = statistics.mean(per)
+        tflops = products * 2.0 * tokens * width * args.vocab / (ms * 1e-3) / 1e12
+        res = {"op": name, "rows": tokens, "width": width, "vocab": args.vocab,
+               "us_per_call": round(ms * 1e3, 2), "median_us": round(statistics.median(per) * 1e3, 2),
+               "achieved_tflops": round(tflops, 1), "frac_of_bf16": round(tflops / rate, 4),
+               "peak": f"{rate} TFLOP/s ({src} cuBLAS BF16)"}
         results.append(res)
         print(json.dumps(res), flush=True)
     assert tile.tile_check_device_status() == 0
