@@ -172,6 +172,58 @@ def test_everything_ignored_and_no_rows():
     assert dx.numel() == 0 and not dweight.any()
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("rows,width,vocab", [(3, 2048, 1000), (200, 2048, 5000), (300, 1001, 777)])
+def test_tokens_the_head_is_sure_of(rows, width, vocab, kind):
+    """Losses from 1e-2 down to 1e-5 keep their digits, and the target's
+    gradient, which is as small.  Both logits of a difference l_v - l_target
+    are off by at most e = sum_error L (the target's, an FP32 sum of width / 32
+    terms in each lane, by less), so a loss of log1p(d) is off by
+    d (2 e + 2^-17).  e^(l - lse) - 1 takes the target's error, and that of an
+    lse rounded to 24 bits, but the tensor cores' error of 1e-5 and more of
+    the logit itself reaches neither."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    t = TYPES[kind]
+    weight = (torch.randn(vocab, width, device="cuda", generator=gen) / width ** 0.5).to(t)
+    target = torch.randint(vocab, (rows,), device="cuda", generator=gen)
+    scale = torch.linspace(12, 18, rows, device="cuda")[:, None]
+    x = (weight[target].float() * scale).to(t)
+    loss, lse = tile.linear_cross_entropy(x, weight, target)
+    l = x.double() @ weight.double().t()
+    mag = (x.double().abs() @ weight.double().abs().t()).amax(1)
+    at = l.gather(1, target[:, None])
+    others = torch.exp(l - at)
+    others.scatter_(1, target[:, None], 0.0)
+    want = torch.log1p(others.sum(1))
+    assert (loss >= 0).all() and want.max() < 0.2 and want.min() < 1e-3
+    e = (width / 32 + 6) * 2.0 ** -23 * mag   # FP32 sums of a lane, and over lanes
+    e_tc = sum_error(width) * mag
+    rel = (e + e_tc).clamp(max=0.5)
+    assert ((loss.double() - want).abs() <= want * (1.1 * rel + 2.0 ** -17)).all()
+    # one row's dx: g_t w_t + sum of the others, with p from the lse handed over
+    dx, _ = tile.linear_cross_entropy_backward(x, weight, target, lse, torch.ones(rows, device="cuda"),
+                                               need_dweight=False)
+    p = torch.exp(l - lse.double()[:, None])
+    g = p.clone()
+    miss = torch.expm1(at[:, 0] - lse.double())
+    g.scatter_(1, target[:, None], miss[:, None])
+    ref = g @ weight.double()
+    half = torch.finfo(t).eps / 2
+    gerr = half * g.abs() + p * (rel + 2.0 ** -20 * lse.double().abs())[:, None]
+    gerr.scatter_(1, target[:, None], (half * miss.abs() + e + 2.0 ** -23 * lse.double())[:, None])
+    if t == torch.float16:
+        gerr += 2.0 ** -39
+    tol = half * ref.abs() + 1.01 * gerr @ weight.double().abs() + \
+        sum_error(vocab) * (g.abs() @ weight.double().abs()) + 2.0 ** -24
+    assert ((dx.double() - ref).abs() <= tol).all()
+    # the same, in the 2-norm, where the roundings of g and of dx are
+    # independent: no worse than 4 roundings and the target's own error
+    off = (dx.double() - ref).norm(dim=1)
+    own = (e + 2.0 ** -23 * lse.double()) * weight[target].double().norm(dim=1)
+    assert (off <= 4 * half * ref.norm(dim=1) + own + 1e-6).all()
+    assert tile.tile_check_device_status() == 0
+
+
 def test_another_ignore_index():
     x, weight, target, dloss = make(50, 64, 300, "f16")
     target[::3] = 0

@@ -7,17 +7,18 @@
 // with FP32 accumulators in tensor memory (gemm_kernel); what becomes of a
 // 256 x 256 tile of it is the epilogue:
 //
-//   forward    a tile of l is reduced to each row's maximum and sum of
-//              exponentials, two numbers per tile and row; a second kernel
-//              joins them and takes the target's logit as a dot product of
-//              its own, in FP32 FMAs: the tensor cores truncate as they add
-//              (at 4096 columns a logit was off by 1e-5), which an lse mostly
-//              averages out and one logit does not (the loss of 4096 tokens
-//              over 131072 entries was 1.5e-6 off in the 2-norm with the
-//              tile's logit).
+//   forward    a tile of l, without the targets' entries, is reduced to each
+//              row's maximum and sum of exponentials, two numbers per tile
+//              and row; a second kernel joins them with the target's logit, a
+//              dot product of its own in FP32 FMAs:
+//              loss = log(1 + sum_{v != target} exp(l_v - l_target)).
+//              So a token that the head is sure of has a loss that keeps its
+//              digits, and never one below 0, though a logit of the tensor
+//              cores is off by more than it (logit_scale).
 //   backward   in pieces of the vocabulary: l is computed again, turned into
 //              g and kept in 16 bits for this piece only; then dW of the
-//              piece's rows is g^T x, and g W is added to an FP32 dx.
+//              piece's rows is g^T x, and g W is added to an FP32 dx.  At the
+//              target g is expm1(l - lse) of an FP32 dot product again.
 //
 // Backward first packs the rows whose target counts (and whose dloss is not
 // 0) to the front of a copy of x, so rows that are ignored cost nothing and
@@ -49,7 +50,7 @@ constexpr int EPI_WARPS = 8;                             // two for each 32 rows
 constexpr int STORE_BYTES = EPI_WARPS * 4096;            // 32 rows x 128 bytes for each
 constexpr int GEMM_SMEM = PIPE_BYTES + STORE_BYTES + 1024;   // + slack to align to 1024
 constexpr int GEMM_THREADS = 32 * (EPI_WARPS + 2);       // and TMA, MMA
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum { EPI_NONE, EPI_LSE, EPI_GRAD, EPI_DWEIGHT, EPI_DX };
 
@@ -75,9 +76,11 @@ struct GemmArgs {
     Job job[2];
     const CeState *state;       // limits the packed rows (m of GRAD and DX, k of DWEIGHT), or NULL
     float2 *partial;            // EPI_LSE: [m][2 n tiles], each half of a tile's columns
-    // EPI_GRAD: packed rows' target, lse log2(e) and scaled dloss
+    const long long *target;    // EPI_LSE: the rows' targets where they are not packed
+    // packed rows' target and, for EPI_GRAD, lse log2(e), p - 1 at the target
+    // and scaled dloss
     const int *ptarget;
-    const float *plse2, *pdloss;
+    const float *plse2, *pmiss, *pdloss;
     int n0;                     // first vocabulary entry of the piece
     int accumulate;             // EPI_DX: add to what is there
     long long slice;            // elements of a slice
@@ -101,6 +104,17 @@ __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// log2(e), by which logits of the tensor cores are multiplied, with what they
+// lost put back.  The tensor cores truncate: each 16 products added take half
+// a unit of the 24th bit off the sum so far, on average, 2^-25 to 2^-24 of it
+// and so, over a sum that grows evenly, 2^-26 to 2^-25 of the whole for each
+// step.  Put back is the least of that: 4096 columns lost 3.9e-6 (random) to
+// 4.4e-6 (x along w) of a logit and 256 2^-26 = 3.8e-6 are put back; the lse
+// of 256 rows over 32768 entries was 8.8e-6 too small, every row alike.
+__device__ __forceinline__ float logit_scale(int k_blocks) {
+    return kLog2e * (1.0f + static_cast<float>(k_blocks * (BK / 16)) * 0x1p-26f);
 }
 
 template <bool BF16>
@@ -488,12 +502,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 constexpr int J = decltype(j)::value, EPI = J ? EPI1 : EPI0;
                 const Job &job = g.job[J];
                 const Extents &e = J ? e1 : e0;
+                const int row0 = w.m * BM + rank * CM + quarter * 32, row = row0 + lane;
+                const int col0 = w.n * job.bn;
+                int skip = -1;   // the tile's column that this row leaves out
+                if (EPI == EPI_LSE && row < e.m) {
+                    const long long t = g.ptarget != nullptr ? g.ptarget[row] : g.target[row];
+                    if (t >= col0 && t < e.n) skip = static_cast<int>(t) - col0;
+                }
                 ok = __all_sync(0xffffffffu, bar_wait(acc_full(acc), acc_phase, aborted, g.status,
                                                       CE_WAIT_TIMEOUT));
                 if (!ok) return;
                 tc_fence_after();
-                const int row0 = w.m * BM + rank * CM + quarter * 32, row = row0 + lane;
-                const int col0 = w.n * job.bn;
                 // this warp's columns of the tile: [from, to), and those that exist
                 const int from = half * (job.bn / 2), to = from + job.bn / 2;
                 const int end = min(to, e.n - col0);
@@ -503,6 +522,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 // for g those up to the next 64, which dW's reduction reads
                 if (row0 >= (EPI == EPI_GRAD ? (e.m + BK - 1) / BK * BK : e.m)) return;
                 if constexpr (EPI == EPI_LSE) {
+                    // the maximum and the sum over exponents of 2
+                    const float scale = logit_scale(e.k_blocks);
                     float m = -INFINITY, s = 0.0f;
                     for (int c = from; c < end; c += 32) {
                         float v[32];
@@ -512,14 +533,20 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
                                 if (j >= limit) v[j] = -INFINITY;
-                        float top = m;
+                        const int hit = skip - c;
+                        if (__any_sync(0xffffffffu, hit >= 0 && hit < 32))
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
-                        const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
-                        s *= ex2(m * kLog2e - ref);
+                            for (int j = 0; j < 32; ++j)
+                                if (j == hit) v[j] = -INFINITY;
+                        float top = v[0];
+#pragma unroll
+                        for (int j = 1; j < 32; ++j) top = fmaxf(top, v[j]);
+                        top = fmaxf(m, top * scale);
+                        const float ref = top == -INFINITY ? 0.0f : top;
+                        s *= ex2(m - ref);
                         float part[4] = {};
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) part[j & 3] += ex2(fmaf(v[j], kLog2e, -ref));
+                        for (int j = 0; j < 32; ++j) part[j & 3] += ex2(fmaf(v[j], scale, -ref));
                         s += (part[0] + part[1]) + (part[2] + part[3]);
                         m = top;
                     }
@@ -530,11 +557,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     const bool in = row < e.m;
                     const int want = in ? g.ptarget[row] - g.n0 - col0 : -1;
                     const float lse2 = in ? g.plse2[row] : 0.0f, dl = in ? g.pdloss[row] : 0.0f;
+                    const float miss = in ? g.pmiss[row] : 0.0f;
+                    const float scale = logit_scale(e.k_blocks);
                     const int limit = in ? e.n - col0 : 0;
                     store_tile16<BF16>(&maps.out, d, buf, lane, row0, col0, from, to,
                                  [&](float v, int c) {
-                                     const float p = ex2(fmaf(v, kLog2e, -lse2));
-                                     return c < limit ? (want == c ? p - 1.0f : p) * dl : 0.0f;
+                                     const float p = ex2(fmaf(v, scale, -lse2));
+                                     return c < limit ? (want == c ? miss : p) * dl : 0.0f;
                                  });
                 } else if constexpr (EPI == EPI_DWEIGHT) {
                     const float f = unscale;
@@ -585,21 +614,58 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     if (warp == EPI_WARPS + 1) tmem_free(tmem, 512);
 }
 
+// ---- a row's own logit -----------------------------------------------------------------
+
+template <class T>
+__device__ __forceinline__ float widen16(unsigned int bits) {
+    if constexpr (std::is_same<T, __half>::value)
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+    else
+        return __uint_as_float(bits << 16);
+}
+
+// sum_h x[h] w[h] over the lanes of a warp (every lane gets it).
+template <class T>
+__device__ __forceinline__ float warp_dot(const unsigned short *x, const unsigned short *w, int n,
+                                          int lane) {
+    float t = 0.0f;
+    if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15) == 0) {
+        const int vectors = n / 8;
+#pragma unroll 4
+        for (int i = lane; i < vectors; i += 32) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x) + i);
+            const uint4 b = __ldg(reinterpret_cast<const uint4 *>(w) + i);
+            const unsigned int p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                t = fmaf(widen16<T>(p[j] & 0xffffu), widen16<T>(q[j] & 0xffffu), t);
+                t = fmaf(widen16<T>(p[j] >> 16), widen16<T>(q[j] >> 16), t);
+            }
+        }
+        x += vectors * 8;
+        w += vectors * 8;
+        n -= vectors * 8;
+    }
+    for (int i = lane; i < n; i += 32) t = fmaf(widen16<T>(x[i]), widen16<T>(w[i]), t);
+    for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+    return t;
+}
+
 // ---- packing rows ----------------------------------------------------------------------
 
 struct PackArgs {
-    const unsigned short *x, *weight;   // weight NULL: only x
+    const unsigned short *x, *weight;
     const long long *target;
     const float *lse, *dloss;           // NULL in a forward call
     long long ignore;
     int rows, width, vocab, ld;
-    int scaled;                         // FP16: gradients by 2^15
-    int row_ctas;                       // CTAs that pack x; the others copy the weight
+    int bf16;                           // FP16: gradients are scaled by 2^15
+    int row_ctas;                       // CTAs that pack x; the others copy the weight (to pw)
     int cta_rows;                       // rows of a CTA that packs x
     unsigned short *px, *pw;
     CeState *state;
     int *place, *ptarget;
-    float *plse2, *pdloss;
+    float *plse2, *pmiss, *pdloss;
     unsigned int *status;
 };
 
@@ -741,7 +807,7 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
     }
     // 32768 / top and top / 32768 are finite and not 0 for any normal top
     top = fminf(fmaxf(top, 1e-30f), 1e30f);
-    const float full = a.scaled ? 32768.0f : 1.0f;
+    const float full = a.bf16 ? 1.0f : 32768.0f;
     if (blockIdx.x == 0 && tid == 0) {
         a.state->valid = valid;
         a.state->unscale = top / full;
@@ -761,8 +827,8 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
                 a.place[i] = in ? at : -1;
                 if (t != a.ignore && (t < 0 || t >= a.vocab)) atomicOr(a.status, CE_BAD_TARGET);
             }
+            if (in) a.ptarget[at] = static_cast<int>(t);
             if (in && a.dloss != nullptr) {
-                a.ptarget[at] = static_cast<int>(t);
                 a.plse2[at] = a.lse[i] * kLog2e;
                 a.pdloss[at] = full * (dl / top);
             }
@@ -771,9 +837,15 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
         for (int q = warp; q < 32; q += 8) {
             const int i = c + q, at = row_at[q];
             if (i >= r1) break;
+            const unsigned short *x = a.x + static_cast<long long>(i) * a.width;
             if (at >= 0)
-                copy_row16(a.x + static_cast<long long>(i) * a.width,
-                           a.px + static_cast<long long>(at) * a.ld, a.width, a.ld, 32);
+                copy_row16(x, a.px + static_cast<long long>(at) * a.ld, a.width, a.ld, 32);
+            if (at >= 0 && a.dloss != nullptr) {
+                const unsigned short *w = a.weight + a.target[i] * a.width;
+                const float l = a.bf16 ? warp_dot<__nv_bfloat16>(x, w, a.width, lane)
+                                       : warp_dot<__half>(x, w, a.width, lane);
+                if (lane == 0) a.pmiss[at] = expm1f(l - a.lse[i]);
+            }
             if (i >= valid)
                 copy_row16(nullptr, a.px + static_cast<long long>(i) * a.ld, 0, a.ld, 32);
         }
@@ -783,43 +855,8 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
 
 // ---- forward: joining the tiles --------------------------------------------------
 
-template <class T>
-__device__ __forceinline__ float widen16(unsigned int bits) {
-    if constexpr (std::is_same<T, __half>::value)
-        return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
-    else
-        return __uint_as_float(bits << 16);
-}
-
-// sum_h x[h] w[h] over the lanes of a warp (every lane gets it).
-template <class T>
-__device__ __forceinline__ float warp_dot(const unsigned short *x, const unsigned short *w, int n,
-                                          int lane) {
-    float t = 0.0f;
-    if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15) == 0) {
-        const int vectors = n / 8;
-#pragma unroll 4
-        for (int i = lane; i < vectors; i += 32) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x) + i);
-            const uint4 b = __ldg(reinterpret_cast<const uint4 *>(w) + i);
-            const unsigned int p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                t = fmaf(widen16<T>(p[j] & 0xffffu), widen16<T>(q[j] & 0xffffu), t);
-                t = fmaf(widen16<T>(p[j] >> 16), widen16<T>(q[j] >> 16), t);
-            }
-        }
-        x += vectors * 8;
-        w += vectors * 8;
-        n -= vectors * 8;
-    }
-    for (int i = lane; i < n; i += 32) t = fmaf(widen16<T>(x[i]), widen16<T>(w[i]), t);
-    for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
-    return t;
-}
-
 struct JoinArgs {
-    const float2 *partial;
+    const float2 *partial;              // exponents of 2
     const unsigned short *x, *weight;   // as they were multiplied
     long long x_ld, weight_ld;
     const long long *target;
@@ -861,16 +898,25 @@ __global__ void __launch_bounds__(128) join_lse_kernel(const JoinArgs a) {
     for (int i = lane; i < a.partials; i += 32) m = fmaxf(m, p[i].x);
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float ref = m == -INFINITY ? 0.0f : m;
-    float s = 0.0f;
+    float s = 0.0f;   // sum over the other entries of 2^(l_v log2(e) - ref)
     for (int i = lane; i < a.partials; i += 32) {
         const float2 q = p[i];
-        s += q.y * expf(q.x - ref);
+        s += q.y * exp2f(q.x - ref);
     }
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const float log_s = logf(s);
     if (lane != 0) return;
-    a.lse[row] = m + log_s;
-    a.loss[row] = (m - l) + log_s;   // m - l is exact where they are close
+    // log(1 + sum exp(l_v - l)), from the larger of the two exponents; the
+    // first where there is no other entry (or none above -infinity: s is 0)
+    const float d = fmaf(l, kLog2e, -m);
+    if (!(d < 0.0f)) {
+        const float log_s = log1pf(s == 0.0f ? 0.0f : s * exp2f(-d));
+        a.lse[row] = l + log_s;
+        a.loss[row] = (l - l) + log_s;   // (NaN for an infinite logit)
+    } else {
+        const float log_s = log2f(s + exp2f(d));
+        a.lse[row] = kLn2 * (ref + log_s);
+        a.loss[row] = kLn2 * (log_s - d);
+    }
 }
 
 // ---- backward: the end ----------------------------------------------------------------
@@ -1039,7 +1085,7 @@ bool forward_packs(int rows, int width, int vocab) {
 
 struct ForwardSpace {
     CeState *state;
-    int *place;
+    int *place, *ptarget;
     unsigned short *x, *w;
     float2 *partial;
     size_t bytes;
@@ -1073,6 +1119,7 @@ ForwardSpace forward_space(void *ws, int rows, int width, int vocab) {
     if (forward_packs(rows, width, vocab)) {
         s.state = c.take<CeState>(1);
         s.place = c.take<int>(rows);
+        s.ptarget = c.take<int>(rows);
         s.x = c.take<unsigned short>(rows * ld);
         if (odd_rows(width)) s.w = c.take<unsigned short>(vocab * ld);
     }
@@ -1103,7 +1150,7 @@ int splits_of(int rows, int width, int vocab) {
 struct BackwardSpace {
     CeState *state;
     int *place, *ptarget;
-    float *plse2, *pdloss;
+    float *plse2, *pmiss, *pdloss;
     int pieces;
     unsigned short *x, *w, *grad;
     float *acc;
@@ -1119,6 +1166,7 @@ BackwardSpace backward_space(void *ws, int rows, int width, int vocab) {
     s.place = c.take<int>(rows);
     s.ptarget = c.take<int>(rows);
     s.plse2 = c.take<float>(rows);
+    s.pmiss = c.take<float>(rows);
     s.pdloss = c.take<float>(rows);
     s.x = c.take<unsigned short>(rows * ld);
     s.w = odd_rows(width) ? c.take<unsigned short>(vocab * ld) : nullptr;
@@ -1135,7 +1183,7 @@ cudaError_t launch_pack(PackArgs p, cudaStream_t stream) {
     p.cta_rows = p.rows <= 8192 ? 8 : static_cast<int>(up((p.rows + 1023) / 1024, 32));
     p.row_ctas = (p.rows + p.cta_rows - 1) / p.cta_rows;
     int weight_ctas = 0;
-    if (p.weight != nullptr) {
+    if (p.pw != nullptr) {
         weight_ctas = sm_count_of_device() * 8;
         if (weight_ctas > (p.vocab + 7) / 8) weight_ctas = (p.vocab + 7) / 8;
     }
@@ -1174,7 +1222,7 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
     if (packs) {
         PackArgs p = {};
         p.x = static_cast<const unsigned short *>(x);
-        p.weight = odd_rows(width) ? static_cast<const unsigned short *>(w) : nullptr;
+        p.weight = static_cast<const unsigned short *>(w);
         p.target = args.target;
         p.ignore = args.ignore;
         p.rows = rows;
@@ -1186,6 +1234,7 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
         p.pw = s.w;
         p.state = s.state;
         p.place = s.place;
+        p.ptarget = s.ptarget;
         p.status = status;
         CE_TRY(launch_pack(p, stream));
         x = s.x;
@@ -1200,6 +1249,8 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
     g.job[0] = {rows, vocab, width, bn, rows_of_a(rows), 1, 16, nullptr, 0, 0};
     g.state = packs ? s.state : nullptr;
     g.partial = s.partial;
+    g.target = args.target;
+    g.ptarget = packs ? s.ptarget : nullptr;
     g.status = status;
     CE_TRY(make_map(&maps.a[0], bf16, x, rows, width, x_ld, g.job[0].a_rows));
     CE_TRY(make_map(&maps.b[0], bf16, w, vocab, width, w_ld, bn / 2));
@@ -1225,7 +1276,7 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
     const unsigned short *w = static_cast<const unsigned short *>(args.weight);
     PackArgs p = {};
     p.x = static_cast<const unsigned short *>(args.x);
-    p.weight = odd_rows(width) ? w : nullptr;
+    p.weight = w;
     p.target = args.target;
     p.lse = args.lse;
     p.dloss = args.dloss;
@@ -1234,13 +1285,14 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
     p.width = width;
     p.vocab = vocab;
     p.ld = static_cast<int>(ld);
-    p.scaled = !bf16;
+    p.bf16 = bf16;
     p.px = s.x;
     p.pw = s.w;
     p.state = s.state;
     p.place = s.place;
     p.ptarget = s.ptarget;
     p.plse2 = s.plse2;
+    p.pmiss = s.pmiss;
     p.pdloss = s.pdloss;
     p.status = status;
     CE_TRY(launch_pack(p, stream));
@@ -1260,6 +1312,7 @@ cudaError_t launch_linear_ce_backward(const LinearCeArgs &args, cudaStream_t str
     g.status = status;
     g.ptarget = s.ptarget;
     g.plse2 = s.plse2;
+    g.pmiss = s.pmiss;
     g.pdloss = s.pdloss;
     g.slice = up(rows, BM) * acc_ld;
     for (int i = 0; i < s.pieces; ++i) {
