@@ -33,15 +33,19 @@ TILE_DEVICE_STATUS(block_norm_backward)
 namespace tile {
 namespace {
 
-// Programs of a call: at most this many, each of at least four rows where
-// there are more rows than SMs.
-constexpr int kMaxUnits = 1024;
+// Programs of a call: at most this many (their column sums are a few bytes of
+// a wide row's, so there may be as many as run at once; the workspace of
+// narrow rows stays below 40 MiB), each of at least four rows where there are
+// more rows than SMs.
+constexpr int kNarrow = 1024;   // columns
 
-long long units_of(long long rows, int slots) {
-    long long u = rows / 4 > slots ? slots : rows;
+int most_units(int width) { return width <= kNarrow ? 2432 : 1024; }
+
+long long units_of(const BlockArgs &a, long long slots) {
+    long long u = a.rows / 4 > slots ? slots : a.rows;
     const long long sms = 152;
-    if (rows / 4 <= slots && u > sms) u = rows / 4 > sms ? rows / 4 : sms;
-    if (u > kMaxUnits) u = kMaxUnits;
+    if (a.rows / 4 <= slots && u > sms) u = a.rows / 4 > sms ? a.rows / 4 : sms;
+    if (u > most_units(a.width)) u = most_units(a.width);
     return u < 1 ? 1 : u;
 }
 
@@ -200,37 +204,70 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockArg
 
 // Joins the programs' column sums, in program order: blockIdx.y 0 and 1 the
 // gamma gradients, the others the gate rows that more than one program
-// holds.  A CTA sums 32 columns with 32 threads each, over 32 contiguous
-// runs of programs, joined in order.  per_gate_units: programs of a gate row
-// where programs keep to one, else 0 (contiguous ranges of rows).
-constexpr int kJoinCols = 32, kJoinRuns = 32;
+// holds.  A CTA sums COLS columns over RUNS contiguous runs of programs,
+// joined in order, with a thread for V columns of a run: four where the width
+// allows (4096 x 8192 FP32, sums not in cache: 8.5 us, 15 with a thread a
+// column).  Rows of up to kNarrow columns have few columns and many programs:
+// 8 columns and 128 runs to a CTA.  per_gate_units:
+// programs of a gate row where programs keep to one, else 0 (contiguous
+// ranges of rows).
+template <int V>
+struct Columns {
+    float v[V];
+};
+template <int V>
+__device__ __forceinline__ Columns<V> load_columns(const float *p) {
+    Columns<V> r;
+    if constexpr (V == 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(p);
+        r = {{q.x, q.y, q.z, q.w}};
+    } else {
+        r.v[0] = *p;
+    }
+    return r;
+}
 
-__global__ void __launch_bounds__(kJoinCols *kJoinRuns)
+template <int V, int COLS, int RUNS>
+__global__ void __launch_bounds__(COLS / V *RUNS)
     block_norm_join_kernel(const BlockArgs a, long long units, long long gates,
                            int per_gate_units) {
-    __shared__ float run_sum[kJoinRuns][kJoinCols];
-    const int c = threadIdx.x % kJoinCols, run = threadIdx.x / kJoinCols;
-    const int col = blockIdx.x * kJoinCols + c;
+    constexpr int LANES = COLS / V;
+    __shared__ Columns<V> run_sum[RUNS][LANES];
+    const int c = threadIdx.x % LANES, run = threadIdx.x / LANES;
+    const int col = blockIdx.x * COLS + c * V;
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are written
     // sum of slot `slot0` of unit u0 and slot `slot` of the units after it
     auto join = [&](long long u0, long long u1, int slot0, int slot) {
         const long long n = u1 - u0 + 1;
-        float t = 0.0f;
+        Columns<V> t = {};
         if (col < a.width) {
             const float *p = a.ws + (u0 * SLOTS + slot) * a.width + col;
             const long long step = static_cast<long long>(SLOTS) * a.width;
-            const int from = static_cast<int>(n * run / kJoinRuns);
-            const int to = static_cast<int>(n * (run + 1) / kJoinRuns);
-#pragma unroll 8
-            for (int u = from; u < to; ++u)
-                t += u == 0 ? p[static_cast<long long>(slot0 - slot) * a.width] : p[u * step];
+            int u = static_cast<int>(n * run / RUNS);
+            const int to = static_cast<int>(n * (run + 1) / RUNS);
+            if (u == 0 && to > 0) {
+                t = load_columns<V>(p + static_cast<long long>(slot0 - slot) * a.width);
+                u = 1;
+            }
+            for (; u < to; u += 8) {   // eight loads at once
+                Columns<V> q[8] = {};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (u + j < to) q[j] = load_columns<V>(p + (u + j) * step);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) t.v[i] += q[j].v[i];
+            }
         }
         run_sum[run][c] = t;
         __syncthreads();
-        t = 0.0f;
+        t = {};
         if (run == 0)
 #pragma unroll
-            for (int i = 0; i < kJoinRuns; ++i) t += run_sum[i][c];
+            for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+                for (int i = 0; i < V; ++i) t.v[i] += run_sum[r][c].v[i];
         __syncthreads();
         return t;   // (run 0's)
     };
@@ -238,8 +275,10 @@ __global__ void __launch_bounds__(kJoinCols *kJoinRuns)
         float *to = blockIdx.y == 0 ? a.dgamma_pre : a.dgamma_post;
         const int slot = blockIdx.y == 0 ? SLOT_PRE : SLOT_POST;
         if (to == nullptr) return;
-        const float t = join(0, units - 1, slot, slot);
-        if (run == 0 && col < a.width) to[col] = t;
+        const Columns<V> t = join(0, units - 1, slot, slot);
+        if (run == 0 && col < a.width)
+#pragma unroll
+            for (int i = 0; i < V; ++i) to[col + i] = t.v[i];
         return;
     }
     for (long long g = blockIdx.y - 2; g < gates; g += gridDim.y - 2) {
@@ -254,11 +293,13 @@ __global__ void __launch_bounds__(kJoinCols *kJoinRuns)
             // the first of every other program
             if (a.rows * u0 / units < g * a.per_gate) slot0 = SLOT_LAST;
         }
-        const float t = join(u0, u1, slot0, SLOT_FIRST);
-        if (run == 0 && col < a.width) {
-            const float p = a.gamma_post != nullptr ? a.gamma_post[col] : 1.0f;
-            a.dgate[g * a.width + col] = p * t;
-        }
+        const Columns<V> t = join(u0, u1, slot0, SLOT_FIRST);
+        if (run == 0 && col < a.width)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float p = a.gamma_post != nullptr ? a.gamma_post[col + i] : 1.0f;
+                a.dgate[g * a.width + col + i] = p * t.v[i];
+            }
     }
 }
 
@@ -328,10 +369,10 @@ cudaError_t launch_ring(const BlockArgs &a, RingPlan p, cudaStream_t stream, Pro
     if (err != cudaSuccess) return err;
     const long long room = static_cast<long long>(sm_count_of_device()) * per_sm / p.cluster;
     if (p.classes == 1) {
-        *out = {units_of(a.rows, room), 0};
+        *out = {units_of(a, room), 0};
     } else {
         const long long gates = (a.rows + a.per_gate - 1) / a.per_gate;
-        long long parts = units_of(a.rows, room) / (gates * p.classes);
+        long long parts = units_of(a, room) / (gates * p.classes);
         p.parts = parts < 1 ? 1 : static_cast<int>(parts);
         *out = {gates * p.classes * p.parts, p.classes * p.parts};
     }
@@ -362,7 +403,7 @@ cudaError_t launch_registers(const BlockArgs &a, cudaStream_t stream, Programs *
         occupancy(block_norm_backward_kernel<T, V, E / V, CL>, cache, threads, 0, &per_sm);
     if (err != cudaSuccess) return err;
     const long long room = static_cast<long long>(sm_count_of_device()) * per_sm / cluster;
-    *out = {units_of(a.rows, room), 0};
+    *out = {units_of(a, room), 0};
     return launch_programs(block_norm_backward_kernel<T, V, E / V, CL>, a, cluster, out->units,
                            threads, cluster, 0, stream);
 }
@@ -379,18 +420,36 @@ cudaError_t launch_typed(const BlockArgs &a, BlockAccess access, cudaStream_t st
     if (access == ACCESS_SHIFTED) {
         const RingPlan p = ring_plan<T, true>(a.width);
         const long long gates = (a.rows + a.per_gate - 1) / a.per_gate;
-        if (p.cluster > 0 && (p.classes == 1 || gates * p.classes <= kMaxUnits))
+        if (p.cluster > 0 && (p.classes == 1 || gates * p.classes <= most_units(a.width)))
             return launch_ring_typed<T, true>(a, p, stream, out);
     }
     if (a.width <= 512 * 16) return launch_registers<T, 1, 16, false>(a, stream, out);
     return launch_registers<T, 1, 32, true>(a, stream, out);
 }
 
+// Launched while the programs run (it waits for their end itself).
+template <int V, int COLS, int RUNS>
+cudaError_t launch_join(const BlockArgs &a, const Programs &programs, long long gates,
+                        cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.width + COLS - 1) / COLS,
+                       2 + static_cast<unsigned>(gates < 1024 ? gates : 1024));
+    cfg.blockDim = dim3(COLS / V * RUNS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, block_norm_join_kernel<V, COLS, RUNS>, a, programs.units, gates,
+                              programs.per_gate);
+}
+
 }  // namespace
 
 size_t block_norm_backward_workspace(long long rows, int width) {
     // programs that keep to a row class of a gate row may be more than rows
-    const long long units = 8 * rows < kMaxUnits ? 8 * rows : kMaxUnits;
+    const long long units = 8 * rows < most_units(width) ? 8 * rows : most_units(width);
     return static_cast<size_t>(units) * SLOTS * static_cast<size_t>(width) * sizeof(float);
 }
 
@@ -410,19 +469,12 @@ cudaError_t launch_block_norm_backward(int elem, BlockAccess access, const Block
     if (err != cudaSuccess) return err;
     const long long gates = a.dgate != nullptr ? (a.rows + a.per_gate - 1) / a.per_gate : 0;
     if (a.dgamma_pre == nullptr && a.dgamma_post == nullptr && gates == 0) return cudaSuccess;
-    // launched while the programs run (it waits for their end itself)
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.width + kJoinCols - 1) / kJoinCols,
-                       2 + static_cast<unsigned>(gates < 1024 ? gates : 1024));
-    cfg.blockDim = dim3(kJoinCols * kJoinRuns);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, block_norm_join_kernel, a, programs.units, gates,
-                              programs.per_gate);
+    const bool fours = a.width % 4 == 0;   // (the workspace is on 16 bytes)
+    if (a.width <= kNarrow)
+        return fours ? launch_join<4, 8, 128>(a, programs, gates, stream)
+                     : launch_join<1, 8, 128>(a, programs, gates, stream);
+    return fours ? launch_join<4, 32, 32>(a, programs, gates, stream)
+                 : launch_join<1, 32, 32>(a, programs, gates, stream);
 }
 
 }  // namespace tile
