@@ -431,6 +431,10 @@ int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *
  *   loss[i] = lse[i] - l_target[i]
  *
  * Both FP32 [rows]; a row whose target is ignore_index gets loss = lse = 0.
+ * The loss is log(1 + sum over the other entries of exp(l_v - l_target)) with
+ * the target's logit as an FP32 sum, so it is never negative and small losses
+ * keep their digits; the other logits' sums are truncated as they grow (the
+ * tensor cores'), with the mean of it put back.
  * dtype: TILE_DTYPE_BF16 or TILE_DTYPE_F16 of in and weight ([vocab][width]);
  * the products of 16-bit elements are exact, and every sum is FP32.  (FP32
  * operands are refused with TILE_ERR_DTYPE: the tensor cores would round
@@ -464,10 +468,11 @@ int tile_linear_cross_entropy(int dtype, const void *in, const void *weight,
  * whatever they hold; so do rows with a target out of range, which set the
  * device status word.
  *
- * g is made in pieces of the vocabulary (a workspace of at most about
- * 512 MiB, or 4096 columns) and held in 16 bits for one piece: dtype
- * values rounded once, FP16 ones after scaling by a power of two taken from
- * the largest |dloss|.  Sums are FP32, din and dweight rounded once.  No
+ * g is made in pieces of the vocabulary (at most about 512 MiB of the
+ * workspace, or 4096 columns; an FP32 din and a copy of in come to that) and
+ * held in 16 bits for one piece: dtype
+ * values of (p - onehot) dloss / max |dloss| rounded once, FP16 ones of 2^15
+ * times that.  Sums are FP32, din and dweight rounded once.  No
  * atomics: results are bitwise reproducible.  rows == 0 writes a zero
  * dweight. */
 size_t tile_linear_cross_entropy_backward_workspace_bytes(int rows, int width, int vocab);

@@ -295,7 +295,12 @@ __device__ __forceinline__ void store_rows16(unsigned short *out, long long ld, 
 // the other into the epilogue's output.  A pair reads 32 KiB per CTA and 64
 // columns of K from L2, where a CTA with a tile of its own reads 48: L2
 // delivers some 12.5 TB/s, which bound the gradients' products with single
-// CTAs (56 % of the tensor cores' time in use).
+// CTAs (56 % of the tensor cores' time in use).  At 4096 tokens x 4096 columns
+// x 32768 entries in BF16 the tensor cores work 94 % of the time for the
+// logits (0.53 ms), 91 % for g (0.56 ms) and 88 % for dx and dW (1.19 ms): the
+// clock under the power limit is what bounds long calls.  A few rows against a
+// large weight are bound by reading it (5 x 2048 x 32768: 29 us, 20 at the
+// rate of a copy); their backward reads it twice.
 //
 // With two jobs the tiles of the first come first; they are long (their
 // reduction is the piece of the vocabulary) and few, 256 of them over 76
