@@ -347,6 +347,58 @@ def test_rows_behind_are_left_as_they_were():
         check(grads[1:9], *ref["dgate"], 400, "dgate")
 
 
+# as many programs as run at once (rows / 4 and more), row classes among them,
+# column sums over all of them
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("rows,width,gate", [(30000, 64, 700), (20001, 257, 9000), (12000, 1001, 0),
+                                             (11000, 1024, 11000), (9999, 1028, 5)])
+def test_many_rows(rows, width, gate, kind):
+    s = make(rows, width, kind, gate, seed=4)
+    hidden, out = tile.block_norm(s["x"], s["residual"], s["gamma_post"], s["gate"], s["gamma_pre"],
+                                  rows_per_gate=gate)
+    h, hm, y, ym = reference(s, True, True, gate, 1.0, 1e-5)
+    check(hidden, h, hm, 64, "hidden")
+    check(out, y, ym, 128, "out")
+    got = dict(zip(("din", "dresidual", "dgamma_post", "dgate", "dgamma_pre"),
+                   tile.block_norm_backward(s["x"], hidden, s["gamma_post"], s["gate"],
+                                            s["gamma_pre"], s["dhidden"], s["dout"],
+                                            rows_per_gate=gate)))
+    for name, (ref, mag) in reference_backward(s, hidden, True, True, gate, 1.0, 1e-5).items():
+        # a column's sum has at most rows / 600 + 160 additions in a chain
+        check(got[name], ref, mag, 400, name)
+    assert tile.tile_check_device_status() == 0
+
+
+@pytest.mark.parametrize("width", [16384, 16383])
+def test_past_two_to_the_31_elements(width):
+    """Rows below and above element 2^31, each against FP64; the gradients'
+    rows that are not looked at are zero, so column sums are those of the
+    rows that are."""
+    rows = (1 << 31) // width + 1000
+    look = torch.tensor([0, 1, (1 << 31) // width, (1 << 31) // width + 1, rows - 2, rows - 1],
+                        device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    few = make(len(look), width, "bf16", 0, seed=9)
+    few["gate"] = torch.randn(1, width, device="cuda", generator=gen)
+    big = {}
+    for name in ("x", "residual", "dhidden", "dout"):
+        big[name] = torch.zeros(rows, width, dtype=torch.bfloat16, device="cuda")
+        big[name][look] = few[name]
+    args = few["gamma_post"], few["gate"], few["gamma_pre"]
+    hidden, out = tile.block_norm(big["x"], big["residual"], *args)
+    h, hm, y, ym = reference(few, True, True, len(look), 1.0, 1e-5)
+    check(hidden[look], h, hm, 64, "hidden")
+    check(out[look], y, ym, 128, "out")
+    del out, big["residual"]
+    names = "din", "dresidual", "dgamma_post", "dgate", "dgamma_pre"
+    got = dict(zip(names, tile.block_norm_backward(big["x"], hidden, *args, big["dhidden"],
+                                                   big["dout"])))
+    ref = reference_backward(few, hidden[look], True, True, len(look), 1.0, 1e-5)
+    for name in names:
+        check(got[name][look] if name in ("din", "dresidual") else got[name], *ref[name], 400, name)
+    assert tile.tile_check_device_status() == 0
+
+
 def test_agrees_with_the_weighted_rmsnorm():
     """Without a block norm and with a zero residual the block norm is the
     library's weighted RMSNorm."""

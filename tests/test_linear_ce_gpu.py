@@ -361,6 +361,67 @@ def test_rows_behind_are_left_as_they_were():
     check_gradients(x, weight, target, losses[1, :37], dloss, big[:37], wbig[:300])
 
 
+@pytest.mark.parametrize("rows,width,vocab", [(6, 4096, 530000), (6, 4095, 530000),
+                                              (600000, 4096, 140), (530000, 64, 4100)])
+def test_past_two_to_the_31_elements(rows, width, vocab):
+    """A weight, a copy of it, an x and a piece's gradients of more than 2^31
+    elements: the loss of every row, dx of the last rows and dweight of the
+    last entries (and of some targets) against FP64, in blocks."""
+    assert max(rows, vocab) * width > 1 << 31 or rows * 4096 > 1 << 31
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    weight = torch.empty(vocab, width, dtype=torch.bfloat16, device="cuda")
+    weight.normal_(0.0, 1.5 / width ** 0.5, generator=gen)
+    target = torch.randint(vocab, (rows,), device="cuda", generator=gen)
+    target[-2:] = vocab - 1
+    x = torch.empty(rows, width, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=gen)
+    dloss = torch.rand(rows, device="cuda", generator=gen) + 0.5
+    loss, lse = tile.linear_cross_entropy(x, weight, target)
+    dx, dweight = tile.linear_cross_entropy_backward(x, weight, target, lse, dloss)
+    last = torch.arange(max(0, rows - 40), rows, device="cuda")
+    cols = torch.cat([torch.arange(max(0, vocab - 40), vocab, device="cuda"), target[:5]]).unique()
+    dw = torch.zeros(len(cols), width, dtype=torch.float64, device="cuda")
+    dw_sq = torch.zeros_like(dw)
+    for r0 in range(0, rows, 30000):
+        r1 = min(rows, r0 + 30000)
+        xr, t = x[r0:r1].double(), target[r0:r1]
+        parts, top = [], []
+        for v0 in range(0, vocab, 60000):
+            l = xr @ weight[v0:v0 + 60000].double().t()
+            parts.append(torch.logsumexp(l, 1))
+            top.append(l.abs().amax(1))
+        want_lse = torch.logsumexp(torch.stack(parts), 0)
+        at = (xr * weight[t].double()).sum(1)
+        # |x w| sums below 1.5 sqrt(width) 8, in place of each logit's own
+        tol = sum_error(width) * 1.5 * 8 * width ** 0.5 + 2.0 ** -17
+        assert ((lse[r0:r1] - want_lse).abs() <= tol + 2.0 ** -23 * want_lse.abs()).all()
+        assert ((loss[r0:r1] - (want_lse - at)).abs() <= 2 * tol + 2.0 ** -22 * want_lse.abs()).all()
+        g = torch.exp(xr @ weight[cols].double().t() - lse[r0:r1, None].double())
+        g -= (t[:, None] == cols).double()
+        g *= dloss[r0:r1, None].double()
+        dw += g.t() @ xr
+        dw_sq += g.square().t() @ xr.square()
+    half = 2.0 ** -8
+    # each of the n terms is rounded to half a step on its own: their errors
+    # add like the root of their squares (within 8 times that), on top of
+    # sum_error of the whole and the output's own rounding
+    tol = half * dw.abs() + 8 * half * dw_sq.sqrt() + sum_error(rows) * dw_sq.sqrt() * rows ** 0.5
+    assert ((dweight[cols].double() - dw).abs() <= tol).all()
+    want = torch.zeros(len(last), width, dtype=torch.float64, device="cuda")
+    want_sq = torch.zeros_like(want)
+    for v0 in range(0, vocab, 60000):
+        w = weight[v0:v0 + 60000].double()
+        g = torch.exp(x[last].double() @ w.t() - lse[last, None].double())
+        g -= (target[last, None] == torch.arange(v0, v0 + len(w), device="cuda")).double()
+        g *= dloss[last, None].double()
+        want += g @ w
+        want_sq += g.square() @ w.square()
+    tol = half * want.abs() + 8 * half * want_sq.sqrt() + \
+        sum_error(vocab) * want_sq.sqrt() * vocab ** 0.5
+    assert ((dx[last].double() - want).abs() <= tol).all()
+    assert tile.tile_check_device_status() == 0
+
+
 def test_end_of_a_training_step():
     """Block norm, loss and both backward passes as a training step runs
     them: the last block's hidden rows are scored, and the gradients reach
