@@ -351,7 +351,11 @@ def test_rows_behind_are_left_as_they_were():
 # column sums over all of them
 @pytest.mark.parametrize("kind", list(TYPES))
 @pytest.mark.parametrize("rows,width,gate", [(30000, 64, 700), (20001, 257, 9000), (12000, 1001, 0),
-                                             (11000, 1024, 11000), (9999, 1028, 5)])
+                                             (11000, 1024, 11000), (9999, 1028, 5),
+                                             # and rows split between CTAs
+                                             (700, 5120, 9), (900, 5111, 0), (500, 6152, 500),
+                                             (300, 9224, 20), (310, 12288, 0), (260, 14600, 7),
+                                             (170, 20480, 3), (90, 32768, 0)])
 def test_many_rows(rows, width, gate, kind):
     s = make(rows, width, kind, gate, seed=4)
     hidden, out = tile.block_norm(s["x"], s["residual"], s["gamma_post"], s["gate"], s["gamma_pre"],

@@ -316,16 +316,25 @@ RingPlan ring_plan(int width) {
     // vectors that hold a row, wherever it starts
     const int vecs = (width + (SHIFT ? N - 1 : 0) + N - 1) / N;
     // (CTAs of 512 threads, one to an SM, before clusters: 8192 x 8192 BF16
-    // took 177 us in clusters of two, two CTAs to an SM, and 149 us so)
+    // took 177 us in clusters of two, two CTAs to an SM, and 149 us so; 4096 x
+    // 16384 283 us in clusters of four and 183 us so)
     int c = 1;
     while (c <= 8 && (vecs + c - 1) / c > 512 * K) c *= 2;
+    // But a single CTA of 288 or 320 threads leaves the registers for a second
+    // one unused (13000 x 5120 BF16: 185 us, 174 us as a cluster of two of 160
+    // threads, three to an SM), and four CTAs of one to an SM take longer than
+    // eight smaller ones (2048 x 32768 BF16: 348 us and 291 us), except where
+    // the masks of shifted rows come twice as often (2000 x 20001: 239 us and
+    // 260 us).
+    if (N == 8 && c == 1 && vecs > 256 * K && vecs <= 320 * K) c = 2;
+    if (c == 4 && !SHIFT) c = 8;
     if (c > 8) return p;
     p.cluster = c;
     p.workers = ((vecs + c - 1) / c + 32 * K - 1) / (32 * K) * 32;
     p.pitch = (c == 1 ? vecs : p.workers * K) * 16;
     // as many CTAs to an SM as registers allow, the ring cut to fit
     int per_sm = 65536 / (p.workers * 128);
-    if (p.workers == 288 || p.workers == 320) per_sm = 2;   // (96 registers)
+    if (N == 4 && (p.workers == 288 || p.workers == 320)) per_sm = 2;   // (up to 92 registers)
     per_sm = per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm;
     p.slots = ((224 << 10) / per_sm - (3 << 10)) / (4 * p.pitch);
     p.slots = p.slots > kRingMost ? kRingMost : p.slots;
@@ -386,9 +395,12 @@ cudaError_t launch_ring_typed(const BlockArgs &a, const RingPlan &p, cudaStream_
     if (p.workers <= 256)
         return one ? launch_ring<T, SHIFT, false, 256, 2>(a, p, stream, out)
                    : launch_ring<T, SHIFT, true, 256, 2>(a, p, stream, out);
-    if (p.workers <= 320)
-        return one ? launch_ring<T, SHIFT, false, 320, 2>(a, p, stream, out)
-                   : launch_ring<T, SHIFT, true, 320, 2>(a, p, stream, out);
+    // FP32 rows keep half as many columns in a thread's registers (2-byte ones
+    // spilled here: 13000 x 5120 BF16 238 us)
+    if constexpr (sizeof(T) == 4)
+        if (p.workers <= 320)
+            return one ? launch_ring<T, SHIFT, false, 320, 2>(a, p, stream, out)
+                       : launch_ring<T, SHIFT, true, 320, 2>(a, p, stream, out);
     return one ? launch_ring<T, SHIFT, false, 512, 1>(a, p, stream, out)
                : launch_ring<T, SHIFT, true, 512, 1>(a, p, stream, out);
 }

@@ -369,17 +369,26 @@ cudaError_t launch_kernel(const BlockArgs &a, int cluster, cudaStream_t stream) 
 }
 
 // 32 two-byte or 16 FP32 columns a thread, up to 512 threads a row, then a
-// cluster of up to 8 CTAs, then 32 columns of either.  (16 two-byte columns a
-// thread from 8192 columns on, in a cluster of two from 16384 on, took 177 us
-// where 32 take 126, at 4096 x 16384.)
+// cluster of up to 8 CTAs, then 32 columns of either.  Two-byte rows of whole
+// vectors take CTAs that leave room for three on an SM where there are 128 to
+// 256 threads (80 registers, nothing spilled: 8192 x 8192 BF16 92 us, 105 us
+// with two) and in clusters of them (2048 x 32768 153 us, 194 us with CTAs of
+// 512 threads), but one CTA of 512 where that is full (4096 x 16384 138 us,
+// 144 us as a cluster of two).
 template <class T, int V>
 cudaError_t launch_rows(const BlockArgs &a, cudaStream_t stream) {
     constexpr int E = V == 8 ? 32 : 16;
     constexpr int MINB = V == 8 ? 1 : 2;   // 64 registers for 16 columns
-    // 96 for 32, as long as that leaves room for two CTAs or more (with 128,
-    // 16384 x 4096 BF16 took 107 us instead of 88)
-    if constexpr (V == 8)
+    // 96 for 32 up to 128 threads and where three CTAs do not fit (with 128
+    // registers 16384 x 4096 BF16 took 107 us instead of 88)
+    if constexpr (V == 8) {
+        if (a.width > 128 * E && a.width <= 256 * E)
+            return launch_kernel<T, V, E, false, 256, 3>(a, 1, stream);
         if (a.width <= 320 * E) return launch_kernel<T, V, E, false, 320, 2>(a, 1, stream);
+        for (int c = 2; c <= 8; c *= 2)
+            if (a.width <= 256 * E * c && (a.width <= 448 * E || a.width > 512 * E))
+                return launch_kernel<T, V, E, true, 256, 3>(a, c, stream);
+    }
     if (a.width <= 512 * E) return launch_kernel<T, V, E, false, 512, MINB>(a, 1, stream);
     for (int c = 2; c <= 8; c *= 2)
         if (a.width <= 512 * E * c) return launch_kernel<T, V, E, true, 512, MINB>(a, c, stream);

@@ -20,7 +20,7 @@
 //
 // Bound by memory from 4096 columns on (32768 x 4096 BF16 267 us, 6.0 TB/s),
 // by the latency of a row's reduction below (8192 x 256 23 us), and with SHIFT
-// by instruction issue (16384 x 4097 BF16 325 us: the masks and the stores by
+// by instruction issue (16384 x 4097 BF16 288 us: the masks and the stores by
 // parts of the end vectors).
 //
 // A cluster adds its CTAs' sums by writing each CTA's six partial sums into
