@@ -724,7 +724,7 @@ __device__ __forceinline__ void copy_row16(const unsigned short *from, unsigned 
         uint4 a[5];   // the loads of four rounds at once
 #pragma unroll
         for (int u = 0; u < 4; ++u) a[u] = block(i0 + u * lanes + lane);
-        // the block after this round's last, for the last lane
+        // the block after these, for the last lane
         a[4] = block(i0 + 4 * lanes);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
