@@ -841,6 +841,15 @@ def _ptr(t, name, dtype, shape, dev):
     raise ValueError(f"{name} must be contiguous")
 
 
+_INT_MAX = 0x7fffffff
+
+
+def _fit_int(*sizes):
+    """Whether the C ABI's int holds every size (ctypes keeps the low 32 bits
+    of what it does not hold)."""
+    return min(sizes) >= 0 and max(sizes) <= _INT_MAX
+
+
 def _device_index(t, name):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -889,12 +898,14 @@ def tile_block_norm(x, residual, hidden, out, gamma_post=None, gate=None, gamma_
     out = norm(hidden; gamma_pre), RMSNorms, of float32, bfloat16 or float16
     rows; see ``tile_block_norm`` in include/tile_rows.h.  ``post`` / ``pre``
     switch the norms (without ``pre``, ``out`` is None); ``rows_per_gate``
-    0 with a gate stands for all rows."""
+    0, and any number from ``rows`` on, stands for all rows."""
     import torch
     code, dev = _row_code(x, "x"), _device_index(x, "x")
     shape, dt, f32 = x.shape, x.dtype, torch.float32
     rows, width = shape
-    vec, per = (width,), rows_per_gate or rows or 1
+    if not _fit_int(rows, width):
+        raise ValueError(f"rows and width must be below 2^31, not {rows} x {width}")
+    vec, per = (width,), min(rows_per_gate, rows) or rows or 1
     a = TileBlockNormArgs(
         _ptr(x, "x", dt, shape, dev), _ptr(residual, "residual", dt, shape, dev),
         _ptr(gamma_post, "gamma_post", f32, vec, dev), _gates(gate, rows, width, per, dev, "gate"),
@@ -905,6 +916,8 @@ def tile_block_norm(x, residual, hidden, out, gamma_post=None, gate=None, gamma_
 
 
 def tile_block_norm_backward_workspace_bytes(rows, width):
+    if not _fit_int(rows, width):
+        return 0
     return load().tile_block_norm_backward_workspace_bytes(rows, width)
 
 
@@ -919,7 +932,9 @@ def tile_block_norm_backward(x, hidden, dhidden, dout, din, dresidual, workspace
     code, dev = _row_code(din, "din"), _device_index(din, "din")
     shape, dt, f32 = din.shape, din.dtype, torch.float32
     rows, width = shape
-    vec, per = (width,), rows_per_gate or rows or 1
+    if not _fit_int(rows, width):
+        raise ValueError(f"rows and width must be below 2^31, not {rows} x {width}")
+    vec, per = (width,), min(rows_per_gate, rows) or rows or 1
     a = TileBlockNormBackwardArgs(
         _ptr(x, "x", dt, shape, dev), _ptr(hidden, "hidden", dt, shape, dev),
         _ptr(dhidden, "dhidden", dt, shape, dev), _ptr(dout, "dout", dt, shape, dev),
@@ -937,14 +952,18 @@ def tile_block_norm_backward(x, hidden, dhidden, dout, din, dresidual, workspace
 # ---- linear cross entropy -------------------------------------------------------
 
 def tile_linear_cross_entropy_workspace_bytes(rows, width, vocab):
+    if not _fit_int(rows, width, vocab):
+        return 0
     return load().tile_linear_cross_entropy_workspace_bytes(rows, width, vocab)
 
 
 def tile_linear_cross_entropy_backward_workspace_bytes(rows, width, vocab):
+    if not _fit_int(rows, width, vocab):
+        return 0
     return load().tile_linear_cross_entropy_backward_workspace_bytes(rows, width, vocab)
 
 
-def _ce_inputs(x, weight, target):
+def _ce_inputs(x, weight, target, ignore_index):
     """(type code, device, x, weight and target pointers, rows, width, vocab)."""
     import torch
     code, dev = _row_code(x, "x"), _device_index(x, "x")
@@ -952,6 +971,10 @@ def _ce_inputs(x, weight, target):
         raise ValueError("x must be bfloat16 or float16")
     rows, width = x.shape
     vocab = weight.shape[0]
+    if not _fit_int(rows, width, vocab):
+        raise ValueError(f"rows, width and vocab must be below 2^31, not {rows}, {width}, {vocab}")
+    if not -1 << 63 <= ignore_index < 1 << 63:
+        raise ValueError("ignore_index must be a 64-bit integer, as the targets are")
     return (code, dev, _ptr(x, "x", x.dtype, x.shape, dev),
             _ptr(weight, "weight", x.dtype, (vocab, width), dev),
             _ptr(target, "target", torch.int64, (rows,), dev), rows, width, vocab)
@@ -962,7 +985,7 @@ def tile_linear_cross_entropy(x, weight, target, loss, lse, workspace, ignore_in
     """loss and log-sum-exp of the rows' logits x weight^T (bfloat16 or
     float16) without keeping them; see include/tile_rows.h."""
     import torch
-    code, dev, px, pw, pt, rows, width, vocab = _ce_inputs(x, weight, target)
+    code, dev, px, pw, pt, rows, width, vocab = _ce_inputs(x, weight, target, ignore_index)
     ws, nbytes = _workspace(workspace, dev)
     _call_on(dev, stream, "tile_linear_cross_entropy", code, px, pw, pt,
              _ptr(loss, "loss", torch.float32, (rows,), dev),
@@ -975,7 +998,7 @@ def tile_linear_cross_entropy_backward(x, weight, target, lse, dloss, dx, dweigh
     """Gradients of ``tile_linear_cross_entropy`` for the gradient ``dloss``
     of each row's loss; ``dx`` or ``dweight`` may be None."""
     import torch
-    code, dev, px, pw, pt, rows, width, vocab = _ce_inputs(x, weight, target)
+    code, dev, px, pw, pt, rows, width, vocab = _ce_inputs(x, weight, target, ignore_index)
     ws, nbytes = _workspace(workspace, dev)
     _call_on(dev, stream, "tile_linear_cross_entropy_backward", code, px, pw, pt,
              _ptr(lse, "lse", torch.float32, (rows,), dev),
