@@ -864,11 +864,21 @@ def _workspace(t, dev):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
+def _same_device(stream, dev):
+    """Refuses a torch stream of another device than index ``dev`` (an integer
+    handle does not say whose it is)."""
+    device = getattr(stream, "device", None)
+    if device is not None and device.index != dev:
+        raise ValueError(f"stream must be one of cuda:{dev} like the tensors, not of {device}")
+
+
 def _call_on(dev, stream, name, *args):
     """Calls a C entry point with device ``dev`` current; ``stream`` None is
     that device's current stream."""
     import torch
     fn = getattr(load(), name)
+    if stream is not None:
+        _same_device(stream, dev)
     if torch._C._cuda_getDevice() == dev:
         s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
         _check(fn(*args, s), name)
@@ -1042,7 +1052,8 @@ def softmax(x, out=None, stream=None):
 
 def _on_stream(fn):
     """A wrapper that allocates runs with its ``stream`` current, so that what
-    it allocates belongs to the stream its kernels run on."""
+    it allocates belongs to the stream its kernels run on.  The stream is one
+    of the tensors' device, which need not be the current one."""
     import functools
 
     @functools.wraps(fn)
@@ -1050,7 +1061,12 @@ def _on_stream(fn):
         if stream is None:
             return fn(*args, **kwargs)
         import torch
-        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        dev = next((t.get_device() for t in (*args, *kwargs.values())
+                    if isinstance(t, torch.Tensor) and t.is_cuda), None)
+        if dev is None:
+            raise ValueError(f"{fn.__name__} takes CUDA tensors (there is no CPU path)")
+        _same_device(stream, dev)
+        s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
         with torch.cuda.stream(s):
             return fn(*args, **kwargs)
     return call
