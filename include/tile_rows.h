@@ -404,8 +404,10 @@ int tile_block_norm(const tile_block_norm_args_t *args, cudaStream_t stream);
  * device `workspace` (16-byte aligned), joined in a fixed order; no atomics.
  * `in` may be NULL without TILE_NORM_POST and gate; `hidden` and dout may
  * be NULL without TILE_NORM_PRE.  rows == 0 writes zero parameter
- * gradients.  dgamma_post needs TILE_NORM_POST, dgamma_pre TILE_NORM_PRE,
- * dgate a gate (TILE_ERR_OP).  Calls that overlap in time need workspaces
+ * gradients.  A row's sums (of in^2, hidden^2 and gate gamma_post in hidden)
+ * have to lie within FP32's range, as the forward's two do.  dgamma_post
+ * needs TILE_NORM_POST, dgamma_pre TILE_NORM_PRE, dgate a gate (TILE_ERR_OP).
+ * Calls that overlap in time need workspaces
  * of their own. */
 typedef struct tile_block_norm_backward_args {
     const void *in, *hidden, *dhidden, *dout;

@@ -134,13 +134,12 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockArg
             }
         }
         row_sum<6, CL>(s, mem, turn, warps, cluster);
-        // gh = dh + r2 gy - ch h
+        // gh = dh + r2 (gy - ch h), db = r1 (u - cb b r1), as in the ring kernel
         const float r2 = a.pre ? 1.0f / sqrtf(fmaf(s[0], inv_n, a.eps)) : 0.0f;
-        const float ch = r2 * r2 * r2 * (s[1] * inv_n);
+        const float ch = r2 * (s[1] * inv_n) * r2;
         const float r1 = a.post ? 1.0f / sqrtf(fmaf(s[2], inv_n, a.eps)) : 1.0f;
-        // db = r1 u - cb b
-        const float ub = fmaf(r2, s[4], s[3]) - ch * s[5];
-        const float cb = a.post ? r1 * r1 * r1 * (ub * inv_n) : 0.0f;
+        const float ub = fmaf(r2, fmaf(-ch, s[5], s[4]), s[3]);
+        const float cb = a.post ? r1 * (ub * inv_n) : 0.0f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (col[k] >= a.width) continue;
@@ -152,11 +151,12 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockArg
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int i = k * V + j;
-                const float gh = fmaf(-ch, h[j], fmaf(r2, dy[j] * g2[i], dh[j]));
+                const float gh = fmaf(r2, fmaf(-ch, h[j], dy[j] * g2[i]), dh[j]);
+                const float unit = b[j] * r1;
                 sum_pre[i] = fmaf(dy[j], h[j] * r2, sum_pre[i]);
-                sum_gate[i] = fmaf(gh, b[j] * r1, sum_gate[i]);
+                sum_gate[i] = fmaf(gh, unit, sum_gate[i]);
                 dr[j] = a.scale * gh;
-                db[j] = fmaf(-cb, b[j], r1 * (w[i] * gh));
+                db[j] = r1 * fmaf(-cb, unit, w[i] * gh);
             }
             const long long at = row * a.width + col[k];
             A::store(din + at, db);

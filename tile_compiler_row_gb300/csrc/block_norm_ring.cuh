@@ -295,12 +295,13 @@ __global__ void __launch_bounds__(MAXT, MINB)
 #pragma unroll
             for (int i = 0; i < 6; ++i) sum[i] = __shfl_sync(0xffffffffu, joined, 4 * i);
         }
-        // gh = dh + r2 gy - ch h,  db = r1 u - cb b
+        // gh = dh + r2 (gy - ch h),  db = r1 (u - cb b r1): no factor is a
+        // power of r1 or r2 that rows far from 1 would take out of range
         const float r2 = a.pre ? inv_sqrt<T>(fmaf(sum[0], inv_n, a.eps)) : 0.0f;
-        const float ch = r2 * r2 * r2 * (sum[1] * inv_n);
+        const float ch = r2 * (sum[1] * inv_n) * r2;
         const float r1 = a.post ? inv_sqrt<T>(fmaf(sum[2], inv_n, a.eps)) : 1.0f;
-        const float ub = fmaf(r2, sum[4], sum[3]) - ch * sum[5];
-        const float cb = a.post ? r1 * r1 * r1 * (ub * inv_n) : 0.0f;
+        const float ub = fmaf(r2, fmaf(-ch, sum[5], sum[4]), sum[3]);
+        const float cb = a.post ? r1 * (ub * inv_n) : 0.0f;
         const F2 r1s = both(r1), r2s = both(r2), mch = both(-ch), mcb = both(-cb),
                  scale = both(a.scale);
         const long long o = part_at(row) + tid * N;
@@ -315,12 +316,12 @@ __global__ void __launch_bounds__(MAXT, MINB)
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int c = k * P + i;
-                const F2 gh = fma2(h[i], mch, fma2(mul2(dy[i], g2[c]), r2s, dh[i]));
-                const F2 t = mul2(gh, r1s);
+                const F2 gh = fma2(fma2(h[i], mch, mul2(dy[i], g2[c])), r2s, dh[i]);
+                const F2 unit = mul2(b[i], r1s);
                 sum_pre[c] = fma2(mul2(h[i], r2s), dy[i], sum_pre[c]);
-                sum_gate[c] = fma2(t, b[i], sum_gate[c]);
+                sum_gate[c] = fma2(gh, unit, sum_gate[c]);
                 dr[i] = mul2(gh, scale);
-                db[i] = fma2(t, w[c], mul2(b[i], mcb));
+                db[i] = mul2(fma2(unit, mcb, mul2(gh, w[c])), r1s);
             }
             T *din = static_cast<T *>(a.din) + o + k * W * N;
             T *dres = static_cast<T *>(a.dresidual) + o + k * W * N;
