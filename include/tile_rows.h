@@ -435,8 +435,12 @@ int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *
  * Both FP32 [rows]; a row whose target is ignore_index gets loss = lse = 0.
  * The loss is log(1 + sum over the other entries of exp(l_v - l_target)) with
  * the target's logit as an FP32 sum, so it is never negative and small losses
- * keep their digits; the other logits' sums are truncated as they grow (the
- * tensor cores'), with the mean of it put back.
+ * keep their digits.  The other logits are sums of the tensor cores, in parts of
+ * at most 4096 columns, which cut off low bits as they add: of random rows
+ * about 2^-26 of a part for each 16 columns, which is put back; of products of
+ * one sign up to 2^-23 of it (2e-5 of the logit at 4096 columns and beyond);
+ * of sums that fit 24 bits, such as rows of few columns, nothing: there the
+ * logit comes out up to 2^-18 of itself (3.8e-6) too large.
  * dtype: TILE_DTYPE_BF16 or TILE_DTYPE_F16 of in and weight ([vocab][width]);
  * the products of 16-bit elements are exact, and every sum is FP32.  (FP32
  * operands are refused with TILE_ERR_DTYPE: the tensor cores would round

@@ -106,15 +106,25 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
-// log2(e), by which logits of the tensor cores are multiplied, with what they
-// lost put back.  The tensor cores truncate: each 16 products added take half
-// a unit of the 24th bit off the sum so far, on average, 2^-25 to 2^-24 of it
-// and so, over a sum that grows evenly, 2^-26 to 2^-25 of the whole for each
-// step.  Put back is the least of that: 4096 columns lost 3.9e-6 (random) to
-// 4.4e-6 (x along w) of a logit and 256 2^-26 = 3.8e-6 are put back; the lse
-// of 256 rows over 32768 entries was 8.8e-6 too small, every row alike.
+// A logit is added up on the tensor cores in parts of PART_BLOCKS k blocks
+// (4096 columns), joined in FP32 registers: what a sum loses grows with its
+// steps, and ends there.  More and shorter parts lose less, but each stops the
+// tensor cores for some 500 cycles (parts of 1024 columns: 4096 x 4096 x 131072
+// BF16 4 % slower, 64 x 8192 x 65536 10 %, 7 % with 2048, 2 % with 4096).
+constexpr int PART_BLOCKS = 64;
+
+// log2(e), by which logits of the tensor cores are multiplied, with some of
+// what they lost put back.  The tensor cores cut off as they add: each 16
+// products added lose, of the sum so far, next to nothing where everything
+// fits its 24 bits (few or small products), 2^-25 to 2^-24 in random rows
+// (so 2^-26 to 2^-25 of a sum that grows evenly), and 2^-24 (BF16) to 2^-23
+// (FP16) of it where all products have one sign, whose low bits are lost too.
+// Put back is 2^-26 a step, the least that random rows lose: 4096 columns lost
+// 3.9e-6 of a logit there and 256 2^-26 = 3.8e-6 are put back (the lse of 256
+// rows over 32768 entries was 8.8e-6 too small, every row alike).  Sums that
+// lose nothing come out that much too large.
 __device__ __forceinline__ float logit_scale(int k_blocks) {
-    return kLog2e * (1.0f + static_cast<float>(k_blocks * (BK / 16)) * 0x1p-26f);
+    return kLog2e * (1.0f + static_cast<float>(min(k_blocks, PART_BLOCKS) * (BK / 16)) * 0x1p-26f);
 }
 
 template <bool BF16>
@@ -217,10 +227,34 @@ __device__ __forceinline__ Extents extents(const Job &j, const CeState *state) {
     return e;
 }
 
-// A tile of FP32 accumulators as 16-bit rows in memory: 32 rows x 64 columns
-// at a time through this warp's part of shared memory and a tensor-map store
-// (128-byte swizzled; whole lines whatever the row stride, and clipped at
-// the matrix's edges).  `value` maps column c + j's accumulator.
+// 32 rows x 64 columns (thread = row, `value` of column j) as 16-bit rows in
+// memory, through this warp's part of shared memory and a tensor-map store
+// (128-byte swizzled; whole lines whatever the row stride, and clipped at the
+// matrix's edges).
+template <bool BF16, class F>
+__device__ __forceinline__ void store_64(const CUtensorMap *map, uint32_t buf, int lane, int row,
+                                         int col, F value) {
+    float v[64];
+#pragma unroll
+    for (int j = 0; j < 64; ++j) v[j] = value(j);
+    if (lane == 0) store_wait_read<0>();   // the buffer's last store has read it
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 64; j += 8)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         buf + lane * 128 + 16 * ((j / 8) ^ (lane & 7))),
+                     "r"(pack2<BF16>(v[j], v[j + 1])), "r"(pack2<BF16>(v[j + 2], v[j + 3])),
+                     "r"(pack2<BF16>(v[j + 4], v[j + 5])), "r"(pack2<BF16>(v[j + 6], v[j + 7]))
+                     : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+        tma_store(map, col, row, buf);
+        store_commit();
+    }
+}
+// A tile of FP32 accumulators so, 64 columns at a time; `value` maps column
+// c + j's accumulator.
 template <bool BF16, class F>
 __device__ __forceinline__ void store_tile16(const CUtensorMap *map, uint32_t tmem, uint32_t buf,
                                              int lane, int row0, int col0, int from, int end,
@@ -228,23 +262,7 @@ __device__ __forceinline__ void store_tile16(const CUtensorMap *map, uint32_t tm
     for (int c = from; c < end; c += 64) {
         float v[64];
         tmem_load64(tmem + c, v);
-#pragma unroll
-        for (int j = 0; j < 64; ++j) v[j] = value(v[j], c + j);
-        if (lane == 0) store_wait_read<0>();   // the buffer's last store has read it
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 64; j += 8)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             buf + lane * 128 + 16 * ((j / 8) ^ (lane & 7))),
-                         "r"(pack2<BF16>(v[j], v[j + 1])), "r"(pack2<BF16>(v[j + 2], v[j + 3])),
-                         "r"(pack2<BF16>(v[j + 4], v[j + 5])), "r"(pack2<BF16>(v[j + 6], v[j + 7]))
-                         : "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-            tma_store(map, col0 + c, row0, buf);
-            store_commit();
-        }
+        store_64<BF16>(map, buf, lane, row0, col0 + c, [&](int j) { return value(v[j], c + j); });
     }
 }
 
@@ -307,9 +325,10 @@ __device__ __forceinline__ void store_rows16(unsigned short *out, long long ld, 
 // pairs leave a sixth of the pairs' time.  So pairs that get one less of
 // them start on the second job's short tiles while the others do their last
 // long one, and all go on in turn from there (tile_at).
-template <int EPI0, int EPI1, bool BF16>
-__global__ void __launch_bounds__(GEMM_THREADS, 1)
-    gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs g) {
+//
+// PARTS: sums of more than PART_BLOCKS k blocks, one accumulator a part.
+template <int EPI0, int EPI1, bool BF16, bool PARTS>
+__device__ __forceinline__ void gemm(const GemmMaps &maps, const GemmArgs &g) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * MOST_STAGES + 4];
     __shared__ uint32_t tmem_slot;
@@ -453,36 +472,41 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             on_tile(t, [&](auto j, Tile, int kb0, int kb1) {
                 constexpr int J = decltype(j)::value, EPI = J ? EPI1 : EPI0;
                 const uint32_t idesc = mma_idesc(BF16, a_mn(EPI), b_mn(EPI), BM, g.job[J].bn);
-                if (!(ok = bar_wait(acc_empty(acc), acc_phase ^ 1u, aborted, g.status,
-                                    CE_WAIT_TIMEOUT)))
-                    return;
-                tc_fence_after();
-                const uint32_t d = tmem + acc * BN;
-                bool first = true;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!(ok = bar_wait(full(stage), phase, aborted, g.status, CE_WAIT_TIMEOUT)))
-                        break;
+                int kb = kb0;
+                do {   // the whole sum, or a part of it
+                    if (!(ok = bar_wait(acc_empty(acc), acc_phase ^ 1u, aborted, g.status,
+                                        CE_WAIT_TIMEOUT)))
+                        return;
                     tc_fence_after();
-                    const uint32_t a = base + stage * stage_bytes, b = a + a_bytes;
-                    const uint64_t da = smem_desc(a, a_mn(EPI) ? 8192 : 16, 1024);
-                    const uint64_t db = smem_desc(b, b_mn(EPI) ? 8192 : 16, 1024);
+                    const uint32_t d = tmem + acc * BN;
+                    const int end = PARTS ? min(kb1, kb + PART_BLOCKS) : kb1;
+                    bool first = true;
+                    for (; kb < end; ++kb) {
+                        if (!(ok = bar_wait(full(stage), phase, aborted, g.status,
+                                            CE_WAIT_TIMEOUT)))
+                            break;
+                        tc_fence_after();
+                        const uint32_t a = base + stage * stage_bytes, b = a + a_bytes;
+                        const uint64_t da = smem_desc(a, a_mn(EPI) ? 8192 : 16, 1024);
+                        const uint64_t db = smem_desc(b, b_mn(EPI) ? 8192 : 16, 1024);
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k) {
-                        // 16 elements along K: 32 bytes of a K-major row, or
-                        // 16 rows of 128 bytes
-                        tc_mma(d, da + k * (a_mn(EPI) ? 2048 >> 4 : 32 >> 4),
-                               db + k * (b_mn(EPI) ? 2048 >> 4 : 32 >> 4), idesc, !first);
-                        first = false;
+                        for (int k = 0; k < BK / 16; ++k) {
+                            // 16 elements along K: 32 bytes of a K-major row, or
+                            // 16 rows of 128 bytes
+                            tc_mma(d, da + k * (a_mn(EPI) ? 2048 >> 4 : 32 >> 4),
+                                   db + k * (b_mn(EPI) ? 2048 >> 4 : 32 >> 4), idesc, !first);
+                            first = false;
+                        }
+                        tc_commit(empty(stage));
+                        if (++stage == stages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
-                    tc_commit(empty(stage));
-                    if (++stage == stages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-                tc_commit(acc_full(acc));
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
+                    tc_commit(acc_full(acc));
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                } while (PARTS && ok && kb < kb1);
             });
         }
         if (*aborted) {   // wait (bounded) until no MMA touches the pair's memory
@@ -500,6 +524,21 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t drained0 = peer_addr(acc_empty(0), 0), drained1 = peer_addr(acc_empty(1), 0);
         const float unscale = EPI1 == EPI_DWEIGHT ? g.state->unscale : 1.0f;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        // whether the accumulator that is due has come
+        auto ready = [&] {
+            const bool in = __all_sync(0xffffffffu, bar_wait(acc_full(acc), acc_phase, aborted,
+                                                             g.status, CE_WAIT_TIMEOUT));
+            if (in) tc_fence_after();
+            return in;
+        };
+        auto drained = [&] {   // this warp has read it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive_peer(acc ? drained1 : drained0);
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        };
         int t;
         for (int i = 0; (t = tile_at(i)) >= 0; ++i) {
             bool ok = true;
@@ -514,14 +553,27 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     const long long t = g.ptarget != nullptr ? g.ptarget[row] : g.target[row];
                     if (t >= col0 && t < e.n) skip = static_cast<int>(t) - col0;
                 }
-                ok = __all_sync(0xffffffffu, bar_wait(acc_full(acc), acc_phase, aborted, g.status,
-                                                      CE_WAIT_TIMEOUT));
-                if (!ok) return;
-                tc_fence_after();
                 // this warp's columns of the tile: [from, to), and those that exist
                 const int from = half * (job.bn / 2), to = from + job.bn / 2;
                 const int end = min(to, e.n - col0);
-                const uint32_t d = tmem + acc * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+                float sum[PARTS ? BN / 2 : 1];   // this row's logits, part after part
+                if constexpr (PARTS) {
+#pragma unroll
+                    for (int j = 0; j < BN / 2; ++j) sum[j] = 0.0f;
+                    for (int kb = kb0;; kb += PART_BLOCKS) {
+                        if (!(ok = ready())) return;
+                        const uint32_t d = tmem + acc * BN + lanes + from;
+                        if (row0 < e.m)
+#pragma unroll
+                            for (int j = 0; j < BN / 2; j += 16)
+                                if (from + j < end) tmem_add16(d + j, sum + j);
+                        if (kb + PART_BLOCKS >= kb1) break;
+                        drained();
+                    }
+                } else {
+                    if (!(ok = ready())) return;
+                }
+                const uint32_t d = tmem + acc * BN + lanes;
                 const bool none = kb0 == kb1;   // no product was made: zero
                 // rows of this warp that are looked at: those that are there, and
                 // for g those up to the next 64, which dW's reduction reads
@@ -530,9 +582,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     // the maximum and the sum over exponents of 2
                     const float scale = logit_scale(e.k_blocks);
                     float m = -INFINITY, s = 0.0f;
-                    for (int c = from; c < end; c += 32) {
-                        float v[32];
-                        tmem_load32(d + c, v);
+                    auto chunk = [&](int c, float (&v)[32]) {
                         const int limit = end - c;
                         if (limit < 32)
 #pragma unroll
@@ -554,6 +604,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                         for (int j = 0; j < 32; ++j) part[j & 3] += ex2(fmaf(v[j], scale, -ref));
                         s += (part[0] + part[1]) + (part[2] + part[3]);
                         m = top;
+                    };
+                    if constexpr (PARTS) {
+#pragma unroll
+                        for (int j = 0; j < BN / 2; j += 32)
+                            if (from + j < end) chunk(from + j, *reinterpret_cast<float (*)[32]>(sum + j));
+                    } else {
+                        for (int c = from; c < end; c += 32) {
+                            float v[32];
+                            tmem_load32(d + c, v);
+                            chunk(c, v);
+                        }
                     }
                     if (row < e.m)
                         g.partial[(static_cast<long long>(row) * e.n_tiles + w.n) * 2 + half] =
@@ -565,11 +626,19 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     const float miss = in ? g.pmiss[row] : 0.0f;
                     const float scale = logit_scale(e.k_blocks);
                     const int limit = in ? e.n - col0 : 0;
-                    store_tile16<BF16>(&maps.out, d, buf, lane, row0, col0, from, to,
-                                 [&](float v, int c) {
-                                     const float p = ex2(fmaf(v, scale, -lse2));
-                                     return c < limit ? (want == c ? miss : p) * dl : 0.0f;
-                                 });
+                    auto grad = [&](float v, int c) {
+                        const float p = ex2(fmaf(v, scale, -lse2));
+                        return c < limit ? (want == c ? miss : p) * dl : 0.0f;
+                    };
+                    if constexpr (PARTS) {
+#pragma unroll
+                        for (int h = 0; h < BN / 2; h += 64)
+                            store_64<BF16>(&maps.out, buf, lane, row0, col0 + from + h, [&](int j) {
+                                return grad(sum[h + j], from + h + j);
+                            });
+                    } else {
+                        store_tile16<BF16>(&maps.out, d, buf, lane, row0, col0, from, to, grad);
+                    }
                 } else if constexpr (EPI == EPI_DWEIGHT) {
                     const float f = unscale;
                     if (job.store) {
@@ -603,11 +672,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 }
             });
             if (!ok) break;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive_peer(acc ? drained1 : drained0);
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
+            drained();
         }
         if (lane == 0) store_wait<0>();   // the stores are written before the CTA ends
     }
@@ -617,6 +682,20 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     cluster_sync();   // neither CTA leaves while the other uses its memory
     tc_fence_after();
     if (warp == EPI_WARPS + 1) tmem_free(tmem, 512);
+}
+
+template <int EPI0, int EPI1, bool BF16>
+__global__ void __launch_bounds__(GEMM_THREADS, 1)
+    gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs g) {
+    gemm<EPI0, EPI1, BF16, false>(maps, g);
+}
+// 16 registers fewer than 320 threads could have leave room for a CTA of the
+// next kernel beside this one, whose dot products (join_lse_kernel) then run
+// under these products (1024 x 16384 x 16384 BF16 345 us, 372 us without).
+template <int EPI, bool BF16>
+__global__ void __maxnreg__(152)
+    gemm_parts_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs g) {
+    gemm<EPI, EPI_NONE, BF16, true>(maps, g);
 }
 
 // ---- a row's own logit -----------------------------------------------------------------
@@ -1034,10 +1113,10 @@ cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned clust
 
 long long job_tiles(const Job &j) { return up(j.m, BM) / BM * (up(j.n, j.bn) / j.bn) * j.splits; }
 
-template <int EPI0, int EPI1, bool BF16>
-cudaError_t launch_gemm_typed(const GemmMaps &maps, const GemmArgs &g, cudaStream_t stream) {
-    static std::atomic<int> ready[kMaxDevices];
-    const auto kernel = gemm_kernel<EPI0, EPI1, BF16>;
+template <class Kernel>
+cudaError_t launch_gemm_kernel(Kernel kernel, std::atomic<int> (&ready)[kMaxDevices],
+                               const GemmMaps &maps, const GemmArgs &g, long long tiles,
+                               cudaStream_t stream) {
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
@@ -1047,13 +1126,22 @@ cudaError_t launch_gemm_typed(const GemmMaps &maps, const GemmArgs &g, cudaStrea
         if (err != cudaSuccess) return err;
         ready[dev].store(1, std::memory_order_release);
     }
-    const long long tiles = job_tiles(g.job[0]) + (EPI1 ? job_tiles(g.job[1]) : 0);
     if (tiles > 0x3fffffff) return cudaErrorInvalidValue;   // tile numbers are ints
     long long pairs = sm_count_of_device() / 2;
     if (pairs > tiles) pairs = tiles;
     if (pairs < 1) pairs = 1;
     return launch_dependent(kernel, static_cast<unsigned>(2 * pairs), 2, GEMM_THREADS, GEMM_SMEM,
                             stream, maps, g);
+}
+template <int EPI0, int EPI1, bool BF16>
+cudaError_t launch_gemm_typed(const GemmMaps &maps, const GemmArgs &g, cudaStream_t stream) {
+    static std::atomic<int> ready[2][kMaxDevices];
+    const long long tiles = job_tiles(g.job[0]) + (EPI1 ? job_tiles(g.job[1]) : 0);
+    if constexpr (EPI0 == EPI_LSE || EPI0 == EPI_GRAD)
+        if (g.job[0].k > PART_BLOCKS * BK)
+            return launch_gemm_kernel(gemm_parts_kernel<EPI0, BF16>, ready[1], maps, g, tiles,
+                                      stream);
+    return launch_gemm_kernel(gemm_kernel<EPI0, EPI1, BF16>, ready[0], maps, g, tiles, stream);
 }
 template <int EPI0, int EPI1>
 cudaError_t launch_gemm(int bf16, const GemmMaps &maps, const GemmArgs &g, cudaStream_t stream) {
