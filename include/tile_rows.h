@@ -419,7 +419,13 @@ typedef struct tile_block_norm_backward_args {
     int dtype;
 } tile_block_norm_backward_args_t;
 
+/* Workspace: 16 width bytes for each program of a call, as many as run at once
+ * (at most 40 MiB in all) and no more than rows; but for widths that are not
+ * multiples of 8 at least 8 for each gate row, up to 1024 (2432 where width
+ * <= 1024).  The first function has enough for any number of gate rows, the
+ * second for this one (0: no gate), which is what a call checks. */
 size_t tile_block_norm_backward_workspace_bytes(int rows, int width);
+size_t tile_block_norm_backward_gated_workspace_bytes(int rows, int width, int gate_rows);
 int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *workspace,
                              size_t workspace_bytes, cudaStream_t stream);
 

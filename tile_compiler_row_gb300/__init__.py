@@ -36,6 +36,7 @@ __all__ = [
     "tile_layernorm_backward_f32", "tile_rmsnorm_backward_f32", "tile_softmax_backward_f32",
     "tile_run_backward_plan_f32", "tile_norm_param_grad_workspace_bytes",
     "tile_block_norm", "tile_block_norm_backward", "tile_block_norm_backward_workspace_bytes",
+    "tile_block_norm_backward_gated_workspace_bytes",
     "tile_linear_cross_entropy", "tile_linear_cross_entropy_workspace_bytes",
     "tile_linear_cross_entropy_backward", "tile_linear_cross_entropy_backward_workspace_bytes",
     "block_norm", "block_norm_backward", "linear_cross_entropy", "linear_cross_entropy_backward",
@@ -208,6 +209,8 @@ def load():
     lib.tile_norm_param_grad_workspace_bytes.restype = ctypes.c_size_t
     lib.tile_block_norm_backward_workspace_bytes.argtypes = [I, I]
     lib.tile_block_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+    lib.tile_block_norm_backward_gated_workspace_bytes.argtypes = [I, I, I]
+    lib.tile_block_norm_backward_gated_workspace_bytes.restype = ctypes.c_size_t
     for name in ("tile_linear_cross_entropy_workspace_bytes",
                  "tile_linear_cross_entropy_backward_workspace_bytes"):
         getattr(lib, name).argtypes = [I, I, I]
@@ -926,9 +929,17 @@ def tile_block_norm(x, residual, hidden, out, gamma_post=None, gate=None, gamma_
 
 
 def tile_block_norm_backward_workspace_bytes(rows, width):
+    """Enough for any number of gate rows."""
     if not _fit_int(rows, width):
         return 0
     return load().tile_block_norm_backward_workspace_bytes(rows, width)
+
+
+def tile_block_norm_backward_gated_workspace_bytes(rows, width, gate_rows):
+    """What a call with this many gate rows (0: no gate) needs."""
+    if not _fit_int(rows, width, gate_rows):
+        return 0
+    return load().tile_block_norm_backward_gated_workspace_bytes(rows, width, gate_rows)
 
 
 def tile_block_norm_backward(x, hidden, dhidden, dout, din, dresidual, workspace,
@@ -1101,7 +1112,8 @@ def block_norm_backward(x, hidden, gamma_post, gate, gamma_pre, dhidden, dout, p
     dgamma_post = torch.empty_like(gamma_post) if post and gamma_post is not None else None
     dgate = torch.empty_like(gate) if gate is not None else None
     dgamma_pre = torch.empty_like(gamma_pre) if pre and gamma_pre is not None else None
-    ws = _scratch(tile_block_norm_backward_workspace_bytes(*like.shape), like)
+    gate_rows = 0 if gate is None else 1 if gate.dim() == 1 else gate.shape[0]
+    ws = _scratch(tile_block_norm_backward_gated_workspace_bytes(*like.shape, gate_rows), like)
     tile_block_norm_backward(x, hidden, dhidden, dout, din, dresidual, ws, gamma_post, gate,
                              gamma_pre, dgamma_post, dgate, dgamma_pre, post, pre, rows_per_gate,
                              residual_scale, eps)

@@ -391,6 +391,6 @@ cudaError_t launch_block_norm(int elem, BlockAccess access, const BlockArgs &a,
                               cudaStream_t stream);
 cudaError_t launch_block_norm_backward(int elem, BlockAccess access, const BlockArgs &a,
                                        cudaStream_t stream);
-size_t block_norm_backward_workspace(long long rows, int width);
+size_t block_norm_backward_workspace(long long rows, int width, long long gates);
 
 }  // namespace tile

@@ -100,7 +100,13 @@ int tile_block_norm(const tile_block_norm_args_t *args, cudaStream_t stream) {
 
 size_t tile_block_norm_backward_workspace_bytes(int rows, int width) {
     if (rows < 1 || width < 1 || width > TILE_MAX_WIDTH) return 0;
-    return tile::block_norm_backward_workspace(rows, width);
+    return tile::block_norm_backward_workspace(rows, width, rows);
+}
+
+size_t tile_block_norm_backward_gated_workspace_bytes(int rows, int width, int gate_rows) {
+    if (rows < 1 || width < 1 || width > TILE_MAX_WIDTH || gate_rows < 0) return 0;
+    const int gates = gate_rows < 1 ? 1 : gate_rows > rows ? rows : gate_rows;
+    return tile::block_norm_backward_workspace(rows, width, gates);
 }
 
 int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *workspace,
@@ -154,10 +160,10 @@ int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *
     const size_t es = elem_size(c.dtype);
     const void *mats[] = {a.x, a.hidden, a.dhidden, a.dout, a.din, a.dresidual};
     if (any_misaligned(mats, 6, es) || misaligned_to(workspace, 16)) return TILE_ERR_ALIGN;
-    const size_t need = tile::block_norm_backward_workspace(c.rows, c.width);
+    const size_t gates = static_cast<size_t>((a.rows + a.per_gate - 1) / a.per_gate);
+    const size_t need = tile::block_norm_backward_workspace(a.rows, a.width, gates);
     if (workspace_bytes < need) return TILE_ERR_WORKSPACE;
     const size_t mat = static_cast<size_t>(c.rows) * static_cast<size_t>(c.width) * es;
-    const size_t gates = static_cast<size_t>((a.rows + a.per_gate - 1) / a.per_gate);
     const Range out[] = {{a.din, mat}, {a.dresidual, mat}, {a.dgamma_post, vec},
                          {a.dgate, gates * vec}, {a.dgamma_pre, vec}, {workspace, need}};
     const Range in[] = {{a.x, mat}, {a.hidden, mat}, {a.dhidden, mat}, {a.dout, mat},

@@ -23,7 +23,8 @@
 // block_norm_backward_kernel here takes what that does not: the widest rows
 // (above 65536 two-byte or 32768 FP32 columns, where a row of four inputs
 // leaves a cluster of 8 CTAs no room for a second one), row matrices that
-// are not all 16-byte aligned, and odd widths with more than 128 gate rows.
+// are not all 16-byte aligned, and odd widths with more row classes in their
+// gate rows than there may be programs (class_units).
 // It loads each row into registers when its turn comes.
 #include "block_norm_ring.cuh"
 #include "device_status.h"
@@ -33,17 +34,27 @@ TILE_DEVICE_STATUS(block_norm_backward)
 namespace tile {
 namespace {
 
-// Programs of a call: at most this many (their column sums are a few bytes of
-// a wide row's, so there may be as many as run at once; the workspace of
-// narrow rows stays below 40 MiB), each of at least four rows where there are
-// more rows than SMs.
+// Programs of a call: at most as many as may run at once, which the workspace
+// has column sums for: registers hold no more than 16384 columns of programs on
+// an SM, or 16 programs of narrow rows (40 MiB of column sums).
 constexpr int kNarrow = 1024;   // columns
+constexpr int kSms = 152;
 
-int most_units(int width) { return width <= kNarrow ? 2432 : 1024; }
+// Row classes of gate rows that programs keep to (RowWalk): the limit for odd
+// widths, whose programs may be more than run at once.
+int class_units(int width) { return width <= kNarrow ? 16 * kSms : 1024; }
 
+int most_units(int width) {
+    const int resident = (kSms * 16384 + width - 1) / width;
+    return resident < class_units(width) ? resident : class_units(width);
+}
+
+// As many programs as run at once (`slots`) where each has four rows and more;
+// with fewer rows, four rows to a program, but a program for each SM; one row
+// to a program where there are fewer rows than SMs.
 long long units_of(const BlockArgs &a, long long slots) {
+    const long long sms = sm_count_of_device();
     long long u = a.rows / 4 > slots ? slots : a.rows;
-    const long long sms = 152;
     if (a.rows / 4 <= slots && u > sms) u = a.rows / 4 > sms ? a.rows / 4 : sms;
     if (u > most_units(a.width)) u = most_units(a.width);
     return u < 1 ? 1 : u;
@@ -432,7 +443,7 @@ cudaError_t launch_typed(const BlockArgs &a, BlockAccess access, cudaStream_t st
     if (access == ACCESS_SHIFTED) {
         const RingPlan p = ring_plan<T, true>(a.width);
         const long long gates = (a.rows + a.per_gate - 1) / a.per_gate;
-        if (p.cluster > 0 && (p.classes == 1 || gates * p.classes <= most_units(a.width)))
+        if (p.cluster > 0 && (p.classes == 1 || gates * p.classes <= class_units(a.width)))
             return launch_ring_typed<T, true>(a, p, stream, out);
     }
     if (a.width <= 512 * 16) return launch_registers<T, 1, 16, false>(a, stream, out);
@@ -459,9 +470,12 @@ cudaError_t launch_join(const BlockArgs &a, const Programs &programs, long long 
 
 }  // namespace
 
-size_t block_norm_backward_workspace(long long rows, int width) {
-    // programs that keep to a row class of a gate row may be more than rows
-    const long long units = 8 * rows < most_units(width) ? 8 * rows : most_units(width);
+size_t block_norm_backward_workspace(long long rows, int width, long long gates) {
+    long long units = rows < most_units(width) ? rows : most_units(width);
+    if (width % 8 != 0) {   // up to 8 row classes (of 2-byte elements) in each gate row
+        const long long classes = 8 * gates < class_units(width) ? 8 * gates : class_units(width);
+        if (classes > units) units = classes;
+    }
     return static_cast<size_t>(units) * SLOTS * static_cast<size_t>(width) * sizeof(float);
 }
 
