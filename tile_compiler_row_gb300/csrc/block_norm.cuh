@@ -379,7 +379,7 @@ struct BlockArgs {
     int width;
     int post, pre;
     float scale, eps;
-    unsigned int *status;
+    unsigned int *status;   // backward
 };
 
 // What the pointers of a call allow: every row and parameter row on vectors;

@@ -8,13 +8,14 @@
 
 namespace {
 
+using tile::cuda_status;
+using tile::elem_size;
 using tile::misaligned_to;
 using tile::Range;
 
 bool valid_dtype(int dtype) {
     return dtype == TILE_DTYPE_F32 || dtype == TILE_DTYPE_BF16 || dtype == TILE_DTYPE_F16;
 }
-size_t elem_size(int dtype) { return dtype == TILE_DTYPE_F32 ? 4 : 2; }
 
 tile::BlockAccess access_of(const void *const *mats, int nmats, const void *const *params,
                             int nparams, int width, size_t es) {
@@ -42,12 +43,6 @@ int check_shape(int norms, int dtype, int rows, int width, const float *gate, in
     if (gate != nullptr && rows_per_gate < 1) return TILE_ERR_SHAPE;
     if (!(std::isfinite(eps) && eps >= 0.0f) || !std::isfinite(scale)) return TILE_ERR_EPS;
     return TILE_OK;
-}
-
-int cuda_status(cudaError_t err) {
-    if (err == cudaSuccess) return TILE_OK;
-    tile::set_last_cuda_error(static_cast<int>(err));
-    return TILE_ERR_CUDA;
 }
 
 }  // namespace

@@ -13,8 +13,6 @@
 #include "block_norm.cuh"
 #include "device_status.h"
 
-TILE_DEVICE_STATUS(block_norm)
-
 namespace tile {
 namespace {
 
@@ -421,12 +419,8 @@ cudaError_t launch_typed(const BlockArgs &a, BlockAccess access, cudaStream_t st
 
 }  // namespace
 
-cudaError_t launch_block_norm(int elem, BlockAccess access, const BlockArgs &args,
+cudaError_t launch_block_norm(int elem, BlockAccess access, const BlockArgs &a,
                               cudaStream_t stream) {
-    BlockArgs a = args;
-    cudaError_t err = cudaSuccess;
-    a.status = status_address(&err);
-    if (a.status == nullptr) return err;
     switch (elem) {
         case ELEM_F32: return launch_typed<float>(a, access, stream);
         case ELEM_BF16: return launch_typed<__nv_bfloat16>(a, access, stream);

@@ -1,10 +1,25 @@
-// Argument checks on addresses shared by the entry points (host only).
+// Argument checks and statuses shared by the entry points (host only).
 #pragma once
 
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/tile_rows.h"
+#include "launch.h"
+
 namespace tile {
+
+// The status of an entry point whose CUDA calls ended with err, which is kept
+// for tile_last_cuda_error.
+inline int cuda_status(cudaError_t err) {
+    if (err == cudaSuccess) return TILE_OK;
+    set_last_cuda_error(static_cast<int>(err));
+    return TILE_ERR_CUDA;
+}
+
+inline size_t elem_size(int dtype) {
+    return dtype == TILE_DTYPE_BF16 || dtype == TILE_DTYPE_F16 ? 2 : 4;
+}
 
 // Whether [a, a + abytes) and [b, b + bbytes) share a byte; NULL overlaps
 // nothing.

@@ -82,8 +82,7 @@ cudaError_t launch_param_grad(int elem, const void *x, const void *dy, const flo
                               cudaStream_t stream);
 cudaError_t status_param_grad(unsigned int *value, cudaStream_t stream);
 
-// Error words of the block-norm kernels (block_norm_fwd.cu, block_norm_bwd.cu).
-cudaError_t status_block_norm(unsigned int *value, cudaStream_t stream);
+// Error word of the block norm's gradient kernels (block_norm_bwd.cu).
 cudaError_t status_block_norm_backward(unsigned int *value, cudaStream_t stream);
 // Error word of the linear cross entropy's kernels (linear_ce.cu).
 cudaError_t status_linear_ce(unsigned int *value, cudaStream_t stream);

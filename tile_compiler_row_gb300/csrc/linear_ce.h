@@ -17,7 +17,6 @@ struct LinearCeArgs {
     void *dx, *dweight;         // backward outputs, either may be NULL
     int rows, width, vocab;
     void *ws;
-    unsigned int *status;
 };
 
 size_t linear_ce_workspace(int rows, int width, int vocab);

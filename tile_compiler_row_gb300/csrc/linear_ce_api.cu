@@ -8,14 +8,9 @@
 
 namespace {
 
+using tile::cuda_status;
 using tile::misaligned_to;
 using tile::Range;
-
-int cuda_status(cudaError_t err) {
-    if (err == cudaSuccess) return TILE_OK;
-    tile::set_last_cuda_error(static_cast<int>(err));
-    return TILE_ERR_CUDA;
-}
 
 int check_shape(int dtype, int rows, int width, int vocab) {
     if (dtype != TILE_DTYPE_BF16 && dtype != TILE_DTYPE_F16) return TILE_ERR_DTYPE;

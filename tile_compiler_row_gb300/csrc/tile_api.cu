@@ -14,6 +14,7 @@
 
 namespace {
 
+using tile::elem_size;
 using tile::misaligned_to;
 using tile::overlaps;
 
@@ -249,8 +250,6 @@ bool coaligned16(const Call &c) {
 
 // Checks shared by every row entry point.  Returns TILE_OK with *noop set
 // when there is nothing to launch.  No CUDA call is made.
-size_t elem_size(int dtype) { return two_byte(dtype) ? 2 : 4; }
-
 int validate(const Call &c, bool *noop) {
     *noop = false;
     if (!valid_op(c.op)) return TILE_ERR_OP;
@@ -900,7 +899,7 @@ int tile_check_device_status(cudaStream_t stream) {
         tile::status_row_sum_f16, tile::status_row_minmax_f16, tile::status_pairs,
         tile::status_backward, tile::status_backward_bf16, tile::status_backward_f16,
         tile::status_param_grad, tile::status_staged, tile::status_multi,
-        tile::status_block_norm, tile::status_block_norm_backward, tile::status_linear_ce};
+        tile::status_block_norm_backward, tile::status_linear_ce};
     for (auto f : fetch) {
         v = 0;
         const cudaError_t err = f(&v, stream);
