@@ -132,3 +132,11 @@ def test_no_workspace_for_sizes_past_an_int():
         assert f(4, 64, 300) > 0
         for sizes in ((BIG + 4, 64, 300), (4, BIG + 64, 300), (4, 64, BIG + 300), (4 - BIG, 64, 300)):
             assert f(*sizes) == 0
+
+
+def test_gradients_of_nothing_are_refused():
+    """Neither the hidden rows nor a gradient of them: no shape to go by."""
+    x, g = torch.zeros(2, 8), torch.zeros(8)
+    for pre in (True, False):
+        with pytest.raises(ValueError, match="hidden"):
+            tile.block_norm_backward(x, None, g, None, g, None, x, pre=pre)

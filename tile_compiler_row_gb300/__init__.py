@@ -1108,6 +1108,8 @@ def block_norm_backward(x, hidden, gamma_post, gate, gamma_pre, dhidden, dout, p
     are None."""
     import torch
     like = hidden if hidden is not None else dhidden
+    if like is None:
+        raise ValueError("hidden (with pre) or dhidden (without) must be a CUDA tensor")
     din, dresidual = torch.empty_like(like), torch.empty_like(like)
     dgamma_post = torch.empty_like(gamma_post) if post and gamma_post is not None else None
     dgate = torch.empty_like(gate) if gate is not None else None
