@@ -680,6 +680,22 @@ int tile_test_force_general_kernels(int on);
 int tile_test_staged_wait_timeout(int op, int plan_id, const tile_row_args_t *args,
                                   unsigned int spin_limit, cudaStream_t stream);
 
+/* The same for the block norm's gradients and the linear cross entropy
+ * (forward): the call, with the first row of the first program, or the first
+ * tiles of the first CTA pair, never copied, and waits of 16 ms instead of 2 s.
+ * BF16 rows of whole 16-byte vectors in CTAs of up to 256 threads (widths up to
+ * 5120, and above 16384 up to 32768), and BF16 rows of up to 4096 columns, are
+ * built for it; TILE_ERR_PLAN for others.  Else arguments and errors of
+ * tile_block_norm_backward and tile_linear_cross_entropy. */
+int tile_test_block_norm_backward_wait_timeout(const tile_block_norm_backward_args_t *args,
+                                               void *workspace, size_t workspace_bytes,
+                                               cudaStream_t stream);
+int tile_test_linear_cross_entropy_wait_timeout(int dtype, const void *in, const void *weight,
+                                                const long long *target, float *loss, float *lse,
+                                                int rows, int width, int vocab,
+                                                long long ignore_index, void *workspace,
+                                                size_t workspace_bytes, cudaStream_t stream);
+
 /* Run `op` (one of the first four op codes) with the built plan `plan_id`
  * instead of the selector's choice (used by the measured plan sweep and by
  * tests that check every plan; tile_run_plan_args_f32 covers every op).

@@ -37,6 +37,7 @@ __all__ = [
     "tile_run_backward_plan_f32", "tile_norm_param_grad_workspace_bytes",
     "tile_block_norm", "tile_block_norm_backward", "tile_block_norm_backward_workspace_bytes",
     "tile_block_norm_backward_gated_workspace_bytes",
+    "tile_test_block_norm_backward_wait_timeout", "tile_test_linear_cross_entropy_wait_timeout",
     "tile_linear_cross_entropy", "tile_linear_cross_entropy_workspace_bytes",
     "tile_linear_cross_entropy_backward", "tile_linear_cross_entropy_backward_workspace_bytes",
     "block_norm", "block_norm_backward", "linear_cross_entropy", "linear_cross_entropy_backward",
@@ -196,6 +197,10 @@ def load():
         "tile_block_norm": [ctypes.POINTER(TileBlockNormArgs), P],
         "tile_block_norm_backward": [ctypes.POINTER(TileBlockNormBackwardArgs), P,
                                      ctypes.c_size_t, P],
+        "tile_test_block_norm_backward_wait_timeout": [
+            ctypes.POINTER(TileBlockNormBackwardArgs), P, ctypes.c_size_t, P],
+        "tile_test_linear_cross_entropy_wait_timeout": [I, P, P, P, P, P, I, I, I,
+                                                        ctypes.c_longlong, P, ctypes.c_size_t, P],
         "tile_linear_cross_entropy": [I, P, P, P, P, P, I, I, I, ctypes.c_longlong, P,
                                       ctypes.c_size_t, P],
         "tile_linear_cross_entropy_backward": [I, P, P, P, P, P, P, P, I, I, I,
@@ -942,10 +947,18 @@ def tile_block_norm_backward_gated_workspace_bytes(rows, width, gate_rows):
     return load().tile_block_norm_backward_gated_workspace_bytes(rows, width, gate_rows)
 
 
+def tile_test_block_norm_backward_wait_timeout(*args, **kwargs):
+    """Test hook: ``tile_block_norm_backward`` with a copy withheld, so that
+    its waits give up (see include/tile_rows.h)."""
+    tile_block_norm_backward(*args, **kwargs,
+                             _entry="tile_test_block_norm_backward_wait_timeout")
+
+
 def tile_block_norm_backward(x, hidden, dhidden, dout, din, dresidual, workspace,
                              gamma_post=None, gate=None, gamma_pre=None, dgamma_post=None,
                              dgate=None, dgamma_pre=None, post=True, pre=True, rows_per_gate=0,
-                             residual_scale=1.0, eps=1e-5, stream=None):
+                             residual_scale=1.0, eps=1e-5, stream=None,
+                             _entry="tile_block_norm_backward"):
     """The gradients of ``tile_block_norm`` (see include/tile_rows.h).
     ``hidden`` is the forward's; ``dhidden`` may be None (``dout`` is then
     the only gradient), as may any parameter gradient."""
@@ -967,7 +980,7 @@ def tile_block_norm_backward(x, hidden, dhidden, dout, din, dresidual, workspace
         _ptr(dgamma_pre, "dgamma_pre", f32, vec, dev), rows, width, per,
         (1 if post else 0) | (2 if pre else 0), residual_scale, eps, code)
     ws, nbytes = _workspace(workspace, dev)
-    _call_on(dev, stream, "tile_block_norm_backward", ctypes.byref(a), ws, nbytes)
+    _call_on(dev, stream, _entry, ctypes.byref(a), ws, nbytes)
 
 
 # ---- linear cross entropy -------------------------------------------------------
@@ -1001,14 +1014,21 @@ def _ce_inputs(x, weight, target, ignore_index):
             _ptr(target, "target", torch.int64, (rows,), dev), rows, width, vocab)
 
 
+def tile_test_linear_cross_entropy_wait_timeout(*args, **kwargs):
+    """Test hook: ``tile_linear_cross_entropy`` with a copy withheld, so that
+    its waits give up (see include/tile_rows.h)."""
+    tile_linear_cross_entropy(*args, **kwargs,
+                              _entry="tile_test_linear_cross_entropy_wait_timeout")
+
+
 def tile_linear_cross_entropy(x, weight, target, loss, lse, workspace, ignore_index=-100,
-                              stream=None):
+                              stream=None, _entry="tile_linear_cross_entropy"):
     """loss and log-sum-exp of the rows' logits x weight^T (bfloat16 or
     float16) without keeping them; see include/tile_rows.h."""
     import torch
     code, dev, px, pw, pt, rows, width, vocab = _ce_inputs(x, weight, target, ignore_index)
     ws, nbytes = _workspace(workspace, dev)
-    _call_on(dev, stream, "tile_linear_cross_entropy", code, px, pw, pt,
+    _call_on(dev, stream, _entry, code, px, pw, pt,
              _ptr(loss, "loss", torch.float32, (rows,), dev),
              _ptr(lse, "lse", torch.float32, (rows,), dev), rows, width, vocab, ignore_index, ws,
              nbytes)

@@ -380,6 +380,7 @@ struct BlockArgs {
     int post, pre;
     float scale, eps;
     unsigned int *status;   // backward
+    bool withheld;          // backward, tests only (tile_test_block_norm_backward_wait_timeout)
 };
 
 // What the pointers of a call allow: every row and parameter row on vectors;

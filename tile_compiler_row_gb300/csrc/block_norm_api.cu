@@ -104,8 +104,12 @@ size_t tile_block_norm_backward_gated_workspace_bytes(int rows, int width, int g
     return tile::block_norm_backward_workspace(rows, width, gates);
 }
 
-int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *workspace,
-                             size_t workspace_bytes, cudaStream_t stream) {
+}  // extern "C"
+
+namespace {
+
+int run_backward(const tile_block_norm_backward_args_t *args, void *workspace,
+                 size_t workspace_bytes, bool withheld, cudaStream_t stream) {
     if (args == nullptr) return TILE_ERR_NULL;
     const tile_block_norm_backward_args_t &c = *args;
     const int st = check_shape(c.norms, c.dtype, c.rows, c.width, c.gate, c.rows_per_gate,
@@ -166,8 +170,25 @@ int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *
     if (tile::any_overlap(out, 6, in, 7)) return TILE_ERR_ALIAS;
     const cudaError_t inj = tile::injected_launch_failure();
     if (inj != cudaSuccess) return cuda_status(inj);
-    return cuda_status(tile::launch_block_norm_backward(
-        c.dtype, access_of(mats, 6, params, 3, c.width, es), a, stream));
+    a.withheld = withheld;
+    const cudaError_t err = tile::launch_block_norm_backward(
+        c.dtype, access_of(mats, 6, params, 3, c.width, es), a, stream);
+    return withheld && err == cudaErrorNotSupported ? TILE_ERR_PLAN : cuda_status(err);
+}
+
+}  // namespace
+
+extern "C" {
+
+int tile_block_norm_backward(const tile_block_norm_backward_args_t *args, void *workspace,
+                             size_t workspace_bytes, cudaStream_t stream) {
+    return run_backward(args, workspace, workspace_bytes, false, stream);
+}
+
+int tile_test_block_norm_backward_wait_timeout(const tile_block_norm_backward_args_t *args,
+                                               void *workspace, size_t workspace_bytes,
+                                               cudaStream_t stream) {
+    return run_backward(args, workspace, workspace_bytes, true, stream);
 }
 
 }  // extern "C"

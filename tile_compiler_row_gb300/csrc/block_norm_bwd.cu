@@ -380,10 +380,10 @@ struct Programs {
     int per_gate;   // programs of a gate row, 0: contiguous ranges of rows
 };
 
-template <class T, bool SHIFT, bool CL, int MAXT, int MINB>
+template <class T, bool SHIFT, bool CL, int MAXT, int MINB, bool WITHHELD = false>
 cudaError_t launch_ring(const BlockArgs &a, RingPlan p, cudaStream_t stream, Programs *out) {
     static OccupancyCache cache;
-    const auto kernel = block_norm_ring_kernel<T, kRingVecs, SHIFT, CL, MAXT, MINB>;
+    const auto kernel = block_norm_ring_kernel<T, kRingVecs, SHIFT, CL, MAXT, MINB, WITHHELD>;
     int per_sm = 0;
     const cudaError_t err = occupancy(kernel, cache, p.workers, p.smem, &per_sm);
     if (err != cudaSuccess) return err;
@@ -403,6 +403,13 @@ template <class T, bool SHIFT>
 cudaError_t launch_ring_typed(const BlockArgs &a, const RingPlan &p, cudaStream_t stream,
                               Programs *out) {
     const bool one = p.cluster == 1;
+    if (a.withheld) {
+        if constexpr (std::is_same<T, __nv_bfloat16>::value && !SHIFT)
+            if (p.workers <= 256)
+                return one ? launch_ring<T, false, false, 256, 2, true>(a, p, stream, out)
+                           : launch_ring<T, false, true, 256, 2, true>(a, p, stream, out);
+        return cudaErrorNotSupported;
+    }
     if (p.workers <= 256)
         return one ? launch_ring<T, SHIFT, false, 256, 2>(a, p, stream, out)
                    : launch_ring<T, SHIFT, true, 256, 2>(a, p, stream, out);
@@ -435,8 +442,10 @@ template <class T>
 cudaError_t launch_typed(const BlockArgs &a, BlockAccess access, cudaStream_t stream,
                          Programs *out) {
     constexpr int N = Vec<T>::N;
+    if (a.withheld && access != ACCESS_VECTORS) return cudaErrorNotSupported;
     if (access == ACCESS_VECTORS) {
         const RingPlan p = ring_plan<T, false>(a.width);
+        if (a.withheld && p.cluster == 0) return cudaErrorNotSupported;
         if (p.cluster > 0) return launch_ring_typed<T, false>(a, p, stream, out);
         return launch_registers<T, N, 32, true>(a, stream, out);
     }

@@ -27,8 +27,9 @@
 // every CTA (st.async on an mbarrier): no cluster-wide barrier in the loop.
 //
 // Waits are bounded: one that runs out sets the device status word and an
-// abort flag, after which no thread of the CTA waits and nothing is copied;
-// the outputs are then invalid, and the call ends.
+// abort flag, after which no thread of the CTA waits for a copy and nothing is
+// copied; the sums are exchanged all the same, row by row.  The outputs are
+// then invalid, and the call ends.
 #pragma once
 
 #include "block_norm.cuh"
@@ -72,11 +73,14 @@ __device__ __forceinline__ uint4 shared_vec(uint32_t at) {
     return v;
 }
 
-template <class T, int K, bool SHIFT, bool CL, int MAXT, int MINB>
+// WITHHELD (tests only): the first program's first row is not copied, and
+// waits are short.
+template <class T, int K, bool SHIFT, bool CL, int MAXT, int MINB, bool WITHHELD = false>
 __global__ void __launch_bounds__(MAXT, MINB)
     block_norm_ring_kernel(const BlockArgs a, const RingPlan plan) {
     using X = Vec<T>;
     constexpr int N = X::N, P = X::P;   // elements, pairs of a vector
+    constexpr unsigned int SPINS = WITHHELD ? kTestBarSpins : kBarSpins;
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ __align__(16) float warp_part[2][6][16];
     __shared__ __align__(16) float cta_part[2][8][8];
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
     int issued = 0;   // thread 0: rows copied so far, at most `slots` ahead
     if (tid == 0)
         for (; issued < slots && issued < walk.count; ++issued)
-            copy_row(walk.first + static_cast<long long>(issued) * walk.step, issued);
+            if (!WITHHELD || issued > 0 || blockIdx.x > 0) copy_row(walk.first + static_cast<long long>(issued) * walk.step, issued);
 
     auto first = [&](int k) { return (v0 + k * W + tid) * N - shift; };   // column of vector k
     auto mine = [&](int k) { return k * W + tid < nv; };
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
             }
             X::widen(q, v);
         };
-        bar_wait(smem_u32(&full[s]), phase, aborted, a.status, BLOCK_WAIT_TIMEOUT);
+        bar_wait<SPINS>(smem_u32(&full[s]), phase, aborted, a.status, BLOCK_WAIT_TIMEOUT);
         if (SHIFT && nv > 0 && part_at(row) + static_cast<long long>(nv) * N > a.rows * width) {
             // the block at the matrix's end: not copied
             if (tid < 4 * N) {
@@ -285,8 +289,8 @@ __global__ void __launch_bounds__(MAXT, MINB)
                         : "memory");
             }
             __syncwarp();
-            bar_wait(smem_u32(&peer[turn]), static_cast<unsigned int>(i_row >> 1) & 1u, aborted,
-                     a.status, BLOCK_WAIT_TIMEOUT);
+            bar_wait_round<SPINS>(smem_u32(&peer[turn]), static_cast<unsigned int>(i_row >> 1) & 1u,
+                                  aborted, a.status, BLOCK_WAIT_TIMEOUT);
             __syncwarp();
             const volatile float *cp = &cta_part[turn][lane & 3][value];
             joined = cp[0] + cp[4 * 8];   // CTAs l & 3 and 4 more (0 where there are fewer)
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
     // an aborted CTA waits (bounded) for the copies it issued
     if (tid == 0 && *aborted)
         for (int i = issued > slots ? issued - slots : 0; i < issued; ++i)
-            for (unsigned int n = 0; n < kBarSpins; ++n)
+            for (unsigned int n = 0; n < SPINS; ++n)
                 if (bar_test(smem_u32(&full[i % slots]), (i / slots) & 1)) break;
     __syncwarp();
     if constexpr (CL) cluster_barrier();   // no CTA leaves while a peer may write to it

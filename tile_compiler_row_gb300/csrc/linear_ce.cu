@@ -327,8 +327,11 @@ __device__ __forceinline__ void store_rows16(unsigned short *out, long long ld, 
 // long one, and all go on in turn from there (tile_at).
 //
 // PARTS: sums of more than PART_BLOCKS k blocks, one accumulator a part.
-template <int EPI0, int EPI1, bool BF16, bool PARTS>
+// WITHHELD (tests only): the first pair's first copies are not made, and waits
+// are short.
+template <int EPI0, int EPI1, bool BF16, bool PARTS, bool WITHHELD>
 __device__ __forceinline__ void gemm(const GemmMaps &maps, const GemmArgs &g) {
+    constexpr unsigned int SPINS = WITHHELD ? kTestBarSpins : kBarSpins;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * MOST_STAGES + 4];
     __shared__ uint32_t tmem_slot;
@@ -431,23 +434,25 @@ __device__ __forceinline__ void gemm(const GemmMaps &maps, const GemmArgs &g) {
                 const int m0 = w.m * BM + rank * CM, n0 = w.n * job.bn + rank * half;
                 const unsigned int bytes = (job.a_rows + half) * BK * 2;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!(ok = bar_wait(empty(stage), phase ^ 1u, aborted, g.status,
-                                        CE_WAIT_TIMEOUT)))
+                    if (!(ok = bar_wait<SPINS>(empty(stage), phase ^ 1u, aborted, g.status,
+                                               CE_WAIT_TIMEOUT)))
                         break;
                     const uint32_t a = base + stage * stage_bytes, b = a + a_bytes;
                     const uint32_t bar = peer_addr(full(stage), 0);
-                    if (rank == 0) bar_expect_tx(full(stage), 2 * bytes);
-                    if (a_mn(EPI)) {
-                        tma_load(a, &maps.a[J], m0, kb * BK, bar);
-                        tma_load(a + 8192, &maps.a[J], m0 + 64, kb * BK, bar);
-                    } else {
-                        tma_load(a, &maps.a[J], kb * BK, m0, bar);
-                    }
-                    if (b_mn(EPI)) {   // (256 columns to a tile)
-                        tma_load(b, &maps.b[J], n0, kb * BK, bar);
-                        tma_load(b + 8192, &maps.b[J], n0 + 64, kb * BK, bar);
-                    } else {
-                        tma_load(b, &maps.b[J], kb * BK, n0, bar);
+                    if (!WITHHELD || issued > 0 || pair > 0) {
+                        if (rank == 0) bar_expect_tx(full(stage), 2 * bytes);
+                        if (a_mn(EPI)) {
+                            tma_load(a, &maps.a[J], m0, kb * BK, bar);
+                            tma_load(a + 8192, &maps.a[J], m0 + 64, kb * BK, bar);
+                        } else {
+                            tma_load(a, &maps.a[J], kb * BK, m0, bar);
+                        }
+                        if (b_mn(EPI)) {   // (256 columns to a tile)
+                            tma_load(b, &maps.b[J], n0, kb * BK, bar);
+                            tma_load(b + 8192, &maps.b[J], n0 + 64, kb * BK, bar);
+                        } else {
+                            tma_load(b, &maps.b[J], kb * BK, n0, bar);
+                        }
                     }
                     ++issued;
                     if (++stage == stages) {
@@ -461,7 +466,7 @@ __device__ __forceinline__ void gemm(const GemmMaps &maps, const GemmArgs &g) {
         // land in shared memory that it no longer owns.
         if (*aborted && rank == 0)
             for (long long i = issued > stages ? issued - stages : 0; i < issued; ++i)
-                for (unsigned int n = 0; n < kBarSpins; ++n)
+                for (unsigned int n = 0; n < SPINS; ++n)
                     if (bar_test(full(static_cast<int>(i % stages)), (i / stages) & 1)) break;
     } else if (warp == EPI_WARPS + 1 && lane == 0 && rank == 0) {   // MMA issuer
         int stage = 0, acc = 0;
@@ -474,16 +479,16 @@ __device__ __forceinline__ void gemm(const GemmMaps &maps, const GemmArgs &g) {
                 const uint32_t idesc = mma_idesc(BF16, a_mn(EPI), b_mn(EPI), BM, g.job[J].bn);
                 int kb = kb0;
                 do {   // the whole sum, or a part of it
-                    if (!(ok = bar_wait(acc_empty(acc), acc_phase ^ 1u, aborted, g.status,
-                                        CE_WAIT_TIMEOUT)))
+                    if (!(ok = bar_wait<SPINS>(acc_empty(acc), acc_phase ^ 1u, aborted, g.status,
+                                               CE_WAIT_TIMEOUT)))
                         return;
                     tc_fence_after();
                     const uint32_t d = tmem + acc * BN;
                     const int end = PARTS ? min(kb1, kb + PART_BLOCKS) : kb1;
                     bool first = true;
                     for (; kb < end; ++kb) {
-                        if (!(ok = bar_wait(full(stage), phase, aborted, g.status,
-                                            CE_WAIT_TIMEOUT)))
+                        if (!(ok = bar_wait<SPINS>(full(stage), phase, aborted, g.status,
+                                                   CE_WAIT_TIMEOUT)))
                             break;
                         tc_fence_after();
                         const uint32_t a = base + stage * stage_bytes, b = a + a_bytes;
@@ -511,7 +516,7 @@ __device__ __forceinline__ void gemm(const GemmMaps &maps, const GemmArgs &g) {
         }
         if (*aborted) {   // wait (bounded) until no MMA touches the pair's memory
             tc_commit(acc_full(acc));
-            for (unsigned int n = 0; n < kBarSpins; ++n)
+            for (unsigned int n = 0; n < SPINS; ++n)
                 if (bar_test(acc_full(acc), acc_phase)) break;
         }
     } else if (warp < EPI_WARPS) {
@@ -527,8 +532,9 @@ __device__ __forceinline__ void gemm(const GemmMaps &maps, const GemmArgs &g) {
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         // whether the accumulator that is due has come
         auto ready = [&] {
-            const bool in = __all_sync(0xffffffffu, bar_wait(acc_full(acc), acc_phase, aborted,
-                                                             g.status, CE_WAIT_TIMEOUT));
+            const bool in =
+                __all_sync(0xffffffffu, bar_wait<SPINS>(acc_full(acc), acc_phase, aborted, g.status,
+                                                        CE_WAIT_TIMEOUT));
             if (in) tc_fence_after();
             return in;
         };
@@ -676,6 +682,10 @@ __device__ __forceinline__ void gemm(const GemmMaps &maps, const GemmArgs &g) {
         }
         if (lane == 0) store_wait<0>();   // the stores are written before the CTA ends
     }
+    // (after an abort: and the copies that the producer's wait does not count, of
+    // a stage that only one CTA of the pair has issued: 0.1 ms, they take 1 us)
+    if (*aborted)
+        for (int i = 0; i < 100; ++i) __nanosleep(1000);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -687,7 +697,11 @@ __device__ __forceinline__ void gemm(const GemmMaps &maps, const GemmArgs &g) {
 template <int EPI0, int EPI1, bool BF16>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs g) {
-    gemm<EPI0, EPI1, BF16, false>(maps, g);
+    gemm<EPI0, EPI1, BF16, false, false>(maps, g);
+}
+__global__ void __launch_bounds__(GEMM_THREADS, 1)
+    gemm_withheld_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs g) {
+    gemm<EPI_LSE, EPI_NONE, true, false, true>(maps, g);
 }
 // 16 registers fewer than 320 threads could have leave room for a CTA of the
 // next kernel beside this one, whose dot products (join_lse_kernel) then run
@@ -695,7 +709,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 template <int EPI, bool BF16>
 __global__ void __maxnreg__(152)
     gemm_parts_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs g) {
-    gemm<EPI, EPI_NONE, BF16, true>(maps, g);
+    gemm<EPI, EPI_NONE, BF16, true, false>(maps, g);
 }
 
 // ---- a row's own logit -----------------------------------------------------------------
@@ -1347,7 +1361,13 @@ cudaError_t launch_linear_ce(const LinearCeArgs &args, cudaStream_t stream) {
     g.status = status;
     CE_TRY(make_map(&maps.a[0], bf16, x, rows, width, x_ld, g.job[0].a_rows));
     CE_TRY(make_map(&maps.b[0], bf16, w, vocab, width, w_ld, bn / 2));
-    CE_TRY((launch_gemm<EPI_LSE, EPI_NONE>(bf16, maps, g, stream)));
+    if (args.withheld) {
+        static std::atomic<int> ready[kMaxDevices];
+        if (!bf16 || width > PART_BLOCKS * BK) return cudaErrorNotSupported;
+        CE_TRY(launch_gemm_kernel(gemm_withheld_kernel, ready, maps, g, job_tiles(g.job[0]), stream));
+    } else {
+        CE_TRY((launch_gemm<EPI_LSE, EPI_NONE>(bf16, maps, g, stream)));
+    }
     const JoinArgs j = {s.partial, static_cast<const unsigned short *>(x),
                         static_cast<const unsigned short *>(w), x_ld, w_ld, args.target,
                         packs ? s.place : nullptr, args.ignore, rows, width, vocab,

@@ -17,6 +17,7 @@ struct LinearCeArgs {
     void *dx, *dweight;         // backward outputs, either may be NULL
     int rows, width, vocab;
     void *ws;
+    bool withheld;              // forward, tests only (tile_test_linear_cross_entropy_wait_timeout)
 };
 
 size_t linear_ce_workspace(int rows, int width, int vocab);

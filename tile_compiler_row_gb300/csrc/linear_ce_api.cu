@@ -38,10 +38,13 @@ size_t tile_linear_cross_entropy_backward_workspace_bytes(int rows, int width, i
     return tile::linear_ce_backward_workspace(rows, width, vocab);
 }
 
-int tile_linear_cross_entropy(int dtype, const void *in, const void *weight,
-                              const long long *target, float *loss, float *lse, int rows,
-                              int width, int vocab, long long ignore_index, void *workspace,
-                              size_t workspace_bytes, cudaStream_t stream) {
+}  // extern "C"
+
+namespace {
+
+int run_forward(int dtype, const void *in, const void *weight, const long long *target, float *loss,
+                float *lse, int rows, int width, int vocab, long long ignore_index, void *workspace,
+                size_t workspace_bytes, bool withheld, cudaStream_t stream) {
     const int st = check_shape(dtype, rows, width, vocab);
     if (st != TILE_OK) return st;
     if (rows == 0) return TILE_OK;
@@ -72,7 +75,30 @@ int tile_linear_cross_entropy(int dtype, const void *in, const void *weight,
     a.width = width;
     a.vocab = vocab;
     a.ws = workspace;
-    return cuda_status(tile::launch_linear_ce(a, stream));
+    a.withheld = withheld;
+    const cudaError_t err = tile::launch_linear_ce(a, stream);
+    return withheld && err == cudaErrorNotSupported ? TILE_ERR_PLAN : cuda_status(err);
+}
+
+}  // namespace
+
+extern "C" {
+
+int tile_linear_cross_entropy(int dtype, const void *in, const void *weight,
+                              const long long *target, float *loss, float *lse, int rows,
+                              int width, int vocab, long long ignore_index, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+    return run_forward(dtype, in, weight, target, loss, lse, rows, width, vocab, ignore_index,
+                       workspace, workspace_bytes, false, stream);
+}
+
+int tile_test_linear_cross_entropy_wait_timeout(int dtype, const void *in, const void *weight,
+                                                const long long *target, float *loss, float *lse,
+                                                int rows, int width, int vocab,
+                                                long long ignore_index, void *workspace,
+                                                size_t workspace_bytes, cudaStream_t stream) {
+    return run_forward(dtype, in, weight, target, loss, lse, rows, width, vocab, ignore_index,
+                       workspace, workspace_bytes, true, stream);
 }
 
 int tile_linear_cross_entropy_backward(int dtype, const void *in, const void *weight,

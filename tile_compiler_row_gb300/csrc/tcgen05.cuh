@@ -53,19 +53,35 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, unsigned int parity) {
 // up to 4.0 us (measured), so a wait that runs out has lasted 2 s; a tile
 // takes microseconds, or 0.1 s where a gradient sums over 20 million tokens.
 constexpr unsigned int kBarSpins = 1u << 19;
+constexpr unsigned int kTestBarSpins = 1u << 12;   // where a test withholds a copy: 16 ms
 
 // Bounded wait for the phase `parity` of a barrier.  A wait that runs out
 // sets `bit` in the device status word and the CTA's abort flag; every
 // other wait of the CTA then gives up too, so no wait can hang the GPU.
+template <unsigned int SPINS = kBarSpins>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned int parity, volatile int *abort_flag,
                                          unsigned int *status, unsigned int bit) {
-    for (unsigned int i = 0; i < kBarSpins; ++i) {
+    for (unsigned int i = 0; i < SPINS; ++i) {
         if (bar_test(bar, parity)) return true;
         if ((i & 63u) == 63u && *abort_flag) return false;
     }
     *abort_flag = 1;
     atomicOr(status, bit);
     return false;
+}
+
+// The same for what every CTA of a cluster sends in each round, whether its own
+// waits gave up or not: it takes no notice of the abort flag, since a CTA that
+// went on without it would count a later round's bytes for this one, and waits
+// four times as long, as the others may have waited for something first.
+template <unsigned int SPINS = kBarSpins>
+__device__ __forceinline__ void bar_wait_round(uint32_t bar, unsigned int parity,
+                                               volatile int *abort_flag, unsigned int *status,
+                                               unsigned int bit) {
+    for (unsigned int i = 0; i < 4 * SPINS; ++i)
+        if (bar_test(bar, parity)) return;
+    *abort_flag = 1;
+    atomicOr(status, bit);
 }
 
 // ---- TMA -------------------------------------------------------------------------
