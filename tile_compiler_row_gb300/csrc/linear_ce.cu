@@ -311,11 +311,11 @@ __device__ __forceinline__ void store_rows16(unsigned short *out, long long ld, 
 // B tiles in shared memory, one thread of the pair issues the MMAs into one of
 // two accumulators in tensor memory (256 columns each), and eight warps turn
 // the other into the epilogue's output.  A pair reads 32 KiB per CTA and 64
-// columns of K from L2, where a CTA with a tile of its own reads 48: L2
-// delivers some 12.5 TB/s, which bound the gradients' products with single
-// CTAs (56 % of the tensor cores' time in use).  At 4096 tokens x 4096 columns
-// x 32768 entries in BF16 the tensor cores work 94 % of the time for the
-// logits (0.53 ms), 91 % for g (0.56 ms) and 88 % for dx and dW (1.19 ms): the
+// columns of K from L2, where a CTA with a tile of its own reads 48, which bound
+// the gradients' products with single CTAs (56 % of the tensor cores' time in
+// use; with pairs L2 moves 17 TB/s there).  At 4096 tokens x 4096 columns
+// x 32768 entries in BF16 the tensor cores work 95 % of the time for the
+// logits (0.52 ms), 91 % for g (0.55 ms) and 88 % for dx and dW (1.15 ms): the
 // clock under the power limit is what bounds long calls.  A few rows against a
 // large weight are bound by reading it (5 x 2048 x 32768: 29 us, 20 at the
 // rate of a copy); their backward reads it twice.
