@@ -65,22 +65,25 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned int parity, vola
         if (bar_test(bar, parity)) return true;
         if ((i & 63u) == 63u && *abort_flag) return false;
     }
-    *abort_flag = 1;
+    if (*abort_flag == 0) *abort_flag = 1;
     atomicOr(status, bit);
     return false;
 }
 
 // The same for what every CTA of a cluster sends in each round, whether its own
-// waits gave up or not: it takes no notice of the abort flag, since a CTA that
-// went on without it would count a later round's bytes for this one, and waits
-// four times as long, as the others may have waited for something first.
+// waits gave up or not: it goes on where only a bar_wait has, since a CTA that
+// left out a round would count a later round's bytes for it, and waits four
+// times as long, as the others may have waited for something first.  One that
+// runs out all the same is the CTA's last.
 template <unsigned int SPINS = kBarSpins>
 __device__ __forceinline__ void bar_wait_round(uint32_t bar, unsigned int parity,
                                                volatile int *abort_flag, unsigned int *status,
                                                unsigned int bit) {
-    for (unsigned int i = 0; i < 4 * SPINS; ++i)
+    for (unsigned int i = 0; i < 4 * SPINS; ++i) {
         if (bar_test(bar, parity)) return;
-    *abort_flag = 1;
+        if ((i & 63u) == 63u && *abort_flag == 2) return;
+    }
+    *abort_flag = 2;
     atomicOr(status, bit);
 }
 
