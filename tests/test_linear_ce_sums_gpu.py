@@ -3,10 +3,11 @@ sum of `width` products allows (test_linear_ce_gpu.py).
 
 A logit is added up in parts of at most 4096 columns, which the tensor cores add
 16 products at a time; parts are joined in FP32 with rounding, and 2^-26 of a
-part is put back for each of its n <= 256 steps.  What a step loses (the
-published measurements of tensor cores): every product and the sum so far is
-cut off 2 bits below the 24 of the largest of them, and the new sum at its 24
-bits, in all at most 16 2^-25 + 2^-23 = 5 2^-23 of it, toward 0.
+part is put back for each of its n <= 256 steps.  What a step may lose, by the
+model that Fasi, Higham, Mikaitis and Pranesh measured on earlier tensor cores
+(Numerical behavior of NVIDIA tensor cores, 2021): every product and the sum so
+far is cut off 2 bits below the 24 of the largest of them, and the new sum at
+its 24 bits, in all at most 16 2^-25 + 2^-23 = 5 2^-23 of it, toward 0.
 
 * Sums that are exact lose nothing: what is put back is n 2^-26 of the logit.
 * Rows of random signs: what the products lose is as often added as taken, and
