@@ -495,6 +495,211 @@ int tile_linear_cross_entropy_backward(int dtype, const void *in, const void *we
                                        void *workspace, size_t workspace_bytes,
                                        cudaStream_t stream);
 
+/* ---- embedding ------------------------------------------------------------
+ * The lookup at the start of a language model and its gradient; the weight is
+ * often the linear head's too, whose gradient
+ * tile_linear_cross_entropy_backward leaves.  (The notes this library follows
+ * have no counterpart.)  For every row i,
+ *
+ *   out[i] = scale * weight[tokens[i]]
+ *
+ * out [rows][width] and weight [vocab][width] of `dtype`, contiguous; tokens
+ * [rows] 64-bit integers on the device.  The product is FP32, rounded once.  A
+ * token equal to ignore_index gives a row of zeros (whatever vocabulary entry
+ * that might be); another one outside [0, vocab) a row of NaN, and sets the
+ * device status word (tile_check_device_status).  Any alignment of the element
+ * type works; 16-byte aligned rows of whole 16-byte vectors are the fastest.
+ * rows == 0 is a no-op; rows up to 2^24, vocab up to 2^30 (TILE_ERR_SHAPE).
+ * TILE_ERR_EPS for a scale that is not finite; other rules and errors as the
+ * row entry points. */
+int tile_embedding(int dtype, const long long *tokens, const void *weight, void *out, int rows,
+                   int width, int vocab, float scale, long long ignore_index,
+                   cudaStream_t stream);
+
+/* Its gradient: dweight[v] = scale * (sum of dout[i] over the rows with
+ * tokens[i] = v), of the whole [vocab][width] matrix (zero where v does not
+ * occur), or, with accumulate != 0, that added to what dweight holds, rounded
+ * once; rows of dweight whose token does not occur are then neither read nor
+ * written.  dweight is of `dtype` or FP32 (TILE_ERR_DTYPE).  Rows whose token is
+ * ignore_index or out of range (the status word) take no part, whatever they
+ * hold.  Sums are FP32, over the positions in order in parts that depend on
+ * the tokens alone: no atomics on values, results are bitwise reproducible.
+ *
+ * `workspace`: device memory of the caller, 256-byte aligned, at least
+ * tile_embedding_backward_workspace_bytes(rows, width, vocab) bytes (0 for few
+ * rows): the positions sorted by token, and partial sums of tokens that occur
+ * often, 8 width bytes for each 64 rows, at most 1024 of them.  Calls that
+ * overlap in time need workspaces of their own.  rows == 0 writes a zero
+ * dweight, or nothing where it accumulates.  May be captured into a CUDA
+ * graph. */
+size_t tile_embedding_backward_workspace_bytes(int rows, int width, int vocab);
+int tile_embedding_backward(int dtype, int dweight_dtype, const long long *tokens,
+                            const void *dout, void *dweight, int rows, int width, int vocab,
+                            float scale, long long ignore_index, int accumulate, void *workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
+
+/* ---- policy loss ------------------------------------------------------------
+ * The clipped loss that a policy is trained with on sampled sequences, with a
+ * term that holds it near a reference, from the negative log probabilities
+ * that tile_linear_cross_entropy returns as `loss`.  (The notes this library
+ * follows have no counterpart.)  For every token, with r = exp(old_nll - nll)
+ * and q = nll - ref_nll,
+ *
+ *   l = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *       + kl_coef (exp(q) - q - 1)
+ *
+ * where A is the token's advantage, or its sequence's with
+ * TILE_POLICY_SEQUENCE_ADVANTAGE.  Writes
+ *
+ *   stats    [4] FP32: the mean of l, of its first term, of exp(q) - q - 1 and
+ *            of whether the clip holds r A back
+ *   weights  [sequences] FP32: the weight of each token of a sequence in the
+ *            means, which the gradient takes
+ *
+ * The means are over all tokens that count, or, with
+ * TILE_POLICY_SEQUENCE_MEAN, over the sequences with such tokens of the means
+ * over them.  Where nothing counts, all are 0.
+ *
+ * Sequences lie one behind the other: sequence s is the rows from offsets[s] up
+ * to offsets[s + 1] ([sequences + 1] 64-bit integers on the device that do not
+ * fall; sequences may be empty).  Rows before the first and behind the last
+ * one do not count, nor do rows whose target is ignore_index; what they hold
+ * is not used.  Offsets that fall or leave [0, rows] set the device
+ * status word and make stats NaN.  offsets NULL: one sequence of all rows
+ * (sequences 1).  target NULL: every row counts.  ref_nll NULL: no such term
+ * (kl_coef 0).
+ *
+ * nll, old_nll, ref_nll [rows], advantage [rows] or [sequences]: FP32.  Whether r
+ * is held back is decided from old_nll - nll as if it had not been rounded; r A
+ * equal to its bound is not.  An advantage of 0 gives a first term of 0.  Sums
+ * are FP32 over 1024 rows and FP64 beyond, bitwise reproducible.  `workspace`:
+ * 16-byte aligned device memory of the caller; calls that overlap in time need
+ * workspaces of their own.  rows == 0 writes zeros.  TILE_ERR_EPS for clip_low
+ * outside [0, 1], a negative or NaN clip_high or a kl_coef that is not finite;
+ * TILE_ERR_SHAPE for rows or sequences above 2^30, sequences < 1, or other than
+ * 1 without offsets; TILE_ERR_OP for unknown flags; other rules and errors as
+ * the row entry points.  May be captured into a CUDA graph. */
+#define TILE_POLICY_SEQUENCE_ADVANTAGE 1   /* advantage is [sequences]            */
+#define TILE_POLICY_SEQUENCE_MEAN      2   /* the mean of the sequences' means    */
+
+typedef struct tile_policy_loss_args {
+    const float *nll, *old_nll;   /* [rows]                                       */
+    const float *ref_nll;         /* [rows] or NULL                               */
+    const float *advantage;       /* [rows], or [sequences]                       */
+    const long long *target;      /* [rows] or NULL                               */
+    const long long *offsets;     /* [sequences + 1] or NULL                      */
+    long long ignore_index;
+    int rows, sequences;
+    int flags;                    /* TILE_POLICY_*                                */
+    float clip_low, clip_high, kl_coef;
+} tile_policy_loss_args_t;
+
+size_t tile_policy_loss_workspace_bytes(int rows, int sequences);
+int tile_policy_loss(const tile_policy_loss_args_t *args, float *stats, float *weights,
+                     void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Its gradient for the forward's `weights` and the gradient dloss ([1] FP32 on
+ * the device; NULL for 1) of stats[0]: dnll [rows] FP32,
+ *
+ *   dnll = dloss weight (r A, or 0 where the clip holds it back,
+ *                        + kl_coef (exp(q) - 1))
+ *
+ * and 0 for rows that do not count: the dloss of
+ * tile_linear_cross_entropy_backward.  args as the forward's
+ * (TILE_POLICY_SEQUENCE_MEAN is in the weights and plays no part).  rows == 0
+ * is a no-op. */
+int tile_policy_loss_backward(const tile_policy_loss_args_t *args, const float *weights,
+                              const float *dloss, float *dnll, cudaStream_t stream);
+
+/* ---- gradient norm and AdamW step ---------------------------------------------
+ * Over many tensors at once, in one launch for up to 1024 (norm) or 384 (step)
+ * of them.  (The notes this library follows have no counterpart.)
+ *
+ * tile_grad_norm writes out [2] FP32:
+ *
+ *   out[0] = norm = scale * sqrt(sum over all tensors of g^2)
+ *   out[1] = factor = scale * min(1, max_norm / norm)
+ *
+ * scale: what the gradients are to be multiplied by (the inverse of a loss
+ * scale), finite and above 0; max_norm above 0, INFINITY for no clip
+ * (TILE_ERR_EPS).  factor is NaN where the norm is not finite.  Squares are FP32
+ * (magnitudes above 1.8e19 come out infinite, far below 1e-19 as nothing), sums
+ * compensated FP32 and FP64: bitwise reproducible.  Tensors are contiguous and
+ * of any size, 0 included, `data` aligned to the element; none: a norm of 0.
+ * `workspace`: 16-byte aligned, tile_grad_norm_workspace_bytes(count) bytes;
+ * calls that overlap in time need workspaces of their own. */
+typedef struct tile_tensor {
+    const void *data;
+    long long n;               /* elements                                        */
+    int dtype;                 /* TILE_DTYPE_*                                    */
+} tile_tensor_t;
+
+size_t tile_grad_norm_workspace_bytes(int count);
+int tile_grad_norm(const tile_tensor_t *tensors, int count, float scale, float max_norm,
+                   float *out, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* One AdamW step of every tensor, in place.  With g = factor * grad and the
+ * step t,
+ *
+ *   exp_avg    = beta1 exp_avg + (1 - beta1) g
+ *   exp_avg_sq = beta2 exp_avg_sq + (1 - beta2) g^2
+ *   param      = (1 - lr weight_decay) param - lr / (1 - beta1^t) exp_avg
+ *                / (sqrt(exp_avg_sq / (1 - beta2^t)) + eps)
+ *   copy       = param rounded to copy_dtype, where wanted
+ *
+ * factor: [1] FP32 on the device (tile_grad_norm's out + 1), NULL for 1; where
+ * it is not finite, nothing is changed.  step (>= 1) and lr may lie on the
+ * device instead, so that a captured step can be replayed with others: NULL
+ * takes the number given (a step below 1 on the device counts as 1).
+ *
+ * param is FP32 (an update is often less than half a 16-bit step of it); the 16-bit
+ * weights that a model runs on are the copy.  TILE_STATE_F32: both states
+ * [n] FP32.  TILE_STATE_E4M3: [n] bytes of e4m3 and FP32 scales
+ * [ceil(n / 256)], a power of two for each 256 elements: exp_avg = code * scale,
+ * exp_avg_sq = (code * scale)^2.  These are rounded up with the
+ * probability of what is cut off (16 bits of SplitMix64's finalizer of seed,
+ * step, the tensor's place in the list and the element): to nearest, exp_avg_sq
+ * could not move by less than 6 %.  The same call gives the same bits.  A zero
+ * state is zero codes with any finite scale.  A state of 256 elements one of which
+ * is not finite becomes NaN.
+ *
+ * Everything else is FP32, the two sums of products rounded after each
+ * operation.  Pointers: aligned to their element; the 16-byte grid (8-byte for
+ * codes and 16-bit tensors) is the fastest.  No written range may overlap another
+ * range of the call (TILE_ERR_ALIAS): a tensor is listed once.  n >= 0, no limit
+ * on count.  TILE_ERR_EPS for betas outside [0, 1), eps that is not finite and
+ * above 0, an lr or weight_decay that is not finite; TILE_ERR_SHAPE for n < 0,
+ * count < 0, step < 1; TILE_ERR_DTYPE for unknown types (copy_dtype: BF16 or
+ * F16); other rules and errors as the row entry points.  May be captured into a
+ * CUDA graph, which then holds the pointers. */
+#define TILE_STATE_F32  0
+#define TILE_STATE_E4M3 1
+
+typedef struct tile_adamw_tensor {
+    float *param;
+    const void *grad;
+    void *exp_avg, *exp_avg_sq;
+    float *exp_avg_scale, *exp_avg_sq_scale;   /* TILE_STATE_E4M3                 */
+    void *copy;                                /* or NULL                         */
+    long long n;
+    float weight_decay;
+    int grad_dtype;                            /* TILE_DTYPE_*                    */
+    int copy_dtype;                            /* with a copy                     */
+} tile_adamw_tensor_t;
+
+typedef struct tile_adamw_config {
+    double lr, beta1, beta2, eps;
+    long long step;
+    const float *lr_device;          /* [1] or NULL                               */
+    const long long *step_device;    /* [1] or NULL                               */
+    const float *factor;             /* [1] or NULL                               */
+    unsigned long long seed;         /* TILE_STATE_E4M3                           */
+    int state;                       /* TILE_STATE_*                              */
+} tile_adamw_config_t;
+
+int tile_adamw(const tile_adamw_tensor_t *tensors, int count, const tile_adamw_config_t *config,
+               cudaStream_t stream);
+
 /* ---- pointwise value/derivative pairs ---------------------------------- */
 
 /* value[k] = sigmoid(in[k]) and derivative[k] = sigmoid'(in[k]) for k < n,

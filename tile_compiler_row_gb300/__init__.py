@@ -14,6 +14,7 @@ and importing the binding without the built library raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 from ._build import LIBRARY
@@ -41,6 +42,11 @@ __all__ = [
     "tile_linear_cross_entropy", "tile_linear_cross_entropy_workspace_bytes",
     "tile_linear_cross_entropy_backward", "tile_linear_cross_entropy_backward_workspace_bytes",
     "block_norm", "block_norm_backward", "linear_cross_entropy", "linear_cross_entropy_backward",
+    "tile_embedding", "tile_embedding_backward", "tile_embedding_backward_workspace_bytes",
+    "tile_policy_loss", "tile_policy_loss_backward", "tile_policy_loss_workspace_bytes",
+    "tile_grad_norm", "tile_grad_norm_workspace_bytes", "tile_adamw",
+    "embedding", "embedding_backward", "policy_loss", "policy_loss_backward", "grad_norm",
+    "adamw", "adamw_state",
     "tile_norm_param_grad_f32", "tile_run_backward_plan_ex",
     "tile_layernorm_backward_bf16", "tile_rmsnorm_backward_bf16", "tile_softmax_backward_bf16",
     "tile_norm_param_grad_bf16", "tile_layernorm_backward_f16", "tile_rmsnorm_backward_f16",
@@ -105,6 +111,25 @@ class TileBlockNormBackwardArgs(ctypes.Structure):
         ("dgamma_pre", ctypes.c_void_p), ("rows", ctypes.c_int), ("width", ctypes.c_int),
         ("rows_per_gate", ctypes.c_int), ("norms", ctypes.c_int),
         ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float), ("dtype", ctypes.c_int),
+    ]
+
+
+class TilePolicyLossArgs(ctypes.Structure):
+    _fields_ = [
+        ("nll", ctypes.c_void_p), ("old_nll", ctypes.c_void_p), ("ref_nll", ctypes.c_void_p),
+        ("advantage", ctypes.c_void_p), ("target", ctypes.c_void_p),
+        ("offsets", ctypes.c_void_p), ("ignore_index", ctypes.c_longlong),
+        ("rows", ctypes.c_int), ("sequences", ctypes.c_int), ("flags", ctypes.c_int),
+        ("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float),
+    ]
+
+
+class TileAdamwConfig(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double), ("step", ctypes.c_longlong), ("lr_device", ctypes.c_void_p),
+        ("step_device", ctypes.c_void_p), ("factor", ctypes.c_void_p),
+        ("seed", ctypes.c_ulonglong), ("state", ctypes.c_int),
     ]
 
 
@@ -205,6 +230,13 @@ def load():
                                       ctypes.c_size_t, P],
         "tile_linear_cross_entropy_backward": [I, P, P, P, P, P, P, P, I, I, I,
                                                ctypes.c_longlong, P, ctypes.c_size_t, P],
+        "tile_embedding": [I, P, P, P, I, I, I, F, ctypes.c_longlong, P],
+        "tile_embedding_backward": [I, I, P, P, P, I, I, I, F, ctypes.c_longlong, I, P,
+                                    ctypes.c_size_t, P],
+        "tile_policy_loss": [ctypes.POINTER(TilePolicyLossArgs), P, P, P, ctypes.c_size_t, P],
+        "tile_policy_loss_backward": [ctypes.POINTER(TilePolicyLossArgs), P, P, P, P],
+        "tile_grad_norm": [P, I, F, F, P, P, ctypes.c_size_t, P],
+        "tile_adamw": [P, I, ctypes.POINTER(TileAdamwConfig), P],
     }
     for name, argtypes in sigs.items():
         fn = getattr(lib, name)
@@ -217,9 +249,14 @@ def load():
     lib.tile_block_norm_backward_gated_workspace_bytes.argtypes = [I, I, I]
     lib.tile_block_norm_backward_gated_workspace_bytes.restype = ctypes.c_size_t
     for name in ("tile_linear_cross_entropy_workspace_bytes",
-                 "tile_linear_cross_entropy_backward_workspace_bytes"):
+                 "tile_linear_cross_entropy_backward_workspace_bytes",
+                 "tile_embedding_backward_workspace_bytes"):
         getattr(lib, name).argtypes = [I, I, I]
         getattr(lib, name).restype = ctypes.c_size_t
+    lib.tile_policy_loss_workspace_bytes.argtypes = [I, I]
+    lib.tile_policy_loss_workspace_bytes.restype = ctypes.c_size_t
+    lib.tile_grad_norm_workspace_bytes.argtypes = [I]
+    lib.tile_grad_norm_workspace_bytes.restype = ctypes.c_size_t
     lib.tile_host_workspace_bytes.argtypes = [I, I, I]
     lib.tile_host_workspace_bytes.restype = ctypes.c_size_t
     lib.tile_status_string.argtypes = [I]
@@ -1049,6 +1086,250 @@ def tile_linear_cross_entropy_backward(x, weight, target, lse, dloss, dx, dweigh
              ignore_index, ws, nbytes)
 
 
+# ---- embedding -----------------------------------------------------------------
+
+def _long(value, name):
+    if not -1 << 63 <= value < 1 << 63:
+        raise ValueError(f"{name} must be a 64-bit integer")
+    return value
+
+
+def tile_embedding(tokens, weight, out, scale=1.0, ignore_index=-100, stream=None):
+    """out[i] = scale * weight[tokens[i]] (float32, bfloat16 or float16); see
+    include/tile_rows.h."""
+    import torch
+    code, dev = _row_code(weight, "weight"), _device_index(weight, "weight")
+    vocab, width = weight.shape
+    rows = tokens.shape[0] if tokens.dim() == 1 else -1
+    if not _fit_int(rows, width, vocab):
+        raise ValueError("tokens must be 1-D, and rows, width and vocab below 2^31")
+    _call_on(dev, stream, "tile_embedding", code,
+             _ptr(tokens, "tokens", torch.int64, (rows,), dev),
+             _ptr(weight, "weight", weight.dtype, weight.shape, dev),
+             _ptr(out, "out", weight.dtype, (rows, width), dev), rows, width, vocab, scale,
+             _long(ignore_index, "ignore_index"))
+
+
+def tile_embedding_backward_workspace_bytes(rows, width, vocab):
+    if not _fit_int(rows, width, vocab):
+        return 0
+    return load().tile_embedding_backward_workspace_bytes(rows, width, vocab)
+
+
+def tile_embedding_backward(tokens, dout, dweight, workspace, scale=1.0, ignore_index=-100,
+                            accumulate=False, stream=None):
+    """dweight = (or, with ``accumulate``, +=) the gradient of
+    ``tile_embedding``'s weight; dweight may be float32 for 16-bit rows."""
+    import torch
+    code, dev = _row_code(dout, "dout"), _device_index(dout, "dout")
+    into = _row_code(dweight, "dweight")
+    rows, width = dout.shape
+    vocab = dweight.shape[0]
+    if not _fit_int(rows, width, vocab):
+        raise ValueError(f"rows, width and vocab must be below 2^31, not {rows}, {width}, {vocab}")
+    ws, nbytes = _workspace(workspace, dev)
+    _call_on(dev, stream, "tile_embedding_backward", code, into,
+             _ptr(tokens, "tokens", torch.int64, (rows,), dev),
+             _ptr(dout, "dout", dout.dtype, dout.shape, dev),
+             _ptr(dweight, "dweight", dweight.dtype, (vocab, width), dev), rows, width, vocab,
+             scale, _long(ignore_index, "ignore_index"), int(bool(accumulate)), ws, nbytes)
+
+
+# ---- policy loss -----------------------------------------------------------------
+
+def tile_policy_loss_workspace_bytes(rows, sequences):
+    if not _fit_int(rows, sequences):
+        return 0
+    return load().tile_policy_loss_workspace_bytes(rows, sequences)
+
+
+def _policy_args(nll, old_nll, advantage, ref_nll, target, offsets, clip_low, clip_high, kl_coef,
+                 sequence_advantage, sequence_mean, ignore_index):
+    """(argument struct, device index, rows, sequences)."""
+    import torch
+    dev, f32 = _device_index(nll, "nll"), torch.float32
+    if nll.dim() != 1:
+        raise ValueError("nll must be 1-D")
+    rows = nll.shape[0]
+    sequences = 1 if offsets is None else offsets.numel() - 1
+    if not _fit_int(rows, sequences) or sequences < 1:
+        raise ValueError("offsets must have at least two elements, and rows be below 2^31")
+    a = TilePolicyLossArgs(
+        _ptr(nll, "nll", f32, (rows,), dev), _ptr(old_nll, "old_nll", f32, (rows,), dev),
+        _ptr(ref_nll, "ref_nll", f32, (rows,), dev),
+        _ptr(advantage, "advantage", f32, (sequences if sequence_advantage else rows,), dev),
+        _ptr(target, "target", torch.int64, (rows,), dev),
+        _ptr(offsets, "offsets", torch.int64, (sequences + 1,), dev),
+        _long(ignore_index, "ignore_index"), rows, sequences,
+        (1 if sequence_advantage else 0) | (2 if sequence_mean else 0), clip_low, clip_high,
+        kl_coef)
+    return a, dev, rows, sequences
+
+
+def tile_policy_loss(nll, old_nll, advantage, stats, weights, workspace, ref_nll=None, target=None,
+                     offsets=None, clip_low=0.2, clip_high=0.2, kl_coef=0.0,
+                     sequence_advantage=False, sequence_mean=False, ignore_index=-100, stream=None):
+    """stats (loss, clipped term, KL term, clipped share) and the token weights
+    of each sequence; see ``tile_policy_loss`` in include/tile_rows.h."""
+    import torch
+    a, dev, _, sequences = _policy_args(nll, old_nll, advantage, ref_nll, target, offsets, clip_low,
+                                        clip_high, kl_coef, sequence_advantage, sequence_mean,
+                                        ignore_index)
+    ws, nbytes = _workspace(workspace, dev)
+    _call_on(dev, stream, "tile_policy_loss", ctypes.byref(a),
+             _ptr(stats, "stats", torch.float32, (4,), dev),
+             _ptr(weights, "weights", torch.float32, (sequences,), dev), ws, nbytes)
+
+
+def tile_policy_loss_backward(nll, old_nll, advantage, weights, dnll, dloss=None, ref_nll=None,
+                              target=None, offsets=None, clip_low=0.2, clip_high=0.2, kl_coef=0.0,
+                              sequence_advantage=False, ignore_index=-100, stream=None):
+    """dnll of ``tile_policy_loss`` for the gradient ``dloss`` of stats[0] (one
+    element on the device; None: 1)."""
+    import torch
+    a, dev, rows, sequences = _policy_args(nll, old_nll, advantage, ref_nll, target, offsets,
+                                           clip_low, clip_high, kl_coef, sequence_advantage, False,
+                                           ignore_index)
+    f32 = torch.float32
+    _call_on(dev, stream, "tile_policy_loss_backward", ctypes.byref(a),
+             _ptr(weights, "weights", f32, (sequences,), dev), _one(dloss, "dloss", f32, dev),
+             _ptr(dnll, "dnll", f32, (rows,), dev))
+
+
+def _one(t, name, dtype, dev):
+    """Pointer of a CUDA tensor of one element, of any number of dimensions."""
+    if t is None:
+        return None
+    if t.numel() != 1:
+        raise ValueError(f"{name} must have one element")
+    return _ptr(t, name, dtype, t.shape, dev)
+
+
+# ---- gradient norm and AdamW step --------------------------------------------------
+#
+# Lists of tensors: each list is gone through by a few C-level passes rather than
+# a call per tensor, and only a list that fails them is looked at one by one.
+
+_IS_CONTIGUOUS, _GET_DEVICE, _NUMEL, _DATA_PTR = map(
+    operator.methodcaller, ("is_contiguous", "get_device", "numel", "data_ptr"))
+_DTYPE = operator.attrgetter("dtype")
+
+
+def _pointers(tensors, name, dtypes, counts, dev):
+    """Pointers of a list of contiguous CUDA tensors on device index ``dev``,
+    of these element counts (None: any) and types."""
+    if counts is not None and len(tensors) != len(counts):
+        raise ValueError(f"{name} must have {len(counts)} tensors like the other lists, "
+                         f"not {len(tensors)}")
+    if (all(map(_IS_CONTIGUOUS, tensors)) and set(map(_GET_DEVICE, tensors)) <= {dev}
+            and set(map(_DTYPE, tensors)) <= dtypes
+            and (counts is None or list(map(_NUMEL, tensors)) == counts)):
+        return list(map(_DATA_PTR, tensors))
+    for i, t in enumerate(tensors):
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}[{i}] must be one of {sorted(map(str, dtypes))}, not {t.dtype}")
+        if counts is not None and t.numel() != counts[i]:
+            raise ValueError(f"{name}[{i}] must have {counts[i]} elements, not {t.numel()}")
+        _ptr(t, f"{name}[{i}]", t.dtype, t.shape, dev)
+    raise ValueError(f"{name} must be CUDA tensors of one device")
+
+
+def _list_device(tensors, name):
+    import torch
+    if isinstance(tensors, torch.Tensor):
+        raise TypeError(f"{name} must be a list of tensors")
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}[{i}] must be a torch.Tensor")
+    return _device_index(tensors[0], f"{name}[0]") if len(tensors) else None
+
+
+def _records(form, count, columns):
+    """C structs of one format from columns of their fields."""
+    import struct
+    return struct.pack(form * count, *[v for row in zip(*columns) for v in row])
+
+
+def tile_grad_norm_workspace_bytes(count):
+    return load().tile_grad_norm_workspace_bytes(count) if _fit_int(count) else 0
+
+
+def tile_grad_norm(grads, out, workspace, scale=1.0, max_norm=None, stream=None):
+    """out = (norm, clipping factor) of all ``grads`` together (float32,
+    bfloat16 or float16, in any mix); see include/tile_rows.h."""
+    import torch
+    _list_device(grads, "grads")
+    dev, count = _device_index(out, "out"), len(grads)
+    kinds = {torch.float32, torch.bfloat16, torch.float16}
+    at = _pointers(grads, "grads", kinds, None, dev)
+    codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    table = _records("2qi4x", count, (at, [t.numel() for t in grads], [codes[t.dtype] for t in grads]))
+    ws, nbytes = _workspace(workspace, dev)
+    _call_on(dev, stream, "tile_grad_norm", table, count, scale,
+             float("inf") if max_norm is None else max_norm,
+             _ptr(out, "out", torch.float32, (2,), dev), ws, nbytes)
+
+
+def tile_adamw(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
+               weight_decay=0.01, factor=None, copies=None, exp_avg_scales=None,
+               exp_avg_sq_scales=None, seed=0, stream=None):
+    """One AdamW step of every tensor of ``params`` (float32), in place, with
+    its state; see ``tile_adamw`` in include/tile_rows.h.  Lists of one length:
+    ``grads`` (float32, bfloat16 or float16), the states (float32, or
+    float8_e4m3fn with the scales), and ``copies`` (bfloat16 or float16, or
+    None).  ``step`` (from 1 on) and ``lr`` are numbers, or tensors of one
+    element on the device (int64, float32); ``weight_decay`` a number or one
+    for each tensor; ``factor`` ``tile_grad_norm``'s second output."""
+    import torch
+    f32, f8 = torch.float32, torch.float8_e4m3fn
+    dev, count = _list_device(params, "params"), len(params)
+    for name, ts in (("grads", grads), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)):
+        _list_device(ts, name)
+    if dev is None:
+        for name, ts in (("grads", grads), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)):
+            if len(ts):
+                raise ValueError(f"{name} must be empty like params")
+        return
+    n = [t.numel() for t in params]
+    none = [0] * count
+    p = _pointers(params, "params", {f32}, n, dev)
+    g = _pointers(grads, "grads", {f32, torch.bfloat16, torch.float16}, n, dev)
+    eight = len(exp_avg) > 0 and exp_avg[0].dtype is f8
+    state = {f8 if eight else f32}
+    m = _pointers(exp_avg, "exp_avg", state, n, dev)
+    v = _pointers(exp_avg_sq, "exp_avg_sq", state, n, dev)
+    ms = vs = c = cc = none
+    if eight:
+        if exp_avg_scales is None or exp_avg_sq_scales is None:
+            raise ValueError("8-bit states need exp_avg_scales and exp_avg_sq_scales")
+        _list_device(exp_avg_scales, "exp_avg_scales")
+        _list_device(exp_avg_sq_scales, "exp_avg_sq_scales")
+        blocks = [-(-k // 256) for k in n]
+        ms = _pointers(exp_avg_scales, "exp_avg_scales", {f32}, blocks, dev)
+        vs = _pointers(exp_avg_sq_scales, "exp_avg_sq_scales", {f32}, blocks, dev)
+    elif exp_avg_scales is not None or exp_avg_sq_scales is not None:
+        raise ValueError("scales belong to 8-bit states")
+    codes = {f32: 0, torch.bfloat16: 1, torch.float16: 2}
+    if copies is not None:
+        _list_device(copies, "copies")
+        c = _pointers(copies, "copies", {torch.bfloat16, torch.float16}, n, dev)
+        cc = [codes[t.dtype] for t in copies]
+    decay = [float(weight_decay)] * count if isinstance(weight_decay, (int, float)) \
+        else list(map(float, weight_decay))
+    if len(decay) != count:
+        raise ValueError(f"weight_decay must be a number or {count} of them")
+    table = _records("8qf2i4x", count, (p, g, m, v, ms, vs, c, n, decay,
+                                        [codes[t.dtype] for t in grads], cc))
+    on_device = isinstance(step, torch.Tensor), isinstance(lr, torch.Tensor)
+    config = TileAdamwConfig(
+        0.0 if on_device[1] else lr, betas[0], betas[1], eps,
+        0 if on_device[0] else _long(step, "step"),
+        _one(lr, "lr", f32, dev) if on_device[1] else None,
+        _one(step, "step", torch.int64, dev) if on_device[0] else None,
+        _one(factor, "factor", f32, dev), seed & 0xFFFFFFFFFFFFFFFF, 1 if eight else 0)
+    _call_on(dev, stream, "tile_adamw", table, count, ctypes.byref(config))
+
+
 # ---------------------------------------------------------------------------
 # convenience wrappers (allocate the output with torch when not given)
 # ---------------------------------------------------------------------------
@@ -1092,7 +1373,8 @@ def _on_stream(fn):
         if stream is None:
             return fn(*args, **kwargs)
         import torch
-        dev = next((t.get_device() for t in (*args, *kwargs.values())
+        dev = next((t.get_device() for a in (*args, *kwargs.values())
+                    for t in (a if isinstance(a, (list, tuple)) else (a,))
                     if isinstance(t, torch.Tensor) and t.is_cuda), None)
         if dev is None:
             raise ValueError(f"{fn.__name__} takes CUDA tensors (there is no CPU path)")
@@ -1167,6 +1449,112 @@ def linear_cross_entropy_backward(x, weight, target, lse, dloss, ignore_index=-1
     tile_linear_cross_entropy_backward(x, weight, target, lse, dloss, dx, dweight, ws,
                                        ignore_index)
     return dx, dweight
+
+
+@_on_stream
+def embedding(tokens, weight, scale=1.0, ignore_index=-100):
+    """scale * weight[tokens], rows of zeros where a token is ignore_index."""
+    import torch
+    _row_code(weight, "weight")
+    out = torch.empty(tokens.shape[0], weight.shape[1], dtype=weight.dtype, device=weight.device)
+    tile_embedding(tokens, weight, out, scale, ignore_index)
+    return out
+
+
+@_on_stream
+def embedding_backward(tokens, dout, vocab=None, scale=1.0, ignore_index=-100, dtype=None,
+                       dweight=None):
+    """The gradient of ``embedding``'s weight: a new [vocab, width] tensor (of
+    dout's type, or ``dtype`` float32), or added to ``dweight``, which is
+    returned (say, what ``linear_cross_entropy_backward`` left for a weight that
+    the head shares)."""
+    import torch
+    add = dweight is not None
+    if add:
+        if vocab not in (None, dweight.shape[0]) or dtype not in (None, dweight.dtype):
+            raise ValueError("vocab and dtype are those of dweight")
+    elif vocab is None:
+        raise ValueError("vocab or dweight is needed")
+    else:
+        dweight = torch.empty(vocab, dout.shape[1], dtype=dtype or dout.dtype, device=dout.device)
+    ws = _scratch(tile_embedding_backward_workspace_bytes(*dout.shape, dweight.shape[0]), dout)
+    tile_embedding_backward(tokens, dout, dweight, ws, scale, ignore_index, add)
+    return dweight
+
+
+def _mean_of(mean):
+    if mean not in ("token", "sequence"):
+        raise ValueError('mean must be "token" or "sequence"')
+    return mean == "sequence"
+
+
+@_on_stream
+def policy_loss(nll, old_nll, advantage, ref_nll=None, target=None, offsets=None,
+                per_sequence=False, clip_low=0.2, clip_high=0.2, kl_coef=0.0, mean="token",
+                ignore_index=-100):
+    """(stats, weights) of ``tile_policy_loss``: stats[0] is the loss, and
+    ``policy_loss_backward`` takes the weights.  ``per_sequence``: an advantage
+    for each sequence; ``mean``: over "token"s or over each "sequence"'s mean."""
+    import torch
+    sequences = 1 if offsets is None else offsets.numel() - 1
+    stats = torch.empty(4, dtype=torch.float32, device=nll.device)
+    weights = torch.empty(max(sequences, 0), dtype=torch.float32, device=nll.device)
+    ws = _scratch(tile_policy_loss_workspace_bytes(nll.shape[0], sequences), nll)
+    tile_policy_loss(nll, old_nll, advantage, stats, weights, ws, ref_nll, target, offsets,
+                     clip_low, clip_high, kl_coef, per_sequence, _mean_of(mean), ignore_index)
+    return stats, weights
+
+
+@_on_stream
+def policy_loss_backward(nll, old_nll, advantage, weights, dloss=None, ref_nll=None, target=None,
+                         offsets=None, per_sequence=False, clip_low=0.2, clip_high=0.2,
+                         kl_coef=0.0, ignore_index=-100):
+    """dnll of ``tile_policy_loss_backward``: the ``dloss`` of
+    ``linear_cross_entropy_backward``."""
+    import torch
+    dnll = torch.empty_like(nll)
+    tile_policy_loss_backward(nll, old_nll, advantage, weights, dnll, dloss, ref_nll, target,
+                              offsets, clip_low, clip_high, kl_coef, per_sequence, ignore_index)
+    return dnll
+
+
+@_on_stream
+def grad_norm(grads, max_norm=None, scale=1.0):
+    """(norm, clipping factor) of all ``grads`` together as a tensor of two;
+    ``adamw`` takes its second element as ``factor``."""
+    import torch
+    if _list_device(grads, "grads") is None:
+        raise ValueError("grads is empty")
+    out = torch.empty(2, dtype=torch.float32, device=grads[0].device)
+    tile_grad_norm(grads, out, _scratch(tile_grad_norm_workspace_bytes(len(grads)), out), scale,
+                   max_norm)
+    return out
+
+
+def adamw(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
+          weight_decay=0.01, factor=None, copies=None, exp_avg_scales=None,
+          exp_avg_sq_scales=None, seed=0, stream=None):
+    """``tile_adamw``; ``adamw_state`` makes the states."""
+    tile_adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_decay, factor,
+               copies, exp_avg_scales, exp_avg_sq_scales, seed, stream)
+
+
+def adamw_state(params, bits=32):
+    """Zero states of ``adamw`` for these parameters: the keyword arguments
+    exp_avg and exp_avg_sq, and with ``bits`` 8 their scales."""
+    import torch
+    if bits not in (8, 32):
+        raise ValueError("states have 8 or 32 bits")
+    kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
+
+    def zeros(blocks=None):
+        return [torch.zeros(p.shape if blocks is None else -(-p.numel() // blocks),
+                            dtype=kind if blocks is None else torch.float32, device=p.device)
+                for p in params]
+    state = {"exp_avg": zeros(), "exp_avg_sq": zeros()}
+    if bits == 8:
+        state.update(exp_avg_scales=zeros(256), exp_avg_sq_scales=zeros(256))
+    return state
 
 
 def run(op, x, residual=None, out=None, eps=1e-5, stream=None):

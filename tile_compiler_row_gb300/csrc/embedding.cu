@@ -1,0 +1,559 @@
+// Embedding lookup, out[i] = scale weight[token[i]], and its gradient,
+// dweight[v] (+)= scale (sum of dout[i] over the rows with token[i] = v).
+//
+// Both are bound by DRAM: the lookup reads each row of the weight that occurs
+// and writes rows x width; the gradient reads rows x width and writes the
+// whole weight's shape, or the rows that occur where it adds.
+//
+// The gradient sums the rows of a token in the order of their positions, in
+// FP32, so that results are bitwise reproducible.  Few rows: a CTA for each
+// row looks for the row's token among all tokens, and the first row of a token
+// sums them.  Many rows: positions are sorted by token (a stable radix sort of
+// up to 9 bits a pass), and the sorted list is summed in runs of kRun
+// positions; a token whose rows lie in several runs is joined from their
+// partial sums.
+#include "device_status.h"
+#include "embedding.h"
+#include "row_windows.cuh"
+
+TILE_DEVICE_STATUS(embedding)
+
+namespace tile {
+namespace {
+
+constexpr unsigned int kBadToken = 1;
+
+// Token at i, or -1 where it has no row: ignored, or out of range (noted).
+__device__ __forceinline__ int token_row(const EmbeddingArgs &a, long long t) {
+    if (t == a.ignore) return -1;
+    if (t >= 0 && t < a.vocab) return static_cast<int>(t);
+    atomicOr(a.status, kBadToken);
+    return -2;
+}
+
+template <class T>
+__device__ __forceinline__ int windows_of(int width, bool vec) {
+    constexpr int V = 16 / sizeof(T);
+    return vec ? width / V : (width + V - 1) / V + 1;
+}
+
+// ---- lookup ---------------------------------------------------------------------
+
+// `lanes` (a power of two) threads a row, up to 4 windows of it each at a time.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) lookup_kernel(const EmbeddingArgs a, int lanes) {
+    constexpr int V = 16 / sizeof(T), U = 4;
+    const int lane = threadIdx.x & (lanes - 1), per = 256 / lanes;
+    const int row = blockIdx.x * per + threadIdx.x / lanes;
+    if (row >= a.rows) return;
+    const int token = token_row(a, __ldg(a.tokens + row));
+    const T *src = static_cast<const T *>(a.weight) + static_cast<long long>(token < 0 ? 0 : token) * a.width;
+    T *dst = static_cast<T *>(a.out) + static_cast<long long>(row) * a.width;
+    const int phase = VEC ? 0 : window_phase(dst);
+    const int windows = windows_of<T>(a.width, VEC);
+    for (int j = lane; j < windows; j += U * lanes) {
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (token >= 0 && j + u * lanes < windows)
+                raw[u] = load_window<T, VEC>(src, (j + u * lanes) * V - phase, a.width);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (j + u * lanes < windows) {
+                float v[V];
+                widen_vec<T>(raw[u], v);
+#pragma unroll
+                for (int i = 0; i < V; ++i)   // an ignored row is 0 whatever the scale, a bad one NaN
+                    v[i] = token >= 0 ? v[i] * a.scale : token == -1 ? 0.0f : __int_as_float(0x7fffffff);
+                store_window<T, V, VEC>(dst, (j + u * lanes) * V - phase, a.width, v);
+            }
+    }
+}
+
+template <class T, bool VEC>
+cudaError_t launch_lookup(const EmbeddingArgs &a, cudaStream_t stream) {
+    const int windows = a.width / (16 / static_cast<int>(sizeof(T))) + (VEC ? 0 : 2);
+    int lanes = 8;
+    while (lanes < 256 && lanes * 4 < windows) lanes *= 2;
+    // few rows: one window a thread
+    while (lanes < 256 && lanes < windows && static_cast<long long>(a.rows) * lanes < 152 * 512) lanes *= 2;
+    const int per = 256 / lanes;
+    lookup_kernel<T, VEC><<<(a.rows + per - 1) / per, 256, 0, stream>>>(a, lanes);
+    return cudaGetLastError();
+}
+
+// ---- gradient: few rows ------------------------------------------------------------
+
+// CTA (i, s): the rows of token[i], if i is the first, in slice s of 32 windows.
+constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32, kFewRows = 2048;
+
+template <class T, class D, bool VEC>
+__global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const EmbeddingArgs a) {
+    constexpr int V = 16 / sizeof(T), U = 4;
+    __shared__ unsigned short list[kFewRows];
+    __shared__ int found[kFewWarps];
+    __shared__ float part[kFewWarps][32][V + 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = blockIdx.x;
+    const long long t = __ldg(a.tokens + i);
+    int token = t == a.ignore || t < 0 || t >= a.vocab ? -1 : static_cast<int>(t);
+    if (token < 0) {
+        if (tid == 0 && blockIdx.y == 0) token_row(a, t);
+        return;
+    }
+    int first = 1;
+    for (int j = tid; j < i; j += kFewThreads) first &= __ldg(a.tokens + j) != t;
+    if (!__syncthreads_and(first)) return;
+    // positions of the token, in order
+    int n = 0;
+    for (int base = i; base < a.rows; base += kFewThreads) {
+        const int j = base + tid;
+        const bool hit = j < a.rows && __ldg(a.tokens + j) == t;
+        const unsigned int mask = __ballot_sync(0xffffffffu, hit);
+        if (lane == 0) found[warp] = __popc(mask);
+        __syncthreads();
+        int before = n;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) {
+            if (w < warp) before += found[w];
+            n += found[w];
+        }
+        if (hit) list[before + __popc(mask & ((1u << lane) - 1))] = static_cast<unsigned short>(j);
+        __syncthreads();
+    }
+    D *dst = static_cast<D *>(a.dweight) + static_cast<long long>(token) * a.width;
+    const int phase = VEC ? 0 : window_phase(dst);
+    const int windows = windows_of<T>(a.width, VEC);
+    const int at = (blockIdx.y * 32 + lane) * V - phase;
+    const bool in = static_cast<int>(blockIdx.y) * 32 + lane < windows;
+    // each warp sums a contiguous part of the list
+    const int from = n * warp / kFewWarps, to = n * (warp + 1) / kFewWarps;
+    float sum[V] = {};
+    for (int k = from; k < to; k += U) {
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (in && k + u < to)
+                raw[u] = load_window<T, VEC>(
+                    static_cast<const T *>(a.dout) + static_cast<long long>(list[k + u]) * a.width, at, a.width);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float v[V];
+            widen_vec<T>(raw[u], v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[e] += v[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) part[warp][lane][e] = sum[e];
+    __syncthreads();
+    if (warp != 0 || !in) return;
+    float old[V] = {};
+    if (a.add) read_window<D, V, VEC>(dst, at, a.width, old);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        sum[e] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) sum[e] += part[w][lane][e];
+        sum[e] = fmaf(sum[e], a.scale, old[e]);
+    }
+    store_window<D, V, VEC>(dst, at, a.width, sum);
+}
+
+// ---- gradient: sorting positions by token --------------------------------------------
+
+constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32, kMaxBits = 9;
+constexpr int kMaxBins = 1 << kMaxBits;
+
+struct Pair {
+    unsigned int key, at;   // token (vocab: none) and position
+};
+
+struct SortPlan {
+    int passes, bits, items, tiles;   // items a thread
+};
+
+SortPlan sort_plan(int rows, int vocab) {
+    int all = 1;
+    while ((1ll << all) <= vocab) ++all;   // keys 0 .. vocab
+    SortPlan p;
+    p.passes = (all + kMaxBits - 1) / kMaxBits;
+    p.bits = (all + p.passes - 1) / p.passes;
+    p.items = rows > 131072 ? 32 : 8;
+    p.tiles = (rows + kSortThreads * p.items - 1) / (kSortThreads * p.items);
+    return p;
+}
+
+__device__ __forceinline__ unsigned int key_at(const EmbeddingArgs &a, int i) {
+    const int row = token_row(a, __ldg(a.tokens + i));
+    return row < 0 ? static_cast<unsigned int>(a.vocab) : static_cast<unsigned int>(row);
+}
+
+// Counts of the first digit in each tile; the later passes' counts to zero.
+__global__ void __launch_bounds__(kSortThreads)
+    digits_kernel(const EmbeddingArgs a, int *counts, int bits, int passes, int tile) {
+    __shared__ int bins[kMaxBins];
+    const int n = 1 << bits, tiles = gridDim.x;
+    for (int d = threadIdx.x; d < n; d += kSortThreads) bins[d] = 0;
+    __syncthreads();
+    const int begin = blockIdx.x * tile, end = min(begin + tile, a.rows);
+    for (int i = begin + threadIdx.x; i < end; i += kSortThreads)
+        atomicAdd(&bins[key_at(a, i) & (n - 1)], 1);
+    __syncthreads();
+    for (int d = threadIdx.x; d < n; d += kSortThreads) {
+        const long long at = static_cast<long long>(blockIdx.x) * n + d;
+        counts[at] = bins[d];
+        for (int p = 1; p < passes; ++p) counts[at + static_cast<long long>(p) * tiles * n] = 0;
+    }
+}
+
+// One stable pass: a pair goes behind those of smaller digits, and behind those
+// of its digit in earlier tiles, warps and places.  Integer atomics count the
+// next digit by the tile that a pair lands in; their order changes nothing.
+template <int ITEMS, bool FIRST>
+__global__ void __launch_bounds__(kSortThreads)
+    scatter_kernel(const EmbeddingArgs a, const Pair *in, Pair *out, const int *counts, int *next,
+                   int bits, int shift, bool last) {
+    __shared__ int warp_bins[kSortWarps][kMaxBins];
+    __shared__ int base[kMaxBins];
+    __shared__ int sums[kSortWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = 1 << bits, tiles = gridDim.x;
+    for (int d = tid; d < kSortWarps * kMaxBins; d += kSortThreads) (&warp_bins[0][0])[d] = 0;
+    // digits 2 tid and 2 tid + 1: pairs before this tile, and in all
+    int before[2] = {}, total[2] = {};
+    const int d0 = 2 * tid;
+    if (d0 < n) {
+#pragma unroll 4
+        for (int t = 0; t < tiles; ++t) {
+            const int2 c = *reinterpret_cast<const int2 *>(counts + static_cast<long long>(t) * n + d0);
+            if (t < static_cast<int>(blockIdx.x)) {
+                before[0] += c.x;
+                before[1] += c.y;
+            }
+            total[0] += c.x;
+            total[1] += c.y;
+        }
+    }
+    int scan = total[0] + total[1];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, scan, d);
+        if (lane >= d) scan += up;
+    }
+    if (lane == 31) sums[warp] = scan;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) scan += sums[w];
+    scan -= total[0] + total[1];
+    if (d0 < n) {
+        base[d0] = scan + before[0];
+        base[d0 + 1] = scan + total[0] + before[1];
+    }
+    const int begin = blockIdx.x * kSortThreads * ITEMS + warp * 32 * ITEMS;
+    Pair pair[ITEMS];
+    int rank[ITEMS];
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+        const int i = begin + r * 32 + lane;
+        if (i < a.rows) {
+            if constexpr (FIRST)
+                pair[r] = Pair{key_at(a, i), static_cast<unsigned int>(i)};
+            else
+                pair[r] = in[i];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+        const bool live = begin + r * 32 + lane < a.rows;
+        const int digit = live ? static_cast<int>(pair[r].key >> shift) & (n - 1) : -1;
+        const unsigned int peers = __match_any_sync(0xffffffffu, digit);
+        rank[r] = __popc(peers & ((1u << lane) - 1));
+        const int had = live ? warp_bins[warp][digit] : 0;
+        __syncwarp();
+        if (live && rank[r] == 0) warp_bins[warp][digit] = had + __popc(peers);
+        rank[r] += had;
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int d = tid; d < n; d += kSortThreads) {
+        int at = base[d];
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int c = warp_bins[w][d];
+            warp_bins[w][d] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r)
+        if (begin + r * 32 + lane < a.rows) {
+            const int to = warp_bins[warp][static_cast<int>(pair[r].key >> shift) & (n - 1)] + rank[r];
+            out[to] = pair[r];
+            if (!last)
+                atomicAdd(next + static_cast<long long>(to / (kSortThreads * ITEMS)) * n +
+                              (static_cast<int>(pair[r].key >> (shift + bits)) & (n - 1)), 1);
+        }
+}
+
+// ---- gradient: sums of the sorted list ------------------------------------------------
+
+constexpr int kSumThreads = 128;
+struct SumPlan {
+    int run, runs;   // positions of a run, and how many there are
+};
+// 64 positions a run; more than 1024 runs would make the partial sums large.
+SumPlan sum_plan(int rows) {
+    SumPlan p;
+    p.run = 64;
+    while ((rows + p.run - 1) / p.run > 1024) p.run *= 2;
+    p.runs = (rows + p.run - 1) / p.run;
+    return p;
+}
+
+// FP32 partial sums [runs][2][windows][V] of tokens that lie in several runs: of
+// a run's first token where it began in an earlier run, and of its last where
+// it began here and goes on.
+template <int V>
+__device__ __forceinline__ float *partial_at(float *partial, int run, int slot, int windows, int j) {
+    return partial + ((static_cast<long long>(run) * 2 + slot) * windows + j) * V;
+}
+template <int V>
+__device__ __forceinline__ void store_partial(float *p, const float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+        *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+
+template <class T, class D, bool VEC>
+__device__ __forceinline__ void finish_row(const EmbeddingArgs &a, D *dst, int at,
+                                           float (&sum)[16 / sizeof(T)]) {
+    constexpr int V = 16 / sizeof(T);
+    float old[V] = {};
+    if (a.add) read_window<D, V, VEC>(dst, at, a.width, old);
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] = fmaf(sum[e], a.scale, old[e]);
+    store_window<D, V, VEC>(dst, at, a.width, sum);
+}
+
+template <class T, class D, bool VEC>
+__global__ void __launch_bounds__(kSumThreads)
+    sum_kernel(const EmbeddingArgs a, const Pair *pairs, float *partial, int run, int runs, int lanes) {
+    constexpr int V = 16 / sizeof(T), U = 8;
+    const int lane = threadIdx.x & (lanes - 1);
+    const int r = blockIdx.x * (kSumThreads / lanes) + threadIdx.x / lanes;
+    const int windows = windows_of<T>(a.width, VEC);
+    const int j = blockIdx.y * lanes + lane;
+    if (r >= runs || j >= windows) return;
+    const int begin = r * run, end = min(begin + run, a.rows);
+    const unsigned int none = a.vocab;
+    unsigned int cur = __ldg(&pairs[begin].key);
+    if (cur == none) return;
+    bool here = begin == 0 || __ldg(&pairs[begin - 1].key) != cur;
+    const T *dout = static_cast<const T *>(a.dout);
+    D *dst = static_cast<D *>(a.dweight) + static_cast<long long>(cur) * a.width;
+    int at = j * V - (VEC ? 0 : window_phase(dst));
+    float sum[V] = {};
+    for (int k = begin; k < end; k += U) {
+        Pair p[U];
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            p[u] = Pair{none, 0};
+            if (k + u < end) p[u] = pairs[k + u];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (p[u].key != none) {
+                const int from = VEC ? j * V : j * V - window_phase(static_cast<const D *>(a.dweight) +
+                                                                    static_cast<long long>(p[u].key) * a.width);
+                raw[u] = load_window<T, VEC>(dout + static_cast<long long>(p[u].at) * a.width, from, a.width);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (p[u].key == none) continue;
+            if (p[u].key != cur) {   // the token's last row was the one before
+                if (here)
+                    finish_row<T, D, VEC>(a, dst, at, sum);
+                else
+                    store_partial<V>(partial_at<V>(partial, r, 0, windows, j), sum);
+                cur = p[u].key;
+                here = true;
+                dst = static_cast<D *>(a.dweight) + static_cast<long long>(cur) * a.width;
+                at = j * V - (VEC ? 0 : window_phase(dst));
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[e] = 0.0f;
+            }
+            float v[V];
+            widen_vec<T>(raw[u], v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[e] += v[e];
+        }
+    }
+    const bool ends = end == a.rows || __ldg(&pairs[end].key) != cur;
+    if (here && ends)
+        finish_row<T, D, VEC>(a, dst, at, sum);
+    else
+        store_partial<V>(partial_at<V>(partial, r, here ? 1 : 0, windows, j), sum);
+}
+
+// The token that begins in a run and goes on behind it: its partial sums.
+template <class T, class D, bool VEC>
+__global__ void __launch_bounds__(kSumThreads)
+    join_kernel(const EmbeddingArgs a, const Pair *pairs, float *partial, int run, int runs, int lanes) {
+    constexpr int V = 16 / sizeof(T);
+    const int lane = threadIdx.x & (lanes - 1);
+    const int r = blockIdx.x * (kSumThreads / lanes) + threadIdx.x / lanes;
+    const int windows = windows_of<T>(a.width, VEC);
+    const int j = blockIdx.y * lanes + lane;
+    if (r >= runs - 1 || j >= windows) return;
+    const int begin = r * run, end = begin + run;   // not the last run: whole
+    const unsigned int cur = __ldg(&pairs[end - 1].key);
+    if (cur == static_cast<unsigned int>(a.vocab) || __ldg(&pairs[end].key) != cur) return;
+    if (__ldg(&pairs[begin].key) == cur && begin > 0 && __ldg(&pairs[begin - 1].key) == cur) return;
+    int low = end, high = a.rows;   // the first place from `end` on with another token
+    while (low < high) {
+        const int mid = low + (high - low) / 2;
+        if (__ldg(&pairs[mid].key) == cur)
+            low = mid + 1;
+        else
+            high = mid;
+    }
+    const int last = (low - 1) / run;
+    float sum[V];
+    const float *own = partial_at<V>(partial, r, 1, windows, j);
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] = own[e];
+#pragma unroll 4
+    for (int q = r + 1; q <= last; ++q) {
+        const float *p = partial_at<V>(partial, q, 0, windows, j);
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+            const float4 t = *reinterpret_cast<const float4 *>(p + e);
+            sum[e] += t.x;
+            sum[e + 1] += t.y;
+            sum[e + 2] += t.z;
+            sum[e + 3] += t.w;
+        }
+    }
+    D *dst = static_cast<D *>(a.dweight) + static_cast<long long>(cur) * a.width;
+    finish_row<T, D, VEC>(a, dst, j * V - (VEC ? 0 : window_phase(dst)), sum);
+}
+
+// ---- gradient: launches -----------------------------------------------------------------
+
+// Workspace: two lists of pairs, the digit counts, the partial sums.
+struct Layout {
+    size_t list, counts, partial, bytes;
+};
+Layout layout(int rows, int width, int vocab) {
+    const SortPlan s = sort_plan(rows, vocab);
+    const SumPlan m = sum_plan(rows);
+    auto round = [](size_t n) { return (n + 255) / 256 * 256; };
+    Layout l;
+    l.list = round(static_cast<size_t>(rows) * sizeof(Pair));
+    l.counts = 2 * l.list;
+    l.partial = l.counts + round(static_cast<size_t>(s.passes) * s.tiles * (1u << s.bits) * sizeof(int));
+    // the most windows are those of an FP32 row of any alignment
+    l.bytes = l.partial + round(static_cast<size_t>(m.runs) * 2 * (static_cast<size_t>(width) + 16) * sizeof(float));
+    return l;
+}
+
+template <class T, class D, bool VEC>
+cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
+    constexpr int V = 16 / sizeof(T);
+    const int windows = VEC ? a.width / V : (a.width + V - 1) / V + 1;
+    if (!a.add) {
+        const cudaError_t err = cudaMemsetAsync(
+            a.dweight, 0, static_cast<size_t>(a.vocab) * a.width * sizeof(D), stream);
+        if (err != cudaSuccess) return err;
+    }
+    if (a.rows <= kFewRows) {
+        few_rows_kernel<T, D, VEC><<<dim3(a.rows, (windows + 31) / 32), kFewThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    }
+    const SortPlan s = sort_plan(a.rows, a.vocab);
+    const SumPlan m = sum_plan(a.rows);
+    const Layout l = layout(a.rows, a.width, a.vocab);
+    char *ws = static_cast<char *>(a.ws);
+    Pair *list[2] = {reinterpret_cast<Pair *>(ws), reinterpret_cast<Pair *>(ws + l.list)};
+    int *counts = reinterpret_cast<int *>(ws + l.counts);
+    float *partial = reinterpret_cast<float *>(ws + l.partial);
+    const size_t table = static_cast<size_t>(s.tiles) << s.bits;
+    digits_kernel<<<s.tiles, kSortThreads, 0, stream>>>(a, counts, s.bits, s.passes, kSortThreads * s.items);
+    for (int p = 0; p < s.passes; ++p) {
+        const bool last = p == s.passes - 1;
+        int *c = counts + p * table;
+        const Pair *in = list[(p + 1) & 1];
+        Pair *out = list[p & 1];
+        if (s.items == 8) {
+            if (p == 0)
+                scatter_kernel<8, true><<<s.tiles, kSortThreads, 0, stream>>>(a, in, out, c, c + table, s.bits, 0, last);
+            else
+                scatter_kernel<8, false><<<s.tiles, kSortThreads, 0, stream>>>(a, in, out, c, c + table, s.bits, p * s.bits, last);
+        } else {
+            if (p == 0)
+                scatter_kernel<32, true><<<s.tiles, kSortThreads, 0, stream>>>(a, in, out, c, c + table, s.bits, 0, last);
+            else
+                scatter_kernel<32, false><<<s.tiles, kSortThreads, 0, stream>>>(a, in, out, c, c + table, s.bits, p * s.bits, last);
+        }
+    }
+    const Pair *sorted = list[(s.passes - 1) & 1];
+    int lanes = 8;
+    while (lanes < kSumThreads && lanes < windows) lanes *= 2;
+    const int per = kSumThreads / lanes;
+    const dim3 grid((m.runs + per - 1) / per, (windows + lanes - 1) / lanes);
+    sum_kernel<T, D, VEC><<<grid, kSumThreads, 0, stream>>>(a, sorted, partial, m.run, m.runs, lanes);
+    if (m.runs > 1)
+        join_kernel<T, D, VEC><<<grid, kSumThreads, 0, stream>>>(a, sorted, partial, m.run, m.runs, lanes);
+    return cudaGetLastError();
+}
+
+template <class T, class D>
+cudaError_t launch_gradient(bool vectors, const EmbeddingArgs &a, cudaStream_t stream) {
+    return vectors ? launch_gradient<T, D, true>(a, stream) : launch_gradient<T, D, false>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_embedding(int elem, bool vectors, EmbeddingArgs a, cudaStream_t stream) {
+    cudaError_t err = cudaSuccess;
+    a.status = status_address(&err);
+    if (a.status == nullptr) return err;
+    switch (elem) {
+        case ELEM_F32:
+            return vectors ? launch_lookup<float, true>(a, stream) : launch_lookup<float, false>(a, stream);
+        case ELEM_BF16:
+            return vectors ? launch_lookup<__nv_bfloat16, true>(a, stream)
+                           : launch_lookup<__nv_bfloat16, false>(a, stream);
+        default:
+            return vectors ? launch_lookup<__half, true>(a, stream) : launch_lookup<__half, false>(a, stream);
+    }
+}
+
+size_t embedding_backward_workspace(int rows, int width, int vocab) {
+    return rows <= kFewRows ? 0 : layout(rows, width, vocab).bytes;
+}
+
+cudaError_t launch_embedding_backward(int elem, int into, bool vectors, EmbeddingArgs a,
+                                      cudaStream_t stream) {
+    cudaError_t err = cudaSuccess;
+    a.status = status_address(&err);
+    if (a.status == nullptr) return err;
+    switch (elem) {
+        case ELEM_F32: return launch_gradient<float, float>(vectors, a, stream);
+        case ELEM_BF16:
+            return into == ELEM_F32 ? launch_gradient<__nv_bfloat16, float>(vectors, a, stream)
+                                    : launch_gradient<__nv_bfloat16, __nv_bfloat16>(vectors, a, stream);
+        default:
+            return into == ELEM_F32 ? launch_gradient<__half, float>(vectors, a, stream)
+                                    : launch_gradient<__half, __half>(vectors, a, stream);
+    }
+}
+
+}  // namespace tile

@@ -86,6 +86,9 @@ cudaError_t status_param_grad(unsigned int *value, cudaStream_t stream);
 cudaError_t status_block_norm_backward(unsigned int *value, cudaStream_t stream);
 // Error word of the linear cross entropy's kernels (linear_ce.cu).
 cudaError_t status_linear_ce(unsigned int *value, cudaStream_t stream);
+// Error words of the embedding (embedding.cu) and the policy loss (policy_loss.cu).
+cudaError_t status_embedding(unsigned int *value, cudaStream_t stream);
+cudaError_t status_policy_loss(unsigned int *value, cudaStream_t stream);
 
 // Largest register stripe per input (floats per thread) of a backward plan:
 // two stripes are held, so plans above it (K * elements per vector) are not

@@ -1,0 +1,619 @@
+// The norm of many gradients with the factor that clips it, and the AdamW step
+// over many tensors.
+//
+//   norm = scale sqrt(sum of g^2),  factor = scale min(1, max / norm)
+//
+//   g = factor grad
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   p = (1 - lr decay) p - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// Bound by DRAM: the norm reads each gradient once; a step reads and writes
+// parameter and states, reads the gradient and writes the 16-bit copy.  The
+// tensors' table (pointers, sizes, and where each begins in the list of all
+// chunks) is a kernel argument of up to 32 KB: no copy to the device, nothing
+// to keep alive, and a captured call holds it.  A chunk finds its tensor by
+// bisection.
+//
+// 8-bit states are e4m3 values with a power of two for each 256 elements, m
+// itself and the root of v (whose range an 8-bit v would not hold).  A step
+// moves v by some 1e-3 of itself, far below e4m3's steps of 1/8 to 1/16, so
+// values are rounded up with the probability of what is cut off: rounded to
+// nearest, v could never shrink.  Scaling by powers of two is exact and costs
+// a bit of range, none of precision.
+#include <cuda_fp8.h>
+
+#include <cmath>
+
+#include "device_status.h"
+#include "optimizer.h"
+#include "row_windows.cuh"
+
+namespace tile {
+namespace {
+
+// ---- tables ---------------------------------------------------------------------
+
+struct NormEntry {
+    const void *p;
+    long long n;
+    int elem, pad;
+};
+struct AdamwEntry {
+    float *param;
+    const void *grad;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    void *copy;
+    long long n;
+    float decay;
+    int index;        // in the caller's list
+    short grad_elem, copy_elem;
+    int vectors;      // every pointer on the grid of the vector accesses
+};
+
+template <class Entry, int N>
+struct Table {
+    int count, first[N + 1];   // first chunk of each tensor
+    Entry entry[N];
+};
+
+template <class Entry, int N>
+__device__ __forceinline__ int tensor_of(const Table<Entry, N> &t, int chunk) {
+    int low = 0, high = t.count - 1;
+    while (low < high) {
+        const int mid = (low + high + 1) / 2;
+        if (t.first[mid] <= chunk)
+            low = mid;
+        else
+            high = mid - 1;
+    }
+    return low;
+}
+
+// ---- gradient norm ----------------------------------------------------------------
+
+constexpr int kNormThreads = 256, kNormLoads = 8, kNormWindows = kNormThreads * kNormLoads;
+
+// Sum of the squares of this thread's windows of a chunk.
+template <class T>
+__device__ __forceinline__ float chunk_squares(const NormEntry &e, long long chunk) {
+    constexpr int V = 16 / sizeof(T);
+    const T *p = static_cast<const T *>(e.p);
+    const int phase = window_phase(p);
+    uint4 raw[kNormLoads];
+#pragma unroll
+    for (int u = 0; u < kNormLoads; ++u) {
+        const long long at = (chunk * kNormWindows + u * kNormThreads + threadIdx.x) * V - phase;
+        raw[u] = make_uint4(0, 0, 0, 0);
+        if (at >= 0 && at + V <= e.n) {
+            raw[u] = __ldcs(reinterpret_cast<const uint4 *>(p + at));
+        } else if (at < e.n) {
+            unsigned int w[4] = {};
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (at + j >= 0 && at + j < e.n) {
+                    if constexpr (sizeof(T) == 4)
+                        w[j] = __float_as_uint(p[at + j]);
+                    else
+                        w[j / 2] |= static_cast<unsigned int>(
+                                        reinterpret_cast<const unsigned short *>(p)[at + j]) << (16 * (j & 1));
+                }
+            raw[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kNormLoads; ++u) {
+        float v[V];
+        widen_vec<T>(raw[u], v);
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) s = fmaf(v[j], v[j], s);
+        sum += s;
+    }
+    return sum;
+}
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kNormThreads)
+    norm_kernel(const __grid_constant__ Table<NormEntry, N> t, double *partial) {
+    __shared__ double part[kNormThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    float sum = 0.0f, cut = 0.0f;   // a thread's sum over its chunks, and what its roundings cut off
+    for (int chunk = blockIdx.x; chunk < t.first[t.count]; chunk += gridDim.x) {
+        const int i = tensor_of(t, chunk);
+        const NormEntry &e = t.entry[i];
+        const long long c = chunk - t.first[i];
+        const float s = e.elem == ELEM_F32 ? chunk_squares<float>(e, c)
+                        : e.elem == ELEM_BF16 ? chunk_squares<__nv_bfloat16>(e, c)
+                                              : chunk_squares<__half>(e, c);
+        const float to = __fadd_rn(sum, s), back = __fsub_rn(to, sum);
+        cut += __fadd_rn(__fsub_rn(sum, __fsub_rn(to, back)), __fsub_rn(s, back));
+        sum = to;
+    }
+    // an infinite sum has no rest
+    const double v = warp_sum(static_cast<double>(sum) + (isfinite(sum) ? static_cast<double>(cut) : 0.0));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    double total = 0.0;
+    for (int w = 0; w < kNormThreads / 32; ++w) total += part[w];
+    partial[blockIdx.x] = total;
+}
+
+constexpr int kNormJoin = 512;
+__global__ void __launch_bounds__(kNormJoin)
+    norm_join_kernel(const double *partial, int count, float scale, float most, float *out) {
+    __shared__ double part[kNormJoin / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial sums are written
+    double v = 0.0;
+    for (int i = threadIdx.x; i < count; i += kNormJoin) v += __ldcg(partial + i);
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    double total = 0.0;
+    for (int w = 0; w < kNormJoin / 32; ++w) total += part[w];
+    const double norm = scale * sqrt(total);
+    out[0] = static_cast<float>(norm);
+    // a norm that is not finite: no factor, and a step that takes it is skipped
+    out[1] = !isfinite(out[0]) ? __int_as_float(0x7fffffff)
+             : norm > most     ? static_cast<float>(scale * (most / norm))
+                               : scale;
+}
+
+// ---- AdamW --------------------------------------------------------------------------
+
+struct Scalars {
+    float lr, beta1, rest1, beta2, rest2, eps;   // rest: 1 - beta
+    float log1, log2;           // of the betas
+    float rate, root;           // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+    long long step;
+    const float *lr_device;
+    const long long *step_device;
+    const float *factor;
+    unsigned long long seed;
+};
+
+// What a step takes from the device, if anything.
+__device__ __forceinline__ void load_scalars(Scalars &s) {
+    if (s.lr_device == nullptr && s.step_device == nullptr) return;
+    if (s.lr_device != nullptr) s.lr = __ldg(s.lr_device);
+    if (s.step_device != nullptr) s.step = max(__ldg(s.step_device), 1ll);
+    const float t = static_cast<float>(s.step);
+    s.rate = s.lr / -expm1f(t * s.log1);
+    s.root = rsqrtf(-expm1f(t * s.log2));
+}
+
+__device__ __forceinline__ float moment1(const Scalars &s, float m, float g) {
+    return __fadd_rn(__fmul_rn(m, s.beta1), __fmul_rn(g, s.rest1));
+}
+__device__ __forceinline__ float moment2(const Scalars &s, float v, float g) {
+    return __fadd_rn(__fmul_rn(v, s.beta2), __fmul_rn(__fmul_rn(g, g), s.rest2));
+}
+__device__ __forceinline__ float updated(const Scalars &s, float p, float keep, float m, float root_v) {
+    return fmaf(p, keep, -s.rate * __fdividef(m, fmaf(root_v, s.root, s.eps)));
+}
+
+// Four gradients from element `at` on.
+__device__ __forceinline__ uint4 load_grads(const void *p, int elem, long long at) {
+    if (elem == ELEM_F32) return __ldcs(reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + at));
+    const uint2 t = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(p) + at));
+    return make_uint4(t.x, t.y, 0, 0);
+}
+__device__ __forceinline__ void widen_grads(uint4 t, int elem, float (&g)[4]) {
+    if (elem == ELEM_F32) {
+        g[0] = __uint_as_float(t.x);
+        g[1] = __uint_as_float(t.y);
+        g[2] = __uint_as_float(t.z);
+        g[3] = __uint_as_float(t.w);
+    } else if (elem == ELEM_BF16) {
+        g[0] = __uint_as_float(t.x << 16);
+        g[1] = __uint_as_float(t.x & 0xffff0000u);
+        g[2] = __uint_as_float(t.y << 16);
+        g[3] = __uint_as_float(t.y & 0xffff0000u);
+    } else {
+        const float2 a = Elem<__half>::widen2(t.x), b = Elem<__half>::widen2(t.y);
+        g[0] = a.x;
+        g[1] = a.y;
+        g[2] = b.x;
+        g[3] = b.y;
+    }
+}
+__device__ __forceinline__ float load_grad(const void *p, int elem, long long at) {
+    if (elem == ELEM_F32) return __ldcs(static_cast<const float *>(p) + at);
+    const unsigned short t = __ldcs(static_cast<const unsigned short *>(p) + at);
+    return elem == ELEM_BF16 ? __uint_as_float(static_cast<unsigned int>(t) << 16)
+                             : __half2float(__ushort_as_half(t));
+}
+__device__ __forceinline__ unsigned int narrow_pair(int elem, float lo, float hi) {
+    return elem == ELEM_BF16 ? Elem<__nv_bfloat16>::narrow2(lo, hi) : Elem<__half>::narrow2(lo, hi);
+}
+__device__ __forceinline__ void store_copy(void *p, int elem, long long at, float v) {
+    if (elem == ELEM_BF16)
+        store_one(static_cast<__nv_bfloat16 *>(p) + at, v);
+    else
+        store_one(static_cast<__half *>(p) + at, v);
+}
+
+constexpr int kAdamwThreads = 256, kAdamwGroups = 4, kAdamwChunk = kAdamwThreads * kAdamwGroups * 4;
+
+template <int N>
+__global__ void __launch_bounds__(kAdamwThreads)
+    adamw_kernel(const __grid_constant__ Table<AdamwEntry, N> t, Scalars s) {
+    constexpr int U = 2;
+    const int i = tensor_of(t, blockIdx.x);
+    const AdamwEntry &e = t.entry[i];
+    const float f = s.factor != nullptr ? __ldg(s.factor) : 1.0f;
+    if (!isfinite(f)) return;   // a step that is skipped
+    load_scalars(s);
+    const float keep = fmaf(-s.lr, e.decay, 1.0f);
+    const long long base = static_cast<long long>(blockIdx.x - t.first[i]) * kAdamwChunk;
+    float *param = e.param, *m = static_cast<float *>(e.m), *v = static_cast<float *>(e.v);
+    if (e.vectors && base + kAdamwChunk <= e.n) {
+#pragma unroll 1
+        for (int k = 0; k < kAdamwGroups; k += U) {
+            float4 pv[U], mv[U], vv[U];
+            uint4 gv[U];
+            long long at[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                at[u] = base + ((k + u) * kAdamwThreads + threadIdx.x) * 4;
+                gv[u] = load_grads(e.grad, e.grad_elem, at[u]);
+                mv[u] = __ldcs(reinterpret_cast<const float4 *>(m + at[u]));
+                vv[u] = __ldcs(reinterpret_cast<const float4 *>(v + at[u]));
+                pv[u] = __ldcs(reinterpret_cast<const float4 *>(param + at[u]));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float g[4], a[4] = {mv[u].x, mv[u].y, mv[u].z, mv[u].w},
+                            b[4] = {vv[u].x, vv[u].y, vv[u].z, vv[u].w},
+                            p[4] = {pv[u].x, pv[u].y, pv[u].z, pv[u].w};
+                widen_grads(gv[u], e.grad_elem, g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    g[j] = __fmul_rn(g[j], f);
+                    a[j] = moment1(s, a[j], g[j]);
+                    b[j] = moment2(s, b[j], g[j]);
+                    p[j] = updated(s, p[j], keep, a[j], __fsqrt_rn(b[j]));
+                }
+                __stcs(reinterpret_cast<float4 *>(m + at[u]), make_float4(a[0], a[1], a[2], a[3]));
+                __stcs(reinterpret_cast<float4 *>(v + at[u]), make_float4(b[0], b[1], b[2], b[3]));
+                __stcs(reinterpret_cast<float4 *>(param + at[u]), make_float4(p[0], p[1], p[2], p[3]));
+                if (e.copy_elem >= 0)
+                    __stcs(reinterpret_cast<uint2 *>(static_cast<unsigned short *>(e.copy) + at[u]),
+                           make_uint2(narrow_pair(e.copy_elem, p[0], p[1]),
+                                      narrow_pair(e.copy_elem, p[2], p[3])));
+            }
+        }
+        return;
+    }
+    for (int k = 0; k < kAdamwGroups; ++k) {
+        float g[4], a[4], b[4], p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const long long at = base + (k * 4 + j) * kAdamwThreads + threadIdx.x;
+            g[j] = a[j] = b[j] = p[j] = 0.0f;
+            if (at >= e.n) continue;
+            g[j] = load_grad(e.grad, e.grad_elem, at);
+            a[j] = __ldcs(m + at);
+            b[j] = __ldcs(v + at);
+            p[j] = __ldcs(param + at);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const long long at = base + (k * 4 + j) * kAdamwThreads + threadIdx.x;
+            if (at >= e.n) continue;
+            g[j] = __fmul_rn(g[j], f);
+            a[j] = moment1(s, a[j], g[j]);
+            b[j] = moment2(s, b[j], g[j]);
+            p[j] = updated(s, p[j], keep, a[j], __fsqrt_rn(b[j]));
+            __stcs(m + at, a[j]);
+            __stcs(v + at, b[j]);
+            __stcs(param + at, p[j]);
+            if (e.copy_elem >= 0) store_copy(e.copy, e.copy_elem, at, p[j]);
+        }
+    }
+}
+
+// ---- AdamW with 8-bit states -----------------------------------------------------------
+
+// SplitMix64's finalizer (Steele, Lea and Flood, "Fast splittable pseudorandom
+// number generators", 2014).
+__host__ __device__ __forceinline__ unsigned long long mix64(unsigned long long z) {
+    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+    z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+    return z ^ (z >> 31);
+}
+constexpr unsigned long long kGolden = 0x9E3779B97F4A7C15ull;
+
+// 32 random bits for element `at`; the two elements of a pair share a word of 64.
+__device__ __forceinline__ unsigned long long pair_bits(unsigned long long key, long long pair) {
+    return mix64(key + static_cast<unsigned long long>(pair + 1) * kGolden);
+}
+
+// The power of two that a block's values are divided by, its inverse: the
+// largest of them comes to 128 to 256.  Blocks under 2^-100 are held as they
+// are (as zeros); one that is not finite stays so.
+struct BlockScale {
+    float scale, inverse;
+};
+__device__ __forceinline__ BlockScale block_scale(unsigned int top) {   // bits of the largest magnitude
+    const unsigned int e = top >> 23;
+    if (e == 255) return BlockScale{__int_as_float(0x7fffffff), __int_as_float(0x7fffffff)};
+    if (e < 27) return BlockScale{1.0f, 1.0f};
+    return BlockScale{__uint_as_float((e - 7) << 23), __uint_as_float((261 - e) << 23)};
+}
+
+// A magnitude below 256 in e4m3's steps: 16 random bits are added below the
+// three bits of the mantissa that stay.  Under 2^-6, where the type's steps no
+// longer shrink, it is moved up to where three bits are such a step.
+__device__ __forceinline__ float round_at_random(float size, unsigned int bits) {
+    const float base = size < 0.015625f ? 0.015625f : 0.0f;
+    const unsigned int w = __float_as_uint(__fadd_rn(size, base)) + (bits << 4);
+    return __fsub_rn(__uint_as_float(w & 0xfff00000u), base);
+}
+
+__device__ __forceinline__ unsigned int narrow_codes(float lo, float hi) {   // exact
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 widen_codes(unsigned int two) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+constexpr int kEightBlocks = 2, kEightChunk = kAdamwThreads / 32 * kStateBlock * kEightBlocks;
+
+template <int N>
+__global__ void __launch_bounds__(kAdamwThreads)
+    adamw8_kernel(const __grid_constant__ Table<AdamwEntry, N> t, Scalars s) {
+    const int i = tensor_of(t, blockIdx.x);
+    const AdamwEntry &e = t.entry[i];
+    const float f = s.factor != nullptr ? __ldg(s.factor) : 1.0f;
+    if (!isfinite(f)) return;   // a step that is skipped
+    load_scalars(s);
+    const float keep = fmaf(-s.lr, e.decay, 1.0f);
+    const unsigned long long key =
+        mix64(mix64(s.seed + static_cast<unsigned long long>(s.step) * kGolden) +
+              static_cast<unsigned long long>(e.index + 1) * kGolden);
+    const int lane = threadIdx.x & 31;
+    const bool vectors = e.vectors != 0;
+    unsigned char *mc = static_cast<unsigned char *>(e.m), *vc = static_cast<unsigned char *>(e.v);
+    for (int k = 0; k < kEightBlocks; ++k) {
+        // a warp for each block of 256; a lane has 8 elements, one behind the
+        // other where they are vectors, else each 32 on
+        const long long block = static_cast<long long>(blockIdx.x - t.first[i]) * (kEightChunk / kStateBlock) +
+                                k * (kAdamwThreads / 32) + (threadIdx.x >> 5);
+        const long long base = block * kStateBlock;
+        if (base >= e.n) return;
+        const bool whole = vectors && base + kStateBlock <= e.n;
+        const long long at = base + lane * 8;
+        float g[8], m[8], v[8], p[8];
+        const float ms = __ldcs(e.m_scale + block), vs = __ldcs(e.v_scale + block);
+        if (whole) {
+            const float4 p0 = __ldcs(reinterpret_cast<const float4 *>(e.param + at));
+            const float4 p1 = __ldcs(reinterpret_cast<const float4 *>(e.param + at) + 1);
+            const uint2 mw = __ldcs(reinterpret_cast<const uint2 *>(mc + at));
+            const uint2 vw = __ldcs(reinterpret_cast<const uint2 *>(vc + at));
+            uint4 g0, g1;
+            if (e.grad_elem == ELEM_F32) {
+                g0 = load_grads(e.grad, ELEM_F32, at);
+                g1 = load_grads(e.grad, ELEM_F32, at + 4);
+            } else {
+                g0 = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(e.grad) + at));
+                g1 = make_uint4(g0.z, g0.w, 0, 0);
+            }
+            float lo[4], hi[4];
+            widen_grads(g0, e.grad_elem, lo);
+            widen_grads(g1, e.grad_elem, hi);
+            const float pp[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                g[j] = lo[j];
+                g[j + 4] = hi[j];
+                const unsigned int mt = (j < 2 ? mw.x : mw.y) >> (16 * (j & 1));
+                const unsigned int vt = (j < 2 ? vw.x : vw.y) >> (16 * (j & 1));
+                const float2 a = widen_codes(mt & 0xffff), b = widen_codes(vt & 0xffff);
+                m[2 * j] = a.x;
+                m[2 * j + 1] = a.y;
+                v[2 * j] = b.x;
+                v[2 * j + 1] = b.y;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[j] = pp[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const long long w = base + j * 32 + lane;
+                g[j] = m[j] = v[j] = p[j] = 0.0f;
+                if (w < e.n) {
+                    g[j] = load_grad(e.grad, e.grad_elem, w);
+                    m[j] = widen_codes(mc[w]).x;
+                    v[j] = widen_codes(vc[w]).x;
+                    p[j] = __ldcs(e.param + w);
+                }
+            }
+        }
+        unsigned int mtop = 0, vtop = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            g[j] = __fmul_rn(g[j], f);
+            m[j] = moment1(s, __fmul_rn(m[j], ms), g[j]);
+            const float root = __fmul_rn(v[j], vs);
+            v[j] = __fsqrt_rn(moment2(s, __fmul_rn(root, root), g[j]));
+            p[j] = updated(s, p[j], keep, m[j], v[j]);
+            mtop = max(mtop, __float_as_uint(m[j]) & 0x7fffffffu);
+            vtop = max(vtop, __float_as_uint(v[j]) & 0x7fffffffu);
+        }
+        const BlockScale mscale = block_scale(__reduce_max_sync(0xffffffffu, mtop));
+        const BlockScale vscale = block_scale(__reduce_max_sync(0xffffffffu, vtop));
+        float mq[8], vq[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const long long w = whole ? at + j : base + j * 32 + lane;
+            const unsigned long long both = pair_bits(key, w >> 1);
+            const unsigned int bits = static_cast<unsigned int>((w & 1) != 0 ? both >> 32 : both);
+            const float size = round_at_random(fabsf(__fmul_rn(m[j], mscale.inverse)), bits & 0xffff);
+            mq[j] = copysignf(size, m[j]);
+            const float r = __fmul_rn(v[j], vscale.inverse);
+            const float q = round_at_random(r, bits >> 16);
+            vq[j] = r > 0.0f ? fmaxf(q, 0.001953125f) : q;   // a root that is not zero stays so
+        }
+        if (lane == 0) {
+            e.m_scale[block] = mscale.scale;
+            e.v_scale[block] = vscale.scale;
+        }
+        if (whole) {
+            unsigned int mw[4], vw[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mw[j] = narrow_codes(mq[2 * j], mq[2 * j + 1]);
+                vw[j] = narrow_codes(vq[2 * j], vq[2 * j + 1]);
+            }
+            __stcs(reinterpret_cast<uint2 *>(mc + at), make_uint2(mw[0] | mw[1] << 16, mw[2] | mw[3] << 16));
+            __stcs(reinterpret_cast<uint2 *>(vc + at), make_uint2(vw[0] | vw[1] << 16, vw[2] | vw[3] << 16));
+            __stcs(reinterpret_cast<float4 *>(e.param + at), make_float4(p[0], p[1], p[2], p[3]));
+            __stcs(reinterpret_cast<float4 *>(e.param + at) + 1, make_float4(p[4], p[5], p[6], p[7]));
+            if (e.copy_elem >= 0)
+                __stcs(reinterpret_cast<uint4 *>(static_cast<unsigned short *>(e.copy) + at),
+                       make_uint4(narrow_pair(e.copy_elem, p[0], p[1]), narrow_pair(e.copy_elem, p[2], p[3]),
+                                  narrow_pair(e.copy_elem, p[4], p[5]), narrow_pair(e.copy_elem, p[6], p[7])));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const long long w = base + j * 32 + lane;
+                if (w >= e.n) continue;
+                mc[w] = static_cast<unsigned char>(narrow_codes(mq[j], 0.0f) & 0xff);
+                vc[w] = static_cast<unsigned char>(narrow_codes(vq[j], 0.0f) & 0xff);
+                __stcs(e.param + w, p[j]);
+                if (e.copy_elem >= 0) store_copy(e.copy, e.copy_elem, w, p[j]);
+            }
+        }
+    }
+}
+
+// ---- launches ---------------------------------------------------------------------------
+
+constexpr int kFewTensors = 32;   // a table this short is a kernel argument of 3 KB
+
+bool on_grid(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+template <int N>
+cudaError_t launch_norm_table(const NormTensor *t, int count, double *partial, int *programs, cudaStream_t stream) {
+    Table<NormEntry, N> table;
+    table.count = count;
+    long long chunks = 0;
+    for (int i = 0; i < count; ++i) {
+        table.entry[i] = NormEntry{t[i].p, t[i].n, t[i].elem, 0};
+        table.first[i] = static_cast<int>(chunks);
+        const long long v = t[i].elem == ELEM_F32 ? 4 : 8;   // windows, with one more for the grid
+        chunks += ((t[i].n + v - 1) / v + 1 + kNormWindows - 1) / kNormWindows;
+        if (chunks > 0x7fffffff) return cudaErrorInvalidValue;
+    }
+    table.first[count] = static_cast<int>(chunks);
+    *programs = chunks < kNormPrograms ? static_cast<int>(chunks) : kNormPrograms;
+    norm_kernel<N><<<*programs, kNormThreads, 0, stream>>>(table, partial);
+    return cudaGetLastError();
+}
+
+template <int N>
+cudaError_t launch_adamw_table(const AdamwTensor *t, int count, int index, const AdamwConfig &c,
+                               const Scalars &s, cudaStream_t stream) {
+    Table<AdamwEntry, N> table;
+    int used = 0;
+    long long chunks = 0;
+    const long long chunk = c.eight ? kEightChunk : kAdamwChunk;
+    for (int i = 0; i < count; ++i) {
+        const AdamwTensor &a = t[i];
+        if (a.n == 0) continue;
+        const size_t four = c.eight ? 8 : 4;   // elements of a vector access
+        const size_t wide = c.eight ? 8 : 16;  // bytes of the states'
+        const size_t grad = a.grad_elem == ELEM_F32 ? 16 : 2 * four;
+        const bool vectors = on_grid(a.param, 16) && on_grid(a.grad, grad) && on_grid(a.m, wide) &&
+                             on_grid(a.v, wide) && on_grid(a.copy, 2 * four);
+        table.entry[used] = AdamwEntry{a.param, a.grad, a.m, a.v, a.m_scale, a.v_scale, a.copy, a.n,
+                                       a.decay, index + i, a.grad_elem, a.copy_elem, vectors};
+        table.first[used++] = static_cast<int>(chunks);
+        chunks += (a.n + chunk - 1) / chunk;
+        if (chunks > 0x7fffffff) return cudaErrorInvalidValue;
+    }
+    if (used == 0) return cudaSuccess;
+    table.count = used;
+    table.first[used] = static_cast<int>(chunks);
+    const unsigned int grid = static_cast<unsigned int>(chunks);
+    if (c.eight)
+        adamw8_kernel<N><<<grid, kAdamwThreads, 0, stream>>>(table, s);
+    else
+        adamw_kernel<N><<<grid, kAdamwThreads, 0, stream>>>(table, s);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t grad_norm_workspace(int count) {
+    const size_t launches = (static_cast<size_t>(count) + kNormTensors - 1) / kNormTensors;
+    return launches * kNormPrograms * sizeof(double);
+}
+
+cudaError_t launch_grad_norm(const NormTensor *t, int count, float scale, float max_norm,
+                             float *out, void *ws, cudaStream_t stream) {
+    double *partial = static_cast<double *>(ws);
+    int total = 0;
+    for (int i = 0; i < count; i += kNormTensors) {
+        const int n = count - i < kNormTensors ? count - i : kNormTensors;
+        int programs = 0;
+        const cudaError_t err = n <= kFewTensors
+            ? launch_norm_table<kFewTensors>(t + i, n, partial + total, &programs, stream)
+            : launch_norm_table<kNormTensors>(t + i, n, partial + total, &programs, stream);
+        if (err != cudaSuccess) return err;
+        total += programs;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kNormJoin);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    // with one launch of sums before it, the join comes up while they run
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = count > 0 && count <= kNormTensors ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, norm_join_kernel, static_cast<const double *>(partial), total, scale,
+                              max_norm, out);
+}
+
+cudaError_t launch_adamw(const AdamwTensor *t, int count, const AdamwConfig &c, cudaStream_t stream) {
+    Scalars s = {};
+    s.lr = static_cast<float>(c.lr);
+    s.beta1 = static_cast<float>(c.beta1);
+    s.rest1 = static_cast<float>(1.0 - c.beta1);
+    s.beta2 = static_cast<float>(c.beta2);
+    s.rest2 = static_cast<float>(1.0 - c.beta2);
+    s.eps = static_cast<float>(c.eps);
+    s.log1 = static_cast<float>(std::log(c.beta1));
+    s.log2 = static_cast<float>(std::log(c.beta2));
+    if (c.step_device == nullptr) {
+        s.rate = static_cast<float>(c.lr / (1.0 - std::pow(c.beta1, static_cast<double>(c.step))));
+        s.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(c.beta2, static_cast<double>(c.step))));
+    }
+    s.step = c.step;
+    s.lr_device = c.lr_device;
+    s.step_device = c.step_device;
+    s.factor = c.factor;
+    s.seed = c.seed;
+    for (int i = 0; i < count; i += kAdamwTensors) {
+        const int n = count - i < kAdamwTensors ? count - i : kAdamwTensors;
+        const cudaError_t err = n <= kFewTensors ? launch_adamw_table<kFewTensors>(t + i, n, i, c, s, stream)
+                                                 : launch_adamw_table<kAdamwTensors>(t + i, n, i, c, s, stream);
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace tile

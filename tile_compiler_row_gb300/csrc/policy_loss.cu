@@ -1,0 +1,372 @@
+// Clipped policy loss with a KL term, and its gradient.  For every token that
+// counts, with x = old_nll - nll, r = exp(x) and q = nll - ref_nll,
+//
+//   l = -min(r A, clip(r, 1 - low, 1 + high) A) + beta (exp(q) - q - 1)
+//   dl/dnll = (r A where it is the smaller one, else 0) + beta (exp(q) - 1)
+//
+// averaged over all tokens, or over sequences of means over their tokens.
+//
+// At most 36 bytes a token: bound by latency up to some 10^5 tokens and by
+// DRAM beyond.  Whether a ratio is clipped is decided by x against the bounds'
+// logarithms, as if x had not been rounded: r's own rounding would move
+// tokens over the border, where the gradient jumps.  Sums are FP32 over a tile
+// of 1024 rows, in a fixed order, and FP64 over tiles and sequences.
+#include "device_status.h"
+#include "policy_loss.h"
+
+TILE_DEVICE_STATUS(policy_loss)
+
+namespace tile {
+namespace {
+
+constexpr unsigned int kBadOffsets = 1;
+constexpr int kThreads = 256, kRows = 4, kTile = kThreads * kRows, kWarps = kThreads / 32;
+constexpr int kMostFused = 8;   // tiles that one cluster does, joined without another launch
+
+// The last sequence in [low, high] that begins at or before row.
+__device__ __forceinline__ int sequence_of(const long long *offsets, long long row, int low, int high) {
+    while (low < high) {
+        const int mid = low + (high - low + 1) / 2;
+        if (__ldg(offsets + mid) <= row)
+            low = mid;
+        else
+            high = mid - 1;
+    }
+    return low;
+}
+
+// The tile's sequences; those of its rows lie in [low, high].
+struct Span {
+    int low, high;
+    long long first, last;   // rows that belong to a sequence
+};
+__device__ __forceinline__ void find_span(const PolicyArgs &a, long long tile0, Span *span) {
+    const long long tile1 = min(tile0 + kTile, static_cast<long long>(a.rows)) - 1;
+    if (a.offsets == nullptr) {
+        if (threadIdx.x == 0) *span = Span{0, 0, 0, a.rows};
+    } else if (threadIdx.x == 0) {
+        span->low = sequence_of(a.offsets, tile0, 0, a.sequences - 1);
+        span->first = __ldg(a.offsets);
+    } else if (threadIdx.x == 32) {
+        span->high = sequence_of(a.offsets, tile1, 0, a.sequences - 1);
+        span->last = __ldg(a.offsets + a.sequences);
+    }
+    __syncthreads();
+}
+
+// Whether old - nll > bound (sign 1) or < bound (sign -1), unrounded.
+__device__ __forceinline__ bool beyond(float old, float nll, float x, float bound, float rest, float sign) {
+    if (x != bound) return sign * x > sign * bound;
+    const float back = __fsub_rn(x, old);   // x + what its rounding cut off is old - nll
+    const float cut = __fsub_rn(__fsub_rn(old, __fsub_rn(x, back)), __fadd_rn(nll, back));
+    return sign * cut > sign * rest;
+}
+
+// A row's inputs.
+struct Token {
+    float nll, old, ref, adv;
+    bool counts;
+};
+
+// Rows tile0 + thread + 256 u of the tile.
+__device__ __forceinline__ void load_tokens(const PolicyArgs &a, long long tile0, const Span &span,
+                                            Token (&t)[kRows], int (&of)[kRows], bool need_of) {
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        const long long row = tile0 + threadIdx.x + u * kThreads;
+        const bool in = row < a.rows && row >= span.first && row < span.last;
+        t[u] = Token{0.0f, 0.0f, 0.0f, 0.0f, in};
+        of[u] = span.low;
+        if (!in) continue;
+        if (a.target != nullptr) t[u].counts = __ldcs(a.target + row) != a.ignore;
+        t[u].nll = __ldcs(a.nll + row);
+        t[u].old = __ldcs(a.old_nll + row);
+        if (a.ref_nll != nullptr) t[u].ref = __ldcs(a.ref_nll + row);
+        if (!a.sequence_advantage) t[u].adv = __ldcs(a.advantage + row);
+    }
+    if (!need_of && !a.sequence_advantage) return;
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+        if (t[u].counts) {
+            if (a.offsets != nullptr)
+                of[u] = sequence_of(a.offsets, tile0 + threadIdx.x + u * kThreads, span.low, span.high);
+            if (a.sequence_advantage) t[u].adv = __ldg(a.advantage + of[u]);
+        }
+}
+
+__device__ __forceinline__ bool is_clipped(const PolicyArgs &a, const Token &t, float x) {
+    return t.adv > 0.0f ? beyond(t.old, t.nll, x, a.high, a.high_rest, 1.0f)
+                        : t.adv < 0.0f && beyond(t.old, t.nll, x, a.low, a.low_rest, -1.0f);
+}
+
+// (surrogate, KL, clipped, 1) of a token; zeros for one that does not count.
+__device__ __forceinline__ float4 parts_of(const PolicyArgs &a, const Token &t) {
+    if (!t.counts) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float x = __fsub_rn(t.old, t.nll);
+    const bool clipped = is_clipped(a, t, x);
+    const float ratio = clipped ? (t.adv > 0.0f ? 1.0f + a.clip_high : 1.0f - a.clip_low) : expf(x);
+    float kl = 0.0f;
+    if (a.ref_nll != nullptr) {
+        const float q = __fsub_rn(t.nll, t.ref);
+        kl = expm1f(q) - q;
+    }
+    return make_float4(t.adv == 0.0f ? 0.0f : -ratio * t.adv, kl, clipped ? 1.0f : 0.0f, 1.0f);
+}
+
+__device__ __forceinline__ float4 add4(float4 p, float4 q) {
+    return make_float4(p.x + q.x, p.y + q.y, p.z + q.z, p.w + q.w);
+}
+__device__ __forceinline__ float4 warp_sum(float4 v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, d);
+        v.w += __shfl_xor_sync(0xffffffffu, v.w, d);
+    }
+    return v;
+}
+
+struct TileMem {
+    Span span;
+    float4 part[kTile];
+};
+
+// Sums of a tile: slots[tile] of all its tokens or, by sequence, slots[tile +
+// s] of those of sequence s (tile and s both grow along the rows: no other
+// tile and sequence share that slot).
+__device__ __forceinline__ void tile_sums(const PolicyArgs &a, int tile, float4 *slots, TileMem &mem) {
+    const long long tile0 = static_cast<long long>(tile) * kTile;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    find_span(a, tile0, &mem.span);
+    const Span span = mem.span;
+    Token t[kRows];
+    int of[kRows];
+    load_tokens(a, tile0, span, t, of, false);
+    if (!a.sequence_mean) {
+        float4 v = parts_of(a, t[0]);
+#pragma unroll
+        for (int u = 1; u < kRows; ++u) v = add4(v, parts_of(a, t[u]));
+        v = warp_sum(v);
+        if (lane == 0) mem.part[warp] = v;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kWarps; ++w) v = add4(v, mem.part[w]);
+            slots[tile] = v;
+        }
+        return;
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) mem.part[threadIdx.x + u * kThreads] = parts_of(a, t[u]);
+    __syncthreads();
+    const int count = span.high - span.low + 1;
+    // a warp for each sequence, or a thread where there are many
+    const bool wide = count <= 8 * kWarps;
+    for (int k = wide ? warp : threadIdx.x; k < count; k += wide ? kWarps : kThreads) {
+        const int s = span.low + k;
+        long long begin = 0, end = a.rows;
+        if (a.offsets != nullptr) {
+            begin = __ldg(a.offsets + s);
+            end = __ldg(a.offsets + s + 1);
+        }
+        const long long most = kTile;   // (offsets that do not grow stay within the tile)
+        const int from = static_cast<int>(max(min(begin - tile0, most), 0ll));
+        const int to = static_cast<int>(max(min(end - tile0, most), 0ll));
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i = from + (wide ? lane : 0); i < to; i += wide ? 32 : 1) v = add4(v, mem.part[i]);
+        if (wide) v = warp_sum(v);
+        if (!wide || lane == 0) slots[static_cast<long long>(tile) + s] = v;
+    }
+}
+
+// Block-wide sums of N doubles, for thread 0 (and in shared memory for all).
+template <int N, int THREADS>
+__device__ __forceinline__ void block_sum(double (&v)[N], double (*mem)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) mem[threadIdx.x >> 5][i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = 0.0;
+        for (int w = 0; w < THREADS / 32; ++w) v[i] += mem[w][i];
+    }
+}
+
+// The slots' sums to stats and weights.
+template <int THREADS>
+__device__ __forceinline__ void join_sums(const PolicyArgs &a, const float4 *slots) {
+    __shared__ double mem[THREADS / 32][4];
+    const int tiles = (a.rows + kTile - 1) / kTile, tid = threadIdx.x;
+    double sum[4] = {};   // surrogate, KL, clipped, and tokens or sequences that count
+    bool bad = false;
+    if (!a.sequence_mean) {
+        for (int t = tid; t < tiles; t += THREADS) {
+            const float4 v = __ldcg(slots + t);
+            sum[0] += v.x;
+            sum[1] += v.y;
+            sum[2] += v.z;
+            sum[3] += v.w;
+        }
+    }
+    for (int base = 0; base < a.sequences; base += THREADS) {
+        const int s = base + tid;
+        long long begin = 0, end = s < a.sequences ? a.rows : 0;
+        if (a.offsets != nullptr && s < a.sequences) {
+            begin = __ldg(a.offsets + s);
+            end = __ldg(a.offsets + s + 1);
+            if (begin < 0 || end < begin || end > a.rows) {
+                bad = true;
+                begin = end = 0;
+            }
+        }
+        if (!a.sequence_mean) continue;
+        double v[4] = {};
+        const int first = static_cast<int>(begin / kTile);
+        const int last = begin < end ? static_cast<int>((end - 1) / kTile) : first - 1;
+        if (last - first < 32)
+            for (int t = first; t <= last; ++t) {
+                const float4 p = __ldcg(slots + static_cast<long long>(t) + s);
+                v[0] += p.x;
+                v[1] += p.y;
+                v[2] += p.z;
+                v[3] += p.w;
+            }
+        // long sequences: the warp together
+        unsigned int left = __ballot_sync(0xffffffffu, last - first >= 32);
+        while (left != 0) {
+            const int from = __ffs(left) - 1;
+            left &= left - 1;
+            const int f = __shfl_sync(0xffffffffu, first, from), l = __shfl_sync(0xffffffffu, last, from);
+            const int of = __shfl_sync(0xffffffffu, s, from);
+            double w[4] = {};
+            for (int t = f + (tid & 31); t <= l; t += 32) {
+                const float4 p = __ldcg(slots + static_cast<long long>(t) + of);
+                w[0] += p.x;
+                w[1] += p.y;
+                w[2] += p.z;
+                w[3] += p.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) w[i] += __shfl_xor_sync(0xffffffffu, w[i], d);
+                if ((tid & 31) == from) v[i] = w[i];
+            }
+        }
+        const bool counts = v[3] > 0.0;
+        if (s < a.sequences) a.weights[s] = counts ? static_cast<float>(1.0 / v[3]) : 0.0f;
+        if (counts) {
+            sum[0] += v[0] / v[3];
+            sum[1] += v[1] / v[3];
+            sum[2] += v[2] / v[3];
+            sum[3] += 1.0;
+        }
+    }
+    bad = __syncthreads_or(bad);
+    block_sum<4, THREADS>(sum, mem);
+    const double share = sum[3] > 0.0 ? 1.0 / sum[3] : 0.0;
+    for (int s = tid; s < a.sequences; s += THREADS)   // (each thread its own ones)
+        a.weights[s] = a.sequence_mean ? static_cast<float>(a.weights[s] * share) : static_cast<float>(share);
+    if (tid != 0) return;
+    const double nan = __longlong_as_double(0x7ff8000000000000ll);
+    if (bad) atomicOr(a.status, kBadOffsets);
+    const double surrogate = bad ? nan : sum[0] * share, kl = bad ? nan : sum[1] * share;
+    a.stats[0] = static_cast<float>(surrogate + static_cast<double>(a.kl_coef) * kl);
+    a.stats[1] = static_cast<float>(surrogate);
+    a.stats[2] = static_cast<float>(kl);
+    a.stats[3] = static_cast<float>(bad ? nan : sum[2] * share);
+}
+
+__global__ void __launch_bounds__(kThreads) tiles_kernel(const PolicyArgs a) {
+    __shared__ TileMem mem;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    tile_sums(a, blockIdx.x, static_cast<float4 *>(a.ws), mem);
+}
+
+constexpr int kJoinThreads = 1024;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const PolicyArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the tiles' sums are written
+    join_sums<kJoinThreads>(a, static_cast<const float4 *>(a.ws));
+}
+
+// A cluster of as many CTAs as there are tiles; the first one joins them.
+__global__ void __launch_bounds__(kThreads) fused_kernel(const PolicyArgs a) {
+    __shared__ TileMem mem;
+    tile_sums(a, blockIdx.x, static_cast<float4 *>(a.ws), mem);
+    __syncthreads();
+    __threadfence();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (blockIdx.x == 0) join_sums<kThreads>(a, static_cast<const float4 *>(a.ws));
+}
+
+__global__ void __launch_bounds__(kThreads) backward_kernel(const PolicyArgs a) {
+    __shared__ Span shared_span;
+    const long long tile0 = static_cast<long long>(blockIdx.x) * kTile;
+    find_span(a, tile0, &shared_span);
+    const Span span = shared_span;
+    const float up = a.dloss != nullptr ? __ldg(a.dloss) : 1.0f;
+    Token t[kRows];
+    int of[kRows];
+    load_tokens(a, tile0, span, t, of, true);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        const long long row = tile0 + threadIdx.x + u * kThreads;
+        if (row >= a.rows) continue;
+        float d = 0.0f;
+        if (t[u].counts) {
+            const float x = __fsub_rn(t[u].old, t[u].nll);
+            if (t[u].adv != 0.0f && !is_clipped(a, t[u], x)) d = expf(x) * t[u].adv;
+            if (a.ref_nll != nullptr) d = fmaf(a.kl_coef, expm1f(__fsub_rn(t[u].nll, t[u].ref)), d);
+            d *= __ldg(a.weights + of[u]) * up;
+        }
+        __stcs(a.dnll + row, d);
+    }
+}
+
+}  // namespace
+
+size_t policy_loss_workspace(int rows, int sequences) {
+    const size_t tiles = (static_cast<size_t>(rows) + kTile - 1) / kTile;
+    return (tiles + static_cast<size_t>(sequences)) * sizeof(float4);
+}
+
+cudaError_t launch_policy_loss(PolicyArgs a, cudaStream_t stream) {
+    cudaError_t err = cudaSuccess;
+    a.status = status_address(&err);
+    if (a.status == nullptr) return err;
+    const int tiles = (a.rows + kTile - 1) / kTile;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(tiles);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (tiles <= kMostFused) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = tiles;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, fused_kernel, a);
+    }
+    err = cudaLaunchKernelEx(&cfg, tiles_kernel, a);
+    if (err != cudaSuccess) return err;
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kJoinThreads);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel, a);
+}
+
+cudaError_t launch_policy_loss_backward(PolicyArgs a, cudaStream_t stream) {
+    backward_kernel<<<(a.rows + kTile - 1) / kTile, kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace tile

@@ -899,7 +899,8 @@ int tile_check_device_status(cudaStream_t stream) {
         tile::status_row_sum_f16, tile::status_row_minmax_f16, tile::status_pairs,
         tile::status_backward, tile::status_backward_bf16, tile::status_backward_f16,
         tile::status_param_grad, tile::status_staged, tile::status_multi,
-        tile::status_block_norm_backward, tile::status_linear_ce};
+        tile::status_block_norm_backward, tile::status_linear_ce, tile::status_embedding,
+        tile::status_policy_loss};
     for (auto f : fetch) {
         v = 0;
         const cudaError_t err = f(&v, stream);
