@@ -572,7 +572,7 @@ int tile_embedding_backward(int dtype, int dweight_dtype, const long long *token
  * nll, old_nll, ref_nll [rows], advantage [rows] or [sequences]: FP32.  Whether r
  * is held back is decided from old_nll - nll as if it had not been rounded; r A
  * equal to its bound is not.  An advantage of 0 gives a first term of 0.  Sums
- * are FP32 over 1024 rows and FP64 beyond, bitwise reproducible.  `workspace`:
+ * are FP32 over 1024 rows and compensated beyond, bitwise reproducible.  `workspace`:
  * 16-byte aligned device memory of the caller; calls that overlap in time need
  * workspaces of their own.  rows == 0 writes zeros.  TILE_ERR_EPS for clip_low
  * outside [0, 1], a negative or NaN clip_high or a kl_coef that is not finite;
@@ -667,8 +667,8 @@ int tile_grad_norm(const tile_tensor_t *tensors, int count, float scale, float m
  * operation.  Pointers: aligned to their element; the 16-byte grid (8-byte for
  * codes and 16-bit tensors) is the fastest.  No written range may overlap another
  * range of the call (TILE_ERR_ALIAS): a tensor is listed once.  n >= 0, no limit
- * on count.  TILE_ERR_EPS for betas outside [0, 1), eps that is not finite and
- * above 0, an lr or weight_decay that is not finite; TILE_ERR_SHAPE for n < 0,
+ * on count.  TILE_ERR_EPS for betas outside [0, 1), eps that is not finite or
+ * below 2^-126, an lr or weight_decay that is not finite; TILE_ERR_SHAPE for n < 0,
  * count < 0, step < 1; TILE_ERR_DTYPE for unknown types (copy_dtype: BF16 or
  * F16); other rules and errors as the row entry points.  May be captured into a
  * CUDA graph, which then holds the pointers. */

@@ -198,7 +198,7 @@ def test_adamw_eight_bit_refusals(lib, row, status):
 @fake_pointers
 @pytest.mark.parametrize("config,status", [
     ({"beta1": 1.0}, EPS), ({"beta1": -0.1}, EPS), ({"beta2": 1.0}, EPS), ({"beta2": NAN}, EPS),
-    ({"eps": 0.0}, EPS), ({"eps": 1e-60}, EPS), ({"eps": INF}, EPS), ({"lr": INF}, EPS), ({"lr": 1e40}, EPS),
+    ({"eps": 0.0}, EPS), ({"eps": 1e-39}, EPS), ({"eps": INF}, EPS), ({"lr": INF}, EPS), ({"lr": 1e40}, EPS),
     ({"step": 0}, SHAPE), ({"step": -5}, SHAPE), ({"state": 2}, OP), ({"lr_device": G + 2}, ALIGN),
     ({"step_device": G + 4}, ALIGN), ({"factor": G + 1}, ALIGN), ({"factor": A}, ALIAS),
     ({"step_device": D + 8}, ALIAS)])

@@ -14,8 +14,9 @@ and importing the binding without the built library raises.
 from __future__ import annotations
 
 import ctypes
-import operator
+import itertools
 import os
+import struct
 
 from ._build import LIBRARY
 
@@ -887,6 +888,7 @@ def _ptr(t, name, dtype, shape, dev):
 
 
 _INT_MAX = 0x7fffffff
+_INF = float("inf")
 
 
 def _fit_int(*sizes):
@@ -1088,8 +1090,30 @@ def tile_linear_cross_entropy_backward(x, weight, target, lse, dloss, dx, dweigh
 
 # ---- embedding -----------------------------------------------------------------
 
+_F32 = _I64 = _F8 = None     # torch dtypes, filled with _CODES
+
+
+def _kinds():
+    """The torch dtypes above, on first use."""
+    global _F32, _I64, _F8
+    import torch
+    _CODES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    _I64, _F8, _F32 = torch.int64, torch.float8_e4m3fn, torch.float32
+
+
+def _rows_of(t, name):
+    """(type code, device index) of a 2-D row tensor on a device."""
+    if _F32 is None:
+        _kinds()
+    code = _CODES.get(getattr(t, "dtype", None))
+    if code is None or t.dim() != 2 or not t.is_cuda:
+        _row_code(t, name)
+        _device_index(t, name)
+    return code, t.get_device()
+
+
 def _long(value, name):
-    if not -1 << 63 <= value < 1 << 63:
+    if not -0x8000000000000000 <= value <= 0x7fffffffffffffff:
         raise ValueError(f"{name} must be a 64-bit integer")
     return value
 
@@ -1097,16 +1121,15 @@ def _long(value, name):
 def tile_embedding(tokens, weight, out, scale=1.0, ignore_index=-100, stream=None):
     """out[i] = scale * weight[tokens[i]] (float32, bfloat16 or float16); see
     include/tile_rows.h."""
-    import torch
-    code, dev = _row_code(weight, "weight"), _device_index(weight, "weight")
-    vocab, width = weight.shape
+    code, dev = _rows_of(weight, "weight")
+    shape, dtype = weight.shape, weight.dtype
+    vocab, width = shape
     rows = tokens.shape[0] if tokens.dim() == 1 else -1
     if not _fit_int(rows, width, vocab):
         raise ValueError("tokens must be 1-D, and rows, width and vocab below 2^31")
-    _call_on(dev, stream, "tile_embedding", code,
-             _ptr(tokens, "tokens", torch.int64, (rows,), dev),
-             _ptr(weight, "weight", weight.dtype, weight.shape, dev),
-             _ptr(out, "out", weight.dtype, (rows, width), dev), rows, width, vocab, scale,
+    _call_on(dev, stream, "tile_embedding", code, _ptr(tokens, "tokens", _I64, (rows,), dev),
+             _ptr(weight, "weight", dtype, shape, dev),
+             _ptr(out, "out", dtype, (rows, width), dev), rows, width, vocab, scale,
              _long(ignore_index, "ignore_index"))
 
 
@@ -1120,19 +1143,18 @@ def tile_embedding_backward(tokens, dout, dweight, workspace, scale=1.0, ignore_
                             accumulate=False, stream=None):
     """dweight = (or, with ``accumulate``, +=) the gradient of
     ``tile_embedding``'s weight; dweight may be float32 for 16-bit rows."""
-    import torch
-    code, dev = _row_code(dout, "dout"), _device_index(dout, "dout")
-    into = _row_code(dweight, "dweight")
+    code, dev = _rows_of(dout, "dout")
+    into, _ = _rows_of(dweight, "dweight")
     rows, width = dout.shape
     vocab = dweight.shape[0]
     if not _fit_int(rows, width, vocab):
         raise ValueError(f"rows, width and vocab must be below 2^31, not {rows}, {width}, {vocab}")
     ws, nbytes = _workspace(workspace, dev)
     _call_on(dev, stream, "tile_embedding_backward", code, into,
-             _ptr(tokens, "tokens", torch.int64, (rows,), dev),
+             _ptr(tokens, "tokens", _I64, (rows,), dev),
              _ptr(dout, "dout", dout.dtype, dout.shape, dev),
              _ptr(dweight, "dweight", dweight.dtype, (vocab, width), dev), rows, width, vocab,
-             scale, _long(ignore_index, "ignore_index"), int(bool(accumulate)), ws, nbytes)
+             scale, _long(ignore_index, "ignore_index"), 1 if accumulate else 0, ws, nbytes)
 
 
 # ---- policy loss -----------------------------------------------------------------
@@ -1145,25 +1167,27 @@ def tile_policy_loss_workspace_bytes(rows, sequences):
 
 def _policy_args(nll, old_nll, advantage, ref_nll, target, offsets, clip_low, clip_high, kl_coef,
                  sequence_advantage, sequence_mean, ignore_index):
-    """(argument struct, device index, rows, sequences)."""
-    import torch
-    dev, f32 = _device_index(nll, "nll"), torch.float32
+    """(argument struct, device index, shape of nll, sequences)."""
+    if _F32 is None:
+        _kinds()
+    dev, f32 = _device_index(nll, "nll"), _F32
     if nll.dim() != 1:
         raise ValueError("nll must be 1-D")
-    rows = nll.shape[0]
+    shape = nll.shape
+    rows = shape[0]
     sequences = 1 if offsets is None else offsets.numel() - 1
     if not _fit_int(rows, sequences) or sequences < 1:
         raise ValueError("offsets must have at least two elements, and rows be below 2^31")
     a = TilePolicyLossArgs(
-        _ptr(nll, "nll", f32, (rows,), dev), _ptr(old_nll, "old_nll", f32, (rows,), dev),
-        _ptr(ref_nll, "ref_nll", f32, (rows,), dev),
-        _ptr(advantage, "advantage", f32, (sequences if sequence_advantage else rows,), dev),
-        _ptr(target, "target", torch.int64, (rows,), dev),
-        _ptr(offsets, "offsets", torch.int64, (sequences + 1,), dev),
+        _ptr(nll, "nll", f32, shape, dev), _ptr(old_nll, "old_nll", f32, shape, dev),
+        _ptr(ref_nll, "ref_nll", f32, shape, dev),
+        _ptr(advantage, "advantage", f32, (sequences,) if sequence_advantage else shape, dev),
+        _ptr(target, "target", _I64, shape, dev),
+        _ptr(offsets, "offsets", _I64, (sequences + 1,), dev),
         _long(ignore_index, "ignore_index"), rows, sequences,
         (1 if sequence_advantage else 0) | (2 if sequence_mean else 0), clip_low, clip_high,
         kl_coef)
-    return a, dev, rows, sequences
+    return a, dev, shape, sequences
 
 
 def tile_policy_loss(nll, old_nll, advantage, stats, weights, workspace, ref_nll=None, target=None,
@@ -1171,14 +1195,13 @@ def tile_policy_loss(nll, old_nll, advantage, stats, weights, workspace, ref_nll
                      sequence_advantage=False, sequence_mean=False, ignore_index=-100, stream=None):
     """stats (loss, clipped term, KL term, clipped share) and the token weights
     of each sequence; see ``tile_policy_loss`` in include/tile_rows.h."""
-    import torch
     a, dev, _, sequences = _policy_args(nll, old_nll, advantage, ref_nll, target, offsets, clip_low,
                                         clip_high, kl_coef, sequence_advantage, sequence_mean,
                                         ignore_index)
     ws, nbytes = _workspace(workspace, dev)
     _call_on(dev, stream, "tile_policy_loss", ctypes.byref(a),
-             _ptr(stats, "stats", torch.float32, (4,), dev),
-             _ptr(weights, "weights", torch.float32, (sequences,), dev), ws, nbytes)
+             _ptr(stats, "stats", _F32, (4,), dev),
+             _ptr(weights, "weights", _F32, (sequences,), dev), ws, nbytes)
 
 
 def tile_policy_loss_backward(nll, old_nll, advantage, weights, dnll, dloss=None, ref_nll=None,
@@ -1186,14 +1209,12 @@ def tile_policy_loss_backward(nll, old_nll, advantage, weights, dnll, dloss=None
                               sequence_advantage=False, ignore_index=-100, stream=None):
     """dnll of ``tile_policy_loss`` for the gradient ``dloss`` of stats[0] (one
     element on the device; None: 1)."""
-    import torch
-    a, dev, rows, sequences = _policy_args(nll, old_nll, advantage, ref_nll, target, offsets,
-                                           clip_low, clip_high, kl_coef, sequence_advantage, False,
-                                           ignore_index)
-    f32 = torch.float32
+    a, dev, shape, sequences = _policy_args(nll, old_nll, advantage, ref_nll, target, offsets,
+                                            clip_low, clip_high, kl_coef, sequence_advantage, False,
+                                            ignore_index)
     _call_on(dev, stream, "tile_policy_loss_backward", ctypes.byref(a),
-             _ptr(weights, "weights", f32, (sequences,), dev), _one(dloss, "dloss", f32, dev),
-             _ptr(dnll, "dnll", f32, (rows,), dev))
+             _ptr(weights, "weights", _F32, (sequences,), dev), _one(dloss, "dloss", _F32, dev),
+             _ptr(dnll, "dnll", _F32, shape, dev))
 
 
 def _one(t, name, dtype, dev):
@@ -1207,47 +1228,63 @@ def _one(t, name, dtype, dev):
 
 # ---- gradient norm and AdamW step --------------------------------------------------
 #
-# Lists of tensors: each list is gone through by a few C-level passes rather than
-# a call per tensor, and only a list that fails them is looked at one by one.
+# A small model has hundreds of tensors of which a call takes five lists: each
+# list is gone through once by one expression a tensor, and only a tensor that
+# fails it is looked at again for the message.
 
-_IS_CONTIGUOUS, _GET_DEVICE, _NUMEL, _DATA_PTR = map(
-    operator.methodcaller, ("is_contiguous", "get_device", "numel", "data_ptr"))
-_DTYPE = operator.attrgetter("dtype")
-
-
-def _pointers(tensors, name, dtypes, counts, dev):
-    """Pointers of a list of contiguous CUDA tensors on device index ``dev``,
-    of these element counts (None: any) and types."""
-    if counts is not None and len(tensors) != len(counts):
+def _columns(tensors, name, types, counts, dev):
+    """(pointers, element counts, type codes) of a list of contiguous CUDA
+    tensors on device index ``dev``, of types that ``types`` has codes for and
+    of these element counts (None: any)."""
+    if len(tensors) != (len(tensors) if counts is None else len(counts)):
         raise ValueError(f"{name} must have {len(counts)} tensors like the other lists, "
                          f"not {len(tensors)}")
-    if (all(map(_IS_CONTIGUOUS, tensors)) and set(map(_GET_DEVICE, tensors)) <= {dev}
-            and set(map(_DTYPE, tensors)) <= dtypes
-            and (counts is None or list(map(_NUMEL, tensors)) == counts)):
-        return list(map(_DATA_PTR, tensors))
+    pointers, sizes, codes = [], [], []
+    try:
+        for t in tensors:
+            code = types.get(t.dtype)
+            if code is None or t.get_device() != dev or not t.is_contiguous():
+                break
+            codes.append(code)
+            sizes.append(t.numel())
+            pointers.append(t.data_ptr())
+        else:
+            if counts is None or sizes == counts:
+                return pointers, sizes, codes
+    except AttributeError:
+        pass
+    _list_of_tensors(tensors, name)
     for i, t in enumerate(tensors):
-        if t.dtype not in dtypes:
-            raise ValueError(f"{name}[{i}] must be one of {sorted(map(str, dtypes))}, not {t.dtype}")
+        if t.dtype not in types:
+            raise ValueError(f"{name}[{i}] must be one of {sorted(map(str, types))}, not {t.dtype}")
         if counts is not None and t.numel() != counts[i]:
             raise ValueError(f"{name}[{i}] must have {counts[i]} elements, not {t.numel()}")
         _ptr(t, f"{name}[{i}]", t.dtype, t.shape, dev)
     raise ValueError(f"{name} must be CUDA tensors of one device")
 
 
-def _list_device(tensors, name):
+def _list_of_tensors(tensors, name):
     import torch
     if isinstance(tensors, torch.Tensor):
         raise TypeError(f"{name} must be a list of tensors")
     for i, t in enumerate(tensors):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}[{i}] must be a torch.Tensor")
-    return _device_index(tensors[0], f"{name}[0]") if len(tensors) else None
+
+
+def _list_device(tensors, name):
+    """Device index of the first tensor of a list, None of an empty one."""
+    import torch
+    if isinstance(tensors, torch.Tensor) or not len(tensors) or \
+            not isinstance(tensors[0], torch.Tensor):
+        _list_of_tensors(tensors, name)
+        return None
+    return _device_index(tensors[0], f"{name}[0]")
 
 
 def _records(form, count, columns):
     """C structs of one format from columns of their fields."""
-    import struct
-    return struct.pack(form * count, *[v for row in zip(*columns) for v in row])
+    return struct.pack(form * count, *itertools.chain.from_iterable(zip(*columns)))
 
 
 def tile_grad_norm_workspace_bytes(count):
@@ -1257,17 +1294,14 @@ def tile_grad_norm_workspace_bytes(count):
 def tile_grad_norm(grads, out, workspace, scale=1.0, max_norm=None, stream=None):
     """out = (norm, clipping factor) of all ``grads`` together (float32,
     bfloat16 or float16, in any mix); see include/tile_rows.h."""
-    import torch
+    if _F32 is None:
+        _kinds()
     _list_device(grads, "grads")
     dev, count = _device_index(out, "out"), len(grads)
-    kinds = {torch.float32, torch.bfloat16, torch.float16}
-    at = _pointers(grads, "grads", kinds, None, dev)
-    codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    table = _records("2qi4x", count, (at, [t.numel() for t in grads], [codes[t.dtype] for t in grads]))
+    table = _records("2qi4x", count, _columns(grads, "grads", _CODES, None, dev))
     ws, nbytes = _workspace(workspace, dev)
     _call_on(dev, stream, "tile_grad_norm", table, count, scale,
-             float("inf") if max_norm is None else max_norm,
-             _ptr(out, "out", torch.float32, (2,), dev), ws, nbytes)
+             _INF if max_norm is None else max_norm, _ptr(out, "out", _F32, (2,), dev), ws, nbytes)
 
 
 def tile_adamw(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
@@ -1280,53 +1314,41 @@ def tile_adamw(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     None).  ``step`` (from 1 on) and ``lr`` are numbers, or tensors of one
     element on the device (int64, float32); ``weight_decay`` a number or one
     for each tensor; ``factor`` ``tile_grad_norm``'s second output."""
-    import torch
-    f32, f8 = torch.float32, torch.float8_e4m3fn
+    if _F32 is None:
+        _kinds()
     dev, count = _list_device(params, "params"), len(params)
-    for name, ts in (("grads", grads), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)):
-        _list_device(ts, name)
-    if dev is None:
-        for name, ts in (("grads", grads), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)):
-            if len(ts):
-                raise ValueError(f"{name} must be empty like params")
-        return
-    n = [t.numel() for t in params]
-    none = [0] * count
-    p = _pointers(params, "params", {f32}, n, dev)
-    g = _pointers(grads, "grads", {f32, torch.bfloat16, torch.float16}, n, dev)
-    eight = len(exp_avg) > 0 and exp_avg[0].dtype is f8
-    state = {f8 if eight else f32}
-    m = _pointers(exp_avg, "exp_avg", state, n, dev)
-    v = _pointers(exp_avg_sq, "exp_avg_sq", state, n, dev)
-    ms = vs = c = cc = none
+    f32 = {_F32: 0}
+    p, n, _ = _columns(params, "params", f32, None, dev)
+    g, _, kinds = _columns(grads, "grads", _CODES, n, dev)
+    eight = count > 0 and len(exp_avg) > 0 and getattr(exp_avg[0], "dtype", None) is _F8
+    state = {_F8: 0} if eight else f32
+    m, _, _ = _columns(exp_avg, "exp_avg", state, n, dev)
+    v, _, _ = _columns(exp_avg_sq, "exp_avg_sq", state, n, dev)
+    ms = vs = c = copy_kinds = [0] * count
     if eight:
         if exp_avg_scales is None or exp_avg_sq_scales is None:
             raise ValueError("8-bit states need exp_avg_scales and exp_avg_sq_scales")
-        _list_device(exp_avg_scales, "exp_avg_scales")
-        _list_device(exp_avg_sq_scales, "exp_avg_sq_scales")
         blocks = [-(-k // 256) for k in n]
-        ms = _pointers(exp_avg_scales, "exp_avg_scales", {f32}, blocks, dev)
-        vs = _pointers(exp_avg_sq_scales, "exp_avg_sq_scales", {f32}, blocks, dev)
-    elif exp_avg_scales is not None or exp_avg_sq_scales is not None:
+        ms, _, _ = _columns(exp_avg_scales, "exp_avg_scales", f32, blocks, dev)
+        vs, _, _ = _columns(exp_avg_sq_scales, "exp_avg_sq_scales", f32, blocks, dev)
+    elif count > 0 and (exp_avg_scales is not None or exp_avg_sq_scales is not None):
         raise ValueError("scales belong to 8-bit states")
-    codes = {f32: 0, torch.bfloat16: 1, torch.float16: 2}
     if copies is not None:
-        _list_device(copies, "copies")
-        c = _pointers(copies, "copies", {torch.bfloat16, torch.float16}, n, dev)
-        cc = [codes[t.dtype] for t in copies]
-    decay = [float(weight_decay)] * count if isinstance(weight_decay, (int, float)) \
-        else list(map(float, weight_decay))
+        halves = {k: i for k, i in _CODES.items() if i != 0}
+        c, _, copy_kinds = _columns(copies, "copies", halves, n, dev)
+    decay = [weight_decay] * count if isinstance(weight_decay, (int, float)) else weight_decay
     if len(decay) != count:
         raise ValueError(f"weight_decay must be a number or {count} of them")
-    table = _records("8qf2i4x", count, (p, g, m, v, ms, vs, c, n, decay,
-                                        [codes[t.dtype] for t in grads], cc))
-    on_device = isinstance(step, torch.Tensor), isinstance(lr, torch.Tensor)
+    if count == 0:
+        return
+    table = _records("8qf2i4x", count, (p, g, m, v, ms, vs, c, n, decay, kinds, copy_kinds))
+    step_at, lr_at = getattr(step, "is_cuda", None), getattr(lr, "is_cuda", None)
     config = TileAdamwConfig(
-        0.0 if on_device[1] else lr, betas[0], betas[1], eps,
-        0 if on_device[0] else _long(step, "step"),
-        _one(lr, "lr", f32, dev) if on_device[1] else None,
-        _one(step, "step", torch.int64, dev) if on_device[0] else None,
-        _one(factor, "factor", f32, dev), seed & 0xFFFFFFFFFFFFFFFF, 1 if eight else 0)
+        lr if lr_at is None else 0.0, betas[0], betas[1], eps,
+        _long(step, "step") if step_at is None else 0,
+        None if lr_at is None else _one(lr, "lr", _F32, dev),
+        None if step_at is None else _one(step, "step", _I64, dev),
+        _one(factor, "factor", _F32, dev), seed & 0xFFFFFFFFFFFFFFFF, 1 if eight else 0)
     _call_on(dev, stream, "tile_adamw", table, count, ctypes.byref(config))
 
 
@@ -1455,8 +1477,8 @@ def linear_cross_entropy_backward(x, weight, target, lse, dloss, ignore_index=-1
 def embedding(tokens, weight, scale=1.0, ignore_index=-100):
     """scale * weight[tokens], rows of zeros where a token is ignore_index."""
     import torch
-    _row_code(weight, "weight")
-    out = torch.empty(tokens.shape[0], weight.shape[1], dtype=weight.dtype, device=weight.device)
+    _rows_of(weight, "weight")
+    out = torch.empty((tokens.shape[0], weight.shape[1]), dtype=weight.dtype, device=weight.device)
     tile_embedding(tokens, weight, out, scale, ignore_index)
     return out
 

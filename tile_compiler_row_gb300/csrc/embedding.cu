@@ -51,19 +51,19 @@ __global__ void __launch_bounds__(256) lookup_kernel(const EmbeddingArgs a, int 
     T *dst = static_cast<T *>(a.out) + static_cast<long long>(row) * a.width;
     const int phase = VEC ? 0 : window_phase(dst);
     const int windows = windows_of<T>(a.width, VEC);
+    const Bounds bounds = bounds_of<T>(a.weight, a.vocab, a.width);
     for (int j = lane; j < windows; j += U * lanes) {
-        uint4 raw[U];
+        RawWindow<VEC> raw[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (token >= 0 && j + u * lanes < windows)
-                raw[u] = load_window<T, VEC>(src, (j + u * lanes) * V - phase, a.width);
-        }
+        for (int u = 0; u < U; ++u)
+            raw[u] = fetch_window<T, VEC>(src, (j + u * lanes) * V - phase, bounds,
+                                          token >= 0 && j + u * lanes < windows);
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (j + u * lanes < windows) {
                 float v[V];
-                widen_vec<T>(raw[u], v);
+                widen_vec<T>(join_window<T, VEC>(raw[u], src, (j + u * lanes) * V - phase, a.width, bounds,
+                                                 token >= 0), v);
 #pragma unroll
                 for (int i = 0; i < V; ++i)   // an ignored row is 0 whatever the scale, a bad one NaN
                     v[i] = token >= 0 ? v[i] * a.scale : token == -1 ? 0.0f : __int_as_float(0x7fffffff);
@@ -129,20 +129,21 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const EmbeddingAr
     const bool in = static_cast<int>(blockIdx.y) * 32 + lane < windows;
     // each warp sums a contiguous part of the list
     const int from = n * warp / kFewWarps, to = n * (warp + 1) / kFewWarps;
+    const Bounds bounds = bounds_of<T>(a.dout, a.rows, a.width);
     float sum[V] = {};
     for (int k = from; k < to; k += U) {
-        uint4 raw[U];
+        RawWindow<VEC> raw[U];
+        const T *row[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (in && k + u < to)
-                raw[u] = load_window<T, VEC>(
-                    static_cast<const T *>(a.dout) + static_cast<long long>(list[k + u]) * a.width, at, a.width);
+            row[u] = static_cast<const T *>(a.dout) + static_cast<long long>(list[min(k + u, to - 1)]) * a.width;
+            raw[u] = fetch_window<T, VEC>(row[u], at, bounds, in && k + u < to);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            if (!in || k + u >= to) continue;
             float v[V];
-            widen_vec<T>(raw[u], v);
+            widen_vec<T>(join_window<T, VEC>(raw[u], row[u], at, a.width, bounds, true), v);
 #pragma unroll
             for (int e = 0; e < V; ++e) sum[e] += v[e];
         }
@@ -192,16 +193,31 @@ __device__ __forceinline__ unsigned int key_at(const EmbeddingArgs &a, int i) {
     return row < 0 ? static_cast<unsigned int>(a.vocab) : static_cast<unsigned int>(row);
 }
 
-// Counts of the first digit in each tile; the later passes' counts to zero.
+// Counts of the first digit in each tile; the later passes' counts to zero;
+// and, in `present`, a bit for each token that occurs (NULL: not wanted).
+template <int ITEMS>
 __global__ void __launch_bounds__(kSortThreads)
-    digits_kernel(const EmbeddingArgs a, int *counts, int bits, int passes, int tile) {
+    digits_kernel(const EmbeddingArgs a, int *counts, unsigned int *present, int bits, int passes) {
+    constexpr int U = 8;
     __shared__ int bins[kMaxBins];
     const int n = 1 << bits, tiles = gridDim.x;
     for (int d = threadIdx.x; d < n; d += kSortThreads) bins[d] = 0;
     __syncthreads();
-    const int begin = blockIdx.x * tile, end = min(begin + tile, a.rows);
-    for (int i = begin + threadIdx.x; i < end; i += kSortThreads)
-        atomicAdd(&bins[key_at(a, i) & (n - 1)], 1);
+    const unsigned int none = a.vocab;
+    for (int r = 0; r < ITEMS; r += U) {
+        unsigned int key[U], word[U];
+        const int begin = (blockIdx.x * ITEMS + r) * kSortThreads + threadIdx.x;
+#pragma unroll
+        for (int u = 0; u < U; ++u) key[u] = begin + u * kSortThreads < a.rows ? key_at(a, begin + u * kSortThreads) : ~0u;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (key[u] != ~0u) atomicAdd(&bins[key[u] & (n - 1)], 1);
+            word[u] = present != nullptr && key[u] < none ? __ldcg(present + (key[u] >> 5)) : ~0u;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)   // a token that occurs often is mostly noted already
+            if ((word[u] >> (key[u] & 31) & 1) == 0) atomicOr(present + (key[u] >> 5), 1u << (key[u] & 31));
+    }
     __syncthreads();
     for (int d = threadIdx.x; d < n; d += kSortThreads) {
         const long long at = static_cast<long long>(blockIdx.x) * n + d;
@@ -210,18 +226,47 @@ __global__ void __launch_bounds__(kSortThreads)
     }
 }
 
+// Zeros to the rows of dweight whose token does not occur: `each` rows from
+// from + part * each on, below `to`, with `lanes` threads a row.
+struct Fill {
+    const unsigned int *present;
+    int from, to, each, lanes;
+};
+template <class D, bool VEC>
+__device__ __forceinline__ void fill_rows(const EmbeddingArgs &a, const Fill &f, int part) {
+    constexpr int N = 16 / sizeof(D);
+    const int lane = threadIdx.x & (f.lanes - 1), per = kSortThreads / f.lanes;
+    const int windows = windows_of<D>(a.width, VEC);
+    const float zero[N] = {};
+    const long long first = f.from + static_cast<long long>(part) * f.each;
+    const long long end = min(first + f.each, static_cast<long long>(f.to));
+    for (long long v = first + threadIdx.x / f.lanes; v < end; v += per) {
+        if (__ldg(f.present + (v >> 5)) >> (v & 31) & 1) continue;
+        D *row = static_cast<D *>(a.dweight) + v * a.width;
+        const int phase = VEC ? 0 : window_phase(row);
+        for (int j = lane; j < windows; j += f.lanes)
+            store_window<D, N, VEC>(row, j * N - phase, a.width, zero);
+    }
+}
+
 // One stable pass: a pair goes behind those of smaller digits, and behind those
 // of its digit in earlier tiles, warps and places.  Integer atomics count the
 // next digit by the tile that a pair lands in; their order changes nothing.
-template <int ITEMS, bool FIRST>
+// The CTAs behind the tiles fill rows of the gradient meanwhile, which the sort
+// leaves DRAM free for.
+template <class D, bool VEC, int ITEMS, bool FIRST>
 __global__ void __launch_bounds__(kSortThreads)
     scatter_kernel(const EmbeddingArgs a, const Pair *in, Pair *out, const int *counts, int *next,
-                   int bits, int shift, bool last) {
+                   int bits, int shift, bool last, int tiles, const Fill fill) {
+    if (static_cast<int>(blockIdx.x) >= tiles) {
+        fill_rows<D, VEC>(a, fill, blockIdx.x - tiles);
+        return;
+    }
     __shared__ int warp_bins[kSortWarps][kMaxBins];
     __shared__ int base[kMaxBins];
     __shared__ int sums[kSortWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n = 1 << bits, tiles = gridDim.x;
+    const int n = 1 << bits;
     for (int d = tid; d < kSortWarps * kMaxBins; d += kSortThreads) (&warp_bins[0][0])[d] = 0;
     // digits 2 tid and 2 tid + 1: pairs before this tile, and in all
     int before[2] = {}, total[2] = {};
@@ -305,10 +350,13 @@ constexpr int kSumThreads = 128;
 struct SumPlan {
     int run, runs;   // positions of a run, and how many there are
 };
-// 64 positions a run; more than 1024 runs would make the partial sums large.
-SumPlan sum_plan(int rows) {
+// 64 positions a run, fewer where that leaves SMs without a CTA (of 16-byte
+// windows of 2-byte rows); more than 1024 runs would make the partial sums large.
+SumPlan sum_plan(int rows, int width) {
+    const long long slices = (width / 8 + kSumThreads - 1) / kSumThreads + 1;
     SumPlan p;
     p.run = 64;
+    while (p.run > 16 && rows / p.run * slices < 152 * 8 && rows / p.run < 512) p.run /= 2;
     while ((rows + p.run - 1) / p.run > 1024) p.run *= 2;
     p.runs = (rows + p.run - 1) / p.run;
     return p;
@@ -317,8 +365,8 @@ SumPlan sum_plan(int rows) {
 // FP32 partial sums [runs][2][windows][V] of tokens that lie in several runs: of
 // a run's first token where it began in an earlier run, and of its last where
 // it began here and goes on.
-template <int V>
-__device__ __forceinline__ float *partial_at(float *partial, int run, int slot, int windows, int j) {
+template <int V, class F>
+__device__ __forceinline__ F *partial_at(F *partial, int run, int slot, int windows, int j) {
     return partial + ((static_cast<long long>(run) * 2 + slot) * windows + j) * V;
 }
 template <int V>
@@ -342,7 +390,7 @@ __device__ __forceinline__ void finish_row(const EmbeddingArgs &a, D *dst, int a
 template <class T, class D, bool VEC>
 __global__ void __launch_bounds__(kSumThreads)
     sum_kernel(const EmbeddingArgs a, const Pair *pairs, float *partial, int run, int runs, int lanes) {
-    constexpr int V = 16 / sizeof(T), U = 8;
+    constexpr int V = 16 / sizeof(T), U = VEC ? 8 : 4;
     const int lane = threadIdx.x & (lanes - 1);
     const int r = blockIdx.x * (kSumThreads / lanes) + threadIdx.x / lanes;
     const int windows = windows_of<T>(a.width, VEC);
@@ -354,26 +402,25 @@ __global__ void __launch_bounds__(kSumThreads)
     if (cur == none) return;
     bool here = begin == 0 || __ldg(&pairs[begin - 1].key) != cur;
     const T *dout = static_cast<const T *>(a.dout);
+    const Bounds bounds = bounds_of<T>(dout, a.rows, a.width);
+    auto window_at = [&](unsigned int key) {   // (any place for no token)
+        return VEC ? j * V : j * V - window_phase(static_cast<const D *>(a.dweight) + static_cast<long long>(key) * a.width);
+    };
     D *dst = static_cast<D *>(a.dweight) + static_cast<long long>(cur) * a.width;
-    int at = j * V - (VEC ? 0 : window_phase(dst));
+    int at = window_at(cur);
     float sum[V] = {};
     for (int k = begin; k < end; k += U) {
         Pair p[U];
-        uint4 raw[U];
+        RawWindow<VEC> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             p[u] = Pair{none, 0};
             if (k + u < end) p[u] = pairs[k + u];
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (p[u].key != none) {
-                const int from = VEC ? j * V : j * V - window_phase(static_cast<const D *>(a.dweight) +
-                                                                    static_cast<long long>(p[u].key) * a.width);
-                raw[u] = load_window<T, VEC>(dout + static_cast<long long>(p[u].at) * a.width, from, a.width);
-            }
-        }
+        for (int u = 0; u < U; ++u)
+            raw[u] = fetch_window<T, VEC>(dout + static_cast<long long>(p[u].at) * a.width, window_at(p[u].key),
+                                          bounds, p[u].key != none);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (p[u].key == none) continue;
@@ -385,12 +432,13 @@ __global__ void __launch_bounds__(kSumThreads)
                 cur = p[u].key;
                 here = true;
                 dst = static_cast<D *>(a.dweight) + static_cast<long long>(cur) * a.width;
-                at = j * V - (VEC ? 0 : window_phase(dst));
+                at = window_at(cur);
 #pragma unroll
                 for (int e = 0; e < V; ++e) sum[e] = 0.0f;
             }
             float v[V];
-            widen_vec<T>(raw[u], v);
+            widen_vec<T>(join_window<T, VEC>(raw[u], dout + static_cast<long long>(p[u].at) * a.width, at, a.width,
+                                             bounds, true), v);
 #pragma unroll
             for (int e = 0; e < V; ++e) sum[e] += v[e];
         }
@@ -402,45 +450,77 @@ __global__ void __launch_bounds__(kSumThreads)
         store_partial<V>(partial_at<V>(partial, r, here ? 1 : 0, windows, j), sum);
 }
 
-// The token that begins in a run and goes on behind it: its partial sums.
+// The token that begins in a run and goes on behind it: its partial sums, in
+// kJoinParts contiguous parts that are then added up (one part: a token of a
+// twelfth of 32768 rows took 20 us).
+constexpr int kJoinParts = 4;
 template <class T, class D, bool VEC>
-__global__ void __launch_bounds__(kSumThreads)
-    join_kernel(const EmbeddingArgs a, const Pair *pairs, float *partial, int run, int runs, int lanes) {
+__global__ void __launch_bounds__(kSumThreads * kJoinParts)
+    join_kernel(const EmbeddingArgs a, const Pair *pairs, const float *partial, int run, int runs, int lanes) {
     constexpr int V = 16 / sizeof(T);
-    const int lane = threadIdx.x & (lanes - 1);
-    const int r = blockIdx.x * (kSumThreads / lanes) + threadIdx.x / lanes;
+    __shared__ float4 parts[kJoinParts - 1][V / 4][kSumThreads];
+    const int part = threadIdx.x / kSumThreads, thread = threadIdx.x % kSumThreads;
+    const int lane = thread & (lanes - 1);
+    const int r = blockIdx.x * (kSumThreads / lanes) + thread / lanes;
     const int windows = windows_of<T>(a.width, VEC);
     const int j = blockIdx.y * lanes + lane;
-    if (r >= runs - 1 || j >= windows) return;
-    const int begin = r * run, end = begin + run;   // not the last run: whole
-    const unsigned int cur = __ldg(&pairs[end - 1].key);
-    if (cur == static_cast<unsigned int>(a.vocab) || __ldg(&pairs[end].key) != cur) return;
-    if (__ldg(&pairs[begin].key) == cur && begin > 0 && __ldg(&pairs[begin - 1].key) == cur) return;
-    int low = end, high = a.rows;   // the first place from `end` on with another token
-    while (low < high) {
-        const int mid = low + (high - low) / 2;
-        if (__ldg(&pairs[mid].key) == cur)
-            low = mid + 1;
-        else
-            high = mid;
+    unsigned int cur = a.vocab;
+    const int begin = r * run, end = begin + run;
+    if (r < runs - 1 && j < windows) {   // not the last run: whole
+        cur = __ldg(&pairs[end - 1].key);
+        const unsigned int next = __ldg(&pairs[end].key), first = __ldg(&pairs[begin].key);
+        const unsigned int prior = begin > 0 ? __ldg(&pairs[begin - 1].key) : a.vocab;
+        if (next != cur || (first == cur && prior == cur)) cur = a.vocab;
     }
-    const int last = (low - 1) / run;
-    float sum[V];
-    const float *own = partial_at<V>(partial, r, 1, windows, j);
+    const bool live = cur != static_cast<unsigned int>(a.vocab);
+    if (!__syncthreads_or(live)) return;
+    float sum[V] = {};
+    if (live) {
+        int low = end, high = a.rows;   // the first place from `end` on with another token
+        while (low < high) {
+            const int mid = low + (high - low) / 2;
+            if (__ldg(&pairs[mid].key) == cur)
+                low = mid + 1;
+            else
+                high = mid;
+        }
+        const int pieces = (low - 1) / run - r;   // besides the one that begins here
+        const int from = r + 1 + static_cast<int>(static_cast<long long>(pieces) * part / kJoinParts);
+        const int to = r + 1 + static_cast<int>(static_cast<long long>(pieces) * (part + 1) / kJoinParts);
+        if (part == 0) {
+            const float *own = partial_at<V>(partial, r, 1, windows, j);
 #pragma unroll
-    for (int e = 0; e < V; ++e) sum[e] = own[e];
+            for (int e = 0; e < V; ++e) sum[e] = own[e];
+        }
 #pragma unroll 4
-    for (int q = r + 1; q <= last; ++q) {
-        const float *p = partial_at<V>(partial, q, 0, windows, j);
+        for (int q = from; q < to; ++q) {
+            const float *p = partial_at<V>(partial, q, 0, windows, j);
+#pragma unroll
+            for (int e = 0; e < V; e += 4) {
+                const float4 t = *reinterpret_cast<const float4 *>(p + e);
+                sum[e] += t.x;
+                sum[e + 1] += t.y;
+                sum[e + 2] += t.z;
+                sum[e + 3] += t.w;
+            }
+        }
+        if (part > 0)
+#pragma unroll
+            for (int e = 0; e < V; e += 4)
+                parts[part - 1][e / 4][thread] = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+    }
+    __syncthreads();
+    if (part != 0 || !live) return;
+#pragma unroll
+    for (int q = 0; q < kJoinParts - 1; ++q)
 #pragma unroll
         for (int e = 0; e < V; e += 4) {
-            const float4 t = *reinterpret_cast<const float4 *>(p + e);
+            const float4 t = parts[q][e / 4][thread];
             sum[e] += t.x;
             sum[e + 1] += t.y;
             sum[e + 2] += t.z;
             sum[e + 3] += t.w;
         }
-    }
     D *dst = static_cast<D *>(a.dweight) + static_cast<long long>(cur) * a.width;
     finish_row<T, D, VEC>(a, dst, j * V - (VEC ? 0 : window_phase(dst)), sum);
 }
@@ -449,59 +529,81 @@ __global__ void __launch_bounds__(kSumThreads)
 
 // Workspace: two lists of pairs, the digit counts, the partial sums.
 struct Layout {
-    size_t list, counts, partial, bytes;
+    size_t list, counts, present, partial, bytes;
 };
 Layout layout(int rows, int width, int vocab) {
     const SortPlan s = sort_plan(rows, vocab);
-    const SumPlan m = sum_plan(rows);
+    const SumPlan m = sum_plan(rows, width);
     auto round = [](size_t n) { return (n + 255) / 256 * 256; };
     Layout l;
     l.list = round(static_cast<size_t>(rows) * sizeof(Pair));
     l.counts = 2 * l.list;
-    l.partial = l.counts + round(static_cast<size_t>(s.passes) * s.tiles * (1u << s.bits) * sizeof(int));
+    l.present = l.counts + round(static_cast<size_t>(s.passes) * s.tiles * (1u << s.bits) * sizeof(int));
+    l.partial = l.present + round((static_cast<size_t>(vocab) + 31) / 32 * sizeof(int));
     // the most windows are those of an FP32 row of any alignment
     l.bytes = l.partial + round(static_cast<size_t>(m.runs) * 2 * (static_cast<size_t>(width) + 16) * sizeof(float));
     return l;
 }
 
+template <class D, bool VEC, int ITEMS>
+void launch_pass(const EmbeddingArgs &a, const SortPlan &s, int pass, const Pair *in, Pair *out, int *counts,
+                 const Fill &fill, cudaStream_t stream) {
+    const size_t table = static_cast<size_t>(s.tiles) << s.bits;
+    int *c = counts + pass * table;
+    const bool last = pass == s.passes - 1;
+    const unsigned int grid = s.tiles + (fill.to - fill.from + fill.each - 1) / fill.each;
+    if (pass == 0)
+        scatter_kernel<D, VEC, ITEMS, true><<<grid, kSortThreads, 0, stream>>>(
+            a, in, out, c, c + table, s.bits, 0, last, s.tiles, fill);
+    else
+        scatter_kernel<D, VEC, ITEMS, false><<<grid, kSortThreads, 0, stream>>>(
+            a, in, out, c, c + table, s.bits, pass * s.bits, last, s.tiles, fill);
+}
+
 template <class T, class D, bool VEC>
 cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 16 / sizeof(T), N = 16 / sizeof(D);
     const int windows = VEC ? a.width / V : (a.width + V - 1) / V + 1;
-    if (!a.add) {
-        const cudaError_t err = cudaMemsetAsync(
-            a.dweight, 0, static_cast<size_t>(a.vocab) * a.width * sizeof(D), stream);
-        if (err != cudaSuccess) return err;
-    }
     if (a.rows <= kFewRows) {
+        if (!a.add) {
+            const cudaError_t err = cudaMemsetAsync(
+                a.dweight, 0, static_cast<size_t>(a.vocab) * a.width * sizeof(D), stream);
+            if (err != cudaSuccess) return err;
+        }
         few_rows_kernel<T, D, VEC><<<dim3(a.rows, (windows + 31) / 32), kFewThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
     const SortPlan s = sort_plan(a.rows, a.vocab);
-    const SumPlan m = sum_plan(a.rows);
+    const SumPlan m = sum_plan(a.rows, a.width);
     const Layout l = layout(a.rows, a.width, a.vocab);
     char *ws = static_cast<char *>(a.ws);
     Pair *list[2] = {reinterpret_cast<Pair *>(ws), reinterpret_cast<Pair *>(ws + l.list)};
     int *counts = reinterpret_cast<int *>(ws + l.counts);
+    unsigned int *present = a.add ? nullptr : reinterpret_cast<unsigned int *>(ws + l.present);
     float *partial = reinterpret_cast<float *>(ws + l.partial);
-    const size_t table = static_cast<size_t>(s.tiles) << s.bits;
-    digits_kernel<<<s.tiles, kSortThreads, 0, stream>>>(a, counts, s.bits, s.passes, kSortThreads * s.items);
+    if (present != nullptr) {
+        const cudaError_t err = cudaMemsetAsync(present, 0, (static_cast<size_t>(a.vocab) + 31) / 32 * sizeof(int), stream);
+        if (err != cudaSuccess) return err;
+    }
+    if (s.items == 8)
+        digits_kernel<8><<<s.tiles, kSortThreads, 0, stream>>>(a, counts, present, s.bits, s.passes);
+    else
+        digits_kernel<32><<<s.tiles, kSortThreads, 0, stream>>>(a, counts, present, s.bits, s.passes);
+    // CTAs of about 32 KB each, in the order of the rows: few that went through
+    // all rows filled 1 GiB at 6.5 TB/s, these at 7.5
+    Fill fill = {present, 0, 0, 1, 8};
+    const int fill_windows = VEC ? a.width / N : (a.width + N - 1) / N + 1;
+    while (fill.lanes < kSortThreads && fill.lanes < fill_windows) fill.lanes *= 2;
+    fill.each = 32768 / (fill_windows * 16) + kSortThreads / fill.lanes;
     for (int p = 0; p < s.passes; ++p) {
-        const bool last = p == s.passes - 1;
-        int *c = counts + p * table;
-        const Pair *in = list[(p + 1) & 1];
-        Pair *out = list[p & 1];
-        if (s.items == 8) {
-            if (p == 0)
-                scatter_kernel<8, true><<<s.tiles, kSortThreads, 0, stream>>>(a, in, out, c, c + table, s.bits, 0, last);
-            else
-                scatter_kernel<8, false><<<s.tiles, kSortThreads, 0, stream>>>(a, in, out, c, c + table, s.bits, p * s.bits, last);
-        } else {
-            if (p == 0)
-                scatter_kernel<32, true><<<s.tiles, kSortThreads, 0, stream>>>(a, in, out, c, c + table, s.bits, 0, last);
-            else
-                scatter_kernel<32, false><<<s.tiles, kSortThreads, 0, stream>>>(a, in, out, c, c + table, s.bits, p * s.bits, last);
+        if (present != nullptr) {   // each pass a share of the rows
+            fill.from = fill.to;
+            fill.to = static_cast<int>(static_cast<long long>(a.vocab) * (p + 1) / s.passes);
         }
+        if (s.items == 8)
+            launch_pass<D, VEC, 8>(a, s, p, list[(p + 1) & 1], list[p & 1], counts, fill, stream);
+        else
+            launch_pass<D, VEC, 32>(a, s, p, list[(p + 1) & 1], list[p & 1], counts, fill, stream);
     }
     const Pair *sorted = list[(s.passes - 1) & 1];
     int lanes = 8;
@@ -510,7 +612,7 @@ cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
     const dim3 grid((m.runs + per - 1) / per, (windows + lanes - 1) / lanes);
     sum_kernel<T, D, VEC><<<grid, kSumThreads, 0, stream>>>(a, sorted, partial, m.run, m.runs, lanes);
     if (m.runs > 1)
-        join_kernel<T, D, VEC><<<grid, kSumThreads, 0, stream>>>(a, sorted, partial, m.run, m.runs, lanes);
+        join_kernel<T, D, VEC><<<grid, kSumThreads * kJoinParts, 0, stream>>>(a, sorted, partial, m.run, m.runs, lanes);
     return cudaGetLastError();
 }
 

@@ -197,8 +197,14 @@ __device__ __forceinline__ float moment1(const Scalars &s, float m, float g) {
 __device__ __forceinline__ float moment2(const Scalars &s, float v, float g) {
     return __fadd_rn(__fmul_rn(v, s.beta2), __fmul_rn(__fmul_rn(g, g), s.rest2));
 }
+// 1 / x to 1 ulp, x between 2^-126 (eps) and 2^65
+__device__ __forceinline__ float reciprocal(float x) {
+    float d;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+    return d;
+}
 __device__ __forceinline__ float updated(const Scalars &s, float p, float keep, float m, float root_v) {
-    return fmaf(p, keep, -s.rate * __fdividef(m, fmaf(root_v, s.root, s.eps)));
+    return fmaf(m * reciprocal(fmaf(root_v, s.root, s.eps)), -s.rate, p * keep);
 }
 
 // Four gradients from element `at` on.
@@ -242,11 +248,11 @@ __device__ __forceinline__ void store_copy(void *p, int elem, long long at, floa
         store_one(static_cast<__half *>(p) + at, v);
 }
 
-constexpr int kAdamwThreads = 256, kAdamwGroups = 4, kAdamwChunk = kAdamwThreads * kAdamwGroups * 4;
+constexpr int kAdamwThreads = 256, kAdamwGroup = kAdamwThreads * 4;
 
 template <int N>
 __global__ void __launch_bounds__(kAdamwThreads)
-    adamw_kernel(const __grid_constant__ Table<AdamwEntry, N> t, Scalars s) {
+    adamw_kernel(const __grid_constant__ Table<AdamwEntry, N> t, Scalars s, int groups) {
     constexpr int U = 2;
     const int i = tensor_of(t, blockIdx.x);
     const AdamwEntry &e = t.entry[i];
@@ -254,47 +260,52 @@ __global__ void __launch_bounds__(kAdamwThreads)
     if (!isfinite(f)) return;   // a step that is skipped
     load_scalars(s);
     const float keep = fmaf(-s.lr, e.decay, 1.0f);
-    const long long base = static_cast<long long>(blockIdx.x - t.first[i]) * kAdamwChunk;
+    const int chunk = groups * kAdamwGroup;   // groups: 1 or even
+    const long long base = static_cast<long long>(blockIdx.x - t.first[i]) * chunk;
     float *param = e.param, *m = static_cast<float *>(e.m), *v = static_cast<float *>(e.v);
-    if (e.vectors && base + kAdamwChunk <= e.n) {
+    auto vectors = [&](auto width, int k) {
+        constexpr int W = decltype(width)::value;
+        float4 pv[W], mv[W], vv[W];
+        uint4 gv[W];
+        long long at[W];
+#pragma unroll
+        for (int u = 0; u < W; ++u) {
+            at[u] = base + ((k + u) * kAdamwThreads + threadIdx.x) * 4;
+            gv[u] = load_grads(e.grad, e.grad_elem, at[u]);
+            mv[u] = __ldcs(reinterpret_cast<const float4 *>(m + at[u]));
+            vv[u] = __ldcs(reinterpret_cast<const float4 *>(v + at[u]));
+            pv[u] = __ldcs(reinterpret_cast<const float4 *>(param + at[u]));
+        }
+#pragma unroll
+        for (int u = 0; u < W; ++u) {
+            float g[4], a[4] = {mv[u].x, mv[u].y, mv[u].z, mv[u].w}, b[4] = {vv[u].x, vv[u].y, vv[u].z, vv[u].w},
+                        p[4] = {pv[u].x, pv[u].y, pv[u].z, pv[u].w};
+            widen_grads(gv[u], e.grad_elem, g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                g[j] = __fmul_rn(g[j], f);
+                a[j] = moment1(s, a[j], g[j]);
+                b[j] = moment2(s, b[j], g[j]);
+                p[j] = updated(s, p[j], keep, a[j], __fsqrt_rn(b[j]));
+            }
+            __stcs(reinterpret_cast<float4 *>(m + at[u]), make_float4(a[0], a[1], a[2], a[3]));
+            __stcs(reinterpret_cast<float4 *>(v + at[u]), make_float4(b[0], b[1], b[2], b[3]));
+            __stcs(reinterpret_cast<float4 *>(param + at[u]), make_float4(p[0], p[1], p[2], p[3]));
+            if (e.copy_elem >= 0)
+                __stcs(reinterpret_cast<uint2 *>(static_cast<unsigned short *>(e.copy) + at[u]),
+                       make_uint2(narrow_pair(e.copy_elem, p[0], p[1]), narrow_pair(e.copy_elem, p[2], p[3])));
+        }
+    };
+    if (e.vectors && base + chunk <= e.n) {
+        if (groups == 1) {
+            vectors(std::integral_constant<int, 1>(), 0);
+        } else {
 #pragma unroll 1
-        for (int k = 0; k < kAdamwGroups; k += U) {
-            float4 pv[U], mv[U], vv[U];
-            uint4 gv[U];
-            long long at[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                at[u] = base + ((k + u) * kAdamwThreads + threadIdx.x) * 4;
-                gv[u] = load_grads(e.grad, e.grad_elem, at[u]);
-                mv[u] = __ldcs(reinterpret_cast<const float4 *>(m + at[u]));
-                vv[u] = __ldcs(reinterpret_cast<const float4 *>(v + at[u]));
-                pv[u] = __ldcs(reinterpret_cast<const float4 *>(param + at[u]));
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float g[4], a[4] = {mv[u].x, mv[u].y, mv[u].z, mv[u].w},
-                            b[4] = {vv[u].x, vv[u].y, vv[u].z, vv[u].w},
-                            p[4] = {pv[u].x, pv[u].y, pv[u].z, pv[u].w};
-                widen_grads(gv[u], e.grad_elem, g);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    g[j] = __fmul_rn(g[j], f);
-                    a[j] = moment1(s, a[j], g[j]);
-                    b[j] = moment2(s, b[j], g[j]);
-                    p[j] = updated(s, p[j], keep, a[j], __fsqrt_rn(b[j]));
-                }
-                __stcs(reinterpret_cast<float4 *>(m + at[u]), make_float4(a[0], a[1], a[2], a[3]));
-                __stcs(reinterpret_cast<float4 *>(v + at[u]), make_float4(b[0], b[1], b[2], b[3]));
-                __stcs(reinterpret_cast<float4 *>(param + at[u]), make_float4(p[0], p[1], p[2], p[3]));
-                if (e.copy_elem >= 0)
-                    __stcs(reinterpret_cast<uint2 *>(static_cast<unsigned short *>(e.copy) + at[u]),
-                           make_uint2(narrow_pair(e.copy_elem, p[0], p[1]),
-                                      narrow_pair(e.copy_elem, p[2], p[3])));
-            }
+            for (int k = 0; k < groups; k += U) vectors(std::integral_constant<int, U>(), k);
         }
         return;
     }
-    for (int k = 0; k < kAdamwGroups; ++k) {
+    for (int k = 0; k < groups && base + k * kAdamwGroup < e.n; ++k) {
         float g[4], a[4], b[4], p[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -333,10 +344,8 @@ __host__ __device__ __forceinline__ unsigned long long mix64(unsigned long long 
 }
 constexpr unsigned long long kGolden = 0x9E3779B97F4A7C15ull;
 
-// 32 random bits for element `at`; the two elements of a pair share a word of 64.
-__device__ __forceinline__ unsigned long long pair_bits(unsigned long long key, long long pair) {
-    return mix64(key + static_cast<unsigned long long>(pair + 1) * kGolden);
-}
+// (32 random bits for each element: the two elements of a pair share a word of
+// 64, of mix64(key + (pair + 1) kGolden).)
 
 // The power of two that a block's values are divided by, its inverse: the
 // largest of them comes to 128 to 256.  Blocks under 2^-100 are held as they
@@ -367,12 +376,83 @@ __device__ __forceinline__ float2 widen_codes(unsigned int two) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
+// Sums of two packed products.  Scalar: the packed addition of packed products
+// came out as one rounding less (a fused multiply-add), against its ".rn".
+__device__ __forceinline__ void add_halves(F2 a, F2 b, float &lo, float &hi) {
+    float a0, a1, b0, b1;
+    unpack(a, a0, a1);
+    unpack(b, b0, b1);
+    lo = __fadd_rn(a0, b0);
+    hi = __fadd_rn(a1, b1);
+}
+// NaN where one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
 
-constexpr int kEightBlocks = 2, kEightChunk = kAdamwThreads / 32 * kStateBlock * kEightBlocks;
+constexpr int kEightWarps = kAdamwThreads / 32;
 
+// What a lane has of a block of 256, as it lies in memory: 8 elements, one
+// behind the other where the block is whole and on the grid, else each 32 on.
+struct EightRaw {
+    float4 p[2];
+    uint4 g[2];
+    unsigned int m[2], v[2];
+    float m_scale, v_scale;
+};
+
+__device__ __forceinline__ void load_eight(const AdamwEntry &e, long long block, int lane, bool whole, EightRaw &r) {
+    const long long base = block * kStateBlock, at = base + lane * 8;
+    const unsigned char *mc = static_cast<const unsigned char *>(e.m), *vc = static_cast<const unsigned char *>(e.v);
+    r.m_scale = __ldcs(e.m_scale + block);
+    r.v_scale = __ldcs(e.v_scale + block);
+    if (whole) {
+        if (e.grad_elem == ELEM_F32) {
+            r.g[0] = load_grads(e.grad, ELEM_F32, at);
+            r.g[1] = load_grads(e.grad, ELEM_F32, at + 4);
+        } else {
+            r.g[0] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(e.grad) + at));
+            r.g[1] = make_uint4(r.g[0].z, r.g[0].w, 0, 0);
+        }
+        const uint2 m = __ldcs(reinterpret_cast<const uint2 *>(mc + at));
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(vc + at));
+        r.m[0] = m.x;
+        r.m[1] = m.y;
+        r.v[0] = v.x;
+        r.v[1] = v.y;
+        r.p[0] = __ldcs(reinterpret_cast<const float4 *>(e.param + at));
+        r.p[1] = __ldcs(reinterpret_cast<const float4 *>(e.param + at) + 1);
+        return;
+    }
+    float p[8], g[8];
+    r.m[0] = r.m[1] = r.v[0] = r.v[1] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const long long w = base + j * 32 + lane;
+        p[j] = g[j] = 0.0f;
+        if (w < e.n) {
+            g[j] = load_grad(e.grad, e.grad_elem, w);
+            p[j] = __ldcs(e.param + w);
+            r.m[j / 4] |= static_cast<unsigned int>(mc[w]) << (8 * (j & 3));
+            r.v[j / 4] |= static_cast<unsigned int>(vc[w]) << (8 * (j & 3));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        r.p[j] = make_float4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
+        r.g[j] = make_uint4(__float_as_uint(g[4 * j]), __float_as_uint(g[4 * j + 1]),
+                            __float_as_uint(g[4 * j + 2]), __float_as_uint(g[4 * j + 3]));
+    }
+}
+
+// A warp for each block of 256, `blocks` of them one after the other with the
+// next one's loads on their way (64 registers without, and half the warps
+// waiting: 735 us for 1.9e8 parameters).
 template <int N>
-__global__ void __launch_bounds__(kAdamwThreads)
-    adamw8_kernel(const __grid_constant__ Table<AdamwEntry, N> t, Scalars s) {
+__global__ void __launch_bounds__(kAdamwThreads, 3)
+    adamw8_kernel(const __grid_constant__ Table<AdamwEntry, N> t, Scalars s, int blocks) {
     const int i = tensor_of(t, blockIdx.x);
     const AdamwEntry &e = t.entry[i];
     const float f = s.factor != nullptr ? __ldg(s.factor) : 1.0f;
@@ -383,43 +463,32 @@ __global__ void __launch_bounds__(kAdamwThreads)
         mix64(mix64(s.seed + static_cast<unsigned long long>(s.step) * kGolden) +
               static_cast<unsigned long long>(e.index + 1) * kGolden);
     const int lane = threadIdx.x & 31;
-    const bool vectors = e.vectors != 0;
     unsigned char *mc = static_cast<unsigned char *>(e.m), *vc = static_cast<unsigned char *>(e.v);
-    for (int k = 0; k < kEightBlocks; ++k) {
-        // a warp for each block of 256; a lane has 8 elements, one behind the
-        // other where they are vectors, else each 32 on
-        const long long block = static_cast<long long>(blockIdx.x - t.first[i]) * (kEightChunk / kStateBlock) +
-                                k * (kAdamwThreads / 32) + (threadIdx.x >> 5);
-        const long long base = block * kStateBlock;
+    const long long first = static_cast<long long>(blockIdx.x - t.first[i]) * blocks * kEightWarps + (threadIdx.x >> 5);
+    auto is_whole = [&](long long block) { return e.vectors != 0 && (block + 1) * kStateBlock <= e.n; };
+    EightRaw next;
+    if (first * kStateBlock < e.n) load_eight(e, first, lane, is_whole(first), next);
+    for (int k = 0; k < blocks; ++k) {
+        const long long block = first + k * kEightWarps, base = block * kStateBlock, at = base + lane * 8;
         if (base >= e.n) return;
-        const bool whole = vectors && base + kStateBlock <= e.n;
-        const long long at = base + lane * 8;
+        const bool whole = is_whole(block);
+        const EightRaw r = next;
+        const long long following = block + kEightWarps;
+        if (k + 1 < blocks && following * kStateBlock < e.n)
+            load_eight(e, following, lane, is_whole(following), next);
         float g[8], m[8], v[8], p[8];
-        const float ms = __ldcs(e.m_scale + block), vs = __ldcs(e.v_scale + block);
-        if (whole) {
-            const float4 p0 = __ldcs(reinterpret_cast<const float4 *>(e.param + at));
-            const float4 p1 = __ldcs(reinterpret_cast<const float4 *>(e.param + at) + 1);
-            const uint2 mw = __ldcs(reinterpret_cast<const uint2 *>(mc + at));
-            const uint2 vw = __ldcs(reinterpret_cast<const uint2 *>(vc + at));
-            uint4 g0, g1;
-            if (e.grad_elem == ELEM_F32) {
-                g0 = load_grads(e.grad, ELEM_F32, at);
-                g1 = load_grads(e.grad, ELEM_F32, at + 4);
-            } else {
-                g0 = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(e.grad) + at));
-                g1 = make_uint4(g0.z, g0.w, 0, 0);
-            }
+        {
+            const int kind = whole ? e.grad_elem : ELEM_F32;
             float lo[4], hi[4];
-            widen_grads(g0, e.grad_elem, lo);
-            widen_grads(g1, e.grad_elem, hi);
-            const float pp[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+            widen_grads(r.g[0], kind, lo);
+            widen_grads(r.g[1], kind, hi);
+            const float pp[8] = {r.p[0].x, r.p[0].y, r.p[0].z, r.p[0].w, r.p[1].x, r.p[1].y, r.p[1].z, r.p[1].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 g[j] = lo[j];
                 g[j + 4] = hi[j];
-                const unsigned int mt = (j < 2 ? mw.x : mw.y) >> (16 * (j & 1));
-                const unsigned int vt = (j < 2 ? vw.x : vw.y) >> (16 * (j & 1));
-                const float2 a = widen_codes(mt & 0xffff), b = widen_codes(vt & 0xffff);
+                const float2 a = widen_codes(r.m[j / 2] >> (16 * (j & 1)) & 0xffff);
+                const float2 b = widen_codes(r.v[j / 2] >> (16 * (j & 1)) & 0xffff);
                 m[2 * j] = a.x;
                 m[2 * j + 1] = a.y;
                 v[2 * j] = b.x;
@@ -427,43 +496,54 @@ __global__ void __launch_bounds__(kAdamwThreads)
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) p[j] = pp[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const long long w = base + j * 32 + lane;
-                g[j] = m[j] = v[j] = p[j] = 0.0f;
-                if (w < e.n) {
-                    g[j] = load_grad(e.grad, e.grad_elem, w);
-                    m[j] = widen_codes(mc[w]).x;
-                    v[j] = widen_codes(vc[w]).x;
-                    p[j] = __ldcs(e.param + w);
-                }
-            }
         }
-        unsigned int mtop = 0, vtop = 0;
+        const float ms = r.m_scale, vs = r.v_scale;
+        // two elements at a time, each operation rounded as its scalar form
+        float mtop = 0.0f, vtop = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            g[j] = __fmul_rn(g[j], f);
-            m[j] = moment1(s, __fmul_rn(m[j], ms), g[j]);
-            const float root = __fmul_rn(v[j], vs);
-            v[j] = __fsqrt_rn(moment2(s, __fmul_rn(root, root), g[j]));
-            p[j] = updated(s, p[j], keep, m[j], v[j]);
-            mtop = max(mtop, __float_as_uint(m[j]) & 0x7fffffffu);
-            vtop = max(vtop, __float_as_uint(v[j]) & 0x7fffffffu);
+        for (int j = 0; j < 8; j += 2) {
+            const F2 g2 = mul2(pack(g[j], g[j + 1]), both(f));
+            const F2 root = mul2(pack(v[j], v[j + 1]), both(vs));
+            add_halves(mul2(mul2(pack(m[j], m[j + 1]), both(ms)), both(s.beta1)), mul2(g2, both(s.rest1)), m[j],
+                       m[j + 1]);
+            add_halves(mul2(mul2(root, root), both(s.beta2)), mul2(mul2(g2, g2), both(s.rest2)), v[j], v[j + 1]);
+            v[j] = __fsqrt_rn(v[j]);
+            v[j + 1] = __fsqrt_rn(v[j + 1]);
+            const F2 below = fma2(pack(v[j], v[j + 1]), both(s.root), both(s.eps));
+            float d0, d1, p0, p1;
+            unpack(below, d0, d1);
+            const F2 step = mul2(pack(m[j], m[j + 1]), pack(reciprocal(d0), reciprocal(d1)));
+            unpack(fma2(step, both(-s.rate), mul2(pack(p[j], p[j + 1]), both(keep))), p0, p1);
+            p[j] = p0;
+            p[j + 1] = p1;
+            mtop = max_nan(mtop, max_nan(fabsf(m[j]), fabsf(m[j + 1])));
+            vtop = max_nan(vtop, max_nan(v[j], v[j + 1]));
         }
-        const BlockScale mscale = block_scale(__reduce_max_sync(0xffffffffu, mtop));
-        const BlockScale vscale = block_scale(__reduce_max_sync(0xffffffffu, vtop));
+        const BlockScale mscale = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
+        const BlockScale vscale = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)));
         float mq[8], vq[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const long long w = whole ? at + j : base + j * 32 + lane;
-            const unsigned long long both = pair_bits(key, w >> 1);
-            const unsigned int bits = static_cast<unsigned int>((w & 1) != 0 ? both >> 32 : both);
+        auto quantise = [&](int j, unsigned int bits) {
             const float size = round_at_random(fabsf(__fmul_rn(m[j], mscale.inverse)), bits & 0xffff);
             mq[j] = copysignf(size, m[j]);
             const float r = __fmul_rn(v[j], vscale.inverse);
             const float q = round_at_random(r, bits >> 16);
             vq[j] = r > 0.0f ? fmaxf(q, 0.001953125f) : q;   // a root that is not zero stays so
+        };
+        if (whole) {   // the two elements of a pair are one lane's
+            const unsigned long long at_pair = key + static_cast<unsigned long long>((at >> 1) + 1) * kGolden;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const unsigned long long two = mix64(at_pair + static_cast<unsigned long long>(j) * kGolden);
+                quantise(2 * j, static_cast<unsigned int>(two));
+                quantise(2 * j + 1, static_cast<unsigned int>(two >> 32));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const long long w = base + j * 32 + lane;
+                const unsigned long long two = mix64(key + static_cast<unsigned long long>((w >> 1) + 1) * kGolden);
+                quantise(j, static_cast<unsigned int>((w & 1) != 0 ? two >> 32 : two));
+            }
         }
         if (lane == 0) {
             e.m_scale[block] = mscale.scale;
@@ -522,13 +602,24 @@ cudaError_t launch_norm_table(const NormTensor *t, int count, double *partial, i
     return cudaGetLastError();
 }
 
+// Elements of a chunk: as many as leave kWantedChunks of them, in 1, 2, 4 .. `most`
+// steps of the smallest (few elements: latency counts).
+constexpr long long kWantedChunks = 152 * 16;
+long long chunk_of(long long elements, long long smallest, int most, int *steps) {
+    *steps = 1;
+    while (*steps < most && elements / (smallest * *steps * 2) >= kWantedChunks) *steps *= 2;
+    return smallest * *steps;
+}
+
 template <int N>
 cudaError_t launch_adamw_table(const AdamwTensor *t, int count, int index, const AdamwConfig &c,
                                const Scalars &s, cudaStream_t stream) {
     Table<AdamwEntry, N> table;
-    int used = 0;
-    long long chunks = 0;
-    const long long chunk = c.eight ? kEightChunk : kAdamwChunk;
+    int used = 0, steps = 0;
+    long long chunks = 0, elements = 0;
+    for (int i = 0; i < count; ++i) elements += t[i].n;
+    const long long chunk = c.eight ? chunk_of(elements, kEightWarps * kStateBlock, 8, &steps)
+                                    : chunk_of(elements, kAdamwGroup, 4, &steps);
     for (int i = 0; i < count; ++i) {
         const AdamwTensor &a = t[i];
         if (a.n == 0) continue;
@@ -548,9 +639,9 @@ cudaError_t launch_adamw_table(const AdamwTensor *t, int count, int index, const
     table.first[used] = static_cast<int>(chunks);
     const unsigned int grid = static_cast<unsigned int>(chunks);
     if (c.eight)
-        adamw8_kernel<N><<<grid, kAdamwThreads, 0, stream>>>(table, s);
+        adamw8_kernel<N><<<grid, kAdamwThreads, 0, stream>>>(table, s, steps);
     else
-        adamw_kernel<N><<<grid, kAdamwThreads, 0, stream>>>(table, s);
+        adamw_kernel<N><<<grid, kAdamwThreads, 0, stream>>>(table, s, steps);
     return cudaGetLastError();
 }
 

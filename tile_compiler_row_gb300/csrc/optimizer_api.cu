@@ -1,5 +1,6 @@
 // C ABI of the gradients' norm and the AdamW step (include/tile_rows.h):
 // argument checks and dispatch.
+#include <float.h>
 #include <stdlib.h>
 
 #include <algorithm>
@@ -108,7 +109,7 @@ int tile_adamw(const tile_adamw_tensor_t *tensors, int count, const tile_adamw_c
     if (count < 0 || (c.step_device == nullptr && c.step < 1)) return TILE_ERR_SHAPE;
     if (count > 0 && tensors == nullptr) return TILE_ERR_NULL;
     if (!(c.beta1 >= 0.0 && c.beta1 < 1.0) || !(c.beta2 >= 0.0 && c.beta2 < 1.0) ||
-        !(std::isfinite(c.eps) && static_cast<float>(c.eps) > 0.0f) ||
+        !(std::isfinite(c.eps) && static_cast<float>(c.eps) >= FLT_MIN) ||
         (c.lr_device == nullptr && !std::isfinite(static_cast<float>(c.lr))))
         return TILE_ERR_EPS;
     if (misaligned_to(c.lr_device, 4) || misaligned_to(c.step_device, 8) || misaligned_to(c.factor, 4))

@@ -10,7 +10,7 @@
 // DRAM beyond.  Whether a ratio is clipped is decided by x against the bounds'
 // logarithms, as if x had not been rounded: r's own rounding would move
 // tokens over the border, where the gradient jumps.  Sums are FP32 over a tile
-// of 1024 rows, in a fixed order, and FP64 over tiles and sequences.
+// of 1024 rows, in a fixed order, and compensated FP32 over tiles and sequences.
 #include "device_status.h"
 #include "policy_loss.h"
 
@@ -34,24 +34,45 @@ __device__ __forceinline__ int sequence_of(const long long *offsets, long long r
     }
     return low;
 }
+// The same by a whole warp, which looks at 32 places at a time.
+__device__ __forceinline__ int sequence_of_warp(const long long *offsets, long long row, int low, int high) {
+    const int lane = threadIdx.x & 31;
+    while (low < high) {
+        const int step = (high - low + 31) / 32, at = low + (lane + 1) * step;
+        const bool before = at <= high && __ldg(offsets + at) <= row;
+        const unsigned int mask = __ballot_sync(0xffffffffu, before);
+        // places up to the first lane that is behind the row (offsets that fall: in range all the same)
+        const int n = mask == 0xffffffffu ? 32 : __ffs(~mask) - 1;
+        const int top = low + (n + 1) * step - 1;
+        low += n * step;
+        if (top < high) high = top;
+    }
+    return low;
+}
 
 // The tile's sequences; those of its rows lie in [low, high].
 struct Span {
     int low, high;
     long long first, last;   // rows that belong to a sequence
 };
-__device__ __forceinline__ void find_span(const PolicyArgs &a, long long tile0, Span *span) {
+// search: whether low and high are wanted (by all threads of the CTA; not
+// yet visible to them).
+__device__ __forceinline__ void find_span(const PolicyArgs &a, long long tile0, bool search, Span *span) {
     const long long tile1 = min(tile0 + kTile, static_cast<long long>(a.rows)) - 1;
+    const int warp = threadIdx.x >> 5;
     if (a.offsets == nullptr) {
         if (threadIdx.x == 0) *span = Span{0, 0, 0, a.rows};
-    } else if (threadIdx.x == 0) {
-        span->low = sequence_of(a.offsets, tile0, 0, a.sequences - 1);
-        span->first = __ldg(a.offsets);
-    } else if (threadIdx.x == 32) {
-        span->high = sequence_of(a.offsets, tile1, 0, a.sequences - 1);
-        span->last = __ldg(a.offsets + a.sequences);
+    } else if (warp < 2) {
+        const long long edge = __ldg(a.offsets + (warp == 0 ? 0 : a.sequences));
+        const int s = search ? sequence_of_warp(a.offsets, warp == 0 ? tile0 : tile1, 0, a.sequences - 1) : 0;
+        if (threadIdx.x == 0) {
+            span->low = s;
+            span->first = edge;
+        } else if (threadIdx.x == 32) {
+            span->high = s;
+            span->last = edge;
+        }
     }
-    __syncthreads();
 }
 
 // Whether old - nll > bound (sign 1) or < bound (sign -1), unrounded.
@@ -68,30 +89,33 @@ struct Token {
     bool counts;
 };
 
-// Rows tile0 + thread + 256 u of the tile.
-__device__ __forceinline__ void load_tokens(const PolicyArgs &a, long long tile0, const Span &span,
-                                            Token (&t)[kRows], int (&of)[kRows], bool need_of) {
+// Rows tile0 + thread + 256 u of the tile, with the loads on their way before
+// the sequences are known (8191 rows, backward: 7.1 us with one after the other).
+__device__ __forceinline__ void load_tokens(const PolicyArgs &a, long long tile0, Token (&t)[kRows]) {
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
         const long long row = tile0 + threadIdx.x + u * kThreads;
-        const bool in = row < a.rows && row >= span.first && row < span.last;
-        t[u] = Token{0.0f, 0.0f, 0.0f, 0.0f, in};
-        of[u] = span.low;
-        if (!in) continue;
-        if (a.target != nullptr) t[u].counts = __ldcs(a.target + row) != a.ignore;
+        t[u] = Token{0.0f, 0.0f, 0.0f, 0.0f, false};
+        if (row >= a.rows) continue;
+        t[u].counts = a.target == nullptr || __ldcs(a.target + row) != a.ignore;
         t[u].nll = __ldcs(a.nll + row);
         t[u].old = __ldcs(a.old_nll + row);
         if (a.ref_nll != nullptr) t[u].ref = __ldcs(a.ref_nll + row);
         if (!a.sequence_advantage) t[u].adv = __ldcs(a.advantage + row);
     }
-    if (!need_of && !a.sequence_advantage) return;
+}
+// Which of them count, and their sequences where those are wanted.
+__device__ __forceinline__ void place_tokens(const PolicyArgs &a, long long tile0, const Span &span,
+                                             Token (&t)[kRows], int (&of)[kRows], bool need_of) {
 #pragma unroll
-    for (int u = 0; u < kRows; ++u)
-        if (t[u].counts) {
-            if (a.offsets != nullptr)
-                of[u] = sequence_of(a.offsets, tile0 + threadIdx.x + u * kThreads, span.low, span.high);
-            if (a.sequence_advantage) t[u].adv = __ldg(a.advantage + of[u]);
-        }
+    for (int u = 0; u < kRows; ++u) {
+        const long long row = tile0 + threadIdx.x + u * kThreads;
+        t[u].counts &= row >= span.first && row < span.last;
+        of[u] = span.low;
+        if (!t[u].counts || !(need_of || a.sequence_advantage)) continue;
+        if (a.offsets != nullptr) of[u] = sequence_of(a.offsets, row, span.low, span.high);
+        if (a.sequence_advantage) t[u].adv = __ldg(a.advantage + of[u]);
+    }
 }
 
 __device__ __forceinline__ bool is_clipped(const PolicyArgs &a, const Token &t, float x) {
@@ -138,11 +162,13 @@ struct TileMem {
 __device__ __forceinline__ void tile_sums(const PolicyArgs &a, int tile, float4 *slots, TileMem &mem) {
     const long long tile0 = static_cast<long long>(tile) * kTile;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    find_span(a, tile0, &mem.span);
-    const Span span = mem.span;
     Token t[kRows];
     int of[kRows];
-    load_tokens(a, tile0, span, t, of, false);
+    load_tokens(a, tile0, t);
+    find_span(a, tile0, a.sequence_mean || a.sequence_advantage, &mem.span);
+    __syncthreads();
+    const Span span = mem.span;
+    place_tokens(a, tile0, span, t, of, false);
     if (!a.sequence_mean) {
         float4 v = parts_of(a, t[0]);
 #pragma unroll
@@ -179,40 +205,58 @@ __device__ __forceinline__ void tile_sums(const PolicyArgs &a, int tile, float4 
     }
 }
 
-// Block-wide sums of N doubles, for thread 0 (and in shared memory for all).
-template <int N, int THREADS>
-__device__ __forceinline__ void block_sum(double (&v)[N], double (*mem)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-        for (int i = 0; i < N; ++i) mem[threadIdx.x >> 5][i] = v[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        v[i] = 0.0;
-        for (int w = 0; w < THREADS / 32; ++w) v[i] += mem[w][i];
+// An FP32 sum with what its roundings cut off (Knuth's two-sum): FP64 sums of
+// the tiles took 40 of 64 us of 1048576 tokens.
+struct Sum {
+    float s, cut;
+    __device__ __forceinline__ void add(float x) {
+        const float to = __fadd_rn(s, x), back = __fsub_rn(to, s);
+        cut += __fadd_rn(__fsub_rn(s, __fsub_rn(to, back)), __fsub_rn(x, back));
+        s = to;
     }
-}
+    __device__ __forceinline__ void add(Sum o) {
+        add(o.s);
+        cut += o.cut;
+    }
+    __device__ __forceinline__ float value() const { return isfinite(s) ? s + cut : s; }
+};
+struct Sums {
+    Sum v[4];   // surrogate, KL, clipped, and tokens or sequences that count
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i].s = v[i].cut = 0.0f;
+    }
+    __device__ __forceinline__ void add(float4 p) {
+        v[0].add(p.x);
+        v[1].add(p.y);
+        v[2].add(p.z);
+        v[3].add(p.w);
+    }
+    // over the warp, for every lane
+    __device__ __forceinline__ void warp() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+                Sum o;
+                o.s = __shfl_xor_sync(0xffffffffu, v[i].s, d);
+                o.cut = __shfl_xor_sync(0xffffffffu, v[i].cut, d);
+                v[i].add(o);
+            }
+    }
+};
 
 // The slots' sums to stats and weights.
 template <int THREADS>
 __device__ __forceinline__ void join_sums(const PolicyArgs &a, const float4 *slots) {
-    __shared__ double mem[THREADS / 32][4];
-    const int tiles = (a.rows + kTile - 1) / kTile, tid = threadIdx.x;
-    double sum[4] = {};   // surrogate, KL, clipped, and tokens or sequences that count
+    __shared__ Sums part[THREADS / 32];
+    __shared__ float shared_share;
+    const int tiles = (a.rows + kTile - 1) / kTile, tid = threadIdx.x, lane = tid & 31;
+    Sums sum;
+    sum.zero();
     bool bad = false;
-    if (!a.sequence_mean) {
-        for (int t = tid; t < tiles; t += THREADS) {
-            const float4 v = __ldcg(slots + t);
-            sum[0] += v.x;
-            sum[1] += v.y;
-            sum[2] += v.z;
-            sum[3] += v.w;
-        }
-    }
+    if (!a.sequence_mean)
+        for (int t = tid; t < tiles; t += THREADS) sum.add(__ldcg(slots + t));
     for (int base = 0; base < a.sequences; base += THREADS) {
         const int s = base + tid;
         long long begin = 0, end = s < a.sequences ? a.rows : 0;
@@ -225,17 +269,13 @@ __device__ __forceinline__ void join_sums(const PolicyArgs &a, const float4 *slo
             }
         }
         if (!a.sequence_mean) continue;
-        double v[4] = {};
+        Sums v;
+        v.zero();
         const int first = static_cast<int>(begin / kTile);
         const int last = begin < end ? static_cast<int>((end - 1) / kTile) : first - 1;
         if (last - first < 32)
-            for (int t = first; t <= last; ++t) {
-                const float4 p = __ldcg(slots + static_cast<long long>(t) + s);
-                v[0] += p.x;
-                v[1] += p.y;
-                v[2] += p.z;
-                v[3] += p.w;
-            }
+#pragma unroll 4
+            for (int t = first; t <= last; ++t) v.add(__ldcg(slots + static_cast<long long>(t) + s));
         // long sequences: the warp together
         unsigned int left = __ballot_sync(0xffffffffu, last - first >= 32);
         while (left != 0) {
@@ -243,43 +283,43 @@ __device__ __forceinline__ void join_sums(const PolicyArgs &a, const float4 *slo
             left &= left - 1;
             const int f = __shfl_sync(0xffffffffu, first, from), l = __shfl_sync(0xffffffffu, last, from);
             const int of = __shfl_sync(0xffffffffu, s, from);
-            double w[4] = {};
-            for (int t = f + (tid & 31); t <= l; t += 32) {
-                const float4 p = __ldcg(slots + static_cast<long long>(t) + of);
-                w[0] += p.x;
-                w[1] += p.y;
-                w[2] += p.z;
-                w[3] += p.w;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) w[i] += __shfl_xor_sync(0xffffffffu, w[i], d);
-                if ((tid & 31) == from) v[i] = w[i];
-            }
+            Sums w;
+            w.zero();
+            for (int t = f + lane; t <= l; t += 32) w.add(__ldcg(slots + static_cast<long long>(t) + of));
+            w.warp();
+            if (lane == from) v = w;
         }
-        const bool counts = v[3] > 0.0;
-        if (s < a.sequences) a.weights[s] = counts ? static_cast<float>(1.0 / v[3]) : 0.0f;
-        if (counts) {
-            sum[0] += v[0] / v[3];
-            sum[1] += v[1] / v[3];
-            sum[2] += v[2] / v[3];
-            sum[3] += 1.0;
-        }
+        const float n = v.v[3].value();   // (a count below 2^30: to FP32's rounding)
+        const bool counts = n > 0.0f;
+        if (s < a.sequences) a.weights[s] = counts ? 1.0f / n : 0.0f;
+        if (counts)
+            sum.add(make_float4(v.v[0].value() / n, v.v[1].value() / n, v.v[2].value() / n, 1.0f));
     }
     bad = __syncthreads_or(bad);
-    block_sum<4, THREADS>(sum, mem);
-    const double share = sum[3] > 0.0 ? 1.0 / sum[3] : 0.0;
+    sum.warp();
+    if (lane == 0) part[tid >> 5] = sum;
+    __syncthreads();
+    if (tid < 32) {
+        sum.zero();
+        if (tid < THREADS / 32) sum = part[tid];
+        sum.warp();
+        const float n = sum.v[3].value(), share = n > 0.0f ? 1.0f / n : 0.0f;
+        if (tid == 0) {
+            shared_share = share;
+            const float nan = __int_as_float(0x7fffffff);
+            if (bad) atomicOr(a.status, kBadOffsets);
+            const float surrogate = bad ? nan : n > 0.0f ? sum.v[0].value() / n : 0.0f;
+            const float kl = bad ? nan : n > 0.0f ? sum.v[1].value() / n : 0.0f;
+            a.stats[0] = fmaf(a.kl_coef, kl, surrogate);
+            a.stats[1] = surrogate;
+            a.stats[2] = kl;
+            a.stats[3] = bad ? nan : n > 0.0f ? sum.v[2].value() / n : 0.0f;
+        }
+    }
+    __syncthreads();
+    const float share = shared_share;
     for (int s = tid; s < a.sequences; s += THREADS)   // (each thread its own ones)
-        a.weights[s] = a.sequence_mean ? static_cast<float>(a.weights[s] * share) : static_cast<float>(share);
-    if (tid != 0) return;
-    const double nan = __longlong_as_double(0x7ff8000000000000ll);
-    if (bad) atomicOr(a.status, kBadOffsets);
-    const double surrogate = bad ? nan : sum[0] * share, kl = bad ? nan : sum[1] * share;
-    a.stats[0] = static_cast<float>(surrogate + static_cast<double>(a.kl_coef) * kl);
-    a.stats[1] = static_cast<float>(surrogate);
-    a.stats[2] = static_cast<float>(kl);
-    a.stats[3] = static_cast<float>(bad ? nan : sum[2] * share);
+        a.weights[s] = a.sequence_mean ? a.weights[s] * share : share;
 }
 
 __global__ void __launch_bounds__(kThreads) tiles_kernel(const PolicyArgs a) {
@@ -308,12 +348,14 @@ __global__ void __launch_bounds__(kThreads) fused_kernel(const PolicyArgs a) {
 __global__ void __launch_bounds__(kThreads) backward_kernel(const PolicyArgs a) {
     __shared__ Span shared_span;
     const long long tile0 = static_cast<long long>(blockIdx.x) * kTile;
-    find_span(a, tile0, &shared_span);
-    const Span span = shared_span;
     const float up = a.dloss != nullptr ? __ldg(a.dloss) : 1.0f;
     Token t[kRows];
     int of[kRows];
-    load_tokens(a, tile0, span, t, of, true);
+    load_tokens(a, tile0, t);
+    find_span(a, tile0, true, &shared_span);
+    __syncthreads();
+    const Span span = shared_span;
+    place_tokens(a, tile0, span, t, of, true);
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
         const long long row = tile0 + threadIdx.x + u * kThreads;

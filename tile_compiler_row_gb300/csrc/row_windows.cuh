@@ -23,50 +23,81 @@ __device__ __forceinline__ uint4 load_vec(const void *p) {
     return __ldg(static_cast<const uint4 *>(p));
 }
 
-// Elements [at, at + V) of the row [row, row + width) of T, 0 outside it.
-// Reads nothing outside the row.
+// The matrix that windows are read from: nothing outside it is.
+struct Bounds {
+    uintptr_t begin, end;
+};
+template <class T>
+__device__ __forceinline__ Bounds bounds_of(const void *p, long long rows, int width) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    return Bounds{b, b + static_cast<size_t>(rows) * width * sizeof(T)};
+}
+
+// The vectors that hold elements [at, at + V) of a row, read without a branch
+// so that many windows are in flight; then the window put together.  A
+// window's elements outside the row hold what lies there: they are not stored.
+template <bool VEC>
+struct RawWindow;
+template <>
+struct RawWindow<true> {
+    uint4 a;
+};
+template <>
+struct RawWindow<false> {
+    uint4 a, b;
+};
+
 template <class T, bool VEC>
-__device__ __forceinline__ uint4 load_window(const T *row, int at, int width) {
-    constexpr int V = 16 / sizeof(T);
-    if constexpr (VEC) return load_vec(row + at);
-    const uintptr_t p = reinterpret_cast<uintptr_t>(row) + static_cast<long long>(at) * sizeof(T);
-    const uintptr_t begin = reinterpret_cast<uintptr_t>(row);
-    const uintptr_t end = begin + static_cast<size_t>(width) * sizeof(T);
-    const uintptr_t low = p & ~static_cast<uintptr_t>(15);
-    const unsigned int shift = static_cast<unsigned int>(p & 15);
-    if (low >= begin && low + (shift != 0 ? 32 : 16) <= end) {
-        const uint4 a = load_vec(reinterpret_cast<const void *>(low));
-        if (shift == 0) return a;
-        const uint4 b = load_vec(reinterpret_cast<const void *>(low + 16));
-        unsigned int w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        if (shift & 8) {
-#pragma unroll
-            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+__device__ __forceinline__ RawWindow<VEC> fetch_window(const T *row, int at, const Bounds &m, bool wanted) {
+    RawWindow<VEC> w = {};
+    if constexpr (VEC) {
+        if (wanted) w.a = load_vec(row + at);
+    } else {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(row) + static_cast<long long>(at) * sizeof(T);
+        const uintptr_t low = p & ~static_cast<uintptr_t>(15);
+        // (ends of the matrix, where a vector would pass them: element by element, below)
+        if (wanted && low >= m.begin && low + 32 <= m.end) {
+            w.a = load_vec(reinterpret_cast<const void *>(low));
+            w.b = load_vec(reinterpret_cast<const void *>(low + 16));
         }
-        if (shift & 4) {
+    }
+    return w;
+}
+
+template <class T, bool VEC>
+__device__ __forceinline__ uint4 join_window(const RawWindow<VEC> &r, const T *row, int at, int width,
+                                             const Bounds &m, bool wanted) {
+    if constexpr (VEC) return r.a;
+    else {
+        constexpr int V = 16 / sizeof(T);
+        const uintptr_t p = reinterpret_cast<uintptr_t>(row) + static_cast<long long>(at) * sizeof(T);
+        const uintptr_t low = p & ~static_cast<uintptr_t>(15);
+        if (wanted && !(low >= m.begin && low + 32 <= m.end)) {
+            unsigned int w[4] = {};
 #pragma unroll
-            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+            for (int j = 0; j < V; ++j)
+                if (at + j >= 0 && at + j < width) {
+                    if constexpr (sizeof(T) == 4)
+                        w[j] = __ldg(reinterpret_cast<const unsigned int *>(row + at + j));
+                    else
+                        w[j / 2] |= static_cast<unsigned int>(
+                                        __ldg(reinterpret_cast<const unsigned short *>(row + at + j)))
+                                    << (16 * (j & 1));
+                }
+            return make_uint4(w[0], w[1], w[2], w[3]);
         }
+        const unsigned int shift = static_cast<unsigned int>(p & 15);
+        unsigned int w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
         if constexpr (sizeof(T) == 2) {
-            if (shift & 2) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-            }
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (shift & 2));
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    unsigned int w[4] = {};
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (at + j >= 0 && at + j < width) {
-            if constexpr (sizeof(T) == 4)
-                w[j] = __ldg(reinterpret_cast<const unsigned int *>(row + at + j));
-            else
-                w[j / 2] |= static_cast<unsigned int>(
-                                __ldg(reinterpret_cast<const unsigned short *>(row + at + j)))
-                            << (16 * (j & 1));
-        }
-    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <class T>
@@ -102,11 +133,11 @@ __device__ __forceinline__ void store_window(D *row, int at, int width, const fl
                                Elem<D>::narrow2(v[i + 6], v[i + 7]));
             *reinterpret_cast<uint4 *>(row + at + i) = t;
         }
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (at + j >= 0 && at + j < width) store_one(row + at + j, v[j]);
+        for (int j = 0; j < V; ++j)
+            if (at + j >= 0 && at + j < width) store_one(row + at + j, v[j]);
+    }
 }
 
 // What the window holds now, widened; 0 outside the row.
@@ -121,12 +152,12 @@ __device__ __forceinline__ void read_window(const D *row, int at, int width, flo
 #pragma unroll
             for (int j = 0; j < N; ++j) v[i + j] = p[j];
         }
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        v[j] = 0.0f;
-        if (at + j >= 0 && at + j < width) v[j] = static_cast<float>(row[at + j]);
+        for (int j = 0; j < V; ++j) {
+            v[j] = 0.0f;
+            if (at + j >= 0 && at + j < width) v[j] = static_cast<float>(row[at + j]);
+        }
     }
 }
 
