@@ -1236,22 +1236,16 @@ def _columns(tensors, name, types, counts, dev):
     """(pointers, element counts, type codes) of a list of contiguous CUDA
     tensors on device index ``dev``, of types that ``types`` has codes for and
     of these element counts (None: any)."""
-    if len(tensors) != (len(tensors) if counts is None else len(counts)):
+    if counts is not None and len(tensors) != len(counts):
         raise ValueError(f"{name} must have {len(counts)} tensors like the other lists, "
                          f"not {len(tensors)}")
-    pointers, sizes, codes = [], [], []
     try:
-        for t in tensors:
-            code = types.get(t.dtype)
-            if code is None or t.get_device() != dev or not t.is_contiguous():
-                break
-            codes.append(code)
-            sizes.append(t.numel())
-            pointers.append(t.data_ptr())
-        else:
-            if counts is None or sizes == counts:
-                return pointers, sizes, codes
-    except AttributeError:
+        sizes = [t.numel() for t in tensors]
+        codes = [types[t.dtype] for t in tensors]
+        pointers = [t.data_ptr() for t in tensors if t.get_device() == dev and t.is_contiguous()]
+        if len(pointers) == len(codes) and (counts is None or sizes == counts):
+            return pointers, sizes, codes
+    except (AttributeError, KeyError):
         pass
     _list_of_tensors(tensors, name)
     for i, t in enumerate(tensors):

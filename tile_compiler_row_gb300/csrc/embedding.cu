@@ -37,6 +37,12 @@ __device__ __forceinline__ int windows_of(int width, bool vec) {
     return vec ? width / V : (width + V - 1) / V + 1;
 }
 
+// The next kernel of the chain may be set up; this one's inputs are written.
+__device__ __forceinline__ void let_next_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- lookup ---------------------------------------------------------------------
 
 // `lanes` (a power of two) threads a row, up to 4 windows of it each at a time.
@@ -200,6 +206,7 @@ __global__ void __launch_bounds__(kSortThreads)
     digits_kernel(const EmbeddingArgs a, int *counts, unsigned int *present, int bits, int passes) {
     constexpr int U = 8;
     __shared__ int bins[kMaxBins];
+    let_next_start();
     const int n = 1 << bits, tiles = gridDim.x;
     for (int d = threadIdx.x; d < n; d += kSortThreads) bins[d] = 0;
     __syncthreads();
@@ -227,15 +234,17 @@ __global__ void __launch_bounds__(kSortThreads)
 }
 
 // Zeros to the rows of dweight whose token does not occur: `each` rows from
-// from + part * each on, below `to`, with `lanes` threads a row.
+// from + part * each on, below `to`, with `lanes` threads a row.  CTAs of the
+// sort, the sums and the join have shares of them, so that DRAM is busy while
+// those wait for loads.
 struct Fill {
     const unsigned int *present;
     int from, to, each, lanes;
 };
-template <class D, bool VEC>
+template <class D, bool VEC, int THREADS>
 __device__ __forceinline__ void fill_rows(const EmbeddingArgs &a, const Fill &f, int part) {
     constexpr int N = 16 / sizeof(D);
-    const int lane = threadIdx.x & (f.lanes - 1), per = kSortThreads / f.lanes;
+    const int lane = threadIdx.x & (f.lanes - 1), per = THREADS / f.lanes;
     const int windows = windows_of<D>(a.width, VEC);
     const float zero[N] = {};
     const long long first = f.from + static_cast<long long>(part) * f.each;
@@ -252,14 +261,14 @@ __device__ __forceinline__ void fill_rows(const EmbeddingArgs &a, const Fill &f,
 // One stable pass: a pair goes behind those of smaller digits, and behind those
 // of its digit in earlier tiles, warps and places.  Integer atomics count the
 // next digit by the tile that a pair lands in; their order changes nothing.
-// The CTAs behind the tiles fill rows of the gradient meanwhile, which the sort
-// leaves DRAM free for.
 template <class D, bool VEC, int ITEMS, bool FIRST>
 __global__ void __launch_bounds__(kSortThreads)
     scatter_kernel(const EmbeddingArgs a, const Pair *in, Pair *out, const int *counts, int *next,
                    int bits, int shift, bool last, int tiles, const Fill fill) {
+    let_next_start();
+    wait_for_previous();
     if (static_cast<int>(blockIdx.x) >= tiles) {
-        fill_rows<D, VEC>(a, fill, blockIdx.x - tiles);
+        fill_rows<D, VEC, kSortThreads>(a, fill, blockIdx.x - tiles);
         return;
     }
     __shared__ int warp_bins[kSortWarps][kMaxBins];
@@ -389,12 +398,19 @@ __device__ __forceinline__ void finish_row(const EmbeddingArgs &a, D *dst, int a
 
 template <class T, class D, bool VEC>
 __global__ void __launch_bounds__(kSumThreads)
-    sum_kernel(const EmbeddingArgs a, const Pair *pairs, float *partial, int run, int runs, int lanes) {
+    sum_kernel(const EmbeddingArgs a, const Pair *pairs, float *partial, int run, int runs, int lanes,
+               int slices, int ctas, const Fill fill) {
     constexpr int V = 16 / sizeof(T), U = VEC ? 8 : 4;
+    let_next_start();
+    wait_for_previous();
+    if (static_cast<int>(blockIdx.x) >= ctas) {
+        fill_rows<D, VEC, kSumThreads>(a, fill, blockIdx.x - ctas);
+        return;
+    }
     const int lane = threadIdx.x & (lanes - 1);
-    const int r = blockIdx.x * (kSumThreads / lanes) + threadIdx.x / lanes;
+    const int r = blockIdx.x / slices * (kSumThreads / lanes) + threadIdx.x / lanes;
     const int windows = windows_of<T>(a.width, VEC);
-    const int j = blockIdx.y * lanes + lane;
+    const int j = blockIdx.x % slices * lanes + lane;
     if (r >= runs || j >= windows) return;
     const int begin = r * run, end = min(begin + run, a.rows);
     const unsigned int none = a.vocab;
@@ -456,14 +472,20 @@ __global__ void __launch_bounds__(kSumThreads)
 constexpr int kJoinParts = 4;
 template <class T, class D, bool VEC>
 __global__ void __launch_bounds__(kSumThreads * kJoinParts)
-    join_kernel(const EmbeddingArgs a, const Pair *pairs, const float *partial, int run, int runs, int lanes) {
+    join_kernel(const EmbeddingArgs a, const Pair *pairs, const float *partial, int run, int runs, int lanes,
+                int slices, int ctas, const Fill fill) {
     constexpr int V = 16 / sizeof(T);
+    wait_for_previous();
+    if (static_cast<int>(blockIdx.x) >= ctas) {
+        fill_rows<D, VEC, kSumThreads * kJoinParts>(a, fill, blockIdx.x - ctas);
+        return;
+    }
     __shared__ float4 parts[kJoinParts - 1][V / 4][kSumThreads];
     const int part = threadIdx.x / kSumThreads, thread = threadIdx.x % kSumThreads;
     const int lane = thread & (lanes - 1);
-    const int r = blockIdx.x * (kSumThreads / lanes) + thread / lanes;
+    const int r = blockIdx.x / slices * (kSumThreads / lanes) + thread / lanes;
     const int windows = windows_of<T>(a.width, VEC);
-    const int j = blockIdx.y * lanes + lane;
+    const int j = blockIdx.x % slices * lanes + lane;
     unsigned int cur = a.vocab;
     const int begin = r * run, end = begin + run;
     if (r < runs - 1 && j < windows) {   // not the last run: whole
@@ -476,15 +498,26 @@ __global__ void __launch_bounds__(kSumThreads * kJoinParts)
     if (!__syncthreads_or(live)) return;
     float sum[V] = {};
     if (live) {
-        int low = end, high = a.rows;   // the first place from `end` on with another token
+        // the run that the token ends in: most end in the next one
+        auto goes_past = [&](int q) {   // whether it fills run q to the end
+            return q < runs && __ldg(&pairs[min((q + 1) * run, a.rows) - 1].key) == cur;
+        };
+        int low = r + 1, step = 1;      // runs before `low` do not end it
+        while (goes_past(low + step - 1)) {
+            low += step;
+            step *= 2;
+        }
+        int high = min(low + step - 1, runs - 1);   // ... and one up to `high` does
         while (low < high) {
             const int mid = low + (high - low) / 2;
-            if (__ldg(&pairs[mid].key) == cur)
+            if (goes_past(mid))
                 low = mid + 1;
             else
                 high = mid;
         }
-        const int pieces = (low - 1) / run - r;   // besides the one that begins here
+        // (a token that ends with its run is not in the next one, and has no piece there)
+        const bool there = low < runs && __ldg(&pairs[low * run].key) == cur;
+        const int pieces = low - r - (there ? 0 : 1);   // besides the one that begins here
         const int from = r + 1 + static_cast<int>(static_cast<long long>(pieces) * part / kJoinParts);
         const int to = r + 1 + static_cast<int>(static_cast<long long>(pieces) * (part + 1) / kJoinParts);
         if (part == 0) {
@@ -545,19 +578,29 @@ Layout layout(int rows, int width, int vocab) {
     return l;
 }
 
+// A kernel of the chain, set up while the one before it runs.
+template <class... P, class... A>
+cudaError_t launch_next(void (*kernel)(P...), unsigned int grid, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 template <class D, bool VEC, int ITEMS>
-void launch_pass(const EmbeddingArgs &a, const SortPlan &s, int pass, const Pair *in, Pair *out, int *counts,
-                 const Fill &fill, cudaStream_t stream) {
+cudaError_t launch_pass(const EmbeddingArgs &a, const SortPlan &s, int pass, const Pair *in, Pair *out,
+                        int *counts, const Fill &fill, int fillers, cudaStream_t stream) {
     const size_t table = static_cast<size_t>(s.tiles) << s.bits;
     int *c = counts + pass * table;
-    const bool last = pass == s.passes - 1;
-    const unsigned int grid = s.tiles + (fill.to - fill.from + fill.each - 1) / fill.each;
-    if (pass == 0)
-        scatter_kernel<D, VEC, ITEMS, true><<<grid, kSortThreads, 0, stream>>>(
-            a, in, out, c, c + table, s.bits, 0, last, s.tiles, fill);
-    else
-        scatter_kernel<D, VEC, ITEMS, false><<<grid, kSortThreads, 0, stream>>>(
-            a, in, out, c, c + table, s.bits, pass * s.bits, last, s.tiles, fill);
+    const auto kernel = pass == 0 ? scatter_kernel<D, VEC, ITEMS, true> : scatter_kernel<D, VEC, ITEMS, false>;
+    return launch_next(kernel, s.tiles + fillers, kSortThreads, stream, a, in, out, c, c + table, s.bits,
+                       pass * s.bits, pass == s.passes - 1, s.tiles, fill);
 }
 
 template <class T, class D, bool VEC>
@@ -581,39 +624,53 @@ cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
     int *counts = reinterpret_cast<int *>(ws + l.counts);
     unsigned int *present = a.add ? nullptr : reinterpret_cast<unsigned int *>(ws + l.present);
     float *partial = reinterpret_cast<float *>(ws + l.partial);
+    cudaError_t err = cudaSuccess;
     if (present != nullptr) {
-        const cudaError_t err = cudaMemsetAsync(present, 0, (static_cast<size_t>(a.vocab) + 31) / 32 * sizeof(int), stream);
+        err = cudaMemsetAsync(present, 0, (static_cast<size_t>(a.vocab) + 31) / 32 * sizeof(int), stream);
         if (err != cudaSuccess) return err;
     }
     if (s.items == 8)
         digits_kernel<8><<<s.tiles, kSortThreads, 0, stream>>>(a, counts, present, s.bits, s.passes);
     else
         digits_kernel<32><<<s.tiles, kSortThreads, 0, stream>>>(a, counts, present, s.bits, s.passes);
-    // CTAs of about 32 KB each, in the order of the rows: few that went through
-    // all rows filled 1 GiB at 6.5 TB/s, these at 7.5
+    err = cudaGetLastError();
+    // Fillers: CTAs of about 32 KB each, in the order of the rows (few CTAs that
+    // went through all rows filled 1 GiB at 6.5 TB/s, these at 7.5).  A pass of
+    // the sort and the join get what DRAM takes while they run, some 5 us, the
+    // sums the rest.
     Fill fill = {present, 0, 0, 1, 8};
+    const long long row_bytes = static_cast<long long>(a.width) * sizeof(D);
     const int fill_windows = VEC ? a.width / N : (a.width + N - 1) / N + 1;
-    while (fill.lanes < kSortThreads && fill.lanes < fill_windows) fill.lanes *= 2;
-    fill.each = 32768 / (fill_windows * 16) + kSortThreads / fill.lanes;
-    for (int p = 0; p < s.passes; ++p) {
-        if (present != nullptr) {   // each pass a share of the rows
-            fill.from = fill.to;
-            fill.to = static_cast<int>(static_cast<long long>(a.vocab) * (p + 1) / s.passes);
-        }
-        if (s.items == 8)
-            launch_pass<D, VEC, 8>(a, s, p, list[(p + 1) & 1], list[p & 1], counts, fill, stream);
-        else
-            launch_pass<D, VEC, 32>(a, s, p, list[(p + 1) & 1], list[p & 1], counts, fill, stream);
+    while (fill.lanes < kSumThreads && fill.lanes < fill_windows) fill.lanes *= 2;
+    fill.each = 32768 / (fill_windows * 16) + kSumThreads * kJoinParts / fill.lanes;
+    const long long rows = present != nullptr ? a.vocab : 0;
+    long long share = (32ll << 20) / row_bytes + 1;
+    if (share > rows / (s.passes + 2)) share = rows / (s.passes + 2);
+    auto fillers = [&](long long to) {   // of the rows up to `to`
+        fill.from = fill.to;
+        fill.to = static_cast<int>(to);
+        return (fill.to - fill.from + fill.each - 1) / fill.each;
+    };
+    for (int p = 0; p < s.passes && err == cudaSuccess; ++p) {
+        const int n = fillers(share * (p + 1));
+        err = s.items == 8
+            ? launch_pass<D, VEC, 8>(a, s, p, list[(p + 1) & 1], list[p & 1], counts, fill, n, stream)
+            : launch_pass<D, VEC, 32>(a, s, p, list[(p + 1) & 1], list[p & 1], counts, fill, n, stream);
     }
+    if (err != cudaSuccess) return err;
     const Pair *sorted = list[(s.passes - 1) & 1];
     int lanes = 8;
     while (lanes < kSumThreads && lanes < windows) lanes *= 2;
-    const int per = kSumThreads / lanes;
-    const dim3 grid((m.runs + per - 1) / per, (windows + lanes - 1) / lanes);
-    sum_kernel<T, D, VEC><<<grid, kSumThreads, 0, stream>>>(a, sorted, partial, m.run, m.runs, lanes);
-    if (m.runs > 1)
-        join_kernel<T, D, VEC><<<grid, kSumThreads * kJoinParts, 0, stream>>>(a, sorted, partial, m.run, m.runs, lanes);
-    return cudaGetLastError();
+    const int per = kSumThreads / lanes, slices = (windows + lanes - 1) / lanes;
+    const int ctas = (m.runs + per - 1) / per * slices;
+    const bool join = m.runs > 1;
+    int n = fillers(join ? rows - share : rows);
+    err = launch_next(sum_kernel<T, D, VEC>, ctas + n, kSumThreads, stream, a, sorted, partial, m.run, m.runs,
+                      lanes, slices, ctas, fill);
+    if (err != cudaSuccess || !join) return err;
+    n = fillers(rows);
+    return launch_next(join_kernel<T, D, VEC>, ctas + n, kSumThreads * kJoinParts, stream, a, sorted,
+                       static_cast<const float *>(partial), m.run, m.runs, lanes, slices, ctas, fill);
 }
 
 template <class T, class D>

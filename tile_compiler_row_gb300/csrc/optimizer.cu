@@ -376,83 +376,102 @@ __device__ __forceinline__ float2 widen_codes(unsigned int two) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
-// Sums of two packed products.  Scalar: the packed addition of packed products
-// came out as one rounding less (a fused multiply-add), against its ".rn".
-__device__ __forceinline__ void add_halves(F2 a, F2 b, float &lo, float &hi) {
-    float a0, a1, b0, b1;
-    unpack(a, a0, a1);
-    unpack(b, b0, b1);
-    lo = __fadd_rn(a0, b0);
-    hi = __fadd_rn(a1, b1);
-}
-// NaN where one of them is.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The largest magnitude, NaN where one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
     float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+// To 1 ulp; below 2^-126 nothing.
+__device__ __forceinline__ float root_of(float x) {
+    float d;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+    return d;
+}
+__device__ __forceinline__ void copy_async(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 :: "r"(static_cast<unsigned int>(__cvta_generic_to_shared(to))), "l"(from) : "memory");
 }
 
 constexpr int kEightWarps = kAdamwThreads / 32;
+// Shared memory of a warp: stages of a block of 256 each, its parameters, its
+// codes of m and v, its gradients (16-bit: three stages, FP32: two).
+constexpr int kEightRoom = 6144;
 
-// What a lane has of a block of 256, as it lies in memory: 8 elements, one
-// behind the other where the block is whole and on the grid, else each 32 on.
-struct EightRaw {
-    float4 p[2];
-    uint4 g[2];
-    unsigned int m[2], v[2];
-    float m_scale, v_scale;
+// The block's vectors on their way to a stage.
+__device__ __forceinline__ void fetch_eight(const AdamwEntry &e, long long block, int lane, char *stage) {
+    const long long base = block * kStateBlock;
+    const char *p = reinterpret_cast<const char *>(e.param + base);
+    copy_async(stage + lane * 16, p + lane * 16);
+    copy_async(stage + 512 + lane * 16, p + 512 + lane * 16);
+    const char *codes = static_cast<const char *>(lane < 16 ? e.m : e.v) + base;
+    copy_async(stage + 1024 + lane * 16, codes + (lane & 15) * 16);
+    const int wide = e.grad_elem == ELEM_F32 ? 1024 : 512;
+    const char *g = static_cast<const char *>(e.grad) + base * (wide / kStateBlock);
+    copy_async(stage + 1536 + lane * 16, g + lane * 16);
+    if (wide == 1024) copy_async(stage + 2048 + lane * 16, g + 512 + lane * 16);
+}
+
+// What a lane holds of a block: 8 elements, one behind the other where the
+// block is whole and on the 16-byte grid, else each 32 on.
+struct Eight {
+    float p[8], g[8];
+    unsigned int m[2], v[2];   // codes
 };
 
-__device__ __forceinline__ void load_eight(const AdamwEntry &e, long long block, int lane, bool whole, EightRaw &r) {
-    const long long base = block * kStateBlock, at = base + lane * 8;
-    const unsigned char *mc = static_cast<const unsigned char *>(e.m), *vc = static_cast<const unsigned char *>(e.v);
-    r.m_scale = __ldcs(e.m_scale + block);
-    r.v_scale = __ldcs(e.v_scale + block);
-    if (whole) {
-        if (e.grad_elem == ELEM_F32) {
-            r.g[0] = load_grads(e.grad, ELEM_F32, at);
-            r.g[1] = load_grads(e.grad, ELEM_F32, at + 4);
-        } else {
-            r.g[0] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(e.grad) + at));
-            r.g[1] = make_uint4(r.g[0].z, r.g[0].w, 0, 0);
-        }
-        const uint2 m = __ldcs(reinterpret_cast<const uint2 *>(mc + at));
-        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(vc + at));
-        r.m[0] = m.x;
-        r.m[1] = m.y;
-        r.v[0] = v.x;
-        r.v[1] = v.y;
-        r.p[0] = __ldcs(reinterpret_cast<const float4 *>(e.param + at));
-        r.p[1] = __ldcs(reinterpret_cast<const float4 *>(e.param + at) + 1);
-        return;
+__device__ __forceinline__ void read_stage(const AdamwEntry &e, int lane, const char *stage, Eight &r) {
+    const float4 p0 = *reinterpret_cast<const float4 *>(stage + lane * 32);
+    const float4 p1 = *reinterpret_cast<const float4 *>(stage + lane * 32 + 16);
+    const uint2 m = *reinterpret_cast<const uint2 *>(stage + 1024 + lane * 8);
+    const uint2 v = *reinterpret_cast<const uint2 *>(stage + 1280 + lane * 8);
+    uint4 g0, g1;
+    if (e.grad_elem == ELEM_F32) {
+        g0 = *reinterpret_cast<const uint4 *>(stage + 1536 + lane * 32);
+        g1 = *reinterpret_cast<const uint4 *>(stage + 1536 + lane * 32 + 16);
+    } else {
+        g0 = *reinterpret_cast<const uint4 *>(stage + 1536 + lane * 16);
+        g1 = make_uint4(g0.z, g0.w, 0, 0);
     }
-    float p[8], g[8];
+    float lo[4], hi[4];
+    widen_grads(g0, e.grad_elem, lo);
+    widen_grads(g1, e.grad_elem, hi);
+    const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        r.p[j] = p[j];
+        r.g[j] = j < 4 ? lo[j & 3] : hi[j & 3];
+    }
+    r.m[0] = m.x;
+    r.m[1] = m.y;
+    r.v[0] = v.x;
+    r.v[1] = v.y;
+}
+
+__device__ __forceinline__ void read_elements(const AdamwEntry &e, long long base, int lane, Eight &r) {
+    const unsigned char *mc = static_cast<const unsigned char *>(e.m), *vc = static_cast<const unsigned char *>(e.v);
     r.m[0] = r.m[1] = r.v[0] = r.v[1] = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const long long w = base + j * 32 + lane;
-        p[j] = g[j] = 0.0f;
+        r.p[j] = r.g[j] = 0.0f;
         if (w < e.n) {
-            g[j] = load_grad(e.grad, e.grad_elem, w);
-            p[j] = __ldcs(e.param + w);
+            r.g[j] = load_grad(e.grad, e.grad_elem, w);
+            r.p[j] = __ldcs(e.param + w);
             r.m[j / 4] |= static_cast<unsigned int>(mc[w]) << (8 * (j & 3));
             r.v[j / 4] |= static_cast<unsigned int>(vc[w]) << (8 * (j & 3));
         }
     }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        r.p[j] = make_float4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
-        r.g[j] = make_uint4(__float_as_uint(g[4 * j]), __float_as_uint(g[4 * j + 1]),
-                            __float_as_uint(g[4 * j + 2]), __float_as_uint(g[4 * j + 3]));
-    }
 }
 
-// A warp for each block of 256, `blocks` of them one after the other with the
-// next one's loads on their way (64 registers without, and half the warps
-// waiting: 735 us for 1.9e8 parameters).
+// A warp for each block of 256, `blocks` of them one after the other, whose
+// vectors the asynchronous copies bring to shared memory two blocks ahead:
+// issue slots and DRAM bind about alike (89 instructions an element, with the
+// block's and then the next one's loads in registers: 735 and 661 us for 1.9e8
+// parameters with FP16 gradients and copies, 458 us of DRAM).
 template <int N>
-__global__ void __launch_bounds__(kAdamwThreads, 3)
+__global__ void __launch_bounds__(kAdamwThreads, 4)
     adamw8_kernel(const __grid_constant__ Table<AdamwEntry, N> t, Scalars s, int blocks) {
+    __shared__ __align__(16) char room[kEightWarps][kEightRoom];
     const int i = tensor_of(t, blockIdx.x);
     const AdamwEntry &e = t.entry[i];
     const float f = s.factor != nullptr ? __ldg(s.factor) : 1.0f;
@@ -466,69 +485,81 @@ __global__ void __launch_bounds__(kAdamwThreads, 3)
     unsigned char *mc = static_cast<unsigned char *>(e.m), *vc = static_cast<unsigned char *>(e.v);
     const long long first = static_cast<long long>(blockIdx.x - t.first[i]) * blocks * kEightWarps + (threadIdx.x >> 5);
     auto is_whole = [&](long long block) { return e.vectors != 0 && (block + 1) * kStateBlock <= e.n; };
-    EightRaw next;
-    if (first * kStateBlock < e.n) load_eight(e, first, lane, is_whole(first), next);
+    char *mine = room[threadIdx.x >> 5];
+    const bool wide = e.grad_elem == ELEM_F32;
+    const int stages = wide ? 2 : 3, size = wide ? 2560 : 2048;
+    // a group for each block of this warp, empty where there is none to copy
+    auto fetch = [&](int k, int stage) {
+        const long long block = first + static_cast<long long>(k) * kEightWarps;
+        if (k < blocks && is_whole(block)) fetch_eight(e, block, lane, mine + stage * size);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int k = 0; k < stages - 1; ++k) fetch(k, k);
+    int stage = 0;
+    float ms = 0.0f, vs = 0.0f;
+    if (first * kStateBlock < e.n) {
+        ms = __ldcs(e.m_scale + first);
+        vs = __ldcs(e.v_scale + first);
+    }
     for (int k = 0; k < blocks; ++k) {
-        const long long block = first + k * kEightWarps, base = block * kStateBlock, at = base + lane * 8;
-        if (base >= e.n) return;
+        const long long block = first + static_cast<long long>(k) * kEightWarps, base = block * kStateBlock;
+        const long long at = base + lane * 8;
+        if (base >= e.n) break;
         const bool whole = is_whole(block);
-        const EightRaw r = next;
+        fetch(k + stages - 1, stage == 0 ? stages - 1 : stage - 1);   // the stage read last
+        if (wide)
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else
+            asm volatile("cp.async.wait_group 2;" ::: "memory");
+        __syncwarp();
+        Eight r;
+        if (whole)
+            read_stage(e, lane, mine + stage * size, r);
+        else
+            read_elements(e, base, lane, r);
+        __syncwarp();   // read, before the stage is written again
+        stage = stage + 1 == stages ? 0 : stage + 1;
+        const float mscale_old = ms, vscale_old = vs;
         const long long following = block + kEightWarps;
-        if (k + 1 < blocks && following * kStateBlock < e.n)
-            load_eight(e, following, lane, is_whole(following), next);
-        float g[8], m[8], v[8], p[8];
-        {
-            const int kind = whole ? e.grad_elem : ELEM_F32;
-            float lo[4], hi[4];
-            widen_grads(r.g[0], kind, lo);
-            widen_grads(r.g[1], kind, hi);
-            const float pp[8] = {r.p[0].x, r.p[0].y, r.p[0].z, r.p[0].w, r.p[1].x, r.p[1].y, r.p[1].z, r.p[1].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                g[j] = lo[j];
-                g[j + 4] = hi[j];
-                const float2 a = widen_codes(r.m[j / 2] >> (16 * (j & 1)) & 0xffff);
-                const float2 b = widen_codes(r.v[j / 2] >> (16 * (j & 1)) & 0xffff);
-                m[2 * j] = a.x;
-                m[2 * j + 1] = a.y;
-                v[2 * j] = b.x;
-                v[2 * j + 1] = b.y;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] = pp[j];
+        if (k + 1 < blocks && following * kStateBlock < e.n) {
+            ms = __ldcs(e.m_scale + following);
+            vs = __ldcs(e.v_scale + following);
         }
-        const float ms = r.m_scale, vs = r.v_scale;
-        // two elements at a time, each operation rounded as its scalar form
-        float mtop = 0.0f, vtop = 0.0f;
+        // two elements at a time
+        float m[8], v[8], mtop = 0.0f, vtop = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-            const F2 g2 = mul2(pack(g[j], g[j + 1]), both(f));
-            const F2 root = mul2(pack(v[j], v[j + 1]), both(vs));
-            add_halves(mul2(mul2(pack(m[j], m[j + 1]), both(ms)), both(s.beta1)), mul2(g2, both(s.rest1)), m[j],
-                       m[j + 1]);
-            add_halves(mul2(mul2(root, root), both(s.beta2)), mul2(mul2(g2, g2), both(s.rest2)), v[j], v[j + 1]);
-            v[j] = __fsqrt_rn(v[j]);
-            v[j + 1] = __fsqrt_rn(v[j + 1]);
+            const float2 mcode = widen_codes(r.m[j / 4] >> (8 * (j & 3)) & 0xffff);
+            const float2 vcode = widen_codes(r.v[j / 4] >> (8 * (j & 3)) & 0xffff);
+            const F2 g2 = mul2(pack(r.g[j], r.g[j + 1]), both(f));
+            const F2 m2 = fma2(mul2(pack(mcode.x, mcode.y), both(mscale_old)), both(s.beta1), mul2(g2, both(s.rest1)));
+            const F2 root = mul2(pack(vcode.x, vcode.y), both(vscale_old));
+            const F2 v2 = fma2(mul2(root, root), both(s.beta2), mul2(mul2(g2, g2), both(s.rest2)));
+            unpack(m2, m[j], m[j + 1]);
+            unpack(v2, v[j], v[j + 1]);
+            v[j] = root_of(v[j]);
+            v[j + 1] = root_of(v[j + 1]);
             const F2 below = fma2(pack(v[j], v[j + 1]), both(s.root), both(s.eps));
-            float d0, d1, p0, p1;
+            float d0, d1;
             unpack(below, d0, d1);
-            const F2 step = mul2(pack(m[j], m[j + 1]), pack(reciprocal(d0), reciprocal(d1)));
-            unpack(fma2(step, both(-s.rate), mul2(pack(p[j], p[j + 1]), both(keep))), p0, p1);
-            p[j] = p0;
-            p[j + 1] = p1;
-            mtop = max_nan(mtop, max_nan(fabsf(m[j]), fabsf(m[j + 1])));
-            vtop = max_nan(vtop, max_nan(v[j], v[j + 1]));
+            const F2 step = mul2(m2, pack(reciprocal(d0), reciprocal(d1)));
+            unpack(fma2(step, both(-s.rate), mul2(pack(r.p[j], r.p[j + 1]), both(keep))), r.p[j], r.p[j + 1]);
+            mtop = max_abs(mtop, m[j], m[j + 1]);
+            vtop = max_abs(vtop, v[j], v[j + 1]);
         }
         const BlockScale mscale = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
         const BlockScale vscale = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)));
-        float mq[8], vq[8];
         auto quantise = [&](int j, unsigned int bits) {
-            const float size = round_at_random(fabsf(__fmul_rn(m[j], mscale.inverse)), bits & 0xffff);
-            mq[j] = copysignf(size, m[j]);
-            const float r = __fmul_rn(v[j], vscale.inverse);
-            const float q = round_at_random(r, bits >> 16);
-            vq[j] = r > 0.0f ? fmaxf(q, 0.001953125f) : q;   // a root that is not zero stays so
+            const float size = round_at_random(fabsf(m[j]), bits & 0xffff);
+            m[j] = copysignf(size, m[j]);
+            const float q = round_at_random(v[j], bits >> 16);
+            v[j] = v[j] > 0.0f ? fmaxf(q, 0.001953125f) : q;   // a root that is not zero stays so
         };
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            unpack(mul2(pack(m[j], m[j + 1]), both(mscale.inverse)), m[j], m[j + 1]);
+            unpack(mul2(pack(v[j], v[j + 1]), both(vscale.inverse)), v[j], v[j + 1]);
+        }
         if (whole) {   // the two elements of a pair are one lane's
             const unsigned long long at_pair = key + static_cast<unsigned long long>((at >> 1) + 1) * kGolden;
 #pragma unroll
@@ -553,29 +584,30 @@ __global__ void __launch_bounds__(kAdamwThreads, 3)
             unsigned int mw[4], vw[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                mw[j] = narrow_codes(mq[2 * j], mq[2 * j + 1]);
-                vw[j] = narrow_codes(vq[2 * j], vq[2 * j + 1]);
+                mw[j] = narrow_codes(m[2 * j], m[2 * j + 1]);
+                vw[j] = narrow_codes(v[2 * j], v[2 * j + 1]);
             }
             __stcs(reinterpret_cast<uint2 *>(mc + at), make_uint2(mw[0] | mw[1] << 16, mw[2] | mw[3] << 16));
             __stcs(reinterpret_cast<uint2 *>(vc + at), make_uint2(vw[0] | vw[1] << 16, vw[2] | vw[3] << 16));
-            __stcs(reinterpret_cast<float4 *>(e.param + at), make_float4(p[0], p[1], p[2], p[3]));
-            __stcs(reinterpret_cast<float4 *>(e.param + at) + 1, make_float4(p[4], p[5], p[6], p[7]));
+            __stcs(reinterpret_cast<float4 *>(e.param + at), make_float4(r.p[0], r.p[1], r.p[2], r.p[3]));
+            __stcs(reinterpret_cast<float4 *>(e.param + at) + 1, make_float4(r.p[4], r.p[5], r.p[6], r.p[7]));
             if (e.copy_elem >= 0)
                 __stcs(reinterpret_cast<uint4 *>(static_cast<unsigned short *>(e.copy) + at),
-                       make_uint4(narrow_pair(e.copy_elem, p[0], p[1]), narrow_pair(e.copy_elem, p[2], p[3]),
-                                  narrow_pair(e.copy_elem, p[4], p[5]), narrow_pair(e.copy_elem, p[6], p[7])));
+                       make_uint4(narrow_pair(e.copy_elem, r.p[0], r.p[1]), narrow_pair(e.copy_elem, r.p[2], r.p[3]),
+                                  narrow_pair(e.copy_elem, r.p[4], r.p[5]), narrow_pair(e.copy_elem, r.p[6], r.p[7])));
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const long long w = base + j * 32 + lane;
                 if (w >= e.n) continue;
-                mc[w] = static_cast<unsigned char>(narrow_codes(mq[j], 0.0f) & 0xff);
-                vc[w] = static_cast<unsigned char>(narrow_codes(vq[j], 0.0f) & 0xff);
-                __stcs(e.param + w, p[j]);
-                if (e.copy_elem >= 0) store_copy(e.copy, e.copy_elem, w, p[j]);
+                mc[w] = static_cast<unsigned char>(narrow_codes(m[j], 0.0f) & 0xff);
+                vc[w] = static_cast<unsigned char>(narrow_codes(v[j], 0.0f) & 0xff);
+                __stcs(e.param + w, r.p[j]);
+                if (e.copy_elem >= 0) store_copy(e.copy, e.copy_elem, w, r.p[j]);
             }
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ---- launches ---------------------------------------------------------------------------
@@ -624,10 +656,9 @@ cudaError_t launch_adamw_table(const AdamwTensor *t, int count, int index, const
         const AdamwTensor &a = t[i];
         if (a.n == 0) continue;
         const size_t four = c.eight ? 8 : 4;   // elements of a vector access
-        const size_t wide = c.eight ? 8 : 16;  // bytes of the states'
         const size_t grad = a.grad_elem == ELEM_F32 ? 16 : 2 * four;
-        const bool vectors = on_grid(a.param, 16) && on_grid(a.grad, grad) && on_grid(a.m, wide) &&
-                             on_grid(a.v, wide) && on_grid(a.copy, 2 * four);
+        const bool vectors = on_grid(a.param, 16) && on_grid(a.grad, grad) && on_grid(a.m, 16) &&
+                             on_grid(a.v, 16) && on_grid(a.copy, 2 * four);
         table.entry[used] = AdamwEntry{a.param, a.grad, a.m, a.v, a.m_scale, a.v_scale, a.copy, a.n,
                                        a.decay, index + i, a.grad_elem, a.copy_elem, vectors};
         table.first[used++] = static_cast<int>(chunks);
