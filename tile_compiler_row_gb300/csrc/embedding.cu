@@ -92,82 +92,109 @@ cudaError_t launch_lookup(const EmbeddingArgs &a, cudaStream_t stream) {
 
 // ---- gradient: few rows ------------------------------------------------------------
 
-// CTA (i, s): the rows of token[i], if i is the first, in slice s of 32 windows.
-constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32, kFewRows = 2048;
+// CTA (i, s): the rows of token[i], if i is the first of them, in slices s, s +
+// gridDim.y .. of 32 windows.  All tokens are in the CTA's registers at once.
+constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32, kMostFew = 2048;
+constexpr int kFewPer = kMostFew / kFewThreads;
 
 template <class T, class D, bool VEC>
 __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const EmbeddingArgs a) {
     constexpr int V = 16 / sizeof(T), U = 4;
-    __shared__ unsigned short list[kFewRows];
-    __shared__ int found[kFewWarps];
+    __shared__ unsigned short list[kMostFew];
+    __shared__ int found[kFewPer * kFewWarps];   // hits of each 32 tokens; then hits before them
+    __shared__ int count;
     __shared__ float part[kFewWarps][32][V + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = blockIdx.x;
     const long long t = __ldg(a.tokens + i);
-    int token = t == a.ignore || t < 0 || t >= a.vocab ? -1 : static_cast<int>(t);
+    const int token = t == a.ignore || t < 0 || t >= a.vocab ? -1 : static_cast<int>(t);
     if (token < 0) {
         if (tid == 0 && blockIdx.y == 0) token_row(a, t);
         return;
     }
-    int first = 1;
-    for (int j = tid; j < i; j += kFewThreads) first &= __ldg(a.tokens + j) != t;
-    if (!__syncthreads_and(first)) return;
-    // positions of the token, in order
-    int n = 0;
-    for (int base = i; base < a.rows; base += kFewThreads) {
-        const int j = base + tid;
-        const bool hit = j < a.rows && __ldg(a.tokens + j) == t;
-        const unsigned int mask = __ballot_sync(0xffffffffu, hit);
-        if (lane == 0) found[warp] = __popc(mask);
-        __syncthreads();
-        int before = n;
+    unsigned int mask[kFewPer];
+    bool first = true;
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) {
-            if (w < warp) before += found[w];
-            n += found[w];
-        }
-        if (hit) list[before + __popc(mask & ((1u << lane) - 1))] = static_cast<unsigned short>(j);
-        __syncthreads();
+    for (int k = 0; k < kFewPer; ++k) {
+        const int j = k * kFewThreads + tid;
+        mask[k] = j < a.rows && __ldg(a.tokens + j) == t;
     }
+#pragma unroll
+    for (int k = 0; k < kFewPer; ++k) {
+        first = first && !(mask[k] != 0 && k * kFewThreads + tid < i);
+        mask[k] = __ballot_sync(0xffffffffu, mask[k] != 0);
+        if (lane == 0) found[k * kFewWarps + warp] = __popc(mask[k]);
+    }
+    if (!__syncthreads_and(first)) return;
+    if (warp == 0) {
+        static_assert(kFewPer * kFewWarps == 64, "two for each lane");
+        const int one = found[2 * lane], two = found[2 * lane + 1];
+        int sum = one + two;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += up;
+        }
+        found[2 * lane] = sum - one - two;
+        found[2 * lane + 1] = sum - two;
+        if (lane == 31) count = sum;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kFewPer; ++k)
+        if (mask[k] >> lane & 1)
+            list[found[k * kFewWarps + warp] + __popc(mask[k] & ((1u << lane) - 1))] =
+                static_cast<unsigned short>(k * kFewThreads + tid);
+    __syncthreads();
     D *dst = static_cast<D *>(a.dweight) + static_cast<long long>(token) * a.width;
-    const int phase = VEC ? 0 : window_phase(dst);
-    const int windows = windows_of<T>(a.width, VEC);
-    const int at = (blockIdx.y * 32 + lane) * V - phase;
-    const bool in = static_cast<int>(blockIdx.y) * 32 + lane < windows;
+    const int phase = VEC ? 0 : window_phase(dst), n = count;
+    const int windows = windows_of<T>(a.width, VEC), slices = (windows + 31) / 32;
+    const Bounds bounds = bounds_of<T>(a.dout, a.rows, a.width);
     // each warp sums a contiguous part of the list
     const int from = n * warp / kFewWarps, to = n * (warp + 1) / kFewWarps;
-    const Bounds bounds = bounds_of<T>(a.dout, a.rows, a.width);
-    float sum[V] = {};
-    for (int k = from; k < to; k += U) {
-        RawWindow<VEC> raw[U];
-        const T *row[U];
+    for (int slice = blockIdx.y; slice < slices; slice += gridDim.y) {
+        const int at = (slice * 32 + lane) * V - phase;
+        const bool in = slice * 32 + lane < windows;
+        float sum[V] = {};
+        for (int k = from; k < to; k += U) {
+            RawWindow<VEC> raw[U];
+            const T *row[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            row[u] = static_cast<const T *>(a.dout) + static_cast<long long>(list[min(k + u, to - 1)]) * a.width;
-            raw[u] = fetch_window<T, VEC>(row[u], at, bounds, in && k + u < to);
+            for (int u = 0; u < U; ++u) {
+                row[u] = static_cast<const T *>(a.dout) + static_cast<long long>(list[min(k + u, to - 1)]) * a.width;
+                raw[u] = fetch_window<T, VEC>(row[u], at, bounds, in && k + u < to);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (!in || k + u >= to) continue;
+                float v[V];
+                widen_vec<T>(join_window<T, VEC>(raw[u], row[u], at, a.width, bounds, true), v);
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[e] += v[e];
+            }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (!in || k + u >= to) continue;
-            float v[V];
-            widen_vec<T>(join_window<T, VEC>(raw[u], row[u], at, a.width, bounds, true), v);
+        for (int e = 0; e < V; ++e) part[warp][lane][e] = sum[e];
+        __syncthreads();
+        if (warp == 0 && in) {
+            float old[V] = {};
+            if (a.add) read_window<D, V, VEC>(dst, at, a.width, old);
 #pragma unroll
-            for (int e = 0; e < V; ++e) sum[e] += v[e];
+            for (int e = 0; e < V; ++e) {
+                sum[e] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kFewWarps; ++w) sum[e] += part[w][lane][e];
+                sum[e] = fmaf(sum[e], a.scale, old[e]);
+            }
+            store_window<D, V, VEC>(dst, at, a.width, sum);
         }
+        __syncthreads();
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e) part[warp][lane][e] = sum[e];
-    __syncthreads();
-    if (warp != 0 || !in) return;
-    float old[V] = {};
-    if (a.add) read_window<D, V, VEC>(dst, at, a.width, old);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        sum[e] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) sum[e] += part[w][lane][e];
-        sum[e] = fmaf(sum[e], a.scale, old[e]);
-    }
-    store_window<D, V, VEC>(dst, at, a.width, sum);
+}
+
+constexpr long long kFewLooks = 1ll << 40;
+// Few rows: sorting them takes longer than each CTA's look at all tokens.
+bool few_rows(int rows, int width) {
+    return rows <= kMostFew && static_cast<long long>(rows) * rows * (width / 256 + 1) <= kFewLooks;
 }
 
 // ---- gradient: sorting positions by token --------------------------------------------
@@ -276,12 +303,25 @@ __global__ void __launch_bounds__(kSortThreads)
     __shared__ int sums[kSortWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = 1 << bits;
+    const int begin = blockIdx.x * kSortThreads * ITEMS + warp * 32 * ITEMS;
+    Pair pair[ITEMS];   // on their way while the counts are added up
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+        const int i = begin + r * 32 + lane;
+        pair[r] = Pair{0, 0};
+        if (i < a.rows) {
+            if constexpr (FIRST)
+                pair[r] = Pair{key_at(a, i), static_cast<unsigned int>(i)};
+            else
+                pair[r] = in[i];
+        }
+    }
     for (int d = tid; d < kSortWarps * kMaxBins; d += kSortThreads) (&warp_bins[0][0])[d] = 0;
     // digits 2 tid and 2 tid + 1: pairs before this tile, and in all
     int before[2] = {}, total[2] = {};
     const int d0 = 2 * tid;
     if (d0 < n) {
-#pragma unroll 4
+#pragma unroll 8
         for (int t = 0; t < tiles; ++t) {
             const int2 c = *reinterpret_cast<const int2 *>(counts + static_cast<long long>(t) * n + d0);
             if (t < static_cast<int>(blockIdx.x)) {
@@ -306,19 +346,7 @@ __global__ void __launch_bounds__(kSortThreads)
         base[d0] = scan + before[0];
         base[d0 + 1] = scan + total[0] + before[1];
     }
-    const int begin = blockIdx.x * kSortThreads * ITEMS + warp * 32 * ITEMS;
-    Pair pair[ITEMS];
     int rank[ITEMS];
-#pragma unroll
-    for (int r = 0; r < ITEMS; ++r) {
-        const int i = begin + r * 32 + lane;
-        if (i < a.rows) {
-            if constexpr (FIRST)
-                pair[r] = Pair{key_at(a, i), static_cast<unsigned int>(i)};
-            else
-                pair[r] = in[i];
-        }
-    }
 #pragma unroll
     for (int r = 0; r < ITEMS; ++r) {
         const bool live = begin + r * 32 + lane < a.rows;
@@ -607,13 +635,15 @@ template <class T, class D, bool VEC>
 cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T), N = 16 / sizeof(D);
     const int windows = VEC ? a.width / V : (a.width + V - 1) / V + 1;
-    if (a.rows <= kFewRows) {
+    if (few_rows(a.rows, a.width)) {
         if (!a.add) {
             const cudaError_t err = cudaMemsetAsync(
                 a.dweight, 0, static_cast<size_t>(a.vocab) * a.width * sizeof(D), stream);
             if (err != cudaSuccess) return err;
         }
-        few_rows_kernel<T, D, VEC><<<dim3(a.rows, (windows + 31) / 32), kFewThreads, 0, stream>>>(a);
+        const int slices = (windows + 31) / 32;   // two to a CTA where there are many
+        const int parts = static_cast<long long>(a.rows) * slices > 4096 ? (slices + 1) / 2 : slices;
+        few_rows_kernel<T, D, VEC><<<dim3(a.rows, parts), kFewThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
     const SortPlan s = sort_plan(a.rows, a.vocab);
@@ -644,7 +674,7 @@ cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
     while (fill.lanes < kSumThreads && fill.lanes < fill_windows) fill.lanes *= 2;
     fill.each = 32768 / (fill_windows * 16) + kSumThreads * kJoinParts / fill.lanes;
     const long long rows = present != nullptr ? a.vocab : 0;
-    long long share = (32ll << 20) / row_bytes + 1;
+    long long share = (64ll << 20) / row_bytes + 1;
     if (share > rows / (s.passes + 2)) share = rows / (s.passes + 2);
     auto fillers = [&](long long to) {   // of the rows up to `to`
         fill.from = fill.to;
@@ -696,7 +726,7 @@ cudaError_t launch_embedding(int elem, bool vectors, EmbeddingArgs a, cudaStream
 }
 
 size_t embedding_backward_workspace(int rows, int width, int vocab) {
-    return rows <= kFewRows ? 0 : layout(rows, width, vocab).bytes;
+    return few_rows(rows, width) ? 0 : layout(rows, width, vocab).bytes;
 }
 
 cudaError_t launch_embedding_backward(int elem, int into, bool vectors, EmbeddingArgs a,

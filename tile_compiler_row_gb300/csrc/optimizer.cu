@@ -360,13 +360,24 @@ __device__ __forceinline__ BlockScale block_scale(unsigned int top) {   // bits 
     return BlockScale{__uint_as_float((e - 7) << 23), __uint_as_float((261 - e) << 23)};
 }
 
-// A magnitude below 256 in e4m3's steps: 16 random bits are added below the
-// three bits of the mantissa that stay.  Under 2^-6, where the type's steps no
-// longer shrink, it is moved up to where three bits are such a step.
+// A magnitude below 256 in e4m3's steps: 16 random bits (bits / 16, of which
+// the low four are 0) are added below the three bits of the mantissa that
+// stay.  Under 2^-6, where the type's steps no longer shrink, it is moved up to
+// where three bits are such a step.  (As written in C this was one instruction
+// more, of 83 for each element, and issue slots bind.)
 __device__ __forceinline__ float round_at_random(float size, unsigned int bits) {
-    const float base = size < 0.015625f ? 0.015625f : 0.0f;
-    const unsigned int w = __float_as_uint(__fadd_rn(size, base)) + (bits << 4);
-    return __fsub_rn(__uint_as_float(w & 0xfff00000u), base);
+    float d;
+    asm("{\n\t.reg .pred small;\n\t.reg .f32 x;\n\t.reg .b32 w;\n\t"
+        "setp.lt.f32 small, %1, 0f3C800000;\n\t"
+        "mov.f32 x, %1;\n\t"
+        "@small add.rn.f32 x, x, 0f3C800000;\n\t"
+        "mov.b32 w, x;\n\t"
+        "add.u32 w, w, %2;\n\t"
+        "and.b32 w, w, 0xfff00000;\n\t"
+        "mov.b32 x, w;\n\t"
+        "@small add.rn.f32 x, x, 0fBC800000;\n\t"
+        "mov.f32 %0, x;\n\t}" : "=f"(d) : "f"(size), "r"(bits));
+    return d;
 }
 
 __device__ __forceinline__ unsigned int narrow_codes(float lo, float hi) {   // exact
@@ -397,77 +408,195 @@ constexpr int kEightWarps = kAdamwThreads / 32;
 // Shared memory of a warp: stages of a block of 256 each, its parameters, its
 // codes of m and v, its gradients (16-bit: three stages, FP32: two).
 constexpr int kEightRoom = 6144;
+constexpr int kEightMost = 4;   // blocks of a warp
 
-// The block's vectors on their way to a stage.
-__device__ __forceinline__ void fetch_eight(const AdamwEntry &e, long long block, int lane, char *stage) {
-    const long long base = block * kStateBlock;
-    const char *p = reinterpret_cast<const char *>(e.param + base);
-    copy_async(stage + lane * 16, p + lane * 16);
-    copy_async(stage + 512 + lane * 16, p + 512 + lane * 16);
-    const char *codes = static_cast<const char *>(lane < 16 ? e.m : e.v) + base;
-    copy_async(stage + 1024 + lane * 16, codes + (lane & 15) * 16);
-    const int wide = e.grad_elem == ELEM_F32 ? 1024 : 512;
-    const char *g = static_cast<const char *>(e.grad) + base * (wide / kStateBlock);
-    copy_async(stage + 1536 + lane * 16, g + lane * 16);
-    if (wide == 1024) copy_async(stage + 2048 + lane * 16, g + 512 + lane * 16);
-}
+struct None {};   // no copy
 
-// What a lane holds of a block: 8 elements, one behind the other where the
-// block is whole and on the 16-byte grid, else each 32 on.
-struct Eight {
-    float p[8], g[8];
-    unsigned int m[2], v[2];   // codes
-};
-
-__device__ __forceinline__ void read_stage(const AdamwEntry &e, int lane, const char *stage, Eight &r) {
-    const float4 p0 = *reinterpret_cast<const float4 *>(stage + lane * 32);
-    const float4 p1 = *reinterpret_cast<const float4 *>(stage + lane * 32 + 16);
-    const uint2 m = *reinterpret_cast<const uint2 *>(stage + 1024 + lane * 8);
-    const uint2 v = *reinterpret_cast<const uint2 *>(stage + 1280 + lane * 8);
-    uint4 g0, g1;
-    if (e.grad_elem == ELEM_F32) {
-        g0 = *reinterpret_cast<const uint4 *>(stage + 1536 + lane * 32);
-        g1 = *reinterpret_cast<const uint4 *>(stage + 1536 + lane * 32 + 16);
+template <class G>
+__device__ __forceinline__ void widen_eight(const uint4 *t, float (&g)[8]) {
+    if constexpr (sizeof(G) == 4) {
+        widen_vec<float>(t[0], *reinterpret_cast<float (*)[4]>(&g[0]));
+        widen_vec<float>(t[1], *reinterpret_cast<float (*)[4]>(&g[4]));
     } else {
-        g0 = *reinterpret_cast<const uint4 *>(stage + 1536 + lane * 16);
-        g1 = make_uint4(g0.z, g0.w, 0, 0);
+        widen_vec<G>(t[0], g);
     }
-    float lo[4], hi[4];
-    widen_grads(g0, e.grad_elem, lo);
-    widen_grads(g1, e.grad_elem, hi);
-    const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        r.p[j] = p[j];
-        r.g[j] = j < 4 ? lo[j & 3] : hi[j & 3];
-    }
-    r.m[0] = m.x;
-    r.m[1] = m.y;
-    r.v[0] = v.x;
-    r.v[1] = v.y;
 }
 
-__device__ __forceinline__ void read_elements(const AdamwEntry &e, long long base, int lane, Eight &r) {
-    const unsigned char *mc = static_cast<const unsigned char *>(e.m), *vc = static_cast<const unsigned char *>(e.v);
-    r.m[0] = r.m[1] = r.v[0] = r.v[1] = 0;
+// The blocks of one CTA.  Places are counted from the chunk's first element, in
+// 32 bits.
+template <class G, class C>
+__device__ __forceinline__ void eight_chunk(const AdamwEntry &e, const Scalars &s, float f, float keep,
+                                            unsigned long long key, long long start, int blocks, char *mine) {
+    constexpr bool WIDE = sizeof(G) == 4;
+    constexpr int STAGES = WIDE ? 2 : 3, SIZE = WIDE ? 2560 : 2048;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long chunk = static_cast<long long>(blocks) * kEightWarps * kStateBlock;
+    const int left = static_cast<int>(min(e.n - start, chunk));        // elements of this CTA
+    const int whole_to = e.vectors != 0 ? left & -kStateBlock : 0;   // ... that whole blocks on the grid have
+    float *param = e.param + start;
+    const G *grad = static_cast<const G *>(e.grad) + start;
+    unsigned char *mc = static_cast<unsigned char *>(e.m) + start, *vc = static_cast<unsigned char *>(e.v) + start;
+    float *m_scale = e.m_scale + start / kStateBlock, *v_scale = e.v_scale + start / kStateBlock;
+    key += (static_cast<unsigned long long>(start) / 2 + 1) * kGolden;
+    // a group of copies for each block of this warp, empty where there is none
+    auto fetch = [&](int base, int stage) {
+        if (base < whole_to) {
+            char *to = mine + stage * SIZE + lane * 16;
+            const char *p = reinterpret_cast<const char *>(param + base) + lane * 16;
+            copy_async(to, p);
+            copy_async(to + 512, p + 512);
+            copy_async(to + 1024, (lane < 16 ? mc : vc) + base + (lane & 15) * 16);
+            const char *g = reinterpret_cast<const char *>(grad + base) + lane * 16;
+            copy_async(to + 1536, g);
+            if constexpr (WIDE) copy_async(to + 2048, g + 512);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    constexpr int STEP = kEightWarps * kStateBlock;
+    int base = warp * kStateBlock;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const long long w = base + j * 32 + lane;
-        r.p[j] = r.g[j] = 0.0f;
-        if (w < e.n) {
-            r.g[j] = load_grad(e.grad, e.grad_elem, w);
-            r.p[j] = __ldcs(e.param + w);
-            r.m[j / 4] |= static_cast<unsigned int>(mc[w]) << (8 * (j & 3));
-            r.v[j / 4] |= static_cast<unsigned int>(vc[w]) << (8 * (j & 3));
+    for (int k = 0; k < STAGES - 1; ++k) fetch(base + k * STEP, k);
+    // the scales of this warp's blocks: lanes 0 .. 3 those of m, 4 .. 7 of v
+    float scales = 0.0f;
+    {
+        const int of = base + (lane & 3) * STEP;
+        if (lane < 8 && of < min(left, base + blocks * STEP))
+            scales = __ldcs((lane < 4 ? m_scale : v_scale) + of / kStateBlock);
+    }
+    int stage = 0;
+    for (int k = 0; base < left; base += STEP, ++k) {
+        const bool whole = base < whole_to;
+        fetch(base + (STAGES - 1) * STEP, stage == 0 ? STAGES - 1 : stage - 1);   // the stage read last
+        asm volatile("cp.async.wait_group %0;" :: "n"(STAGES - 1) : "memory");
+        __syncwarp();
+        float p[8], g[8];
+        unsigned int mw[2], vw[2];
+        const int at = base + lane * 8;
+        if (whole) {
+            const char *from = mine + stage * SIZE;
+            const float4 p0 = *reinterpret_cast<const float4 *>(from + lane * 32);
+            const float4 p1 = *reinterpret_cast<const float4 *>(from + lane * 32 + 16);
+            const uint2 a = *reinterpret_cast<const uint2 *>(from + 1024 + lane * 8);
+            const uint2 b = *reinterpret_cast<const uint2 *>(from + 1280 + lane * 8);
+            uint4 raw[2];
+            raw[0] = *reinterpret_cast<const uint4 *>(from + 1536 + lane * (WIDE ? 32 : 16));
+            if constexpr (WIDE) raw[1] = *reinterpret_cast<const uint4 *>(from + 1536 + lane * 32 + 16);
+            widen_eight<G>(raw, g);
+            const float q[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[j] = q[j];
+            mw[0] = a.x;
+            mw[1] = a.y;
+            vw[0] = b.x;
+            vw[1] = b.y;
+        } else {   // a lane has each 32nd element of the block
+            mw[0] = mw[1] = vw[0] = vw[1] = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int w = base + j * 32 + lane;
+                p[j] = g[j] = 0.0f;
+                if (w < left) {
+                    g[j] = static_cast<float>(grad[w]);
+                    p[j] = __ldcs(param + w);
+                    mw[j / 4] |= static_cast<unsigned int>(mc[w]) << (8 * (j & 3));
+                    vw[j / 4] |= static_cast<unsigned int>(vc[w]) << (8 * (j & 3));
+                }
+            }
+        }
+        __syncwarp();   // read, before the stage is written again
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        const F2 m_old = both(__shfl_sync(0xffffffffu, scales, k));
+        const F2 v_old = both(__shfl_sync(0xffffffffu, scales, 4 + k));
+        // two elements at a time
+        float m[8], v[8], mtop = 0.0f, vtop = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const float2 mcode = widen_codes(mw[j / 4] >> (8 * (j & 3)) & 0xffff);
+            const float2 vcode = widen_codes(vw[j / 4] >> (8 * (j & 3)) & 0xffff);
+            const F2 g2 = mul2(pack(g[j], g[j + 1]), both(f));
+            const F2 m2 = fma2(mul2(pack(mcode.x, mcode.y), m_old), both(s.beta1), mul2(g2, both(s.rest1)));
+            const F2 root = mul2(pack(vcode.x, vcode.y), v_old);
+            const F2 v2 = fma2(mul2(root, root), both(s.beta2), mul2(mul2(g2, g2), both(s.rest2)));
+            unpack(m2, m[j], m[j + 1]);
+            unpack(v2, v[j], v[j + 1]);
+            v[j] = root_of(v[j]);
+            v[j + 1] = root_of(v[j + 1]);
+            const F2 below = fma2(pack(v[j], v[j + 1]), both(s.root), both(s.eps));
+            float d0, d1;
+            unpack(below, d0, d1);
+            const F2 step = mul2(m2, pack(reciprocal(d0), reciprocal(d1)));
+            unpack(fma2(step, both(-s.rate), mul2(pack(p[j], p[j + 1]), both(keep))), p[j], p[j + 1]);
+            mtop = max_abs(mtop, m[j], m[j + 1]);
+            vtop = max_abs(vtop, v[j], v[j + 1]);
+        }
+        const BlockScale mscale = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
+        const BlockScale vscale = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)));
+        if (lane == 0) {
+            m_scale[base / kStateBlock] = mscale.scale;
+            v_scale[base / kStateBlock] = vscale.scale;
+        }
+        // low half of the bits: m, high half: v
+        auto quantise = [&](int j, unsigned int bits) {
+            const float size = round_at_random(fabsf(m[j]), (bits & 0xffff) << 4);
+            m[j] = copysignf(size, m[j]);
+            const float q = round_at_random(v[j], (bits >> 16) << 4);
+            v[j] = v[j] > 0.0f ? fmaxf(q, 0.001953125f) : q;   // a root that is not zero stays so
+        };
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            unpack(mul2(pack(m[j], m[j + 1]), both(mscale.inverse)), m[j], m[j + 1]);
+            unpack(mul2(pack(v[j], v[j + 1]), both(vscale.inverse)), v[j], v[j + 1]);
+        }
+        if (whole) {   // the two elements of a pair are one lane's
+            const unsigned long long at_pair = key + static_cast<unsigned long long>(static_cast<unsigned int>(at) / 2) * kGolden;
+            unsigned int m4[4], v4[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const unsigned long long two = mix64(at_pair + static_cast<unsigned long long>(j) * kGolden);
+                quantise(2 * j, static_cast<unsigned int>(two));
+                quantise(2 * j + 1, static_cast<unsigned int>(two >> 32));
+                m4[j] = narrow_codes(m[2 * j], m[2 * j + 1]);
+                v4[j] = narrow_codes(v[2 * j], v[2 * j + 1]);
+            }
+            __stcs(reinterpret_cast<uint2 *>(mc + at), make_uint2(m4[0] | m4[1] << 16, m4[2] | m4[3] << 16));
+            __stcs(reinterpret_cast<uint2 *>(vc + at), make_uint2(v4[0] | v4[1] << 16, v4[2] | v4[3] << 16));
+            __stcs(reinterpret_cast<float4 *>(param + at), make_float4(p[0], p[1], p[2], p[3]));
+            __stcs(reinterpret_cast<float4 *>(param + at) + 1, make_float4(p[4], p[5], p[6], p[7]));
+            if constexpr (!std::is_same<C, None>::value)
+                __stcs(reinterpret_cast<uint4 *>(static_cast<C *>(e.copy) + start + at),
+                       make_uint4(Elem<C>::narrow2(p[0], p[1]), Elem<C>::narrow2(p[2], p[3]),
+                                  Elem<C>::narrow2(p[4], p[5]), Elem<C>::narrow2(p[6], p[7])));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int w = base + j * 32 + lane;
+                const unsigned long long two = mix64(key + static_cast<unsigned long long>(static_cast<unsigned int>(w) / 2) * kGolden);
+                quantise(j, static_cast<unsigned int>((w & 1) != 0 ? two >> 32 : two));
+                if (w >= left) continue;
+                mc[w] = static_cast<unsigned char>(narrow_codes(m[j], 0.0f) & 0xff);
+                vc[w] = static_cast<unsigned char>(narrow_codes(v[j], 0.0f) & 0xff);
+                __stcs(param + w, p[j]);
+                if constexpr (!std::is_same<C, None>::value) store_one(static_cast<C *>(e.copy) + start + w, p[j]);
+            }
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <class G>
+__device__ __forceinline__ void eight_chunk_of(const AdamwEntry &e, const Scalars &s, float f, float keep,
+                                               unsigned long long key, long long start, int blocks, char *mine) {
+    if (e.copy_elem == ELEM_BF16)
+        eight_chunk<G, __nv_bfloat16>(e, s, f, keep, key, start, blocks, mine);
+    else if (e.copy_elem == ELEM_F16)
+        eight_chunk<G, __half>(e, s, f, keep, key, start, blocks, mine);
+    else
+        eight_chunk<G, None>(e, s, f, keep, key, start, blocks, mine);
 }
 
 // A warp for each block of 256, `blocks` of them one after the other, whose
-// vectors the asynchronous copies bring to shared memory two blocks ahead:
-// issue slots and DRAM bind about alike (89 instructions an element, with the
-// block's and then the next one's loads in registers: 735 and 661 us for 1.9e8
-// parameters with FP16 gradients and copies, 458 us of DRAM).
+// vectors asynchronous copies bring to shared memory two blocks ahead.  Issue
+// slots and DRAM bind about alike.
 template <int N>
 __global__ void __launch_bounds__(kAdamwThreads, 4)
     adamw8_kernel(const __grid_constant__ Table<AdamwEntry, N> t, Scalars s, int blocks) {
@@ -481,133 +610,14 @@ __global__ void __launch_bounds__(kAdamwThreads, 4)
     const unsigned long long key =
         mix64(mix64(s.seed + static_cast<unsigned long long>(s.step) * kGolden) +
               static_cast<unsigned long long>(e.index + 1) * kGolden);
-    const int lane = threadIdx.x & 31;
-    unsigned char *mc = static_cast<unsigned char *>(e.m), *vc = static_cast<unsigned char *>(e.v);
-    const long long first = static_cast<long long>(blockIdx.x - t.first[i]) * blocks * kEightWarps + (threadIdx.x >> 5);
-    auto is_whole = [&](long long block) { return e.vectors != 0 && (block + 1) * kStateBlock <= e.n; };
+    const long long start = static_cast<long long>(blockIdx.x - t.first[i]) * blocks * (kEightWarps * kStateBlock);
     char *mine = room[threadIdx.x >> 5];
-    const bool wide = e.grad_elem == ELEM_F32;
-    const int stages = wide ? 2 : 3, size = wide ? 2560 : 2048;
-    // a group for each block of this warp, empty where there is none to copy
-    auto fetch = [&](int k, int stage) {
-        const long long block = first + static_cast<long long>(k) * kEightWarps;
-        if (k < blocks && is_whole(block)) fetch_eight(e, block, lane, mine + stage * size);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    for (int k = 0; k < stages - 1; ++k) fetch(k, k);
-    int stage = 0;
-    float ms = 0.0f, vs = 0.0f;
-    if (first * kStateBlock < e.n) {
-        ms = __ldcs(e.m_scale + first);
-        vs = __ldcs(e.v_scale + first);
-    }
-    for (int k = 0; k < blocks; ++k) {
-        const long long block = first + static_cast<long long>(k) * kEightWarps, base = block * kStateBlock;
-        const long long at = base + lane * 8;
-        if (base >= e.n) break;
-        const bool whole = is_whole(block);
-        fetch(k + stages - 1, stage == 0 ? stages - 1 : stage - 1);   // the stage read last
-        if (wide)
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else
-            asm volatile("cp.async.wait_group 2;" ::: "memory");
-        __syncwarp();
-        Eight r;
-        if (whole)
-            read_stage(e, lane, mine + stage * size, r);
-        else
-            read_elements(e, base, lane, r);
-        __syncwarp();   // read, before the stage is written again
-        stage = stage + 1 == stages ? 0 : stage + 1;
-        const float mscale_old = ms, vscale_old = vs;
-        const long long following = block + kEightWarps;
-        if (k + 1 < blocks && following * kStateBlock < e.n) {
-            ms = __ldcs(e.m_scale + following);
-            vs = __ldcs(e.v_scale + following);
-        }
-        // two elements at a time
-        float m[8], v[8], mtop = 0.0f, vtop = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const float2 mcode = widen_codes(r.m[j / 4] >> (8 * (j & 3)) & 0xffff);
-            const float2 vcode = widen_codes(r.v[j / 4] >> (8 * (j & 3)) & 0xffff);
-            const F2 g2 = mul2(pack(r.g[j], r.g[j + 1]), both(f));
-            const F2 m2 = fma2(mul2(pack(mcode.x, mcode.y), both(mscale_old)), both(s.beta1), mul2(g2, both(s.rest1)));
-            const F2 root = mul2(pack(vcode.x, vcode.y), both(vscale_old));
-            const F2 v2 = fma2(mul2(root, root), both(s.beta2), mul2(mul2(g2, g2), both(s.rest2)));
-            unpack(m2, m[j], m[j + 1]);
-            unpack(v2, v[j], v[j + 1]);
-            v[j] = root_of(v[j]);
-            v[j + 1] = root_of(v[j + 1]);
-            const F2 below = fma2(pack(v[j], v[j + 1]), both(s.root), both(s.eps));
-            float d0, d1;
-            unpack(below, d0, d1);
-            const F2 step = mul2(m2, pack(reciprocal(d0), reciprocal(d1)));
-            unpack(fma2(step, both(-s.rate), mul2(pack(r.p[j], r.p[j + 1]), both(keep))), r.p[j], r.p[j + 1]);
-            mtop = max_abs(mtop, m[j], m[j + 1]);
-            vtop = max_abs(vtop, v[j], v[j + 1]);
-        }
-        const BlockScale mscale = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
-        const BlockScale vscale = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)));
-        auto quantise = [&](int j, unsigned int bits) {
-            const float size = round_at_random(fabsf(m[j]), bits & 0xffff);
-            m[j] = copysignf(size, m[j]);
-            const float q = round_at_random(v[j], bits >> 16);
-            v[j] = v[j] > 0.0f ? fmaxf(q, 0.001953125f) : q;   // a root that is not zero stays so
-        };
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            unpack(mul2(pack(m[j], m[j + 1]), both(mscale.inverse)), m[j], m[j + 1]);
-            unpack(mul2(pack(v[j], v[j + 1]), both(vscale.inverse)), v[j], v[j + 1]);
-        }
-        if (whole) {   // the two elements of a pair are one lane's
-            const unsigned long long at_pair = key + static_cast<unsigned long long>((at >> 1) + 1) * kGolden;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const unsigned long long two = mix64(at_pair + static_cast<unsigned long long>(j) * kGolden);
-                quantise(2 * j, static_cast<unsigned int>(two));
-                quantise(2 * j + 1, static_cast<unsigned int>(two >> 32));
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const long long w = base + j * 32 + lane;
-                const unsigned long long two = mix64(key + static_cast<unsigned long long>((w >> 1) + 1) * kGolden);
-                quantise(j, static_cast<unsigned int>((w & 1) != 0 ? two >> 32 : two));
-            }
-        }
-        if (lane == 0) {
-            e.m_scale[block] = mscale.scale;
-            e.v_scale[block] = vscale.scale;
-        }
-        if (whole) {
-            unsigned int mw[4], vw[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                mw[j] = narrow_codes(m[2 * j], m[2 * j + 1]);
-                vw[j] = narrow_codes(v[2 * j], v[2 * j + 1]);
-            }
-            __stcs(reinterpret_cast<uint2 *>(mc + at), make_uint2(mw[0] | mw[1] << 16, mw[2] | mw[3] << 16));
-            __stcs(reinterpret_cast<uint2 *>(vc + at), make_uint2(vw[0] | vw[1] << 16, vw[2] | vw[3] << 16));
-            __stcs(reinterpret_cast<float4 *>(e.param + at), make_float4(r.p[0], r.p[1], r.p[2], r.p[3]));
-            __stcs(reinterpret_cast<float4 *>(e.param + at) + 1, make_float4(r.p[4], r.p[5], r.p[6], r.p[7]));
-            if (e.copy_elem >= 0)
-                __stcs(reinterpret_cast<uint4 *>(static_cast<unsigned short *>(e.copy) + at),
-                       make_uint4(narrow_pair(e.copy_elem, r.p[0], r.p[1]), narrow_pair(e.copy_elem, r.p[2], r.p[3]),
-                                  narrow_pair(e.copy_elem, r.p[4], r.p[5]), narrow_pair(e.copy_elem, r.p[6], r.p[7])));
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const long long w = base + j * 32 + lane;
-                if (w >= e.n) continue;
-                mc[w] = static_cast<unsigned char>(narrow_codes(m[j], 0.0f) & 0xff);
-                vc[w] = static_cast<unsigned char>(narrow_codes(v[j], 0.0f) & 0xff);
-                __stcs(e.param + w, r.p[j]);
-                if (e.copy_elem >= 0) store_copy(e.copy, e.copy_elem, w, r.p[j]);
-            }
-        }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (e.grad_elem == ELEM_F32)
+        eight_chunk_of<float>(e, s, f, keep, key, start, blocks, mine);
+    else if (e.grad_elem == ELEM_BF16)
+        eight_chunk_of<__nv_bfloat16>(e, s, f, keep, key, start, blocks, mine);
+    else
+        eight_chunk_of<__half>(e, s, f, keep, key, start, blocks, mine);
 }
 
 // ---- launches ---------------------------------------------------------------------------
@@ -635,7 +645,11 @@ cudaError_t launch_norm_table(const NormTensor *t, int count, double *partial, i
 }
 
 // Elements of a chunk: as many as leave kWantedChunks of them, in 1, 2, 4 .. `most`
-// steps of the smallest (few elements: latency counts).
+// steps of the smallest (few elements: latency counts).  At most 2048 in FP32
+// and 8192 with 8-bit states: short CTAs that follow one another keep the
+// accesses in the order of the memory (1.2e9 parameters in FP32: 4.93 ms with
+// 1024, 4.75 with 2048, 4.81 with 4096, 4.93 with 8192; 1.9e8 with 8 bits: 625
+// us with 2048, 522 with 8192, 533 with 16384, 550 with 32768).
 constexpr long long kWantedChunks = 152 * 16;
 long long chunk_of(long long elements, long long smallest, int most, int *steps) {
     *steps = 1;
@@ -650,8 +664,8 @@ cudaError_t launch_adamw_table(const AdamwTensor *t, int count, int index, const
     int used = 0, steps = 0;
     long long chunks = 0, elements = 0;
     for (int i = 0; i < count; ++i) elements += t[i].n;
-    const long long chunk = c.eight ? chunk_of(elements, kEightWarps * kStateBlock, 8, &steps)
-                                    : chunk_of(elements, kAdamwGroup, 4, &steps);
+    const long long chunk = c.eight ? chunk_of(elements, kEightWarps * kStateBlock, kEightMost, &steps)
+                                    : chunk_of(elements, kAdamwGroup, 2, &steps);
     for (int i = 0; i < count; ++i) {
         const AdamwTensor &a = t[i];
         if (a.n == 0) continue;
