@@ -92,109 +92,129 @@ cudaError_t launch_lookup(const EmbeddingArgs &a, cudaStream_t stream) {
 
 // ---- gradient: few rows ------------------------------------------------------------
 
-// CTA (i, s): the rows of token[i], if i is the first of them, in slices s, s +
-// gridDim.y .. of 32 windows.  All tokens are in the CTA's registers at once.
+// CTA (i, s): the rows of token[i], if i is the first of them; PER tokens of all
+// rows in each thread's registers.  A token of many rows: each CTA has slice s
+// of 32 windows, its warps parts of the rows.  One of a few: the CTAs of the
+// first slices have a slice for each warp, and the others leave.
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32, kMostFew = 2048;
-constexpr int kFewPer = kMostFew / kFewThreads;
 
-template <class T, class D, bool VEC>
+template <class T, class D, bool VEC, int PER>
 __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const EmbeddingArgs a) {
     constexpr int V = 16 / sizeof(T), U = 4;
-    __shared__ unsigned short list[kMostFew];
-    __shared__ int found[kFewPer * kFewWarps];   // hits of each 32 tokens; then hits before them
+    __shared__ unsigned short list[kFewThreads * PER];
+    __shared__ int found[PER * kFewWarps];   // hits of each 32 tokens; then hits before them
     __shared__ int count;
     __shared__ float part[kFewWarps][32][V + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = blockIdx.x;
     const long long t = __ldg(a.tokens + i);
+    unsigned int mask[PER];
+    bool first = true;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int j = k * kFewThreads + tid;
+        mask[k] = j < a.rows && __ldg(a.tokens + j) == t;
+    }
     const int token = t == a.ignore || t < 0 || t >= a.vocab ? -1 : static_cast<int>(t);
     if (token < 0) {
         if (tid == 0 && blockIdx.y == 0) token_row(a, t);
         return;
     }
-    unsigned int mask[kFewPer];
-    bool first = true;
 #pragma unroll
-    for (int k = 0; k < kFewPer; ++k) {
-        const int j = k * kFewThreads + tid;
-        mask[k] = j < a.rows && __ldg(a.tokens + j) == t;
-    }
-#pragma unroll
-    for (int k = 0; k < kFewPer; ++k) {
+    for (int k = 0; k < PER; ++k) {
         first = first && !(mask[k] != 0 && k * kFewThreads + tid < i);
         mask[k] = __ballot_sync(0xffffffffu, mask[k] != 0);
         if (lane == 0) found[k * kFewWarps + warp] = __popc(mask[k]);
     }
     if (!__syncthreads_and(first)) return;
-    if (warp == 0) {
-        static_assert(kFewPer * kFewWarps == 64, "two for each lane");
-        const int one = found[2 * lane], two = found[2 * lane + 1];
-        int sum = one + two;
+    int n = 0;
+    if constexpr (PER == 1) {
+        int before = 0;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += up;
+        for (int w = 0; w < kFewWarps; ++w) {
+            const int c = found[w];
+            before += w < warp ? c : 0;
+            n += c;
         }
-        found[2 * lane] = sum - one - two;
-        found[2 * lane + 1] = sum - two;
-        if (lane == 31) count = sum;
+        if (mask[0] >> lane & 1)
+            list[before + __popc(mask[0] & ((1u << lane) - 1))] = static_cast<unsigned short>(tid);
+    } else {
+        if (warp == 0) {
+            static_assert(PER * kFewWarps == 64, "two for each lane");
+            const int one = found[2 * lane], two = found[2 * lane + 1];
+            int sum = one + two;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += up;
+            }
+            found[2 * lane] = sum - one - two;
+            found[2 * lane + 1] = sum - two;
+            if (lane == 31) count = sum;
+        }
+        __syncthreads();
+        n = count;
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            if (mask[k] >> lane & 1)
+                list[found[k * kFewWarps + warp] + __popc(mask[k] & ((1u << lane) - 1))] =
+                    static_cast<unsigned short>(k * kFewThreads + tid);
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kFewPer; ++k)
-        if (mask[k] >> lane & 1)
-            list[found[k * kFewWarps + warp] + __popc(mask[k] & ((1u << lane) - 1))] =
-                static_cast<unsigned short>(k * kFewThreads + tid);
-    __syncthreads();
+    const bool split = n > kFewWarps / 2;
+    const int slice = split ? blockIdx.y : blockIdx.y * kFewWarps + warp;
     D *dst = static_cast<D *>(a.dweight) + static_cast<long long>(token) * a.width;
-    const int phase = VEC ? 0 : window_phase(dst), n = count;
-    const int windows = windows_of<T>(a.width, VEC), slices = (windows + 31) / 32;
+    const int phase = VEC ? 0 : window_phase(dst);
+    const int windows = windows_of<T>(a.width, VEC);
+    if (!split && static_cast<int>(blockIdx.y) * kFewWarps * 32 >= windows) return;
+    __syncthreads();
     const Bounds bounds = bounds_of<T>(a.dout, a.rows, a.width);
-    // each warp sums a contiguous part of the list
-    const int from = n * warp / kFewWarps, to = n * (warp + 1) / kFewWarps;
-    for (int slice = blockIdx.y; slice < slices; slice += gridDim.y) {
-        const int at = (slice * 32 + lane) * V - phase;
-        const bool in = slice * 32 + lane < windows;
-        float sum[V] = {};
-        for (int k = from; k < to; k += U) {
-            RawWindow<VEC> raw[U];
-            const T *row[U];
+    const int from = split ? n * warp / kFewWarps : 0, to = split ? n * (warp + 1) / kFewWarps : n;
+    const int at = (slice * 32 + lane) * V - phase;
+    const bool in = slice * 32 + lane < windows;
+    float sum[V] = {}, old[V] = {};
+    if (a.add && in && (!split || warp == 0)) read_window<D, V, VEC>(dst, at, a.width, old);
+    for (int k = from; k < to; k += U) {
+        RawWindow<VEC> raw[U];
+        const T *row[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                row[u] = static_cast<const T *>(a.dout) + static_cast<long long>(list[min(k + u, to - 1)]) * a.width;
-                raw[u] = fetch_window<T, VEC>(row[u], at, bounds, in && k + u < to);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (!in || k + u >= to) continue;
-                float v[V];
-                widen_vec<T>(join_window<T, VEC>(raw[u], row[u], at, a.width, bounds, true), v);
-#pragma unroll
-                for (int e = 0; e < V; ++e) sum[e] += v[e];
-            }
+        for (int u = 0; u < U; ++u) {
+            row[u] = static_cast<const T *>(a.dout) + static_cast<long long>(list[min(k + u, to - 1)]) * a.width;
+            raw[u] = fetch_window<T, VEC>(row[u], at, bounds, in && k + u < to);
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!in || k + u >= to) continue;
+            float v[V];
+            widen_vec<T>(join_window<T, VEC>(raw[u], row[u], at, a.width, bounds, true), v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[e] += v[e];
+        }
+    }
+    if (split) {
 #pragma unroll
         for (int e = 0; e < V; ++e) part[warp][lane][e] = sum[e];
         __syncthreads();
-        if (warp == 0 && in) {
-            float old[V] = {};
-            if (a.add) read_window<D, V, VEC>(dst, at, a.width, old);
+        if (warp != 0) return;
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                sum[e] = 0.0f;
+        for (int e = 0; e < V; ++e) {
+            sum[e] = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kFewWarps; ++w) sum[e] += part[w][lane][e];
-                sum[e] = fmaf(sum[e], a.scale, old[e]);
-            }
-            store_window<D, V, VEC>(dst, at, a.width, sum);
+            for (int w = 0; w < kFewWarps; ++w) sum[e] += part[w][lane][e];
         }
-        __syncthreads();
     }
+    if (!in) return;
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] = fmaf(sum[e], a.scale, old[e]);
+    store_window<D, V, VEC>(dst, at, a.width, sum);
 }
 
-constexpr long long kFewLooks = 1ll << 40;
-// Few rows: sorting them takes longer than each CTA's look at all tokens.
+// Few rows: each CTA looks at all tokens, 1 to 2 ns a CTA, where ranking them,
+// the sums and the join take 8 to 14 us.  (rows x width, BF16, all tokens
+// different, few | ranked: 256 x 4096 5.6 | 8.9 us, 512 x 1024 6.0 | 10.3, 1024 x
+// 256 5.1 | 10.3, 1024 x 1024 10.3 | 9.8, 512 x 4096 18 | 9.9, 2048 x 256 8.3 |
+// 11.5, of one token 27 | 18.)
 bool few_rows(int rows, int width) {
-    return rows <= kMostFew && static_cast<long long>(rows) * rows * (width / 256 + 1) <= kFewLooks;
+    const long long ctas = static_cast<long long>(rows) * (width / 128 + 1);
+    return rows <= kFewThreads ? ctas <= 16384 : rows <= kMostFew && ctas <= 6000;
 }
 
 // ---- gradient: sorting positions by token --------------------------------------------
@@ -381,6 +401,63 @@ __global__ void __launch_bounds__(kSortThreads)
         }
 }
 
+// Up to kMostRanked positions go to their places at once: the place of i is the
+// number of j with a smaller key, or the same key and j < i.  CTA b counts them
+// for positions 32 b .. 32 b + 31 against all keys in its shared memory.  (The
+// passes above, with three launches, took 15 us more of 5000 rows.)
+constexpr int kMostRanked = 8192, kRankThreads = 256, kRankPer = 4;
+__global__ void __launch_bounds__(kRankThreads)
+    rank_kernel(const EmbeddingArgs a, Pair *out, unsigned int *present) {
+    constexpr int U = 8;
+    __shared__ uint4 keys[kMostRanked / 4];
+    unsigned int *key = reinterpret_cast<unsigned int *>(keys);
+    let_next_start();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int vectors = (a.rows + 127) / 128 * 32;   // of four keys: the same number for each lane
+    for (int begin = tid; begin < vectors * 4; begin += U * kRankThreads) {
+        long long t[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            t[u] = begin + u * kRankThreads < a.rows ? __ldg(a.tokens + begin + u * kRankThreads) : a.ignore;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = begin + u * kRankThreads;
+            if (j >= vectors * 4) continue;
+            const bool valid = t[u] != a.ignore && t[u] >= 0 && t[u] < a.vocab;
+            if (blockIdx.x == 0 && !valid && t[u] != a.ignore) token_row(a, t[u]);
+            key[j] = j >= a.rows ? ~0u : valid ? static_cast<unsigned int>(t[u]) : static_cast<unsigned int>(a.vocab);
+        }
+    }
+    __syncthreads();
+    const int base = blockIdx.x * 32, first = base + warp * kRankPer;
+    unsigned int own[kRankPer];
+    int count[kRankPer];
+#pragma unroll
+    for (int q = 0; q < kRankPer; ++q) {
+        own[q] = key[first + q];   // (behind the last row: not used)
+        // of this CTA's 32 positions, those before it with the same key
+        count[q] = lane < warp * kRankPer + q && key[base + lane] == own[q];
+    }
+#pragma unroll 4
+    for (int v = lane; v < vectors; v += 32) {
+        const uint4 k = keys[v];
+        const unsigned int more = v < base / 4;   // before this CTA's positions equal keys count
+#pragma unroll
+        for (int q = 0; q < kRankPer; ++q) {
+            const unsigned int bound = own[q] + more;
+            count[q] += (k.x < bound) + (k.y < bound) + (k.z < bound) + (k.w < bound);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kRankPer; ++q) {
+        const int place = __reduce_add_sync(0xffffffffu, count[q]);
+        if (lane != q || first + q >= a.rows) continue;
+        out[place] = Pair{own[q], static_cast<unsigned int>(first + q)};
+        if (present != nullptr && own[q] < static_cast<unsigned int>(a.vocab))
+            atomicOr(present + (own[q] >> 5), 1u << (own[q] & 31));
+    }
+}
+
 // ---- gradient: sums of the sorted list ------------------------------------------------
 
 constexpr int kSumThreads = 128;
@@ -428,23 +505,29 @@ template <class T, class D, bool VEC>
 __global__ void __launch_bounds__(kSumThreads)
     sum_kernel(const EmbeddingArgs a, const Pair *pairs, float *partial, int run, int runs, int lanes,
                int slices, int ctas, const Fill fill) {
-    constexpr int V = 16 / sizeof(T), U = VEC ? 8 : 4;
+    constexpr int V = 16 / sizeof(T), U = VEC ? 8 : 2;
     let_next_start();
     wait_for_previous();
-    if (static_cast<int>(blockIdx.x) >= ctas) {
-        fill_rows<D, VEC, kSumThreads>(a, fill, blockIdx.x - ctas);
+    // (fillers evenly between the CTAs that sum: 32768 x 4096 BF16 239 us, behind them 220)
+    const int cta = blockIdx.x;
+    if (cta >= ctas) {
+        fill_rows<D, VEC, kSumThreads>(a, fill, cta - ctas);
         return;
     }
     const int lane = threadIdx.x & (lanes - 1);
-    const int r = blockIdx.x / slices * (kSumThreads / lanes) + threadIdx.x / lanes;
+    const int r = cta / slices * (kSumThreads / lanes) + threadIdx.x / lanes;
     const int windows = windows_of<T>(a.width, VEC);
-    const int j = blockIdx.x % slices * lanes + lane;
+    const int j = cta % slices * lanes + lane;
     if (r >= runs || j >= windows) return;
     const int begin = r * run, end = min(begin + run, a.rows);
     const unsigned int none = a.vocab;
-    unsigned int cur = __ldg(&pairs[begin].key);
+    Pair next[U];   // the pairs of the rows after these
+#pragma unroll
+    for (int u = 0; u < U; ++u) next[u] = begin + u < end ? pairs[begin + u] : Pair{none, 0};
+    const unsigned int prior = begin > 0 ? __ldg(&pairs[begin - 1].key) : ~0u;
+    unsigned int cur = next[0].key;
     if (cur == none) return;
-    bool here = begin == 0 || __ldg(&pairs[begin - 1].key) != cur;
+    bool here = prior != cur;
     const T *dout = static_cast<const T *>(a.dout);
     const Bounds bounds = bounds_of<T>(dout, a.rows, a.width);
     auto window_at = [&](unsigned int key) {   // (any place for no token)
@@ -458,8 +541,8 @@ __global__ void __launch_bounds__(kSumThreads)
         RawWindow<VEC> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            p[u] = Pair{none, 0};
-            if (k + u < end) p[u] = pairs[k + u];
+            p[u] = next[u];
+            next[u] = k + U + u < end ? pairs[k + U + u] : Pair{none, 0};
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -641,9 +724,11 @@ cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
                 a.dweight, 0, static_cast<size_t>(a.vocab) * a.width * sizeof(D), stream);
             if (err != cudaSuccess) return err;
         }
-        const int slices = (windows + 31) / 32;   // two to a CTA where there are many
-        const int parts = static_cast<long long>(a.rows) * slices > 4096 ? (slices + 1) / 2 : slices;
-        few_rows_kernel<T, D, VEC><<<dim3(a.rows, parts), kFewThreads, 0, stream>>>(a);
+        const dim3 grid(a.rows, (windows + 31) / 32);
+        if (a.rows <= kFewThreads)
+            few_rows_kernel<T, D, VEC, 1><<<grid, kFewThreads, 0, stream>>>(a);
+        else
+            few_rows_kernel<T, D, VEC, 8><<<grid, kFewThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
     const SortPlan s = sort_plan(a.rows, a.vocab);
@@ -659,7 +744,10 @@ cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
         err = cudaMemsetAsync(present, 0, (static_cast<size_t>(a.vocab) + 31) / 32 * sizeof(int), stream);
         if (err != cudaSuccess) return err;
     }
-    if (s.items == 8)
+    const int passes = a.rows <= kMostRanked ? 0 : s.passes;
+    if (passes == 0)
+        rank_kernel<<<(a.rows + 31) / 32, kRankThreads, 0, stream>>>(a, list[0], present);
+    else if (s.items == 8)
         digits_kernel<8><<<s.tiles, kSortThreads, 0, stream>>>(a, counts, present, s.bits, s.passes);
     else
         digits_kernel<32><<<s.tiles, kSortThreads, 0, stream>>>(a, counts, present, s.bits, s.passes);
@@ -675,20 +763,20 @@ cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
     fill.each = 32768 / (fill_windows * 16) + kSumThreads * kJoinParts / fill.lanes;
     const long long rows = present != nullptr ? a.vocab : 0;
     long long share = (64ll << 20) / row_bytes + 1;
-    if (share > rows / (s.passes + 2)) share = rows / (s.passes + 2);
+    if (share > rows / (passes + 2)) share = rows / (passes + 2);
     auto fillers = [&](long long to) {   // of the rows up to `to`
         fill.from = fill.to;
         fill.to = static_cast<int>(to);
         return (fill.to - fill.from + fill.each - 1) / fill.each;
     };
-    for (int p = 0; p < s.passes && err == cudaSuccess; ++p) {
+    for (int p = 0; p < passes && err == cudaSuccess; ++p) {
         const int n = fillers(share * (p + 1));
         err = s.items == 8
             ? launch_pass<D, VEC, 8>(a, s, p, list[(p + 1) & 1], list[p & 1], counts, fill, n, stream)
             : launch_pass<D, VEC, 32>(a, s, p, list[(p + 1) & 1], list[p & 1], counts, fill, n, stream);
     }
     if (err != cudaSuccess) return err;
-    const Pair *sorted = list[(s.passes - 1) & 1];
+    const Pair *sorted = list[passes == 0 ? 0 : (passes - 1) & 1];
     int lanes = 8;
     while (lanes < kSumThreads && lanes < windows) lanes *= 2;
     const int per = kSumThreads / lanes, slices = (windows + lanes - 1) / lanes;
