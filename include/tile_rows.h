@@ -664,8 +664,7 @@ int tile_grad_norm(const tile_tensor_t *tensors, int count, float scale, float m
  * is not finite becomes NaN.
  *
  * Everything else is FP32; exp_avg and exp_avg_sq are rounded after each product
- * and sum (TILE_STATE_F32) or fused (TILE_STATE_E4M3, where values of
- * exp_avg_sq below 2^-126 are nothing).  Pointers: aligned to their element; the 16-byte grid is the fastest.  No written range may overlap another
+ * and sum.  Pointers: aligned to their element; the 16-byte grid is the fastest.  No written range may overlap another
  * range of the call (TILE_ERR_ALIAS): a tensor is listed once.  n >= 0, no limit
  * on count.  TILE_ERR_EPS for betas outside [0, 1), eps that is not finite or
  * below 2^-126, an lr or weight_decay that is not finite; TILE_ERR_SHAPE for n < 0,

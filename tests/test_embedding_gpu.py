@@ -102,7 +102,7 @@ def test_lookup_of_ignored_and_bad_tokens():
     assert torch.isnan(out[0]).all() and (out[1] == 0).all()
 
 
-def check_gradient(token, dout, scale, got, old=None, vocab=None):
+def check_gradient(token, dout, scale, got, old=None):
     vocab, width = got.shape
     keep = (token >= 0) & (token < vocab) & (token != IGNORE)
     t, d = token[keep], dout[keep].double()
@@ -136,8 +136,17 @@ def tokens(rows, vocab, kind, seed=5):
 
 
 SHAPES = [(1, 1, 1), (1, 64, 7), (48, 1024, 200), (300, 1537, 100), (2048, 65, 5000),
-          (2049, 65, 5000), (2500, 8, 1), (5000, 257, 513), (4097, 1000, 512), (20000, 24, 70000),
+          (2049, 65, 5000), (2500, 8, 1), (5000, 257, 513), (4097, 1000, 512), (256, 8200, 40),
+          (257, 64, 3000), (8192, 40, 900), (8193, 40, 900), (20000, 24, 70000), (9000, 8, 300001),
           (140000, 16, 300)]
+
+
+@pytest.mark.parametrize("rows,vocab,kind", [(1 << 20, 100000, "rare"), (1 << 20, 3, "uniform"),
+                                             (1 << 24, 100000, "padded")])
+def test_gradient_of_many_rows(rows, vocab, kind):
+    token = tokens(rows, vocab, kind)
+    dout = normal(3, rows, 3)
+    check_gradient(token, dout, 0.7, tile.embedding_backward(token, dout, vocab, scale=0.7))
 
 
 @pytest.mark.parametrize("kind", ["uniform", "one", "padded", "rare", "none"])

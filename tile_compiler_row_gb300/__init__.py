@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import itertools
+import operator
 import os
 import struct
 
@@ -1142,14 +1143,15 @@ def tile_embedding_backward_workspace_bytes(rows, width, vocab):
 def tile_embedding_backward(tokens, dout, dweight, workspace, scale=1.0, ignore_index=-100,
                             accumulate=False, stream=None):
     """dweight = (or, with ``accumulate``, +=) the gradient of
-    ``tile_embedding``'s weight; dweight may be float32 for 16-bit rows."""
+    ``tile_embedding``'s weight; dweight may be float32 for 16-bit rows, and
+    workspace None where none is needed (0 bytes)."""
     code, dev = _rows_of(dout, "dout")
     into, _ = _rows_of(dweight, "dweight")
     rows, width = dout.shape
     vocab = dweight.shape[0]
     if not _fit_int(rows, width, vocab):
         raise ValueError(f"rows, width and vocab must be below 2^31, not {rows}, {width}, {vocab}")
-    ws, nbytes = _workspace(workspace, dev)
+    ws, nbytes = (None, 0) if workspace is None else _workspace(workspace, dev)
     _call_on(dev, stream, "tile_embedding_backward", code, into,
              _ptr(tokens, "tokens", _I64, (rows,), dev),
              _ptr(dout, "dout", dout.dtype, dout.shape, dev),
@@ -1232,20 +1234,26 @@ def _one(t, name, dtype, dev):
 # list is gone through once by one expression a tensor, and only a tensor that
 # fails it is looked at again for the message.
 
+_DTYPE_OF = operator.attrgetter("dtype")
+
+
 def _columns(tensors, name, types, counts, dev):
-    """(pointers, element counts, type codes) of a list of contiguous CUDA
-    tensors on device index ``dev``, of types that ``types`` has codes for and
-    of these element counts (None: any)."""
+    """(pointers, element counts, types) of a list of contiguous CUDA tensors
+    on device index ``dev``, of types that ``types`` has codes for and of these
+    element counts (None: any)."""
+    if hasattr(tensors, "dtype"):
+        raise TypeError(f"{name} must be a list of tensors")
     if counts is not None and len(tensors) != len(counts):
         raise ValueError(f"{name} must have {len(counts)} tensors like the other lists, "
                          f"not {len(tensors)}")
     try:
         sizes = [t.numel() for t in tensors]
-        codes = [types[t.dtype] for t in tensors]
+        kinds = list(map(_DTYPE_OF, tensors))
         pointers = [t.data_ptr() for t in tensors if t.get_device() == dev and t.is_contiguous()]
-        if len(pointers) == len(codes) and (counts is None or sizes == counts):
-            return pointers, sizes, codes
-    except (AttributeError, KeyError):
+        if types.keys() >= set(kinds) and len(pointers) == len(kinds) and \
+                (counts is None or sizes == counts):
+            return pointers, sizes, kinds
+    except AttributeError:
         pass
     _list_of_tensors(tensors, name)
     for i, t in enumerate(tensors):
@@ -1290,11 +1298,11 @@ def tile_grad_norm(grads, out, workspace, scale=1.0, max_norm=None, stream=None)
     bfloat16 or float16, in any mix); see include/tile_rows.h."""
     if _F32 is None:
         _kinds()
-    _list_device(grads, "grads")
-    dev, count = _device_index(out, "out"), len(grads)
-    table = _records("2qi4x", count, _columns(grads, "grads", _CODES, None, dev))
+    dev = _device_index(out, "out")
+    p, n, kinds = _columns(grads, "grads", _CODES, None, dev)
+    table = _records("2qi4x", len(p), (p, n, [_CODES[k] for k in kinds]))
     ws, nbytes = _workspace(workspace, dev)
-    _call_on(dev, stream, "tile_grad_norm", table, count, scale,
+    _call_on(dev, stream, "tile_grad_norm", table, len(p), scale,
              _INF if max_norm is None else max_norm, _ptr(out, "out", _F32, (2,), dev), ws, nbytes)
 
 
@@ -1330,12 +1338,14 @@ def tile_adamw(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     if copies is not None:
         halves = {k: i for k, i in _CODES.items() if i != 0}
         c, _, copy_kinds = _columns(copies, "copies", halves, n, dev)
+        copy_kinds = [halves[k] for k in copy_kinds]
     decay = [weight_decay] * count if isinstance(weight_decay, (int, float)) else weight_decay
     if len(decay) != count:
         raise ValueError(f"weight_decay must be a number or {count} of them")
     if count == 0:
         return
-    table = _records("8qf2i4x", count, (p, g, m, v, ms, vs, c, n, decay, kinds, copy_kinds))
+    table = _records("8qf2i4x", count, (p, g, m, v, ms, vs, c, n, decay,
+                                        [_CODES[k] for k in kinds], copy_kinds))
     step_at, lr_at = getattr(step, "is_cuda", None), getattr(lr, "is_cuda", None)
     config = TileAdamwConfig(
         lr if lr_at is None else 0.0, betas[0], betas[1], eps,
@@ -1493,8 +1503,9 @@ def embedding_backward(tokens, dout, vocab=None, scale=1.0, ignore_index=-100, d
         raise ValueError("vocab or dweight is needed")
     else:
         dweight = torch.empty(vocab, dout.shape[1], dtype=dtype or dout.dtype, device=dout.device)
-    ws = _scratch(tile_embedding_backward_workspace_bytes(*dout.shape, dweight.shape[0]), dout)
-    tile_embedding_backward(tokens, dout, dweight, ws, scale, ignore_index, add)
+    need = tile_embedding_backward_workspace_bytes(*dout.shape, dweight.shape[0])
+    tile_embedding_backward(tokens, dout, dweight, _scratch(need, dout) if need else None, scale,
+                            ignore_index, add)
     return dweight
 
 

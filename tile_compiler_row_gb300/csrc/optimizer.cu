@@ -120,9 +120,32 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-template <int N>
+// Thread 0's sum over the CTA.
+template <int THREADS>
+__device__ __forceinline__ double cta_sum(double v, double *part) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double total = 0.0;
+    if (threadIdx.x == 0)
+        for (int w = 0; w < THREADS / 32; ++w) total += part[w];
+    return total;
+}
+
+// The norm and the factor.
+__device__ __forceinline__ void finish_norm(double total, float scale, float most, float *out) {
+    const double norm = scale * sqrt(total);
+    out[0] = static_cast<float>(norm);
+    // a norm that is not finite: no factor, and a step that takes it is skipped
+    out[1] = !isfinite(out[0]) ? __int_as_float(0x7fffffff)
+             : norm > most     ? static_cast<float>(scale * (most / norm))
+                               : scale;
+}
+
+// FUSED: the grid is one cluster, whose first CTA joins the partial sums.
+template <int N, bool FUSED>
 __global__ void __launch_bounds__(kNormThreads)
-    norm_kernel(const __grid_constant__ Table<NormEntry, N> t, double *partial) {
+    norm_kernel(const __grid_constant__ Table<NormEntry, N> t, double *partial, float scale, float most, float *out) {
     __shared__ double part[kNormThreads / 32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float sum = 0.0f, cut = 0.0f;   // a thread's sum over its chunks, and what its roundings cut off
@@ -138,13 +161,19 @@ __global__ void __launch_bounds__(kNormThreads)
         sum = to;
     }
     // an infinite sum has no rest
-    const double v = warp_sum(static_cast<double>(sum) + (isfinite(sum) ? static_cast<double>(cut) : 0.0));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-    double total = 0.0;
-    for (int w = 0; w < kNormThreads / 32; ++w) total += part[w];
-    partial[blockIdx.x] = total;
+    const double v = static_cast<double>(sum) + (isfinite(sum) ? static_cast<double>(cut) : 0.0);
+    const double total = cta_sum<kNormThreads>(v, part);
+    if (threadIdx.x == 0) partial[blockIdx.x] = total;
+    if constexpr (FUSED) {
+        __syncthreads();
+        __threadfence();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (blockIdx.x != 0 || threadIdx.x != 0) return;
+        double all = 0.0;
+        for (unsigned int i = 0; i < gridDim.x; ++i) all += __ldcg(partial + i);
+        finish_norm(all, scale, most, out);
+    }
 }
 
 constexpr int kNormJoin = 512;
@@ -154,18 +183,8 @@ __global__ void __launch_bounds__(kNormJoin)
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial sums are written
     double v = 0.0;
     for (int i = threadIdx.x; i < count; i += kNormJoin) v += __ldcg(partial + i);
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-    double total = 0.0;
-    for (int w = 0; w < kNormJoin / 32; ++w) total += part[w];
-    const double norm = scale * sqrt(total);
-    out[0] = static_cast<float>(norm);
-    // a norm that is not finite: no factor, and a step that takes it is skipped
-    out[1] = !isfinite(out[0]) ? __int_as_float(0x7fffffff)
-             : norm > most     ? static_cast<float>(scale * (most / norm))
-                               : scale;
+    const double total = cta_sum<kNormJoin>(v, part);
+    if (threadIdx.x == 0) finish_norm(total, scale, most, out);
 }
 
 // ---- AdamW --------------------------------------------------------------------------
@@ -393,11 +412,14 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
     asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-// To 1 ulp; below 2^-126 nothing.
-__device__ __forceinline__ float root_of(float x) {
-    float d;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
-    return d;
+// Sums of two packed products.  Scalar: the packed addition of packed products
+// came out as one rounding less (a fused multiply-add), against its ".rn".
+__device__ __forceinline__ void add_halves(F2 a, F2 b, float &lo, float &hi) {
+    float a0, a1, b0, b1;
+    unpack(a, a0, a1);
+    unpack(b, b0, b1);
+    lo = __fadd_rn(a0, b0);
+    hi = __fadd_rn(a1, b1);
 }
 __device__ __forceinline__ void copy_async(void *to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
@@ -514,17 +536,16 @@ __device__ __forceinline__ void eight_chunk(const AdamwEntry &e, const Scalars &
             const float2 mcode = widen_codes(mw[j / 4] >> (8 * (j & 3)) & 0xffff);
             const float2 vcode = widen_codes(vw[j / 4] >> (8 * (j & 3)) & 0xffff);
             const F2 g2 = mul2(pack(g[j], g[j + 1]), both(f));
-            const F2 m2 = fma2(mul2(pack(mcode.x, mcode.y), m_old), both(s.beta1), mul2(g2, both(s.rest1)));
             const F2 root = mul2(pack(vcode.x, vcode.y), v_old);
-            const F2 v2 = fma2(mul2(root, root), both(s.beta2), mul2(mul2(g2, g2), both(s.rest2)));
-            unpack(m2, m[j], m[j + 1]);
-            unpack(v2, v[j], v[j + 1]);
-            v[j] = root_of(v[j]);
-            v[j + 1] = root_of(v[j + 1]);
+            add_halves(mul2(mul2(pack(mcode.x, mcode.y), m_old), both(s.beta1)), mul2(g2, both(s.rest1)), m[j],
+                       m[j + 1]);
+            add_halves(mul2(mul2(root, root), both(s.beta2)), mul2(mul2(g2, g2), both(s.rest2)), v[j], v[j + 1]);
+            v[j] = __fsqrt_rn(v[j]);
+            v[j + 1] = __fsqrt_rn(v[j + 1]);
             const F2 below = fma2(pack(v[j], v[j + 1]), both(s.root), both(s.eps));
             float d0, d1;
             unpack(below, d0, d1);
-            const F2 step = mul2(m2, pack(reciprocal(d0), reciprocal(d1)));
+            const F2 step = mul2(pack(m[j], m[j + 1]), pack(reciprocal(d0), reciprocal(d1)));
             unpack(fma2(step, both(-s.rate), mul2(pack(p[j], p[j + 1]), both(keep))), p[j], p[j + 1]);
             mtop = max_abs(mtop, m[j], m[j + 1]);
             vtop = max_abs(vtop, v[j], v[j + 1]);
@@ -626,8 +647,12 @@ constexpr int kFewTensors = 32;   // a table this short is a kernel argument of 
 
 bool on_grid(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
+constexpr int kNormCluster = 8, kNormFew = 32;   // CTAs of a cluster, and chunks that one takes
+
+// out != NULL: the norm too, where there are few chunks (*programs is 0 then).
 template <int N>
-cudaError_t launch_norm_table(const NormTensor *t, int count, double *partial, int *programs, cudaStream_t stream) {
+cudaError_t launch_norm_table(const NormTensor *t, int count, double *partial, int *programs, float scale,
+                              float most, float *out, cudaStream_t stream) {
     Table<NormEntry, N> table;
     table.count = count;
     long long chunks = 0;
@@ -639,9 +664,23 @@ cudaError_t launch_norm_table(const NormTensor *t, int count, double *partial, i
         if (chunks > 0x7fffffff) return cudaErrorInvalidValue;
     }
     table.first[count] = static_cast<int>(chunks);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.blockDim = dim3(kNormThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (out != nullptr && chunks <= kNormFew) {
+        cfg.gridDim = dim3(static_cast<unsigned int>(chunks < kNormCluster ? chunks : kNormCluster));
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cfg.gridDim.x;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+        *programs = 0;
+        return cudaLaunchKernelEx(&cfg, norm_kernel<N, true>, table, partial, scale, most, out);
+    }
     *programs = chunks < kNormPrograms ? static_cast<int>(chunks) : kNormPrograms;
-    norm_kernel<N><<<*programs, kNormThreads, 0, stream>>>(table, partial);
-    return cudaGetLastError();
+    cfg.gridDim = dim3(*programs);
+    return cudaLaunchKernelEx(&cfg, norm_kernel<N, false>, table, partial, scale, most, out);
 }
 
 // Elements of a chunk: as many as leave kWantedChunks of them, in 1, 2, 4 .. `most`
@@ -701,13 +740,14 @@ cudaError_t launch_grad_norm(const NormTensor *t, int count, float scale, float 
                              float *out, void *ws, cudaStream_t stream) {
     double *partial = static_cast<double *>(ws);
     int total = 0;
+    float *whole = count > 0 && count <= kNormTensors ? out : nullptr;   // one launch of sums at most
     for (int i = 0; i < count; i += kNormTensors) {
         const int n = count - i < kNormTensors ? count - i : kNormTensors;
         int programs = 0;
         const cudaError_t err = n <= kFewTensors
-            ? launch_norm_table<kFewTensors>(t + i, n, partial + total, &programs, stream)
-            : launch_norm_table<kNormTensors>(t + i, n, partial + total, &programs, stream);
-        if (err != cudaSuccess) return err;
+            ? launch_norm_table<kFewTensors>(t + i, n, partial + total, &programs, scale, max_norm, whole, stream)
+            : launch_norm_table<kNormTensors>(t + i, n, partial + total, &programs, scale, max_norm, whole, stream);
+        if (err != cudaSuccess || (whole != nullptr && programs == 0)) return err;
         total += programs;
     }
     cudaLaunchConfig_t cfg = {};

@@ -6,7 +6,8 @@ achieved bandwidth from the op's algorithmic bytes (each input element read
 once, each output element written once), reported against the measured HBM
 copy bandwidth.  The linear cross entropy (at most 4096 of the rows, against a
 vocabulary of ``--vocab`` entries) is reported by its matrix products, against
-the measured BF16 rate.  Inputs are uniform random device tensors (timing
+the measured BF16 rate; the embedding, the policy loss, the gradient norm and the
+AdamW step by the bytes they cannot do without.  Inputs are uniform random device tensors (timing
 only; parity is covered by the GPU tests).  The default 65536 x 4096 shape keeps
 every working set far above the 129 MB L2.
 
@@ -159,6 +160,36 @@ def main(argv=None):
         losses[f"linear_cross_entropy_backward_{kind}"] = (
             lambda xs=xs, w=w, target=target, lse=lse, dloss=dloss:
                 tile.linear_cross_entropy_backward(xs, w, target, lse, dloss), 3)
+    # the two ends of a training step: name -> (callable, bytes)
+    tokens = torch.randint(args.vocab, (rows,), device="cuda", generator=gen)
+    found = int(tokens.unique().numel())
+    ends = {}
+    for kind, a, o in (("f32", x, y), ("bf16", xb, yb), ("f16", xh, yh)):
+        size = a.element_size()
+        w = a[:args.vocab] if args.vocab <= rows else torch.zeros(args.vocab, width, dtype=a.dtype, device="cuda")
+        dw = torch.empty(args.vocab, width, dtype=a.dtype, device="cuda")
+        ews = torch.empty(tile.tile_embedding_backward_workspace_bytes(rows, width, args.vocab) + 1,
+                          dtype=torch.uint8, device="cuda")
+        ends[f"embedding_{kind}"] = (
+            lambda w=w, o=o: tile.tile_embedding(tokens, w, o), (rows + found) * width * size)
+        ends[f"embedding_backward_{kind}"] = (
+            lambda a=a, dw=dw, ews=ews: tile.tile_embedding_backward(tokens, a, dw, ews),
+            (rows + args.vocab) * width * size)
+        ends[f"grad_norm_{kind}"] = (lambda a=a: tile.grad_norm([a], 1.0), n * size)
+    vec = [torch.rand(rows, device="cuda", generator=gen) for _ in range(4)]
+    offsets = torch.arange(0, rows + 1, max(1, rows // 64), device="cuda")
+    weights = tile.policy_loss(vec[0], vec[1], vec[2], vec[3], offsets=offsets, kl_coef=0.1)[1]
+    dnll = torch.empty(rows, device="cuda")
+    ends["policy_loss"] = (lambda: tile.policy_loss(vec[0], vec[1], vec[2], vec[3], offsets=offsets,
+                                                    kl_coef=0.1), 16 * rows)
+    ends["policy_loss_backward"] = (lambda: tile.tile_policy_loss_backward(
+        vec[0], vec[1], vec[2], weights, dnll, None, vec[3], offsets=offsets, kl_coef=0.1), 20 * rows)
+    # (the parameters are the BF16 case's rows in FP32; the gradients are small)
+    states = {bits: tile.adamw_state([x], bits) for bits in (32, 8)}
+    params, grads, copies = [x.clone()], [xb * 1e-3], [xb.clone()]
+    for bits, per in ((32, 28), (8, 16)):
+        ends[f"adamw_{bits}bit_bf16"] = (
+            lambda bits=bits: tile.adamw(params, grads, **states[bits], step=1, copies=copies), per * n)
     only = set(args.only.split(",")) if args.only else None
     peak, src = measured_hbm_gbs()
     stream = torch.cuda.current_stream()
@@ -182,6 +213,18 @@ def main(argv=None):
         ms = statistics.mean(per)
         gbs = bpe * n / (ms * 1e-3) / 1e9
         res = {"op": name, "rows": rows, "width": width, "bytes_per_elem": bpe,
+               "us_per_call": round(ms * 1e3, 2), "median_us": round(statistics.median(per) * 1e3, 2),
+               "achieved_gbs": round(gbs, 1), "frac_of_copy": round(gbs / peak, 4),
+               "peak": f"{peak} GB/s ({src} HBM copy)"}
+        results.append(res)
+        print(json.dumps(res), flush=True)
+    for name, (fn, nbytes) in ends.items():
+        if only and name not in only:
+            continue
+        per = timed(fn)
+        ms = statistics.mean(per)
+        gbs = nbytes / (ms * 1e-3) / 1e9
+        res = {"op": name, "rows": rows, "width": width, "bytes": nbytes,
                "us_per_call": round(ms * 1e3, 2), "median_us": round(statistics.median(per) * 1e3, 2),
                "achieved_gbs": round(gbs, 1), "frac_of_copy": round(gbs / peak, 4),
                "peak": f"{peak} GB/s ({src} HBM copy)"}
