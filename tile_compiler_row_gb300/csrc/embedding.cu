@@ -464,21 +464,24 @@ constexpr int kSumThreads = 128;
 struct SumPlan {
     int run, runs;   // positions of a run, and how many there are
 };
-// 64 positions a run, fewer where that leaves SMs without a CTA (of 16-byte
-// windows of 2-byte rows); more than 1024 runs would make the partial sums large.
+// 64 positions a run; fewer, down to 8, where that leaves SMs without enough
+// threads (32768 x 1536 BF16, added: 82 us with 64); more where the partial sums
+// would pass 64 MiB.
 SumPlan sum_plan(int rows, int width) {
-    const long long slices = (width / 8 + kSumThreads - 1) / kSumThreads + 1;
+    const long long windows = width / 8 + 1;
+    auto bytes = [&](int run) { return (static_cast<long long>(rows) + run - 1) / run * 8 * (width + 16); };
     SumPlan p;
     p.run = 64;
-    while (p.run > 16 && rows / p.run * slices < 152 * 8 && rows / p.run < 512) p.run /= 2;
-    while ((rows + p.run - 1) / p.run > 1024) p.run *= 2;
+    while (p.run > 8 && rows / p.run * windows < 152 * 1536) p.run /= 2;
+    while (bytes(p.run) > (64ll << 20) && p.run < rows) p.run *= 2;
     p.runs = (rows + p.run - 1) / p.run;
     return p;
 }
 
-// FP32 partial sums [runs][2][windows][V] of tokens that lie in several runs: of
-// a run's first token where it began in an earlier run, and of its last where
-// it began here and goes on.
+// A token belongs to the run that it begins in, which goes on up to as many
+// rows behind its end to finish it.  Longer ones leave FP32 partial sums
+// [runs][2][windows][V]: of a run's first token where it began in an earlier run,
+// and of its last where it began here and goes on.
 template <int V, class F>
 __device__ __forceinline__ F *partial_at(F *partial, int run, int slot, int windows, int j) {
     return partial + ((static_cast<long long>(run) * 2 + slot) * windows + j) * V;
@@ -547,14 +550,27 @@ __global__ void __launch_bounds__(kSumThreads)
     const int j = cta % slices * lanes + lane;
     if (r >= runs || j >= windows) return;
     const int begin = r * run, end = min(begin + run, a.rows);
-    const unsigned int none = a.vocab;
+    const unsigned int none = a.vocab, edge = ~0u;
+    auto key_of = [&](long long k) { return k >= 0 && k < a.rows ? __ldg(&pairs[k].key) : edge; };
+    const unsigned int before = key_of(begin - run - 1ll), prior = key_of(begin - 1ll), front = key_of(begin),
+                       tail = key_of(end - 1ll), after = key_of(end), far = key_of(static_cast<long long>(end) + run);
+    if (front == none) return;
+    // the first token goes on from an earlier run: that run's, if it began in the
+    // one before this and ends here
+    const bool left = prior == front, taken = left && (begin == run || before != front) && after != front;
+    // the last one goes on, began here and ends in the next run: this run's
+    const bool extend = tail != none && after == tail && !(tail == front && left) && far != tail;
+    const int stop = extend ? min(end + run, a.rows) : end;
+    auto pair_at = [&](int k) {   // no token where the row is not this run's
+        Pair p = k < stop ? pairs[k] : Pair{none, 0};
+        if (k >= end ? p.key != tail : taken && p.key == front) p.key = none;
+        return p;
+    };
     Pair next[U];   // the pairs of the rows after these
 #pragma unroll
-    for (int u = 0; u < U; ++u) next[u] = begin + u < end ? pairs[begin + u] : Pair{none, 0};
-    const unsigned int prior = begin > 0 ? __ldg(&pairs[begin - 1].key) : ~0u;
-    unsigned int cur = next[0].key;
-    if (cur == none) return;
-    bool here = prior != cur;
+    for (int u = 0; u < U; ++u) next[u] = pair_at(begin + u);
+    unsigned int cur = taken ? none : front;
+    bool here = !left;
     const T *dout = static_cast<const T *>(a.dout);
     const Bounds bounds = bounds_of<T>(dout, a.rows, a.width);
     auto window_at = [&](unsigned int key) {   // (any place for no token)
@@ -564,14 +580,15 @@ __global__ void __launch_bounds__(kSumThreads)
     int at = window_at(cur);
     float sum[V] = {};
     OldWindow<D, V> held;   // of the present token
-    for (int k = begin; k < end; k += U) {
+    for (int k = begin; k < stop; k += U) {
         Pair p[U];
         RawWindow<VEC> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             p[u] = next[u];
-            next[u] = k + U + u < end ? pairs[k + U + u] : Pair{none, 0};
+            next[u] = pair_at(k + U + u);
         }
+        if (k >= end && p[0].key == none) break;
 #pragma unroll
         for (int u = 0; u < U; ++u)
             raw[u] = fetch_window<T, VEC>(dout + static_cast<long long>(p[u].at) * a.width, window_at(p[u].key),
@@ -587,7 +604,9 @@ __global__ void __launch_bounds__(kSumThreads)
         for (int u = 0; u < U; ++u) {
             if (p[u].key == none) continue;
             if (p[u].key != cur) {   // the token's last row was the one before
-                if (here)
+                if (cur == none)
+                    ;
+                else if (here)
                     finish_row<T, D, VEC>(a, dst, at, sum, AHEAD ? &held : nullptr);
                 else
                     store_partial<V>(partial_at<V>(partial, r, 0, windows, j), sum);
@@ -608,21 +627,21 @@ __global__ void __launch_bounds__(kSumThreads)
             for (int e = 0; e < V; ++e) sum[e] += v[e];
         }
     }
-    const bool ends = end == a.rows || __ldg(&pairs[end].key) != cur;
-    if (here && ends)
+    if (cur == none) return;
+    if (here && (extend || after != cur))
         finish_row<T, D, VEC>(a, dst, at, sum, AHEAD ? &held : nullptr);
     else
         store_partial<V>(partial_at<V>(partial, r, here ? 1 : 0, windows, j), sum);
 }
 
-// The token that begins in a run and goes on behind it: its partial sums, in
-// kJoinParts contiguous parts that are then added up (one part: a token of a
-// twelfth of 32768 rows took 20 us).
-constexpr int kJoinParts = 4;
+// The tokens that begin in a run and go on behind the next one: their partial
+// sums, in kJoinParts contiguous parts that are then added up (one part: a token
+// of a twelfth of 32768 rows took 20 us).  A CTA for each 32 runs and slice.
+constexpr int kJoinParts = 4, kJoinRuns = 32;
 template <class T, class D, bool VEC>
 __global__ void __launch_bounds__(kSumThreads * kJoinParts)
-    join_kernel(const EmbeddingArgs a, const Pair *pairs, const float *partial, int run, int runs, int lanes,
-                int slices, int ctas, const Fill fill) {
+    join_kernel(const EmbeddingArgs a, const Pair *pairs, const float *partial, int run, int runs, int slices,
+                int ctas, const Fill fill) {
     constexpr int V = 16 / sizeof(T);
     wait_for_previous();
     if (static_cast<int>(blockIdx.x) >= ctas) {
@@ -630,28 +649,33 @@ __global__ void __launch_bounds__(kSumThreads * kJoinParts)
         return;
     }
     __shared__ float4 parts[kJoinParts - 1][V / 4][kSumThreads];
+    __shared__ unsigned int live_runs;
     const int part = threadIdx.x / kSumThreads, thread = threadIdx.x % kSumThreads;
-    const int lane = thread & (lanes - 1);
-    const int r = blockIdx.x / slices * (kSumThreads / lanes) + thread / lanes;
+    const int first_run = static_cast<int>(blockIdx.x) / slices * kJoinRuns;
     const int windows = windows_of<T>(a.width, VEC);
-    const int j = blockIdx.x % slices * lanes + lane;
-    unsigned int cur = a.vocab;
-    const int begin = r * run, end = begin + run;
-    if (r < runs - 1 && j < windows) {   // not the last run: whole
-        cur = __ldg(&pairs[end - 1].key);
-        const unsigned int next = __ldg(&pairs[end].key), first = __ldg(&pairs[begin].key);
-        const unsigned int prior = begin > 0 ? __ldg(&pairs[begin - 1].key) : a.vocab;
-        if (next != cur || (first == cur && prior == cur)) cur = a.vocab;
+    const int j = static_cast<int>(blockIdx.x) % slices * kSumThreads + thread;
+    const unsigned int none = a.vocab;
+    if (threadIdx.x < 32) {
+        const long long begin = (static_cast<long long>(first_run) + threadIdx.x) * run, end = begin + run;
+        bool live = false;
+        if (end + run < a.rows) {
+            const unsigned int tail = __ldg(&pairs[end - 1].key), after = __ldg(&pairs[end].key);
+            const unsigned int far = __ldg(&pairs[end + run].key), front = __ldg(&pairs[begin].key);
+            const unsigned int prior = begin > 0 ? __ldg(&pairs[begin - 1].key) : ~0u;
+            live = tail != none && after == tail && far == tail && !(tail == front && prior == front);
+        }
+        const unsigned int mask = __ballot_sync(0xffffffffu, live);
+        if (threadIdx.x == 0) live_runs = mask;
     }
-    const bool live = cur != static_cast<unsigned int>(a.vocab);
-    if (!__syncthreads_or(live)) return;
-    float sum[V] = {};
-    if (live) {
-        // the run that the token ends in: most end in the next one
+    __syncthreads();
+    for (unsigned int left = live_runs; left != 0; left &= left - 1) {
+        const int r = first_run + __ffs(left) - 1;
+        const unsigned int cur = __ldg(&pairs[(r + 1) * run - 1].key);
+        // the run that the token ends in
         auto goes_past = [&](int q) {   // whether it fills run q to the end
             return q < runs && __ldg(&pairs[min((q + 1) * run, a.rows) - 1].key) == cur;
         };
-        int low = r + 1, step = 1;      // runs before `low` do not end it
+        int low = r + 2, step = 1;      // runs before `low` do not end it
         while (goes_past(low + step - 1)) {
             low += step;
             step *= 2;
@@ -669,42 +693,47 @@ __global__ void __launch_bounds__(kSumThreads * kJoinParts)
         const int pieces = low - r - (there ? 0 : 1);   // besides the one that begins here
         const int from = r + 1 + static_cast<int>(static_cast<long long>(pieces) * part / kJoinParts);
         const int to = r + 1 + static_cast<int>(static_cast<long long>(pieces) * (part + 1) / kJoinParts);
-        if (part == 0) {
-            const float *own = partial_at<V>(partial, r, 1, windows, j);
+        float sum[V] = {};
+        if (j < windows) {
+            if (part == 0) {
+                const float *own = partial_at<V>(partial, r, 1, windows, j);
 #pragma unroll
-            for (int e = 0; e < V; ++e) sum[e] = own[e];
-        }
+                for (int e = 0; e < V; ++e) sum[e] = own[e];
+            }
 #pragma unroll 4
-        for (int q = from; q < to; ++q) {
-            const float *p = partial_at<V>(partial, q, 0, windows, j);
+            for (int q = from; q < to; ++q) {
+                const float *p = partial_at<V>(partial, q, 0, windows, j);
 #pragma unroll
-            for (int e = 0; e < V; e += 4) {
-                const float4 t = *reinterpret_cast<const float4 *>(p + e);
-                sum[e] += t.x;
-                sum[e + 1] += t.y;
-                sum[e + 2] += t.z;
-                sum[e + 3] += t.w;
+                for (int e = 0; e < V; e += 4) {
+                    const float4 t = *reinterpret_cast<const float4 *>(p + e);
+                    sum[e] += t.x;
+                    sum[e + 1] += t.y;
+                    sum[e + 2] += t.z;
+                    sum[e + 3] += t.w;
+                }
             }
         }
         if (part > 0)
 #pragma unroll
             for (int e = 0; e < V; e += 4)
                 parts[part - 1][e / 4][thread] = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
-    }
-    __syncthreads();
-    if (part != 0 || !live) return;
+        __syncthreads();
+        if (part == 0 && j < windows) {
 #pragma unroll
-    for (int q = 0; q < kJoinParts - 1; ++q)
+            for (int q = 0; q < kJoinParts - 1; ++q)
 #pragma unroll
-        for (int e = 0; e < V; e += 4) {
-            const float4 t = parts[q][e / 4][thread];
-            sum[e] += t.x;
-            sum[e + 1] += t.y;
-            sum[e + 2] += t.z;
-            sum[e + 3] += t.w;
+                for (int e = 0; e < V; e += 4) {
+                    const float4 t = parts[q][e / 4][thread];
+                    sum[e] += t.x;
+                    sum[e + 1] += t.y;
+                    sum[e + 2] += t.z;
+                    sum[e + 3] += t.w;
+                }
+            D *dst = static_cast<D *>(a.dweight) + static_cast<long long>(cur) * a.width;
+            finish_row<T, D, VEC>(a, dst, j * V - (VEC ? 0 : window_phase(dst)), sum);
         }
-    D *dst = static_cast<D *>(a.dweight) + static_cast<long long>(cur) * a.width;
-    finish_row<T, D, VEC>(a, dst, j * V - (VEC ? 0 : window_phase(dst)), sum);
+        __syncthreads();
+    }
 }
 
 // ---- gradient: launches -----------------------------------------------------------------
@@ -819,7 +848,7 @@ cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
     while (lanes < kSumThreads && lanes < windows) lanes *= 2;
     const int per = kSumThreads / lanes, slices = (windows + lanes - 1) / lanes;
     const int ctas = (m.runs + per - 1) / per * slices;
-    const bool join = m.runs > 1;
+    const bool join = m.runs > 2;
     int n = fillers(join ? rows - share : rows);
     auto sums = sum_kernel<T, D, VEC, false>;
     if constexpr (VEC)
@@ -828,8 +857,10 @@ cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
                       lanes, slices, ctas, fill);
     if (err != cudaSuccess || !join) return err;
     n = fillers(rows);
-    return launch_next(join_kernel<T, D, VEC>, ctas + n, kSumThreads * kJoinParts, stream, a, sorted,
-                       static_cast<const float *>(partial), m.run, m.runs, lanes, slices, ctas, fill);
+    const int join_slices = (windows + kSumThreads - 1) / kSumThreads;
+    const int join_ctas = (m.runs + kJoinRuns - 1) / kJoinRuns * join_slices;
+    return launch_next(join_kernel<T, D, VEC>, join_ctas + n, kSumThreads * kJoinParts, stream, a, sorted,
+                       static_cast<const float *>(partial), m.run, m.runs, join_slices, join_ctas, fill);
 }
 
 template <class T, class D>
