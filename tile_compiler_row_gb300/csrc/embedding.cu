@@ -45,7 +45,9 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 
 // ---- lookup ---------------------------------------------------------------------
 
-// `lanes` (a power of two) threads a row, up to 4 windows of it each at a time.
+// `lanes` (a power of two) threads a row, up to 4 windows of it each at a time;
+// of a row off the 16-byte grid, those that are whole, and the elements at its
+// ends one by one.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(256) lookup_kernel(const EmbeddingArgs a, int lanes) {
     constexpr int V = 16 / sizeof(T), U = 4;
@@ -55,32 +57,42 @@ __global__ void __launch_bounds__(256) lookup_kernel(const EmbeddingArgs a, int 
     const int token = token_row(a, __ldg(a.tokens + row));
     const T *src = static_cast<const T *>(a.weight) + static_cast<long long>(token < 0 ? 0 : token) * a.width;
     T *dst = static_cast<T *>(a.out) + static_cast<long long>(row) * a.width;
-    const int phase = VEC ? 0 : window_phase(dst);
-    const int windows = windows_of<T>(a.width, VEC);
+    auto scaled = [&](float v) {   // an ignored row is 0 whatever the scale, a bad one NaN
+        return token >= 0 ? v * a.scale : token == -1 ? 0.0f : __int_as_float(0x7fffffff);
+    };
+    int head = 0;
+    if constexpr (!VEC) {
+        head = min((V - window_phase(dst)) % V, a.width);
+        const int body = (a.width - head) / V * V;
+        for (int e = lane; e < a.width - body; e += lanes) {
+            const int at = e < head ? e : body + e;
+            store_one(dst + at, scaled(token >= 0 ? static_cast<float>(src[at]) : 0.0f));
+        }
+    }
+    const int windows = (a.width - head) / V;
     const Bounds bounds = bounds_of<T>(a.weight, a.vocab, a.width);
     for (int j = lane; j < windows; j += U * lanes) {
         RawWindow<VEC> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            raw[u] = fetch_window<T, VEC>(src, (j + u * lanes) * V - phase, bounds,
+            raw[u] = fetch_window<T, VEC>(src, (j + u * lanes) * V + head, bounds,
                                           token >= 0 && j + u * lanes < windows);
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (j + u * lanes < windows) {
+                const int at = (j + u * lanes) * V + head;
                 float v[V];
-                widen_vec<T>(join_window<T, VEC>(raw[u], src, (j + u * lanes) * V - phase, a.width, bounds,
-                                                 token >= 0), v);
+                widen_vec<T>(token >= 0 ? join_window<T, VEC>(raw[u], src, at, a.width) : make_uint4(0, 0, 0, 0), v);
 #pragma unroll
-                for (int i = 0; i < V; ++i)   // an ignored row is 0 whatever the scale, a bad one NaN
-                    v[i] = token >= 0 ? v[i] * a.scale : token == -1 ? 0.0f : __int_as_float(0x7fffffff);
-                store_window<T, V, VEC>(dst, (j + u * lanes) * V - phase, a.width, v);
+                for (int i = 0; i < V; ++i) v[i] = scaled(v[i]);
+                store_window<T, V, true>(dst, at, a.width, v);
             }
     }
 }
 
 template <class T, bool VEC>
 cudaError_t launch_lookup(const EmbeddingArgs &a, cudaStream_t stream) {
-    const int windows = a.width / (16 / static_cast<int>(sizeof(T))) + (VEC ? 0 : 2);
+    const int windows = a.width / (16 / static_cast<int>(sizeof(T)));
     int lanes = 8;
     while (lanes < 256 && lanes * 4 < windows) lanes *= 2;
     // few rows: one window a thread
@@ -184,7 +196,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const EmbeddingAr
         for (int u = 0; u < U; ++u) {
             if (!in || k + u >= to) continue;
             float v[V];
-            widen_vec<T>(join_window<T, VEC>(raw[u], row[u], at, a.width, bounds, true), v);
+            widen_vec<T>(join_window<T, VEC>(raw[u], row[u], at, a.width), v);
 #pragma unroll
             for (int e = 0; e < V; ++e) sum[e] += v[e];
         }
@@ -621,8 +633,7 @@ __global__ void __launch_bounds__(kSumThreads)
             if constexpr (AHEAD)
                 if (u == 0 && k == begin) held = old[0];
             float v[V];
-            widen_vec<T>(join_window<T, VEC>(raw[u], dout + static_cast<long long>(p[u].at) * a.width, at, a.width,
-                                             bounds, true), v);
+            widen_vec<T>(join_window<T, VEC>(raw[u], dout + static_cast<long long>(p[u].at) * a.width, at, a.width), v);
 #pragma unroll
             for (int e = 0; e < V; ++e) sum[e] += v[e];
         }

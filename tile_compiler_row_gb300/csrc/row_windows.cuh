@@ -25,12 +25,12 @@ __device__ __forceinline__ uint4 load_vec(const void *p) {
 
 // The matrix that windows are read from: nothing outside it is.
 struct Bounds {
-    uintptr_t begin, end;
+    uintptr_t begin;
+    long long last;   // bytes from the begin at which two vectors still fit
 };
 template <class T>
 __device__ __forceinline__ Bounds bounds_of(const void *p, long long rows, int width) {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-    return Bounds{b, b + static_cast<size_t>(rows) * width * sizeof(T)};
+    return Bounds{reinterpret_cast<uintptr_t>(p), rows * width * static_cast<long long>(sizeof(T)) - 32};
 }
 
 // The vectors that hold elements [at, at + V) of a row, read without a branch
@@ -45,6 +45,7 @@ struct RawWindow<true> {
 template <>
 struct RawWindow<false> {
     uint4 a, b;
+    bool whole;   // both vectors lie in the matrix
 };
 
 template <class T, bool VEC>
@@ -56,7 +57,9 @@ __device__ __forceinline__ RawWindow<VEC> fetch_window(const T *row, int at, con
         const uintptr_t p = reinterpret_cast<uintptr_t>(row) + static_cast<long long>(at) * sizeof(T);
         const uintptr_t low = p & ~static_cast<uintptr_t>(15);
         // (ends of the matrix, where a vector would pass them: element by element, below)
-        if (wanted && low >= m.begin && low + 32 <= m.end) {
+        const long long off = static_cast<long long>(low - m.begin);
+        w.whole = off >= 0 && off <= m.last;
+        if (wanted && w.whole) {
             w.a = load_vec(reinterpret_cast<const void *>(low));
             w.b = load_vec(reinterpret_cast<const void *>(low + 16));
         }
@@ -65,15 +68,12 @@ __device__ __forceinline__ RawWindow<VEC> fetch_window(const T *row, int at, con
 }
 
 template <class T, bool VEC>
-__device__ __forceinline__ uint4 join_window(const RawWindow<VEC> &r, const T *row, int at, int width,
-                                             const Bounds &m, bool wanted) {
+__device__ __forceinline__ uint4 join_window(const RawWindow<VEC> &r, const T *row, int at, int width) {
     if constexpr (VEC) return r.a;
     else {
         constexpr int V = 16 / sizeof(T);
-        const uintptr_t p = reinterpret_cast<uintptr_t>(row) + static_cast<long long>(at) * sizeof(T);
-        const uintptr_t low = p & ~static_cast<uintptr_t>(15);
-        if (wanted && !(low >= m.begin && low + 32 <= m.end)) {
-            unsigned int w[4] = {};
+        unsigned int w[4] = {};
+        if (!r.whole) {
 #pragma unroll
             for (int j = 0; j < V; ++j)
                 if (at + j >= 0 && at + j < width) {
@@ -86,17 +86,23 @@ __device__ __forceinline__ uint4 join_window(const RawWindow<VEC> &r, const T *r
                 }
             return make_uint4(w[0], w[1], w[2], w[3]);
         }
-        const unsigned int shift = static_cast<unsigned int>(p & 15);
-        unsigned int w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-#pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
-#pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
-        if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (shift & 2));
+        // bytes by which the window lies behind the first vector: the same for
+        // all windows of a row, so these branches do not diverge
+        const unsigned int shift = static_cast<unsigned int>(
+            (reinterpret_cast<uintptr_t>(row) + static_cast<long long>(at) * sizeof(T)) & 15);
+        const unsigned int bits = sizeof(T) == 4 ? 0 : 8 * (shift & 2);
+        auto from = [&](unsigned int a, unsigned int b, unsigned int c, unsigned int d, unsigned int e) {
+            if constexpr (sizeof(T) == 4) return make_uint4(a, b, c, d);
+            else
+                return make_uint4(__funnelshift_r(a, b, bits), __funnelshift_r(b, c, bits),
+                                  __funnelshift_r(c, d, bits), __funnelshift_r(d, e, bits));
+        };
+        switch (shift >> 2) {
+            case 0: return from(r.a.x, r.a.y, r.a.z, r.a.w, r.b.x);
+            case 1: return from(r.a.y, r.a.z, r.a.w, r.b.x, r.b.y);
+            case 2: return from(r.a.z, r.a.w, r.b.x, r.b.y, r.b.z);
+            default: return from(r.a.w, r.b.x, r.b.y, r.b.z, r.b.w);
         }
-        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
