@@ -528,7 +528,7 @@ int tile_embedding(int dtype, const long long *tokens, const void *weight, void 
  * `workspace`: device memory of the caller, 256-byte aligned, at least
  * tile_embedding_backward_workspace_bytes(rows, width, vocab) bytes (0 for few
  * rows): the positions sorted by token, and partial sums of tokens that occur
- * often, 8 width bytes for each 64 rows, at most 1024 of them.  Calls that
+ * often (64 MiB at most).  Calls that
  * overlap in time need workspaces of their own.  rows == 0 writes a zero
  * dweight, or nothing where it accumulates.  May be captured into a CUDA
  * graph. */
@@ -572,7 +572,7 @@ int tile_embedding_backward(int dtype, int dweight_dtype, const long long *token
  * nll, old_nll, ref_nll [rows], advantage [rows] or [sequences]: FP32.  Whether r
  * is held back is decided from old_nll - nll as if it had not been rounded; r A
  * equal to its bound is not.  An advantage of 0 gives a first term of 0.  Sums
- * are FP32 over 1024 rows and compensated beyond, bitwise reproducible.  `workspace`:
+ * are FP32 over 512 rows and compensated beyond, bitwise reproducible.  `workspace`:
  * 16-byte aligned device memory of the caller; calls that overlap in time need
  * workspaces of their own.  rows == 0 writes zeros.  TILE_ERR_EPS for clip_low
  * outside [0, 1], a negative or NaN clip_high or a kl_coef that is not finite;

@@ -5,7 +5,7 @@ and expm1f by 2 ulp (2^-22), each product and sum by 2^-24.  So r is off by (2^-
 + |x| 2^-24) r, r A by 2^-24 more, and e^q - 1 - q by 2^-22 |e^q - 1| + |q (e^q - 1)|
 2^-24 + 2^-24 of itself; a held-back r A by 2^-23 (its bound and the product).  A
 weight is rounded once or twice, and the gradient has three more products.  A mean
-adds at most 1023 FP32 roundings of partial sums of a tile's magnitudes.
+adds at most 511 FP32 roundings of partial sums of a tile's magnitudes.
 """
 
 import math
@@ -87,7 +87,7 @@ def reference(nll, kw, mean, dloss=1.0):
     for t, t_off in ((-ra, ra_off), (kl, kl_off), (held.double(), 0 * kl)):
         t = torch.where(keep, t, 0.0)
         means.append((w * t).sum())
-        off.append((w * torch.where(keep, t_off, 0.0)).sum() + 1024 * U * (w * t.abs()).sum() + U * means[-1].abs())
+        off.append((w * torch.where(keep, t_off, 0.0)).sum() + 512 * U * (w * t.abs()).sum() + U * means[-1].abs())
     stats = torch.stack([means[0] + beta * means[1], *means])
     off = torch.stack([off[0] + beta * off[1] + U * stats[0].abs(), *off])
     d = torch.where(held, 0.0, ra) + beta * e

@@ -3,15 +3,23 @@
 //
 // Both are bound by DRAM: the lookup reads each row of the weight that occurs
 // and writes rows x width; the gradient reads rows x width and writes the
-// whole weight's shape, or the rows that occur where it adds.
+// whole weight's shape, or reads and writes the rows that occur where it adds.
 //
 // The gradient sums the rows of a token in the order of their positions, in
 // FP32, so that results are bitwise reproducible.  Few rows: a CTA for each
 // row looks for the row's token among all tokens, and the first row of a token
-// sums them.  Many rows: positions are sorted by token (a stable radix sort of
-// up to 9 bits a pass), and the sorted list is summed in runs of kRun
-// positions; a token whose rows lie in several runs is joined from their
-// partial sums.
+// sums them (one launch, no workspace).  More rows: positions are brought in
+// the order of their tokens, up to 8192 by counting, more by a stable radix
+// sort of up to 9 bits a pass; then the list is summed in runs of 8 to 64
+// positions, and a token that fills more than a run is joined from partial
+// sums.  The rows of tokens that do not occur are zeroed by CTAs that the
+// launches of this chain carry along.
+//
+// (One GB300, a copy moves 6.68 TB/s.  32768 x 4096 BF16 against 131072
+// entries: lookup 59 us of the device's time, 0.93 of that rate; gradient 214
+// us, 0.94, added to another 125.  5000 x 1537 FP32 against 50001, a third of it
+// ignored: 69 us, 0.71.  Rows off the 16-byte grid cost two loads a window and
+// the shifts: 32768 x 4097 BF16 lookup 99 us.)
 #include "device_status.h"
 #include "embedding.h"
 #include "row_windows.cuh"
@@ -413,10 +421,10 @@ __global__ void __launch_bounds__(kSortThreads)
         }
 }
 
-// Up to kMostRanked positions go to their places at once: the place of i is the
+// Up to kMostRanked positions go to their places at once: that of i is the
 // number of j with a smaller key, or the same key and j < i.  CTA b counts them
 // for positions 32 b .. 32 b + 31 against all keys in its shared memory.  (The
-// passes above, with three launches, took 15 us more of 5000 rows.)
+// passes above, with three launches, took 8 to 14 us more of 512 to 2048 rows.)
 constexpr int kMostRanked = 8192, kRankThreads = 256, kRankPer = 4;
 __global__ void __launch_bounds__(kRankThreads)
     rank_kernel(const EmbeddingArgs a, Pair *out, unsigned int *present) {
@@ -479,8 +487,9 @@ struct SumPlan {
 // 64 positions a run; fewer, down to 8, where that leaves SMs without enough
 // threads (32768 x 1536 BF16, added: 82 us with 64); more where the partial sums
 // would pass 64 MiB.
-SumPlan sum_plan(int rows, int width) {
-    const long long windows = width / 8 + 1;
+// (vector: elements of a window; the workspace has room for the runs of 8, the most.)
+SumPlan sum_plan(int rows, int width, int vector) {
+    const long long windows = width / vector + 1;
     auto bytes = [&](int run) { return (static_cast<long long>(rows) + run - 1) / run * 8 * (width + 16); };
     SumPlan p;
     p.run = 64;
@@ -755,7 +764,7 @@ struct Layout {
 };
 Layout layout(int rows, int width, int vocab) {
     const SortPlan s = sort_plan(rows, vocab);
-    const SumPlan m = sum_plan(rows, width);
+    const SumPlan m = sum_plan(rows, width, 8);
     auto round = [](size_t n) { return (n + 255) / 256 * 256; };
     Layout l;
     l.list = round(static_cast<size_t>(rows) * sizeof(Pair));
@@ -810,7 +819,7 @@ cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
         return cudaGetLastError();
     }
     const SortPlan s = sort_plan(a.rows, a.vocab);
-    const SumPlan m = sum_plan(a.rows, a.width);
+    const SumPlan m = sum_plan(a.rows, a.width, V);
     const Layout l = layout(a.rows, a.width, a.vocab);
     char *ws = static_cast<char *>(a.ws);
     Pair *list[2] = {reinterpret_cast<Pair *>(ws), reinterpret_cast<Pair *>(ws + l.list)};

@@ -6,11 +6,20 @@
 //
 // averaged over all tokens, or over sequences of means over their tokens.
 //
-// At most 36 bytes a token: bound by latency up to some 10^5 tokens and by
-// DRAM beyond.  Whether a ratio is clipped is decided by x against the bounds'
-// logarithms, as if x had not been rounded: r's own rounding would move
-// tokens over the border, where the gradient jumps.  Sums are FP32 over a tile
-// of 1024 rows, in a fixed order, and compensated FP32 over tiles and sequences.
+// At most 36 bytes a token: bound by latency up to some 10^5 tokens, and by how
+// many loads are on their way beyond.  A tile is 512 rows, two to a thread, all
+// its loads issued before the sequences are looked for; the tiles' sums are
+// joined by a second launch that comes up meanwhile, or, of up to 8 tiles, by
+// the first CTA of their cluster.  (Device times in a graph: 1048576 tokens, 512
+// sequences: 9.4 us forward, 7.3 backward, where the bytes are 4 us; 8191
+// tokens: 4.8 and 3.0.  With 1024 rows, four to a thread: 10.4, 8.9, 5.9, 4.3;
+// with 256 rows 11.2, 8.3, 4.8, 2.6.  A join of 1024 threads took 0.5 to 0.8 us
+// more than one of 512.)
+//
+// Whether a ratio is clipped is decided by x against the bounds' logarithms,
+// as if x had not been rounded: r's own rounding would move tokens over the
+// border, where the gradient jumps.  Sums are FP32 over a tile, in a fixed
+// order, and compensated FP32 over tiles and sequences.
 #include "device_status.h"
 #include "policy_loss.h"
 
@@ -20,7 +29,7 @@ namespace tile {
 namespace {
 
 constexpr unsigned int kBadOffsets = 1;
-constexpr int kThreads = 256, kRows = 4, kTile = kThreads * kRows, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kRows = 2, kTile = kThreads * kRows, kWarps = kThreads / 32;
 constexpr int kMostFused = 8;   // tiles that one cluster does, joined without another launch
 
 // The last sequence in [low, high] that begins at or before row.
@@ -90,7 +99,7 @@ struct Token {
 };
 
 // Rows tile0 + thread + 256 u of the tile, with the loads on their way before
-// the sequences are known (8191 rows, backward: 7.1 us with one after the other).
+// the sequences are known.
 __device__ __forceinline__ void load_tokens(const PolicyArgs &a, long long tile0, Token (&t)[kRows]) {
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
@@ -206,7 +215,7 @@ __device__ __forceinline__ void tile_sums(const PolicyArgs &a, int tile, float4 
 }
 
 // An FP32 sum with what its roundings cut off (Knuth's two-sum): FP64 sums of
-// the tiles took 40 of 64 us of 1048576 tokens.
+// the tiles by all threads took 40 us more of 1048576 tokens.
 struct Sum {
     float s, cut;
     __device__ __forceinline__ void add(float x) {
@@ -328,7 +337,7 @@ __global__ void __launch_bounds__(kThreads) tiles_kernel(const PolicyArgs a) {
     tile_sums(a, blockIdx.x, static_cast<float4 *>(a.ws), mem);
 }
 
-constexpr int kJoinThreads = 1024;
+constexpr int kJoinThreads = 512;
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PolicyArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the tiles' sums are written
     join_sums<kJoinThreads>(a, static_cast<const float4 *>(a.ws));
