@@ -223,6 +223,37 @@ def test_a_workspace_is_what_is_written():
         assert torch.equal(got, again)
 
 
+def test_no_rows():
+    weight, none = normal(1, 7, 40), torch.empty(0, dtype=torch.int64, device="cuda")
+    assert tile.embedding(none, weight).shape == (0, 40)
+    dout = torch.empty(0, 40, device="cuda")
+    assert not tile.embedding_backward(none, dout, 7).any()
+    old = weight.clone()
+    assert torch.equal(tile.embedding_backward(none, dout, dweight=weight), old)
+
+
+@pytest.mark.parametrize("vocab", [300, 300001])
+@pytest.mark.parametrize("rows", [3000, 20000])
+def test_calls_one_after_another_in_one_workspace(rows, vocab):
+    """Each launch is set up while the one before it runs: what a call finds in
+    the workspace is its own, not the last call's."""
+    width = 72
+    sets = [(tokens(rows, vocab, kind, seed), normal(seed, rows, width)) for kind, seed in
+            (("rare", 1), ("uniform", 2), ("padded", 3))]
+    want = [tile.embedding_backward(t, d, vocab) for t, d in sets]
+    ws = torch.empty(tile.tile_embedding_backward_workspace_bytes(rows, width, vocab), dtype=torch.uint8,
+                     device="cuda")
+    got = [[torch.empty(vocab, width, device="cuda") for _ in sets] for _ in range(4 if vocab > 1000 else 20)]
+    torch.cuda.synchronize()
+    for outs in got:
+        for (t, d), o in zip(sets, outs):
+            tile.tile_embedding_backward(t, d, o, ws)
+    torch.cuda.synchronize()
+    for outs in got:
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+
+
 def test_gradient_against_differences():
     """(L(w + h d) - L(w - h d)) / 2h of L = sum(out c) is linear in w: FP64 sums
     of the FP32 lookups agree with <dweight, d> to their roundings, 2^-24 of

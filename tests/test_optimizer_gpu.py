@@ -334,6 +334,14 @@ def test_large_tensor():
     assert not p[:-5].any()
 
 
+def test_copies_of_some():
+    s = make([300, 300], torch.float32, False, torch.float16)
+    s["copies"][0] = None
+    was = s["params"][1].clone()
+    tile.adamw(**s, step=1)
+    assert torch.equal(s["copies"][1], s["params"][1].half()) and not torch.equal(was, s["params"][1])
+
+
 def test_neighbours_are_left_alone():
     for eight in (False, True):
         for shift in (0, 3):

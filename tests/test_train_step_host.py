@@ -322,6 +322,9 @@ def test_lists_of_tensors(calls):
     tile.tile_adamw(p, g, p, p, 1, copies=c, weight_decay=[0.1, 0])
     table = calls[-1][1][0]
     assert len(table) == 160 and struct.unpack("8qf2i4x", table[80:])[7:] == (700, 0.0, 0, 2)
+    tile.tile_adamw(p, g, p, p, 1, copies=[None, c[1]])
+    table = calls.pop()[1][0]
+    assert struct.unpack("8qf2i4x", table[:80])[6] == 0 and struct.unpack("8qf2i4x", table[80:])[6] != 0
     e = [on_device(12, dtype=f8), on_device(700, dtype=f8)]
     s = [on_device(1), on_device(3)]
     tile.tile_adamw(p, g, e, e, on_device(1, dtype=torch.int64), on_device(1), exp_avg_scales=s, exp_avg_sq_scales=s)

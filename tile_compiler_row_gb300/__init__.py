@@ -1312,8 +1312,8 @@ def tile_adamw(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     """One AdamW step of every tensor of ``params`` (float32), in place, with
     its state; see ``tile_adamw`` in include/tile_rows.h.  Lists of one length:
     ``grads`` (float32, bfloat16 or float16), the states (float32, or
-    float8_e4m3fn with the scales), and ``copies`` (bfloat16 or float16, or
-    None).  ``step`` (from 1 on) and ``lr`` are numbers, or tensors of one
+    float8_e4m3fn with the scales), and, where wanted, ``copies`` (bfloat16 or
+    float16, None for a parameter without one).  ``step`` (from 1 on) and ``lr`` are numbers, or tensors of one
     element on the device (int64, float32); ``weight_decay`` a number or one
     for each tensor; ``factor`` ``tile_grad_norm``'s second output."""
     if _F32 is None:
@@ -1336,9 +1336,15 @@ def tile_adamw(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     elif count > 0 and (exp_avg_scales is not None or exp_avg_sq_scales is not None):
         raise ValueError("scales belong to 8-bit states")
     if copies is not None:
+        if hasattr(copies, "dtype") or len(copies) != count:
+            raise ValueError(f"copies must be a list of {count} tensors or None")
         halves = {k: i for k, i in _CODES.items() if i != 0}
-        c, _, copy_kinds = _columns(copies, "copies", halves, n, dev)
-        copy_kinds = [halves[k] for k in copy_kinds]
+        which = [i for i, t in enumerate(copies) if t is not None]
+        at, _, types = _columns([copies[i] for i in which], "copies", halves,
+                                [n[i] for i in which], dev)
+        c, copy_kinds = [0] * count, [0] * count
+        for i, a, k in zip(which, at, types):
+            c[i], copy_kinds[i] = a, halves[k]
     decay = [weight_decay] * count if isinstance(weight_decay, (int, float)) else weight_decay
     if len(decay) != count:
         raise ValueError(f"weight_decay must be a number or {count} of them")

@@ -45,7 +45,9 @@ __device__ __forceinline__ int windows_of(int width, bool vec) {
     return vec ? width / V : (width + V - 1) / V + 1;
 }
 
-// The next kernel of the chain may be set up; this one's inputs are written.
+// The next kernel of the chain may be set up; this one's inputs are written.  (What
+// an earlier kernel of the chain wrote is not read through the read-only cache:
+// this kernel may have begun before.)
 __device__ __forceinline__ void let_next_start() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -317,7 +319,7 @@ __device__ __forceinline__ void fill_rows(const EmbeddingArgs &a, const Fill &f,
     const long long first = f.from + static_cast<long long>(part) * f.each;
     const long long end = min(first + f.each, static_cast<long long>(f.to));
     for (long long v = first + threadIdx.x / f.lanes; v < end; v += per) {
-        if (__ldg(f.present + (v >> 5)) >> (v & 31) & 1) continue;
+        if (f.present[v >> 5] >> (v & 31) & 1) continue;
         D *row = static_cast<D *>(a.dweight) + v * a.width;
         const int phase = VEC ? 0 : window_phase(row);
         for (int j = lane; j < windows; j += f.lanes)
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kSumThreads)
     if (r >= runs || j >= windows) return;
     const int begin = r * run, end = min(begin + run, a.rows);
     const unsigned int none = a.vocab, edge = ~0u;
-    auto key_of = [&](long long k) { return k >= 0 && k < a.rows ? __ldg(&pairs[k].key) : edge; };
+    auto key_of = [&](long long k) { return k >= 0 && k < a.rows ? pairs[k].key : edge; };
     const unsigned int before = key_of(begin - run - 1ll), prior = key_of(begin - 1ll), front = key_of(begin),
                        tail = key_of(end - 1ll), after = key_of(end), far = key_of(static_cast<long long>(end) + run);
     if (front == none) return;
@@ -679,9 +681,9 @@ __global__ void __launch_bounds__(kSumThreads * kJoinParts)
         const long long begin = (static_cast<long long>(first_run) + threadIdx.x) * run, end = begin + run;
         bool live = false;
         if (end + run < a.rows) {
-            const unsigned int tail = __ldg(&pairs[end - 1].key), after = __ldg(&pairs[end].key);
-            const unsigned int far = __ldg(&pairs[end + run].key), front = __ldg(&pairs[begin].key);
-            const unsigned int prior = begin > 0 ? __ldg(&pairs[begin - 1].key) : ~0u;
+            const unsigned int tail = pairs[end - 1].key, after = pairs[end].key;
+            const unsigned int far = pairs[end + run].key, front = pairs[begin].key;
+            const unsigned int prior = begin > 0 ? pairs[begin - 1].key : ~0u;
             live = tail != none && after == tail && far == tail && !(tail == front && prior == front);
         }
         const unsigned int mask = __ballot_sync(0xffffffffu, live);
@@ -690,10 +692,10 @@ __global__ void __launch_bounds__(kSumThreads * kJoinParts)
     __syncthreads();
     for (unsigned int left = live_runs; left != 0; left &= left - 1) {
         const int r = first_run + __ffs(left) - 1;
-        const unsigned int cur = __ldg(&pairs[(r + 1) * run - 1].key);
+        const unsigned int cur = pairs[(r + 1) * run - 1].key;
         // the run that the token ends in
         auto goes_past = [&](int q) {   // whether it fills run q to the end
-            return q < runs && __ldg(&pairs[min((q + 1) * run, a.rows) - 1].key) == cur;
+            return q < runs && pairs[min((q + 1) * run, a.rows) - 1].key == cur;
         };
         int low = r + 2, step = 1;      // runs before `low` do not end it
         while (goes_past(low + step - 1)) {
@@ -709,7 +711,7 @@ __global__ void __launch_bounds__(kSumThreads * kJoinParts)
                 high = mid;
         }
         // (a token that ends with its run is not in the next one, and has no piece there)
-        const bool there = low < runs && __ldg(&pairs[low * run].key) == cur;
+        const bool there = low < runs && pairs[low * run].key == cur;
         const int pieces = low - r - (there ? 0 : 1);   // besides the one that begins here
         const int from = r + 1 + static_cast<int>(static_cast<long long>(pieces) * part / kJoinParts);
         const int to = r + 1 + static_cast<int>(static_cast<long long>(pieces) * (part + 1) / kJoinParts);
