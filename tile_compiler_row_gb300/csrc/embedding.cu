@@ -557,8 +557,7 @@ template <class T, class D, bool VEC, bool AHEAD>
 __global__ void __launch_bounds__(kSumThreads)
     sum_kernel(const EmbeddingArgs a, const Pair *pairs, float *partial, int run, int runs, int lanes,
                int slices, int ctas, const Fill fill) {
-    constexpr int V = 16 / sizeof(T), U = AHEAD ? 4 : VEC ? 8 : 2;
-    static_assert(VEC || !AHEAD, "vectors");
+    constexpr int V = 16 / sizeof(T), U = !VEC ? 2 : AHEAD ? 4 : 8;
     let_next_start();
     wait_for_previous();
     // (fillers evenly between the CTAs that sum: 32768 x 4096 BF16 239 us, behind them 220)
@@ -599,6 +598,8 @@ __global__ void __launch_bounds__(kSumThreads)
     auto window_at = [&](unsigned int key) {   // (any place for no token)
         return VEC ? j * V : j * V - window_phase(static_cast<const D *>(a.dweight) + static_cast<long long>(key) * a.width);
     };
+    // (a window that a row's end cuts is read element by element, at the token's last row)
+    auto inside = [&](int to) { return VEC || (to >= 0 && to + V <= a.width); };
     D *dst = static_cast<D *>(a.dweight) + static_cast<long long>(cur) * a.width;
     int at = window_at(cur);
     float sum[V] = {};
@@ -619,9 +620,11 @@ __global__ void __launch_bounds__(kSumThreads)
         OldWindow<D, V> old[AHEAD ? U : 1];
         if constexpr (AHEAD) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (p[u].key != none && p[u].key != (u > 0 ? p[u - 1].key : k == begin ? none : cur))
-                    old[u].load(static_cast<const D *>(a.dweight) + static_cast<long long>(p[u].key) * a.width + j * V);
+            for (int u = 0; u < U; ++u) {
+                const int to = window_at(p[u].key);
+                if (p[u].key != none && p[u].key != (u > 0 ? p[u - 1].key : k == begin ? none : cur) && inside(to))
+                    old[u].load(static_cast<const D *>(a.dweight) + static_cast<long long>(p[u].key) * a.width + to);
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -630,7 +633,7 @@ __global__ void __launch_bounds__(kSumThreads)
                 if (cur == none)
                     ;
                 else if (here)
-                    finish_row<T, D, VEC>(a, dst, at, sum, AHEAD ? &held : nullptr);
+                    finish_row<T, D, VEC>(a, dst, at, sum, AHEAD && inside(at) ? &held : nullptr);
                 else
                     store_partial<V>(partial_at<V>(partial, r, 0, windows, j), sum);
                 cur = p[u].key;
@@ -651,7 +654,7 @@ __global__ void __launch_bounds__(kSumThreads)
     }
     if (cur == none) return;
     if (here && (extend || after != cur))
-        finish_row<T, D, VEC>(a, dst, at, sum, AHEAD ? &held : nullptr);
+        finish_row<T, D, VEC>(a, dst, at, sum, AHEAD && inside(at) ? &held : nullptr);
     else
         store_partial<V>(partial_at<V>(partial, r, here ? 1 : 0, windows, j), sum);
 }
@@ -872,9 +875,7 @@ cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
     const int ctas = (m.runs + per - 1) / per * slices;
     const bool join = m.runs > 2;
     int n = fillers(join ? rows - share : rows);
-    auto sums = sum_kernel<T, D, VEC, false>;
-    if constexpr (VEC)
-        if (a.add) sums = sum_kernel<T, D, true, true>;
+    const auto sums = a.add ? sum_kernel<T, D, VEC, true> : sum_kernel<T, D, VEC, false>;
     err = launch_next(sums, ctas + n, kSumThreads, stream, a, sorted, partial, m.run, m.runs,
                       lanes, slices, ctas, fill);
     if (err != cudaSuccess || !join) return err;
