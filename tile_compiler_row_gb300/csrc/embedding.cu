@@ -241,7 +241,7 @@ bool few_rows(int rows, int width) {
 
 // ---- gradient: sorting positions by token --------------------------------------------
 
-constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32, kMaxBits = 9;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kMaxBits = 9;
 constexpr int kMaxBins = 1 << kMaxBits;
 
 struct Pair {
@@ -249,7 +249,7 @@ struct Pair {
 };
 
 struct SortPlan {
-    int passes, bits, items, tiles;   // items a thread
+    int passes, bits, items, tiles;   // items a thread: 2, 4 or 16
 };
 
 SortPlan sort_plan(int rows, int vocab) {
@@ -258,7 +258,11 @@ SortPlan sort_plan(int rows, int vocab) {
     SortPlan p;
     p.passes = (all + kMaxBits - 1) / kMaxBits;
     p.bits = (all + p.passes - 1) / p.passes;
-    p.items = rows > 131072 ? 32 : 8;
+    // Each tile adds up the counts of all tiles: short ones are done sooner while
+    // they are few.  (Ranking 32768, 131072 and 2^20 positions, with the sums of 64
+    // columns: 21, 50 and - us with 2 items, 24, 37 and - with 4, - and 136 with
+    // 16; CTAs of 256 threads of 8 or 32 items 27, 41 and 147.)
+    p.items = rows <= 49152 ? 2 : rows <= 131072 ? 4 : 16;
     p.tiles = (rows + kSortThreads * p.items - 1) / (kSortThreads * p.items);
     return p;
 }
@@ -273,7 +277,7 @@ __device__ __forceinline__ unsigned int key_at(const EmbeddingArgs &a, int i) {
 template <int ITEMS>
 __global__ void __launch_bounds__(kSortThreads)
     digits_kernel(const EmbeddingArgs a, int *counts, unsigned int *present, int bits, int passes) {
-    constexpr int U = 8;
+    constexpr int U = ITEMS < 8 ? ITEMS : 8;
     __shared__ int bins[kMaxBins];
     let_next_start();
     const int n = 1 << bits, tiles = gridDim.x;
@@ -839,10 +843,12 @@ cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
     const int passes = a.rows <= kMostRanked ? 0 : s.passes;
     if (passes == 0)
         rank_kernel<<<(a.rows + 31) / 32, kRankThreads, 0, stream>>>(a, list[0], present);
-    else if (s.items == 8)
-        digits_kernel<8><<<s.tiles, kSortThreads, 0, stream>>>(a, counts, present, s.bits, s.passes);
+    else if (s.items == 2)
+        digits_kernel<2><<<s.tiles, kSortThreads, 0, stream>>>(a, counts, present, s.bits, s.passes);
+    else if (s.items == 4)
+        digits_kernel<4><<<s.tiles, kSortThreads, 0, stream>>>(a, counts, present, s.bits, s.passes);
     else
-        digits_kernel<32><<<s.tiles, kSortThreads, 0, stream>>>(a, counts, present, s.bits, s.passes);
+        digits_kernel<16><<<s.tiles, kSortThreads, 0, stream>>>(a, counts, present, s.bits, s.passes);
     err = cudaGetLastError();
     // Fillers: CTAs of about 32 KB each, in the order of the rows (few CTAs that
     // went through all rows filled 1 GiB at 6.5 TB/s, these at 7.5).  A pass of
@@ -863,9 +869,8 @@ cudaError_t launch_gradient(const EmbeddingArgs &a, cudaStream_t stream) {
     };
     for (int p = 0; p < passes && err == cudaSuccess; ++p) {
         const int n = fillers(share * (p + 1));
-        err = s.items == 8
-            ? launch_pass<D, VEC, 8>(a, s, p, list[(p + 1) & 1], list[p & 1], counts, fill, n, stream)
-            : launch_pass<D, VEC, 32>(a, s, p, list[(p + 1) & 1], list[p & 1], counts, fill, n, stream);
+        const auto pass = s.items == 2 ? launch_pass<D, VEC, 2> : s.items == 4 ? launch_pass<D, VEC, 4> : launch_pass<D, VEC, 16>;
+        err = pass(a, s, p, list[(p + 1) & 1], list[p & 1], counts, fill, n, stream);
     }
     if (err != cudaSuccess) return err;
     const Pair *sorted = list[passes == 0 ? 0 : (passes - 1) & 1];
