@@ -137,7 +137,7 @@ def tokens(rows, vocab, kind, seed=5):
 
 SHAPES = [(1, 1, 1), (1, 64, 7), (48, 1024, 200), (300, 1537, 100), (2048, 65, 5000),
           (2049, 65, 5000), (2500, 8, 1), (5000, 257, 513), (4097, 1000, 512), (256, 8200, 40),
-          (257, 64, 3000), (8192, 40, 900), (8193, 40, 900), (20000, 24, 70000), (9000, 8, 300001),
+          (257, 64, 3000), (6144, 40, 900), (6145, 40, 900), (20000, 24, 70000), (9000, 8, 300001),
           (50000, 24, 700), (140000, 16, 300)]
 
 

@@ -9,15 +9,15 @@
 // FP32, so that results are bitwise reproducible.  Few rows: a CTA for each
 // row looks for the row's token among all tokens, and the first row of a token
 // sums them (one launch, no workspace).  More rows: positions are brought in
-// the order of their tokens, up to 8192 by counting, more by a stable radix
+// the order of their tokens, up to 6144 by counting, more by a stable radix
 // sort of up to 9 bits a pass; then the list is summed in runs of 8 to 64
 // positions, and a token that fills more than a run is joined from partial
 // sums.  The rows of tokens that do not occur are zeroed by CTAs that the
 // launches of this chain carry along.
 //
 // (One GB300, a copy moves 6.68 TB/s.  32768 x 4096 BF16 against 131072
-// entries: lookup 59 us of the device's time, 0.93 of that rate; gradient 214
-// us, 0.94, added to another 125.  5000 x 1537 FP32 against 50001, a third of it
+// entries: lookup 59 us of the device's time, 0.93 of that rate; gradient 208
+// us, 0.97, added to another 116.  5000 x 1537 FP32 against 50001, a third of it
 // ignored: 69 us, 0.71.  Rows off the 16-byte grid cost two loads a window and
 // the shifts: 32768 x 4097 BF16 lookup 99 us.)
 #include "device_status.h"
@@ -429,9 +429,10 @@ __global__ void __launch_bounds__(kSortThreads)
 
 // Up to kMostRanked positions go to their places at once: that of i is the
 // number of j with a smaller key, or the same key and j < i.  CTA b counts them
-// for positions 32 b .. 32 b + 31 against all keys in its shared memory.  (The
-// passes above, with three launches, took 8 to 14 us more of 512 to 2048 rows.)
-constexpr int kMostRanked = 8192, kRankThreads = 256, kRankPer = 4;
+// for positions 32 b .. 32 b + 31 against all keys in its shared memory.  (With the
+// sums of 1024 columns, ranked | sorted by the passes above: 1000 rows 6.8 | 14.4
+// us, 2500 9.2 | 16.7, 4000 11.3 | 18.6, 6000 17 | 20, 8192 23 | 21.)
+constexpr int kMostRanked = 6144, kRankThreads = 512, kRankPer = 2;
 __global__ void __launch_bounds__(kRankThreads)
     rank_kernel(const EmbeddingArgs a, Pair *out, unsigned int *present) {
     constexpr int U = 8;
