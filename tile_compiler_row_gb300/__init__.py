@@ -1247,11 +1247,18 @@ def _columns(tensors, name, types, counts, dev):
         raise ValueError(f"{name} must have {len(counts)} tensors like the other lists, "
                          f"not {len(tensors)}")
     try:
-        sizes = [t.numel() for t in tensors]
+        sizes = [t.numel() for t in tensors] if counts is None else counts
+        kind = tensors[0].dtype if len(tensors) else None
+        pointers = [t.data_ptr() for t, n in zip(tensors, sizes)
+                    if t.dtype is kind and t.numel() == n and t.get_device() == dev
+                    and t.is_contiguous()] if kind in types else []
+        if len(pointers) == len(sizes):
+            return pointers, sizes, [kind] * len(sizes)
+        # of several types
         kinds = list(map(_DTYPE_OF, tensors))
-        pointers = [t.data_ptr() for t in tensors if t.get_device() == dev and t.is_contiguous()]
-        if types.keys() >= set(kinds) and len(pointers) == len(kinds) and \
-                (counts is None or sizes == counts):
+        pointers = [t.data_ptr() for t, n in zip(tensors, sizes)
+                    if t.numel() == n and t.get_device() == dev and t.is_contiguous()]
+        if types.keys() >= set(kinds) and len(pointers) == len(sizes):
             return pointers, sizes, kinds
     except AttributeError:
         pass
