@@ -664,13 +664,15 @@ int tile_grad_norm(const tile_tensor_t *tensors, int count, float scale, float m
  * is not finite becomes NaN.
  *
  * Everything else is FP32; exp_avg and exp_avg_sq are rounded after each product
- * and sum.  Pointers: aligned to their element; the 16-byte grid is the fastest.  No written range may overlap another
- * range of the call (TILE_ERR_ALIAS): a tensor is listed once.  n >= 0, no limit
- * on count.  TILE_ERR_EPS for betas outside [0, 1), eps that is not finite or
- * below 2^-126, an lr or weight_decay that is not finite; TILE_ERR_SHAPE for n < 0,
- * count < 0, step < 1; TILE_ERR_DTYPE for unknown types (copy_dtype: BF16 or
- * F16); other rules and errors as the row entry points.  May be captured into a
- * CUDA graph, which then holds the pointers. */
+ * and sum.  Pointers: aligned to their element; the 16-byte grid is the fastest,
+ * and with FP32 states so are tensors that are off it by the same elements.  No
+ * written range may overlap another range of the call (TILE_ERR_ALIAS): a tensor
+ * is listed once.  n >= 0, no limit on count.  TILE_ERR_EPS for betas outside
+ * [0, 1), eps that is not finite or below 2^-126, an lr or weight_decay that is
+ * not finite; TILE_ERR_SHAPE for n < 0, count < 0, step < 1; TILE_ERR_DTYPE for
+ * unknown types (copy_dtype: BF16 or F16); other rules and errors as the row
+ * entry points.  May be captured into a CUDA graph, which then holds the
+ * pointers. */
 #define TILE_STATE_F32  0
 #define TILE_STATE_E4M3 1
 

@@ -228,6 +228,22 @@ def test_step(dtype, shift, eight):
         check_step(s, step=4, decay=[0.1 * (i % 3) for i in range(len(SIZES))])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shifts", [(1, 2, 3, 1, 2), (0, 1, 0, 0, 0), (2, 2, 2, 2, 3), (3, 3, 3, 0, 3)])
+def test_step_of_unlike_alignments(dtype, shifts):
+    s = make(SIZES + [2, 4, 5, 1027], dtype, False, torch.bfloat16)
+    for name, shift in zip(("params", "grads", "exp_avg", "exp_avg_sq", "copies"), shifts):
+        s[name] = views(s[name], shift)[0]
+    check_step(s, step=3, factor=0.3)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3, 5])
+def test_step_of_like_alignments(shift):
+    """Off the grid by the same elements, of every short length."""
+    for copy in (None, torch.float16):
+        check_step(make([*range(1, 12), 1023, 1024, 1025, 1027, 1028, 4099], torch.bfloat16, False, copy, shift), step=2)
+
+
 @pytest.mark.parametrize("eight", [False, True])
 def test_first_step_from_zero(eight):
     params = [normal(1, 1000).view(10, 100), normal(2, 257)]
