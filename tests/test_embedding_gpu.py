@@ -315,3 +315,83 @@ def test_streams_graphs_and_calls_at_once():
         torch.cuda.synchronize()
         assert torch.equal(grad, tile.embedding_backward(t, d, 500))
         assert torch.equal(out, tile.embedding(t, grad))
+
+
+# ---- sums that are exact ------------------------------------------------------------
+#
+# A bound of n roundings says nothing of a token that occurs a million times.  Of
+# whole numbers, and a scale of 1/2, every sum in any order is exact in FP32 as long
+# as the magnitudes add up to less than 2^24: the gradient is that of FP64, rounded
+# once to its type.  One row left out, taken twice or put to another token shows.
+
+PAIRS = [(torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32),
+         (torch.float16, torch.float16), (torch.float16, torch.float32)]
+LENGTHS = {"lengths": [1, 2, 7, 8, 9, 15, 16, 17, 63, 64, 65, 127, 128, 129, 191, 192, 193, 256, 320, 1000],
+           "whole runs": [64, 128, 64, 256, 192, 64, 64, 512, 1024, 320, 1536]}
+
+
+def whole(seed, most, *shape, dtype=torch.float32):
+    return torch.randint(-most, most + 1, shape, device="cuda", generator=gen(seed)).to(dtype)
+
+
+def tokens_of_lengths(rows, vocab, lengths, seed=5):
+    """Tokens that occur as often as `lengths` has it, one after another, shuffled: runs
+    of the sorted list end in, at and next to them."""
+    counts = torch.tensor(lengths, device="cuda").repeat(rows // sum(lengths) + 1)
+    names = torch.arange(counts.numel(), device="cuda") % vocab
+    t = torch.repeat_interleave(names.sort().values, counts)[:rows]
+    return t[torch.randperm(rows, device="cuda", generator=gen(seed))]
+
+
+def check_exact(rows, width, vocab, kind, pairs=PAIRS, most=2, source=0, target=0):
+    token = tokens_of_lengths(rows, vocab, LENGTHS[kind]) if kind in LENGTHS else tokens(rows, vocab, kind)
+    keep = token != IGNORE
+    assert most * int(torch.bincount(token[keep], minlength=1).max()) + 200 < 1 << 24
+    for dtype, into in pairs:
+        dout = whole(3, most, rows, width, dtype=dtype)
+        total = torch.zeros(vocab, width, device="cuda", dtype=torch.float64).index_add_(
+            0, token[keep], dout[keep].double())
+        dout = offset_view(dout, source)
+        for old in (None, whole(4, 100, vocab, width, dtype=into)):
+            room = torch.full((vocab * width + 32,), 7.0, dtype=into, device="cuda")
+            got = room[target:target + vocab * width].view(vocab, width)
+            if old is not None:
+                got.copy_(old)
+            need = tile.tile_embedding_backward_workspace_bytes(rows, width, vocab)
+            ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda") if need else None
+            tile.tile_embedding_backward(token, dout, got, ws, 0.5, accumulate=old is not None)
+            want = (total * 0.5 + (0.0 if old is None else old.double())).float().to(into)
+            assert torch.equal(got, want), (dtype, into, old is not None, int((got != want).sum()))
+            assert (room[:target] == 7.0).all() and (room[target + vocab * width:] == 7.0).all()
+            del got, room, ws, want
+
+
+@pytest.mark.parametrize("kind", ["uniform", "one", "padded", "rare", *LENGTHS])
+@pytest.mark.parametrize("rows,width,vocab", SHAPES)
+def test_exact_gradient(rows, width, vocab, kind):
+    check_exact(rows, width, vocab, kind)
+
+
+@pytest.mark.parametrize("kind", ["one", "padded", *LENGTHS])
+@pytest.mark.parametrize("rows", [60, 3000, 9000])
+@pytest.mark.parametrize("width,source,target", [(1, 0, 1), (33, 1, 0), (64, 1, 1), (129, 3, 2), (257, 0, 0)])
+def test_exact_gradient_from_any_alignment(rows, width, source, target, kind):
+    check_exact(rows, width, 60, kind, source=source, target=target)
+
+
+@pytest.mark.parametrize("rows,vocab,kind", [(1 << 20, 100000, "rare"), (1 << 20, 3, "uniform"),
+                                             (1 << 20, 900, "lengths"), (1 << 20, 900, "whole runs"), (131072, 70, "lengths"),
+                                             (131073, 70, "lengths"), (1 << 20, 1, "one"),
+                                             (1 << 24, 100000, "padded")])
+def test_exact_gradient_of_many_rows(rows, vocab, kind):
+    # (of 2^24 rows, half of one token and so 8.4e6 of them, -1 .. 1)
+    check_exact(rows, 3, vocab, kind, PAIRS[:1], 2 if rows < 1 << 22 else 1)
+
+
+# runs of more than 64 positions, where the partial sums would pass 64 MiB
+@pytest.mark.parametrize("kind", ["one", "padded", "rare", *LENGTHS])
+@pytest.mark.parametrize("rows,width,pair", [(131072, 4096, 1), (140001, 4001, 0), (1 << 20, 520, 4),
+                                             (1 << 20, 1100, 2)])
+def test_exact_gradient_of_long_runs(rows, width, kind, pair):
+    assert rows * (width + 16) > 1 << 29
+    check_exact(rows, width, 300, kind, PAIRS[pair:pair + 1])
