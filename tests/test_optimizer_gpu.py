@@ -423,3 +423,28 @@ def test_streams():
     for k in s:
         for x, y, z in zip(s[k], t[k], u[k]):
             assert torch.equal(x, y) and torch.equal(x, z)
+
+
+# ---- many elements --------------------------------------------------------------------
+#
+# From 152 x 16 chunks on a CTA takes several steps of the smallest chunk: 2 in FP32 from
+# 5e6 elements on, with 8-bit states 2 from 1e7 and 4 from 2e7 on (a warp's second and
+# later blocks, whose scales other lanes hold and whose copies lie in used stages).
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_step_of_many_elements(dtype, shift):
+    s = make([3000001, 77, 2100003], dtype, False, torch.bfloat16, shift)
+    check_step(s, step=3, factor=0.3)
+
+
+@pytest.mark.parametrize("dtype,total,copy,shift", [
+    (torch.float32, 2.1e7, None, 0), (torch.bfloat16, 2.1e7, torch.bfloat16, 0),
+    (torch.float16, 2.1e7, torch.float16, 0), (torch.float32, 1.1e7, torch.float16, 0),
+    (torch.bfloat16, 1.1e7, None, 0), (torch.bfloat16, 2.1e7, torch.float16, 3)])
+def test_eight_bit_step_of_many_elements(dtype, total, copy, shift):
+    """Whole blocks, a last one that is cut, and blocks before it that a CTA's last warps have not."""
+    sizes = [int(total * 0.7) // 8192 * 8192 + 2048 * 3 + 256 * 2 + 5, 77, int(total * 0.3) // 8192 * 8192 + 8192]
+    s = make(sizes, dtype, True, copy, shift)
+    check_step(s, step=3, factor=0.3, seed=9)
