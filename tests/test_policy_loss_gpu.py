@@ -291,3 +291,35 @@ def test_workspace_streams_and_graphs():
             s2, w2 = tile.policy_loss(held, mean="sequence", **k)
             assert torch.equal(s, s2) and torch.equal(w, w2)
             assert torch.equal(d, tile.policy_loss_backward(held, weights=w2, **k))
+
+
+@pytest.mark.parametrize("mean", ["token", "sequence"])
+@pytest.mark.parametrize("rows", [1, 300, 20000])
+@pytest.mark.parametrize("size", [1e-6, 1e-4, 1e-3, 0.05, 0.3, 0.5, 0.7, 1.0, 3.0])
+def test_kl_of_a_policy_near_its_reference(size, rows, mean):
+    """The KL term against itself: e^q - q - 1 is about q^2 / 2 there, so nothing of the
+    size of q's own ulp may be left in it.  In roundings of 2^-24 of the term: q is
+    off by one of itself, which is q (e^q - 1) / kl of the term, 3.6 at most up to
+    |q| = 3.  Then five of the term's own up to 1/2, or beyond it expm1f's ulp, up to
+    2 |e^q - 1| / kl = 8.8, and one of the difference: 14 in all.  The terms are
+    positive, so each of the sums over a tile (16 to a lane and 5 between lanes, or 2, 5
+    and 8) adds one at most: 21; the sums beyond are compensated, 1; two quotients,
+    and three of the weights that the reference takes: 41."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+
+    def uniform(n):
+        return torch.rand(n, device="cuda", generator=g)
+    nll = 0.1 + uniform(rows)
+    ref = nll - (2 * uniform(rows) - 1) * size
+    offsets = torch.tensor([0, rows // 3, rows // 3, rows], device="cuda")
+    stats, weights = tile.policy_loss(nll, nll.clone(), torch.ones_like(nll), ref_nll=ref, offsets=offsets,
+                                      kl_coef=1.0, mean=mean)
+    q = nll.double() - ref.double()
+    q2 = q * q     # e^q - q - 1: the series up to 1/2 (the first term left out: 2^-60 of it), else expm1
+    series = torch.zeros_like(q)
+    for k in range(16, 1, -1):
+        series = series * q + 1.0 / math.factorial(k)
+    kl = torch.where(q.abs() <= 0.5, q2 * series, torch.expm1(q) - q)
+    w = torch.repeat_interleave(weights.double(), offsets[1:] - offsets[:-1])
+    want = (w * kl).sum().item()
+    assert float(stats[2]) >= 0 and abs(float(stats[2]) - want) <= 41 * U * want, (float(stats[2]), want)
