@@ -567,20 +567,21 @@ int tile_embedding_backward(int dtype, int dweight_dtype, const long long *token
  * is not used.  Offsets that fall or leave [0, rows] set the device
  * status word and make stats NaN.  offsets NULL: one sequence of all rows
  * (sequences 1).  target NULL: every row counts.  ref_nll NULL: no such term
- * (kl_coef 0).
+ * (kl_coef 0).  kl_coef 0 with a ref_nll: stats[2] alone looks at it, loss and
+ * gradient are those without one.
  *
  * nll, old_nll, ref_nll [rows], advantage [rows] or [sequences]: FP32.  Whether r
  * is held back is decided from old_nll - nll as if it had not been rounded; r A
  * equal to its bound is not.  An advantage of 0 gives a first term of 0.
  * exp(q) - q - 1 is good to 14 roundings of 2^-24 of itself up to |q| = 3, however
- * small q is.  Sums
- * are FP32 over 512 rows and compensated beyond, bitwise reproducible.  `workspace`:
- * 16-byte aligned device memory of the caller; calls that overlap in time need
- * workspaces of their own.  rows == 0 writes zeros.  TILE_ERR_EPS for clip_low
- * outside [0, 1], a negative or NaN clip_high or a kl_coef that is not finite;
- * TILE_ERR_SHAPE for rows or sequences above 2^30, sequences < 1, or other than
- * 1 without offsets; TILE_ERR_OP for unknown flags; other rules and errors as
- * the row entry points.  May be captured into a CUDA graph. */
+ * small q is.  Sums are FP32 over 512 rows and compensated beyond, bitwise
+ * reproducible.  `workspace`: 16-byte aligned device memory of the caller; calls
+ * that overlap in time need workspaces of their own.  rows == 0 writes zeros.
+ * TILE_ERR_EPS for clip_low outside [0, 1], a negative or NaN clip_high or a
+ * kl_coef that is not finite; TILE_ERR_SHAPE for rows or sequences above 2^30,
+ * sequences < 1, or other than 1 without offsets; TILE_ERR_OP for unknown flags;
+ * other rules and errors as the row entry points.  May be captured into a CUDA
+ * graph. */
 #define TILE_POLICY_SEQUENCE_ADVANTAGE 1   /* advantage is [sequences]            */
 #define TILE_POLICY_SEQUENCE_MEAN      2   /* the mean of the sequences' means    */
 

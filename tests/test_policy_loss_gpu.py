@@ -323,3 +323,26 @@ def test_kl_of_a_policy_near_its_reference(size, rows, mean):
     w = torch.repeat_interleave(weights.double(), offsets[1:] - offsets[:-1])
     want = (w * kl).sum().item()
     assert float(stats[2]) >= 0 and abs(float(stats[2]) - want) <= 41 * U * want, (float(stats[2]), want)
+
+
+@pytest.mark.parametrize("mean", ["token", "sequence"])
+@pytest.mark.parametrize("rows", [40, 9000])
+def test_no_kl_term_whatever_the_reference_holds(rows, mean):
+    """kl_coef 0 with a reference (its term is looked at, not trained on): loss and
+    gradient are those without one, where e^q overflows or is NaN too."""
+    nll, kw = inputs(rows, 6, ignored=0.3)
+    kw["kl_coef"] = 0.0
+    nll[::5] += 150.0
+    kw["old_nll"] = kw["old_nll"] + torch.where(nll > 100.0, 150.0, 0.0)
+    without = dict(kw, ref_nll=None)
+    want, weights = tile.policy_loss(nll, mean=mean, **without)
+    want_d = tile.policy_loss_backward(nll, weights=weights, **without)
+    assert torch.isfinite(want).all() and torch.isfinite(want_d).all()
+    for bad in (None, float("nan"), float("inf"), -float("inf")):
+        if bad is not None:
+            kw["ref_nll"] = torch.full_like(nll, bad)
+        stats, w = tile.policy_loss(nll, mean=mean, **kw)
+        assert torch.equal(w, weights)
+        assert torch.equal(stats[[0, 1, 3]], want[[0, 1, 3]])
+        assert not torch.isfinite(stats[2])
+        assert torch.equal(tile.policy_loss_backward(nll, weights=w, **kw), want_d)

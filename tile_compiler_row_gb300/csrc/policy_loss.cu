@@ -331,7 +331,8 @@ __device__ __forceinline__ void join_sums(const PolicyArgs &a, const float4 *slo
             if (bad) atomicOr(a.status, kBadOffsets);
             const float surrogate = bad ? nan : n > 0.0f ? sum.v[0].value() / n : 0.0f;
             const float kl = bad ? nan : n > 0.0f ? sum.v[1].value() / n : 0.0f;
-            a.stats[0] = fmaf(a.kl_coef, kl, surrogate);
+            // (a term that is only looked at: e^q may be infinite, and 0 times it NaN)
+            a.stats[0] = a.kl_coef != 0.0f ? fmaf(a.kl_coef, kl, surrogate) : surrogate;
             a.stats[1] = surrogate;
             a.stats[2] = kl;
             a.stats[3] = bad ? nan : n > 0.0f ? sum.v[2].value() / n : 0.0f;

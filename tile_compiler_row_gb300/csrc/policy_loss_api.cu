@@ -131,6 +131,7 @@ int tile_policy_loss_backward(const tile_policy_loss_args_t *args, const float *
     if (tile::any_overlap(written, 1, read, kReads + 2)) return TILE_ERR_ALIAS;
     const cudaError_t inj = tile::injected_launch_failure();
     if (inj != cudaSuccess) return cuda_status(inj);
+    if (c.kl_coef == 0.0f) a.ref_nll = nullptr;   // no term, whatever e^q would be
     a.weights = const_cast<float *>(weights);
     a.dloss = dloss;
     a.dnll = dnll;
