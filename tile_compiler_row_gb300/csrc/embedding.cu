@@ -259,10 +259,13 @@ SortPlan sort_plan(int rows, int vocab) {
     p.passes = (all + kMaxBits - 1) / kMaxBits;
     p.bits = (all + p.passes - 1) / p.passes;
     // Each tile adds up the counts of all tiles: short ones are done sooner while
-    // they are few.  (Ranking 32768, 131072 and 2^20 positions, with the sums of 64
-    // columns: 21, 50 and - us with 2 items, 24, 37 and - with 4, - and 136 with
-    // 16; CTAs of 256 threads of 8 or 32 items 27, 41 and 147.)
-    p.items = rows <= 49152 ? 2 : rows <= 131072 ? 4 : 16;
+    // they are few.  (The gradient of 64 BF16 columns, added, tokens by frequency, with
+    // 2, 4 and 16 items: 32768 rows 34, 36 and 64 us, 65536 49, 54 and 73, 98304 66, 62
+    // and 85, 140000 89, 80 and 100, 196608 112, 104 and 116, 262144 143, 140 and 139,
+    // 393216 201, 193 and 186, 2^20 394, 249 and 211; with 1024 columns the orders
+    // are the same.  The counts that all tiles read grow with the square of the
+    // rows all the same: 2^24 rows take 3.6 ms, of which the bytes are 0.35.)
+    p.items = rows <= 81920 ? 2 : rows <= 262144 ? 4 : 16;
     p.tiles = (rows + kSortThreads * p.items - 1) / (kSortThreads * p.items);
     return p;
 }
