@@ -106,7 +106,8 @@ cudaError_t launch_lookup(const EmbeddingArgs &a, cudaStream_t stream) {
     int lanes = 8;
     while (lanes < 256 && lanes * 4 < windows) lanes *= 2;
     // few rows: one window a thread
-    while (lanes < 256 && lanes < windows && static_cast<long long>(a.rows) * lanes < 152 * 512) lanes *= 2;
+    const long long few = sm_count_of_device() * 512;
+    while (lanes < 256 && lanes < windows && static_cast<long long>(a.rows) * lanes < few) lanes *= 2;
     const int per = 256 / lanes;
     lookup_kernel<T, VEC><<<(a.rows + per - 1) / per, 256, 0, stream>>>(a, lanes);
     return cudaGetLastError();
@@ -494,16 +495,19 @@ constexpr int kSumThreads = 128;
 struct SumPlan {
     int run, runs;   // positions of a run, and how many there are
 };
+// Where a run ends decides the order of additions, so its length goes by 152 SMs, a
+// whole GPU of this kind, on every device: the same bits there.
+constexpr int kRunSms = 152;
 // 64 positions a run; fewer, down to 8, where that leaves SMs without enough
 // threads (32768 x 1536 BF16, added: 82 us with 64); more where the partial sums
-// would pass 64 MiB.
+// would pass 64 MiB (131072 x 4096: 128 positions, 2^20 x 4096: 1024).
 // (vector: elements of a window; the workspace has room for the runs of 8, the most.)
 SumPlan sum_plan(int rows, int width, int vector) {
     const long long windows = width / vector + 1;
     auto bytes = [&](int run) { return (static_cast<long long>(rows) + run - 1) / run * 8 * (width + 16); };
     SumPlan p;
     p.run = 64;
-    while (p.run > 8 && rows / p.run * windows < 152 * 1536) p.run /= 2;
+    while (p.run > 8 && rows / p.run * windows < kRunSms * 1536) p.run /= 2;
     while (bytes(p.run) > (64ll << 20) && p.run < rows) p.run *= 2;
     p.runs = (rows + p.run - 1) / p.run;
     return p;

@@ -704,16 +704,17 @@ cudaError_t launch_norm_table(const NormTensor *t, int count, double *partial, i
     return cudaLaunchKernelEx(&cfg, norm_kernel<N, false>, table, partial, scale, most, out);
 }
 
-// Elements of a chunk: as many as leave kWantedChunks of them, in 1, 2, 4 .. `most`
+// Elements of a chunk: as many as leave kChunksPerSm of them for each SM, in 1, 2, 4 .. `most`
 // steps of the smallest (few elements: latency counts).  At most 2048 in FP32
 // and 8192 with 8-bit states: short CTAs that follow one another keep the
 // accesses in the order of the memory (1.2e9 parameters in FP32: 4.93 ms with
 // 1024, 4.75 with 2048, 4.81 with 4096, 4.93 with 8192; 1.9e8 with 8 bits: 625
 // us with 2048, 522 with 8192, 533 with 16384, 550 with 32768).
-constexpr long long kWantedChunks = 152 * 16;
+constexpr long long kChunksPerSm = 16;
 long long chunk_of(long long elements, long long smallest, int most, int *steps) {
+    const long long wanted = sm_count_of_device() * kChunksPerSm;
     *steps = 1;
-    while (*steps < most && elements / (smallest * *steps * 2) >= kWantedChunks) *steps *= 2;
+    while (*steps < most && elements / (smallest * *steps * 2) >= wanted) *steps *= 2;
     return smallest * *steps;
 }
 

@@ -15,8 +15,10 @@ struct NormTensor {
     int elem;
 };
 
-// The norm's CTAs leave this many partial sums for each launch at most.
-constexpr int kNormPrograms = 1216;
+// The norm's CTAs leave this many partial sums for each launch at most: 8 for each of
+// 152 SMs, a whole GPU of this kind.  The same on every device: it decides the order
+// of additions, so the bits, and the workspace.
+constexpr int kNormPrograms = 152 * 8;
 constexpr int kNormTensors = 1024;   // tensors of one launch
 size_t grad_norm_workspace(int count);
 // out: [2] norm and factor; ws: grad_norm_workspace(count) bytes.  Tensors of no
