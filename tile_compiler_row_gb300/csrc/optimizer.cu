@@ -321,16 +321,7 @@ __global__ void __launch_bounds__(kAdamwThreads)
                        make_uint2(narrow_pair(e.copy_elem, p[0], p[1]), narrow_pair(e.copy_elem, p[2], p[3])));
         }
     };
-    auto element = [&](long long at) {
-        const float g = __fmul_rn(load_grad(e.grad, e.grad_elem, at), f);
-        const float a = moment1(s, __ldcs(m + at), g), b = moment2(s, __ldcs(v + at), g);
-        const float p = updated(s, __ldcs(param + at), keep, a, __fsqrt_rn(b));
-        __stcs(m + at, a);
-        __stcs(v + at, b);
-        __stcs(param + at, p);
-        if (e.copy_elem >= 0) store_copy(e.copy, e.copy_elem, at, p);
-    };
-    if (base == 0 && static_cast<int>(threadIdx.x) < e.head) element(static_cast<int>(threadIdx.x) - e.head);
+    long long at0 = base == 0 ? -static_cast<long long>(e.head) : base, end = min(base + chunk, e.n);
     if (e.vectors && base + chunk <= e.n) {
         if (groups == 1) {
             vectors(std::integral_constant<int, 1>(), 0);
@@ -338,15 +329,16 @@ __global__ void __launch_bounds__(kAdamwThreads)
 #pragma unroll 1
             for (int k = 0; k < groups; k += U) vectors(std::integral_constant<int, U>(), k);
         }
-        return;
+        end = base == 0 ? 0 : at0;   // what lies in front of the grid is left
     }
-    for (int k = 0; k < groups && base + k * kAdamwGroup < e.n; ++k) {
+#pragma unroll 1
+    for (; at0 < end; at0 += kAdamwGroup) {
         float g[4], a[4], b[4], p[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const long long at = base + (k * 4 + j) * kAdamwThreads + threadIdx.x;
+            const long long at = at0 + j * kAdamwThreads + threadIdx.x;
             g[j] = a[j] = b[j] = p[j] = 0.0f;
-            if (at >= e.n) continue;
+            if (at >= end) continue;
             g[j] = load_grad(e.grad, e.grad_elem, at);
             a[j] = __ldcs(m + at);
             b[j] = __ldcs(v + at);
@@ -354,8 +346,8 @@ __global__ void __launch_bounds__(kAdamwThreads)
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const long long at = base + (k * 4 + j) * kAdamwThreads + threadIdx.x;
-            if (at >= e.n) continue;
+            const long long at = at0 + j * kAdamwThreads + threadIdx.x;
+            if (at >= end) continue;
             g[j] = __fmul_rn(g[j], f);
             a[j] = moment1(s, a[j], g[j]);
             b[j] = moment2(s, b[j], g[j]);
