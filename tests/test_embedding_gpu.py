@@ -395,3 +395,19 @@ def test_exact_gradient_of_many_rows(rows, vocab, kind):
 def test_exact_gradient_of_long_runs(rows, width, kind, pair):
     assert rows * (width + 16) > 1 << 29
     check_exact(rows, width, 300, kind, PAIRS[pair:pair + 1])
+
+
+@pytest.mark.parametrize("rows,width,vocab", [(7000, 5, 511), (7000, 5, 512), (7000, 3, 262143), (7000, 3, 262144),
+                                              (9000, 1, (1 << 27) - 1), (9000, 1, (1 << 27) + 3), (3000, 1, (1 << 27) + 3)])
+def test_exact_gradient_of_vocabularies_at_a_digit_end(rows, width, vocab):
+    """1 to 4 passes of the sort, the last entries among the tokens."""
+    token = tokens(rows, vocab, "uniform")
+    token[::3] = vocab - 1 - token[::3] % 7
+    dout = whole(3, 2, rows, width)
+    for add in (False, True):
+        got = torch.full((vocab, width), 3.0 if add else float("nan"), device="cuda")
+        ws = torch.full((tile.tile_embedding_backward_workspace_bytes(rows, width, vocab),), 0xFF, dtype=torch.uint8,
+                        device="cuda")
+        tile.tile_embedding_backward(token, dout, got, ws, accumulate=add)
+        want = torch.full((vocab, width), 3.0 if add else 0.0, device="cuda").index_add_(0, token, dout)
+        assert torch.equal(got, want)
