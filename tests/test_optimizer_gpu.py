@@ -448,3 +448,12 @@ def test_eight_bit_step_of_many_elements(dtype, total, copy, shift):
     sizes = [int(total * 0.7) // 8192 * 8192 + 2048 * 3 + 256 * 2 + 5, 77, int(total * 0.3) // 8192 * 8192 + 8192]
     s = make(sizes, dtype, True, copy, shift)
     check_step(s, step=3, factor=0.3, seed=9)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_an_eps_that_leaves_decay_alone(eight):
+    """Above 2^126 the reciprocal is 0; the parameter's factor and product round once each."""
+    params, grads = [normal(1, 1000)], [normal(2, 1000)]
+    was = params[0].clone()
+    tile.adamw(params, grads, **tile.adamw_state(params, 8 if eight else 32), step=1, lr=0.5, weight_decay=0.5, eps=1e38)
+    assert ((params[0].double() - was.double() * 0.75).abs() <= 2.0 ** -23 * was.double().abs()).all()

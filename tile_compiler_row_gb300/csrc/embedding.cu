@@ -11,15 +11,16 @@
 // sums them (one launch, no workspace).  More rows: positions are brought in
 // the order of their tokens, up to 6144 by counting, more by a stable radix
 // sort of up to 9 bits a pass; then the list is summed in runs of 8 to 64
-// positions, and a token that fills more than a run is joined from partial
-// sums.  The rows of tokens that do not occur are zeroed by CTAs that the
-// launches of this chain carry along.
+// positions (more where the partial sums would pass 64 MiB), and a token that
+// fills more than a run is joined from partial sums.  The rows of tokens that
+// do not occur are zeroed by CTAs that the launches of this chain carry along.
 //
 // (One GB300, a copy moves 6.68 TB/s.  32768 x 4096 BF16 against 131072
-// entries: lookup 59 us of the device's time, 0.93 of that rate; gradient 208
-// us, 0.97, added to another 116.  5000 x 1537 FP32 against 50001, a third of it
-// ignored: 69 us, 0.71.  Rows off the 16-byte grid cost two loads a window and
-// the shifts: 32768 x 4097 BF16 lookup 99 us.)
+// entries: lookup 59 us of the device's time, 0.93 of that rate; gradient 209
+// us, 0.96, added to another 116, 0.60; in FP32 352, 1.03, and added 143, 0.69.
+// 5000 x 1537 FP32 against 50001, a third of it ignored: 69 us, 0.71.  Rows off
+// the 16-byte grid cost two loads a window and the shifts: 32768 x 4097 BF16 lookup
+// 80 us, 0.69, gradient 254, 0.79, added 190, 0.37.)
 #include "device_status.h"
 #include "embedding.h"
 #include "row_windows.cuh"
@@ -231,10 +232,16 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const EmbeddingAr
 }
 
 // Few rows: each CTA looks at all tokens, 1 to 2 ns a CTA, where ranking them,
-// the sums and the join take 8 to 14 us.  (rows x width, BF16, all tokens
-// different, few | ranked: 256 x 4096 5.6 | 8.9 us, 512 x 1024 6.0 | 10.3, 1024 x
-// 256 5.1 | 10.3, 1024 x 1024 10.3 | 9.8, 512 x 4096 18 | 9.9, 2048 x 256 8.3 |
-// 11.5, of one token 27 | 18.)
+// the sums and the join are a chain of launches.  The rule counts CTAs of 128 columns:
+// FP32's, 16-bit types have half as many.  (Device times in a graph, all tokens
+// different, new gradient of 4096 entries, few | ranked.  BF16: 256 x 4096 11.3 |
+// 14.4 us, 512 x 1024 8.5 | 12.5, 1024 x 256 6.7 | 12.3, 1024 x 512 8.5 | 12.4, 1024 x
+// 1024 12.9 | 13.6, 512 x 4096 23.7 | 14.8, 2048 x 256 9.5 | 12.4, of one token 29 |
+// 27.  FP32: 256 x 4096 19.0 | 20.4, 512 x 1024 13.3 | 12.3, 1024 x 256 8.2 | 12.3,
+// 1024 x 512 12.6 | 12.4, 2048 x 256 12.4 | 12.3.  Added to, in BF16 5.9 | 5.7, 6.2 |
+// 6.2, 5.4 | 6.7, 6.7 | 7.0, 10.5 | 6.7, 18.0 | 6.7, 8.6 | 7.7; in FP32, where the
+// rule keeps more than it should, 9.5 | 6.2, 9.8 | 5.9, 6.4 | 6.7, 10.3 | 6.7, 11.1 |
+// 7.5.)
 bool few_rows(int rows, int width) {
     const long long ctas = static_cast<long long>(rows) * (width / 128 + 1);
     return rows <= kFewThreads ? ctas <= 16384 : rows <= kMostFew && ctas <= 6000;
@@ -499,7 +506,7 @@ struct SumPlan {
 // whole GPU of this kind, on every device: the same bits there.
 constexpr int kRunSms = 152;
 // 64 positions a run; fewer, down to 8, where that leaves SMs without enough
-// threads (32768 x 1536 BF16, added: 82 us with 64); more where the partial sums
+// threads (32768 x 1536 BF16, added: 77 us, with 64 82); more where the partial sums
 // would pass 64 MiB (131072 x 4096: 128 positions, 2^20 x 4096: 1024).
 // (vector: elements of a window; the workspace has room for the runs of 8, the most.)
 SumPlan sum_plan(int rows, int width, int vector) {

@@ -15,9 +15,12 @@
 // bisection.
 //
 // (One GB300, a copy moves 6.68 TB/s.  1.2e9 parameters: norm of BF16 gradients
-// 352 us, 1.03 of that rate; step with a BF16 copy 4.75 ms, 1.07.  1.9e8
-// parameters with 8-bit states, FP16 gradients and copies: 480 us, 0.95.  11
-// tensors of 1.3e5 elements: 5.8 and 2.7 us, the host's part of a call 23.)
+// 350 us, 1.03 of that rate; step with a BF16 copy 4.74 ms, 1.07.  1.9e8
+// parameters with 8-bit states, FP16 gradients and copies: 478 us, 0.96.  11
+// tensors of 1.3e5 elements: 5.7 and 2.8 us, of a call, which is the host's, 23 to
+// 30 and 30 to 34.  Tensors of unlike starts are taken one element at a time: 1.3e8
+// parameters, BF16 gradients and copies, 884 us where the grid takes 536, with 8-bit
+// states 542 and 331.)
 //
 // 8-bit states are e4m3 values with a power of two for each 256 elements, m
 // itself and the root of v (whose range an 8-bit v would not hold).  A step
@@ -222,7 +225,8 @@ __device__ __forceinline__ float moment1(const Scalars &s, float m, float g) {
 __device__ __forceinline__ float moment2(const Scalars &s, float v, float g) {
     return __fadd_rn(__fmul_rn(v, s.beta2), __fmul_rn(__fmul_rn(g, g), s.rest2));
 }
-// 1 / x to 1 ulp, x between 2^-126 (eps) and 2^65
+// 1 / x to 1 ulp, x from 2^-126 (the least eps) to 2^126: a root of v below 2^64 times
+// 1 / sqrt(1 - b2^t) below 2^27 comes to 2^91, and an eps above 2^126 gives 0, no update.
 __device__ __forceinline__ float reciprocal(float x) {
     float d;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
@@ -733,8 +737,8 @@ cudaError_t launch_adamw_table(const AdamwTensor *t, int count, int index, const
                    on(a.copy, 2, 2 * four);
         };
         // tensors that lie one behind the other in buffers alike are off the grid
-        // by the same elements (1.3e8 parameters, BF16 gradients and copies: 984 us
-        // one by one, on the grid 531)
+        // by the same elements (1.3e8 parameters, BF16 gradients and copies: 543 us,
+        // on the grid 536, of unlike starts 884)
         int head = 0;
         while (!c.eight && head < 3 && head + 1 < a.n && !grid(head)) ++head;
         const bool vectors = grid(head);

@@ -6,15 +6,20 @@
 //
 // averaged over all tokens, or over sequences of means over their tokens.
 //
-// At most 36 bytes a token: bound by latency up to some 10^5 tokens, and by how
-// many loads are on their way beyond.  A tile is 512 rows, two to a thread, all
-// its loads issued before the sequences are looked for; the tiles' sums are
-// joined by a second launch that comes up meanwhile, or, of up to 8 tiles, by
-// the first CTA of their cluster.  (Device times in a graph: 1048576 tokens, 512
-// sequences: 9.6 us forward, 7.3 backward, where the bytes are 4 us; 8191
-// tokens: 4.8 and 3.0.  With 1024 rows, four to a thread: 10.4, 8.9, 5.9, 4.3;
-// with 256 rows 11.2, 8.3, 4.8, 2.6.  A join of 1024 threads took 0.5 to 0.8 us
-// more than one of 512.)
+// 24 bytes a token forward and 28 backward at most: bound by latency up to some
+// 10^5 tokens, and by how many loads are on their way beyond.  A tile is 512 rows,
+// two to a thread, all its loads issued before the sequences are looked for; the
+// tiles' sums are joined by a second launch that comes up meanwhile, or, of up to
+// 8 tiles, by the first CTA of their cluster.  (Device times in a graph: 1048576
+// tokens, 512 sequences: 9.8 us forward, 7.4 backward, where the bytes are 4 us; 8191
+// tokens: 5.1 and 3.1.  With expm1f alone for the KL term, tiles of 512, 1024 (four
+// rows to a thread) and 256 rows: 9.4, 10.4 and 11.2; 7.3, 8.9 and 8.3; 4.8, 5.9 and
+// 4.8; 3.0, 4.3 and 2.6.  A join of 1024 threads took 0.5 to 0.8 us more than one
+// of 512.)
+//
+// One CTA joins: it looks at each sequence's offsets, and for means over sequences
+// adds up each one's tiles.  That grows with the sequences: 16384 of 1048576 tokens
+// take 19 us, and 58 for their means (512: 9.8 and 14.6).
 //
 // Whether a ratio is clipped is decided by x against the bounds' logarithms,
 // as if x had not been rounded: r's own rounding would move tokens over the
@@ -136,7 +141,8 @@ __device__ __forceinline__ bool is_clipped(const PolicyArgs &a, const Token &t, 
 // at Chebyshev's nodes (2^-25 of it; with the roundings 3.2 of 2^-24): the term is about
 // q^2 / 2 there, and expm1f(q) - q would leave an ulp of q in it, as much as the
 // term itself at |q| = 1e-7, where a policy is still at its reference.  (Both are
-// computed: 1048576 tokens 9.6 us; with a branch between them 9.8, expm1f alone 9.4.)
+// computed.  In one run, 1048576 tokens: 9.6 us; with a branch between them 9.8,
+// expm1f alone 9.4.)
 __device__ __forceinline__ float kl_term(float q) {
     float p = 0.00019962186f;
     p = fmaf(p, q, 0.0013982197f);
